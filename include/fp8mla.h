@@ -32,6 +32,13 @@
  *       paged cache, with per-row scales amax / 448 or one given per-tensor
  *       scale.  InfiniCore page, Summary: the paged_caching write kernel.
  *
+ * and what a decode step does around it, also over a cache held in 4 bits:
+ *
+ *   rotary_table / rotary_apply -- rotary positions of query and key heads.
+ *   paged_kv_append -- a step's K and V into the cache, K rotated on the way.
+ *   paged_cache_read -- cached rows back as bf16.
+ *   paged_gqa_decode_fp4 -- grouped-query decode over the 4-bit cache.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Every pointer argument that names a tensor is a DEVICE pointer unless
@@ -97,7 +104,8 @@ typedef enum {
  *  both modes; sparse MLA). */
 typedef enum { FP8MLA_DOT_16BIT = 0, FP8MLA_DOT_FP8 = 1 } fp8mla_dot_mode_t;
 
-/* Encoding of the cache bytes.  Only FP8MLA_KV_E4M3 (OCP e4m3 "fn", or a
+/* Encoding of the cache bytes.  Unless an entry point names the 4-bit cache
+ * (FP8MLA_KV_E2M1) too, only FP8MLA_KV_E4M3 (OCP e4m3 "fn", or a
  * uint8 view of it) is accepted; the others are refused with
  * FP8MLA_ERR_UNSUPPORTED_DTYPE instead of being misread (aiter page,
  * Technical details: "a typed cache in the other arch's encoding is
@@ -106,8 +114,12 @@ typedef enum {
   FP8MLA_KV_E4M3 = 0,
   FP8MLA_KV_E4M3FNUZ = 1,
   FP8MLA_KV_E5M2 = 2,
-  FP8MLA_KV_OTHER = 3
+  FP8MLA_KV_OTHER = 3,
+  FP8MLA_KV_E2M1 = 4 /* the 4-bit cache: paged_kv_append, paged_cache_read and paged_gqa_decode_fp4 only */
 } fp8mla_kv_dtype_t;
+
+/* Type of the values rotary_apply turns. */
+typedef enum { FP8MLA_BF16 = 0, FP8MLA_F16 = 1, FP8MLA_F32 = 2 } fp8mla_dtype_t;
 
 /* Device status bits reported by fp8mla_get_last_device_error. */
 #define FP8MLA_DEV_WAIT_TIMEOUT 0x1u   /* a bounded mbarrier wait ran out; the CTA stopped */
@@ -115,6 +127,7 @@ typedef enum {
 #define FP8MLA_DEV_BAD_SEQLEN 0x4u     /* seqlen < 0 or more pages than the block table row */
 #define FP8MLA_DEV_BAD_INDEX 0x8u      /* top-k index outside [-1, num_tokens) */
 #define FP8MLA_DEV_BAD_SLOT 0x10u      /* cache-write slot >= num_blocks * page_size */
+#define FP8MLA_DEV_BAD_POSITION 0x20u  /* position >= the rows of the rotary table */
 
 /* ------------------------------------------------------------------ MLA ---
  * Work units.  The dense MLA kernel runs one work unit per pair of SMs (the
@@ -334,6 +347,133 @@ FP8MLA_API fp8mla_status_t fp8_paged_cache_write(const void* x, int64_t x_token_
                                                  int num_blocks, fp8mla_kv_dtype_t kv_dtype, void* cache,
                                                  const float* tensor_scale, float* token_scales,
                                                  fp8mla_stream_t stream);
+
+/* --------------------------------------------------------------- rotary ---
+ * A pair (a, b) of a head at position p turns by the angle p * inv_freq[i]:
+ *   (a c - b s, b c + a s),  c = factor cos(angle), s = factor sin(angle).
+ * Pair i of the rotated part (rot dims from rot_offset) is its dims
+ * (i, i + rot / 2), or (2i, 2i + 1) when interleaved.  Scaling for long
+ * contexts is a matter of inv_freq and factor.
+ *
+ * rotary_table -- table[p][i] = (cos, sin) of p * inv_freq[i], times factor.
+ *   inv_freq  float64 [half] (device)
+ *   table     float32 [n_positions, half, 2] (device, written); angles, cosines
+ *             and sines are computed in 64 bits and rounded once
+ * Requires 1 <= half <= 4096, factor > 0.  n_positions = 0 is a no-op. */
+FP8MLA_API fp8mla_status_t rotary_table(const double* inv_freq, int half, int64_t n_positions, double factor,
+                                        float* table, fp8mla_stream_t stream);
+
+/* rotary_apply -- rotate the heads of q and (h_k > 0) of k.
+ *   q, k          dtype [n_tokens, heads, head_dim], token and head strides in
+ *                 elements, the dims of a head contiguous
+ *   q_out, k_out  the same shapes with strides of their own; may be q and k
+ *                 (in place), must not overlap them otherwise
+ *   positions     int32 or (positions_64 != 0) int64 [n_tokens] (device)
+ *   table         float32 [n_positions, rot / 2, 2], 8-byte aligned
+ *   inverse       1: turn by the negative angle (the transpose: the gradient of
+ *                 the rotation, and its inverse where factor is 1)
+ * Every value is computed in float32 (products and sum each rounded) and
+ * rounded once; dims outside the rotated part are copied.  A token with a
+ * negative position is padding: its heads are not written.  A position >=
+ * n_positions sets FP8MLA_DEV_BAD_POSITION and its heads are not written.
+ * Requires 2 <= head_dim <= 8192, rot even, rot_offset + rot <= head_dim.  Any
+ * stride and alignment of the type works; 16-byte aligned tensors whose
+ * strides and rot_offset are multiples of 8 and rot of 16 go 8 pairs at a time. */
+FP8MLA_API fp8mla_status_t rotary_apply(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                                        int64_t q_out_token_stride, int64_t q_out_head_stride, int h_q, const void* k,
+                                        int64_t k_token_stride, int64_t k_head_stride, void* k_out,
+                                        int64_t k_out_token_stride, int64_t k_out_head_stride, int h_k,
+                                        fp8mla_dtype_t dtype, const void* positions, int positions_64,
+                                        const float* table, int64_t n_positions, int n_tokens, int head_dim, int rot,
+                                        int rot_offset, int interleaved, int inverse, fp8mla_stream_t stream);
+
+/* ---------------------------------------------------------- 4-bit cache ---
+ * A cached row of head_dim values is head_dim / 2 bytes of E2M1 codes (sign,
+ * 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6; the even
+ * dimension in the low nibble) and head_dim / 16 E4M3 block scales, with one
+ * float32 scale for the whole cache:
+ *   value = scale * s8[d / 16] * E2M1(code[d]).
+ * codes [num_blocks, h_kv, page_size, head_dim / 2], block scales
+ * [num_blocks, h_kv, page_size, head_dim / 16], both 16-byte aligned.  A
+ * calibrated scale is amax / (448 * 6).
+ *
+ * paged_kv_append -- a step's new K and V rows into their slots, K rotated on
+ * the way; optionally the step's queries rotated along.
+ *   k, v          bf16 [n_tokens, h_kv, head_dim] (strides in elements,
+ *                 multiples of 8; 16-byte aligned).  v and v_cache NULL: one
+ *                 cache only (the dense MLA cache is h_kv = 1, page 64, 576)
+ *   slot_mapping  int32 [n_tokens]: as fp8_paged_cache_write (a negative slot
+ *                 skips the token's K and V)
+ *   positions     int32 or int64 [n_tokens], with table.  A negative position
+ *                 is padding: nothing of the token is written; one >=
+ *                 n_positions sets FP8MLA_DEV_BAD_POSITION, likewise
+ *   table         as rotary_apply's, 16-byte aligned; NULL: no rotation (then
+ *                 q is NULL and positions are not read)
+ *   kv_dtype      FP8MLA_KV_E4M3: k_scale (one float32, written codes are
+ *                 E4M3(x fp32(1 / scale))) or k_row_scales (float32
+ *                 [num_blocks, h_kv, page_size], written: amax / 448), exactly
+ *                 one of them; FP8MLA_KV_E2M1: k_scale and k_block_scales
+ *                 (written).  The same for v
+ *   q, q_out      bf16 [n_tokens, h_q, head_dim] or NULL; q_out contiguous,
+ *                 rotated like K
+ * The rotated row is quantised from float32.  E4M3 rows follow
+ * fp8_paged_cache_write's arithmetic; an E2M1 block stores
+ * s8 = E4M3(amax * fp32(1 / fp32(6 scale))) and codes
+ * E2M1(x * fp32(1 / fp32(s8 scale))), 0 where s8 is 0.  Rounding is to nearest
+ * even with saturation.  Rows must be finite and scales normal floats > 0 for
+ * which 6 * 448 * scale and scale / 512 are normal too.  Two tokens with one
+ * slot race.  Requires head_dim a multiple of 16 in [16, 1024]; with a table
+ * rot a multiple of 16 and rot_offset of 8 (of 16 when interleaved); in E2M1
+ * with the half layout rot a multiple of 32 and rot_offset of 16. */
+FP8MLA_API fp8mla_status_t paged_kv_append(
+    const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+    int64_t v_head_stride, const int32_t* slot_mapping, int n_tokens, int h_kv, int head_dim, int page_size,
+    int num_blocks, fp8mla_kv_dtype_t kv_dtype, void* k_cache, void* v_cache, const float* k_scale,
+    const float* v_scale, float* k_row_scales, float* v_row_scales, void* k_block_scales, void* v_block_scales,
+    const void* positions, int positions_64, const float* table, int64_t n_positions, int rot, int rot_offset,
+    int interleaved, const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out, int h_q,
+    fp8mla_stream_t stream);
+
+/* paged_cache_read -- rows of a paged cache as bf16: out[i][h] is the row of
+ * slot slots[i], KV head h, dequantised in float32 and rounded once.
+ *   scales        as paged_kv_append: scale, row_scales, or scale and
+ *                 block_scales (E2M1)
+ *   out           bf16 [n, h_kv, head_dim], 16-byte aligned.  A negative slot
+ *                 gives zeros; one past the cache too, with FP8MLA_DEV_BAD_SLOT
+ * head_dim a multiple of 8 (16 for E2M1) up to 1024. */
+FP8MLA_API fp8mla_status_t paged_cache_read(const void* cache, fp8mla_kv_dtype_t kv_dtype, const float* scale,
+                                            const float* row_scales, const void* block_scales, const int32_t* slots,
+                                            int n, int h_kv, int head_dim, int page_size, int num_blocks, void* out,
+                                            fp8mla_stream_t stream);
+
+/* paged_gqa_decode_fp4 -- paged_gqa_decode_ext over 4-bit caches.
+ *   q            bf16 [bs, q_len, h_q, head_dim], 16-byte aligned
+ *   k_cache, v_cache, k_block_scales, v_block_scales  as above
+ *   k_scale, v_scale  float32 [1] each (device)
+ *   block_table, seqlens, spec_mask, window, sinks, out, lse  as
+ *                paged_gqa_decode_ext
+ *   num_splits   0 = auto (paged_gqa_fp4_num_splits for this GPU with the
+ *                block table's capacity); k >= 1 forced, at most one shard per
+ *                128 keys
+ *   workspace    >= paged_gqa_fp4_workspace_bytes of the split count, 256-byte
+ *                aligned; may be NULL when that is 0
+ * Products take K and V exactly and Q as it is; P is rounded to f16.
+ * Requires head_dim 64, 128 or 256, page_size 16, 32, 64, 128 or 256, q_len <=
+ * 16, h_q % h_kv == 0 and q_len * (h_q / h_kv) <= 128. */
+FP8MLA_API fp8mla_status_t paged_gqa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
+                                                const void* k_block_scales, const void* v_block_scales, int num_blocks,
+                                                const float* k_scale, const float* v_scale,
+                                                const int32_t* block_table, int max_blocks, const int32_t* seqlens,
+                                                float softmax_scale, int q_len, const uint8_t* spec_mask, int window,
+                                                const float* sinks, int num_splits, void* workspace,
+                                                size_t workspace_bytes, void* out, float* lse, int bs, int h_q,
+                                                int h_kv, int head_dim, int page_size, fp8mla_stream_t stream);
+
+/* Number of key shards paged_gqa_decode_fp4 uses for these arguments
+ * (num_splits as passed: 0 = auto), and its workspace with that many.  Host-only. */
+FP8MLA_API int paged_gqa_fp4_num_splits(int bs, int h_q, int h_kv, int max_seqlen, int q_len, int window, int num_sms,
+                                        int num_splits);
+FP8MLA_API size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int head_dim, int q_len, int splits);
 
 /* ------------------------------------------------------ no allocation ---
  * fp8mla_decode_no_alloc -- the dense MLA decode for callers that cannot

@@ -25,12 +25,14 @@ STATUS_NAMES = {0: "ok", 1: "invalid argument", 2: "unsupported KV cache encodin
 DOT_16BIT = 0
 DOT_FP8 = 1
 KV_E4M3, KV_E4M3FNUZ, KV_E5M2, KV_OTHER = 0, 1, 2, 3
+KV_E2M1 = 4  # the 4-bit cache: paged_kv_append, paged_cache_read, paged_gqa_decode_fp4
 
 DEV_WAIT_TIMEOUT = 0x1
 DEV_BAD_PAGE = 0x2
 DEV_BAD_SEQLEN = 0x4
 DEV_BAD_INDEX = 0x8
 DEV_BAD_SLOT = 0x10
+DEV_BAD_POSITION = 0x20
 
 MLA_D, MLA_DV, MLA_PAGE, MLA_ROWS = 576, 512, 64, 128
 
@@ -46,6 +48,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_int64
 _SZ = ctypes.c_size_t
 
 _SIGNATURES = {
@@ -67,6 +70,16 @@ _SIGNATURES = {
     "paged_gqa_ext_num_splits": (_I, [_I, _I, _I, _I, _I, _I, _I]),
     "fp8mla_decode_no_alloc": (_I, [_P, _P, _I, _I, _P, _I, _P, _P, _F, _I, _P, _P, _I, _I, _I, _I, _P]),
     "fp8_paged_cache_write": (_I, [_P, ctypes.c_int64, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "rotary_table": (_I, [_P, _I, _L, ctypes.c_double, _P, _P]),
+    "rotary_apply": (_I, [_P, _L, _L, _P, _L, _L, _I, _P, _L, _L, _P, _L, _L, _I, _I, _P, _I, _P, _L, _I, _I, _I, _I,
+                          _I, _I, _P]),
+    "paged_kv_append": (_I, [_P, _L, _L, _P, _L, _L, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                             _I, _P, _L, _I, _I, _I, _P, _L, _L, _P, _I, _P]),
+    "paged_cache_read": (_I, [_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "paged_gqa_decode_fp4": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _P, _F, _I, _P, _I, _P, _I, _P, _SZ, _P,
+                                  _P, _I, _I, _I, _I, _I, _P]),
+    "paged_gqa_fp4_num_splits": (_I, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "paged_gqa_fp4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "fp8mla_get_last_device_error": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "fp8mla_get_wait_timeout_site": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "fp8mla_set_wait_test": (_I, [ctypes.c_int32, ctypes.c_uint64]),
@@ -105,6 +118,35 @@ def _ptr(t) -> int | None:
 
 def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+class _Here:
+    """No device switch: the tensors' device is the current one."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE_CTX = _Here()
+
+
+def _on(device):
+    """Context in which ``device`` is the current one (launches and one-time setup go by the current device)."""
+    return _HERE_CTX if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+_SMS: dict[int, int] = {}
+
+
+def _sms() -> int:
+    """SM count of the current device, asked once per device."""
+    dev = torch.cuda.current_device()
+    if dev not in _SMS:
+        _SMS[dev] = num_sms(dev)
+    return _SMS[dev]
 
 
 def kv_dtype_code(t: torch.Tensor) -> int:
@@ -445,6 +487,408 @@ def paged_cache_write(x: torch.Tensor, slot_mapping: torch.Tensor, cache: torch.
                                        kv_dtype_code(cache4), _ptr(cache4), _ptr(tensor_scale),
                                        _ptr(token_scales), _stream(x3.device)),
            "fp8_paged_cache_write")
+
+
+# ----------------------------------------------------------------- rotary --
+
+
+def rotary_frequencies(rot_dim: int, theta: float = 10000.0, scaling: dict | None = None):
+    """(inv_freq float64 [rot_dim / 2] on the CPU, factor) for ``rotary_table``.
+
+    inv_freq[i] = theta ** (-2 i / rot_dim), stretched for contexts longer than the trained ones:
+      None                       as it is
+      dict(type="linear", factor)             every frequency divided by factor
+      dict(type="ntk", factor)                theta * factor ** (rot_dim / (rot_dim - 2))
+      dict(type="bands", factor, trained, low=1.0, high=4.0)
+          frequencies that turn fewer than `low` times over `trained` positions are divided by
+          factor, those that turn more than `high` times kept, those between blended
+      dict(type="yarn", factor, trained, fast=32.0, slow=1.0, attention=None)
+          the blend runs over the pair index, from the pair that turns `fast` times over `trained`
+          positions to the one that turns `slow` times; the table's factor is `attention`,
+          0.1 ln(factor) + 1 if that is None
+      dict(type="factors", factors, attention=1.0)   inv_freq[i] / factors[i]
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even")
+    if not (theta > 0 and math.isfinite(theta)):
+        raise ValueError("theta must be positive")
+    half = rot_dim // 2
+
+    def powers(base):
+        return [base ** (-2.0 * i / rot_dim) for i in range(half)]
+
+    def need(names, optional=()):
+        for n in names:
+            if n not in scaling:
+                raise ValueError(f"rotary scaling {kind!r} needs {n!r}")
+        extra = set(scaling) - {"type", *names, *optional}
+        if extra:
+            raise ValueError(f"rotary scaling {kind!r} does not take {sorted(extra)}")
+        for n in ("factor", "trained"):
+            if n in scaling and not scaling[n] > 0:
+                raise ValueError(f"{n} must be positive")
+
+    f, out_factor = powers(theta), 1.0
+    kind = None if scaling is None else scaling.get("type")
+    if kind is None:
+        if scaling is not None:
+            raise ValueError("rotary scaling needs a 'type'")
+    elif kind == "linear":
+        need(["factor"])
+        f = [x / scaling["factor"] for x in f]
+    elif kind == "ntk":
+        need(["factor"])
+        if rot_dim < 4:
+            raise ValueError("rotary scaling 'ntk' needs rot_dim >= 4")
+        f = powers(theta * scaling["factor"] ** (rot_dim / (rot_dim - 2)))
+    elif kind == "bands":
+        need(["factor", "trained"], ("low", "high"))
+        lo, hi = scaling.get("low", 1.0), scaling.get("high", 4.0)
+        if not hi > lo:
+            raise ValueError("high must be above low")
+        keep = [min(1.0, max(0.0, (scaling["trained"] * x / (2 * math.pi) - lo) / (hi - lo))) for x in f]
+        f = [x * k + x / scaling["factor"] * (1 - k) for x, k in zip(f, keep)]
+    elif kind == "yarn":
+        need(["factor", "trained"], ("fast", "slow", "attention"))
+        at = [rot_dim * math.log(scaling["trained"] / (turns * 2 * math.pi)) / (2 * math.log(theta))
+              for turns in (scaling.get("fast", 32.0), scaling.get("slow", 1.0))]
+        lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot_dim - 1)
+        keep = [1 - min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3))) for i in range(half)]
+        f = [x * k + x / scaling["factor"] * (1 - k) for x, k in zip(f, keep)]
+        out_factor = scaling.get("attention")
+        if out_factor is None:
+            out_factor = 0.1 * math.log(scaling["factor"]) + 1.0 if scaling["factor"] > 1 else 1.0
+    elif kind == "factors":
+        need(["factors"], ("attention",))
+        if len(scaling["factors"]) != half or not all(x > 0 for x in scaling["factors"]):
+            raise ValueError("factors must be rot_dim / 2 positive numbers")
+        f = [x / y for x, y in zip(f, scaling["factors"])]
+        out_factor = scaling.get("attention", 1.0)
+    else:
+        raise ValueError(f"rotary scaling type {kind!r}")
+    return torch.tensor(f, dtype=torch.float64), float(out_factor)
+
+
+def rotary_table(inv_freq: torch.Tensor, n_positions: int, *, factor: float = 1.0, device=None,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """float32 [n_positions, len(inv_freq), 2]: (cos, sin) of position * inv_freq, times factor.
+    inv_freq float64 [rot / 2] (moved to `device`, by default its own or the current one)."""
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be float64 [rot / 2]")
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if device is None and inv_freq.is_cuda:
+        dev = inv_freq.device
+    if out is not None:
+        _need(out, "out", torch.float32, 3)
+        dev = out.device
+        if tuple(out.shape) != (n_positions, inv_freq.shape[0], 2):
+            raise ValueError("out must be [n_positions, rot / 2, 2]")
+    else:
+        out = torch.empty((n_positions, inv_freq.shape[0], 2), dtype=torch.float32, device=dev)
+    f = inv_freq.to(out.device).contiguous()
+    with _on(out.device):
+        _check(lib().rotary_table(_ptr(f), f.shape[0], n_positions, float(factor), _ptr(out), _stream(out.device)),
+               "rotary_table")
+    return out
+
+
+_ROTARY_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _heads(x, name, dtype, dev, n, head_dim=None):
+    """Checks rows [n, heads, head_dim] whose heads are contiguous; returns (token stride, head stride)."""
+    if x.device != dev or x.dtype != dtype or x.dim() != 3 or x.shape[0] != n:
+        raise ValueError(f"{name} must be {dtype} [{n}, heads, head_dim] on {dev}")
+    if head_dim is not None and x.shape[2] != head_dim:
+        raise ValueError(f"{name} must have head_dim {head_dim}")
+    st = x.stride()
+    if st[2] != 1 and x.shape[2] > 1:
+        raise ValueError(f"{name}: the dims of a head must be contiguous")
+    return st[0], st[1]
+
+
+def _positions(positions, dev, n):
+    if positions.device != dev or positions.dim() != 1 or positions.shape[0] != n or not positions.is_contiguous():
+        raise ValueError(f"positions must be contiguous [{n}] on {dev}")
+    if positions.dtype == torch.int32:
+        return 0
+    if positions.dtype == torch.int64:
+        return 1
+    raise ValueError("positions must be int32 or int64")
+
+
+def _table(table, dev):
+    if table.device != dev or table.dtype != torch.float32 or table.dim() != 3 or table.shape[2] != 2 \
+            or not table.is_contiguous():
+        raise ValueError(f"table must be contiguous float32 [n_positions, rot / 2, 2] on {dev}")
+    return table.shape[0], 2 * table.shape[1]
+
+
+def rotary_apply(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: torch.Tensor, *,
+                 interleaved: bool = False, rot_offset: int = 0, inverse: bool = False,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
+    """Rotate query and key heads by their positions.  q [n, h_q, head_dim] and k [n, h_k, head_dim]
+    or None, both bfloat16, float16 or float32 (strided along tokens and heads); positions int32 or
+    int64 [n]; table float32 [n_positions, rot / 2, 2] (``rotary_table``).
+
+    Dims [rot_offset, rot_offset + rot) of a head turn in pairs (i, i + rot / 2), or (2i, 2i + 1) when
+    interleaved; the others are copied.  inverse=True turns back (the transpose: the gradient of the
+    rotation).  A token with a negative position is padding: its output rows are left as they are.
+    q_out / k_out may be q / k (in place); new contiguous tensors when not given.  Returns (q_out, k_out)."""
+    dev, dtype = q.device, q.dtype
+    if not q.is_cuda or dtype not in _ROTARY_TYPES:
+        raise ValueError("q must be a CUDA tensor of bfloat16, float16 or float32")
+    n = q.shape[0] if q.dim() else 0
+    qs = _heads(q, "q", dtype, dev, n)
+    hd = q.shape[2]
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dtype, device=dev)
+    qo = _heads(q_out, "q_out", dtype, dev, n, hd)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    ks = ko = (0, 0)
+    h_k = 0
+    if k is not None:
+        ks = _heads(k, "k", dtype, dev, n, hd)
+        h_k = k.shape[1]
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=dtype, device=dev)
+        ko = _heads(k_out, "k_out", dtype, dev, n, hd)
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have k's shape")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    wide = _positions(positions, dev, n)
+    n_pos, rot = _table(table, dev)
+    with _on(dev):
+        _check(lib().rotary_apply(q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), qo[0], qo[1], q.shape[1], _ptr(k),
+                                  ks[0], ks[1], _ptr(k_out), ko[0], ko[1], h_k, _ROTARY_TYPES[dtype],
+                                  positions.data_ptr(), wide, table.data_ptr(), n_pos, n, hd, rot, rot_offset,
+                                  1 if interleaved else 0, 1 if inverse else 0, _stream(dev)),
+               "rotary_apply")
+    return q_out, k_out
+
+
+# ---------------------------------------------- append, read back, 4 bits --
+
+
+_FP4_TYPES = tuple(x for x in (torch.uint8, getattr(torch, "float4_e2m1fn_x2", None)) if x is not None)
+_BYTE_SCALES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _cache4(cache, name, dev):
+    """A cache as [num_blocks, h_kv, page, bytes a row]; the dense MLA form [num_pages, page, d] is one head."""
+    if cache.device != dev or not cache.is_contiguous() or cache.dim() not in (3, 4):
+        raise ValueError(f"{name} must be contiguous [num_blocks, h_kv, page, ...] on {dev}")
+    return tuple(cache.shape) if cache.dim() == 4 else (cache.shape[0], 1, cache.shape[1], cache.shape[2])
+
+
+def _cache_scales(name, shape, hd, kv_dtype, scale, row_scales, block_scales, dev):
+    """The scales that go with a cache of `shape` rows: which are given, and their shapes."""
+    if kv_dtype == KV_E2M1:
+        if scale is None or block_scales is None or row_scales is not None:
+            raise ValueError(f"{name}: a 4-bit cache takes one scale and its block scales")
+        if block_scales.device != dev or block_scales.dtype not in _BYTE_SCALES or not block_scales.is_contiguous() \
+                or block_scales.numel() != shape[0] * shape[1] * shape[2] * (hd // 16) \
+                or block_scales.shape[-1] != hd // 16:
+            raise ValueError(f"{name}: block scales must be contiguous E4M3 [num_blocks, h_kv, page, head_dim / 16]")
+    elif (scale is None) == (row_scales is None):
+        raise ValueError(f"{name}: give one scale or one per row")
+    if scale is not None and (scale.device != dev or scale.dtype != torch.float32 or scale.numel() != 1):
+        raise ValueError(f"{name}: the scale must be one float32 on {dev}")
+    if row_scales is not None and (row_scales.device != dev or row_scales.dtype != torch.float32
+                                   or not row_scales.is_contiguous()
+                                   or row_scales.numel() != shape[0] * shape[1] * shape[2]
+                                   or row_scales.shape[-1] != shape[2]):
+        raise ValueError(f"{name}: row scales must be contiguous float32 [num_blocks, h_kv, page]")
+
+
+def _kv_code(cache, block_scales) -> int:
+    """Block scales mark a 4-bit cache; without them the cache is E4M3 (or refused by the library)."""
+    if block_scales is not None:
+        return KV_E2M1 if cache.dtype in _FP4_TYPES else KV_OTHER
+    return kv_dtype_code(cache)
+
+
+def paged_kv_append(k: torch.Tensor, v: torch.Tensor | None, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                    v_cache: torch.Tensor | None = None, *, positions: torch.Tensor | None = None,
+                    table: torch.Tensor | None = None, interleaved: bool = False, rot_offset: int = 0,
+                    k_scale=None, v_scale=None, k_row_scales=None, v_row_scales=None, k_block_scales=None,
+                    v_block_scales=None, q: torch.Tensor | None = None, q_out: torch.Tensor | None = None):
+    """Write new K and V rows into paged caches in one launch, K rotated by its position on the way.
+
+    k, v bf16 [n, h_kv, head_dim] (strided along tokens and heads; v and v_cache may be None); caches
+    E4M3 (or uint8) [num_blocks, h_kv, page, head_dim] with k_scale (float32 [1]) or k_row_scales
+    (float32 [num_blocks, h_kv, page], written), or 4-bit (uint8 [num_blocks, h_kv, page,
+    head_dim / 2]) with k_scale and k_block_scales (E4M3 [num_blocks, h_kv, page, head_dim / 16],
+    written); the same for V.  The dense MLA cache [num_pages, page, d] takes k [n, d] or [n, 1, d].
+    slot_mapping int32 [n] (block * page + offset; negative = skip K and V).  With a table
+    (``rotary_table``) and positions (int32 or int64 [n]; negative = padding, nothing is written) K's
+    dims [rot_offset, rot_offset + rot) turn as in ``rotary_apply``, and queries q bf16
+    [n, h_q, head_dim] can be rotated along: returns them (q_out, new when not given), or None."""
+    dev = k.device
+    if not k.is_cuda or k.dtype != torch.bfloat16:
+        raise ValueError("k must be a CUDA bf16 tensor")
+    if k.dim() == 2:
+        k = k.unsqueeze(1)
+    if v is not None and v.dim() == 2:
+        v = v.unsqueeze(1)
+    n = k.shape[0]
+    ks = _heads(k, "k", torch.bfloat16, dev, n)
+    h_kv, hd = k.shape[1], k.shape[2]
+    code = _kv_code(k_cache, k_block_scales)
+    shape = _cache4(k_cache, "k_cache", dev)
+    if shape[1] != h_kv or shape[3] != (hd // 2 if code == KV_E2M1 else hd):
+        raise ValueError("k and k_cache shapes disagree")
+    _cache_scales("k", shape, hd, code, k_scale, k_row_scales, k_block_scales, dev)
+    if slot_mapping.device != dev or slot_mapping.dtype != torch.int32 or slot_mapping.dim() != 1 \
+            or slot_mapping.shape[0] != n or not slot_mapping.is_contiguous():
+        raise ValueError(f"slot_mapping must be contiguous int32 [{n}] on {dev}")
+    vs = (0, 0)
+    if (v is None) != (v_cache is None):
+        raise ValueError("v and v_cache go together")
+    if v is not None:
+        vs = _heads(v, "v", torch.bfloat16, dev, n, hd)
+        if v.shape != k.shape or _cache4(v_cache, "v_cache", dev) != shape or _kv_code(v_cache, v_block_scales) != code:
+            raise ValueError("v and v_cache must match k and k_cache")
+        _cache_scales("v", shape, hd, code, v_scale, v_row_scales, v_block_scales, dev)
+    elif v_scale is not None or v_row_scales is not None or v_block_scales is not None:
+        raise ValueError("scales for v without v")
+    wide, n_pos, rot = 0, 0, 0
+    if table is not None:
+        if positions is None:
+            raise ValueError("a table needs positions")
+        wide = _positions(positions, dev, n)
+        n_pos, rot = _table(table, dev)
+    qs, h_q = (0, 0), 0
+    if q is not None:
+        if table is None:
+            raise ValueError("q is rotated by a table: give one")
+        qs = _heads(q, "q", torch.bfloat16, dev, n, hd)
+        h_q = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        if q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or q_out.device != dev \
+                or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous bf16 of q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    with _on(dev):
+        _check(lib().paged_kv_append(k.data_ptr(), ks[0], ks[1], _ptr(v), vs[0], vs[1], slot_mapping.data_ptr(), n,
+                                     h_kv, hd, shape[2], shape[0], code, k_cache.data_ptr(), _ptr(v_cache),
+                                     _ptr(k_scale), _ptr(v_scale), _ptr(k_row_scales), _ptr(v_row_scales),
+                                     _ptr(k_block_scales), _ptr(v_block_scales),
+                                     None if table is None else positions.data_ptr(), wide, _ptr(table), n_pos, rot,
+                                     rot_offset, 1 if interleaved else 0, _ptr(q), qs[0], qs[1], _ptr(q_out), h_q,
+                                     _stream(dev)),
+               "paged_kv_append")
+    return q_out
+
+
+def paged_cache_read(cache: torch.Tensor, slots: torch.Tensor, *, scale=None, row_scales=None, block_scales=None,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows of a paged cache as bf16 [n, h_kv, head_dim], dequantised in float32 and rounded once.
+    cache and its scales as for ``paged_kv_append``; slots int32 [n] (negative = a row of zeros)."""
+    dev = cache.device
+    if not cache.is_cuda:
+        raise ValueError("cache must be a CUDA tensor")
+    code = _kv_code(cache, block_scales)
+    shape = _cache4(cache, "cache", dev)
+    hd = shape[3] * (2 if code == KV_E2M1 else 1)
+    _cache_scales("cache", shape, hd, code, scale, row_scales, block_scales, dev)
+    if slots.device != dev or slots.dtype != torch.int32 or slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError(f"slots must be contiguous int32 [n] on {dev}")
+    n = slots.shape[0]
+    if out is None:
+        out = torch.empty((n, shape[1], hd), dtype=torch.bfloat16, device=dev)
+    if tuple(out.shape) != (n, shape[1], hd) or out.dtype != torch.bfloat16 or out.device != dev \
+            or not out.is_contiguous():
+        raise ValueError("out must be contiguous bf16 [n, h_kv, head_dim]")
+    with _on(dev):
+        _check(lib().paged_cache_read(cache.data_ptr(), code, _ptr(scale), _ptr(row_scales), _ptr(block_scales),
+                                      slots.data_ptr(), n, shape[1], hd, shape[2], shape[0], out.data_ptr(),
+                                      _stream(dev)),
+               "paged_cache_read")
+    return out
+
+
+def gqa_fp4_num_splits(bs: int, h_q: int, h_kv: int, max_seqlen: int, q_len: int = 1, window: int = 0,
+                       num_splits: int = 0, sms: int | None = None) -> int:
+    return lib().paged_gqa_fp4_num_splits(bs, h_q, h_kv, max_seqlen, q_len, window, _sms() if sms is None else sms,
+                                          num_splits)
+
+
+def gqa_fp4_workspace_bytes(bs: int, h_q: int, h_kv: int, head_dim: int, q_len: int, splits: int) -> int:
+    return lib().paged_gqa_fp4_workspace_bytes(bs, h_q, h_kv, head_dim, q_len, splits)
+
+
+def paged_gqa_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         k_block_scales: torch.Tensor, v_block_scales: torch.Tensor, block_table: torch.Tensor,
+                         seqlens: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                         softmax_scale: float | None = None, spec_mask=None, window: int = 0, sinks=None,
+                         num_splits: int = 0, max_seqlen: int | None = None, out=None, lse=None, workspace=None):
+    """Paged GQA decode over 4-bit caches.  q bf16 [bs, q_len, h_q, hd] (the sequence's last q_len cache
+    positions) or [bs, h_q, hd]; caches uint8 [num_blocks, h_kv, page, hd / 2] (two E2M1 codes a byte),
+    block scales E4M3 [num_blocks, h_kv, page, hd / 16], k_scale / v_scale float32 [1]; block_table int32
+    [bs, max_blocks], seqlens int32 [bs]; spec_mask, window and sinks as ``paged_gqa_decode_ext``.
+    Returns (out bf16 like q, lse float32 without its last dim)."""
+    dev = q.device
+    if not q.is_cuda or q.dtype != torch.bfloat16 or q.dim() not in (3, 4) or not q.is_contiguous():
+        raise ValueError("q must be a contiguous CUDA bf16 tensor [bs, q_len, h_q, hd] or [bs, h_q, hd]")
+    shape = q.shape
+    bs, h_q, hd = shape[0], shape[-2], shape[-1]
+    q_len = shape[1] if q.dim() == 4 else 1
+    kshape = _cache4(k_cache, "k_cache", dev)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype \
+            or v_cache.device != dev or not v_cache.is_contiguous():
+        raise ValueError("k_cache and v_cache must match")
+    if k_cache.dtype not in _FP4_TYPES:
+        raise FP8MLAError(2, "paged_gqa_decode_fp4")
+    if kshape[3] * 2 != hd:
+        raise ValueError("head_dim mismatch")
+    num_blocks, h_kv, page = kshape[:3]
+    _cache_scales("k", kshape, hd, KV_E2M1, k_scale, None, k_block_scales, dev)
+    _cache_scales("v", kshape, hd, KV_E2M1, v_scale, None, v_block_scales, dev)
+    if block_table.device != dev or block_table.dtype != torch.int32 or block_table.dim() != 2 \
+            or block_table.shape[0] != bs or not block_table.is_contiguous():
+        raise ValueError(f"block_table must be contiguous int32 [{bs}, max_blocks] on {dev}")
+    if seqlens.device != dev or seqlens.dtype != torch.int32 or tuple(seqlens.shape) != (bs,) \
+            or not seqlens.is_contiguous():
+        raise ValueError(f"seqlens must be contiguous int32 [{bs}] on {dev}")
+    if spec_mask is not None and (spec_mask.device != dev or spec_mask.dtype != torch.uint8
+                                  or tuple(spec_mask.shape) != (bs, q_len, q_len) or not spec_mask.is_contiguous()):
+        raise ValueError("spec_mask must be contiguous uint8 [bs, q_len, q_len]")
+    if sinks is not None and (sinks.device != dev or sinks.dtype != torch.float32 or tuple(sinks.shape) != (h_q,)
+                              or not sinks.is_contiguous()):
+        raise ValueError("sinks must be contiguous float32 [h_q]")
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(hd)
+    max_blocks = block_table.shape[1]
+    capacity = max_blocks * page
+    with _on(dev):
+        splits = gqa_fp4_num_splits(bs, h_q, h_kv, min(capacity if max_seqlen is None else max_seqlen, capacity,
+                                                       0x7FFFFF00), q_len, window, num_splits) \
+            if num_splits >= 0 else num_splits  # a negative count is the library's to refuse
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        elif out.shape != shape or out.dtype != torch.bfloat16 or out.device != dev or not out.is_contiguous():
+            raise ValueError("out must be contiguous bf16 of q's shape")
+        if lse is None:
+            lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        elif lse.shape != shape[:-1] or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous float32 of q's shape without head_dim")
+        if workspace is None and splits > 1:
+            workspace = torch.empty((gqa_fp4_workspace_bytes(bs, h_q, h_kv, hd, q_len, splits),), dtype=torch.uint8,
+                                    device=dev)
+        _check(lib().paged_gqa_decode_fp4(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                          k_block_scales.data_ptr(), v_block_scales.data_ptr(), num_blocks,
+                                          k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), max_blocks,
+                                          seqlens.data_ptr(), float(softmax_scale), q_len, _ptr(spec_mask),
+                                          int(window), _ptr(sinks), splits, _ptr(workspace),
+                                          0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                          out.data_ptr(), lse.data_ptr(), bs, h_q, h_kv, hd, page, _stream(dev)),
+               "paged_gqa_decode_fp4")
+    return out, lse
 
 
 def wait_timeout_site(device=None):

@@ -46,10 +46,6 @@ __device__ uint32_t g_status_cw;
 
 constexpr int kCwThreads = 256;
 
-// n / d by a multiply-high (see make_fast_div)
-struct FastDiv {
-  uint32_t d, m, s;
-};
 constexpr int kCwMaxChunks = 4;  // 16-byte chunks (8 bf16) a lane holds per row; head_dim <= 8 * 32 * 4
 
 constexpr float kTinyAmax = 5.42101086242752217e-20f;  // 2^-64
@@ -69,10 +65,6 @@ __device__ __forceinline__ uint32_t encode_bf16x2(uint32_t w, float inv) {
 __device__ __forceinline__ uint32_t encode_bf16x2_lifted(uint32_t w, float inv) {
   return pack_e4m3x2(__fmul_rn(__fmul_rn(bf16_lo(w), kTinyLift), inv),
                      __fmul_rn(__fmul_rn(bf16_hi(w), kTinyLift), inv));
-}
-
-__device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv& f) {
-  return f.d == 1 ? n : (__umulhi(n, f.m) >> f.s);
 }
 
 // Rows per group per step: two while a lane holds at most two chunks of a
@@ -225,35 +217,6 @@ __global__ void __launch_bounds__(kCwThreads, 4) cache_write_kernel(
     if (!more2) break;
     base = nb2;
   }
-}
-
-// Constants of fast_div for divisor d (numerators below 2^31): with
-// l = ceil(log2 d), m = floor(2^(31 + l) / d) + 1 < 2^32 gives
-// n / d = (n * m) >> (31 + l) for every n < 2^31 (d = 1 is passed through).
-FastDiv make_fast_div(int d) {
-  FastDiv f;
-  f.d = static_cast<uint32_t>(d);
-  f.m = 0;
-  f.s = 0;
-  if (d <= 1) return f;
-  uint32_t l = 0;
-  while ((1ull << l) < static_cast<uint64_t>(d)) ++l;
-  f.m = static_cast<uint32_t>((1ull << (31 + l)) / static_cast<uint64_t>(d) + 1);
-  f.s = l - 1;
-  return f;
-}
-
-// SM count of the current device, queried once per device (152 if unknown).
-int device_sms() {
-  static std::atomic<int> sms[64];  // zero-initialised: static storage
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-  int n = sms[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 152;
-    sms[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
 }
 
 template <int kL, int kC>

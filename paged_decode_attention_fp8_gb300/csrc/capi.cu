@@ -9,7 +9,10 @@
 #include "cache_write.h"
 #include "fp8mla.h"
 #include "gqa_decode.h"
+#include "gqa_fp4.h"
+#include "kv_append.h"
 #include "mla_decode.h"
+#include "rotary.h"
 #include "sparse_mla.h"
 
 namespace fp8mla {
@@ -408,12 +411,146 @@ fp8mla_status_t fp8_paged_cache_write(const void* x, int64_t x_token_stride, con
   return cache_write_entry(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+fp8mla_status_t rotary_table(const double* inv_freq, int half, int64_t n_positions, double factor, float* table,
+                             fp8mla_stream_t stream) {
+  return rotary_table_entry(inv_freq, half, n_positions, factor, table, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fp8mla_status_t rotary_apply(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                             int64_t q_out_token_stride, int64_t q_out_head_stride, int h_q, const void* k,
+                             int64_t k_token_stride, int64_t k_head_stride, void* k_out, int64_t k_out_token_stride,
+                             int64_t k_out_head_stride, int h_k, fp8mla_dtype_t dtype, const void* positions,
+                             int positions_64, const float* table, int64_t n_positions, int n_tokens, int head_dim,
+                             int rot, int rot_offset, int interleaved, int inverse, fp8mla_stream_t stream) {
+  RotaryArgs a;
+  a.x[0] = q, a.x[1] = k;
+  a.out[0] = q_out, a.out[1] = k_out;
+  a.x_token[0] = q_token_stride, a.x_token[1] = k_token_stride;
+  a.x_head[0] = q_head_stride, a.x_head[1] = k_head_stride;
+  a.out_token[0] = q_out_token_stride, a.out_token[1] = k_out_token_stride;
+  a.out_head[0] = q_out_head_stride, a.out_head[1] = k_out_head_stride;
+  a.heads[0] = h_q, a.heads[1] = h_k;
+  a.positions = positions;
+  a.positions_64 = positions_64;
+  a.table = table;
+  a.n_positions = n_positions;
+  a.n_tokens = n_tokens;
+  a.head_dim = head_dim;
+  a.rot = rot;
+  a.rot_offset = rot_offset;
+  a.interleaved = interleaved;
+  a.inverse = inverse;
+  a.dtype = dtype;
+  return rotary_apply_entry(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fp8mla_status_t paged_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                                int64_t v_token_stride, int64_t v_head_stride, const int32_t* slot_mapping,
+                                int n_tokens, int h_kv, int head_dim, int page_size, int num_blocks,
+                                fp8mla_kv_dtype_t kv_dtype, void* k_cache, void* v_cache, const float* k_scale,
+                                const float* v_scale, float* k_row_scales, float* v_row_scales, void* k_block_scales,
+                                void* v_block_scales, const void* positions, int positions_64, const float* table,
+                                int64_t n_positions, int rot, int rot_offset, int interleaved, const void* q,
+                                int64_t q_token_stride, int64_t q_head_stride, void* q_out, int h_q,
+                                fp8mla_stream_t stream) {
+  KvAppendArgs a;
+  a.side[0] = CacheSide{k, k_token_stride, k_head_stride, k_cache, k_scale, k_row_scales, k_block_scales};
+  a.side[1] = CacheSide{v, v_token_stride, v_head_stride, v_cache, v_scale, v_row_scales, v_block_scales};
+  a.q = q;
+  a.q_token = q_token_stride;
+  a.q_head = q_head_stride;
+  a.q_out = q_out;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.positions_64 = positions_64;
+  a.table = table;
+  a.n_positions = n_positions;
+  a.rot = rot;
+  a.rot_offset = rot_offset;
+  a.interleaved = interleaved;
+  a.n_tokens = n_tokens;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.head_dim = head_dim;
+  a.page_size = page_size;
+  a.num_blocks = num_blocks;
+  a.kv_dtype = kv_dtype;
+  return kv_append_entry(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fp8mla_status_t paged_cache_read(const void* cache, fp8mla_kv_dtype_t kv_dtype, const float* scale,
+                                 const float* row_scales, const void* block_scales, const int32_t* slots, int n,
+                                 int h_kv, int head_dim, int page_size, int num_blocks, void* out,
+                                 fp8mla_stream_t stream) {
+  CacheReadArgs a;
+  a.cache = cache;
+  a.scale = scale;
+  a.row_scales = row_scales;
+  a.block_scales = block_scales;
+  a.slots = slots;
+  a.out = out;
+  a.n = n;
+  a.h_kv = h_kv;
+  a.head_dim = head_dim;
+  a.page_size = page_size;
+  a.num_blocks = num_blocks;
+  a.kv_dtype = kv_dtype;
+  return cache_read_entry(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fp8mla_status_t paged_gqa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
+                                     const void* k_block_scales, const void* v_block_scales, int num_blocks,
+                                     const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                     int max_blocks, const int32_t* seqlens, float softmax_scale, int q_len,
+                                     const uint8_t* spec_mask, int window, const float* sinks, int num_splits,
+                                     void* workspace, size_t workspace_bytes, void* out, float* lse, int bs, int h_q,
+                                     int h_kv, int head_dim, int page_size, fp8mla_stream_t stream) {
+  Fp4DecodeArgs a;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_block_scales = k_block_scales;
+  a.v_block_scales = v_block_scales;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_table = block_table;
+  a.seqlens = seqlens;
+  a.spec_mask = spec_mask;
+  a.sinks = sinks;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.out = out;
+  a.lse = lse;
+  a.softmax_scale = softmax_scale;
+  a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks;
+  a.q_len = q_len;
+  a.window = window;
+  a.num_splits = num_splits;
+  a.bs = bs;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.head_dim = head_dim;
+  a.page_size = page_size;
+  return fp4_decode_entry(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int paged_gqa_fp4_num_splits(int bs, int h_q, int h_kv, int max_seqlen, int q_len, int window, int num_sms,
+                             int num_splits) {
+  return fp4_choose_splits(bs, h_q, h_kv, max_seqlen, q_len, window, num_sms, num_splits);
+}
+
+size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int head_dim, int q_len, int splits) {
+  return fp4_workspace_bytes(bs, h_q, h_kv, head_dim, q_len, splits);
+}
+
 fp8mla_status_t fp8mla_get_last_device_error(fp8mla_stream_t stream, uint32_t* code_out) {
   if (code_out == nullptr) return FP8MLA_ERR_INVALID_ARG;
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return FP8MLA_ERR_CUDA;
   *code_out = mla_read_and_clear_status() | metadata_read_and_clear_status() |
               sparse_read_and_clear_status() | gqa_read_and_clear_status() |
-              cache_write_read_and_clear_status();
+              cache_write_read_and_clear_status() | rotary_read_and_clear_status() |
+              kv_append_read_and_clear_status() | fp4_read_and_clear_status();
   return FP8MLA_OK;
 }
 

@@ -167,4 +167,66 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, si
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// The end of one output row: key weights summed to l against reference m (log2
+// units of the scaled scores), an optional sink logit `sink` (natural units,
+// -inf = none) joining the denominator once.  Returns the output factor f
+// (times the accumulated P.V) and the row's LSE (natural log).  No key and no
+// sink: f = 0, LSE -inf; no key with a sink: f = 0, LSE = sink.
+__device__ __forceinline__ void finish_row(float m, float l, float sink, float v_scale, float* f, float* lse) {
+  if (sink == kNegInf) {
+    *f = l > 0.f ? v_scale / l : 0.f;
+    *lse = l > 0.f ? (m + lg2_approx(l)) * kLn2 : kNegInf;
+    return;
+  }
+  const float sk2 = sink * kLog2e;
+  if (!(l > 0.f)) {
+    *f = 0.f;
+    *lse = sink;
+    return;
+  }
+  const float mm = fmaxf(m, sk2);
+  const float wk = ex2_approx(m - mm);
+  const float den = l * wk + ex2_approx(sk2 - mm);
+  *f = v_scale * wk / den;
+  *lse = (mm + lg2_approx(den)) * kLn2;
+}
+
+// n / d by a multiply-high (see make_fast_div)
+struct FastDiv {
+  uint32_t d, m, s;
+};
+
+__device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv& f) {
+  return f.d == 1 ? n : (__umulhi(n, f.m) >> f.s);
+}
+
+// Constants of fast_div for divisor d (numerators below 2^31): with
+// l = ceil(log2 d), m = floor(2^(31 + l) / d) + 1 < 2^32 gives
+// n / d = (n * m) >> (31 + l) for every n < 2^31 (d = 1 is passed through).
+inline FastDiv make_fast_div(int d) {
+  FastDiv f;
+  f.d = static_cast<uint32_t>(d);
+  f.m = 0;
+  f.s = 0;
+  if (d <= 1) return f;
+  uint32_t l = 0;
+  while ((1ull << l) < static_cast<uint64_t>(d)) ++l;
+  f.m = static_cast<uint32_t>((1ull << (31 + l)) / static_cast<uint64_t>(d) + 1);
+  f.s = l - 1;
+  return f;
+}
+
+// SM count of the current device, queried once per device (152 if unknown).
+inline int device_sms() {
+  static std::atomic<int> sms[64];  // zero-initialised: static storage
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  int n = sms[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 152;
+    sms[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 }  // namespace fp8mla

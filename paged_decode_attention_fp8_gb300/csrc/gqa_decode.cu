@@ -97,30 +97,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
-// The end of one output row: key weights summed to l against reference m (log2
-// units of the scaled scores), an optional sink logit `sink` (natural units,
-// -inf = none) joining the denominator once.  Returns the output factor f
-// (times the accumulated P.V) and the row's LSE (natural log).  No key and no
-// sink: f = 0, LSE -inf; no key with a sink: f = 0, LSE = sink.
-__device__ __forceinline__ void finish_row(float m, float l, float sink, float v_scale, float* f, float* lse) {
-  if (sink == kNegInf) {
-    *f = l > 0.f ? v_scale / l : 0.f;
-    *lse = l > 0.f ? (m + lg2_approx(l)) * kLn2 : kNegInf;
-    return;
-  }
-  const float sk2 = sink * kLog2e;
-  if (!(l > 0.f)) {
-    *f = 0.f;
-    *lse = sink;
-    return;
-  }
-  const float mm = fmaxf(m, sk2);
-  const float wk = ex2_approx(m - mm);
-  const float den = l * wk + ex2_approx(sk2 - mm);
-  *f = v_scale * wk / den;
-  *lse = (mm + lg2_approx(den)) * kLn2;
-}
-
 // ------------------------------------------------------------------------
 // The decode kernel: E4M3 operands straight from the TMA tiles, Q and P as two
 // E4M3 terms (see the file comment).

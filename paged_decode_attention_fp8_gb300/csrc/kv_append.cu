@@ -1,0 +1,553 @@
+// Appending a step's K and V to a paged cache with the rotary position applied
+// on the way, and reading cached rows back as bf16.
+//
+// Append: K's row (token, head) is rotated (see rotary.cu: two float32
+// products and a sum a value), V's is taken as it is; both are quantised from
+// float32, without a rounding to bf16 between, and land in the token's slot:
+//   E4M3, per-tensor scale: code = E4M3(x * inv), inv = fp32(1 / scale)
+//   E4M3, per-row scales:   scale = fp32(amax / 448), inv = fp32(448 / amax)
+//                           (1 for a zero row; a row with amax < 2^-64 is
+//                           lifted by 2^64 first), as the cache write does
+//   E2M1 in blocks of 16:   s8 = E4M3(amax * fp32(1 / fp32(6 scale))),
+//                           code = E2M1(x * fp32(1 / fp32(s8 * scale))),
+//                           0 where s8 is 0
+// Every float operation and conversion rounds to nearest even, conversions
+// saturate.  The same launch can rotate the step's queries (bf16 in and out).
+//
+// HBM-bound: 2 bytes in and 1 (or 9/16) out per value.  A group of L lanes
+// owns a row and each lane two 16-byte chunks of it at a time: those of a
+// rotated piece are partners (half layout: c and c + rot / 16, so a rotation
+// stays in the lane; interleaved: neighbours), the others neighbours.  A block
+// of 16 values is a lane's two chunks, or in the half layout the same chunk of
+// two neighbouring lanes: one shuffle.  K, V and Q rows are three classes of
+// CTAs of one grid; a warp takes kRows rows per group at a time, their loads
+// issued before the first is worked on.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "common.cuh"
+#include "kv_append.h"
+
+namespace fp8mla {
+namespace {
+
+__device__ uint32_t g_status_append;
+
+constexpr int kThreads = 256;
+constexpr int kMaxHeadDim = 1024;
+constexpr float kTinyAmax = 5.42101086242752217e-20f;  // 2^-64
+constexpr float kTinyLift = 1.84467440737095516e19f;   // 2^64
+
+enum Kind { kTensor = 0, kRowScales = 1, kFp4 = 2, kQuery = 3 };
+
+struct Source {
+  const uint16_t* x;
+  int64_t token, head;
+  uint8_t* out;        // cache, or the rotated queries
+  const float* scale;
+  float* row_scales;
+  uint8_t* block_scales;
+  FastDiv heads;
+  uint32_t rows;       // tokens * heads
+};
+
+struct Params {
+  Source src[3];       // K, V, Q
+  const int32_t* slots;
+  const void* positions;
+  const float2* table;  // null: no rotation
+  int64_t n_positions;
+  FastDiv page;
+  uint32_t num_slots;
+  int positions_64, rot, rot_offset, interleaved, head_dim;
+  uint32_t first[4];   // CTAs [first[i], first[i + 1]) take class i
+};
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
+  x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
+  x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
+}
+
+__device__ __forceinline__ float amax8(const float (&x)[8]) {
+  float m = fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2]));
+  m = fmax3(m, fabsf(x[3]), fabsf(x[4]));
+  m = fmax3(m, fabsf(x[5]), fabsf(x[6]));
+  return fmaxf(m, fabsf(x[7]));
+}
+
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], inv);
+  return make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
+}
+
+// One row's piece of a lane: chunks c0 and c1 (8 values each) as floats.
+struct Piece {
+  float a[8], b[8];
+};
+
+// kL lanes a row, kP pairs of chunks a lane, kRows rows a group at a time.
+template <int kL, int kP, int kKind>
+__device__ __forceinline__ void run_class(const Params& prm, const Source& src, bool rotate, uint32_t cta,
+                                          uint32_t ctas) {
+  constexpr int kRows = kP == 1 ? 2 : 1;
+  constexpr int kWarpRows = 32 / kL * kRows;
+  const int lane = threadIdx.x % 32, sub = lane % kL, grp = lane / kL;
+  const int pairs = prm.head_dim / 16;
+  const int rot_pairs = rotate ? prm.rot / 16 : 0;
+  const int off_chunk = prm.rot_offset / 8;
+  const bool half = rotate && !prm.interleaved;
+  // the lane's chunks and whether they turn; half layout: rotated pairs first, then the rest in order
+  int c0[kP], c1[kP];
+  bool turn[kP], live[kP];
+#pragma unroll
+  for (int j = 0; j < kP; ++j) {
+    const int p = sub + j * kL;
+    live[j] = p < pairs;
+    if (half) {
+      turn[j] = p < rot_pairs;
+      if (turn[j]) {
+        c0[j] = off_chunk + p;
+        c1[j] = c0[j] + rot_pairs;
+      } else {
+        c0[j] = 2 * (p - rot_pairs);
+        c1[j] = c0[j] + 1;
+        if (c0[j] >= off_chunk) c0[j] += 2 * rot_pairs;
+        if (c1[j] >= off_chunk) c1[j] += 2 * rot_pairs;
+      }
+    } else {
+      c0[j] = 2 * p;
+      c1[j] = c0[j] + 1;
+      turn[j] = rotate && c0[j] >= off_chunk && c0[j] < off_chunk + 2 * rot_pairs;
+    }
+  }
+  float tensor_inv = 1.f, scale = 1.f, inv6 = 1.f;
+  if constexpr (kKind == kTensor) tensor_inv = __fdiv_rn(1.f, __ldg(src.scale));
+  if constexpr (kKind == kFp4) {
+    scale = __ldg(src.scale);
+    inv6 = __fdiv_rn(1.f, __fmul_rn(scale, 6.f));
+  }
+
+  const uint32_t warp_id = cta * (kThreads / 32) + threadIdx.x / 32;
+  const uint32_t stride = ctas * (kThreads / 32) * kWarpRows;
+  for (uint32_t base = warp_id * kWarpRows; base < src.rows; base += stride) {
+    uint4 va[kRows][kP], vb[kRows][kP];
+    int32_t slot[kRows];
+    int64_t pos[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const uint32_t row = base + r * (32 / kL) + grp;
+      slot[r] = -1;
+      pos[r] = 0;
+#pragma unroll
+      for (int j = 0; j < kP; ++j) va[r][j] = vb[r][j] = make_uint4(0, 0, 0, 0);
+      if (row < src.rows) {
+        const uint32_t token = fast_div(row, src.heads), head = row - token * src.heads.d;
+        slot[r] = kKind == kQuery ? 0 : __ldg(prm.slots + token);
+        if (prm.table != nullptr)
+          pos[r] = prm.positions_64 ? __ldg(static_cast<const long long*>(prm.positions) + token)
+                                    : __ldg(static_cast<const int32_t*>(prm.positions) + token);
+        const uint4* x = reinterpret_cast<const uint4*>(src.x + token * src.token + head * src.head);
+#pragma unroll
+        for (int j = 0; j < kP; ++j)
+          if (live[j]) {
+            va[r][j] = __ldcs(x + c0[j]);
+            vb[r][j] = __ldcs(x + c1[j]);
+          }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const uint32_t row = base + r * (32 / kL) + grp;
+      bool ok = row < src.rows && slot[r] >= 0 && pos[r] >= 0;
+      if (ok && pos[r] >= prm.n_positions && prm.table != nullptr) {
+        if (sub == 0) atomicOr(&g_status_append, FP8MLA_DEV_BAD_POSITION);
+        ok = false;
+      }
+      if (ok && kKind != kQuery && static_cast<uint32_t>(slot[r]) >= prm.num_slots) {
+        if (sub == 0) atomicOr(&g_status_append, FP8MLA_DEV_BAD_SLOT);
+        ok = false;
+      }
+      Piece p[kP];
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        unpack8(va[r][j], p[j].a);
+        unpack8(vb[r][j], p[j].b);
+        if (ok && live[j] && turn[j]) {
+          const int pair0 = half ? 8 * (sub + j * kL) : 4 * (c0[j] - off_chunk);  // first of the piece's 8 pairs
+          const float4* cs = reinterpret_cast<const float4*>(prm.table + pos[r] * (prm.rot / 2) + pair0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // two pairs at a time: (cos, sin, cos, sin)
+            const float4 w = __ldg(cs + i);
+            auto turned = [](float& x, float& y, float c, float s) {
+              const float rx = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+              y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+              x = rx;
+            };
+            if (half) {
+              turned(p[j].a[2 * i], p[j].b[2 * i], w.x, w.y);
+              turned(p[j].a[2 * i + 1], p[j].b[2 * i + 1], w.z, w.w);
+            } else {
+              float(&x)[8] = i < 2 ? p[j].a : p[j].b;
+              turned(x[4 * (i % 2)], x[4 * (i % 2) + 1], w.x, w.y);
+              turned(x[4 * (i % 2) + 2], x[4 * (i % 2) + 3], w.z, w.w);
+            }
+          }
+        }
+      }
+      if constexpr (kKind == kQuery) {
+        if (ok) {
+          uint4* dst = reinterpret_cast<uint4*>(src.out) + static_cast<int64_t>(row) * (prm.head_dim / 8);
+#pragma unroll
+          for (int j = 0; j < kP; ++j)
+            if (live[j]) {
+              const auto& a = p[j].a;
+              const auto& b = p[j].b;
+              dst[c0[j]] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                                      pack_bf16x2(a[6], a[7]));
+              dst[c1[j]] = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]), pack_bf16x2(b[4], b[5]),
+                                      pack_bf16x2(b[6], b[7]));
+            }
+        }
+        continue;
+      }
+      // the row in the cache: (block * h_kv + head) * page + offset
+      const uint32_t head = row - fast_div(row, src.heads) * src.heads.d;
+      const uint32_t block = fast_div(static_cast<uint32_t>(slot[r]) & 0x7FFFFFFFu, prm.page);
+      const int64_t dst_row = (static_cast<int64_t>(block) * src.heads.d + head) * prm.page.d +
+                              (static_cast<uint32_t>(slot[r]) - block * prm.page.d);
+      if constexpr (kKind == kFp4) {
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+          float ma = amax8(p[j].a), mb = amax8(p[j].b);
+          const float xa = __shfl_xor_sync(0xffffffffu, ma, 1), xb = __shfl_xor_sync(0xffffffffu, mb, 1);
+          if (half && turn[j]) {
+            ma = fmaxf(ma, xa);
+            mb = fmaxf(mb, xb);
+          } else {
+            ma = mb = fmaxf(ma, mb);
+          }
+          if (ok && live[j]) {
+            const uint32_t s8a = pack_e4m3x2(__fmul_rn(ma, inv6), 0.f) & 0xFFu;
+            const uint32_t s8b = pack_e4m3x2(__fmul_rn(mb, inv6), 0.f) & 0xFFu;
+            const float sa = f16_lo(e4m3x2_to_f16x2(s8a)), sb = f16_lo(e4m3x2_to_f16x2(s8b));
+            const float ia = __fdiv_rn(1.f, __fmul_rn(sa, scale)), ib = __fdiv_rn(1.f, __fmul_rn(sb, scale));
+            float ya[8], yb[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              ya[i] = __fmul_rn(p[j].a[i], ia);
+              yb[i] = __fmul_rn(p[j].b[i], ib);
+            }
+            uint32_t* dst = reinterpret_cast<uint32_t*>(src.out + dst_row * (prm.head_dim / 2));
+            dst[c0[j]] = s8a != 0 ? pack_e2m1x8(ya) : 0u;
+            dst[c1[j]] = s8b != 0 ? pack_e2m1x8(yb) : 0u;
+            uint8_t* sc = src.block_scales + dst_row * (prm.head_dim / 16);
+            if ((c0[j] & 1) == 0) sc[c0[j] / 2] = static_cast<uint8_t>(s8a);
+            if ((c1[j] & 1) == 0) sc[c1[j] / 2] = static_cast<uint8_t>(s8b);
+          }
+        }
+      } else {
+        float inv = tensor_inv;
+        if constexpr (kKind == kRowScales) {
+          float m = 0.f;
+#pragma unroll
+          for (int j = 0; j < kP; ++j) m = fmax3(m, amax8(p[j].a), amax8(p[j].b));
+#pragma unroll
+          for (int o = kL / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const bool lifted = m < kTinyAmax;
+          if (lifted) {
+#pragma unroll
+            for (int j = 0; j < kP; ++j)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                p[j].a[i] = __fmul_rn(p[j].a[i], kTinyLift);
+                p[j].b[i] = __fmul_rn(p[j].b[i], kTinyLift);
+              }
+          }
+          inv = m > 0.f ? __fdiv_rn(448.f, lifted ? __fmul_rn(m, kTinyLift) : m) : 1.f;
+          if (ok && sub == 0) src.row_scales[dst_row] = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+        }
+        if (ok) {
+          uint2* dst = reinterpret_cast<uint2*>(src.out + dst_row * prm.head_dim);
+#pragma unroll
+          for (int j = 0; j < kP; ++j)
+            if (live[j]) {
+              dst[c0[j]] = encode8(p[j].a, inv);
+              dst[c1[j]] = encode8(p[j].b, inv);
+            }
+        }
+      }
+    }
+  }
+}
+
+template <int kL, int kP, int kKind>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ Params prm) {
+  const uint32_t c = blockIdx.x;
+  if (c < prm.first[1])
+    run_class<kL, kP, kKind>(prm, prm.src[0], prm.table != nullptr, c, prm.first[1]);
+  else if (c < prm.first[2])
+    run_class<kL, kP, kKind>(prm, prm.src[1], false, c - prm.first[1], prm.first[2] - prm.first[1]);
+  else
+    run_class<kL, kP, kQuery>(prm, prm.src[2], true, c - prm.first[2], prm.first[3] - prm.first[2]);
+}
+
+template <int kL, int kP>
+cudaError_t launch_append(Params& p, int kind, cudaStream_t stream) {
+  constexpr uint32_t kBlockRows = kThreads / 32 * (32 / kL) * (kP == 1 ? 2 : 1);
+  p.first[0] = 0;
+  const uint32_t cap = static_cast<uint32_t>(device_sms()) * 8;
+  for (int i = 0; i < 3; ++i)
+    p.first[i + 1] = p.first[i] + std::min((p.src[i].rows + kBlockRows - 1) / kBlockRows, cap);
+  switch (kind) {
+    case kTensor: kv_append_kernel<kL, kP, kTensor><<<p.first[3], kThreads, 0, stream>>>(p); break;
+    case kRowScales: kv_append_kernel<kL, kP, kRowScales><<<p.first[3], kThreads, 0, stream>>>(p); break;
+    default: kv_append_kernel<kL, kP, kFp4><<<p.first[3], kThreads, 0, stream>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ read ----
+
+struct ReadParams {
+  const uint8_t* cache;
+  const float* scale;
+  const float* row_scales;
+  const uint8_t* block_scales;
+  const int32_t* slots;
+  uint4* out;
+  FastDiv heads, page;
+  uint32_t rows, num_slots;
+  int head_dim;
+};
+
+// Rows of a paged cache as bf16: value = fp32(E4M3 * scale), or fp32(E2M1 * fp32(s8 * scale)), rounded once.
+// A group of kL lanes per row, 16 values (two 16-byte stores) a lane at a time; 8 in a last odd chunk.
+template <int kL, int kKind>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadParams prm) {
+  constexpr int kRows = 2;
+  const int lane = threadIdx.x % 32, sub = lane % kL, grp = lane / kL;
+  const int chunks = prm.head_dim / 8;
+  float scale = 1.f;
+  if constexpr (kKind != kRowScales) scale = __ldg(prm.scale);
+  const uint32_t stride = gridDim.x * (kThreads / 32) * (32 / kL) * kRows;
+  for (uint32_t base = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * (32 / kL) * kRows; base < prm.rows;
+       base += stride) {
+    int64_t src[kRows];
+    float rs[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const uint32_t row = base + r * (32 / kL) + grp;
+      src[r] = -1;
+      rs[r] = scale;
+      if (row < prm.rows) {
+        const uint32_t i = fast_div(row, prm.heads), head = row - i * prm.heads.d;
+        const int32_t slot = __ldg(prm.slots + i);
+        if (slot >= 0 && static_cast<uint32_t>(slot) >= prm.num_slots) {
+          if (sub == 0) atomicOr(&g_status_append, FP8MLA_DEV_BAD_SLOT);
+        } else if (slot >= 0) {
+          const uint32_t block = fast_div(static_cast<uint32_t>(slot), prm.page);
+          src[r] = (static_cast<int64_t>(block) * prm.heads.d + head) * prm.page.d + (slot - block * prm.page.d);
+          if constexpr (kKind == kRowScales) rs[r] = __ldg(prm.row_scales + src[r]);
+        }
+      }
+    }
+    for (int c = 2 * sub; c < chunks; c += 2 * kL) {
+      const bool two = c + 1 < chunks;
+      uint4 w[kRows];
+      float s[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        w[r] = make_uint4(0, 0, 0, 0);
+        s[r] = rs[r];
+        if (src[r] < 0) continue;
+        if constexpr (kKind == kFp4) {
+          const uint2 x = __ldcs(reinterpret_cast<const uint2*>(prm.cache + src[r] * (prm.head_dim / 2) + c * 4));
+          w[r].x = x.x, w[r].y = x.y;
+          const uint32_t s8 = __ldg(prm.block_scales + src[r] * (prm.head_dim / 16) + c / 2);
+          s[r] = __fmul_rn(f16_lo(e4m3x2_to_f16x2(s8)), scale);
+        } else {
+          const uint2* x = reinterpret_cast<const uint2*>(prm.cache + src[r] * prm.head_dim + c * 8);
+          const uint2 lo = __ldcs(x);
+          w[r].x = lo.x, w[r].y = lo.y;
+          if (two) {
+            const uint2 hi = __ldcs(x + 1);
+            w[r].z = hi.x, w[r].w = hi.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const uint32_t row = base + r * (32 / kL) + grp;
+        if (row >= prm.rows) continue;
+        uint32_t h[8];  // f16x2
+        if constexpr (kKind == kFp4) {
+          uint32_t a[4], b[4];
+          e2m1x8_to_f16x2(w[r].x, a);
+          e2m1x8_to_f16x2(w[r].y, b);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = a[i], h[4 + i] = b[i];
+        } else {
+          const uint32_t q[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            h[2 * i] = e4m3x2_to_f16x2(q[i]);
+            h[2 * i + 1] = e4m3x2_to_f16x2(q[i] >> 16);
+          }
+        }
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          o[i] = src[r] < 0 ? 0u : pack_bf16x2(__fmul_rn(f16_lo(h[i]), s[r]), __fmul_rn(f16_hi(h[i]), s[r]));
+        uint4* dst = prm.out + static_cast<int64_t>(row) * chunks + c;
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        if (two) dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    }
+  }
+}
+
+template <int kL>
+cudaError_t launch_read(const ReadParams& p, int kind, cudaStream_t stream) {
+  constexpr uint32_t kBlockRows = kThreads / 32 * (32 / kL) * 2;
+  const unsigned blocks = std::min<unsigned>((p.rows + kBlockRows - 1) / kBlockRows, device_sms() * 8);
+  switch (kind) {
+    case kTensor: cache_read_kernel<kL, kTensor><<<blocks, kThreads, 0, stream>>>(p); break;
+    case kRowScales: cache_read_kernel<kL, kRowScales><<<blocks, kThreads, 0, stream>>>(p); break;
+    default: cache_read_kernel<kL, kFp4><<<blocks, kThreads, 0, stream>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// The cache's kind from the scales given, or -1: E4M3 takes one scale or one per row, E2M1 one scale and the blocks'.
+int kind_of(fp8mla_kv_dtype_t t, const void* scale, const void* row_scales, const void* block_scales) {
+  if (t == FP8MLA_KV_E2M1)
+    return scale != nullptr && block_scales != nullptr && row_scales == nullptr ? kFp4 : -1;
+  if (block_scales != nullptr || (scale == nullptr) == (row_scales == nullptr)) return -1;
+  return scale != nullptr ? kTensor : kRowScales;
+}
+
+}  // namespace
+
+fp8mla_status_t kv_append_entry(const KvAppendArgs& a, cudaStream_t stream) {
+  if (a.kv_dtype != FP8MLA_KV_E4M3 && a.kv_dtype != FP8MLA_KV_E2M1) return FP8MLA_ERR_UNSUPPORTED_DTYPE;
+  if (a.n_tokens < 0 || a.h_kv < 1 || a.head_dim < 16 || a.head_dim % 16 != 0 || a.head_dim > kMaxHeadDim ||
+      a.page_size < 1 || a.num_blocks < 1 || (a.q != nullptr && a.h_q < 1))
+    return FP8MLA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(a.n_tokens) * std::max(a.h_kv, a.q != nullptr ? a.h_q : 1) >= (1ll << 31) ||
+      static_cast<int64_t>(a.num_blocks) * a.page_size >= (1ll << 31))
+    return FP8MLA_ERR_INVALID_ARG;
+  const bool has_v = a.side[1].x != nullptr || a.side[1].cache != nullptr;
+  const int kind = kind_of(a.kv_dtype, a.side[0].scale, a.side[0].row_scales, a.side[0].block_scales);
+  if (kind < 0) return FP8MLA_ERR_INVALID_ARG;
+  if (has_v && kind_of(a.kv_dtype, a.side[1].scale, a.side[1].row_scales, a.side[1].block_scales) != kind)
+    return FP8MLA_ERR_INVALID_ARG;
+  if (a.table != nullptr) {
+    if (a.rot < 16 || a.rot % 16 != 0 || a.rot_offset < 0 || a.rot_offset % (a.interleaved ? 16 : 8) != 0 ||
+        a.rot > a.head_dim - a.rot_offset || a.n_positions < 1 || misaligned(a.table, 16))
+      return FP8MLA_ERR_INVALID_ARG;
+    // blocks of 16 values do not straddle a half layout's pieces
+    if (kind == kFp4 && !a.interleaved && (a.rot % 32 != 0 || a.rot_offset % 16 != 0)) return FP8MLA_ERR_INVALID_ARG;
+  } else if (a.q != nullptr) {
+    return FP8MLA_ERR_INVALID_ARG;  // nothing to rotate the queries with
+  }
+  if (a.n_tokens == 0) return FP8MLA_OK;
+  if (a.slot_mapping == nullptr || (a.table != nullptr && a.positions == nullptr)) return FP8MLA_ERR_INVALID_ARG;
+  for (int i = 0; i < (has_v ? 2 : 1); ++i) {
+    const CacheSide& s = a.side[i];
+    if (s.x == nullptr || s.cache == nullptr || misaligned(s.x, 16) || misaligned(s.cache, 16) ||
+        (s.token | s.head) % 8 != 0 || misaligned(s.row_scales, 4) || misaligned(s.scale, 4))
+      return FP8MLA_ERR_INVALID_ARG;
+  }
+  if (a.q != nullptr && (a.q_out == nullptr || misaligned(a.q, 16) || misaligned(a.q_out, 16) ||
+                         (a.q_token | a.q_head) % 8 != 0))
+    return FP8MLA_ERR_INVALID_ARG;
+  Params p;
+  for (int i = 0; i < 2; ++i) {
+    const CacheSide& s = a.side[i];
+    p.src[i].x = static_cast<const uint16_t*>(s.x);
+    p.src[i].token = s.token;
+    p.src[i].head = s.head;
+    p.src[i].out = static_cast<uint8_t*>(s.cache);
+    p.src[i].scale = s.scale;
+    p.src[i].row_scales = s.row_scales;
+    p.src[i].block_scales = static_cast<uint8_t*>(s.block_scales);
+    p.src[i].heads = make_fast_div(a.h_kv);
+    p.src[i].rows = i == 0 || has_v ? static_cast<uint32_t>(a.n_tokens) * a.h_kv : 0;
+  }
+  p.src[2] = Source{static_cast<const uint16_t*>(a.q), a.q_token, a.q_head, static_cast<uint8_t*>(a.q_out), nullptr,
+                    nullptr, nullptr, make_fast_div(a.q != nullptr ? a.h_q : 1),
+                    a.q != nullptr ? static_cast<uint32_t>(a.n_tokens) * a.h_q : 0};
+  p.slots = a.slot_mapping;
+  p.positions = a.positions;
+  p.positions_64 = a.positions_64;
+  p.table = reinterpret_cast<const float2*>(a.table);
+  p.n_positions = a.n_positions;
+  p.page = make_fast_div(a.page_size);
+  p.num_slots = static_cast<uint32_t>(static_cast<int64_t>(a.num_blocks) * a.page_size);
+  p.rot = a.rot;
+  p.rot_offset = a.rot_offset;
+  p.interleaved = a.interleaved;
+  p.head_dim = a.head_dim;
+  const int pairs = a.head_dim / 16;
+  cudaError_t e;
+  if (pairs <= 1) e = launch_append<1, 1>(p, kind, stream);
+  else if (pairs <= 2) e = launch_append<2, 1>(p, kind, stream);
+  else if (pairs <= 4) e = launch_append<4, 1>(p, kind, stream);
+  else if (pairs <= 8) e = launch_append<8, 1>(p, kind, stream);
+  else if (pairs <= 16) e = launch_append<16, 1>(p, kind, stream);
+  else if (pairs <= 32) e = launch_append<32, 1>(p, kind, stream);
+  else e = launch_append<32, 2>(p, kind, stream);
+  return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
+}
+
+fp8mla_status_t cache_read_entry(const CacheReadArgs& a, cudaStream_t stream) {
+  if (a.kv_dtype != FP8MLA_KV_E4M3 && a.kv_dtype != FP8MLA_KV_E2M1) return FP8MLA_ERR_UNSUPPORTED_DTYPE;
+  if (a.n < 0 || a.h_kv < 1 || a.page_size < 1 || a.num_blocks < 1 || a.head_dim < 8 || a.head_dim > kMaxHeadDim ||
+      a.head_dim % (a.kv_dtype == FP8MLA_KV_E2M1 ? 16 : 8) != 0)
+    return FP8MLA_ERR_INVALID_ARG;
+  const int kind = kind_of(a.kv_dtype, a.scale, a.row_scales, a.block_scales);
+  if (kind < 0) return FP8MLA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(a.n) * a.h_kv >= (1ll << 31) ||
+      static_cast<int64_t>(a.num_blocks) * a.page_size >= (1ll << 31))
+    return FP8MLA_ERR_INVALID_ARG;
+  if (a.n == 0) return FP8MLA_OK;
+  if (a.cache == nullptr || a.slots == nullptr || a.out == nullptr || misaligned(a.cache, 16) ||
+      misaligned(a.out, 16) || misaligned(a.scale, 4) || misaligned(a.row_scales, 4))
+    return FP8MLA_ERR_INVALID_ARG;
+  ReadParams p;
+  p.cache = static_cast<const uint8_t*>(a.cache);
+  p.scale = a.scale;
+  p.row_scales = a.row_scales;
+  p.block_scales = static_cast<const uint8_t*>(a.block_scales);
+  p.slots = a.slots;
+  p.out = static_cast<uint4*>(a.out);
+  p.heads = make_fast_div(a.h_kv);
+  p.page = make_fast_div(a.page_size);
+  p.rows = static_cast<uint32_t>(a.n) * a.h_kv;
+  p.num_slots = static_cast<uint32_t>(static_cast<int64_t>(a.num_blocks) * a.page_size);
+  p.head_dim = a.head_dim;
+  const int pairs = (a.head_dim + 15) / 16;
+  cudaError_t e;
+  if (pairs <= 1) e = launch_read<1>(p, kind, stream);
+  else if (pairs <= 2) e = launch_read<2>(p, kind, stream);
+  else if (pairs <= 4) e = launch_read<4>(p, kind, stream);
+  else if (pairs <= 8) e = launch_read<8>(p, kind, stream);
+  else if (pairs <= 16) e = launch_read<16>(p, kind, stream);
+  else e = launch_read<32>(p, kind, stream);
+  return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
+}
+
+uint32_t kv_append_read_and_clear_status() {
+  uint32_t v = 0, z = 0;
+  cudaMemcpyFromSymbol(&v, g_status_append, sizeof(v));
+  cudaMemcpyToSymbol(g_status_append, &z, sizeof(z));
+  return v;
+}
+
+}  // namespace fp8mla
