@@ -452,14 +452,19 @@ FP8MLA_API fp8mla_status_t paged_cache_read(const void* cache, fp8mla_kv_dtype_t
  *   k_scale, v_scale  float32 [1] each (device)
  *   block_table, seqlens, spec_mask, window, sinks, out, lse  as
  *                paged_gqa_decode_ext
- *   num_splits   0 = auto (paged_gqa_fp4_num_splits for this GPU with the
- *                block table's capacity); k >= 1 forced, at most one shard per
- *                128 keys
- *   workspace    >= paged_gqa_fp4_workspace_bytes of the split count, 256-byte
- *                aligned; may be NULL when that is 0
+ *   num_splits   0 = auto: one CTA per (sequence, KV head) where the block
+ *                table holds at most 1024 keys or the sequences fill the GPU
+ *                many times over, else the keys of all sequences cut into
+ *                equal pieces, one per CTA that fits on the GPU; 1 = one CTA
+ *                each; k > 1 = every sequence in k shards, at most one per
+ *                128 keys of the block table
+ *   workspace    >= paged_gqa_fp4_workspace_bytes with max_seqlen the block
+ *                table's max_blocks * page_size, 256-byte aligned; may be
+ *                NULL when that is 0
  * Products take K and V exactly and Q as it is; P is rounded to f16.
- * Requires head_dim 64, 128 or 256, page_size 16, 32, 64, 128 or 256, q_len <=
- * 16, h_q % h_kv == 0 and q_len * (h_q / h_kv) <= 128. */
+ * Scales are normal floats > 0.  Requires head_dim 64, 128 or 256, page_size
+ * 16, 32, 64, 128 or 256, q_len <= 16, h_q % h_kv == 0, q_len * (h_q / h_kv)
+ * <= 128 and fewer than 2^32 rows (num_blocks * h_kv * page_size) a cache. */
 FP8MLA_API fp8mla_status_t paged_gqa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
                                                 const void* k_block_scales, const void* v_block_scales, int num_blocks,
                                                 const float* k_scale, const float* v_scale,
@@ -469,11 +474,10 @@ FP8MLA_API fp8mla_status_t paged_gqa_decode_fp4(const void* q, const void* k_cac
                                                 size_t workspace_bytes, void* out, float* lse, int bs, int h_q,
                                                 int h_kv, int head_dim, int page_size, fp8mla_stream_t stream);
 
-/* Number of key shards paged_gqa_decode_fp4 uses for these arguments
- * (num_splits as passed: 0 = auto), and its workspace with that many.  Host-only. */
-FP8MLA_API int paged_gqa_fp4_num_splits(int bs, int h_q, int h_kv, int max_seqlen, int q_len, int window, int num_sms,
-                                        int num_splits);
-FP8MLA_API size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int head_dim, int q_len, int splits);
+/* Workspace bytes of paged_gqa_decode_fp4 with these arguments (auto uses the
+ * SM count of the current device); 0 where nothing has to be merged. */
+FP8MLA_API size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int head_dim, int q_len,
+                                                int64_t max_seqlen, int window, int num_splits);
 
 /* ------------------------------------------------------ no allocation ---
  * fp8mla_decode_no_alloc -- the dense MLA decode for callers that cannot

@@ -78,8 +78,7 @@ _SIGNATURES = {
     "paged_cache_read": (_I, [_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
     "paged_gqa_decode_fp4": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _P, _F, _I, _P, _I, _P, _I, _P, _SZ, _P,
                                   _P, _I, _I, _I, _I, _I, _P]),
-    "paged_gqa_fp4_num_splits": (_I, [_I, _I, _I, _I, _I, _I, _I, _I]),
-    "paged_gqa_fp4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "paged_gqa_fp4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _L, _I, _I]),
     "fp8mla_get_last_device_error": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "fp8mla_get_wait_timeout_site": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "fp8mla_set_wait_test": (_I, [ctypes.c_int32, ctypes.c_uint64]),
@@ -136,17 +135,6 @@ _HERE_CTX = _Here()
 def _on(device):
     """Context in which ``device`` is the current one (launches and one-time setup go by the current device)."""
     return _HERE_CTX if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-_SMS: dict[int, int] = {}
-
-
-def _sms() -> int:
-    """SM count of the current device, asked once per device."""
-    dev = torch.cuda.current_device()
-    if dev not in _SMS:
-        _SMS[dev] = num_sms(dev)
-    return _SMS[dev]
 
 
 def kv_dtype_code(t: torch.Tensor) -> int:
@@ -812,21 +800,17 @@ def paged_cache_read(cache: torch.Tensor, slots: torch.Tensor, *, scale=None, ro
     return out
 
 
-def gqa_fp4_num_splits(bs: int, h_q: int, h_kv: int, max_seqlen: int, q_len: int = 1, window: int = 0,
-                       num_splits: int = 0, sms: int | None = None) -> int:
-    return lib().paged_gqa_fp4_num_splits(bs, h_q, h_kv, max_seqlen, q_len, window, _sms() if sms is None else sms,
-                                          num_splits)
-
-
-def gqa_fp4_workspace_bytes(bs: int, h_q: int, h_kv: int, head_dim: int, q_len: int, splits: int) -> int:
-    return lib().paged_gqa_fp4_workspace_bytes(bs, h_q, h_kv, head_dim, q_len, splits)
+def gqa_fp4_workspace_bytes(bs: int, h_q: int, h_kv: int, head_dim: int, max_seqlen: int, q_len: int = 1,
+                            window: int = 0, num_splits: int = 0) -> int:
+    """Workspace of ``paged_gqa_decode_fp4`` on the current device; max_seqlen = the block table's keys."""
+    return lib().paged_gqa_fp4_workspace_bytes(bs, h_q, h_kv, head_dim, q_len, max_seqlen, window, num_splits)
 
 
 def paged_gqa_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                          k_block_scales: torch.Tensor, v_block_scales: torch.Tensor, block_table: torch.Tensor,
                          seqlens: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                          softmax_scale: float | None = None, spec_mask=None, window: int = 0, sinks=None,
-                         num_splits: int = 0, max_seqlen: int | None = None, out=None, lse=None, workspace=None):
+                         num_splits: int = 0, out=None, lse=None, workspace=None):
     """Paged GQA decode over 4-bit caches.  q bf16 [bs, q_len, h_q, hd] (the sequence's last q_len cache
     positions) or [bs, h_q, hd]; caches uint8 [num_blocks, h_kv, page, hd / 2] (two E2M1 codes a byte),
     block scales E4M3 [num_blocks, h_kv, page, hd / 16], k_scale / v_scale float32 [1]; block_table int32
@@ -864,11 +848,7 @@ def paged_gqa_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(hd)
     max_blocks = block_table.shape[1]
-    capacity = max_blocks * page
     with _on(dev):
-        splits = gqa_fp4_num_splits(bs, h_q, h_kv, min(capacity if max_seqlen is None else max_seqlen, capacity,
-                                                       0x7FFFFF00), q_len, window, num_splits) \
-            if num_splits >= 0 else num_splits  # a negative count is the library's to refuse
         if out is None:
             out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
         elif out.shape != shape or out.dtype != torch.bfloat16 or out.device != dev or not out.is_contiguous():
@@ -877,14 +857,15 @@ def paged_gqa_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
             lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
         elif lse.shape != shape[:-1] or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 of q's shape without head_dim")
-        if workspace is None and splits > 1:
-            workspace = torch.empty((gqa_fp4_workspace_bytes(bs, h_q, h_kv, hd, q_len, splits),), dtype=torch.uint8,
-                                    device=dev)
+        if workspace is None:
+            need = gqa_fp4_workspace_bytes(bs, h_q, h_kv, hd, max_blocks * page, q_len, window, num_splits)
+            if need:
+                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
         _check(lib().paged_gqa_decode_fp4(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                           k_block_scales.data_ptr(), v_block_scales.data_ptr(), num_blocks,
                                           k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), max_blocks,
                                           seqlens.data_ptr(), float(softmax_scale), q_len, _ptr(spec_mask),
-                                          int(window), _ptr(sinks), splits, _ptr(workspace),
+                                          int(window), _ptr(sinks), int(num_splits), _ptr(workspace),
                                           0 if workspace is None else workspace.numel() * workspace.element_size(),
                                           out.data_ptr(), lse.data_ptr(), bs, h_q, h_kv, hd, page, _stream(dev)),
                "paged_gqa_decode_fp4")

@@ -535,13 +535,9 @@ fp8mla_status_t paged_gqa_decode_fp4(const void* q, const void* k_cache, const v
   return fp4_decode_entry(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
-int paged_gqa_fp4_num_splits(int bs, int h_q, int h_kv, int max_seqlen, int q_len, int window, int num_sms,
-                             int num_splits) {
-  return fp4_choose_splits(bs, h_q, h_kv, max_seqlen, q_len, window, num_sms, num_splits);
-}
-
-size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int head_dim, int q_len, int splits) {
-  return fp4_workspace_bytes(bs, h_q, h_kv, head_dim, q_len, splits);
+size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int head_dim, int q_len, int64_t max_seqlen,
+                                     int window, int num_splits) {
+  return fp4_workspace_bytes(bs, h_q, h_kv, head_dim, q_len, max_seqlen, window, num_splits);
 }
 
 fp8mla_status_t fp8mla_get_last_device_error(fp8mla_stream_t stream, uint32_t* code_out) {

@@ -39,12 +39,16 @@
 //     from and moves only when a score passes it by more than 15: P stays
 //     within f16 (2^15), weights down to 2^-21 of the largest keep f16's
 //     relative precision, and most tiles need no shuffle.
-//   * The keys of a (sequence, KV head) are cut into contiguous shards over
-//     CTAs when the grid would not fill the GPU, merged by a second kernel.
+//   * The work -- every (sequence, KV head)'s tiles in one line -- is cut into
+//     equal pieces, one per CTA that fits on the GPU at once: lengths are known
+//     on the device only, so each CTA sums them itself.  A piece holds the end
+//     of one sequence, whole ones, and the beginning of another; whole ones are
+//     written at once, the others' partial states merged by a second kernel.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "gqa_fp4.h"
@@ -56,12 +60,22 @@ __device__ uint32_t g_status_fp4;
 namespace fp4 {
 
 constexpr int kTile = 16;       // keys of a tile
-constexpr int kWarps = 8;
-constexpr int kStages = 4;      // tiles of a warp's ring
 constexpr int kMaxQLen = 16;
 constexpr int kMaxCols = 128;   // q_len * (h_q / h_kv)
+constexpr int kMaxLine = 1024;  // sequences whose lengths a CTA sums
+constexpr int kMinTiles = 16;   // tiles of a piece, where there are fewer than GPU-filling
+constexpr int kFixed = 32;      // what a sequence costs a CTA beside its tiles, in tiles: fill, drain and merge
 constexpr float kBelow = 7.f;   // a reference lies this far below the largest score (log2) ...
 constexpr float kTau = 15.f;    // ... and moves when a score is this far above it
+
+// Warps of a CTA, CTAs of an SM, tiles a warp takes at a time, and stages of its ring.
+template <int kHd, int kNT>
+struct Shape {
+  static constexpr int kWarps = 4;
+  static constexpr int kPerSm = kHd == 256 ? 2 : 3;
+  static constexpr int kU = kHd == 256 || kNT == 2 ? 1 : 2;
+  static constexpr int kStages = kU == 2 ? 3 : 4;
+};
 
 struct Params {
   const uint16_t* q;
@@ -77,9 +91,12 @@ struct Params {
   const float* sinks;
   uint16_t* out;
   float* lse;
-  float4* ws_o;   // [slot][NT * hd / 16][32 lanes] fragments
-  float2* ws_ml;  // [slot][NT * 8]
-  int num_blocks, max_blocks, h_q, h_kv, group, splits, q_len, window;
+  float4* ws_o;    // [slot][NT * hd / 16][32 lanes] fragments
+  float2* ws_ml;   // [slot][NT * 8]
+  int2* ws_span;   // [bs * h_kv]: first and last piece of a (sequence, KV head) (balanced only)
+  int num_blocks, max_blocks, bs, h_q, h_kv, group, q_len, window;
+  int splits;      // shards of every sequence, one CTA each (1: no merge), or 0: balanced pieces
+  int units;       // balanced: pieces there may be
   int page_shift;  // log2(page_size / 16)
   float softmax_scale;
 };
@@ -120,176 +137,296 @@ __device__ __forceinline__ int q_exponent(float amax) {
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
+// A load that stays where it is written, before the waits that follow.
+__device__ __forceinline__ uint4 ldg_now(const uint4* p) {
+  uint4 x;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+  return x;
+}
+
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 
 // Fragment positions -> keys of the tile: row g of S^T is key (g / 2) + 4 (g % 2), row g + 8 that plus 8, so the
 // pairs (2t, 2t + 1) and (2t + 8, 2t + 9) of P^T's contraction are keys t, t + 4 and t + 8, t + 12.
 
+// Keys that the call reads of a sequence of length s_k: none, and a status bit, where that is negative or longer
+// than the block table; and the first tile that any token's window reaches.
+__device__ __forceinline__ int checked_len(const Params& prm, int s_k) {
+  const int page = kTile << prm.page_shift;
+  if (s_k >= 0 && ((static_cast<long long>(s_k) + page - 1) >> (4 + prm.page_shift)) <= prm.max_blocks) return s_k;
+  atomicOr(&g_status_fp4, FP8MLA_DEV_BAD_SEQLEN);
+  return 0;
+}
+__device__ __forceinline__ int first_tile(const Params& prm, int s_k) {
+  return prm.window > 0 ? max(0, s_k - prm.q_len - prm.window + 1) / kTile : 0;
+}
+__device__ __forceinline__ int tiles_of(const Params& prm, int s_k) {
+  return max(0, (s_k + kTile - 1) / kTile - first_tile(prm, s_k));
+}
+
 template <int kHd, int kNT>
-__global__ void __launch_bounds__(kWarps * 32, kNT == 1 && kHd <= 128 ? 2 : 1) fp4_decode_kernel(const Params prm) {
+__global__ void __launch_bounds__(Shape<kHd, kNT>::kWarps * 32, Shape<kHd, kNT>::kPerSm)
+    fp4_decode_kernel(const __grid_constant__ Params prm) {
   using L = Lay<kHd>;
+  constexpr int kWarps = Shape<kHd, kNT>::kWarps, kU = Shape<kHd, kNT>::kU, kStages = Shape<kHd, kNT>::kStages;
+  constexpr int kStage = kU * L::kBytes;
   constexpr int kSteps = kHd / 16;     // products of a tile, for K and for V
   constexpr int kKWords = kHd / 32;    // 32-bit words of a lane's part of a K row
-  constexpr int kVWords = kHd >= 64 ? kHd / 64 : 1;  // of a lane's part of a V row
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kVWords = kHd / 64;    // of a lane's part of a V row
+  constexpr int kCopies = L::kChunks / 32;
+  extern __shared__ __align__(128) uint8_t smem[];  // a 512-byte copy of a warp covers whole 128-byte lines
   __shared__ uint32_t s_vis[kMaxQLen];
   __shared__ float s_m[kWarps][kNT * 8], s_l[kWarps][kNT * 8];
+  __shared__ uint4 s_q[kNT][kSteps / 2][32];  // Q's fragments of two products a lane
+  __shared__ float s_cq[kNT * 8];             // score to log2 units, then a finished row's factor
+  __shared__ int64_t s_row[kNT * 8];
+  __shared__ int s_line[kMaxLine + 1];
+  __shared__ int s_part[2][kWarps];
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
-  const int split = blockIdx.x % prm.splits;
-  const int seq = blockIdx.x / prm.splits;
-  const int b = seq / prm.h_kv, kvh = seq % prm.h_kv;
   const int col0 = blockIdx.y * (kNT * 8);
   const int ncols = min(prm.q_len * prm.group - col0, kNT * 8);
+  const int page = kTile << prm.page_shift;
 
   griddep_wait();
-  griddep_launch_dependents();
 
-  const int page = kTile << prm.page_shift;
-  int s_k = prm.seqlens[b];
-  if (s_k < 0 || (static_cast<long long>(s_k) + page - 1) / page > prm.max_blocks) {
-    if (threadIdx.x == 0) atomicOr(&g_status_fp4, FP8MLA_DEV_BAD_SEQLEN);
-    s_k = 0;
+  // ---- this CTA's stretch [cur, end) of a line on which a sequence's KV heads lie one after the other, each
+  // taking kFixed places and then one for every tile
+  int cur = 0, end = 1;
+  const int unit = blockIdx.x;
+  if (prm.splits == 0) {
+    // prefix sums of the sequences' places (of one KV head), a CTA's width of sequences at a time
+    constexpr int kThreads = kWarps * 32, kRuns = kMaxLine / kThreads;
+    int len[kRuns];
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+      const int b = i * kThreads + threadIdx.x;
+      len[i] = b < prm.bs ? __ldg(prm.seqlens + b) : 0;
+    }
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+      if (i * kThreads >= prm.bs) break;
+      const int b = i * kThreads + threadIdx.x;
+      const int tiles = tiles_of(prm, checked_len(prm, len[i]));
+      const int places = tiles > 0 ? tiles + kFixed : 0;
+      if (tiles == 0 && b < prm.bs && unit == 0 && blockIdx.y == 0)  // nothing to attend to: the merge writes it
+        for (int h = 0; h < prm.h_kv; ++h) prm.ws_span[b * prm.h_kv + h] = make_int2(1, 0);
+      int inc = places;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      if (lane == 31) s_part[i & 1][warp] = inc;
+      __syncthreads();
+      int start = before;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) start += s_part[i & 1][w];
+        before += s_part[i & 1][w];
+      }
+      if (b < prm.bs) s_line[b] = start + inc - places;
+    }
+    if (threadIdx.x == 0) s_line[prm.bs] = before;
+    __syncthreads();
+    const int work = s_line[prm.bs] * prm.h_kv;
+    const int pieces = max(1, min(prm.units, work / (kMinTiles + kFixed)));
+    if (unit >= pieces) return;
+    const int each = work / pieces, rest = work - each * pieces;  // cut u at floor(work u / pieces)
+    cur = each * unit + rest * unit / pieces;
+    end = each * (unit + 1) + rest * (unit + 1) / pieces;
   }
-  const int start = s_k - prm.q_len;  // position of the block's first token
-  const int k_lo = prm.window > 0 ? max(0, start - prm.window + 1) : 0;
-  const int tile_lo = k_lo / kTile;
-  const int tiles = max(0, (s_k + kTile - 1) / kTile - tile_lo);
-  const int t0 = tile_lo + static_cast<int>(static_cast<long long>(split) * tiles / prm.splits);
-  const int t1 = tile_lo + static_cast<int>(static_cast<long long>(split + 1) * tiles / prm.splits);
-  const int n_mine = t1 - t0 > warp ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;
 
-  const int32_t* bt_row = prm.block_table + static_cast<size_t>(b) * prm.max_blocks;
-  uint8_t* ring = smem + warp * (kStages * L::kBytes);
-
-  // Entries of the block table, 32 tiles of this warp at a time.
-  int entry = 0;
-  auto fetch_entries = [&](int i0) {
-    const int i = i0 + lane;
-    entry = 0;
-    if (i < n_mine) {
-      entry = __ldg(bt_row + ((t0 + warp + i * kWarps) >> prm.page_shift));
-      if (entry < 0 || entry >= prm.num_blocks) {
-        atomicOr(&g_status_fp4, FP8MLA_DEV_BAD_PAGE);
-        entry = 0;
-      }
-    }
-  };
-  auto issue = [&](int i) {
-    if (i < n_mine) {
-      if ((i & 31) == 0) fetch_entries(i);
-      const int blk = __shfl_sync(0xffffffffu, entry, i & 31);
-      const int tile = t0 + warp + i * kWarps;
-      const int in_page = tile & ((1 << prm.page_shift) - 1);
-      const int64_t row = (static_cast<int64_t>(blk) * prm.h_kv + kvh) * page + in_page * kTile;
-      const uint32_t st = smem_u32(ring + (i % kStages) * L::kBytes);
-      const uint8_t* ksrc = prm.k + row * L::kRow;
-      const uint8_t* vsrc = prm.v + row * L::kRow;
+  const int c_lane = lane * 16;  // this lane's bytes of a code tile
+  uint32_t kdst[kCopies], vdst[kCopies];  // and where they go in a stage
+  const uint32_t ring = smem_u32(smem) + warp * (kStages * kStage);
 #pragma unroll
-      for (int c = lane; c < L::kChunks; c += 32) {
-        const int r = c / (L::kRow / 16), cc = c % (L::kRow / 16);
-        cp_async16(st + L::kK + k_place<kHd>(r, cc), ksrc + c * 16, 16u);
-        cp_async16(st + L::kV + v_place<kHd>(r, cc), vsrc + c * 16, 16u);
-      }
-      if (lane < 2 * L::kSChunks) {
-        const bool is_v = lane >= L::kSChunks;
-        const int c = is_v ? lane - L::kSChunks : lane;
-        cp_async16(st + (is_v ? L::kVs : L::kKs) + c * 16, (is_v ? prm.vs : prm.ks) + row * L::kSRow + c * 16, 16u);
-      }
-    }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  for (int i = 0; i < kCopies; ++i) {
+    const int c = lane + 32 * i, r = c / (L::kRow / 16), cc = c % (L::kRow / 16);
+    kdst[i] = L::kK + k_place<kHd>(r, cc);
+    vdst[i] = L::kV + v_place<kHd>(r, cc);
+  }
+  const bool sc_lane = lane < 2 * L::kSChunks;
+  const bool sc_v = lane >= L::kSChunks;
+  const uint8_t* sc_base = (sc_v ? prm.vs : prm.ks) + (sc_v ? lane - L::kSChunks : lane) * 16;
+  const uint32_t sc_dst = (sc_v ? L::kVs + (lane - L::kSChunks) * 16 : L::kKs + lane * 16);
+  const uint8_t* k_base = prm.k + c_lane;
+  const uint8_t* v_base = prm.v + c_lane;
+  const int r0 = (g >> 1) + 4 * (g & 1);  // keys of fragment rows g and g + 8
+  const int r1 = r0 + 8;
+  const float c0 = prm.softmax_scale * kLog2e * __ldg(prm.k_scale);
 
-  // Which keys of the speculative block its token i sees: its mask row, or those up to itself.
-  if (threadIdx.x < prm.q_len) {
-    uint32_t bits = 0;
-    if (prm.spec_mask != nullptr) {
-      const uint8_t* row = prm.spec_mask + (static_cast<size_t>(b) * prm.q_len + threadIdx.x) * prm.q_len;
-      for (int c = 0; c < prm.q_len; ++c)
-        if (__ldg(row + c)) bits |= 1u << c;
+  while (cur < end) {
+    // ---- the segment: tiles [t0, t1) of one (sequence, KV head)
+    int b, kvh, t0, t1, s_k;
+    long long slot = -1;  // where its partial state goes, or -1: the rows are finished here
+    if (prm.splits == 0) {
+      const int at = cur / prm.h_kv;
+      int lo = 0, hi = prm.bs;  // s_line[lo] <= at < s_line[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (s_line[mid] <= at) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
+      const int places = s_line[b + 1] - s_line[b];
+      int off = cur - s_line[b] * prm.h_kv;
+      kvh = off / places;
+      off -= kvh * places;
+      const int first = max(0, off - kFixed);
+      const int stop = min(end - cur + off, places);
+      const int last = max(0, stop - kFixed), tiles = places - kFixed;
+      cur += stop - off;
+      if (first == last) continue;  // the cut fell into the places before the first tile
+      if (last - first < tiles)
+        slot = (static_cast<long long>(blockIdx.y) * prm.units + unit) * 2 + (first == 0 ? 1 : 0);
+      if (threadIdx.x == 0 && blockIdx.y == 0) {
+        if (first == 0) prm.ws_span[b * prm.h_kv + kvh].x = unit;
+        if (last == tiles) prm.ws_span[b * prm.h_kv + kvh].y = unit;
+      }
+      s_k = __ldg(prm.seqlens + b);
+      t0 = first_tile(prm, s_k) + first;
+      t1 = first_tile(prm, s_k) + last;
     } else {
-      bits = (2u << threadIdx.x) - 1u;
+      const int seq = unit / prm.splits, split = unit - seq * prm.splits;
+      b = seq / prm.h_kv;
+      kvh = seq - b * prm.h_kv;
+      s_k = checked_len(prm, __ldg(prm.seqlens + b));
+      const int tiles = tiles_of(prm, s_k);
+      t0 = first_tile(prm, s_k) + static_cast<int>(static_cast<long long>(split) * tiles / prm.splits);
+      t1 = first_tile(prm, s_k) + static_cast<int>(static_cast<long long>(split + 1) * tiles / prm.splits);
+      if (prm.splits > 1) slot = static_cast<long long>(blockIdx.y) * gridDim.x + unit;
+      cur = end;
     }
-    s_vis[threadIdx.x] = bits;
-  }
+    const int start = s_k - prm.q_len;  // position of the block's first token
+    const int k_lo = prm.window > 0 ? max(0, start - prm.window + 1) : 0;
+    const int mine0 = t0 + warp * kU;  // this warp's tiles: kU from here, kU more kWarps * kU later, ...
+    const int n_mine = t1 > mine0 ? (t1 - mine0 + kWarps * kU - 1) / (kWarps * kU) : 0;
+    const int32_t* bt_row = prm.block_table + static_cast<size_t>(b) * prm.max_blocks;
 
-  // Q's fragments: lane (g, t) holds dims [t hd/4, (t + 1) hd/4) of column g, as f16 with a power of two out
-  uint32_t qf[kNT][kSteps][2];
-  float cq[kNT][2];
-  int tok[kNT][2];
-  {
-    const float c0 = prm.softmax_scale * kLog2e * __ldg(prm.k_scale);
+    // Q's values are asked for first: lane (g, t) of warp n takes dims [t hd/4, (t + 1) hd/4) of column 8 n + g
+    uint4 qx[kSteps / 2];
+    if (warp < kNT) {
+      const int c = warp * 8 + g, col = col0 + c, token = col / prm.group;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          prm.q + ((static_cast<size_t>(b) * prm.q_len + token) * prm.h_q + kvh * prm.group + col - token * prm.group) *
+                      kHd + t * (kHd / 4));
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-      const int col = col0 + n * 8 + g;
-      uint32_t w[kSteps * 2];
-      if (n * 8 + g < ncols) {
-        const uint16_t* src = prm.q + ((static_cast<size_t>(b) * prm.q_len + col / prm.group) * prm.h_q +
-                                       kvh * prm.group + col % prm.group) * kHd + t * (kHd / 4);
-#pragma unroll
-        for (int j = 0; j < kSteps / 2; ++j) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + j);
-          w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+      for (int j = 0; j < kSteps / 2; ++j) qx[j] = c < ncols ? ldg_now(src + j) : make_uint4(0, 0, 0, 0);
+    }
+
+    // Entries of the block table (as the tile's first row in the cache), 32 tiles of this warp at a time.
+    uint32_t entry = 0;
+    const uint32_t block_rows = prm.h_kv * page;
+    auto fetch_entries = [&](int i0) {
+      const int tile = mine0 + (i0 + lane / kU) * (kWarps * kU) + lane % kU;
+      entry = 0;
+      if (tile < t1) {
+        int blk = __ldg(bt_row + (tile >> prm.page_shift));
+        if (blk < 0 || blk >= prm.num_blocks) {
+          atomicOr(&g_status_fp4, FP8MLA_DEV_BAD_PAGE);
+          blk = 0;
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kSteps * 2; ++j) w[j] = 0;
+        entry = blk * block_rows + kvh * page + (tile & ((1 << prm.page_shift) - 1)) * kTile;
       }
+    };
+    uint32_t put = ring;  // the stage that is filled next
+    auto issue = [&](int i) {
+      if (i < n_mine) {
+        if (i % (32 / kU) == 0) fetch_entries(i);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const uint32_t row = __shfl_sync(0xffffffffu, entry, i % (32 / kU) * kU + u);
+          if (u > 0 && mine0 + i * (kWarps * kU) + u >= t1) break;  // past the segment's end: an old tile stays there
+          const uint8_t* ksrc = k_base + static_cast<uint64_t>(row) * L::kRow;
+          const uint8_t* vsrc = v_base + static_cast<uint64_t>(row) * L::kRow;
+#pragma unroll
+          for (int j = 0; j < kCopies; ++j) {
+            cp_async16(put + kdst[j] + u * L::kBytes, ksrc + 512 * j, 16u);
+            cp_async16(put + vdst[j] + u * L::kBytes, vsrc + 512 * j, 16u);
+          }
+          if (sc_lane)
+            cp_async16(put + sc_dst + u * L::kBytes, sc_base + static_cast<uint64_t>(row) * L::kSRow, 16u);
+        }
+        put += kStage;
+        if (put == ring + kStages * kStage) put = ring;
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+    // Which keys of the speculative block its token i sees: its mask row, or those up to itself.
+    if (threadIdx.x < prm.q_len) {
+      uint32_t bits = 0;
+      if (prm.spec_mask != nullptr) {
+        const uint8_t* row = prm.spec_mask + (static_cast<size_t>(b) * prm.q_len + threadIdx.x) * prm.q_len;
+        for (int c = 0; c < prm.q_len; ++c)
+          if (__ldg(row + c)) bits |= 1u << c;
+      } else {
+        bits = (2u << threadIdx.x) - 1u;
+      }
+      s_vis[threadIdx.x] = bits;
+    }
+
+    if (warp < kNT) {  // Q's fragments, as f16 with a power of two out
       float amax = 0.f;
 #pragma unroll
-      for (int j = 0; j < kSteps * 2; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
+      for (int j = 0; j < kSteps / 2; ++j) {
+        amax = fmax3(amax, fmaxf(fabsf(bf16_lo(qx[j].x)), fabsf(bf16_hi(qx[j].x))),
+                     fmaxf(fabsf(bf16_lo(qx[j].y)), fabsf(bf16_hi(qx[j].y))));
+        amax = fmax3(amax, fmaxf(fabsf(bf16_lo(qx[j].z)), fabsf(bf16_hi(qx[j].z))),
+                     fmaxf(fabsf(bf16_lo(qx[j].w)), fabsf(bf16_hi(qx[j].w))));
+      }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       const int e = q_exponent(amax);
-      const float inv = exp2i(-e), qs = exp2i(e);
+      const float inv = exp2i(-e);
+      auto scaled = [&](uint32_t w) { return pack_f16x2(bf16_lo(w) * inv, bf16_hi(w) * inv); };
 #pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        qf[n][j][0] = pack_f16x2(bf16_lo(w[2 * j]) * inv, bf16_hi(w[2 * j]) * inv);
-        qf[n][j][1] = pack_f16x2(bf16_lo(w[2 * j + 1]) * inv, bf16_hi(w[2 * j + 1]) * inv);
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        cq[n][k] = c0 * __shfl_sync(0xffffffffu, qs, 4 * (2 * t + k));
-        tok[n][k] = min((col0 + n * 8 + 2 * t + k) / prm.group, prm.q_len - 1);
-      }
+      for (int j = 0; j < kSteps / 2; ++j)
+        s_q[warp][j][lane] = make_uint4(scaled(qx[j].x), scaled(qx[j].y), scaled(qx[j].z), scaled(qx[j].w));
+      if (t == 0) s_cq[warp * 8 + g] = c0 * exp2i(e);
     }
-  }
-  __syncthreads();  // s_vis
-
-  // Tiles whose keys every column sees: before the speculative block (or, for one token, the end) and, with a
-  // window, from the last token's first key on.
-  const int full_end = prm.q_len == 1 && prm.spec_mask == nullptr ? s_k : max(0, start);
-  const int full_lo = prm.window > 0 ? max(0, s_k - prm.window) : 0;
-
-  float o[kNT][kSteps][4];
-  float m[kNT][2], l[kNT][2];
+    __syncthreads();  // s_vis, s_q, s_cq
+    float cq[kNT][2];
 #pragma unroll
-  for (int n = 0; n < kNT; ++n) {
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[n][j][k] = 0.f;
-    m[n][0] = m[n][1] = kNegInf;
-    l[n][0] = l[n][1] = 0.f;
-  }
-  const int r0 = (g >> 1) + 4 * (g & 1);  // keys of fragment rows g and g + 8
-  const int r1 = r0 + 8;
+    for (int n = 0; n < kNT; ++n) cq[n][0] = s_cq[n * 8 + 2 * t], cq[n][1] = s_cq[n * 8 + 2 * t + 1];
 
-  for (int i = 0; i < n_mine; ++i) {
-    cp_async_wait_group<kStages - 2>();
-    __syncwarp();
-    issue(i + kStages - 1);
-    const uint8_t* st = ring + (i % kStages) * L::kBytes;
-    const int tok0 = (t0 + warp + i * kWarps) * kTile;
+    // Tiles whose keys every column sees: before the speculative block (or, for one token, the end) and, with a
+    // window, from the last token's first key on.
+    const int keys_end = min(s_k, t1 * kTile);  // the segment's
+    const int full_end = min(keys_end, prm.q_len == 1 && prm.spec_mask == nullptr ? s_k : max(0, start));
+    const int full_lo = prm.window > 0 ? max(0, s_k - prm.window) : 0;
 
-    // ---- S^T = K Q^T
-    float s[kNT][4];
+    // u = score * cq (log2 units); p = 2^(u + neg_m); a score above `limit` moves the reference
+    float o[kNT][kSteps][4];
+    float neg_m[kNT][2], limit[kNT][2], l[kNT][2];
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-    {
+    for (int n = 0; n < kNT; ++n) {
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[n][j][k] = 0.f;
+      neg_m[n][0] = neg_m[n][1] = 0.f;
+      limit[n][0] = limit[n][1] = kNegInf;  // no key seen yet
+      l[n][0] = l[n][1] = 0.f;
+    }
+
+    // eight columns' fragments stay in registers, sixteen are read for every tile
+    constexpr bool kQRegs = kNT == 1 && kHd <= 128;
+    uint4 qr[kQRegs ? kNT : 1][kQRegs ? kSteps / 2 : 1];
+    if constexpr (kQRegs) {
+#pragma unroll
+      for (int w = 0; w < kSteps / 2; ++w) qr[0][w] = s_q[0][w][lane];
+    }
+
+    // S^T = K Q^T of the tile at st
+    auto scores = [&](const uint8_t* st, float (&s)[kNT][4]) {
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
       uint32_t ka[kKWords], kb[kKWords];
       if constexpr (kHd == 64) {
         const uint2 x = *reinterpret_cast<const uint2*>(st + L::kK + k_place<kHd>(r0, t >> 1) + (t & 1) * 8);
@@ -333,161 +470,192 @@ __global__ void __launch_bounds__(kWarps * 32, kNT == 1 && kHd <= 128 ? 2 : 1) f
         }
 #pragma unroll
         for (int n = 0; n < kNT; ++n) {
-          mma_f16_16x8x16(s[n], x[0], y[0], x[1], y[1], qf[n][2 * w][0], qf[n][2 * w][1]);
-          mma_f16_16x8x16(s[n], x[2], y[2], x[3], y[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
+          uint4 q;
+          if constexpr (kQRegs) q = qr[n][w];
+          else q = s_q[n][w][lane];
+          mma_f16_16x8x16(s[n], x[0], y[0], x[1], y[1], q.x, q.y);
+          mma_f16_16x8x16(s[n], x[2], y[2], x[3], y[3], q.z, q.w);
         }
       }
-    }
+    };
 
-    // ---- softmax: u = score in log2 units
-    const bool whole = tok0 + kTile <= full_end && tok0 >= full_lo;
-    bool grow = false;
+    const uint8_t* st = smem + warp * (kStages * kStage);
+    const uint8_t* const st_end = st + kStages * kStage;
+    int tok0 = mine0 * kTile;
+    auto tiles = [&](auto masked) {
+      constexpr bool kMasked = decltype(masked)::value;
+      float s[kU][kNT][4];
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) {
+      for (int u = 0; u < kU; ++u) scores(st + u * L::kBytes, s[u]);
+      uint32_t hidden = 0;  // bit 8 u + 4 n + k: key k / 2 of tile u is not for column k % 2 of column tile n
+      if constexpr (kMasked) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[n][k] *= cq[n][k & 1];
-      if (!whole) {
+        for (int u = 0; u < kU; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int p = tok0 + (k < 2 ? r0 : r1);
-          const int ti = tok[n][k & 1];
-          const int c_blk = p - start;
-          const bool vis = p < s_k && (c_blk < 0 || ((s_vis[ti] >> c_blk) & 1u)) &&
-                           (prm.window == 0 || ti - c_blk < prm.window);
-          if (!vis) s[n][k] = kNegInf;
-        }
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int p = tok0 + u * kTile + (k < 2 ? r0 : r1);
+              const int ti = min((col0 + n * 8 + 2 * t + (k & 1)) / prm.group, prm.q_len - 1);
+              const int c_blk = p - start;
+              const bool vis = p < keys_end && (c_blk < 0 || ((s_vis[ti] >> c_blk) & 1u)) &&
+                               (prm.window == 0 || ti - c_blk < prm.window);
+              if (!vis) {
+                s[u][n][k] = kNegInf;
+                hidden |= 1u << (8 * u + 4 * n + k);
+              }
+            }
       }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) grow |= fmaxf(s[n][k], s[n][k + 2]) > m[n][k] + kTau;
-    }
-    if (__any_sync(0xffffffffu, grow)) {
+      float top[kNT][2];
+      bool grow = false;
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float mx = fmaxf(s[n][k], s[n][k + 2]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          if (mx > m[n][k] + kTau) {
-            const float alpha = ex2_approx(m[n][k] - (mx - kBelow));
-            m[n][k] = mx - kBelow;
-            l[n][k] *= alpha;
+          top[n][k] = fmaxf(s[0][n][k], s[0][n][k + 2]);
+          if constexpr (kU == 2) top[n][k] = fmax3(top[n][k], s[kU - 1][n][k], s[kU - 1][n][k + 2]);
+          grow |= top[n][k] > limit[n][k];
+        }
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-            for (int j = 0; j < kSteps; ++j) {
-              o[n][j][k] *= alpha;
-              o[n][j][k + 2] *= alpha;
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float mx = top[n][k];
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            if (mx > limit[n][k]) {
+              const float m = mx * cq[n][k] - kBelow;
+              const float alpha = limit[n][k] == kNegInf ? 0.f : ex2_approx(-neg_m[n][k] - m);
+              neg_m[n][k] = -m;
+              limit[n][k] = (m + kTau) / cq[n][k];
+              l[n][k] *= alpha;
+#pragma unroll
+              for (int j = 0; j < kSteps; ++j) {
+                o[n][j][k] *= alpha;
+                o[n][j][k + 2] *= alpha;
+              }
             }
           }
-        }
-    }
-    uint32_t pf[kNT][2];
-#pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-      float p[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) p[k] = ex2_approx(s[n][k] - (m[n][k & 1] == kNegInf ? 0.f : m[n][k & 1]));
-      l[n][0] += p[0] + p[2];
-      l[n][1] += p[1] + p[3];
-      pf[n][0] = movmatrix_trans(pack_f16x2(p[0], p[1]));
-      pf[n][1] = movmatrix_trans(pack_f16x2(p[2], p[3]));
-    }
-
-    // ---- O^T += V^T P^T
-    {
-      uint32_t v[4][kVWords];
-      uint32_t sc[4];  // scale bytes of the lane's dims, keys t, t + 4, t + 8, t + 12
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = t + 4 * k;
-        if constexpr (kHd == 64) {
-          v[k][0] = *reinterpret_cast<const uint32_t*>(st + L::kV + v_place<kHd>(r, g >> 2) + (g & 3) * 4);
-          sc[k] = st[L::kVs + r * 4 + (g >> 1)];
-        } else if constexpr (kHd == 128) {
-          const uint2 x = *reinterpret_cast<const uint2*>(st + L::kV + v_place<kHd>(r, g >> 1) + (g & 1) * 8);
-          v[k][0] = x.x, v[k][1] = x.y;
-          sc[k] = st[L::kVs + r * 8 + g];
-        } else {
-          const uint4 x = *reinterpret_cast<const uint4*>(st + L::kV + v_place<kHd>(r, g));
-          v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
-          sc[k] = *reinterpret_cast<const uint16_t*>(st + L::kVs + r * 16 + 2 * g);
-        }
-        // a key that no column sees has a zero weight; its scale may be anything (NaN), so it is zeroed
-        if (!whole && (tok0 + r >= s_k || tok0 + r < k_lo)) sc[k] = 0;
       }
+      uint32_t pf[kU][kNT][2];
 #pragma unroll
-      for (int w = 0; w < kVWords; ++w) {
-        if (kHd == 256 && w == 2) {
+      for (int u = 0; u < kU; ++u)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sc[k] >>= 8;
+        for (int n = 0; n < kNT; ++n) {
+          float p[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) p[k] = ex2_approx(fmaf(s[u][n][k], cq[n][k & 1], neg_m[n][k & 1]));
+          if constexpr (kMasked) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if ((hidden >> (8 * u + 4 * n + k)) & 1u) p[k] = 0.f;
+          }
+          l[n][0] += p[0] + p[2];
+          l[n][1] += p[1] + p[3];
+          pf[u][n][0] = movmatrix_trans(pack_f16x2(p[0], p[1]));
+          pf[u][n][1] = movmatrix_trans(pack_f16x2(p[2], p[3]));
         }
-        const uint32_t sab = e4m3x2_to_f16x2((sc[0] & 0xFFu) | ((sc[1] & 0xFFu) << 8));
-        const uint32_t scd = e4m3x2_to_f16x2((sc[2] & 0xFFu) | ((sc[3] & 0xFFu) << 8));
-        constexpr uint32_t kLow = 0x0F0F0F0Fu;
-        uint32_t x[4], y[4], z[4], u[4];
-        e2m1x8_to_f16x2((v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), x);
-        e2m1x8_to_f16x2(((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow), y);
-        e2m1x8_to_f16x2((v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), z);
-        e2m1x8_to_f16x2(((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow), u);
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint8_t* sv = st + u * L::kBytes;
+        uint32_t v[4][kVWords];
+        uint32_t sc[4];  // scale bytes of the lane's dims, keys t, t + 4, t + 8, t + 12
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t a0 = mul_f16x2(x[k], sab), a1 = mul_f16x2(y[k], sab);
-          const uint32_t a2 = mul_f16x2(z[k], scd), a3 = mul_f16x2(u[k], scd);
+          const int r = t + 4 * k;
+          if constexpr (kHd == 64) {
+            v[k][0] = *reinterpret_cast<const uint32_t*>(sv + L::kV + v_place<kHd>(r, g >> 2) + (g & 3) * 4);
+            sc[k] = sv[L::kVs + r * 4 + (g >> 1)];
+          } else if constexpr (kHd == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(sv + L::kV + v_place<kHd>(r, g >> 1) + (g & 1) * 8);
+            v[k][0] = x.x, v[k][1] = x.y;
+            sc[k] = sv[L::kVs + r * 8 + g];
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(sv + L::kV + v_place<kHd>(r, g));
+            v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+            sc[k] = *reinterpret_cast<const uint16_t*>(sv + L::kVs + r * 16 + 2 * g);
+          }
+        }
+        if constexpr (kMasked) {  // a key that no column sees has a zero weight; its scale may be anything (NaN), so it is zeroed
 #pragma unroll
-          for (int n = 0; n < kNT; ++n) mma_f16_16x8x16(o[n][4 * w + k], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+          for (int k = 0; k < 4; ++k)
+            if (const int p = tok0 + u * kTile + t + 4 * k; p >= keys_end || p < k_lo) sc[k] = 0;
+        }
+#pragma unroll
+        for (int w = 0; w < kVWords; ++w) {
+          uint32_t s01, s23;  // scale bytes of two keys, one beside the other
+          if constexpr (kHd == 256) {
+            s01 = prmt(sc[0], sc[1], w < 2 ? 0x0040 : 0x0051);
+            s23 = prmt(sc[2], sc[3], w < 2 ? 0x0040 : 0x0051);
+          } else {
+            s01 = sc[0] | (sc[1] << 8);
+            s23 = sc[2] | (sc[3] << 8);
+          }
+          const uint32_t sab = e4m3x2_to_f16x2(s01), scd = e4m3x2_to_f16x2(s23);
+          constexpr uint32_t kLow = 0x0F0F0F0Fu;
+          uint32_t x[4], y[4], z[4], h[4];
+          e2m1x8_to_f16x2((v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), x);
+          e2m1x8_to_f16x2(((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow), y);
+          e2m1x8_to_f16x2((v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), z);
+          e2m1x8_to_f16x2(((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow), h);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a0 = mul_f16x2(x[k], sab), a1 = mul_f16x2(y[k], sab);
+            const uint32_t a2 = mul_f16x2(z[k], scd), a3 = mul_f16x2(h[k], scd);
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) mma_f16_16x8x16(o[n][4 * w + k], a0, a1, a2, a3, pf[u][n][0], pf[u][n][1]);
+          }
         }
       }
+      st += kStage;
+      if (st == st_end) st -= kStages * kStage;
+      tok0 += kWarps * kU * kTile;
+    };
+    for (int i = 0; i < n_mine; ++i) {
+      cp_async_wait_group<kStages - 2>();
+      __syncwarp();
+      issue(i + kStages - 1);
+      if (tok0 + kU * kTile <= full_end && tok0 >= full_lo) tiles(std::false_type{});
+      else tiles(std::true_type{});
     }
-  }
 
-  // ---- the warps' states are merged in shared memory, in fragment order
-  cp_async_wait_all();
+    // ---- the warps' states are merged in shared memory, in fragment order
+    cp_async_wait_all();
 #pragma unroll
-  for (int n = 0; n < kNT; ++n)
+    for (int n = 0; n < kNT; ++n)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float x = l[n][k];
-      x += __shfl_xor_sync(0xffffffffu, x, 4);
-      x += __shfl_xor_sync(0xffffffffu, x, 8);
-      x += __shfl_xor_sync(0xffffffffu, x, 16);
-      l[n][k] = x;
-      if (g == 0) {
-        s_m[warp][n * 8 + 2 * t + k] = m[n][k];
-        s_l[warp][n * 8 + 2 * t + k] = x;
+      for (int k = 0; k < 2; ++k) {
+        float x = l[n][k];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (g == 0) {
+          s_m[warp][n * 8 + 2 * t + k] = limit[n][k] == kNegInf ? kNegInf : -neg_m[n][k];
+          s_l[warp][n * 8 + 2 * t + k] = x;
+        }
       }
+    __syncthreads();  // also: every warp is done with its ring
+    float4* part = reinterpret_cast<float4*>(smem);  // [warp][n][j][lane]
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+      float f[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float mx = kNegInf;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][n * 8 + 2 * t + k]);
+        f[k] = limit[n][k] == kNegInf ? 0.f : ex2_approx(-neg_m[n][k] - mx);
+      }
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+        part[((warp * kNT + n) * kSteps + j) * 32 + lane] =
+            make_float4(o[n][j][0] * f[0], o[n][j][1] * f[1], o[n][j][2] * f[0], o[n][j][3] * f[1]);
     }
-  __syncthreads();  // also: every warp is done with its ring
-  float4* part = reinterpret_cast<float4*>(smem);  // [warp][n][j][lane]
-#pragma unroll
-  for (int n = 0; n < kNT; ++n) {
-    float f[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float mx = kNegInf;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][n * 8 + 2 * t + k]);
-      f[k] = m[n][k] == kNegInf ? 0.f : ex2_approx(m[n][k] - mx);
-    }
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j)
-      part[((warp * kNT + n) * kSteps + j) * 32 + lane] =
-          make_float4(o[n][j][0] * f[0], o[n][j][1] * f[1], o[n][j][2] * f[0], o[n][j][3] * f[1]);
-  }
-  __syncthreads();
-  const float v_scale = __ldg(prm.v_scale);
-  const size_t slot = (static_cast<size_t>(seq) * gridDim.y + blockIdx.y) * prm.splits + split;
-  for (int x = threadIdx.x; x < kNT * kSteps * 32; x += kWarps * 32) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 y = part[w * (kNT * kSteps * 32) + x];
-      a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
-    }
-    const int n = x / (kSteps * 32), j = x / 32 % kSteps, gg = x % 32 / 4, tt = x % 4;
-    if (prm.splits > 1) prm.ws_o[slot * (kNT * kSteps * 32) + x] = a;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = n * 8 + 2 * tt + k;
+    if (threadIdx.x < kNT * 8) {  // a column's end: its sums, its row, and what its values are multiplied by
+      const int c = threadIdx.x;
       float mx = kNegInf, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][c]);
@@ -495,66 +663,140 @@ __global__ void __launch_bounds__(kWarps * 32, kNT == 1 && kHd <= 128 ? 2 : 1) f
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) sum += s_l[w][c] * ex2_approx(s_m[w][c] - mx);
       }
-      if (prm.splits > 1) {
-        if (j == 0 && gg == 0) prm.ws_ml[slot * (kNT * 8) + c] = make_float2(mx, sum);
+      if (slot >= 0) {
+        prm.ws_ml[slot * (kNT * 8) + c] = make_float2(mx, sum);
+      } else if (c < ncols) {
+        const int col = col0 + c, token = col / prm.group, hq = kvh * prm.group + col - token * prm.group;
+        const int64_t row = (static_cast<int64_t>(b) * prm.q_len + token) * prm.h_q + hq;
+        float fac, lse;
+        finish_row(mx, sum, prm.sinks ? __ldg(prm.sinks + hq) : kNegInf, __ldg(prm.v_scale), &fac, &lse);
+        s_cq[c] = fac;
+        s_row[c] = row;
+        prm.lse[row] = lse;
+      }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < kNT * kSteps * 32; x += kWarps * 32) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 y = part[w * (kNT * kSteps * 32) + x];
+        a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
+      }
+      if (slot >= 0) {
+        prm.ws_o[slot * (kNT * kSteps * 32) + x] = a;
         continue;
       }
-      if (c >= ncols) continue;
-      const int col = col0 + c, hq = kvh * prm.group + col % prm.group;
-      const size_t row = (static_cast<size_t>(b) * prm.q_len + col / prm.group) * prm.h_q + hq;
-      float fac, lse;
-      finish_row(mx, sum, prm.sinks ? prm.sinks[hq] : kNegInf, v_scale, &fac, &lse);
-      *reinterpret_cast<uint32_t*>(prm.out + row * kHd + gg * (kHd / 8) + 2 * j) =
-          pack_bf16x2((k ? a.y : a.x) * fac, (k ? a.w : a.z) * fac);
-      if (j == 0 && gg == 0) prm.lse[row] = lse;
+      const int n = x / (kSteps * 32), j = x / 32 % kSteps, c = n * 8 + 2 * (x % 4);
+      const int d = x % 32 / 4 * (kHd / 8) + 2 * j;
+      if (c < ncols)
+        *reinterpret_cast<uint32_t*>(prm.out + s_row[c] * kHd + d) = pack_bf16x2(a.x * s_cq[c], a.z * s_cq[c]);
+      if (c + 1 < ncols)
+        *reinterpret_cast<uint32_t*>(prm.out + s_row[c + 1] * kHd + d) =
+            pack_bf16x2(a.y * s_cq[c + 1], a.w * s_cq[c + 1]);
     }
+    __syncthreads();  // the ring is free for the next segment's copies
   }
 }
 
-// Merge of the shards: one CTA per (sequence, KV head, column tile); thread x owns one float4 of the fragment order
-// (two dims of two columns), each weighted by 2^(m_s - M).
-template <int kHd, int kNT>
-__global__ void __launch_bounds__(256) fp4_combine_kernel(const Params prm) {
+// Merge of the shards of one (sequence, KV head) and column tile.  Lane x of a warp owns one float4 of the fragment
+// order (two dims of two columns) of one step (16 dims).  With kGroups = 1 the four warps take four steps; with 4
+// they take shards w, w + 4, ... of one step and meet in shared memory (few sequences, many shards).
+template <int kHd, int kNT, int kGroups>
+__global__ void __launch_bounds__(128) fp4_combine_kernel(const __grid_constant__ Params prm) {
   constexpr int kSteps = kHd / 16, kFrag = kNT * kSteps * 32;
+  __shared__ float4 s_o[kGroups][32], s_ml[kGroups][32];
   griddep_wait();
-  const int seq = blockIdx.x, b = seq / prm.h_kv, kvh = seq % prm.h_kv;
+  const int seq = blockIdx.x;
+  const int group = kGroups == 1 ? 0 : threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int frag = kGroups == 1 ? blockIdx.z * 4 + threadIdx.x / 32 : blockIdx.z;
+  const int n = frag / kSteps, j = frag % kSteps;
   const int col0 = blockIdx.y * (kNT * 8);
   const int ncols = min(prm.q_len * prm.group - col0, kNT * 8);
-  const size_t slot0 = (static_cast<size_t>(seq) * gridDim.y + blockIdx.y) * prm.splits;
-  const float v_scale = __ldg(prm.v_scale);
-  for (int x = threadIdx.x; x < kFrag; x += 256) {
-    const int n = x / (kSteps * 32), j = x / 32 % kSteps, gg = x % 32 / 4, tt = x % 4;
-    const int c = n * 8 + 2 * tt;
-    if (c >= ncols) continue;
-    float m0 = kNegInf, m1 = kNegInf;
-    for (int s = 0; s < prm.splits; ++s) {
-      const float4 ml = *reinterpret_cast<const float4*>(prm.ws_ml + (slot0 + s) * (kNT * 8) + c);
-      m0 = fmaxf(m0, ml.x);
-      m1 = fmaxf(m1, ml.z);
+  const int c = n * 8 + 2 * (lane % 4);
+  // the shards' slots: first, then next, next + step, ...
+  long long first, next;
+  int step, count;
+  if (prm.splits == 0) {
+    const int2 span = __ldg(prm.ws_span + seq);
+    if (span.x == span.y) return;  // within one piece: written there
+    const long long base = static_cast<long long>(blockIdx.y) * prm.units * 2;
+    first = base + 2 * span.x + 1;
+    next = base + 2 * (span.x + 1);
+    step = 2;
+    count = span.y - span.x + 1;  // 0 where there is no key (1, 0)
+  } else {
+    first = (static_cast<long long>(blockIdx.y) * gridDim.x + seq) * prm.splits;
+    next = first + 1;
+    step = 1;
+    count = prm.splits;
+  }
+  const int b = seq / prm.h_kv, kvh = seq % prm.h_kv;
+  float m0 = kNegInf, m1 = kNegInf, l0 = 0.f, l1 = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = group; s0 < count; s0 += 4 * kGroups) {  // four shards' loads in flight
+    float4 ml[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = s0 + kGroups * i;
+      ml[i] = make_float4(kNegInf, 0.f, kNegInf, 0.f);
+      y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < count) {
+        const long long slot = s == 0 ? first : next + (s - 1) * step;
+        ml[i] = *reinterpret_cast<const float4*>(prm.ws_ml + slot * (kNT * 8) + c);
+        y[i] = prm.ws_o[slot * kFrag + frag * 32 + lane];
+      }
+    }
+    float x0 = m0, x1 = m1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x0 = fmaxf(x0, ml[i].x);
+      x1 = fmaxf(x1, ml[i].z);
+    }
+    const float b0 = x0 == kNegInf ? 0.f : x0, b1 = x1 == kNegInf ? 0.f : x1;
+    const float f0 = ex2_approx(m0 - b0), f1 = ex2_approx(m1 - b1);
+    m0 = x0, m1 = x1;
+    l0 *= f0, l1 *= f1;
+    a.x *= f0, a.y *= f1, a.z *= f0, a.w *= f1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float w0 = ex2_approx(ml[i].x - b0), w1 = ex2_approx(ml[i].z - b1);
+      l0 += ml[i].y * w0, l1 += ml[i].w * w1;
+      a.x += y[i].x * w0, a.y += y[i].y * w1, a.z += y[i].z * w0, a.w += y[i].w * w1;
+    }
+  }
+  if constexpr (kGroups > 1) {
+    s_o[group][lane] = a;
+    s_ml[group][lane] = make_float4(m0, l0, m1, l1);
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int w = 1; w < kGroups; ++w) {
+      m0 = fmaxf(m0, s_ml[w][lane].x);
+      m1 = fmaxf(m1, s_ml[w][lane].z);
     }
     const float b0 = m0 == kNegInf ? 0.f : m0, b1 = m1 == kNegInf ? 0.f : m1;
-    float l0 = 0.f, l1 = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < prm.splits; ++s) {
-      const float4 ml = *reinterpret_cast<const float4*>(prm.ws_ml + (slot0 + s) * (kNT * 8) + c);
-      const float4 y = prm.ws_o[(slot0 + s) * kFrag + x];
+    l0 = l1 = 0.f;
+    a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kGroups; ++w) {
+      const float4 ml = s_ml[w][lane], y = s_o[w][lane];
       const float w0 = ex2_approx(ml.x - b0), w1 = ex2_approx(ml.z - b1);
-      l0 += ml.y * w0;
-      l1 += ml.w * w1;
+      l0 += ml.y * w0, l1 += ml.w * w1;
       a.x += y.x * w0, a.y += y.y * w1, a.z += y.z * w0, a.w += y.w * w1;
     }
+  }
+  const float v_scale = __ldg(prm.v_scale);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (c + k >= ncols) continue;
-      const int col = col0 + c + k, hq = kvh * prm.group + col % prm.group;
-      const size_t row = (static_cast<size_t>(b) * prm.q_len + col / prm.group) * prm.h_q + hq;
-      float fac, lse;
-      finish_row(k ? m1 : m0, k ? l1 : l0, prm.sinks ? prm.sinks[hq] : kNegInf, v_scale, &fac, &lse);
-      *reinterpret_cast<uint32_t*>(prm.out + row * kHd + gg * (kHd / 8) + 2 * j) =
-          pack_bf16x2((k ? a.y : a.x) * fac, (k ? a.w : a.z) * fac);
-      if (j == 0 && gg == 0) prm.lse[row] = lse;
-    }
+  for (int k = 0; k < 2; ++k) {
+    if (c + k >= ncols) continue;
+    const int col = col0 + c + k, hq = kvh * prm.group + col % prm.group;
+    const size_t row = (static_cast<size_t>(b) * prm.q_len + col / prm.group) * prm.h_q + hq;
+    float fac, lse;
+    finish_row(k ? m1 : m0, k ? l1 : l0, prm.sinks ? prm.sinks[hq] : kNegInf, v_scale, &fac, &lse);
+    *reinterpret_cast<uint32_t*>(prm.out + row * kHd + lane / 4 * (kHd / 8) + 2 * j) =
+        pack_bf16x2((k ? a.y : a.x) * fac, (k ? a.w : a.z) * fac);
+    if (j == 0 && lane < 4) prm.lse[row] = lse;
   }
 }
 
@@ -567,61 +809,88 @@ int col_tiles(int cols, int* nt) {  // columns run eight or sixteen to a CTA
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// How a call is laid out: shards of every sequence (1: none, 0: balanced pieces), pieces, and the workspace.
+struct Plan {
+  int nt, ct, splits, units;
+  size_t slots, ml, span, bytes;  // partial states, and where (m, l) and the spans of pieces begin
+};
+
+Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long capacity, int window, int num_splits) {
+  Plan p;
+  p.ct = col_tiles(q_len * (h_q / h_kv), &p.nt);
+  long long longest = std::max(capacity, 1LL);
+  if (window > 0) longest = std::min(longest, static_cast<long long>(window) + q_len - 1 + kTile);
+  const long long tiles = (longest + kTile - 1) / kTile;
+  const long long seqs = static_cast<long long>(bs) * h_kv;
+  const int resident = device_sms() * (head_dim == 256 ? 2 : 3);  // Shape::kPerSm
+  p.units = 0;
+  if (num_splits > 0) {
+    p.splits = static_cast<int>(std::min<long long>(num_splits, std::max(1LL, (tiles + 7) / 8)));
+  } else if (tiles <= 64 || seqs * p.ct >= 8LL * resident || bs > kMaxLine ||
+             seqs * (tiles + kFixed) > 0x7FFFFFFFll) {
+    // Short contexts: one CTA a sequence takes no longer than a piece and its merge.  Many sequences: their CTAs
+    // balance by themselves.  (The line's places are counted in 32 bits.)
+    p.splits = 1;
+  } else {
+    p.splits = 0;
+    p.units = std::max(1, resident / p.ct);
+  }
+  p.slots = p.splits == 1 ? 0 : static_cast<size_t>(p.ct) * (p.splits == 0 ? 2 * p.units : seqs * p.splits);
+  p.ml = round_up(p.slots * p.nt * 8 * head_dim * sizeof(float), 256);
+  p.span = p.ml + round_up(p.slots * p.nt * 8 * sizeof(float2), 256);
+  p.bytes = p.span + (p.splits == 0 ? round_up(static_cast<size_t>(seqs) * sizeof(int2), 256) : 0);
+  return p;
+}
+
+bool sizes_ok(int bs, int h_q, int h_kv, int head_dim, int q_len, int window, int num_splits) {
+  return (head_dim == 64 || head_dim == 128 || head_dim == 256) && bs >= 0 && h_q >= 1 && h_kv >= 1 &&
+         h_q % h_kv == 0 && q_len >= 1 && q_len <= kMaxQLen &&
+         static_cast<long long>(q_len) * (h_q / h_kv) <= kMaxCols && window >= 0 && num_splits >= 0;
+}
+
 template <int kHd, int kNT>
 cudaError_t launch(const Params& prm, int seqs, int ct, cudaStream_t stream) {
-  const size_t smem = std::max<size_t>(static_cast<size_t>(kWarps) * kStages * Lay<kHd>::kBytes,
-                                       static_cast<size_t>(kWarps) * kNT * (kHd / 16) * 32 * sizeof(float4));
+  constexpr int kWarps = Shape<kHd, kNT>::kWarps;
+  constexpr size_t smem = std::max<size_t>(static_cast<size_t>(kWarps) * Shape<kHd, kNT>::kStages *
+                                               Shape<kHd, kNT>::kU * Lay<kHd>::kBytes,
+                                           static_cast<size_t>(kWarps) * kNT * (kHd / 16) * 32 * sizeof(float4));
+  static_assert(Shape<kHd, kNT>::kPerSm * (smem + 12 * 1024) <= 233472, "the CTAs fit in an SM's shared memory");
   static std::atomic<uint64_t> configured{0};
   cudaError_t e = configure_once(configured, [&] {
     return cudaFuncSetAttribute(reinterpret_cast<const void*>(fp4_decode_kernel<kHd, kNT>),
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   });
   if (e != cudaSuccess) return e;
-  e = launch_dependent(fp4_decode_kernel<kHd, kNT>,
-                       dim3(static_cast<unsigned>(seqs) * static_cast<unsigned>(prm.splits), ct), dim3(kWarps * 32),
-                       smem, stream, prm);
+  const unsigned grid = prm.splits == 0 ? static_cast<unsigned>(prm.units)
+                                        : static_cast<unsigned>(seqs) * static_cast<unsigned>(prm.splits);
+  e = launch_dependent(fp4_decode_kernel<kHd, kNT>, dim3(grid, ct), dim3(kWarps * 32), smem, stream, prm);
   if (e != cudaSuccess || prm.splits == 1) return e;
-  return launch_dependent(fp4_combine_kernel<kHd, kNT>, dim3(static_cast<unsigned>(seqs), ct), dim3(256), 0, stream,
-                          prm);
+  constexpr unsigned kFrags = kNT * (kHd / 16);
+  if (static_cast<long long>(seqs) * ct >= device_sms())
+    return launch_dependent(fp4_combine_kernel<kHd, kNT, 1>, dim3(static_cast<unsigned>(seqs), ct, kFrags / 4),
+                            dim3(128), 0, stream, prm);
+  return launch_dependent(fp4_combine_kernel<kHd, kNT, 4>, dim3(static_cast<unsigned>(seqs), ct, kFrags), dim3(128),
+                          0, stream, prm);
 }
 
 }  // namespace fp4
 
-int fp4_choose_splits(int bs, int h_q, int h_kv, int max_seqlen, int q_len, int window, int num_sms, int num_splits) {
-  if (bs < 1 || h_kv < 1 || h_q < h_kv || q_len < 1 || num_sms < 1) return 1;
-  long long longest = std::max(max_seqlen, 1);
-  if (window > 0) longest = std::min(longest, static_cast<long long>(window) + q_len - 1 + fp4::kTile);
-  const long long tiles = (longest + fp4::kTile - 1) / fp4::kTile;
-  const long long most = std::max(1LL, std::min(256LL, (tiles + fp4::kWarps - 1) / fp4::kWarps));
-  if (num_splits > 0) return static_cast<int>(std::min<long long>(num_splits, most));
-  int nt = 1;
-  const long long ctas = static_cast<long long>(bs) * h_kv *
-                         fp4::col_tiles(static_cast<int>(std::min<long long>(
-                             static_cast<long long>(q_len) * (h_q / h_kv), fp4::kMaxCols)), &nt);
-  const long long want = (4LL * num_sms + ctas - 1) / ctas;
-  return static_cast<int>(std::max(1LL, std::min(want, most)));
-}
-
-size_t fp4_workspace_bytes(int bs, int h_q, int h_kv, int head_dim, int q_len, int splits) {
-  if (bs < 1 || h_kv < 1 || h_q < h_kv || q_len < 1 || splits < 2) return 0;
-  int nt = 1;
-  const long long cols = static_cast<long long>(q_len) * (h_q / h_kv);
-  if (cols > fp4::kMaxCols) return 0;
-  const int ct = fp4::col_tiles(static_cast<int>(cols), &nt);
-  const size_t slots = static_cast<size_t>(bs) * h_kv * ct * splits;
-  return fp4::round_up(slots * nt * 8 * head_dim * sizeof(float), 256) +
-         fp4::round_up(slots * nt * 8 * sizeof(float2), 256);
+size_t fp4_workspace_bytes(int bs, int h_q, int h_kv, int head_dim, int q_len, long long max_seqlen, int window,
+                           int num_splits) {
+  if (!fp4::sizes_ok(bs, h_q, h_kv, head_dim, q_len, window, num_splits) || bs == 0) return 0;
+  return fp4::make_plan(bs, h_q, h_kv, head_dim, q_len, max_seqlen, window, num_splits).bytes;
 }
 
 fp8mla_status_t fp4_decode_entry(const Fp4DecodeArgs& a, cudaStream_t stream) {
-  if ((a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256) || a.bs < 0 || a.h_q < 1 || a.h_kv < 1 ||
-      a.h_q % a.h_kv != 0 || a.q_len < 1 || a.q_len > fp4::kMaxQLen ||
-      static_cast<long long>(a.q_len) * (a.h_q / a.h_kv) > fp4::kMaxCols || a.window < 0 || a.num_blocks < 1 ||
-      a.max_blocks < 1 || a.num_splits < 0 || !(a.softmax_scale > 0.f))
+  if (!fp4::sizes_ok(a.bs, a.h_q, a.h_kv, a.head_dim, a.q_len, a.window, a.num_splits) || a.num_blocks < 1 ||
+      a.max_blocks < 1 || !(a.softmax_scale > 0.f))
     return FP8MLA_ERR_INVALID_ARG;
   int page_shift = 0;
   while (page_shift < 5 && (fp4::kTile << page_shift) != a.page_size) ++page_shift;
   if (page_shift == 5) return FP8MLA_ERR_INVALID_ARG;  // 16, 32, 64, 128 or 256 keys a page
+  if (static_cast<long long>(a.num_blocks) * a.page_size >= (1ll << 31) ||
+      static_cast<long long>(a.num_blocks) * a.page_size * a.h_kv >= (1ll << 32))
+    return FP8MLA_ERR_INVALID_ARG;  // rows are counted in 32 bits
   if (a.bs == 0) return FP8MLA_OK;
   if (a.q == nullptr || a.k_cache == nullptr || a.v_cache == nullptr || a.k_block_scales == nullptr ||
       a.v_block_scales == nullptr || a.k_scale == nullptr || a.v_scale == nullptr || a.block_table == nullptr ||
@@ -631,17 +900,16 @@ fp8mla_status_t fp4_decode_entry(const Fp4DecodeArgs& a, cudaStream_t stream) {
        reinterpret_cast<uintptr_t>(a.v_cache) | reinterpret_cast<uintptr_t>(a.k_block_scales) |
        reinterpret_cast<uintptr_t>(a.v_block_scales) | reinterpret_cast<uintptr_t>(a.out)) & 15u)
     return FP8MLA_ERR_INVALID_ARG;
-  const long long capacity = std::min(static_cast<long long>(a.max_blocks) * a.page_size, 0x7FFFFFFFll - 256);
-  int splits = fp4_choose_splits(a.bs, a.h_q, a.h_kv, static_cast<int>(capacity), a.q_len, a.window, device_sms(),
-                                 a.num_splits);
-  int nt = 1;
-  const int ct = fp4::col_tiles(a.q_len * (a.h_q / a.h_kv), &nt);
-  const size_t need = fp4_workspace_bytes(a.bs, a.h_q, a.h_kv, a.head_dim, a.q_len, splits);
-  if (splits > 1) {
+  const long long capacity = static_cast<long long>(a.max_blocks) * a.page_size;
+  if (capacity > 0x7FFFFF00ll) return FP8MLA_ERR_INVALID_ARG;
+  const fp4::Plan plan =
+      fp4::make_plan(a.bs, a.h_q, a.h_kv, a.head_dim, a.q_len, capacity, a.window, a.num_splits);
+  if (plan.bytes > 0) {
     if (a.workspace == nullptr || (reinterpret_cast<uintptr_t>(a.workspace) & 255u)) return FP8MLA_ERR_INVALID_ARG;
-    if (a.workspace_bytes < need) return FP8MLA_ERR_WORKSPACE_TOO_SMALL;
+    if (a.workspace_bytes < plan.bytes) return FP8MLA_ERR_WORKSPACE_TOO_SMALL;
   }
-  if (static_cast<long long>(a.bs) * a.h_kv * splits > 0x7FFFFFFFll) return FP8MLA_ERR_INVALID_ARG;
+  const long long seqs = static_cast<long long>(a.bs) * a.h_kv;
+  if (seqs * std::max(plan.splits, 1) > 0x7FFFFFFFll) return FP8MLA_ERR_INVALID_ARG;
   fp4::Params p;
   p.q = static_cast<const uint16_t*>(a.q);
   p.k = static_cast<const uint8_t*>(a.k_cache);
@@ -656,30 +924,30 @@ fp8mla_status_t fp4_decode_entry(const Fp4DecodeArgs& a, cudaStream_t stream) {
   p.sinks = a.sinks;
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
-  const size_t slots = static_cast<size_t>(a.bs) * a.h_kv * ct * splits;
   p.ws_o = static_cast<float4*>(a.workspace);
-  p.ws_ml = splits > 1 ? reinterpret_cast<float2*>(static_cast<char*>(a.workspace) +
-                                                   fp4::round_up(slots * nt * 8 * a.head_dim * sizeof(float), 256))
-                       : nullptr;
+  p.ws_ml = plan.bytes > 0 ? reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + plan.ml) : nullptr;
+  p.ws_span = plan.splits == 0 ? reinterpret_cast<int2*>(static_cast<char*>(a.workspace) + plan.span) : nullptr;
   p.num_blocks = a.num_blocks;
   p.max_blocks = a.max_blocks;
+  p.bs = a.bs;
   p.h_q = a.h_q;
   p.h_kv = a.h_kv;
   p.group = a.h_q / a.h_kv;
-  p.splits = splits;
+  p.splits = plan.splits;
+  p.units = plan.units;
   p.q_len = a.q_len;
   p.window = a.window;
   p.page_shift = page_shift;
   p.softmax_scale = a.softmax_scale;
-  const int seqs = a.bs * a.h_kv;
+  const int n = static_cast<int>(seqs);
   cudaError_t e;
-  switch (a.head_dim + nt) {
-    case 64 + 1: e = fp4::launch<64, 1>(p, seqs, ct, stream); break;
-    case 64 + 2: e = fp4::launch<64, 2>(p, seqs, ct, stream); break;
-    case 128 + 1: e = fp4::launch<128, 1>(p, seqs, ct, stream); break;
-    case 128 + 2: e = fp4::launch<128, 2>(p, seqs, ct, stream); break;
-    case 256 + 1: e = fp4::launch<256, 1>(p, seqs, ct, stream); break;
-    default: e = fp4::launch<256, 2>(p, seqs, ct, stream); break;
+  switch (a.head_dim + plan.nt) {
+    case 64 + 1: e = fp4::launch<64, 1>(p, n, plan.ct, stream); break;
+    case 64 + 2: e = fp4::launch<64, 2>(p, n, plan.ct, stream); break;
+    case 128 + 1: e = fp4::launch<128, 1>(p, n, plan.ct, stream); break;
+    case 128 + 2: e = fp4::launch<128, 2>(p, n, plan.ct, stream); break;
+    case 256 + 1: e = fp4::launch<256, 1>(p, n, plan.ct, stream); break;
+    default: e = fp4::launch<256, 2>(p, n, plan.ct, stream); break;
   }
   return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
 }

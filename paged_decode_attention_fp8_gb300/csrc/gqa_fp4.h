@@ -31,8 +31,8 @@ struct Fp4DecodeArgs {
 };
 
 fp8mla_status_t fp4_decode_entry(const Fp4DecodeArgs& a, cudaStream_t stream);
-size_t fp4_workspace_bytes(int bs, int h_q, int h_kv, int head_dim, int q_len, int splits);
-int fp4_choose_splits(int bs, int h_q, int h_kv, int max_seqlen, int q_len, int window, int num_sms, int num_splits);
+size_t fp4_workspace_bytes(int bs, int h_q, int h_kv, int head_dim, int q_len, long long max_seqlen, int window,
+                           int num_splits);
 uint32_t fp4_read_and_clear_status();
 
 }  // namespace fp8mla

@@ -131,7 +131,7 @@ def test_single_sequences(lens):
 def test_a_small_grid_is_split_and_merged():
     """One sequence of one KV head: the keys are cut over the GPU; every forced count agrees too."""
     x = Inputs(6, [9001], 1, 4, 128, 16)
-    assert fm.gqa_fp4_num_splits(1, 4, 1, 9008) > 1
+    assert fm.gqa_fp4_workspace_bytes(1, 4, 1, 128, 9008) > 0
     for splits in (0, 1, 2, 3, 16, 60, 1000):
         x.check(*x.run(num_splits=splits))
 
@@ -253,7 +253,7 @@ def test_outputs_given_graph_and_two_streams():
     want, want_lse = fm.paged_gqa_decode_fp4(**t, num_splits=4)
     out3, _ = fm.paged_gqa_decode_fp4(**{**t, "q": t["q"][:, 0].contiguous()}, num_splits=4)
     assert out3.shape == (3, 8, 128) and torch.equal(out3, want[:, 0])
-    need = fm.gqa_fp4_workspace_bytes(3, 8, 2, 128, 1, 4)
+    need = fm.gqa_fp4_workspace_bytes(3, 8, 2, 128, x.bt.shape[1] * 16, num_splits=4)
     streams, outs = [torch.cuda.Stream() for _ in range(2)], []
     torch.cuda.synchronize()
     for s in streams:

@@ -119,7 +119,8 @@ def _decode(**over):
                                   dict(blocks=0), dict(mb=0), dict(bs=-1), dict(q=None), dict(kc=None), dict(vb=None),
                                   dict(ks=None), dict(bt=None), dict(sl=None), dict(out=None), dict(lse=None),
                                   dict(q=P + 8), dict(kc=P + 8), dict(vb=P + 4), dict(out=P + 2),
-                                  dict(splits=2, mb=64, ws=None), dict(splits=2, mb=64, ws=P + 64)])
+                                  dict(splits=2, mb=64, ws=None), dict(splits=2, mb=64, ws=P + 64),
+                                  dict(splits=0, mb=4096, ws=None), dict(blocks=1 << 27), dict(mb=1 << 28)])
 def test_decode_refusals(over):
     assert _decode(**over) == 1
 
@@ -129,19 +130,25 @@ def test_decode_workspace_and_empty_batch():
     assert _decode(bs=0, q=None, out=None, lse=None) == 0
 
 
-def test_split_rule_and_workspace():
-    lib = fm.lib()
-    # one shard per 128 keys at most, however many are asked for
-    assert lib.paged_gqa_fp4_num_splits(1, 4, 1, 1024, 1, 0, 152, 100) == 8
-    assert lib.paged_gqa_fp4_num_splits(1, 4, 1, 16, 1, 0, 152, 100) == 1
-    # a window bounds the keys that can be shared out: 100 + 15 keys in one shard
-    assert lib.paged_gqa_fp4_num_splits(1, 4, 1, 100000, 1, 100, 152, 100) == 1
-    assert lib.paged_gqa_fp4_num_splits(1, 4, 1, 1 << 20, 1, 0, 152, 0) > 100
-    assert lib.paged_gqa_fp4_workspace_bytes(3, 8, 2, 128, 1, 1) == 0
-    # 3 * 2 slots a shard, 8 columns of 128 floats and a pair of floats each
-    assert lib.paged_gqa_fp4_workspace_bytes(3, 8, 2, 128, 1, 4) == 24 * 8 * 128 * 4 + 24 * 8 * 8
+def test_workspace_of_each_layout():
+    size = fm.gqa_fp4_workspace_bytes
+    slot = 8 * 128 * 4 + 8 * 8  # eight columns of 128 floats and a pair of floats each
+    assert size(3, 8, 2, 128, 4096, num_splits=1) == 0
+    assert size(3, 8, 2, 128, 1024) == 0                    # short contexts: one CTA each
+    assert size(2000, 8, 2, 128, 8192) == 0                 # more sequences than a CTA sums
+    assert size(3, 8, 2, 128, 4096, num_splits=4) == 24 * slot
+    # at most one shard per 128 keys, however many are asked for; a window bounds the keys
+    assert size(1, 4, 1, 128, 1000, num_splits=100) == 8 * 8 * 128 * 4 + 8 * 8 * 8
+    assert size(1, 4, 1, 128, 16, num_splits=100) == 0
+    assert size(1, 4, 1, 128, 100000, window=100, num_splits=100) == 0
     # sixteen columns a tile past eight
-    assert lib.paged_gqa_fp4_workspace_bytes(1, 24, 2, 64, 1, 2) == 4 * 16 * 64 * 4 + 4 * 16 * 8
+    assert size(1, 24, 2, 64, 256, num_splits=2) == 4 * 16 * 64 * 4 + 4 * 16 * 8
+    auto = size(1, 4, 1, 128, 1 << 17)                      # two states a piece, and the line of tiles
+    assert auto >= 2 * slot and auto % 256 == 0
+    for bad in (dict(head_dim=96), dict(h_q=5), dict(q_len=17), dict(window=-1), dict(num_splits=-1), dict(bs=0)):
+        a = dict(bs=1, h_q=4, h_kv=2, head_dim=128, max_seqlen=1 << 17)
+        a.update(bad)
+        assert size(**a) == 0
 
 
 def test_the_other_entries_refuse_the_4_bit_encoding():
