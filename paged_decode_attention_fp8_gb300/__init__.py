@@ -3,14 +3,16 @@
 Python binding of ``libfp8mla.so`` (declared in ``include/fp8mla.h``).  This
 module only marshals arguments: it checks dtypes and shapes, allocates
 outputs with torch when the caller does not pass them, and hands raw device
-pointers and the current CUDA stream to the C ABI.  Every step of the
-attention runs in the library's CUDA kernels; there is no other code path,
-and a missing library is an error.
+pointers and the current CUDA stream to the C ABI (rotary, append, read-back
+and 4-bit decode calls through the native ``_binding``, the others through
+ctypes).  Every step of the attention runs in the library's CUDA kernels;
+there is no other code path, and a missing library is an error.
 """
 
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 
@@ -106,6 +108,24 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_binding = None
+
+
+def _native():
+    """The native marshalling of the per-step operators (raises if it has not been built)."""
+    global _binding
+    if _binding is None:
+        lib()
+        try:
+            module = importlib.import_module("._binding", __name__)
+        except ImportError as e:
+            raise RuntimeError("the native binding is missing or was built for another torch: build it with "
+                               "`python -m paged_decode_attention_fp8_gb300.build`") from e
+        module.set_error(FP8MLAError)
+        _binding = module
+    return _binding
+
+
 def _check(status: int, where: str) -> None:
     if status != OK:
         raise FP8MLAError(status, where)
@@ -117,24 +137,6 @@ def _ptr(t) -> int | None:
 
 def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
-
-
-class _Here:
-    """No device switch: the tensors' device is the current one."""
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE_CTX = _Here()
-
-
-def _on(device):
-    """Context in which ``device`` is the current one (launches and one-time setup go by the current device)."""
-    return _HERE_CTX if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def kv_dtype_code(t: torch.Tensor) -> int:
@@ -574,42 +576,10 @@ def rotary_table(inv_freq: torch.Tensor, n_positions: int, *, factor: float = 1.
     else:
         out = torch.empty((n_positions, inv_freq.shape[0], 2), dtype=torch.float32, device=dev)
     f = inv_freq.to(out.device).contiguous()
-    with _on(out.device):
+    with torch.cuda.device(out.device):
         _check(lib().rotary_table(_ptr(f), f.shape[0], n_positions, float(factor), _ptr(out), _stream(out.device)),
                "rotary_table")
     return out
-
-
-_ROTARY_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-
-
-def _heads(x, name, dtype, dev, n, head_dim=None):
-    """Checks rows [n, heads, head_dim] whose heads are contiguous; returns (token stride, head stride)."""
-    if x.device != dev or x.dtype != dtype or x.dim() != 3 or x.shape[0] != n:
-        raise ValueError(f"{name} must be {dtype} [{n}, heads, head_dim] on {dev}")
-    if head_dim is not None and x.shape[2] != head_dim:
-        raise ValueError(f"{name} must have head_dim {head_dim}")
-    st = x.stride()
-    if st[2] != 1 and x.shape[2] > 1:
-        raise ValueError(f"{name}: the dims of a head must be contiguous")
-    return st[0], st[1]
-
-
-def _positions(positions, dev, n):
-    if positions.device != dev or positions.dim() != 1 or positions.shape[0] != n or not positions.is_contiguous():
-        raise ValueError(f"positions must be contiguous [{n}] on {dev}")
-    if positions.dtype == torch.int32:
-        return 0
-    if positions.dtype == torch.int64:
-        return 1
-    raise ValueError("positions must be int32 or int64")
-
-
-def _table(table, dev):
-    if table.device != dev or table.dtype != torch.float32 or table.dim() != 3 or table.shape[2] != 2 \
-            or not table.is_contiguous():
-        raise ValueError(f"table must be contiguous float32 [n_positions, rot / 2, 2] on {dev}")
-    return table.shape[0], 2 * table.shape[1]
 
 
 def rotary_apply(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: torch.Tensor, *,
@@ -623,79 +593,10 @@ def rotary_apply(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     interleaved; the others are copied.  inverse=True turns back (the transpose: the gradient of the
     rotation).  A token with a negative position is padding: its output rows are left as they are.
     q_out / k_out may be q / k (in place); new contiguous tensors when not given.  Returns (q_out, k_out)."""
-    dev, dtype = q.device, q.dtype
-    if not q.is_cuda or dtype not in _ROTARY_TYPES:
-        raise ValueError("q must be a CUDA tensor of bfloat16, float16 or float32")
-    n = q.shape[0] if q.dim() else 0
-    qs = _heads(q, "q", dtype, dev, n)
-    hd = q.shape[2]
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dtype, device=dev)
-    qo = _heads(q_out, "q_out", dtype, dev, n, hd)
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
-    ks = ko = (0, 0)
-    h_k = 0
-    if k is not None:
-        ks = _heads(k, "k", dtype, dev, n, hd)
-        h_k = k.shape[1]
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=dtype, device=dev)
-        ko = _heads(k_out, "k_out", dtype, dev, n, hd)
-        if k_out.shape != k.shape:
-            raise ValueError("k_out must have k's shape")
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    wide = _positions(positions, dev, n)
-    n_pos, rot = _table(table, dev)
-    with _on(dev):
-        _check(lib().rotary_apply(q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), qo[0], qo[1], q.shape[1], _ptr(k),
-                                  ks[0], ks[1], _ptr(k_out), ko[0], ko[1], h_k, _ROTARY_TYPES[dtype],
-                                  positions.data_ptr(), wide, table.data_ptr(), n_pos, n, hd, rot, rot_offset,
-                                  1 if interleaved else 0, 1 if inverse else 0, _stream(dev)),
-               "rotary_apply")
-    return q_out, k_out
+    return _native().rotary_apply(q, k, positions, table, interleaved, rot_offset, inverse, q_out, k_out)
 
 
 # ---------------------------------------------- append, read back, 4 bits --
-
-
-_FP4_TYPES = tuple(x for x in (torch.uint8, getattr(torch, "float4_e2m1fn_x2", None)) if x is not None)
-_BYTE_SCALES = (torch.float8_e4m3fn, torch.uint8)
-
-
-def _cache4(cache, name, dev):
-    """A cache as [num_blocks, h_kv, page, bytes a row]; the dense MLA form [num_pages, page, d] is one head."""
-    if cache.device != dev or not cache.is_contiguous() or cache.dim() not in (3, 4):
-        raise ValueError(f"{name} must be contiguous [num_blocks, h_kv, page, ...] on {dev}")
-    return tuple(cache.shape) if cache.dim() == 4 else (cache.shape[0], 1, cache.shape[1], cache.shape[2])
-
-
-def _cache_scales(name, shape, hd, kv_dtype, scale, row_scales, block_scales, dev):
-    """The scales that go with a cache of `shape` rows: which are given, and their shapes."""
-    if kv_dtype == KV_E2M1:
-        if scale is None or block_scales is None or row_scales is not None:
-            raise ValueError(f"{name}: a 4-bit cache takes one scale and its block scales")
-        if block_scales.device != dev or block_scales.dtype not in _BYTE_SCALES or not block_scales.is_contiguous() \
-                or block_scales.numel() != shape[0] * shape[1] * shape[2] * (hd // 16) \
-                or block_scales.shape[-1] != hd // 16:
-            raise ValueError(f"{name}: block scales must be contiguous E4M3 [num_blocks, h_kv, page, head_dim / 16]")
-    elif (scale is None) == (row_scales is None):
-        raise ValueError(f"{name}: give one scale or one per row")
-    if scale is not None and (scale.device != dev or scale.dtype != torch.float32 or scale.numel() != 1):
-        raise ValueError(f"{name}: the scale must be one float32 on {dev}")
-    if row_scales is not None and (row_scales.device != dev or row_scales.dtype != torch.float32
-                                   or not row_scales.is_contiguous()
-                                   or row_scales.numel() != shape[0] * shape[1] * shape[2]
-                                   or row_scales.shape[-1] != shape[2]):
-        raise ValueError(f"{name}: row scales must be contiguous float32 [num_blocks, h_kv, page]")
-
-
-def _kv_code(cache, block_scales) -> int:
-    """Block scales mark a 4-bit cache; without them the cache is E4M3 (or refused by the library)."""
-    if block_scales is not None:
-        return KV_E2M1 if cache.dtype in _FP4_TYPES else KV_OTHER
-    return kv_dtype_code(cache)
 
 
 def paged_kv_append(k: torch.Tensor, v: torch.Tensor | None, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
@@ -714,90 +615,16 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor | None, slot_mapping: torch
     (``rotary_table``) and positions (int32 or int64 [n]; negative = padding, nothing is written) K's
     dims [rot_offset, rot_offset + rot) turn as in ``rotary_apply``, and queries q bf16
     [n, h_q, head_dim] can be rotated along: returns them (q_out, new when not given), or None."""
-    dev = k.device
-    if not k.is_cuda or k.dtype != torch.bfloat16:
-        raise ValueError("k must be a CUDA bf16 tensor")
-    if k.dim() == 2:
-        k = k.unsqueeze(1)
-    if v is not None and v.dim() == 2:
-        v = v.unsqueeze(1)
-    n = k.shape[0]
-    ks = _heads(k, "k", torch.bfloat16, dev, n)
-    h_kv, hd = k.shape[1], k.shape[2]
-    code = _kv_code(k_cache, k_block_scales)
-    shape = _cache4(k_cache, "k_cache", dev)
-    if shape[1] != h_kv or shape[3] != (hd // 2 if code == KV_E2M1 else hd):
-        raise ValueError("k and k_cache shapes disagree")
-    _cache_scales("k", shape, hd, code, k_scale, k_row_scales, k_block_scales, dev)
-    if slot_mapping.device != dev or slot_mapping.dtype != torch.int32 or slot_mapping.dim() != 1 \
-            or slot_mapping.shape[0] != n or not slot_mapping.is_contiguous():
-        raise ValueError(f"slot_mapping must be contiguous int32 [{n}] on {dev}")
-    vs = (0, 0)
-    if (v is None) != (v_cache is None):
-        raise ValueError("v and v_cache go together")
-    if v is not None:
-        vs = _heads(v, "v", torch.bfloat16, dev, n, hd)
-        if v.shape != k.shape or _cache4(v_cache, "v_cache", dev) != shape or _kv_code(v_cache, v_block_scales) != code:
-            raise ValueError("v and v_cache must match k and k_cache")
-        _cache_scales("v", shape, hd, code, v_scale, v_row_scales, v_block_scales, dev)
-    elif v_scale is not None or v_row_scales is not None or v_block_scales is not None:
-        raise ValueError("scales for v without v")
-    wide, n_pos, rot = 0, 0, 0
-    if table is not None:
-        if positions is None:
-            raise ValueError("a table needs positions")
-        wide = _positions(positions, dev, n)
-        n_pos, rot = _table(table, dev)
-    qs, h_q = (0, 0), 0
-    if q is not None:
-        if table is None:
-            raise ValueError("q is rotated by a table: give one")
-        qs = _heads(q, "q", torch.bfloat16, dev, n, hd)
-        h_q = q.shape[1]
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-        if q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or q_out.device != dev \
-                or not q_out.is_contiguous():
-            raise ValueError("q_out must be contiguous bf16 of q's shape")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    with _on(dev):
-        _check(lib().paged_kv_append(k.data_ptr(), ks[0], ks[1], _ptr(v), vs[0], vs[1], slot_mapping.data_ptr(), n,
-                                     h_kv, hd, shape[2], shape[0], code, k_cache.data_ptr(), _ptr(v_cache),
-                                     _ptr(k_scale), _ptr(v_scale), _ptr(k_row_scales), _ptr(v_row_scales),
-                                     _ptr(k_block_scales), _ptr(v_block_scales),
-                                     None if table is None else positions.data_ptr(), wide, _ptr(table), n_pos, rot,
-                                     rot_offset, 1 if interleaved else 0, _ptr(q), qs[0], qs[1], _ptr(q_out), h_q,
-                                     _stream(dev)),
-               "paged_kv_append")
-    return q_out
+    return _native().paged_kv_append(k, v, slot_mapping, k_cache, v_cache, positions, table, interleaved, rot_offset,
+                                     k_scale, v_scale, k_row_scales, v_row_scales, k_block_scales, v_block_scales, q,
+                                     q_out)
 
 
 def paged_cache_read(cache: torch.Tensor, slots: torch.Tensor, *, scale=None, row_scales=None, block_scales=None,
                      out: torch.Tensor | None = None) -> torch.Tensor:
     """Rows of a paged cache as bf16 [n, h_kv, head_dim], dequantised in float32 and rounded once.
     cache and its scales as for ``paged_kv_append``; slots int32 [n] (negative = a row of zeros)."""
-    dev = cache.device
-    if not cache.is_cuda:
-        raise ValueError("cache must be a CUDA tensor")
-    code = _kv_code(cache, block_scales)
-    shape = _cache4(cache, "cache", dev)
-    hd = shape[3] * (2 if code == KV_E2M1 else 1)
-    _cache_scales("cache", shape, hd, code, scale, row_scales, block_scales, dev)
-    if slots.device != dev or slots.dtype != torch.int32 or slots.dim() != 1 or not slots.is_contiguous():
-        raise ValueError(f"slots must be contiguous int32 [n] on {dev}")
-    n = slots.shape[0]
-    if out is None:
-        out = torch.empty((n, shape[1], hd), dtype=torch.bfloat16, device=dev)
-    if tuple(out.shape) != (n, shape[1], hd) or out.dtype != torch.bfloat16 or out.device != dev \
-            or not out.is_contiguous():
-        raise ValueError("out must be contiguous bf16 [n, h_kv, head_dim]")
-    with _on(dev):
-        _check(lib().paged_cache_read(cache.data_ptr(), code, _ptr(scale), _ptr(row_scales), _ptr(block_scales),
-                                      slots.data_ptr(), n, shape[1], hd, shape[2], shape[0], out.data_ptr(),
-                                      _stream(dev)),
-               "paged_cache_read")
-    return out
+    return _native().paged_cache_read(cache, slots, scale, row_scales, block_scales, out)
 
 
 def gqa_fp4_workspace_bytes(bs: int, h_q: int, h_kv: int, head_dim: int, max_seqlen: int, q_len: int = 1,
@@ -816,60 +643,9 @@ def paged_gqa_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     block scales E4M3 [num_blocks, h_kv, page, hd / 16], k_scale / v_scale float32 [1]; block_table int32
     [bs, max_blocks], seqlens int32 [bs]; spec_mask, window and sinks as ``paged_gqa_decode_ext``.
     Returns (out bf16 like q, lse float32 without its last dim)."""
-    dev = q.device
-    if not q.is_cuda or q.dtype != torch.bfloat16 or q.dim() not in (3, 4) or not q.is_contiguous():
-        raise ValueError("q must be a contiguous CUDA bf16 tensor [bs, q_len, h_q, hd] or [bs, h_q, hd]")
-    shape = q.shape
-    bs, h_q, hd = shape[0], shape[-2], shape[-1]
-    q_len = shape[1] if q.dim() == 4 else 1
-    kshape = _cache4(k_cache, "k_cache", dev)
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype \
-            or v_cache.device != dev or not v_cache.is_contiguous():
-        raise ValueError("k_cache and v_cache must match")
-    if k_cache.dtype not in _FP4_TYPES:
-        raise FP8MLAError(2, "paged_gqa_decode_fp4")
-    if kshape[3] * 2 != hd:
-        raise ValueError("head_dim mismatch")
-    num_blocks, h_kv, page = kshape[:3]
-    _cache_scales("k", kshape, hd, KV_E2M1, k_scale, None, k_block_scales, dev)
-    _cache_scales("v", kshape, hd, KV_E2M1, v_scale, None, v_block_scales, dev)
-    if block_table.device != dev or block_table.dtype != torch.int32 or block_table.dim() != 2 \
-            or block_table.shape[0] != bs or not block_table.is_contiguous():
-        raise ValueError(f"block_table must be contiguous int32 [{bs}, max_blocks] on {dev}")
-    if seqlens.device != dev or seqlens.dtype != torch.int32 or tuple(seqlens.shape) != (bs,) \
-            or not seqlens.is_contiguous():
-        raise ValueError(f"seqlens must be contiguous int32 [{bs}] on {dev}")
-    if spec_mask is not None and (spec_mask.device != dev or spec_mask.dtype != torch.uint8
-                                  or tuple(spec_mask.shape) != (bs, q_len, q_len) or not spec_mask.is_contiguous()):
-        raise ValueError("spec_mask must be contiguous uint8 [bs, q_len, q_len]")
-    if sinks is not None and (sinks.device != dev or sinks.dtype != torch.float32 or tuple(sinks.shape) != (h_q,)
-                              or not sinks.is_contiguous()):
-        raise ValueError("sinks must be contiguous float32 [h_q]")
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(hd)
-    max_blocks = block_table.shape[1]
-    with _on(dev):
-        if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        elif out.shape != shape or out.dtype != torch.bfloat16 or out.device != dev or not out.is_contiguous():
-            raise ValueError("out must be contiguous bf16 of q's shape")
-        if lse is None:
-            lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-        elif lse.shape != shape[:-1] or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
-            raise ValueError("lse must be contiguous float32 of q's shape without head_dim")
-        if workspace is None:
-            need = gqa_fp4_workspace_bytes(bs, h_q, h_kv, hd, max_blocks * page, q_len, window, num_splits)
-            if need:
-                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        _check(lib().paged_gqa_decode_fp4(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                          k_block_scales.data_ptr(), v_block_scales.data_ptr(), num_blocks,
-                                          k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), max_blocks,
-                                          seqlens.data_ptr(), float(softmax_scale), q_len, _ptr(spec_mask),
-                                          int(window), _ptr(sinks), int(num_splits), _ptr(workspace),
-                                          0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                          out.data_ptr(), lse.data_ptr(), bs, h_q, h_kv, hd, page, _stream(dev)),
-               "paged_gqa_decode_fp4")
-    return out, lse
+    return _native().paged_gqa_decode_fp4(q, k_cache, v_cache, k_block_scales, v_block_scales, block_table, seqlens,
+                                          k_scale, v_scale, softmax_scale, spec_mask, window, sinks, num_splits, out,
+                                          lse, workspace)
 
 
 def wait_timeout_site(device=None):

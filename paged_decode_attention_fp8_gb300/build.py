@@ -3,7 +3,9 @@
 Each .cu file under csrc/ compiles to an object in parallel; the objects
 link into one shared library next to this file.  The CUDA runtime is linked
 statically, so the library loads on a machine without a GPU driver (it
-reports an error on its first CUDA call there).
+reports an error on its first CUDA call there).  csrc/binding.cpp, the native
+marshalling of the per-step operators, compiles beside them against the
+installed torch and links into _binding.so.
 """
 
 from __future__ import annotations
@@ -14,12 +16,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8mla.so")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,6 +48,31 @@ def _compile(src: str, obj: str, extra) -> None:
         sys.stderr.write(res.stderr)
 
 
+def _run(cmd, what: str) -> None:
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{res.stdout}\n{res.stderr}")
+
+
+def _compile_binding(src: str, obj: str) -> None:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in inc), "-c", src, "-o",
+          obj], "compiling the binding")
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _run(["g++", "-shared", "-o", BINDING + ".tmp", obj, f"-L{HERE}", "-l:libfp8mla.so", f"-L{libs}", "-ltorch_python",
+          "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], "linking the binding")
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def _stale(target: str, deps) -> bool:
     if not os.path.exists(target):
         return True
@@ -63,9 +92,12 @@ def build(verbose: bool = False, extra=(), force: bool = False) -> str:
         objs.append(obj)
         if force or _stale(obj, [src, *headers]):
             jobs.append((src, obj))
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
-            futs = [ex.submit(_compile, s, o, extra) for s, o in jobs]
+    bind_src, bind_obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o")
+    bind_stale = force or _stale(bind_obj, [bind_src, os.path.join(ROOT, "include", "fp8mla.h"), __file__])
+    if jobs or bind_stale:
+        with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
+            futs = [ex.submit(_compile_binding, bind_src, bind_obj)] if bind_stale else []
+            futs += [ex.submit(_compile, s, o, extra) for s, o in jobs]
             for f in futs:
                 f.result()
     if force or jobs or _stale(LIB, objs):
@@ -75,6 +107,8 @@ def build(verbose: bool = False, extra=(), force: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, LIB)
+    if bind_stale or _stale(BINDING, [bind_obj, LIB]):
+        _link_binding(bind_obj)
     if verbose:
         print(LIB)
     return LIB
