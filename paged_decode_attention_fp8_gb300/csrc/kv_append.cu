@@ -20,8 +20,10 @@
 // stays in the lane; interleaved: neighbours), the others neighbours.  A block
 // of 16 values is a lane's two chunks, or in the half layout the same chunk of
 // two neighbouring lanes: one shuffle.  K, V and Q rows are three classes of
-// CTAs of one grid; a warp takes kRows rows per group at a time, their loads
-// issued before the first is worked on.
+// CTAs of one grid, one wave of them, and each warp walks its rows in a
+// pipeline: the chain position -> table row -> rotation is longer than a
+// memory access, so slots and positions come two steps ahead, values and the
+// table's rows (into L1) one.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -36,6 +38,12 @@ namespace {
 __device__ uint32_t g_status_append;
 
 constexpr int kThreads = 256;
+constexpr int kReadCtasPerSm = 3;
+// CTAs of an SM: registers for one piece a lane in flight, or for two and three.
+template <int kP>
+__host__ __device__ constexpr int append_ctas() {
+  return kP == 1 ? 4 : (kP == 2 ? 3 : 2);
+}
 constexpr int kMaxHeadDim = 1024;
 constexpr float kTinyAmax = 5.42101086242752217e-20f;  // 2^-64
 constexpr float kTinyLift = 1.84467440737095516e19f;   // 2^64
@@ -89,12 +97,22 @@ struct Piece {
   float a[8], b[8];
 };
 
-// kL lanes a row, kP pairs of chunks a lane, kRows rows a group at a time.
+// What a step needs to know of its rows, and their values.
+struct Where {
+  int32_t slot, pos;  // pos: -1 padding, -2 past the table
+};
+template <int kP>
+struct Values {
+  uint4 a[kP], b[kP];
+};
+
+// kL lanes a row, kP pairs of chunks a lane.  A warp's steps are a pipeline: slots and positions two steps ahead,
+// values one ahead, and the table's rows asked into L1 one ahead (where every lane has one piece: a prompt's K and V
+// 23.4 us, without 25.4; with two pieces, of which a latent row's lanes turn few, it cost 1.4 us of 17.9).
 template <int kL, int kP, int kKind>
 __device__ __forceinline__ void run_class(const Params& prm, const Source& src, bool rotate, uint32_t cta,
                                           uint32_t ctas) {
-  constexpr int kRows = kP == 1 ? 2 : 1;
-  constexpr int kWarpRows = 32 / kL * kRows;
+  constexpr int kWarpRows = 32 / kL;
   const int lane = threadIdx.x % 32, sub = lane % kL, grp = lane / kL;
   const int pairs = prm.head_dim / 16;
   const int rot_pairs = rotate ? prm.rot / 16 : 0;
@@ -125,167 +143,199 @@ __device__ __forceinline__ void run_class(const Params& prm, const Source& src, 
     }
   }
   float tensor_inv = 1.f, scale = 1.f, inv6 = 1.f;
-  if constexpr (kKind == kTensor) tensor_inv = __fdiv_rn(1.f, __ldg(src.scale));
+  if constexpr (kKind == kTensor) tensor_inv = __frcp_rn(__ldg(src.scale));
   if constexpr (kKind == kFp4) {
     scale = __ldg(src.scale);
-    inv6 = __fdiv_rn(1.f, __fmul_rn(scale, 6.f));
+    inv6 = __frcp_rn(__fmul_rn(scale, 6.f));
   }
+  // the 8 pairs of a turning piece in the row of a position
+  auto table_at = [&](int32_t pos, int j) {
+    const int pair0 = half ? 8 * (sub + j * kL) : 4 * (c0[j] - off_chunk);
+    return reinterpret_cast<const float4*>(prm.table + static_cast<int64_t>(pos) * (prm.rot / 2) + pair0);
+  };
 
-  const uint32_t warp_id = cta * (kThreads / 32) + threadIdx.x / 32;
-  const uint32_t stride = ctas * (kThreads / 32) * kWarpRows;
-  for (uint32_t base = warp_id * kWarpRows; base < src.rows; base += stride) {
-    uint4 va[kRows][kP], vb[kRows][kP];
-    int32_t slot[kRows];
-    int64_t pos[kRows];
+  auto look = [&](uint32_t base, Where& w) {
+    const uint32_t row = base + grp;
+    w.slot = -1;
+    w.pos = -1;
+    if (row < src.rows) {
+      const uint32_t token = fast_div(row, src.heads);
+      w.slot = kKind == kQuery ? 0 : __ldg(prm.slots + token);
+      w.pos = 0;
+      if (prm.table != nullptr) {
+        const int64_t p = prm.positions_64 ? __ldg(static_cast<const long long*>(prm.positions) + token)
+                                           : __ldg(static_cast<const int32_t*>(prm.positions) + token);
+        w.pos = p < 0 ? -1 : (p < prm.n_positions ? static_cast<int32_t>(p) : -2);
+      }
+    }
+  };
+  auto load = [&](uint32_t base, Values<kP>& v) {
+    const uint32_t row = base + grp;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const uint32_t row = base + r * (32 / kL) + grp;
-      slot[r] = -1;
-      pos[r] = 0;
+    for (int j = 0; j < kP; ++j) v.a[j] = v.b[j] = make_uint4(0, 0, 0, 0);
+    if (row < src.rows) {
+      const uint32_t token = fast_div(row, src.heads), head = row - token * src.heads.d;
+      const uint4* x = reinterpret_cast<const uint4*>(src.x + token * src.token + head * src.head);
 #pragma unroll
-      for (int j = 0; j < kP; ++j) va[r][j] = vb[r][j] = make_uint4(0, 0, 0, 0);
-      if (row < src.rows) {
-        const uint32_t token = fast_div(row, src.heads), head = row - token * src.heads.d;
-        slot[r] = kKind == kQuery ? 0 : __ldg(prm.slots + token);
-        if (prm.table != nullptr)
-          pos[r] = prm.positions_64 ? __ldg(static_cast<const long long*>(prm.positions) + token)
-                                    : __ldg(static_cast<const int32_t*>(prm.positions) + token);
-        const uint4* x = reinterpret_cast<const uint4*>(src.x + token * src.token + head * src.head);
+      for (int j = 0; j < kP; ++j)
+        if (live[j]) {
+          v.a[j] = __ldcs(x + c0[j]);
+          v.b[j] = __ldcs(x + c1[j]);
+        }
+    }
+  };
+  auto ask = [&](const Where& w) {  // the table's row into L1
+    if (kP == 1 && rotate && w.pos >= 0 && live[0] && turn[0])
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(table_at(w.pos, 0)));
+  };
+  auto process = [&](uint32_t base, const Where& w, const Values<kP>& v) {
+    const uint32_t row = base + grp;
+    bool ok = row < src.rows && w.slot >= 0 && w.pos >= 0;
+    if (w.pos == -2 && w.slot >= 0 && sub == 0) atomicOr(&g_status_append, FP8MLA_DEV_BAD_POSITION);
+    if (ok && kKind != kQuery && static_cast<uint32_t>(w.slot) >= prm.num_slots) {
+      if (sub == 0) atomicOr(&g_status_append, FP8MLA_DEV_BAD_SLOT);
+      ok = false;
+    }
+    Piece p[kP];
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      unpack8(v.a[j], p[j].a);
+      unpack8(v.b[j], p[j].b);
+      if (ok && live[j] && turn[j]) {
+        const float4* at = table_at(w.pos, j);
+        float4 cs[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cs[i] = __ldg(at + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // two pairs at a time: (cos, sin, cos, sin)
+          auto turned = [](float& x, float& y, float c, float s) {
+            const float rx = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+            y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+            x = rx;
+          };
+          if (half) {
+            turned(p[j].a[2 * i], p[j].b[2 * i], cs[i].x, cs[i].y);
+            turned(p[j].a[2 * i + 1], p[j].b[2 * i + 1], cs[i].z, cs[i].w);
+          } else {
+            float(&x)[8] = i < 2 ? p[j].a : p[j].b;
+            turned(x[4 * (i % 2)], x[4 * (i % 2) + 1], cs[i].x, cs[i].y);
+            turned(x[4 * (i % 2) + 2], x[4 * (i % 2) + 3], cs[i].z, cs[i].w);
+          }
+        }
+      }
+    }
+    if constexpr (kKind == kQuery) {
+      if (ok) {
+        uint4* dst = reinterpret_cast<uint4*>(src.out) + static_cast<int64_t>(row) * (prm.head_dim / 8);
 #pragma unroll
         for (int j = 0; j < kP; ++j)
           if (live[j]) {
-            va[r][j] = __ldcs(x + c0[j]);
-            vb[r][j] = __ldcs(x + c1[j]);
+            const auto& a = p[j].a;
+            const auto& b = p[j].b;
+            dst[c0[j]] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                                    pack_bf16x2(a[6], a[7]));
+            dst[c1[j]] = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]), pack_bf16x2(b[4], b[5]),
+                                    pack_bf16x2(b[6], b[7]));
           }
       }
+      return;
     }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const uint32_t row = base + r * (32 / kL) + grp;
-      bool ok = row < src.rows && slot[r] >= 0 && pos[r] >= 0;
-      if (ok && pos[r] >= prm.n_positions && prm.table != nullptr) {
-        if (sub == 0) atomicOr(&g_status_append, FP8MLA_DEV_BAD_POSITION);
-        ok = false;
-      }
-      if (ok && kKind != kQuery && static_cast<uint32_t>(slot[r]) >= prm.num_slots) {
-        if (sub == 0) atomicOr(&g_status_append, FP8MLA_DEV_BAD_SLOT);
-        ok = false;
-      }
-      Piece p[kP];
+    // the row in the cache: (block * h_kv + head) * page + offset
+    const uint32_t head = row - fast_div(row, src.heads) * src.heads.d;
+    const uint32_t block = fast_div(static_cast<uint32_t>(w.slot) & 0x7FFFFFFFu, prm.page);
+    const int64_t dst_row = (static_cast<int64_t>(block) * src.heads.d + head) * prm.page.d +
+                            (static_cast<uint32_t>(w.slot) - block * prm.page.d);
+    if constexpr (kKind == kFp4) {
 #pragma unroll
       for (int j = 0; j < kP; ++j) {
-        unpack8(va[r][j], p[j].a);
-        unpack8(vb[r][j], p[j].b);
-        if (ok && live[j] && turn[j]) {
-          const int pair0 = half ? 8 * (sub + j * kL) : 4 * (c0[j] - off_chunk);  // first of the piece's 8 pairs
-          const float4* cs = reinterpret_cast<const float4*>(prm.table + pos[r] * (prm.rot / 2) + pair0);
+        // Block of a chunk: a lane's two chunks, or (half layout) one chunk of this lane and of its neighbour, so
+        // that two lanes share two blocks.  Each lane works out one scale; neighbours then swap.
+        const float ma = amax8(p[j].a), mb = amax8(p[j].b);
+        const bool shared = half && turn[j];
+        const bool odd = shared && (sub & 1);
+        const float theirs = __shfl_xor_sync(0xffffffffu, odd ? ma : mb, 1);
+        const float amax = fmaxf(odd ? mb : ma, shared ? theirs : mb);
+        const uint32_t s8 = pack_e4m3x2(__fmul_rn(amax, inv6), 0.f) & 0xFFu;
+        const float inv = __frcp_rn(__fmul_rn(f16_lo(e4m3x2_to_f16x2(s8)), scale));
+        const uint32_t s8x = __shfl_xor_sync(0xffffffffu, s8, 1);
+        const float invx = __shfl_xor_sync(0xffffffffu, inv, 1);
+        if (ok && live[j]) {
+          const uint32_t s8a = odd ? s8x : s8, s8b = shared && !odd ? s8x : s8;
+          const float ia = odd ? invx : inv, ib = shared && !odd ? invx : inv;
+          float ya[8], yb[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // two pairs at a time: (cos, sin, cos, sin)
-            const float4 w = __ldg(cs + i);
-            auto turned = [](float& x, float& y, float c, float s) {
-              const float rx = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
-              y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
-              x = rx;
-            };
-            if (half) {
-              turned(p[j].a[2 * i], p[j].b[2 * i], w.x, w.y);
-              turned(p[j].a[2 * i + 1], p[j].b[2 * i + 1], w.z, w.w);
-            } else {
-              float(&x)[8] = i < 2 ? p[j].a : p[j].b;
-              turned(x[4 * (i % 2)], x[4 * (i % 2) + 1], w.x, w.y);
-              turned(x[4 * (i % 2) + 2], x[4 * (i % 2) + 3], w.z, w.w);
-            }
+          for (int i = 0; i < 8; ++i) {
+            ya[i] = __fmul_rn(p[j].a[i], ia);
+            yb[i] = __fmul_rn(p[j].b[i], ib);
           }
+          uint32_t* dst = reinterpret_cast<uint32_t*>(src.out + dst_row * (prm.head_dim / 2));
+          dst[c0[j]] = s8a != 0 ? pack_e2m1x8(ya) : 0u;
+          dst[c1[j]] = s8b != 0 ? pack_e2m1x8(yb) : 0u;
+          uint8_t* sc = src.block_scales + dst_row * (prm.head_dim / 16);
+          if ((c0[j] & 1) == 0) sc[c0[j] / 2] = static_cast<uint8_t>(s8a);
+          if ((c1[j] & 1) == 0) sc[c1[j] / 2] = static_cast<uint8_t>(s8b);
         }
       }
-      if constexpr (kKind == kQuery) {
-        if (ok) {
-          uint4* dst = reinterpret_cast<uint4*>(src.out) + static_cast<int64_t>(row) * (prm.head_dim / 8);
+    } else {
+      float inv = tensor_inv;
+      if constexpr (kKind == kRowScales) {
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < kP; ++j) m = fmax3(m, amax8(p[j].a), amax8(p[j].b));
+#pragma unroll
+        for (int o = kL / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const bool lifted = m < kTinyAmax;
+        if (lifted) {
 #pragma unroll
           for (int j = 0; j < kP; ++j)
-            if (live[j]) {
-              const auto& a = p[j].a;
-              const auto& b = p[j].b;
-              dst[c0[j]] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
-                                      pack_bf16x2(a[6], a[7]));
-              dst[c1[j]] = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]), pack_bf16x2(b[4], b[5]),
-                                      pack_bf16x2(b[6], b[7]));
-            }
-        }
-        continue;
-      }
-      // the row in the cache: (block * h_kv + head) * page + offset
-      const uint32_t head = row - fast_div(row, src.heads) * src.heads.d;
-      const uint32_t block = fast_div(static_cast<uint32_t>(slot[r]) & 0x7FFFFFFFu, prm.page);
-      const int64_t dst_row = (static_cast<int64_t>(block) * src.heads.d + head) * prm.page.d +
-                              (static_cast<uint32_t>(slot[r]) - block * prm.page.d);
-      if constexpr (kKind == kFp4) {
-#pragma unroll
-        for (int j = 0; j < kP; ++j) {
-          float ma = amax8(p[j].a), mb = amax8(p[j].b);
-          const float xa = __shfl_xor_sync(0xffffffffu, ma, 1), xb = __shfl_xor_sync(0xffffffffu, mb, 1);
-          if (half && turn[j]) {
-            ma = fmaxf(ma, xa);
-            mb = fmaxf(mb, xb);
-          } else {
-            ma = mb = fmaxf(ma, mb);
-          }
-          if (ok && live[j]) {
-            const uint32_t s8a = pack_e4m3x2(__fmul_rn(ma, inv6), 0.f) & 0xFFu;
-            const uint32_t s8b = pack_e4m3x2(__fmul_rn(mb, inv6), 0.f) & 0xFFu;
-            const float sa = f16_lo(e4m3x2_to_f16x2(s8a)), sb = f16_lo(e4m3x2_to_f16x2(s8b));
-            const float ia = __fdiv_rn(1.f, __fmul_rn(sa, scale)), ib = __fdiv_rn(1.f, __fmul_rn(sb, scale));
-            float ya[8], yb[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              ya[i] = __fmul_rn(p[j].a[i], ia);
-              yb[i] = __fmul_rn(p[j].b[i], ib);
-            }
-            uint32_t* dst = reinterpret_cast<uint32_t*>(src.out + dst_row * (prm.head_dim / 2));
-            dst[c0[j]] = s8a != 0 ? pack_e2m1x8(ya) : 0u;
-            dst[c1[j]] = s8b != 0 ? pack_e2m1x8(yb) : 0u;
-            uint8_t* sc = src.block_scales + dst_row * (prm.head_dim / 16);
-            if ((c0[j] & 1) == 0) sc[c0[j] / 2] = static_cast<uint8_t>(s8a);
-            if ((c1[j] & 1) == 0) sc[c1[j] / 2] = static_cast<uint8_t>(s8b);
-          }
-        }
-      } else {
-        float inv = tensor_inv;
-        if constexpr (kKind == kRowScales) {
-          float m = 0.f;
-#pragma unroll
-          for (int j = 0; j < kP; ++j) m = fmax3(m, amax8(p[j].a), amax8(p[j].b));
-#pragma unroll
-          for (int o = kL / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const bool lifted = m < kTinyAmax;
-          if (lifted) {
-#pragma unroll
-            for (int j = 0; j < kP; ++j)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                p[j].a[i] = __fmul_rn(p[j].a[i], kTinyLift);
-                p[j].b[i] = __fmul_rn(p[j].b[i], kTinyLift);
-              }
-          }
-          inv = m > 0.f ? __fdiv_rn(448.f, lifted ? __fmul_rn(m, kTinyLift) : m) : 1.f;
-          if (ok && sub == 0) src.row_scales[dst_row] = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
-        }
-        if (ok) {
-          uint2* dst = reinterpret_cast<uint2*>(src.out + dst_row * prm.head_dim);
-#pragma unroll
-          for (int j = 0; j < kP; ++j)
-            if (live[j]) {
-              dst[c0[j]] = encode8(p[j].a, inv);
-              dst[c1[j]] = encode8(p[j].b, inv);
+              p[j].a[i] = __fmul_rn(p[j].a[i], kTinyLift);
+              p[j].b[i] = __fmul_rn(p[j].b[i], kTinyLift);
             }
         }
+        inv = m > 0.f ? __fdiv_rn(448.f, lifted ? __fmul_rn(m, kTinyLift) : m) : 1.f;
+        if (ok && sub == 0) src.row_scales[dst_row] = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+      }
+      if (ok) {
+        uint2* dst = reinterpret_cast<uint2*>(src.out + dst_row * prm.head_dim);
+#pragma unroll
+        for (int j = 0; j < kP; ++j)
+          if (live[j]) {
+            dst[c0[j]] = encode8(p[j].a, inv);
+            dst[c1[j]] = encode8(p[j].b, inv);
+          }
       }
     }
+  };
+
+  uint32_t base = (cta * (kThreads / 32) + threadIdx.x / 32) * kWarpRows;
+  if (base >= src.rows) return;  // the same for the whole warp
+  const uint32_t stride = ctas * (kThreads / 32) * kWarpRows;  // sums stay below 2^32: rows are below 2^31
+  Where w0, w1, w2;
+  Values<kP> v0, v1;
+  look(base, w0);
+  load(base, v0);
+  look(base + stride, w1);
+  for (;;) {
+    const bool more = base + stride < src.rows;
+    if (more) {
+      load(base + stride, v1);
+      look(base + 2 * stride, w2);
+      ask(w1);
+    }
+    process(base, w0, v0);
+    if (!more) break;
+    base += stride;
+    w0 = w1;
+    w1 = w2;
+    v0 = v1;
   }
 }
 
 template <int kL, int kP, int kKind>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ Params prm) {
+__global__ void __launch_bounds__(kThreads, append_ctas<kP>()) kv_append_kernel(const __grid_constant__ Params prm) {
+  griddep_wait();
   const uint32_t c = blockIdx.x;
   if (c < prm.first[1])
     run_class<kL, kP, kKind>(prm, prm.src[0], prm.table != nullptr, c, prm.first[1]);
@@ -297,17 +347,24 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
 
 template <int kL, int kP>
 cudaError_t launch_append(Params& p, int kind, cudaStream_t stream) {
-  constexpr uint32_t kBlockRows = kThreads / 32 * (32 / kL) * (kP == 1 ? 2 : 1);
+  constexpr uint32_t kBlockRows = kThreads / 32 * (32 / kL);
+  // One wave of resident CTAs, shared out by the classes' rows.  A rotated row of K takes longer than one of V (a
+  // prompt: 21.9 us with 13 : 10, 23.2 with 1 : 1, 23.4 with 2 : 1), less so where quantising weighs more.
+  const uint64_t cap = static_cast<uint64_t>(device_sms()) * append_ctas<kP>();
+  const uint64_t weight[3] = {p.table == nullptr ? 10u : (kind == kFp4 ? 11u : 13u), 10, 10};
+  const uint64_t rows = weight[0] * p.src[0].rows + weight[1] * p.src[1].rows + weight[2] * p.src[2].rows;
   p.first[0] = 0;
-  const uint32_t cap = static_cast<uint32_t>(device_sms()) * 8;
-  for (int i = 0; i < 3; ++i)
-    p.first[i + 1] = p.first[i] + std::min((p.src[i].rows + kBlockRows - 1) / kBlockRows, cap);
-  switch (kind) {
-    case kTensor: kv_append_kernel<kL, kP, kTensor><<<p.first[3], kThreads, 0, stream>>>(p); break;
-    case kRowScales: kv_append_kernel<kL, kP, kRowScales><<<p.first[3], kThreads, 0, stream>>>(p); break;
-    default: kv_append_kernel<kL, kP, kFp4><<<p.first[3], kThreads, 0, stream>>>(p); break;
+  for (int i = 0; i < 3; ++i) {
+    const uint64_t need = (p.src[i].rows + kBlockRows - 1) / kBlockRows;
+    const uint64_t share = std::max<uint64_t>(1, cap * weight[i] * p.src[i].rows / rows);
+    p.first[i + 1] = p.first[i] + static_cast<uint32_t>(std::min(need, share));
   }
-  return cudaGetLastError();
+  const dim3 grid(p.first[3]), block(kThreads);
+  switch (kind) {
+    case kTensor: return launch_dependent(kv_append_kernel<kL, kP, kTensor>, grid, block, 0, stream, p);
+    case kRowScales: return launch_dependent(kv_append_kernel<kL, kP, kRowScales>, grid, block, 0, stream, p);
+    default: return launch_dependent(kv_append_kernel<kL, kP, kFp4>, grid, block, 0, stream, p);
+  }
 }
 
 // ------------------------------------------------------------------ read ----
@@ -325,101 +382,142 @@ struct ReadParams {
 };
 
 // Rows of a paged cache as bf16: value = fp32(E4M3 * scale), or fp32(E2M1 * fp32(s8 * scale)), rounded once.
-// A group of kL lanes per row, 16 values (two 16-byte stores) a lane at a time; 8 in a last odd chunk.
-template <int kL, int kKind>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadParams prm) {
+// A group of kL lanes per row, kW values (16; 8 where head_dim is no multiple of 16) a lane at a time.  The same
+// pipeline as the append: slots two steps ahead, codes and scales one ahead.
+template <int kL, int kKind, int kW>
+__global__ void __launch_bounds__(kThreads, kReadCtasPerSm) cache_read_kernel(const __grid_constant__ ReadParams prm) {
   constexpr int kRows = 2;
+  constexpr int kBytes = kKind == kFp4 ? kW / 2 : kW;  // of codes a lane takes
+  griddep_wait();
   const int lane = threadIdx.x % 32, sub = lane % kL, grp = lane / kL;
-  const int chunks = prm.head_dim / 8;
+  const int pieces = prm.head_dim / kW;
+  const int per_lane = (pieces + kL - 1) / kL;  // 1 up to head_dim 512
   float scale = 1.f;
   if constexpr (kKind != kRowScales) scale = __ldg(prm.scale);
-  const uint32_t stride = gridDim.x * (kThreads / 32) * (32 / kL) * kRows;
-  for (uint32_t base = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * (32 / kL) * kRows; base < prm.rows;
-       base += stride) {
-    int64_t src[kRows];
-    float rs[kRows];
+
+  struct Row {
+    int64_t src[kRows];  // row in the cache, or -1
+    uint4 w[kRows];      // first piece's codes
+    float s[kRows];      // and their scale
+  };
+  auto slots_of = [&](uint32_t base, int32_t (&slot)[kRows]) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const uint32_t row = base + r * (32 / kL) + grp;
-      src[r] = -1;
-      rs[r] = scale;
-      if (row < prm.rows) {
-        const uint32_t i = fast_div(row, prm.heads), head = row - i * prm.heads.d;
-        const int32_t slot = __ldg(prm.slots + i);
-        if (slot >= 0 && static_cast<uint32_t>(slot) >= prm.num_slots) {
-          if (sub == 0) atomicOr(&g_status_append, FP8MLA_DEV_BAD_SLOT);
-        } else if (slot >= 0) {
-          const uint32_t block = fast_div(static_cast<uint32_t>(slot), prm.page);
-          src[r] = (static_cast<int64_t>(block) * prm.heads.d + head) * prm.page.d + (slot - block * prm.page.d);
-          if constexpr (kKind == kRowScales) rs[r] = __ldg(prm.row_scales + src[r]);
-        }
+      slot[r] = row < prm.rows ? __ldg(prm.slots + fast_div(row, prm.heads)) : -1;
+    }
+  };
+  auto fetch = [&](int64_t src, int piece, uint4& w, float& s) {
+    const uint8_t* at = prm.cache + src * (kKind == kFp4 ? prm.head_dim / 2 : prm.head_dim) + piece * kBytes;
+    w = make_uint4(0, 0, 0, 0);
+    if constexpr (kBytes == 16) {
+      w = __ldcs(reinterpret_cast<const uint4*>(at));
+    } else {
+      const uint2 x = __ldcs(reinterpret_cast<const uint2*>(at));
+      w.x = x.x, w.y = x.y;
+    }
+    if constexpr (kKind == kFp4) {
+      const uint32_t s8 = __ldg(prm.block_scales + src * (prm.head_dim / 16) + piece);
+      s = __fmul_rn(f16_lo(e4m3x2_to_f16x2(s8)), scale);
+    } else if constexpr (kKind == kRowScales) {
+      s = __ldg(prm.row_scales + src);
+    } else {
+      s = scale;
+    }
+  };
+  auto load = [&](uint32_t base, const int32_t (&slot)[kRows], Row& x) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const uint32_t row = base + r * (32 / kL) + grp;
+      const uint32_t head = row - fast_div(row, prm.heads) * prm.heads.d;
+      x.src[r] = -1;
+      x.s[r] = 0.f;
+      x.w[r] = make_uint4(0, 0, 0, 0);
+      if (slot[r] >= 0 && static_cast<uint32_t>(slot[r]) >= prm.num_slots) {
+        if (sub == 0) atomicOr(&g_status_append, FP8MLA_DEV_BAD_SLOT);
+      } else if (slot[r] >= 0) {
+        const uint32_t block = fast_div(static_cast<uint32_t>(slot[r]), prm.page);
+        x.src[r] = (static_cast<int64_t>(block) * prm.heads.d + head) * prm.page.d + (slot[r] - block * prm.page.d);
+        if (sub < pieces) fetch(x.src[r], sub, x.w[r], x.s[r]);
       }
     }
-    for (int c = 2 * sub; c < chunks; c += 2 * kL) {
-      const bool two = c + 1 < chunks;
-      uint4 w[kRows];
-      float s[kRows];
+  };
+  auto store = [&](uint32_t row, int piece, const uint4& w, float s) {
+    uint32_t o[kW / 2];
+    if constexpr (kKind == kFp4) {
+      uint32_t h[4];
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        w[r] = make_uint4(0, 0, 0, 0);
-        s[r] = rs[r];
-        if (src[r] < 0) continue;
-        if constexpr (kKind == kFp4) {
-          const uint2 x = __ldcs(reinterpret_cast<const uint2*>(prm.cache + src[r] * (prm.head_dim / 2) + c * 4));
-          w[r].x = x.x, w[r].y = x.y;
-          const uint32_t s8 = __ldg(prm.block_scales + src[r] * (prm.head_dim / 16) + c / 2);
-          s[r] = __fmul_rn(f16_lo(e4m3x2_to_f16x2(s8)), scale);
-        } else {
-          const uint2* x = reinterpret_cast<const uint2*>(prm.cache + src[r] * prm.head_dim + c * 8);
-          const uint2 lo = __ldcs(x);
-          w[r].x = lo.x, w[r].y = lo.y;
-          if (two) {
-            const uint2 hi = __ldcs(x + 1);
-            w[r].z = hi.x, w[r].w = hi.y;
-          }
-        }
+      for (int k = 0; k < kW / 8; ++k) {
+        e2m1x8_to_f16x2(k ? w.y : w.x, h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[4 * k + i] = h[i];
       }
+    } else {
+      const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const uint32_t row = base + r * (32 / kL) + grp;
-        if (row >= prm.rows) continue;
-        uint32_t h[8];  // f16x2
-        if constexpr (kKind == kFp4) {
-          uint32_t a[4], b[4];
-          e2m1x8_to_f16x2(w[r].x, a);
-          e2m1x8_to_f16x2(w[r].y, b);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) h[i] = a[i], h[4 + i] = b[i];
-        } else {
-          const uint32_t q[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            h[2 * i] = e4m3x2_to_f16x2(q[i]);
-            h[2 * i + 1] = e4m3x2_to_f16x2(q[i] >> 16);
-          }
-        }
-        uint32_t o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          o[i] = src[r] < 0 ? 0u : pack_bf16x2(__fmul_rn(f16_lo(h[i]), s[r]), __fmul_rn(f16_hi(h[i]), s[r]));
-        uint4* dst = prm.out + static_cast<int64_t>(row) * chunks + c;
-        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        if (two) dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      for (int i = 0; i < kW / 4; ++i) {
+        o[2 * i] = e4m3x2_to_f16x2(q[i]);
+        o[2 * i + 1] = e4m3x2_to_f16x2(q[i] >> 16);
       }
     }
+#pragma unroll
+    for (int i = 0; i < kW / 2; ++i) o[i] = pack_bf16x2(__fmul_rn(f16_lo(o[i]), s), __fmul_rn(f16_hi(o[i]), s));
+    uint4* dst = prm.out + (static_cast<int64_t>(row) * prm.head_dim + piece * kW) / 8;
+#pragma unroll
+    for (int i = 0; i < kW / 8; ++i) __stcs(dst + i, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+  };
+  auto process = [&](uint32_t base, const Row& x) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const uint32_t row = base + r * (32 / kL) + grp;
+      if (row >= prm.rows) continue;
+      const bool none = x.src[r] < 0;  // a row of zeros
+      if (sub < pieces) store(row, sub, none ? make_uint4(0, 0, 0, 0) : x.w[r], none ? 0.f : x.s[r]);
+      for (int j = 1; j < per_lane; ++j) {
+        const int piece = sub + j * kL;
+        if (piece >= pieces) break;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        float s = 0.f;
+        if (!none) fetch(x.src[r], piece, w, s);
+        store(row, piece, w, s);
+      }
+    }
+  };
+
+  constexpr uint32_t kWarpRows = 32 / kL * kRows;
+  uint32_t base = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kWarpRows;
+  if (base >= prm.rows) return;  // the same for the whole warp
+  const uint32_t stride = gridDim.x * (kThreads / 32) * kWarpRows;
+  int32_t s1[kRows], s2[kRows];
+  Row x0, x1;
+  slots_of(base, s1);
+  load(base, s1, x0);
+  slots_of(base + stride, s1);
+  for (;;) {
+    const bool more = base + stride < prm.rows;
+    if (more) {
+      load(base + stride, s1, x1);
+      slots_of(base + 2 * stride, s2);
+    }
+    process(base, x0);
+    if (!more) break;
+    base += stride;
+    x0 = x1;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) s1[r] = s2[r];
   }
 }
 
-template <int kL>
+template <int kL, int kW>
 cudaError_t launch_read(const ReadParams& p, int kind, cudaStream_t stream) {
   constexpr uint32_t kBlockRows = kThreads / 32 * (32 / kL) * 2;
-  const unsigned blocks = std::min<unsigned>((p.rows + kBlockRows - 1) / kBlockRows, device_sms() * 8);
+  const unsigned blocks = std::min<unsigned>((p.rows + kBlockRows - 1) / kBlockRows, device_sms() * kReadCtasPerSm);
+  const dim3 grid(blocks), block(kThreads);
   switch (kind) {
-    case kTensor: cache_read_kernel<kL, kTensor><<<blocks, kThreads, 0, stream>>>(p); break;
-    case kRowScales: cache_read_kernel<kL, kRowScales><<<blocks, kThreads, 0, stream>>>(p); break;
-    default: cache_read_kernel<kL, kFp4><<<blocks, kThreads, 0, stream>>>(p); break;
+    case kTensor: return launch_dependent(cache_read_kernel<kL, kTensor, kW>, grid, block, 0, stream, p);
+    case kRowScales: return launch_dependent(cache_read_kernel<kL, kRowScales, kW>, grid, block, 0, stream, p);
+    default: return launch_dependent(cache_read_kernel<kL, kFp4, 16>, grid, block, 0, stream, p);
   }
-  return cudaGetLastError();
 }
 
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
@@ -449,7 +547,7 @@ fp8mla_status_t kv_append_entry(const KvAppendArgs& a, cudaStream_t stream) {
     return FP8MLA_ERR_INVALID_ARG;
   if (a.table != nullptr) {
     if (a.rot < 16 || a.rot % 16 != 0 || a.rot_offset < 0 || a.rot_offset % (a.interleaved ? 16 : 8) != 0 ||
-        a.rot > a.head_dim - a.rot_offset || a.n_positions < 1 || misaligned(a.table, 16))
+        a.rot > a.head_dim - a.rot_offset || a.n_positions < 1 || a.n_positions > 0x7FFFFFFF || misaligned(a.table, 16))
       return FP8MLA_ERR_INVALID_ARG;
     // blocks of 16 values do not straddle a half layout's pieces
     if (kind == kFp4 && !a.interleaved && (a.rot % 32 != 0 || a.rot_offset % 16 != 0)) return FP8MLA_ERR_INVALID_ARG;
@@ -496,12 +594,15 @@ fp8mla_status_t kv_append_entry(const KvAppendArgs& a, cudaStream_t stream) {
   p.head_dim = a.head_dim;
   const int pairs = a.head_dim / 16;
   cudaError_t e;
+  // the fewest lanes with one piece each; three where that leaves fewer of them idle (head_dim 192, 576)
   if (pairs <= 1) e = launch_append<1, 1>(p, kind, stream);
   else if (pairs <= 2) e = launch_append<2, 1>(p, kind, stream);
   else if (pairs <= 4) e = launch_append<4, 1>(p, kind, stream);
   else if (pairs <= 8) e = launch_append<8, 1>(p, kind, stream);
+  else if (pairs <= 12) e = launch_append<4, 3>(p, kind, stream);
   else if (pairs <= 16) e = launch_append<16, 1>(p, kind, stream);
   else if (pairs <= 32) e = launch_append<32, 1>(p, kind, stream);
+  else if (pairs <= 48) e = launch_append<16, 3>(p, kind, stream);
   else e = launch_append<32, 2>(p, kind, stream);
   return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
 }
@@ -532,14 +633,15 @@ fp8mla_status_t cache_read_entry(const CacheReadArgs& a, cudaStream_t stream) {
   p.rows = static_cast<uint32_t>(a.n) * a.h_kv;
   p.num_slots = static_cast<uint32_t>(static_cast<int64_t>(a.num_blocks) * a.page_size);
   p.head_dim = a.head_dim;
-  const int pairs = (a.head_dim + 15) / 16;
+  const int pieces = a.head_dim / 16;
   cudaError_t e;
-  if (pairs <= 1) e = launch_read<1>(p, kind, stream);
-  else if (pairs <= 2) e = launch_read<2>(p, kind, stream);
-  else if (pairs <= 4) e = launch_read<4>(p, kind, stream);
-  else if (pairs <= 8) e = launch_read<8>(p, kind, stream);
-  else if (pairs <= 16) e = launch_read<16>(p, kind, stream);
-  else e = launch_read<32>(p, kind, stream);
+  if (a.head_dim % 16 != 0) e = launch_read<32, 8>(p, kind, stream);  // a rare width: lanes may idle
+  else if (pieces <= 1) e = launch_read<1, 16>(p, kind, stream);
+  else if (pieces <= 2) e = launch_read<2, 16>(p, kind, stream);
+  else if (pieces <= 4) e = launch_read<4, 16>(p, kind, stream);
+  else if (pieces <= 8) e = launch_read<8, 16>(p, kind, stream);
+  else if (pieces <= 16) e = launch_read<16, 16>(p, kind, stream);
+  else e = launch_read<32, 16>(p, kind, stream);
   return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
 }
 

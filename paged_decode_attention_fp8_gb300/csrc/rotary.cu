@@ -35,6 +35,7 @@ __device__ uint32_t g_status_rot;
 
 constexpr int kThreads = 256;
 constexpr int kHeadsInFlight = 4;
+constexpr int kCtasPerSm = 3;
 
 __global__ void __launch_bounds__(256) rotary_table_kernel(const double* __restrict__ inv_freq, int half,
                                                            int64_t total, double factor, float2* __restrict__ table) {
@@ -95,19 +96,13 @@ struct Params {
 // kV: pairs of a piece (8, or 1 where the sizes, strides or addresses do not allow 16-byte accesses); a copied
 // piece is kV values.
 template <typename T, int kV, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Params prm) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) rotary_kernel(const __grid_constant__ Params prm) {
+  griddep_wait();
   const int ul = threadIdx.x % prm.unit_lanes;
   const int hl = threadIdx.x / prm.unit_lanes % prm.head_lanes;
   const int tl = threadIdx.x / (prm.unit_lanes * prm.head_lanes);
   const int64_t token = static_cast<int64_t>(blockIdx.x) * prm.token_lanes + tl;
   if (tl >= prm.token_lanes || token >= prm.n_tokens) return;
-  const int64_t pos = prm.positions_64 ? __ldg(static_cast<const long long*>(prm.positions) + token)
-                                       : __ldg(static_cast<const int32_t*>(prm.positions) + token);
-  if (pos < 0) return;  // padding
-  if (pos >= prm.n_positions) {
-    if (ul == 0 && hl == 0) atomicOr(&g_status_rot, FP8MLA_DEV_BAD_POSITION);
-    return;
-  }
   const int heads = prm.heads[0] + prm.heads[1];
   auto head_in = [&](int h) {
     const int w = h >= prm.heads[0];
@@ -117,26 +112,26 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     const int w = h >= prm.heads[0];
     return static_cast<T*>(prm.out[w]) + token * prm.out_token[w] + (h - (w ? prm.heads[0] : 0)) * prm.out_head[w];
   };
+  int64_t pos = -1;
+  bool known = false;
+  auto skipped = [&]() {  // asked after the first heads' loads have gone out: whether the token has no position
+    if (!known) {
+      pos = prm.positions_64 ? __ldg(static_cast<const long long*>(prm.positions) + token)
+                             : __ldg(static_cast<const int32_t*>(prm.positions) + token);
+      known = true;
+      if (pos >= prm.n_positions) {
+        if (ul == 0 && hl == 0) atomicOr(&g_status_rot, FP8MLA_DEV_BAD_POSITION);
+        pos = -1;
+      }
+    }
+    return pos < 0;  // padding, or past the table
+  };
   for (int u = ul; u < prm.units; u += prm.unit_lanes) {
     if (u < prm.rot_units) {
       // first value of each half of the piece; kV pairs
       const int d0 = prm.rot_offset + (kInterleaved ? 2 * kV * u : kV * u);
       const int d1 = kInterleaved ? d0 + kV : d0 + prm.rot / 2;
       float2 cs[kV];
-      const float2* row = prm.table + pos * (prm.rot / 2) + kV * u;
-      if constexpr (kV == 1) {
-        cs[0] = __ldg(row);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kV / 2; ++i) {
-          const float4 x = __ldg(reinterpret_cast<const float4*>(row) + i);
-          cs[2 * i] = make_float2(x.x, x.y), cs[2 * i + 1] = make_float2(x.z, x.w);
-        }
-      }
-      if (prm.inverse) {
-#pragma unroll
-        for (int i = 0; i < kV; ++i) cs[i].y = -cs[i].y;
-      }
       for (int h0 = hl; h0 < heads; h0 += prm.head_lanes * kHeadsInFlight) {
         Vec<T, kV> a[kHeadsInFlight], b[kHeadsInFlight];
 #pragma unroll
@@ -146,6 +141,23 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
             const T* p = head_in(h);
             a[k].load(p + d0);
             b[k].load(p + d1);
+          }
+        }
+        if (skipped()) return;
+        if (h0 == hl) {
+          const float2* row = prm.table + pos * (prm.rot / 2) + kV * u;
+          if constexpr (kV == 1) {
+            cs[0] = __ldg(row);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kV / 2; ++i) {
+              const float4 x = __ldg(reinterpret_cast<const float4*>(row) + i);
+              cs[2 * i] = make_float2(x.x, x.y), cs[2 * i + 1] = make_float2(x.z, x.w);
+            }
+          }
+          if (prm.inverse) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) cs[i].y = -cs[i].y;
           }
         }
 #pragma unroll
@@ -177,6 +189,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         }
       }
     } else {  // a copied piece, outside the rotated part
+      if (skipped()) return;
       int d = (u - prm.rot_units) * kV;
       if (d >= prm.rot_offset) d += prm.rot;
       for (int h = hl; h < heads; h += prm.head_lanes) {
@@ -221,18 +234,12 @@ cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t stream) {
   p.token_lanes = std::min(kThreads / (p.unit_lanes * p.head_lanes), a.n_tokens);
   const int threads = (p.unit_lanes * p.head_lanes * p.token_lanes + 31) / 32 * 32;
   const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.n_tokens) + p.token_lanes - 1) / p.token_lanes);
-  if (wide) {
-    if (a.interleaved)
-      rotary_kernel<T, 8, true><<<blocks, threads, 0, stream>>>(p);
-    else
-      rotary_kernel<T, 8, false><<<blocks, threads, 0, stream>>>(p);
-  } else {
-    if (a.interleaved)
-      rotary_kernel<T, 1, true><<<blocks, threads, 0, stream>>>(p);
-    else
-      rotary_kernel<T, 1, false><<<blocks, threads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  const dim3 grid(blocks), block(threads);
+  if (wide)
+    return a.interleaved ? launch_dependent(rotary_kernel<T, 8, true>, grid, block, 0, stream, p)
+                         : launch_dependent(rotary_kernel<T, 8, false>, grid, block, 0, stream, p);
+  return a.interleaved ? launch_dependent(rotary_kernel<T, 1, true>, grid, block, 0, stream, p)
+                       : launch_dependent(rotary_kernel<T, 1, false>, grid, block, 0, stream, p);
 }
 
 }  // namespace
