@@ -65,15 +65,22 @@ constexpr int kMaxCols = 128;   // q_len * (h_q / h_kv)
 constexpr int kMaxLine = 1024;  // sequences whose lengths a CTA sums
 constexpr int kMinTiles = 16;   // tiles of a piece, where there are fewer than GPU-filling
 constexpr int kFixed = 32;      // what a sequence costs a CTA beside its tiles, in tiles: fill, drain and merge
+constexpr int kShort = 64;      // tiles up to which a sequence is not cut
+constexpr int kShortFew = 96;   // the same where wide CTAs take it (one sequence, 8 KV heads: 1500 keys 10.4 us, cut
+                                // 10.9; 2048 keys 11.9 and 11.4)
 constexpr float kBelow = 7.f;   // a reference lies this far below the largest score (log2) ...
 constexpr float kTau = 15.f;    // ... and moves when a score is this far above it
 
-// Warps of a CTA, CTAs of an SM, tiles a warp takes at a time, and stages of its ring.
-template <int kHd, int kNT>
+// Warps of a CTA, CTAs of an SM, tiles a warp takes at a time, and stages of its ring.  Throughput: twelve warps of up
+// to 168 registers on an SM (eight at head_dim 256, twice the accumulators), in small CTAs, so that a piece's fill and
+// merge hide behind the other CTAs' loops (the 32-context batch: 8 warps x 2 CTAs 78 us, 4 x 4 70, 4 x 3 with two
+// tiles at a time 63).  kWide: an SM's warps in one CTA, for few sequences of short contexts, where a warp's few tiles
+// in a row are what takes the time.
+template <int kHd, int kNT, bool kWide>
 struct Shape {
-  static constexpr int kWarps = 4;
-  static constexpr int kPerSm = kHd == 256 ? 2 : 3;
-  static constexpr int kU = kHd == 256 || kNT == 2 ? 1 : 2;
+  static constexpr int kWarps = kWide ? (kHd == 256 ? 8 : (kNT == 1 ? 16 : 12)) : 4;
+  static constexpr int kPerSm = kWide ? 1 : (kHd == 256 ? 2 : 3);
+  static constexpr int kU = kWide || kHd == 256 || kNT == 2 ? 1 : 2;
   static constexpr int kStages = kU == 2 ? 3 : 4;
 };
 
@@ -164,18 +171,19 @@ __device__ __forceinline__ int tiles_of(const Params& prm, int s_k) {
   return max(0, (s_k + kTile - 1) / kTile - first_tile(prm, s_k));
 }
 
-template <int kHd, int kNT>
-__global__ void __launch_bounds__(Shape<kHd, kNT>::kWarps * 32, Shape<kHd, kNT>::kPerSm)
+template <int kHd, int kNT, bool kWide>
+__global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd, kNT, kWide>::kPerSm)
     fp4_decode_kernel(const __grid_constant__ Params prm) {
   using L = Lay<kHd>;
-  constexpr int kWarps = Shape<kHd, kNT>::kWarps, kU = Shape<kHd, kNT>::kU, kStages = Shape<kHd, kNT>::kStages;
+  using S = Shape<kHd, kNT, kWide>;
+  constexpr int kWarps = S::kWarps, kU = S::kU, kStages = S::kStages;
   constexpr int kStage = kU * L::kBytes;
   constexpr int kSteps = kHd / 16;     // products of a tile, for K and for V
   constexpr int kKWords = kHd / 32;    // 32-bit words of a lane's part of a K row
   constexpr int kVWords = kHd / 64;    // of a lane's part of a V row
   constexpr int kCopies = L::kChunks / 32;
   extern __shared__ __align__(128) uint8_t smem[];  // a 512-byte copy of a warp covers whole 128-byte lines
-  __shared__ uint32_t s_vis[kMaxQLen];
+  __shared__ uint32_t s_vis[kMaxQLen], s_any;
   __shared__ float s_m[kWarps][kNT * 8], s_l[kWarps][kNT * 8];
   __shared__ uint4 s_q[kNT][kSteps / 2][32];  // Q's fragments of two products a lane
   __shared__ float s_cq[kNT * 8];             // score to log2 units, then a finished row's factor
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT>::kWarps * 32, Shape<kHd, kNT>:
   const int unit = blockIdx.x;
   if (prm.splits == 0) {
     // prefix sums of the sequences' places (of one KV head), a CTA's width of sequences at a time
-    constexpr int kThreads = kWarps * 32, kRuns = kMaxLine / kThreads;
+    constexpr int kThreads = kWarps * 32, kRuns = (kMaxLine + kThreads - 1) / kThreads;
     int len[kRuns];
 #pragma unroll
     for (int i = 0; i < kRuns; ++i) {
@@ -301,7 +309,8 @@ __global__ void __launch_bounds__(Shape<kHd, kNT>::kWarps * 32, Shape<kHd, kNT>:
       cur = end;
     }
     const int start = s_k - prm.q_len;  // position of the block's first token
-    const int k_lo = prm.window > 0 ? max(0, start - prm.window + 1) : 0;
+    const int tok_lo = prm.q_len > 1 ? col0 / prm.group : 0;  // the first token of this CTA's columns
+    const int k_lo = prm.window > 0 ? max(0, start + tok_lo - prm.window + 1) : 0;
     const int mine0 = t0 + warp * kU;  // this warp's tiles: kU from here, kU more kWarps * kU later, ...
     const int n_mine = t1 > mine0 ? (t1 - mine0 + kWarps * kU - 1) / (kWarps * kU) : 0;
     const int32_t* bt_row = prm.block_table + static_cast<size_t>(b) * prm.max_blocks;
@@ -370,7 +379,18 @@ __global__ void __launch_bounds__(Shape<kHd, kNT>::kWarps * 32, Shape<kHd, kNT>:
       }
       s_vis[threadIdx.x] = bits;
     }
-
+    if (warp == 0) {  // which keys of the block any of those tokens sees
+      __syncwarp();
+      uint32_t any = s_vis[tok_lo];
+      if (prm.q_len > 1) {
+        any = 0;
+        for (int i = tok_lo; i <= (col0 + ncols - 1) / prm.group; ++i) {
+          const uint32_t near = prm.window == 0 || i < prm.window ? ~0u : ~0u << (i - prm.window + 1);
+          any |= s_vis[i] & near;
+        }
+      }
+      if (lane == 0) s_any = any;
+    }
     if (warp < kNT) {  // Q's fragments, as f16 with a power of two out
       float amax = 0.f;
 #pragma unroll
@@ -416,7 +436,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT>::kWarps * 32, Shape<kHd, kNT>:
     }
 
     // eight columns' fragments stay in registers, sixteen are read for every tile
-    constexpr bool kQRegs = kNT == 1 && kHd <= 128;
+    constexpr bool kQRegs = kNT == 1 && kHd <= 128 && !kWide;
     uint4 qr[kQRegs ? kNT : 1][kQRegs ? kSteps / 2 : 1];
     if constexpr (kQRegs) {
 #pragma unroll
@@ -579,10 +599,13 @@ __global__ void __launch_bounds__(Shape<kHd, kNT>::kWarps * 32, Shape<kHd, kNT>:
             sc[k] = *reinterpret_cast<const uint16_t*>(sv + L::kVs + r * 16 + 2 * g);
           }
         }
-        if constexpr (kMasked) {  // a key that no column sees has a zero weight; its scale may be anything (NaN), so it is zeroed
+        if constexpr (kMasked) {  // a key that no column sees has a zero weight; its scale may be anything (NaN), so it
+                                  // is zeroed
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (const int p = tok0 + u * kTile + t + 4 * k; p >= keys_end || p < k_lo) sc[k] = 0;
+          for (int k = 0; k < 4; ++k) {
+            const int p = tok0 + u * kTile + t + 4 * k;
+            if (p >= keys_end || p < k_lo || (p >= start && !((s_any >> (p - start)) & 1u))) sc[k] = 0;
+          }
         }
 #pragma unroll
         for (int w = 0; w < kVWords; ++w) {
@@ -700,10 +723,10 @@ __global__ void __launch_bounds__(Shape<kHd, kNT>::kWarps * 32, Shape<kHd, kNT>:
 }
 
 // Merge of the shards of one (sequence, KV head) and column tile.  Lane x of a warp owns one float4 of the fragment
-// order (two dims of two columns) of one step (16 dims).  With kGroups = 1 the four warps take four steps; with 4
-// they take shards w, w + 4, ... of one step and meet in shared memory (few sequences, many shards).
+// order (two dims of two columns) of one step (16 dims).  With kGroups = 1 the four warps take four steps; with 8
+// the warps take shards w, w + 8, ... of one step and meet in shared memory (few sequences, many shards).
 template <int kHd, int kNT, int kGroups>
-__global__ void __launch_bounds__(128) fp4_combine_kernel(const __grid_constant__ Params prm) {
+__global__ void __launch_bounds__(kGroups == 1 ? 128 : kGroups * 32) fp4_combine_kernel(const __grid_constant__ Params prm) {
   constexpr int kSteps = kHd / 16, kFrag = kNT * kSteps * 32;
   __shared__ float4 s_o[kGroups][32], s_ml[kGroups][32];
   griddep_wait();
@@ -812,6 +835,7 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // How a call is laid out: shards of every sequence (1: none, 0: balanced pieces), pieces, and the workspace.
 struct Plan {
   int nt, ct, splits, units;
+  bool wide;
   size_t slots, ml, span, bytes;  // partial states, and where (m, l) and the spans of pieces begin
 };
 
@@ -824,13 +848,16 @@ Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long cap
   const long long seqs = static_cast<long long>(bs) * h_kv;
   const int resident = device_sms() * (head_dim == 256 ? 2 : 3);  // Shape::kPerSm
   p.units = 0;
+  p.wide = false;
+  const bool few = seqs * p.ct <= device_sms();  // a wide CTA has an SM of its own
   if (num_splits > 0) {
     p.splits = static_cast<int>(std::min<long long>(num_splits, std::max(1LL, (tiles + 7) / 8)));
-  } else if (tiles <= 64 || seqs * p.ct >= 8LL * resident || bs > kMaxLine ||
+  } else if (tiles <= (few ? kShortFew : kShort) || seqs * p.ct >= 8LL * resident || bs > kMaxLine ||
              seqs * (tiles + kFixed) > 0x7FFFFFFFll) {
     // Short contexts: one CTA a sequence takes no longer than a piece and its merge.  Many sequences: their CTAs
     // balance by themselves.  (The line's places are counted in 32 bits.)
     p.splits = 1;
+    p.wide = few && tiles > 4;
   } else {
     p.splits = 0;
     p.units = std::max(1, resident / p.ct);
@@ -848,28 +875,34 @@ bool sizes_ok(int bs, int h_q, int h_kv, int head_dim, int q_len, int window, in
          static_cast<long long>(q_len) * (h_q / h_kv) <= kMaxCols && window >= 0 && num_splits >= 0;
 }
 
-template <int kHd, int kNT>
-cudaError_t launch(const Params& prm, int seqs, int ct, cudaStream_t stream) {
-  constexpr int kWarps = Shape<kHd, kNT>::kWarps;
-  constexpr size_t smem = std::max<size_t>(static_cast<size_t>(kWarps) * Shape<kHd, kNT>::kStages *
-                                               Shape<kHd, kNT>::kU * Lay<kHd>::kBytes,
-                                           static_cast<size_t>(kWarps) * kNT * (kHd / 16) * 32 * sizeof(float4));
-  static_assert(Shape<kHd, kNT>::kPerSm * (smem + 12 * 1024) <= 233472, "the CTAs fit in an SM's shared memory");
+template <int kHd, int kNT, bool kWide>
+cudaError_t launch_decode(const Params& prm, int seqs, int ct, cudaStream_t stream) {
+  using S = Shape<kHd, kNT, kWide>;
+  constexpr size_t smem =
+      std::max<size_t>(static_cast<size_t>(S::kWarps) * S::kStages * S::kU * Lay<kHd>::kBytes,
+                       static_cast<size_t>(S::kWarps) * kNT * (kHd / 16) * 32 * sizeof(float4));
+  static_assert(S::kPerSm * (smem + 16 * 1024) <= 233472, "the CTAs fit in an SM's shared memory");
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = configure_once(configured, [&] {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(fp4_decode_kernel<kHd, kNT>),
+  const cudaError_t e = configure_once(configured, [&] {
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(fp4_decode_kernel<kHd, kNT, kWide>),
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   });
   if (e != cudaSuccess) return e;
   const unsigned grid = prm.splits == 0 ? static_cast<unsigned>(prm.units)
                                         : static_cast<unsigned>(seqs) * static_cast<unsigned>(prm.splits);
-  e = launch_dependent(fp4_decode_kernel<kHd, kNT>, dim3(grid, ct), dim3(kWarps * 32), smem, stream, prm);
+  return launch_dependent(fp4_decode_kernel<kHd, kNT, kWide>, dim3(grid, ct), dim3(S::kWarps * 32), smem, stream, prm);
+}
+
+template <int kHd, int kNT>
+cudaError_t launch(const Params& prm, bool wide, int seqs, int ct, cudaStream_t stream) {
+  const cudaError_t e = wide ? launch_decode<kHd, kNT, true>(prm, seqs, ct, stream)
+                             : launch_decode<kHd, kNT, false>(prm, seqs, ct, stream);
   if (e != cudaSuccess || prm.splits == 1) return e;
   constexpr unsigned kFrags = kNT * (kHd / 16);
   if (static_cast<long long>(seqs) * ct >= device_sms())
     return launch_dependent(fp4_combine_kernel<kHd, kNT, 1>, dim3(static_cast<unsigned>(seqs), ct, kFrags / 4),
                             dim3(128), 0, stream, prm);
-  return launch_dependent(fp4_combine_kernel<kHd, kNT, 4>, dim3(static_cast<unsigned>(seqs), ct, kFrags), dim3(128),
+  return launch_dependent(fp4_combine_kernel<kHd, kNT, 8>, dim3(static_cast<unsigned>(seqs), ct, kFrags), dim3(256),
                           0, stream, prm);
 }
 
@@ -942,12 +975,12 @@ fp8mla_status_t fp4_decode_entry(const Fp4DecodeArgs& a, cudaStream_t stream) {
   const int n = static_cast<int>(seqs);
   cudaError_t e;
   switch (a.head_dim + plan.nt) {
-    case 64 + 1: e = fp4::launch<64, 1>(p, n, plan.ct, stream); break;
-    case 64 + 2: e = fp4::launch<64, 2>(p, n, plan.ct, stream); break;
-    case 128 + 1: e = fp4::launch<128, 1>(p, n, plan.ct, stream); break;
-    case 128 + 2: e = fp4::launch<128, 2>(p, n, plan.ct, stream); break;
-    case 256 + 1: e = fp4::launch<256, 1>(p, n, plan.ct, stream); break;
-    default: e = fp4::launch<256, 2>(p, n, plan.ct, stream); break;
+    case 64 + 1: e = fp4::launch<64, 1>(p, plan.wide, n, plan.ct, stream); break;
+    case 64 + 2: e = fp4::launch<64, 2>(p, plan.wide, n, plan.ct, stream); break;
+    case 128 + 1: e = fp4::launch<128, 1>(p, plan.wide, n, plan.ct, stream); break;
+    case 128 + 2: e = fp4::launch<128, 2>(p, plan.wide, n, plan.ct, stream); break;
+    case 256 + 1: e = fp4::launch<256, 1>(p, plan.wide, n, plan.ct, stream); break;
+    default: e = fp4::launch<256, 2>(p, plan.wide, n, plan.ct, stream); break;
   }
   return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
 }

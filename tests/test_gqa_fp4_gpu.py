@@ -174,6 +174,91 @@ def test_rows_that_see_nothing():
         assert torch.allclose(lse[0, 1].cpu(), want)
 
 
+def test_hidden_keys_may_hold_anything():
+    """NaN scales on keys that no token sees -- hidden by the mask, or left behind by the window -- change nothing;
+    with 60 columns each column tile has its own set of tokens."""
+    for q_len, group, window in ((4, 4, 0), (4, 4, 3), (5, 12, 0), (5, 12, 40), (1, 4, 0)):
+        x = Inputs(20 + group + window, [700, 40, 5, 2000], 2, group, 128, 16, q_len, mask=True)
+        x.mask[:, :, q_len - 1] = 0  # the block's last key is hidden from every token ...
+        if q_len == 5:
+            x.mask[:, :, 1] = 0
+            x.mask[:, 4, 1] = 1      # ... and the second from all but the last, of another column tile than the first
+        for b, n in enumerate(x.lens):
+            hidden = [n - 1] + ([n - q_len - window] if window and n > window + q_len else [])
+            for j in hidden:
+                for s8 in x.s8:
+                    s8[x.bt[b, j // 16], :, j % 16] = 0x7F
+        for splits in (0, 1, 2):
+            x.check(*x.run(window=window, num_splits=splits), window=window)
+
+
+@pytest.mark.parametrize("q_len,group,mask,window,sinks", [(1, 4, False, 0, True), (4, 4, True, 1500, True),
+                                                           (4, 4, True, 1600, True), (3, 7, False, 100, False),
+                                                           (16, 8, True, 0, True)])
+def test_balanced_pieces_with_options(q_len, group, mask, window, sinks):
+    """Contexts long and unequal enough that the keys are cut on the device, at cuts of its own choosing."""
+    x = Inputs(30 + q_len + window, [5000, 0, 3, 1700, 2900, 17], 2, group, 64, 16, q_len, mask, sinks)
+    assert fm.gqa_fp4_workspace_bytes(6, 2 * group, 2, 64, x.bt.shape[1] * 16, q_len, window) > 0 or \
+        window + q_len + 15 <= 96 * 16  # a window of no more tiles leaves nothing to cut
+    x.check(*x.run(window=window), window=window)
+
+
+@pytest.mark.parametrize("bs", [31, 128, 129, 700, 1024, 1025])
+def test_many_sequences(bs):
+    """Batches around the widths in which lengths are summed; most short or empty, some long, sharing a few pages."""
+    rng = np.random.default_rng(bs)
+    x = Inputs(40, [64 * 16], 2, 4, 64, 16, spare=1)
+    pages = x.bt[0]
+    x.lens = np.where(rng.random(bs) < 0.8, rng.integers(0, 40, bs), rng.integers(0, 4000, bs)).astype(np.int32)
+    x.lens[-1] = 3333
+    x.bt = pages[rng.integers(0, 64, (bs, 250))].astype(np.int32)
+    x.q = torch.from_numpy(rng.standard_normal((bs, 1, 8, 64))).to(torch.bfloat16)
+    rows = [(0, 0), (bs - 1, 7), (bs // 2, 3)] + [(int(b), 5) for b in rng.integers(0, bs, 8)]
+    out, lse = x.run()
+    x.check(out, lse, rows=rows)
+    one, lse1 = x.run(num_splits=1)  # the same sums in another order: float32 and f16 roundings apart
+    x.check(one, lse1, rows=rows)
+    empty = torch.from_numpy(x.lens == 0).to(DEV)
+    assert torch.all(out[empty] == 0) and torch.all(torch.isneginf(lse[empty]))
+    live = ~empty
+    assert torch.all((lse[live] - lse1[live]).abs() <= 2.0 ** -16)
+    assert torch.all((out[live] - one[live]).abs().float() <= 2.0 ** -7 * one[live].abs().float() + 2.0 ** -9)
+
+
+def test_bad_lengths_among_balanced_pieces():
+    x = Inputs(50, [3000, 2000, 2500], 2, 4, 64, 16)
+    good, good_lse = x.run()
+    for n in (-1, 16 * x.bt.shape[1] + 1):
+        x.lens[1] = n
+        out, lse = x.run()
+        assert fm.last_device_error() == fm.DEV_BAD_SEQLEN
+        assert torch.all(out[1] == 0) and torch.all(torch.isneginf(lse[1]))
+        assert torch.all((lse[[0, 2]] - good_lse[[0, 2]]).abs() <= 2.0 ** -16)
+
+
+def test_offsets_past_32_bits():
+    """Pages whose byte offsets pass 2^32 in codes and 2^29 in scales give what the same pages near the front do."""
+    x = Inputs(51, [500, 130], 8, 4, 128, 16)
+    want, want_lse = x.run()
+    blocks = 620000  # 5.1 GB of codes a cache
+    far = blocks - 1 - 7 * np.arange(x.codes[0].shape[0])
+    d = lambda a: torch.from_numpy(a).to(DEV)  # noqa: E731
+    big = []
+    for i in range(2):
+        for small, width in ((x.codes[i], 64), (x.s8[i], 8)):
+            t = torch.zeros((blocks, 8, 16, width), dtype=torch.uint8, device=DEV)
+            t[torch.from_numpy(far).to(DEV)] = d(small)
+            big.append(t)
+    for splits in (0, 3):
+        out, lse = fm.paged_gqa_decode_fp4(x.q.to(DEV), big[0], big[2], big[1], big[3], d(far[x.bt].astype(np.int32)),
+                                           d(x.lens), torch.tensor([x.scale[0]], device=DEV),
+                                           torch.tensor([x.scale[1]], device=DEV), softmax_scale=x.softmax_scale,
+                                           num_splits=splits)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) or splits == 3
+        x.check(out, lse)
+
+
 def test_extreme_scores():
     """Scores that differ by hundreds, rising and falling along the keys: the reference moves often."""
     for sign in (1.0, -1.0):
