@@ -93,6 +93,14 @@ void need_heads(const Tensor& x, const char* name, ScalarType type, const c10::D
   if (x.size(2) > 1 && x.stride(2) != 1) bad(std::string(name) + ": the dims of a head must be contiguous");
 }
 
+// The same for an output: no two of its rows may share memory.
+void need_heads_out(const Tensor& x, const char* name, c10::IntArrayRef shape, ScalarType type, const c10::Device& dev) {
+  need_heads(x, name, type, dev, shape[0], shape[2]);
+  if (x.sizes() != shape) bad(std::string(name) + " must have its input's shape");
+  if ((x.size(0) > 1 && x.stride(0) == 0) || (x.size(1) > 1 && x.stride(1) == 0))
+    bad(std::string(name) + ": its rows overlap");
+}
+
 // int32 or int64 [n]; returns whether they are 64 bits wide.
 int need_positions(const Tensor& p, const c10::Device& dev, int64_t n) {
   if (p.device() != dev || p.dim() != 1 || p.size(0) != n || !p.is_contiguous())
@@ -231,16 +239,14 @@ PyObject* py_rotary_apply(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       q_new = make(q.sizes(), type, dev);
       q_out = &q_new;
     } else {
-      need_heads(*q_out, "q_out", type, dev, n, hd);
-      if (q_out->sizes() != q.sizes()) bad("q_out must have q's shape");
+      need_heads_out(*q_out, "q_out", q.sizes(), type, dev);
     }
     if (k != nullptr) {
       if (k_out == nullptr) {
         k_new = make(k->sizes(), type, dev);
         k_out = &k_new;
       } else {
-        need_heads(*k_out, "k_out", type, dev, n, hd);
-        if (k_out->sizes() != k->sizes()) bad("k_out must have k's shape");
+        need_heads_out(*k_out, "k_out", k->sizes(), type, dev);
       }
     }
     const fp8mla_dtype_t code =

@@ -9,28 +9,41 @@
 //
 // What bounds it: a (key, KV head) pair is head_dim + head_dim / 8 bytes of K
 // and V together (144 at 128), read once; the products are a few per cent of
-// the tensor rate, but every code has to become a 16-bit operand, so the issue
-// slots of turning codes into operands are the second limit.  At the copy
-// bandwidth an SM has about six cycles per key of 256 values.
+// the tensor rate.  At the copy bandwidth an SM has about six cycles per key of
+// 256 values, and every code has to become a 16-bit operand in that time: a
+// conversion and a multiplication for two codes, which issue at half rate, so
+// the instructions that make operands and the memory are both close to their
+// limit.  Measured (32 contexts of 1024 to 16384 keys, 8 KV heads, head_dim
+// 128, group 4): 62.7 us a call, 0.77 of the measured copy bandwidth; leaving
+// the loads out would save 1.5 us, the scale multiplications 9.5, the
+// conversions of V 10.  Sixteen columns double the products and leave twelve
+// warps less to hide with: four-token blocks under a 4096-key window 46.6 us,
+// 0.45.  head_dim 64 halves the bytes of a tile but not its overhead: three
+// contexts of 50k to 131k keys 18.9 us, 0.35, of which 8 are the lengths' sums,
+// the first tiles, the merge and two launches.
 //
 // Design:
 //   * A warp works alone on tiles of 16 keys: it fetches them into its own
-//     ring in shared memory by 16-byte cp.async several tiles ahead, keeps
-//     its own running maximum, sum and accumulator, and meets the CTA's other
-//     warps only at the end.  No barrier in the loop but __syncwarp.
+//     ring in shared memory by 16-byte cp.async, two to three steps ahead,
+//     keeps its own running maximum, sum and accumulator, and meets the CTA's
+//     other warps only at the end of a piece.
 //   * Codes go from shared memory to registers to the product's A fragment:
 //     S^T = K Q^T (M = 16 keys, N = 8 columns, K = head_dim) and
 //     O^T = V^T P^T (M = 16 dims, N = 8 columns, K = 16 keys) as register-
 //     fragment products, for which a code is converted in the lane that needs
 //     it.  A tensor-memory product would need the expanded 16-bit tile written
 //     to shared or tensor memory first: 512 bytes a key against the 128 that
-//     an SM can store in a cycle, four of the six cycles a key has.
+//     an SM can store in a cycle, four of the six cycles a key has.  (The
+//     block-scaled 4-bit product takes neither Q and P in 16 bits nor V, whose
+//     scales run along the dims and not along the contraction.)
 //   * The order of the contraction is free, so each lane takes contiguous
 //     bytes: lane (g, t) of K row g holds dims [t hd/4, (t + 1) hd/4), and Q's
 //     fragment is laid out to match; of V, lane (g, t) holds the hd/8 dims
 //     from g hd/8 of keys t, t + 4, t + 8, t + 12.  A code's byte holds two
 //     neighbouring dims; for V the operand pairs two keys instead, formed on
-//     the nibbles (two shift-and-select steps for eight codes).
+//     the nibbles (a shift and a select for eight codes).  Fragment rows g and
+//     g + 8 of S^T are keys (g / 2) + 4 (g % 2) and that plus 8, so that the
+//     same pairs come out of the probabilities' transpose.
 //   * E2M1 * E4M3 has at most six significant bits and lies in f16's range
 //     (subnormals included), so K and V operands are exact.  Q is bf16 times
 //     a power of two per column, exact in f16 down to 2^-38 of its largest
@@ -137,10 +150,10 @@ __device__ __forceinline__ int v_place(int r, int c) {
   return r * 128 + ((c ^ ((r & 3) << 1)) << 4);
 }
 
-// Power of two e with amax * 2^-e in [2^14, 2^15) (clamped so that 2^e and 2^-e are normal).
+// e with amax * 2^-e in [2^14, 2^15); not below -100 (2^-e has to be a float: smaller queries lose bits, down to 0).
 __device__ __forceinline__ int q_exponent(float amax) {
   const int expo = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu);
-  return max(-100, min(100, expo - 127 - 14));
+  return min(max(-100, expo - 127 - 14), 113);
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
@@ -152,9 +165,6 @@ __device__ __forceinline__ uint4 ldg_now(const uint4* p) {
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
-
-// Fragment positions -> keys of the tile: row g of S^T is key (g / 2) + 4 (g % 2), row g + 8 that plus 8, so the
-// pairs (2t, 2t + 1) and (2t + 8, 2t + 9) of P^T's contraction are keys t, t + 4 and t + 8, t + 12.
 
 // Keys that the call reads of a sequence of length s_k: none, and a status bit, where that is negative or longer
 // than the block table; and the first tile that any token's window reaches.
@@ -839,10 +849,14 @@ struct Plan {
   size_t slots, ml, span, bytes;  // partial states, and where (m, l) and the spans of pieces begin
 };
 
+// A window no shorter than any sequence hides nothing.
+int seen_window(int window, long long capacity) { return window >= capacity ? 0 : window; }
+
 Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long capacity, int window, int num_splits) {
   Plan p;
   p.ct = col_tiles(q_len * (h_q / h_kv), &p.nt);
   long long longest = std::max(capacity, 1LL);
+  window = seen_window(window, capacity);
   if (window > 0) longest = std::min(longest, static_cast<long long>(window) + q_len - 1 + kTile);
   const long long tiles = (longest + kTile - 1) / kTile;
   const long long seqs = static_cast<long long>(bs) * h_kv;
@@ -969,7 +983,7 @@ fp8mla_status_t fp4_decode_entry(const Fp4DecodeArgs& a, cudaStream_t stream) {
   p.splits = plan.splits;
   p.units = plan.units;
   p.q_len = a.q_len;
-  p.window = a.window;
+  p.window = fp4::seen_window(a.window, capacity);
   p.page_shift = page_shift;
   p.softmax_scale = a.softmax_scale;
   const int n = static_cast<int>(seqs);

@@ -160,6 +160,15 @@ def test_blocks_windows_and_sinks(q_len, group, mask, window, sinks, hd, splits)
     x.check(*x.run(window=window, num_splits=splits), window=window)
 
 
+def test_a_window_longer_than_every_sequence_hides_nothing():
+    x = Inputs(60, [700, 48, 0, 3, 3000], 2, 4, 64, 16, 3)
+    for splits in (0, 1, 3):
+        want, want_lse = x.run(num_splits=splits)
+        for window in (3008, 1 << 30, (1 << 31) - 1):
+            out, lse = x.run(num_splits=splits, window=window)
+            assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 def test_rows_that_see_nothing():
     """A block whose mask hides everything from a token of a cache no longer than the block: zeros and -inf,
     or the sink's logit."""
@@ -277,6 +286,7 @@ def test_queries_of_every_size():
     for h, e in enumerate((-60, -20, 0, 3)):
         x.q[0, 0, h] = (x.q[0, 0, h].double() * 2.0 ** e).to(torch.bfloat16)
     x.q[0, 0, 4] = 0
+    x.q[0, 0, 6] = (x.q[0, 0, 6].double() * 2.0 ** -133).to(torch.bfloat16)  # subnormal: scores of zero
     x.q[0, 0, 5] = x.q[0, 0, 5] * 2.0 ** -30
     x.q[0, 0, 5, 77] = 3.0
     x.check(*x.run())

@@ -182,7 +182,8 @@ def test_wrapper_refusals():
     for bad in [dict(q=q.cpu()), dict(q=q.double()), dict(q=q[..., ::2]), dict(k=q[:3]), dict(k=q.float()),
                 dict(k=q[..., :16]), dict(positions=pos[:3]), dict(positions=pos.float()), dict(positions=pos.cpu()),
                 dict(table=table.double()), dict(table=table[..., 0]), dict(table=table.cpu()),
-                dict(q_out=q[:, :1]), dict(q_out=q.float()), dict(k_out=q)]:
+                dict(q_out=q[:, :1]), dict(q_out=q.float()), dict(k_out=q),
+                dict(q_out=q[:1].expand(4, 2, 32)), dict(q_out=q[:, :1].expand(4, 2, 32))]:
         a = dict(q=q, k=None, positions=pos, table=table)
         kw = {n: v for n, v in bad.items() if n.endswith("_out")}
         a.update({n: v for n, v in bad.items() if n not in kw})
