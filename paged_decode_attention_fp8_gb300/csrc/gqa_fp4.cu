@@ -19,7 +19,7 @@
 // conversions of V 10.  Sixteen columns double the products and leave twelve
 // warps less to hide with: four-token blocks under a 4096-key window 46.6 us,
 // 0.45.  head_dim 64 halves the bytes of a tile but not its overhead: three
-// contexts of 50k to 131k keys 18.9 us, 0.35, of which 8 are the lengths' sums,
+// contexts of 50k to 131k keys 17.9 us, 0.37, of which 8 are the lengths' sums,
 // the first tiles, the merge and two launches.
 //
 // Design:
@@ -733,8 +733,9 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
 }
 
 // Merge of the shards of one (sequence, KV head) and column tile.  Lane x of a warp owns one float4 of the fragment
-// order (two dims of two columns) of one step (16 dims).  With kGroups = 1 the four warps take four steps; with 8
-// the warps take shards w, w + 8, ... of one step and meet in shared memory (few sequences, many shards).
+// order (two dims of two columns) of one step (16 dims).  With kGroups = 1 the four warps take four steps; with 16
+// the warps take shards w, w + 16, ... of one step and meet in shared memory (few sequences, many shards: three
+// contexts cut into 76 shards each take 17.9 us a call, 18.9 with 8 warps, 20.9 with 4, 19.5 with 32).
 template <int kHd, int kNT, int kGroups>
 __global__ void __launch_bounds__(kGroups == 1 ? 128 : kGroups * 32) fp4_combine_kernel(const __grid_constant__ Params prm) {
   constexpr int kSteps = kHd / 16, kFrag = kNT * kSteps * 32;
@@ -916,7 +917,7 @@ cudaError_t launch(const Params& prm, bool wide, int seqs, int ct, cudaStream_t 
   if (static_cast<long long>(seqs) * ct >= device_sms())
     return launch_dependent(fp4_combine_kernel<kHd, kNT, 1>, dim3(static_cast<unsigned>(seqs), ct, kFrags / 4),
                             dim3(128), 0, stream, prm);
-  return launch_dependent(fp4_combine_kernel<kHd, kNT, 8>, dim3(static_cast<unsigned>(seqs), ct, kFrags), dim3(256),
+  return launch_dependent(fp4_combine_kernel<kHd, kNT, 16>, dim3(static_cast<unsigned>(seqs), ct, kFrags), dim3(512),
                           0, stream, prm);
 }
 
