@@ -314,6 +314,7 @@ PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       bad("scales for v without v");
     }
     int wide = 0;
+    if (table == nullptr && pos != nullptr) bad("positions without a table");
     if (table != nullptr) {
       if (pos == nullptr) bad("a table needs positions");
       wide = need_positions(*pos, dev, n);

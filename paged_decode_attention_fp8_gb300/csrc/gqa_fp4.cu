@@ -166,6 +166,12 @@ __device__ __forceinline__ uint4 ldg_now(const uint4* p) {
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 
+// finish_row, with a NaN sum passed on (finish_row takes one for no key at all).
+__device__ __forceinline__ void finish(float m, float l, float sink, float v_scale, float* f, float* lse) {
+  finish_row(m, l, sink, v_scale, f, lse);
+  if (l != l) *f = *lse = l;
+}
+
 // Keys that the call reads of a sequence of length s_k: none, and a status bit, where that is negative or longer
 // than the block table; and the first tile that any token's window reaches.
 __device__ __forceinline__ int checked_len(const Params& prm, int s_k) {
@@ -544,7 +550,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
         for (int k = 0; k < 2; ++k) {
           top[n][k] = fmaxf(s[0][n][k], s[0][n][k + 2]);
           if constexpr (kU == 2) top[n][k] = fmax3(top[n][k], s[kU - 1][n][k], s[kU - 1][n][k + 2]);
-          grow |= top[n][k] > limit[n][k];
+          grow |= !(top[n][k] <= limit[n][k]);  // (a NaN score moves it, and its column stays NaN)
         }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -555,7 +561,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            if (mx > limit[n][k]) {
+            if (!(mx <= limit[n][k])) {
               const float m = mx * cq[n][k] - kBelow;
               const float alpha = limit[n][k] == kNegInf ? 0.f : ex2_approx(-neg_m[n][k] - m);
               neg_m[n][k] = -m;
@@ -692,17 +698,16 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
       float mx = kNegInf, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][c]);
-      if (mx != kNegInf) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += s_l[w][c] * ex2_approx(s_m[w][c] - mx);
-      }
+      for (int w = 0; w < kWarps; ++w)
+        sum += s_m[w][c] == kNegInf ? 0.f : s_l[w][c] * ex2_approx(s_m[w][c] - (mx == kNegInf ? 0.f : mx));
       if (slot >= 0) {
         prm.ws_ml[slot * (kNT * 8) + c] = make_float2(mx, sum);
       } else if (c < ncols) {
         const int col = col0 + c, token = col / prm.group, hq = kvh * prm.group + col - token * prm.group;
         const int64_t row = (static_cast<int64_t>(b) * prm.q_len + token) * prm.h_q + hq;
         float fac, lse;
-        finish_row(mx, sum, prm.sinks ? __ldg(prm.sinks + hq) : kNegInf, __ldg(prm.v_scale), &fac, &lse);
+        finish(mx, sum, prm.sinks ? __ldg(prm.sinks + hq) : kNegInf, __ldg(prm.v_scale), &fac, &lse);
         s_cq[c] = fac;
         s_row[c] = row;
         prm.lse[row] = lse;
@@ -827,7 +832,7 @@ __global__ void __launch_bounds__(kGroups == 1 ? 128 : kGroups * 32) fp4_combine
     const int col = col0 + c + k, hq = kvh * prm.group + col % prm.group;
     const size_t row = (static_cast<size_t>(b) * prm.q_len + col / prm.group) * prm.h_q + hq;
     float fac, lse;
-    finish_row(k ? m1 : m0, k ? l1 : l0, prm.sinks ? prm.sinks[hq] : kNegInf, v_scale, &fac, &lse);
+    finish(k ? m1 : m0, k ? l1 : l0, prm.sinks ? prm.sinks[hq] : kNegInf, v_scale, &fac, &lse);
     *reinterpret_cast<uint32_t*>(prm.out + row * kHd + lane / 4 * (kHd / 8) + 2 * j) =
         pack_bf16x2((k ? a.y : a.x) * fac, (k ? a.w : a.z) * fac);
     if (j == 0 && lane < 4) prm.lse[row] = lse;

@@ -319,6 +319,38 @@ def test_served_batch_sampled():
     assert torch.equal(out, moved) and torch.equal(lse, lse3)
 
 
+@pytest.mark.parametrize("lens", [[50, 300, 20], [2000, 3000, 700]])
+def test_nan_propagates_to_what_it_touches(lens):
+    """A NaN query value: its row alone.  A NaN K scale on a visible key: every row of that KV head that sees it.  A NaN
+    V scale: those rows' 16 dims alone, not the LSE.  Direct, cut and balanced."""
+    x = Inputs(70, lens, 2, 4, 128, 16)
+    for splits in (0, 1, 2):
+        want, want_lse = x.run(num_splits=splits)
+        q = x.q.clone()
+        x.q[1, 0, 2, 5] = math.nan
+        out, lse = x.run(num_splits=splits)
+        assert torch.all(torch.isnan(out[1, 0, 2])) and torch.isnan(lse[1, 0, 2])
+        out[1, 0, 2], lse[1, 0, 2] = want[1, 0, 2], want_lse[1, 0, 2]
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        x.q = q
+        page = x.bt[0, 2], 1, 3
+        kept = x.s8[0][page].copy()
+        x.s8[0][page] = 0x7F
+        out, lse = x.run(num_splits=splits)
+        assert torch.all(torch.isnan(out[0, 0, 4:])) and torch.all(torch.isnan(lse[0, 0, 4:]))
+        out[0, 0, 4:], lse[0, 0, 4:] = want[0, 0, 4:], want_lse[0, 0, 4:]
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        x.s8[0][page] = kept
+        kept = x.s8[1][page].copy()
+        x.s8[1][page + (5,)] = 0x7F
+        out, lse = x.run(num_splits=splits)
+        assert torch.all(torch.isnan(out[0, 0, 4:, 80:96])) and torch.equal(lse, want_lse)
+        out[0, 0, 4:, 80:96] = want[0, 0, 4:, 80:96]
+        assert torch.equal(out, want)
+        x.s8[1][page] = kept
+    assert fm.last_device_error() == 0
+
+
 def test_bad_pages_and_lengths_are_reported():
     x = Inputs(16, [100, 50], 1, 4, 64, 16)
     good, _ = x.run()

@@ -263,6 +263,20 @@ def test_read_of_odd_widths(kind, hd):
     assert fm.last_device_error() == 0
 
 
+@pytest.mark.skipif(not hasattr(torch, "float4_e2m1fn_x2"), reason="torch has no packed 4-bit type")
+def test_packed_4_bit_type_is_the_same_bytes():
+    c, d = (Caches("fp4", 3, 2, 16, 64, (0.01, 0.012)) for _ in range(2))
+    k, slots = _rows(71, (20, 2, 64)).to(DEV), _slots(72, 20, 3, 16).to(DEV)
+    fm.paged_kv_append(k, k, slots, c.dev[0], c.dev[1], **c.kwargs())
+    typed = [x.view(torch.float4_e2m1fn_x2) for x in d.dev]
+    fm.paged_kv_append(k, k, slots, typed[0], typed[1], **d.kwargs())
+    for i in range(2):
+        assert torch.equal(c.dev[i], d.dev[i]) and torch.equal(c.dev_blocks[i], d.dev_blocks[i])
+    a = fm.paged_cache_read(c.dev[0], slots, scale=c.dev_scale[0], block_scales=c.dev_blocks[0])
+    b = fm.paged_cache_read(typed[0], slots, scale=d.dev_scale[0], block_scales=d.dev_blocks[0])
+    assert torch.equal(a, b)
+
+
 def test_offsets_past_32_bits():
     """Slots whose byte offset in the cache passes 2^32 land there, and nowhere else."""
     blocks, h_kv, page, hd = 70000, 8, 64, 128  # 4.6 GB of E4M3 codes
@@ -294,7 +308,7 @@ def test_wrapper_refusals():
                 dict(slot_mapping=slots.long()), dict(slot_mapping=slots[:2]), dict(k_cache=c.dev[0][:, :1]),
                 dict(k_cache=e.dev[0]), dict(v_cache=e.dev[1]), dict(k_scale=None), dict(v_block_scales=None),
                 dict(k_scale=torch.zeros(2, device=DEV)), dict(k_row_scales=c.dev_rows[0]),
-                dict(k_block_scales=c.dev_blocks[0][..., :2]), dict(q=k), dict(q_out=k), dict(table=table),
+                dict(k_block_scales=c.dev_blocks[0][..., :2]), dict(q=k), dict(q_out=k), dict(table=table), dict(positions=pos),
                 dict(table=table, positions=pos.float()), dict(table=table, positions=pos, q=k, q_out=k[:, :1]),
                 dict(table=table.double(), positions=pos)]:
         with pytest.raises(ValueError):
