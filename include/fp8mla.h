@@ -453,8 +453,9 @@ FP8MLA_API fp8mla_status_t paged_cache_read(const void* cache, fp8mla_kv_dtype_t
  *   block_table, seqlens, spec_mask, window, sinks, out, lse  as
  *                paged_gqa_decode_ext
  *   num_splits   0 = auto: one CTA per (sequence, KV head) where the block
- *                table holds at most 1024 keys (1536 with fewer of them than
- *                SMs) or the sequences fill the GPU many times over, else the keys of all sequences cut into
+ *                table holds few keys (1024 with few sequences, up to 4096 as
+ *                one CTA each comes to fill the GPU) or the sequences fill it
+ *                many times over, else the keys of all sequences cut into
  *                equal pieces, one per CTA that fits on the GPU; 1 = one CTA
  *                each; k > 1 = every sequence in k shards, at most one per
  *                128 keys of the block table

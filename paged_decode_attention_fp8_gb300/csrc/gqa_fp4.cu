@@ -76,11 +76,11 @@ constexpr int kTile = 16;       // keys of a tile
 constexpr int kMaxQLen = 16;
 constexpr int kMaxCols = 128;   // q_len * (h_q / h_kv)
 constexpr int kMaxLine = 1024;  // sequences whose lengths a CTA sums
-constexpr int kMinTiles = 16;   // tiles of a piece, where there are fewer than GPU-filling
+constexpr int kMinTiles = 8;    // places of a piece, where there are fewer than the GPU takes at once
 constexpr int kFixed = 32;      // what a sequence costs a CTA beside its tiles, in tiles: fill, drain and merge
-constexpr int kShort = 64;      // tiles up to which a sequence is not cut
-constexpr int kShortFew = 96;   // the same where wide CTAs take it (one sequence, 8 KV heads: 1500 keys 10.4 us, cut
-                                // 10.9; 2048 keys 11.9 and 11.4)
+constexpr int kShort = 96;      // tiles up to which a sequence is not cut (200 of 94 tiles: 16.7 us, cut 18.1)
+constexpr int kShortFew = 64;   // the same where wide CTAs take it, of which few leave the GPU idle (8 of 69 tiles: 10.0
+                                // us, cut 8.8; 8 of 49 tiles: 8.7 and 8.7)
 constexpr float kBelow = 7.f;   // a reference lies this far below the largest score (log2) ...
 constexpr float kTau = 15.f;    // ... and moves when a score is this far above it
 
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
     if (threadIdx.x == 0) s_line[prm.bs] = before;
     __syncthreads();
     const int work = s_line[prm.bs] * prm.h_kv;
-    const int pieces = max(1, min(prm.units, work / (kMinTiles + kFixed)));
+    const int pieces = max(1, min(prm.units, work / kMinTiles));
     if (unit >= pieces) return;
     const int each = work / pieces, rest = work - each * pieces;  // cut u at floor(work u / pieces)
     cur = each * unit + rest * unit / pieces;
@@ -869,10 +869,13 @@ Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long cap
   const int resident = device_sms() * (head_dim == 256 ? 2 : 3);  // Shape::kPerSm
   p.units = 0;
   p.wide = false;
-  const bool few = seqs * p.ct <= device_sms();  // a wide CTA has an SM of its own
+  // A wide CTA has an SM of its own; cutting gains by the SMs that would otherwise idle.
+  const long long sms = device_sms();
+  const bool few = seqs * p.ct <= sms;
+  const long long short_few = few ? std::min<long long>(256, kShortFew * sms / (sms - 3 * seqs * p.ct / 4)) : 0;
   if (num_splits > 0) {
     p.splits = static_cast<int>(std::min<long long>(num_splits, std::max(1LL, (tiles + 7) / 8)));
-  } else if (tiles <= (few ? kShortFew : kShort) || seqs * p.ct >= 8LL * resident || bs > kMaxLine ||
+  } else if (tiles <= (few ? short_few : kShort) || seqs * p.ct >= 8LL * resident || bs > kMaxLine ||
              seqs * (tiles + kFixed) > 0x7FFFFFFFll) {
     // Short contexts: one CTA a sequence takes no longer than a piece and its merge.  Many sequences: their CTAs
     // balance by themselves.  (The line's places are counted in 32 bits.)
@@ -918,12 +921,16 @@ cudaError_t launch(const Params& prm, bool wide, int seqs, int ct, cudaStream_t 
   const cudaError_t e = wide ? launch_decode<kHd, kNT, true>(prm, seqs, ct, stream)
                              : launch_decode<kHd, kNT, false>(prm, seqs, ct, stream);
   if (e != cudaSuccess || prm.splits == 1) return e;
+  // warps for the shards that a sequence has on average, four at a time each (100 sequences cut into 5: 19.4 us a call
+  // with one warp, 25.3 with sixteen, most of them idle; 6 cut into 76: 17.9 with sixteen, 20.9 with four)
   constexpr unsigned kFrags = kNT * (kHd / 16);
-  if (static_cast<long long>(seqs) * ct >= device_sms())
-    return launch_dependent(fp4_combine_kernel<kHd, kNT, 1>, dim3(static_cast<unsigned>(seqs), ct, kFrags / 4),
-                            dim3(128), 0, stream, prm);
-  return launch_dependent(fp4_combine_kernel<kHd, kNT, 16>, dim3(static_cast<unsigned>(seqs), ct, kFrags), dim3(512),
-                          0, stream, prm);
+  const unsigned s = static_cast<unsigned>(seqs);
+  const int shards = prm.splits == 0 ? prm.units / seqs + 1 : prm.splits;
+  if (shards <= 8)
+    return launch_dependent(fp4_combine_kernel<kHd, kNT, 1>, dim3(s, ct, kFrags / 4), dim3(128), 0, stream, prm);
+  if (shards <= 24)
+    return launch_dependent(fp4_combine_kernel<kHd, kNT, 4>, dim3(s, ct, kFrags), dim3(128), 0, stream, prm);
+  return launch_dependent(fp4_combine_kernel<kHd, kNT, 16>, dim3(s, ct, kFrags), dim3(512), 0, stream, prm);
 }
 
 }  // namespace fp4
