@@ -79,8 +79,6 @@ constexpr int kMaxLine = 1024;  // sequences whose lengths a CTA sums
 constexpr int kMinTiles = 8;    // places of a piece, where there are fewer than the GPU takes at once
 constexpr int kFixed = 32;      // what a sequence costs a CTA beside its tiles, in tiles: fill, drain and merge
 constexpr int kShort = 96;      // tiles up to which a sequence is not cut (200 of 94 tiles: 16.7 us, cut 18.1)
-constexpr int kShortFew = 64;   // the same where wide CTAs take it, of which few leave the GPU idle (8 of 69 tiles: 10.0
-                                // us, cut 8.8; 8 of 49 tiles: 8.7 and 8.7)
 constexpr float kBelow = 7.f;   // a reference lies this far below the largest score (log2) ...
 constexpr float kTau = 15.f;    // ... and moves when a score is this far above it
 
@@ -869,10 +867,13 @@ Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long cap
   const int resident = device_sms() * (head_dim == 256 ? 2 : 3);  // Shape::kPerSm
   p.units = 0;
   p.wide = false;
-  // A wide CTA has an SM of its own; cutting gains by the SMs that would otherwise idle.
+  // A wide CTA has an SM of its own; cutting gains by the SMs that would otherwise idle.  With next to all of them idle
+  // it pays from three or four tiles a warp on (8 sequences of 49 tiles: 8.7 us uncut and cut, of 69 tiles 10.0 and
+  // 8.8; sixteen columns, 4 of 25 tiles 9.3 and 9.6, of 47 tiles 10.4 and 9.7; head_dim 256, 8 of 38 tiles 10.0, 8.9).
   const long long sms = device_sms();
   const bool few = seqs * p.ct <= sms;
-  const long long short_few = few ? std::min<long long>(256, kShortFew * sms / (sms - 3 * seqs * p.ct / 4)) : 0;
+  const int wide_tiles = head_dim == 256 ? 24 : (p.nt == 1 ? 64 : 36);
+  const long long short_few = few ? std::min<long long>(256, wide_tiles * sms / (sms - 3 * seqs * p.ct / 4)) : 0;
   if (num_splits > 0) {
     p.splits = static_cast<int>(std::min<long long>(num_splits, std::max(1LL, (tiles + 7) / 8)));
   } else if (tiles <= (few ? short_few : kShort) || seqs * p.ct >= 8LL * resident || bs > kMaxLine ||
