@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(kGroups == 1 ? 128 : kGroups * 32) fp4_combine
   long long first, next;
   int step, count;
   if (prm.splits == 0) {
-    const int2 span = __ldg(prm.ws_span + seq);
+    const int2 span = prm.ws_span[seq];
     if (span.x == span.y) return;  // within one piece: written there
     const long long base = static_cast<long long>(blockIdx.y) * prm.units * 2;
     first = base + 2 * span.x + 1;
