@@ -420,8 +420,10 @@ FP8MLA_API fp8mla_status_t rotary_apply(const void* q, int64_t q_token_stride, i
  * fp8_paged_cache_write's arithmetic; an E2M1 block stores
  * s8 = E4M3(amax * fp32(1 / fp32(6 scale))) and codes
  * E2M1(x * fp32(1 / fp32(s8 scale))), 0 where s8 is 0.  Rounding is to nearest
- * even with saturation.  Rows must be finite and scales normal floats > 0 for
- * which 6 * 448 * scale and scale / 512 are normal too.  Two tokens with one
+ * even with saturation.  Rows must be finite, with two exceptions: an infinity
+ * saturates (not with row scales), and a NaN is stored as NaN, in E2M1 in its
+ * block's scale.  Scales are normal floats > 0 for which 6 * 448 * scale and
+ * scale / 512 are normal too.  Two tokens with one
  * slot race.  Requires head_dim a multiple of 16 in [16, 1024]; with a table
  * rot a multiple of 16 and rot_offset of 8 (of 16 when interleaved); in E2M1
  * with the half layout rot a multiple of 32 and rot_offset of 16. */

@@ -513,6 +513,12 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
       }
     };
 
+    auto sees = [&](int p, int c) {  // whether key p is for column c
+      const int ti = min((col0 + c) / prm.group, prm.q_len - 1);
+      const int c_blk = p - start;
+      return p < keys_end && (c_blk < 0 || ((s_vis[ti] >> c_blk) & 1u)) && (prm.window == 0 || ti - c_blk < prm.window);
+    };
+
     const uint8_t* st = smem + warp * (kStages * kStage);
     const uint8_t* const st_end = st + kStages * kStage;
     int tok0 = mine0 * kTile;
@@ -529,12 +535,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
           for (int n = 0; n < kNT; ++n)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int p = tok0 + u * kTile + (k < 2 ? r0 : r1);
-              const int ti = min((col0 + n * 8 + 2 * t + (k & 1)) / prm.group, prm.q_len - 1);
-              const int c_blk = p - start;
-              const bool vis = p < keys_end && (c_blk < 0 || ((s_vis[ti] >> c_blk) & 1u)) &&
-                               (prm.window == 0 || ti - c_blk < prm.window);
-              if (!vis) {
+              if (!sees(tok0 + u * kTile + (k < 2 ? r0 : r1), n * 8 + 2 * t + (k & 1))) {
                 s[u][n][k] = kNegInf;
                 hidden |= 1u << (8 * u + 4 * n + k);
               }
@@ -613,13 +614,19 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
             sc[k] = *reinterpret_cast<const uint16_t*>(sv + L::kVs + r * 16 + 2 * g);
           }
         }
-        if constexpr (kMasked) {  // a key that no column sees has a zero weight; its scale may be anything (NaN), so it
-                                  // is zeroed
+        // A weight of zero does not hide a NaN, so a key that no column sees has its scales zeroed, whatever they are,
+        // and so has a NaN scale; the columns that see that one get their NaN after the product.
+        bool nans = false;
+        if constexpr (kMasked) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int p = tok0 + u * kTile + t + 4 * k;
             if (p >= keys_end || p < k_lo || (p >= start && !((s_any >> (p - start)) & 1u))) sc[k] = 0;
+#pragma unroll
+            for (uint32_t m = 0x7Fu; m <= (kHd == 256 ? 0x7F00u : 0x7Fu); m <<= 8)
+              if ((sc[k] & m) == m) sc[k] &= ~(m | (m << 1)), nans = true;
           }
+          nans = __any_sync(0xffffffffu, nans);
         }
 #pragma unroll
         for (int w = 0; w < kVWords; ++w) {
@@ -644,6 +651,27 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
             const uint32_t a2 = mul_f16x2(z[k], scd), a3 = mul_f16x2(h[k], scd);
 #pragma unroll
             for (int n = 0; n < kNT; ++n) mma_f16_16x8x16(o[n][4 * w + k], a0, a1, a2, a3, pf[u][n][0], pf[u][n][1]);
+          }
+        }
+        if constexpr (kMasked) {
+          if (nans) {
+            for (int r = 0; r < kTile; ++r) {
+#pragma unroll
+              for (int w = 0; w < (kHd == 256 ? 2 : 1); ++w) {
+                const int block = kHd == 64 ? g >> 1 : (kHd == 128 ? g : 2 * g + w);
+                if ((sv[L::kVs + r * (kHd / 16) + block] & 0x7F) != 0x7F) continue;
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    if (!sees(tok0 + u * kTile + r, n * 8 + 2 * t + k)) continue;
+                    constexpr int kOf = kHd == 256 ? kSteps / 2 : kSteps;  // steps of a block's dims
+#pragma unroll
+                    for (int j = 0; j < kOf; ++j)
+                      o[n][w * kOf + j][k] = o[n][w * kOf + j][k + 2] = __int_as_float(0x7FFFFFFF);
+                  }
+              }
+            }
           }
         }
       }
@@ -736,9 +764,9 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
 }
 
 // Merge of the shards of one (sequence, KV head) and column tile.  Lane x of a warp owns one float4 of the fragment
-// order (two dims of two columns) of one step (16 dims).  With kGroups = 1 the four warps take four steps; with 16
-// the warps take shards w, w + 16, ... of one step and meet in shared memory (few sequences, many shards: three
-// contexts cut into 76 shards each take 17.9 us a call, 18.9 with 8 warps, 20.9 with 4, 19.5 with 32).
+// order (two dims of two columns) of one step (16 dims).  With kGroups = 1 the four warps take four steps; with
+// more, the warps take shards w, w + kGroups, ... of one step and meet in shared memory (few sequences, many shards:
+// three contexts cut into 76 shards each take 17.9 us a call with 16, 18.9 with 8, 20.9 with 4, 19.5 with 32).
 template <int kHd, int kNT, int kGroups>
 __global__ void __launch_bounds__(kGroups == 1 ? 128 : kGroups * 32) fp4_combine_kernel(const __grid_constant__ Params prm) {
   constexpr int kSteps = kHd / 16, kFrag = kNT * kSteps * 32;

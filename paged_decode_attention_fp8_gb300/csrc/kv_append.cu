@@ -10,7 +10,8 @@
 //                           lifted by 2^64 first), as the cache write does
 //   E2M1 in blocks of 16:   s8 = E4M3(amax * fp32(1 / fp32(6 scale))),
 //                           code = E2M1(x * fp32(1 / fp32(s8 * scale))),
-//                           0 where s8 is 0
+//                           0 where s8 is 0; a NaN, for which E2M1 has no
+//                           code, makes s8 and so its block NaN
 // Every float operation and conversion rounds to nearest even, conversions
 // saturate.  The same launch can rotate the step's queries (bf16 in and out).
 //
@@ -82,11 +83,13 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
 }
 
+template <bool kNan = false>  // kNan: NaN where a value is
 __device__ __forceinline__ float amax8(const float (&x)[8]) {
-  float m = fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2]));
-  m = fmax3(m, fabsf(x[3]), fabsf(x[4]));
-  m = fmax3(m, fabsf(x[5]), fabsf(x[6]));
-  return fmaxf(m, fabsf(x[7]));
+  auto max3 = [](float a, float b, float c) { return kNan ? fmax3_nan(a, b, c) : fmax3(a, b, c); };
+  float m = max3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2]));
+  m = max3(m, fabsf(x[3]), fabsf(x[4]));
+  m = max3(m, fabsf(x[5]), fabsf(x[6]));
+  return max3(m, m, fabsf(x[7]));
 }
 
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
@@ -254,11 +257,12 @@ __device__ __forceinline__ void run_class(const Params& prm, const Source& src, 
       for (int j = 0; j < kP; ++j) {
         // Block of a chunk: a lane's two chunks, or (half layout) one chunk of this lane and of its neighbour, so
         // that two lanes share two blocks.  Each lane works out one scale; neighbours then swap.
-        const float ma = amax8(p[j].a), mb = amax8(p[j].b);
+        const float ma = amax8<true>(p[j].a), mb = amax8<true>(p[j].b);
         const bool shared = half && turn[j];
         const bool odd = shared && (sub & 1);
         const float theirs = __shfl_xor_sync(0xffffffffu, odd ? ma : mb, 1);
-        const float amax = fmaxf(odd ? mb : ma, shared ? theirs : mb);
+        const float other = shared ? theirs : mb;
+        const float amax = fmax3_nan(odd ? mb : ma, other, other);
         const uint32_t s8 = pack_e4m3x2(__fmul_rn(amax, inv6), 0.f) & 0xFFu;
         const float inv = __frcp_rn(__fmul_rn(f16_lo(e4m3x2_to_f16x2(s8)), scale));
         const uint32_t s8x = __shfl_xor_sync(0xffffffffu, s8, 1);

@@ -319,6 +319,29 @@ def test_served_batch_sampled():
     assert torch.equal(out, moved) and torch.equal(lse, lse3)
 
 
+@pytest.mark.parametrize("hd,q_len,group", [(64, 4, 2), (64, 4, 5), (128, 4, 2), (128, 6, 8), (256, 3, 2), (256, 16, 4)])
+def test_a_nan_value_stays_with_the_tokens_that_see_it(hd, q_len, group):
+    """A NaN V scale on the block's last key, which the last token alone sees, and on the key that the window leaves to
+    the first token alone: those tokens' 16 dims are NaN and nothing else changes by a bit."""
+    lens, window = [700, 40, 2000], 33
+    x = Inputs(80 + hd + q_len, lens, 2, group, hd, 32, q_len)
+    for splits in (0, 1, 2):
+        want, want_lse = x.run(window=window, num_splits=splits)
+        for b, n in enumerate(lens):
+            first = n - q_len + 1 - window
+            for j, tok, blk in [(n - 1, q_len - 1, hd // 16 - 1)] + ([(first, 0, 1)] if first >= 0 else []):
+                at = x.bt[b, j // 32], 1, j % 32, blk
+                kept = x.s8[1][at]
+                x.s8[1][at] = 0xFF
+                out, lse = x.run(window=window, num_splits=splits)
+                x.s8[1][at] = kept
+                touched = out[b, tok, group:, 16 * blk:16 * blk + 16]
+                assert torch.all(torch.isnan(touched)), (splits, b, j)
+                touched.copy_(want[b, tok, group:, 16 * blk:16 * blk + 16])
+                assert torch.equal(out, want) and torch.equal(lse, want_lse), (splits, b, j)
+    assert fm.last_device_error() == 0
+
+
 @pytest.mark.parametrize("lens", [[50, 300, 20], [2000, 3000, 700]])
 def test_nan_propagates_to_what_it_touches(lens):
     """A NaN query value: its row alone.  A NaN K scale on a visible key: every row of that KV head that sees it.  A NaN

@@ -217,6 +217,50 @@ def test_many_rows_walk_the_grid():
     assert np.all(left == SENTINEL)
 
 
+@pytest.mark.parametrize("rot,interleaved", [(0, False), (64, False), (64, True)])
+def test_nan_and_infinity_in_four_bits(rot, interleaved):
+    """E2M1 has no NaN, so a NaN makes its block's scale NaN (with its partner's block where it is turned) and no other
+    block changes; an infinity is stored as the largest value, 448 * 6 scales."""
+    n, h_kv, hd, scale = 9, 2, 64, (0.01, 0.02)
+    k, v = _rows(51, (n, h_kv, hd)), _rows(52, (n, h_kv, hd))
+    bad = [(0, 0, 0), (1, 1, 37), (4, 0, 63), (8, 1, 20)]
+    slots = _slots(53, n, 2, 16)
+    pos = torch.arange(1, n + 1)
+    c = Caches("fp4", 2, h_kv, 16, hd, scale)
+    table, kw = None, {}
+    if rot:
+        table = fm.rotary_table(fm.rotary_frequencies(rot)[0], 100)
+        kw = dict(positions=pos.to(DEV), table=table, interleaved=interleaved)
+    kn, vn = k.clone(), v.clone()
+    for at in bad:
+        kn[at] = vn[at] = float("nan")
+    vn[5, 1, 18] = -float("inf")
+    fm.paged_kv_append(kn.to(DEV), vn.to(DEV), slots.to(DEV), c.dev[0], c.dev[1], **kw, **c.kwargs())
+    c.write(0, rotate_f32(k, pos, table.cpu().numpy(), interleaved=interleaved) if rot else k.float().numpy(), slots)
+    c.write(1, v.float().numpy(), slots)
+    got = [[x.cpu().numpy() for x in y] for y in (c.dev, c.dev_blocks)]
+    back = [fm.paged_cache_read(c.dev[i], slots.to(DEV), scale=c.dev_scale[i], block_scales=c.dev_blocks[i]).cpu()
+            for i in range(2)]
+    for i in range(2):
+        touched = {(t, h, d // 16) for t, h, d in bad}
+        if rot and i == 0:
+            touched |= {(t, h, (d ^ 1 if interleaved else (d + rot // 2) % rot) // 16) for t, h, d in bad}
+        for t, h, b in sorted(touched):
+            s = int(slots[t])
+            at = s // 16, h, s % 16
+            assert got[1][i][at + (b,)] & 0x7F == 0x7F
+            assert torch.all(torch.isnan(back[i][t, h, 16 * b:16 * b + 16]))
+            c.blocks[i][at + (b,)] = got[1][i][at + (b,)]
+            c.codes[i][at][8 * b:8 * b + 8] = got[0][i][at][8 * b:8 * b + 8]
+        assert int(torch.isnan(back[i]).sum()) == 16 * len(touched)
+    s = int(slots[5])
+    at = s // 16, 1, s % 16
+    assert got[1][1][at + (1,)] == 0x7E and got[0][1][at][9] & 0x0F == 0x0F  # 448, and -6
+    assert back[1][5, 1, 18] == _bf16(-np.float32(448 * 6) * np.float32(scale[1]))
+    c.blocks[1][at + (1,)], c.codes[1][at][8:16] = 0x7E, got[0][1][at][8:16]
+    c.check()
+
+
 def test_bad_slots_and_positions_are_reported():
     f, _ = fm.rotary_frequencies(64)
     table = fm.rotary_table(f, 100)
