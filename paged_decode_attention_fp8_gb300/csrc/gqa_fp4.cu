@@ -14,10 +14,10 @@
 // conversion and a multiplication for two codes, which issue at half rate, so
 // the instructions that make operands and the memory are both close to their
 // limit.  Measured (32 contexts of 1024 to 16384 keys, 8 KV heads, head_dim
-// 128, group 4): 62.7 us a call, 0.77 of the measured copy bandwidth; leaving
+// 128, group 4): 63.4 us a call, 0.77 of the measured copy bandwidth; leaving
 // the loads out would save 1.5 us, the scale multiplications 9.5, the
 // conversions of V 10.  Sixteen columns double the products and leave twelve
-// warps less to hide with: four-token blocks under a 4096-key window 46.6 us,
+// warps less to hide with: four-token blocks under a 4096-key window 46.9 us,
 // 0.45.  head_dim 64 halves the bytes of a tile but not its overhead: three
 // contexts of 50k to 131k keys 17.9 us, 0.37, of which 8 are the lengths' sums,
 // the first tiles, the merge and two launches.
