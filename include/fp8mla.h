@@ -454,12 +454,12 @@ FP8MLA_API fp8mla_status_t paged_cache_read(const void* cache, fp8mla_kv_dtype_t
  *   k_scale, v_scale  float32 [1] each (device)
  *   block_table, seqlens, spec_mask, window, sinks, out, lse  as
  *                paged_gqa_decode_ext
- *   num_splits   0 = auto: one CTA per (sequence, KV head) where the block
- *                table holds few keys (1024 with few sequences, up to 4096 as
- *                one CTA each comes to fill the GPU) or the sequences fill it
- *                many times over, else the keys of all sequences cut into
- *                equal pieces, one per CTA that fits on the GPU; 1 = one CTA
- *                each; k > 1 = every sequence in k shards, at most one per
+ *   num_splits   0 = auto: one CTA, or a cluster of two, four or eight, per
+ *                (sequence, KV head) where the block table holds few keys (from
+ *                about 1000 up with few sequences, more as they come to fill the
+ *                GPU), one CTA where the sequences fill it many times
+ *                over, else the keys of all sequences cut into equal pieces,
+ *                one per CTA that fits on the GPU; 1 = one CTA each; k > 1 = every sequence in k shards, at most one per
  *                128 keys of the block table
  *   workspace    >= paged_gqa_fp4_workspace_bytes with max_seqlen the block
  *                table's max_blocks * page_size, 256-byte aligned; may be

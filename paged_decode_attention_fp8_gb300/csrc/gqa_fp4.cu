@@ -57,6 +57,11 @@
 //     on the device only, so each CTA sums them itself.  A piece holds the end
 //     of one sequence, whole ones, and the beginning of another; whole ones are
 //     written at once, the others' partial states merged by a second kernel.
+//     Few sequences of short contexts, for which two launches are too many, go
+//     uncut, to one CTA of up to sixteen warps each or to a cluster of two to
+//     eight, whose CTAs take their tiles in turn and merge over the cluster's
+//     shared memory (one context of 777 keys, 8 KV heads: 6.7 us a call; one
+//     CTA each 8.2).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -76,6 +81,7 @@ constexpr int kTile = 16;       // keys of a tile
 constexpr int kMaxQLen = 16;
 constexpr int kMaxCols = 128;   // q_len * (h_q / h_kv)
 constexpr int kMaxLine = 1024;  // sequences whose lengths a CTA sums
+constexpr int kMaxCluster = 8;  // CTAs that share a sequence and merge in shared memory
 constexpr int kMinTiles = 8;    // places of a piece, where there are fewer than the GPU takes at once
 constexpr int kFixed = 32;      // what a sequence costs a CTA beside its tiles, in tiles: fill, drain and merge
 constexpr int kShort = 96;      // tiles up to which a sequence is not cut (200 of 94 tiles: 16.7 us, cut 18.1)
@@ -85,8 +91,8 @@ constexpr float kTau = 15.f;    // ... and moves when a score is this far above 
 // Warps of a CTA, CTAs of an SM, tiles a warp takes at a time, and stages of its ring.  Throughput: twelve warps of up
 // to 168 registers on an SM (eight at head_dim 256, twice the accumulators), in small CTAs, so that a piece's fill and
 // merge hide behind the other CTAs' loops (the 32-context batch: 8 warps x 2 CTAs 78 us, 4 x 4 70, 4 x 3 with two
-// tiles at a time 63).  kWide: an SM's warps in one CTA, for few sequences of short contexts, where a warp's few tiles
-// in a row are what takes the time.
+// tiles at a time 63).  kWide: an SM's warps in one CTA, alone or in a cluster, for few sequences of short contexts,
+// where a warp's few tiles in a row are what takes the time.
 template <int kHd, int kNT, bool kWide>
 struct Shape {
   static constexpr int kWarps = kWide ? (kHd == 256 ? 8 : (kNT == 1 ? 16 : 12)) : 4;
@@ -113,7 +119,7 @@ struct Params {
   float2* ws_ml;   // [slot][NT * 8]
   int2* ws_span;   // [bs * h_kv]: first and last piece of a (sequence, KV head) (balanced only)
   int num_blocks, max_blocks, bs, h_q, h_kv, group, q_len, window;
-  int splits;      // shards of every sequence, one CTA each (1: no merge), or 0: balanced pieces
+  int splits;      // shards of every sequence, one CTA each (1: no merge), or 0: balanced pieces; kWide: a cluster's CTAs
   int units;       // balanced: pieces there may be
   int page_shift;  // log2(page_size / 16)
   float softmax_scale;
@@ -155,10 +161,21 @@ __device__ __forceinline__ int q_exponent(float amax) {
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
-// A load that stays where it is written, before the waits that follow.
+// Loads that stay where they are written, before the waits that follow.
 __device__ __forceinline__ uint4 ldg_now(const uint4* p) {
   uint4 x;
   asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+  return x;
+}
+
+__device__ __forceinline__ int32_t ldg_now(const int32_t* p) {
+  int32_t x;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ int32_t ldg_now(const uint8_t* p) {
+  int32_t x;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(x) : "l"(p));
   return x;
 }
 
@@ -201,6 +218,9 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
   __shared__ float s_m[kWarps][kNT * 8], s_l[kWarps][kNT * 8];
   __shared__ uint4 s_q[kNT][kSteps / 2][32];  // Q's fragments of two products a lane
   __shared__ float s_cq[kNT * 8];             // score to log2 units, then a finished row's factor
+  __shared__ float s_sink[kNT * 8], s_vscale;
+  __shared__ float2 s_ml[kNT * 8];                 // this CTA's maxima and sums, for its cluster
+  __shared__ float s_weight[kMaxCluster][kNT * 8];  // what the cluster's states are multiplied by
   __shared__ int64_t s_row[kNT * 8];
   __shared__ int s_line[kMaxLine + 1];
   __shared__ int s_part[2][kWarps];
@@ -261,6 +281,10 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
     end = each * (unit + 1) + rest * (unit + 1) / pieces;
   }
 
+  // A warp's first tile of a segment, and how far it is to its next.  The CTAs of a cluster take turns.
+  const int mine = (kWide ? unit % prm.splits * kWarps : 0) * kU + warp * kU;
+  const int stride = kWarps * kU * (kWide ? prm.splits : 1);
+
   const int c_lane = lane * 16;  // this lane's bytes of a code tile
   uint32_t kdst[kCopies], vdst[kCopies];  // and where they go in a stage
   const uint32_t ring = smem_u32(smem) + warp * (kStages * kStage);
@@ -279,6 +303,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
   const int r0 = (g >> 1) + 4 * (g & 1);  // keys of fragment rows g and g + 8
   const int r1 = r0 + 8;
   const float c0 = prm.softmax_scale * kLog2e * __ldg(prm.k_scale);
+  if (kWide && threadIdx.x == 0) s_vscale = __ldg(prm.v_scale);
 
   while (cur < end) {
     // ---- the segment: tiles [t0, t1) of one (sequence, KV head)
@@ -308,46 +333,76 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
         if (first == 0) prm.ws_span[b * prm.h_kv + kvh].x = unit;
         if (last == tiles) prm.ws_span[b * prm.h_kv + kvh].y = unit;
       }
-      s_k = __ldg(prm.seqlens + b);
-      t0 = first_tile(prm, s_k) + first;
-      t1 = first_tile(prm, s_k) + last;
+      t0 = first;
+      t1 = last;
     } else {
-      const int seq = unit / prm.splits, split = unit - seq * prm.splits;
+      const int seq = unit / prm.splits;
       b = seq / prm.h_kv;
       kvh = seq - b * prm.h_kv;
-      s_k = checked_len(prm, __ldg(prm.seqlens + b));
-      const int tiles = tiles_of(prm, s_k);
-      t0 = first_tile(prm, s_k) + static_cast<int>(static_cast<long long>(split) * tiles / prm.splits);
-      t1 = first_tile(prm, s_k) + static_cast<int>(static_cast<long long>(split + 1) * tiles / prm.splits);
-      if (prm.splits > 1) slot = static_cast<long long>(blockIdx.y) * gridDim.x + unit;
+      if (!kWide && prm.splits > 1) slot = static_cast<long long>(blockIdx.y) * gridDim.x + unit;
       cur = end;
     }
+    auto lengths = [&]() {
+      if (prm.splits == 0) {
+        s_k = __ldg(prm.seqlens + b);
+        t0 += first_tile(prm, s_k);
+        t1 += first_tile(prm, s_k);
+      } else {
+        s_k = checked_len(prm, __ldg(prm.seqlens + b));
+        const int tiles = tiles_of(prm, s_k), split = kWide ? 0 : unit % prm.splits, splits = kWide ? 1 : prm.splits;
+        t0 = first_tile(prm, s_k) + static_cast<int>(static_cast<long long>(split) * tiles / splits);
+        t1 = first_tile(prm, s_k) + static_cast<int>(static_cast<long long>(split + 1) * tiles / splits);
+      }
+    };
+    const int32_t* bt_row = prm.block_table + static_cast<size_t>(b) * prm.max_blocks;
+    // Where a call's latency is what counts (kWide), what does not depend on the sequence's length is asked for before
+    // it has come: the first tiles' places in the block table (without a window they are known), Q, sinks and mask.
+    int32_t guessed = 0;
+    bool guess = false;
+    if constexpr (kWide) {
+      guess = prm.window == 0;
+      const int at = (lane / kU * stride + mine + lane % kU) >> prm.page_shift;
+      if (guess && at < prm.max_blocks) guessed = ldg_now(bt_row + at);
+    } else {
+      lengths();
+    }
+    // Q's values: lane (g, t) of warp n takes dims [t hd/4, (t + 1) hd/4) of column 8 n + g; and the column's sink
+    uint4 qx[kSteps / 2];
+    float sink = kNegInf;
+    if (warp < kNT) {
+      const int c = warp * 8 + g, col = col0 + c, token = col / prm.group, hq = kvh * prm.group + col - token * prm.group;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          prm.q + ((static_cast<size_t>(b) * prm.q_len + token) * prm.h_q + hq) * kHd + t * (kHd / 4));
+#pragma unroll
+      for (int j = 0; j < kSteps / 2; ++j) qx[j] = c < ncols ? ldg_now(src + j) : make_uint4(0, 0, 0, 0);
+      if (kWide && prm.sinks != nullptr && c < ncols) sink = __int_as_float(ldg_now(reinterpret_cast<const int32_t*>(prm.sinks) + hq));
+    }
+    // The speculative block's mask, by the last warp: lane (r, c) of half-warp r takes byte c of rows r, r + 2, ...
+    int32_t seen[kMaxQLen / 2];
+    auto ask_mask = [&]() {
+      const uint8_t* rows = prm.spec_mask + static_cast<size_t>(b) * prm.q_len * prm.q_len;
+#pragma unroll
+      for (int i = 0; i < kMaxQLen / 2; ++i) {
+        const int r = 2 * i + lane / 16, c = lane % 16;
+        seen[i] = r < prm.q_len && c < prm.q_len ? ldg_now(rows + r * prm.q_len + c) : 0;
+      }
+    };
+    if (kWide && prm.spec_mask != nullptr && warp == kWarps - 1) ask_mask();
+    if constexpr (kWide) lengths();
     const int start = s_k - prm.q_len;  // position of the block's first token
     const int tok_lo = prm.q_len > 1 ? col0 / prm.group : 0;  // the first token of this CTA's columns
     const int k_lo = prm.window > 0 ? max(0, start + tok_lo - prm.window + 1) : 0;
-    const int mine0 = t0 + warp * kU;  // this warp's tiles: kU from here, kU more kWarps * kU later, ...
-    const int n_mine = t1 > mine0 ? (t1 - mine0 + kWarps * kU - 1) / (kWarps * kU) : 0;
-    const int32_t* bt_row = prm.block_table + static_cast<size_t>(b) * prm.max_blocks;
-
-    // Q's values are asked for first: lane (g, t) of warp n takes dims [t hd/4, (t + 1) hd/4) of column 8 n + g
-    uint4 qx[kSteps / 2];
-    if (warp < kNT) {
-      const int c = warp * 8 + g, col = col0 + c, token = col / prm.group;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          prm.q + ((static_cast<size_t>(b) * prm.q_len + token) * prm.h_q + kvh * prm.group + col - token * prm.group) *
-                      kHd + t * (kHd / 4));
-#pragma unroll
-      for (int j = 0; j < kSteps / 2; ++j) qx[j] = c < ncols ? ldg_now(src + j) : make_uint4(0, 0, 0, 0);
-    }
+    const int mine0 = t0 + mine;  // this warp's tiles: kU from here, kU more `stride` later, ...
+    const int n_mine = t1 > mine0 ? (t1 - mine0 + stride - 1) / stride : 0;
 
     // Entries of the block table (as the tile's first row in the cache), 32 tiles of this warp at a time.
     uint32_t entry = 0;
     const uint32_t block_rows = prm.h_kv * page;
-    auto fetch_entries = [&](int i0) {
-      const int tile = mine0 + (i0 + lane / kU) * (kWarps * kU) + lane % kU;
+    auto fetch_entries = [&](int i0, auto first) {
+      const int tile = mine0 + (i0 + lane / kU) * stride + lane % kU;
       entry = 0;
       if (tile < t1) {
-        int blk = __ldg(bt_row + (tile >> prm.page_shift));
+        int blk = decltype(first)::value && guess ? guessed : __ldg(bt_row + (tile >> prm.page_shift));
         if (blk < 0 || blk >= prm.num_blocks) {
           atomicOr(&g_status_fp4, FP8MLA_DEV_BAD_PAGE);
           blk = 0;
@@ -356,13 +411,13 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
       }
     };
     uint32_t put = ring;  // the stage that is filled next
-    auto issue = [&](int i) {
+    auto issue = [&](int i, auto first) {
       if (i < n_mine) {
-        if (i % (32 / kU) == 0) fetch_entries(i);
+        if (i % (32 / kU) == 0) fetch_entries(i, first);
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const uint32_t row = __shfl_sync(0xffffffffu, entry, i % (32 / kU) * kU + u);
-          if (u > 0 && mine0 + i * (kWarps * kU) + u >= t1) break;  // past the segment's end: an old tile stays there
+          if (u > 0 && mine0 + i * stride + u >= t1) break;  // past the segment's end: an old tile stays there
           const uint8_t* ksrc = k_base + static_cast<uint64_t>(row) * L::kRow;
           const uint8_t* vsrc = v_base + static_cast<uint64_t>(row) * L::kRow;
 #pragma unroll
@@ -379,30 +434,29 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
       cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    for (int i = 0; i < kStages - 1; ++i) issue(i, std::true_type{});
 
-    // Which keys of the speculative block its token i sees: its mask row, or those up to itself.
-    if (threadIdx.x < prm.q_len) {
-      uint32_t bits = 0;
-      if (prm.spec_mask != nullptr) {
-        const uint8_t* row = prm.spec_mask + (static_cast<size_t>(b) * prm.q_len + threadIdx.x) * prm.q_len;
-        for (int c = 0; c < prm.q_len; ++c)
-          if (__ldg(row + c)) bits |= 1u << c;
-      } else {
-        bits = (2u << threadIdx.x) - 1u;
-      }
-      s_vis[threadIdx.x] = bits;
-    }
-    if (warp == 0) {  // which keys of the block any of those tokens sees
-      __syncwarp();
-      uint32_t any = s_vis[tok_lo];
-      if (prm.q_len > 1) {
-        any = 0;
-        for (int i = tok_lo; i <= (col0 + ncols - 1) / prm.group; ++i) {
-          const uint32_t near = prm.window == 0 || i < prm.window ? ~0u : ~0u << (i - prm.window + 1);
-          any |= s_vis[i] & near;
+    // Which keys of the speculative block its token i sees: its mask row, or those up to itself; and which keys any
+    // token of this CTA's columns sees.
+    if (warp == kWarps - 1) {
+      uint32_t bits = (2u << lane) - 1u;
+      if (!kWide && prm.spec_mask != nullptr) {
+        const uint8_t* row = prm.spec_mask + (static_cast<size_t>(b) * prm.q_len + lane) * prm.q_len;
+        bits = 0;
+        if (lane < prm.q_len)
+          for (int c = 0; c < prm.q_len; ++c)
+            if (__ldg(row + c)) bits |= 1u << c;
+      } else if (prm.spec_mask != nullptr) {
+#pragma unroll
+        for (int i = 0; i < kMaxQLen / 2; ++i) {
+          const uint32_t two = __ballot_sync(0xffffffffu, seen[i] != 0);
+          if (lane / 2 == i) bits = lane & 1 ? two >> 16 : two & 0xFFFFu;
         }
       }
+      if (lane < prm.q_len) s_vis[lane] = bits;
+      const uint32_t near = prm.window == 0 || lane < prm.window ? ~0u : ~0u << (lane - prm.window + 1);
+      const bool ours = lane >= tok_lo && lane <= (col0 + ncols - 1) / prm.group;
+      const uint32_t any = __reduce_or_sync(0xffffffffu, ours ? bits & near : 0u);
       if (lane == 0) s_any = any;
     }
     if (warp < kNT) {  // Q's fragments, as f16 with a power of two out
@@ -422,7 +476,10 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
 #pragma unroll
       for (int j = 0; j < kSteps / 2; ++j)
         s_q[warp][j][lane] = make_uint4(scaled(qx[j].x), scaled(qx[j].y), scaled(qx[j].z), scaled(qx[j].w));
-      if (t == 0) s_cq[warp * 8 + g] = c0 * exp2i(e);
+      if (t == 0) {
+        s_cq[warp * 8 + g] = c0 * exp2i(e);
+        if (kWide) s_sink[warp * 8 + g] = sink;
+      }
     }
     __syncthreads();  // s_vis, s_q, s_cq
     float cq[kNT][2];
@@ -677,12 +734,12 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
       }
       st += kStage;
       if (st == st_end) st -= kStages * kStage;
-      tok0 += kWarps * kU * kTile;
+      tok0 += stride * kTile;
     };
     for (int i = 0; i < n_mine; ++i) {
       cp_async_wait_group<kStages - 2>();
       __syncwarp();
-      issue(i + kStages - 1);
+      issue(i + kStages - 1, std::false_type{});
       if (tok0 + kU * kTile <= full_end && tok0 >= full_lo) tiles(std::false_type{});
       else tiles(std::true_type{});
     }
@@ -729,28 +786,22 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
         sum += s_m[w][c] == kNegInf ? 0.f : s_l[w][c] * ex2_approx(s_m[w][c] - (mx == kNegInf ? 0.f : mx));
       if (slot >= 0) {
         prm.ws_ml[slot * (kNT * 8) + c] = make_float2(mx, sum);
+      } else if (kWide && prm.splits > 1) {
+        s_ml[c] = make_float2(mx, sum);
       } else if (c < ncols) {
         const int col = col0 + c, token = col / prm.group, hq = kvh * prm.group + col - token * prm.group;
         const int64_t row = (static_cast<int64_t>(b) * prm.q_len + token) * prm.h_q + hq;
         float fac, lse;
-        finish(mx, sum, prm.sinks ? __ldg(prm.sinks + hq) : kNegInf, __ldg(prm.v_scale), &fac, &lse);
+        const float sk = kWide ? s_sink[c] : (prm.sinks ? __ldg(prm.sinks + hq) : kNegInf);
+        finish(mx, sum, sk, kWide ? s_vscale : __ldg(prm.v_scale), &fac, &lse);
         s_cq[c] = fac;
         s_row[c] = row;
         prm.lse[row] = lse;
       }
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < kNT * kSteps * 32; x += kWarps * 32) {
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 y = part[w * (kNT * kSteps * 32) + x];
-        a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
-      }
-      if (slot >= 0) {
-        prm.ws_o[slot * (kNT * kSteps * 32) + x] = a;
-        continue;
-      }
+    constexpr int kFrag = kNT * kSteps * 32;
+    auto write = [&](int x, const float4& a) {  // the finished fragment x
       const int n = x / (kSteps * 32), j = x / 32 % kSteps, c = n * 8 + 2 * (x % 4);
       const int d = x % 32 / 4 * (kHd / 8) + 2 * j;
       if (c < ncols)
@@ -758,6 +809,69 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
       if (c + 1 < ncols)
         *reinterpret_cast<uint32_t*>(prm.out + s_row[c + 1] * kHd + d) =
             pack_bf16x2(a.y * s_cq[c + 1], a.w * s_cq[c + 1]);
+    };
+    for (int x = threadIdx.x; x < kFrag; x += kWarps * 32) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 y = part[w * kFrag + x];
+        a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
+      }
+      if (slot >= 0) prm.ws_o[slot * kFrag + x] = a;
+      else if (kWide && prm.splits > 1) part[x] = a;  // (the only thread that reads the others of x)
+      else write(x, a);
+    }
+    if (kWide && prm.splits > 1) {
+      // The cluster's states, in the order of its CTAs: every CTA works out the weights, and merges its share of the
+      // fragments.  (Fetching those beside the weights cost the loop registers: 7.1 us instead of 6.7 for one context.)
+      cluster_sync();
+      const int rank = unit % prm.splits, share = kFrag / prm.splits;
+      if (threadIdx.x < kNT * 8) {
+        const int c = threadIdx.x;
+        float2 ml[kMaxCluster];
+        float mx = kNegInf, sum = 0.f;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          ml[r] = make_float2(kNegInf, 0.f);
+          if (r < prm.splits) ml[r] = ld_cluster(&s_ml[c], r);
+        }
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) mx = fmaxf(mx, ml[r].x);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          const float weight = ml[r].x == kNegInf ? 0.f : ex2_approx(ml[r].x - (mx == kNegInf ? 0.f : mx));
+          s_weight[r][c] = weight;
+          sum += ml[r].y * weight;
+        }
+        if (c < ncols) {
+          const int col = col0 + c, token = col / prm.group, hq = kvh * prm.group + col - token * prm.group;
+          const int64_t row = (static_cast<int64_t>(b) * prm.q_len + token) * prm.h_q + hq;
+          float fac, lse;
+          finish(mx, sum, s_sink[c], s_vscale, &fac, &lse);
+          s_cq[c] = fac;
+          s_row[c] = row;
+          if (rank == 0) prm.lse[row] = lse;
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < share; i += kWarps * 32) {
+        const int x = rank * share + i, c = x / (kSteps * 32) * 8 + 2 * (x % 4);
+        float4 y[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          y[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r < prm.splits) y[r] = ld_cluster(&part[x], r);
+        }
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          const float w0 = s_weight[r][c], w1 = s_weight[r][c + 1];
+          a.x += y[r].x * w0, a.y += y[r].y * w1, a.z += y[r].z * w0, a.w += y[r].w * w1;
+        }
+        write(x, a);
+      }
+      __syncwarp();
+      cluster_sync();  // until its last reader, a CTA's shared memory stays
     }
     __syncthreads();  // the ring is free for the next segment's copies
   }
@@ -797,6 +911,11 @@ __global__ void __launch_bounds__(kGroups == 1 ? 128 : kGroups * 32) fp4_combine
     count = prm.splits;
   }
   const int b = seq / prm.h_kv, kvh = seq % prm.h_kv;
+  const float v_scale = __ldg(prm.v_scale);
+  float sink[2] = {kNegInf, kNegInf};
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (prm.sinks != nullptr && c + k < ncols) sink[k] = __ldg(prm.sinks + kvh * prm.group + (col0 + c + k) % prm.group);
   float m0 = kNegInf, m1 = kNegInf, l0 = 0.f, l1 = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = group; s0 < count; s0 += 4 * kGroups) {  // four shards' loads in flight
@@ -851,14 +970,13 @@ __global__ void __launch_bounds__(kGroups == 1 ? 128 : kGroups * 32) fp4_combine
       a.x += y.x * w0, a.y += y.y * w1, a.z += y.z * w0, a.w += y.w * w1;
     }
   }
-  const float v_scale = __ldg(prm.v_scale);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (c + k >= ncols) continue;
     const int col = col0 + c + k, hq = kvh * prm.group + col % prm.group;
     const size_t row = (static_cast<size_t>(b) * prm.q_len + col / prm.group) * prm.h_q + hq;
     float fac, lse;
-    finish(k ? m1 : m0, k ? l1 : l0, prm.sinks ? prm.sinks[hq] : kNegInf, v_scale, &fac, &lse);
+    finish(k ? m1 : m0, k ? l1 : l0, sink[k], v_scale, &fac, &lse);
     *reinterpret_cast<uint32_t*>(prm.out + row * kHd + lane / 4 * (kHd / 8) + 2 * j) =
         pack_bf16x2((k ? a.y : a.x) * fac, (k ? a.w : a.z) * fac);
     if (j == 0 && lane < 4) prm.lse[row] = lse;
@@ -874,10 +992,11 @@ int col_tiles(int cols, int* nt) {  // columns run eight or sixteen to a CTA
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// How a call is laid out: shards of every sequence (1: none, 0: balanced pieces), pieces, and the workspace.
+// How a call is laid out: shards of every sequence (1: none, 0: balanced pieces; wide: CTAs of its cluster), pieces, and
+// the workspace.
 struct Plan {
   int nt, ct, splits, units;
-  bool wide;
+  bool wide;    // an SM's warps in one CTA, `splits` of them in a cluster for a sequence
   size_t slots, ml, span, bytes;  // partial states, and where (m, l) and the spans of pieces begin
 };
 
@@ -895,26 +1014,38 @@ Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long cap
   const int resident = device_sms() * (head_dim == 256 ? 2 : 3);  // Shape::kPerSm
   p.units = 0;
   p.wide = false;
-  // A wide CTA has an SM of its own; cutting gains by the SMs that would otherwise idle.  With next to all of them idle
-  // it pays from three or four tiles a warp on (8 sequences of 49 tiles: 8.7 us uncut and cut, of 69 tiles 10.0 and
-  // 8.8; sixteen columns, 4 of 25 tiles 9.3 and 9.6, of 47 tiles 10.4 and 9.7; head_dim 256, 8 of 38 tiles 10.0, 8.9).
-  const long long sms = device_sms();
-  const bool few = seqs * p.ct <= sms;
-  const int wide_tiles = head_dim == 256 ? 24 : (p.nt == 1 ? 64 : 36);
-  const long long short_few = few ? std::min<long long>(256, wide_tiles * sms / (sms - 3 * seqs * p.ct / 4)) : 0;
+  // Few sequences: an SM's warps in one CTA, and CTAs in a cluster, which merges without a second kernel, as far as
+  // clusters of that size fit on the GPU at once (eight CTAs 15 times, four 36 times).  A cluster's merge takes 1.4 us,
+  // so short contexts stay with one CTA (8 sequences of 25 tiles: 6.3 us, in clusters of eight 7.1; of 50 tiles 7.7 and
+  // 7.1; sixteen columns, of 50 tiles 10.5 and 8.6).
+  const long long sms = device_sms(), ctas = seqs * p.ct;
+  const bool few = ctas <= sms;
+  const int cluster = ctas * 12 <= sms ? 8 : (ctas * 19 <= sms * 4 ? 4 : (ctas * 19 <= sms * 9 ? 2 : 1));
+  const int alone = (head_dim == 64 ? 56 : (head_dim == 256 ? 20 : (p.nt == 1 ? 36 : 24))) * (cluster > 2 ? 4 : 7) / 4;
+  // Cutting into pieces gains by the SMs that would otherwise idle and by equal shares, and pays for the second kernel:
+  // with clusters from about three tiles for each of their CTAs on (hd 128, eight columns: 2 x 8 CTAs 50 tiles 6.9 us
+  // and cut 8.4, 100 tiles 7.2 and 7.0; 8 x 8 CTAs 100 tiles 7.2 and 7.8, 400 tiles 10.1 and 8.6; 32 x 4 CTAs 200
+  // tiles 9.9 and 11.5, 400 tiles 13.4 and 13.4); without, where 36 % to 100 % of the SMs have a CTA, from 64 tiles up
+  // to four times as many.
+  long long uncut = kShort;
+  if (few && cluster == 1)
+    uncut = std::min<long long>(256, (head_dim == 256 ? 24 : (p.nt == 1 ? 64 : 36)) * sms / (sms - 3 * ctas / 4));
+  else if (few)
+    uncut = 24 + ctas * cluster * (head_dim == 256 ? 4 : (p.nt == 1 ? 6 : 3)) / 2;
   if (num_splits > 0) {
     p.splits = static_cast<int>(std::min<long long>(num_splits, std::max(1LL, (tiles + 7) / 8)));
-  } else if (tiles <= (few ? short_few : kShort) || seqs * p.ct >= 8LL * resident || bs > kMaxLine ||
+  } else if (tiles <= uncut || ctas >= 8LL * resident || bs > kMaxLine ||
              seqs * (tiles + kFixed) > 0x7FFFFFFFll) {
-    // Short contexts: one CTA a sequence takes no longer than a piece and its merge.  Many sequences: their CTAs
-    // balance by themselves.  (The line's places are counted in 32 bits.)
+    // Short contexts: one CTA or cluster a sequence takes no longer than pieces and their merge.  Many sequences: their
+    // CTAs balance by themselves.  (The line's places are counted in 32 bits.)
     p.splits = 1;
     p.wide = few && tiles > 4;
+    if (p.wide && tiles > alone) p.splits = cluster;
   } else {
     p.splits = 0;
     p.units = std::max(1, resident / p.ct);
   }
-  p.slots = p.splits == 1 ? 0 : static_cast<size_t>(p.ct) * (p.splits == 0 ? 2 * p.units : seqs * p.splits);
+  p.slots = p.splits == 1 || p.wide ? 0 : static_cast<size_t>(p.ct) * (p.splits == 0 ? 2 * p.units : seqs * p.splits);
   p.ml = round_up(p.slots * p.nt * 8 * head_dim * sizeof(float), 256);
   p.span = p.ml + round_up(p.slots * p.nt * 8 * sizeof(float2), 256);
   p.bytes = p.span + (p.splits == 0 ? round_up(static_cast<size_t>(seqs) * sizeof(int2), 256) : 0);
@@ -942,6 +1073,9 @@ cudaError_t launch_decode(const Params& prm, int seqs, int ct, cudaStream_t stre
   if (e != cudaSuccess) return e;
   const unsigned grid = prm.splits == 0 ? static_cast<unsigned>(prm.units)
                                         : static_cast<unsigned>(seqs) * static_cast<unsigned>(prm.splits);
+  if (kWide && prm.splits > 1)
+    return launch_dependent_clusters(prm.splits, fp4_decode_kernel<kHd, kNT, kWide>, dim3(grid, ct),
+                                     dim3(S::kWarps * 32), smem, stream, prm);
   return launch_dependent(fp4_decode_kernel<kHd, kNT, kWide>, dim3(grid, ct), dim3(S::kWarps * 32), smem, stream, prm);
 }
 
@@ -949,7 +1083,7 @@ template <int kHd, int kNT>
 cudaError_t launch(const Params& prm, bool wide, int seqs, int ct, cudaStream_t stream) {
   const cudaError_t e = wide ? launch_decode<kHd, kNT, true>(prm, seqs, ct, stream)
                              : launch_decode<kHd, kNT, false>(prm, seqs, ct, stream);
-  if (e != cudaSuccess || prm.splits == 1) return e;
+  if (e != cudaSuccess || prm.splits == 1 || wide) return e;
   // warps for the shards that a sequence has on average, four at a time each (100 sequences cut into 5: 19.4 us a call
   // with one warp, 25.3 with sixteen, most of them idle; 6 cut into 76: 17.9 with sixteen, 20.9 with four)
   constexpr unsigned kFrags = kNT * (kHd / 16);

@@ -306,6 +306,34 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   return r;
 }
 
+// Thread-block clusters: a barrier of all their threads (shared-memory writes
+// before it are seen after it), and a read of the place that `p` has in the
+// shared memory of the CTA of rank `rank`.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster(const float4* p, uint32_t rank) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(cluster_address(p, rank))
+               : "memory");
+  return x;
+}
+__device__ __forceinline__ float2 ld_cluster(const float2* p, uint32_t rank) {
+  float2 x;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(x.x), "=f"(x.y)
+               : "r"(cluster_address(p, rank))
+               : "memory");
+  return x;
+}
+
 // Two floats -> two E4M3 bytes (round to nearest even, saturate to +-448); lo in the low byte.
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   uint16_t r;

@@ -207,9 +207,38 @@ def test_hidden_keys_may_hold_anything():
 def test_balanced_pieces_with_options(q_len, group, mask, window, sinks):
     """Contexts long and unequal enough that the keys are cut on the device, at cuts of its own choosing."""
     x = Inputs(30 + q_len + window, [5000, 0, 3, 1700, 2900, 17], 2, group, 64, 16, q_len, mask, sinks)
-    assert fm.gqa_fp4_workspace_bytes(6, 2 * group, 2, 64, x.bt.shape[1] * 16, q_len, window) > 0 or \
-        window == 100  # which leaves nothing to cut
+    # (these windows leave so little that clusters take the sequences uncut)
+    assert (fm.gqa_fp4_workspace_bytes(6, 2 * group, 2, 64, x.bt.shape[1] * 16, q_len, window) > 0) == (window == 0)
     x.check(*x.run(window=window), window=window)
+
+
+@pytest.mark.parametrize("q_len,group,mask,window,sinks", [(4, 4, True, 4100, True), (3, 7, False, 5000, False)])
+def test_balanced_pieces_with_windows(q_len, group, mask, window, sinks):
+    x = Inputs(35 + q_len, [9000, 0, 3, 4700, 2900, 17], 2, group, 64, 16, q_len, mask, sinks)
+    assert fm.gqa_fp4_workspace_bytes(6, 2 * group, 2, 64, x.bt.shape[1] * 16, q_len, window) > 0
+    x.check(*x.run(window=window), window=window)
+
+
+# Sequences in clusters of eight, four and two CTAs: (sequences, KV heads) give the size.
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("bs,h_kv", [(5, 2), (7, 4), (14, 5)])
+@pytest.mark.parametrize("q_len,group,mask,window,sinks", [(1, 5, False, 0, True), (1, 16, False, 900, False),
+                                                           (4, 3, True, 0, False), (5, 2, True, 700, True)])
+def test_clusters(hd, bs, h_kv, q_len, group, mask, window, sinks):
+    """Contexts of none, of fewer tiles than a cluster has warps, on and off its last tile, and of several rounds."""
+    lens = ([1600, 0, 1, 17, 1025] + [33 * i for i in range(20)])[:bs]
+    x = Inputs(200 + hd + bs + q_len + group, lens, h_kv, group, hd, 16, q_len, mask, sinks)
+    assert fm.gqa_fp4_workspace_bytes(bs, h_kv * group, h_kv, hd, x.bt.shape[1] * 16, q_len, window) == 0
+    rows = [(b, h) for b in range(5) for h in (0, h_kv * group - 1)] + [(bs - 1, group)]
+    out, lse = x.run(window=window)
+    x.check(out, lse, window=window, rows=rows)
+    one, lse1 = x.run(window=window, num_splits=1)  # the same sums in another order
+    live = torch.isfinite(lse1)
+    assert torch.equal(live, torch.isfinite(lse))
+    assert torch.all((lse[live] - lse1[live]).abs() <= 2.0 ** -16)
+    assert torch.all((out - one).abs().float() <= 2.0 ** -7 * one.abs().float() + 2.0 ** -9)
+    again, lse2 = x.run(window=window)
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
 
 
 @pytest.mark.parametrize("bs", [31, 128, 129, 700, 1024, 1025])

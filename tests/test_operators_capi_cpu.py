@@ -134,8 +134,9 @@ def test_workspace_of_each_layout():
     size = fm.gqa_fp4_workspace_bytes
     slot = 8 * 128 * 4 + 8 * 8  # eight columns of 128 floats and a pair of floats each
     assert size(3, 8, 2, 128, 4096, num_splits=1) == 0
-    # short contexts: one CTA each, longer ones where those come to fill the GPU (152 SMs here)
-    assert size(3, 8, 2, 128, 1040) == 0 < size(3, 8, 2, 128, 1056)
+    # short contexts: one CTA or one cluster each, longer ones where those come to fill the GPU (152 SMs here)
+    assert size(3, 8, 2, 128, 2688) == 0 < size(3, 8, 2, 128, 2704)
+    assert size(30, 8, 2, 128, 6144) == 0 < size(30, 8, 2, 128, 6160)
     assert size(50, 8, 2, 128, 2016) == 0 < size(50, 8, 2, 128, 2032)
     assert size(100, 8, 2, 128, 1536) == 0 < size(100, 8, 2, 128, 1552)
     assert size(2000, 8, 2, 128, 8192) == 0                 # more sequences than a CTA sums
