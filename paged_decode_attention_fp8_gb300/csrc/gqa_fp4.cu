@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
   __shared__ float2 s_ml[kNT * 8];                 // this CTA's maxima and sums, for its cluster
   __shared__ float s_weight[kMaxCluster][kNT * 8];  // what the cluster's states are multiplied by
   __shared__ int64_t s_row[kNT * 8];
+  __shared__ int s_tok[kNT * 8];              // a column's token
   __shared__ int s_line[kMaxLine + 1];
   __shared__ int s_part[2][kWarps];
 
@@ -478,6 +479,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
         s_q[warp][j][lane] = make_uint4(scaled(qx[j].x), scaled(qx[j].y), scaled(qx[j].z), scaled(qx[j].w));
       if (t == 0) {
         s_cq[warp * 8 + g] = c0 * exp2i(e);
+        s_tok[warp * 8 + g] = min((col0 + warp * 8 + g) / prm.group, prm.q_len - 1);
         if (kWide) s_sink[warp * 8 + g] = sink;
       }
     }
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
     };
 
     auto sees = [&](int p, int c) {  // whether key p is for column c
-      const int ti = min((col0 + c) / prm.group, prm.q_len - 1);
+      const int ti = s_tok[c];
       const int c_blk = p - start;
       return p < keys_end && (c_blk < 0 || ((s_vis[ti] >> c_blk) & 1u)) && (prm.window == 0 || ti - c_blk < prm.window);
     };
@@ -1005,7 +1007,8 @@ int seen_window(int window, long long capacity) { return window >= capacity ? 0 
 
 Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long capacity, int window, int num_splits) {
   Plan p;
-  p.ct = col_tiles(q_len * (h_q / h_kv), &p.nt);
+  const int cols = q_len * (h_q / h_kv);
+  p.ct = col_tiles(cols, &p.nt);
   long long longest = std::max(capacity, 1LL);
   window = seen_window(window, capacity);
   if (window > 0) longest = std::min(longest, static_cast<long long>(window) + q_len - 1 + kTile);
@@ -1018,20 +1021,41 @@ Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long cap
   // clusters of that size fit on the GPU at once (eight CTAs 15 times, four 36 times).  A cluster's merge takes 1.4 us,
   // so short contexts stay with one CTA (8 sequences of 25 tiles: 6.3 us, in clusters of eight 7.1; of 50 tiles 7.7 and
   // 7.1; sixteen columns, of 50 tiles 10.5 and 8.6).
-  const long long sms = device_sms(), ctas = seqs * p.ct;
-  const bool few = ctas <= sms;
-  const int cluster = ctas * 12 <= sms ? 8 : (ctas * 19 <= sms * 4 ? 4 : (ctas * 19 <= sms * 9 ? 2 : 1));
-  const int alone = (head_dim == 64 ? 56 : (head_dim == 256 ? 20 : (p.nt == 1 ? 36 : 24))) * (cluster > 2 ? 4 : 7) / 4;
   // Cutting into pieces gains by the SMs that would otherwise idle and by equal shares, and pays for the second kernel:
   // with clusters from about three tiles for each of their CTAs on (hd 128, eight columns: 2 x 8 CTAs 50 tiles 6.9 us
   // and cut 8.4, 100 tiles 7.2 and 7.0; 8 x 8 CTAs 100 tiles 7.2 and 7.8, 400 tiles 10.1 and 8.6; 32 x 4 CTAs 200
   // tiles 9.9 and 11.5, 400 tiles 13.4 and 13.4); without, where 36 % to 100 % of the SMs have a CTA, from 64 tiles up
   // to four times as many.
-  long long uncut = kShort;
-  if (few && cluster == 1)
-    uncut = std::min<long long>(256, (head_dim == 256 ? 24 : (p.nt == 1 ? 64 : 36)) * sms / (sms - 3 * ctas / 4));
-  else if (few)
-    uncut = 24 + ctas * cluster * (head_dim == 256 ? 4 : (p.nt == 1 ? 6 : 3)) / 2;
+  const long long sms = device_sms();
+  long long ctas, uncut;
+  int cluster, alone;
+  bool few;
+  auto lay_out = [&] {
+    ctas = seqs * p.ct;
+    few = ctas <= sms;
+    cluster = ctas * 12 <= sms ? 8 : (ctas * 19 <= sms * 4 ? 4 : (ctas * 19 <= sms * 9 ? 2 : 1));
+    alone = (head_dim == 64 ? 56 : (head_dim == 256 ? 20 : (p.nt == 1 ? 36 : 24))) * (cluster > 2 ? 4 : 7) / 4;
+    if (!few)
+      uncut = kShort;
+    else if (cluster == 1)
+      uncut = std::min<long long>(256, (head_dim == 256 ? 24 : (p.nt == 1 ? 64 : 36)) * sms / (sms - 3 * ctas / 4));
+    else
+      uncut = 24 + ctas * cluster * (head_dim == 256 ? 4 : (p.nt == 1 ? 6 : 3)) / 2;
+  };
+  lay_out();
+  if (p.nt == 2 && num_splits == 0 && seqs * ((cols + 7) / 8) <= sms) {
+    // SMs to spare: eight columns a CTA, whose keys come from L2 the second time (8 x 16 columns of 25 tiles 8.4 us, in
+    // eights 7.1, of 100 tiles 9.6 and 8.4, of 200 tiles 10.0 and 10.4; 32 x 16 of 25 tiles 8.5 and 7.2, of 100 tiles
+    // 10.9 and 10.6, of 200 tiles 13.0 and 13.7)
+    const Plan sixteen = p;
+    p.nt = 1;
+    p.ct = (cols + 7) / 8;
+    lay_out();
+    if (tiles > std::min(uncut, 150LL)) {
+      p = sixteen;
+      lay_out();
+    }
+  }
   if (num_splits > 0) {
     p.splits = static_cast<int>(std::min<long long>(num_splits, std::max(1LL, (tiles + 7) / 8)));
   } else if (tiles <= uncut || ctas >= 8LL * resident || bs > kMaxLine ||

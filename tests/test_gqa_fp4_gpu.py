@@ -212,7 +212,7 @@ def test_balanced_pieces_with_options(q_len, group, mask, window, sinks):
     x.check(*x.run(window=window), window=window)
 
 
-@pytest.mark.parametrize("q_len,group,mask,window,sinks", [(4, 4, True, 4100, True), (3, 7, False, 5000, False)])
+@pytest.mark.parametrize("q_len,group,mask,window,sinks", [(4, 4, True, 8100, True), (3, 7, False, 5000, False)])
 def test_balanced_pieces_with_windows(q_len, group, mask, window, sinks):
     x = Inputs(35 + q_len, [9000, 0, 3, 4700, 2900, 17], 2, group, 64, 16, q_len, mask, sinks)
     assert fm.gqa_fp4_workspace_bytes(6, 2 * group, 2, 64, x.bt.shape[1] * 16, q_len, window) > 0
@@ -239,6 +239,20 @@ def test_clusters(hd, bs, h_kv, q_len, group, mask, window, sinks):
     assert torch.all((out - one).abs().float() <= 2.0 ** -7 * one.abs().float() + 2.0 ** -9)
     again, lse2 = x.run(window=window)
     assert torch.equal(again, out) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("bs", [6, 16, 30])
+def test_clusters_of_sixteen_columns(hd, bs):
+    """Contexts too long for tiles of eight columns and too short to be cut: clusters of eight, four and two CTAs."""
+    x = Inputs(300 + hd + bs, ([2500, 0, 15, 2065] + [33 * i for i in range(30)])[:bs], 2, 4, hd, 16, 4, mask=True)
+    assert fm.gqa_fp4_workspace_bytes(bs, 8, 2, hd, x.bt.shape[1] * 16, 4) == 0
+    out, lse = x.run()
+    x.check(out, lse, rows=[(b, h) for b in range(4) for h in (0, 5)] + [(bs - 1, 7)])
+    one, lse1 = x.run(num_splits=1)  # the same sums in another order
+    live = torch.isfinite(lse1)
+    assert torch.equal(live, torch.isfinite(lse)) and torch.all((lse[live] - lse1[live]).abs() <= 2.0 ** -16)
+    assert torch.all((out - one).abs().float() <= 2.0 ** -7 * one.abs().float() + 2.0 ** -9)
 
 
 @pytest.mark.parametrize("bs", [31, 128, 129, 700, 1024, 1025])
