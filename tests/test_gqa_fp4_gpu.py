@@ -362,11 +362,12 @@ def test_served_batch_sampled():
     assert torch.equal(out, moved) and torch.equal(lse, lse3)
 
 
+@pytest.mark.parametrize("window", [33, 900])
 @pytest.mark.parametrize("hd,q_len,group", [(64, 4, 2), (64, 4, 5), (128, 4, 2), (128, 6, 8), (256, 3, 2), (256, 16, 4)])
-def test_a_nan_value_stays_with_the_tokens_that_see_it(hd, q_len, group):
+def test_a_nan_value_stays_with_the_tokens_that_see_it(hd, q_len, group, window):
     """A NaN V scale on the block's last key, which the last token alone sees, and on the key that the window leaves to
     the first token alone: those tokens' 16 dims are NaN and nothing else changes by a bit."""
-    lens, window = [700, 40, 2000], 33
+    lens = [700, 40, 2000]
     x = Inputs(80 + hd + q_len, lens, 2, group, hd, 32, q_len)
     for splits in (0, 1, 2):
         want, want_lse = x.run(window=window, num_splits=splits)
@@ -385,10 +386,10 @@ def test_a_nan_value_stays_with_the_tokens_that_see_it(hd, q_len, group):
     assert fm.last_device_error() == 0
 
 
-@pytest.mark.parametrize("lens", [[50, 300, 20], [2000, 3000, 700]])
+@pytest.mark.parametrize("lens", [[50, 300, 20], [2000, 3000, 700], [900, 1300, 700]])
 def test_nan_propagates_to_what_it_touches(lens):
     """A NaN query value: its row alone.  A NaN K scale on a visible key: every row of that KV head that sees it.  A NaN
-    V scale: those rows' 16 dims alone, not the LSE.  Direct, cut and balanced."""
+    V scale: those rows' 16 dims alone, not the LSE.  Direct, cut, balanced and in clusters."""
     x = Inputs(70, lens, 2, 4, 128, 16)
     for splits in (0, 1, 2):
         want, want_lse = x.run(num_splits=splits)
@@ -434,6 +435,55 @@ def test_bad_pages_and_lengths_are_reported():
         assert fm.last_device_error() == fm.DEV_BAD_SEQLEN
         assert torch.all(out[1] == 0) and torch.all(torch.isneginf(lse[1]))
         assert torch.equal(out[0], good[0])
+
+
+def test_clusters_report_replay_and_overlap():
+    """Errors of one sequence leave the others alone, entries past a sequence's end are not looked at; a captured call
+    follows its lengths; two calls at once."""
+    x = Inputs(19, [900, 400, 16], 2, 4, 128, 16)
+    assert fm.gqa_fp4_workspace_bytes(3, 8, 2, 128, x.bt.shape[1] * 16) == 0
+    good, good_lse = x.run()
+    x.bt[1, 25:] = -7
+    x.bt[2, 1:] = 1 << 30
+    out, lse = x.run()
+    assert fm.last_device_error() == 0 and torch.equal(out, good) and torch.equal(lse, good_lse)
+    for page, entry in ((0, -1), (24, x.codes[0].shape[0])):
+        kept, x.bt[1, page] = x.bt[1, page], entry
+        out, _ = x.run()
+        assert fm.last_device_error() == fm.DEV_BAD_PAGE
+        assert torch.equal(out[[0, 2]], good[[0, 2]])
+        x.bt[1, page] = kept
+    for n in (-1, 16 * x.bt.shape[1] + 1):
+        x.lens[0] = n
+        out, lse = x.run()
+        assert fm.last_device_error() == fm.DEV_BAD_SEQLEN
+        assert torch.all(out[0] == 0) and torch.all(torch.isneginf(lse[0])) and torch.equal(out[1:], good[1:])
+    x.lens[0] = 900
+    d = lambda a: torch.from_numpy(a).to(DEV)  # noqa: E731
+    t = dict(q=x.q.to(DEV), k_cache=d(x.codes[0]), v_cache=d(x.codes[1]), k_block_scales=d(x.s8[0]),
+             v_block_scales=d(x.s8[1]), block_table=d(x.bt), seqlens=d(x.lens), softmax_scale=x.softmax_scale,
+             k_scale=torch.tensor([x.scale[0]], device=DEV), v_scale=torch.tensor([x.scale[1]], device=DEV))
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for s in streams:
+        with torch.cuda.stream(s):
+            out, lse = torch.empty_like(good), torch.empty_like(good_lse)
+            for _ in range(20):
+                fm.paged_gqa_decode_fp4(**t, out=out, lse=lse)
+            outs.append((out, lse))
+    torch.cuda.synchronize()
+    for out, lse in outs:
+        assert torch.equal(out, good) and torch.equal(lse, good_lse)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fm.paged_gqa_decode_fp4(**t, out=out, lse=lse)
+        fm.paged_gqa_decode_fp4(**t, out=out, lse=lse)
+    for lens in ([17, 0, 3], [890, 399, 1]):
+        t["seqlens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        x.lens = np.asarray(lens, np.int32)
+        g.replay()
+        torch.cuda.synchronize()
+        x.check(out, lse)
 
 
 def test_outputs_given_graph_and_two_streams():
