@@ -27,7 +27,7 @@
 // table's rows (into L1) one.  A 16384-token prompt, 8 KV heads of 128, E4M3:
 // 22.0 us, 4.97 TB/s, 0.73 of the measured copy bandwidth (131072 tokens 0.78);
 // 2049 latent rows of 576 with 16 query heads 12.9 us, 0.91; 65537 rows x 8
-// heads read back 35.1 us, 0.85; 8193 tokens into 4 bits and back 27.0 us, where
+// heads read back 35.1 us, 0.85; 8193 tokens into 4 bits and back 25.2 us, where
 // a block's two conversions and reciprocal weigh as much as its bytes.
 #include <cuda_runtime.h>
 
@@ -43,7 +43,7 @@ namespace {
 __device__ uint32_t g_status_append;
 
 constexpr int kThreads = 256;
-constexpr int kReadCtasPerSm = 3;
+constexpr int kReadCtasPerSm = 5;
 // CTAs of an SM: registers for one piece a lane in flight, or for two and three.
 template <int kP>
 __host__ __device__ constexpr int append_ctas() {
@@ -391,10 +391,11 @@ struct ReadParams {
 
 // Rows of a paged cache as bf16: value = fp32(E4M3 * scale), or fp32(E2M1 * fp32(s8 * scale)), rounded once.
 // A group of kL lanes per row, kW values (16; 8 where head_dim is no multiple of 16) a lane at a time.  The same
-// pipeline as the append: slots two steps ahead, codes and scales one ahead.
+// pipeline as the append: slots two steps ahead, codes and scales one ahead.  One row a step and five CTAs an SM
+// (65537 x 8 rows 35.1 us, 8193 x 8 rows 6.0; two rows and three CTAs 35.1 and 6.6; one row, six 33.5 and 6.0 but
+// 32768 x 8 rows 19.8 instead of 16.1; four 36.9, eight 42.7).
 template <int kL, int kKind, int kW>
 __global__ void __launch_bounds__(kThreads, kReadCtasPerSm) cache_read_kernel(const __grid_constant__ ReadParams prm) {
-  constexpr int kRows = 2;
   constexpr int kBytes = kKind == kFp4 ? kW / 2 : kW;  // of codes a lane takes
   griddep_wait();
   const int lane = threadIdx.x % 32, sub = lane % kL, grp = lane / kL;
@@ -404,16 +405,13 @@ __global__ void __launch_bounds__(kThreads, kReadCtasPerSm) cache_read_kernel(co
   if constexpr (kKind != kRowScales) scale = __ldg(prm.scale);
 
   struct Row {
-    int64_t src[kRows];  // row in the cache, or -1
-    uint4 w[kRows];      // first piece's codes
-    float s[kRows];      // and their scale
+    int64_t src;  // row in the cache, or -1
+    uint4 w;      // first piece's codes
+    float s;      // and their scale
   };
-  auto slots_of = [&](uint32_t base, int32_t (&slot)[kRows]) {
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const uint32_t row = base + r * (32 / kL) + grp;
-      slot[r] = row < prm.rows ? __ldg(prm.slots + fast_div(row, prm.heads)) : -1;
-    }
+  auto slot_of = [&](uint32_t base) {
+    const uint32_t row = base + grp;
+    return row < prm.rows ? __ldg(prm.slots + fast_div(row, prm.heads)) : -1;
   };
   auto fetch = [&](int64_t src, int piece, uint4& w, float& s) {
     const uint8_t* at = prm.cache + src * (kKind == kFp4 ? prm.head_dim / 2 : prm.head_dim) + piece * kBytes;
@@ -433,21 +431,18 @@ __global__ void __launch_bounds__(kThreads, kReadCtasPerSm) cache_read_kernel(co
       s = scale;
     }
   };
-  auto load = [&](uint32_t base, const int32_t (&slot)[kRows], Row& x) {
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const uint32_t row = base + r * (32 / kL) + grp;
-      const uint32_t head = row - fast_div(row, prm.heads) * prm.heads.d;
-      x.src[r] = -1;
-      x.s[r] = 0.f;
-      x.w[r] = make_uint4(0, 0, 0, 0);
-      if (slot[r] >= 0 && static_cast<uint32_t>(slot[r]) >= prm.num_slots) {
-        if (sub == 0) atomicOr(&g_status_append, FP8MLA_DEV_BAD_SLOT);
-      } else if (slot[r] >= 0) {
-        const uint32_t block = fast_div(static_cast<uint32_t>(slot[r]), prm.page);
-        x.src[r] = (static_cast<int64_t>(block) * prm.heads.d + head) * prm.page.d + (slot[r] - block * prm.page.d);
-        if (sub < pieces) fetch(x.src[r], sub, x.w[r], x.s[r]);
-      }
+  auto load = [&](uint32_t base, int32_t slot, Row& x) {
+    const uint32_t row = base + grp;
+    const uint32_t head = row - fast_div(row, prm.heads) * prm.heads.d;
+    x.src = -1;
+    x.s = 0.f;
+    x.w = make_uint4(0, 0, 0, 0);
+    if (slot >= 0 && static_cast<uint32_t>(slot) >= prm.num_slots) {
+      if (sub == 0) atomicOr(&g_status_append, FP8MLA_DEV_BAD_SLOT);
+    } else if (slot >= 0) {
+      const uint32_t block = fast_div(static_cast<uint32_t>(slot), prm.page);
+      x.src = (static_cast<int64_t>(block) * prm.heads.d + head) * prm.page.d + (slot - block * prm.page.d);
+      if (sub < pieces) fetch(x.src, sub, x.w, x.s);
     }
   };
   auto store = [&](uint32_t row, int piece, const uint4& w, float s) {
@@ -475,50 +470,44 @@ __global__ void __launch_bounds__(kThreads, kReadCtasPerSm) cache_read_kernel(co
     for (int i = 0; i < kW / 8; ++i) __stcs(dst + i, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
   };
   auto process = [&](uint32_t base, const Row& x) {
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const uint32_t row = base + r * (32 / kL) + grp;
-      if (row >= prm.rows) continue;
-      const bool none = x.src[r] < 0;  // a row of zeros
-      if (sub < pieces) store(row, sub, none ? make_uint4(0, 0, 0, 0) : x.w[r], none ? 0.f : x.s[r]);
-      for (int j = 1; j < per_lane; ++j) {
-        const int piece = sub + j * kL;
-        if (piece >= pieces) break;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        float s = 0.f;
-        if (!none) fetch(x.src[r], piece, w, s);
-        store(row, piece, w, s);
-      }
+    const uint32_t row = base + grp;
+    if (row >= prm.rows) return;
+    const bool none = x.src < 0;  // a row of zeros
+    if (sub < pieces) store(row, sub, none ? make_uint4(0, 0, 0, 0) : x.w, none ? 0.f : x.s);
+    for (int j = 1; j < per_lane; ++j) {
+      const int piece = sub + j * kL;
+      if (piece >= pieces) break;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      float s = 0.f;
+      if (x.src >= 0) fetch(x.src, piece, w, s);
+      store(row, piece, w, s);
     }
   };
 
-  constexpr uint32_t kWarpRows = 32 / kL * kRows;
+  constexpr uint32_t kWarpRows = 32 / kL;
   uint32_t base = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kWarpRows;
   if (base >= prm.rows) return;  // the same for the whole warp
   const uint32_t stride = gridDim.x * (kThreads / 32) * kWarpRows;
-  int32_t s1[kRows], s2[kRows];
   Row x0, x1;
-  slots_of(base, s1);
-  load(base, s1, x0);
-  slots_of(base + stride, s1);
+  load(base, slot_of(base), x0);
+  int32_t s1 = slot_of(base + stride), s2 = -1;
   for (;;) {
     const bool more = base + stride < prm.rows;
     if (more) {
       load(base + stride, s1, x1);
-      slots_of(base + 2 * stride, s2);
+      s2 = slot_of(base + 2 * stride);
     }
     process(base, x0);
     if (!more) break;
     base += stride;
     x0 = x1;
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) s1[r] = s2[r];
+    s1 = s2;
   }
 }
 
 template <int kL, int kW>
 cudaError_t launch_read(const ReadParams& p, int kind, cudaStream_t stream) {
-  constexpr uint32_t kBlockRows = kThreads / 32 * (32 / kL) * 2;
+  constexpr uint32_t kBlockRows = kThreads / 32 * (32 / kL);
   const unsigned blocks = std::min<unsigned>((p.rows + kBlockRows - 1) / kBlockRows, device_sms() * kReadCtasPerSm);
   const dim3 grid(blocks), block(kThreads);
   switch (kind) {
