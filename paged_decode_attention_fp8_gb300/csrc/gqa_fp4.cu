@@ -60,7 +60,7 @@
 //     Few sequences of short contexts, for which two launches are too many, go
 //     uncut, to one CTA of up to sixteen warps each or to a cluster of two to
 //     eight, whose CTAs take their tiles in turn and merge over the cluster's
-//     shared memory (one context of 777 keys, 8 KV heads: 6.7 us a call; one
+//     shared memory (one context of 777 keys, 8 KV heads: 6.5 us a call; one
 //     CTA each 8.2).
 #include <cuda_runtime.h>
 
@@ -91,12 +91,17 @@ constexpr float kTau = 15.f;    // ... and moves when a score is this far above 
 // Warps of a CTA, CTAs of an SM, tiles a warp takes at a time, and stages of its ring.  Throughput: twelve warps of up
 // to 168 registers on an SM (eight at head_dim 256, twice the accumulators), in small CTAs, so that a piece's fill and
 // merge hide behind the other CTAs' loops (the 32-context batch: 8 warps x 2 CTAs 78 us, 4 x 4 70, 4 x 3 with two
-// tiles at a time 63).  kWide: an SM's warps in one CTA, alone or in a cluster, for few sequences of short contexts,
-// where a warp's few tiles in a row are what takes the time.
-template <int kHd, int kNT, bool kWide>
+// tiles at a time 63).  kWideCtas: an SM's warps in one CTA, alone or in a cluster, for few sequences of short contexts,
+// where a warp's few tiles in a row are what takes the time.  kWholeCtas: the throughput form without the code for pieces,
+// for whole sequences (456 of one tile 5.3 us, with it 6.2).  kNarrowCtas: the same in CTAs of two warps, for more sequences
+// of short contexts than there are places for the others.
+enum Ctas { kFillingCtas, kWholeCtas, kWideCtas, kNarrowCtas };
+template <int kHd, int kNT, Ctas kCtas>
 struct Shape {
-  static constexpr int kWarps = kWide ? (kHd == 256 ? 8 : (kNT == 1 ? 16 : 12)) : 4;
-  static constexpr int kPerSm = kWide ? 1 : (kHd == 256 ? 2 : 3);
+  static constexpr bool kWide = kCtas == kWideCtas, kNarrow = kCtas == kNarrowCtas;
+  static constexpr int kWarps = kWide ? (kHd == 256 ? 8 : (kNT == 1 ? 16 : 12)) : (kNarrow ? 2 : 4);
+  static constexpr int kPerSm =
+      kWide ? 1 : (kHd == 256 ? 2 : (kHd == 64 && kNT == 1 && kCtas != kFillingCtas ? 4 : 3)) * (kNarrow ? 2 : 1);
   static constexpr int kU = kWide || kHd == 256 || kNT == 2 ? 1 : 2;
   static constexpr int kStages = kU == 2 ? 3 : 4;
 };
@@ -119,7 +124,7 @@ struct Params {
   float2* ws_ml;   // [slot][NT * 8]
   int2* ws_span;   // [bs * h_kv]: first and last piece of a (sequence, KV head) (balanced only)
   int num_blocks, max_blocks, bs, h_q, h_kv, group, q_len, window;
-  int splits;      // shards of every sequence, one CTA each (1: no merge), or 0: balanced pieces; kWide: a cluster's CTAs
+  int splits;      // shards of every sequence, one CTA each (1: no merge), or 0: balanced pieces; wide: a cluster's CTAs
   int units;       // balanced: pieces there may be
   int page_shift;  // log2(page_size / 16)
   float softmax_scale;
@@ -202,11 +207,12 @@ __device__ __forceinline__ int tiles_of(const Params& prm, int s_k) {
   return max(0, (s_k + kTile - 1) / kTile - first_tile(prm, s_k));
 }
 
-template <int kHd, int kNT, bool kWide>
-__global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd, kNT, kWide>::kPerSm)
+template <int kHd, int kNT, Ctas kCtas>
+__global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd, kNT, kCtas>::kPerSm)
     fp4_decode_kernel(const __grid_constant__ Params prm) {
   using L = Lay<kHd>;
-  using S = Shape<kHd, kNT, kWide>;
+  using S = Shape<kHd, kNT, kCtas>;
+  constexpr bool kWide = S::kWide, kCut = kCtas == kFillingCtas;  // kCut: a CTA may have a part of a sequence
   constexpr int kWarps = S::kWarps, kU = S::kU, kStages = S::kStages;
   constexpr int kStage = kU * L::kBytes;
   constexpr int kSteps = kHd / 16;     // products of a tile, for K and for V
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
   __shared__ float s_weight[kMaxCluster][kNT * 8];  // what the cluster's states are multiplied by
   __shared__ int64_t s_row[kNT * 8];
   __shared__ int s_tok[kNT * 8];              // a column's token
-  __shared__ int s_line[kMaxLine + 1];
+  __shared__ int s_line[kCut ? kMaxLine + 1 : 1];
   __shared__ int s_part[2][kWarps];
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -238,7 +244,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
   // taking kFixed places and then one for every tile
   int cur = 0, end = 1;
   const int unit = blockIdx.x;
-  if (prm.splits == 0) {
+  if (kCut && prm.splits == 0) {
     // prefix sums of the sequences' places (of one KV head), a CTA's width of sequences at a time
     constexpr int kThreads = kWarps * 32, kRuns = (kMaxLine + kThreads - 1) / kThreads;
     int len[kRuns];
@@ -310,7 +316,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
     // ---- the segment: tiles [t0, t1) of one (sequence, KV head)
     int b, kvh, t0, t1, s_k;
     long long slot = -1;  // where its partial state goes, or -1: the rows are finished here
-    if (prm.splits == 0) {
+    if (kCut && prm.splits == 0) {
       const int at = cur / prm.h_kv;
       int lo = 0, hi = prm.bs;  // s_line[lo] <= at < s_line[hi]
       while (hi - lo > 1) {
@@ -337,26 +343,26 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
       t0 = first;
       t1 = last;
     } else {
-      const int seq = unit / prm.splits;
+      const int seq = kCut || kWide ? unit / prm.splits : unit;
       b = seq / prm.h_kv;
       kvh = seq - b * prm.h_kv;
-      if (!kWide && prm.splits > 1) slot = static_cast<long long>(blockIdx.y) * gridDim.x + unit;
+      if (kCut && prm.splits > 1) slot = static_cast<long long>(blockIdx.y) * gridDim.x + unit;
       cur = end;
     }
     auto lengths = [&]() {
-      if (prm.splits == 0) {
+      if (kCut && prm.splits == 0) {
         s_k = __ldg(prm.seqlens + b);
         t0 += first_tile(prm, s_k);
         t1 += first_tile(prm, s_k);
       } else {
         s_k = checked_len(prm, __ldg(prm.seqlens + b));
-        const int tiles = tiles_of(prm, s_k), split = kWide ? 0 : unit % prm.splits, splits = kWide ? 1 : prm.splits;
+        const int tiles = tiles_of(prm, s_k), split = kCut ? unit % prm.splits : 0, splits = kCut ? prm.splits : 1;
         t0 = first_tile(prm, s_k) + static_cast<int>(static_cast<long long>(split) * tiles / splits);
         t1 = first_tile(prm, s_k) + static_cast<int>(static_cast<long long>(split + 1) * tiles / splits);
       }
     };
     const int32_t* bt_row = prm.block_table + static_cast<size_t>(b) * prm.max_blocks;
-    // Where a call's latency is what counts (kWide), what does not depend on the sequence's length is asked for before
+    // Where a call's latency is what counts (wide), what does not depend on the sequence's length is asked for before
     // it has come: the first tiles' places in the block table (without a window they are known), Q, sinks and mask.
     int32_t guessed = 0;
     bool guess = false;
@@ -376,7 +382,8 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
           prm.q + ((static_cast<size_t>(b) * prm.q_len + token) * prm.h_q + hq) * kHd + t * (kHd / 4));
 #pragma unroll
       for (int j = 0; j < kSteps / 2; ++j) qx[j] = c < ncols ? ldg_now(src + j) : make_uint4(0, 0, 0, 0);
-      if (kWide && prm.sinks != nullptr && c < ncols) sink = __int_as_float(ldg_now(reinterpret_cast<const int32_t*>(prm.sinks) + hq));
+      if (kWide && prm.sinks != nullptr && c < ncols)
+        sink = __int_as_float(ldg_now(reinterpret_cast<const int32_t*>(prm.sinks) + hq));
     }
     // The speculative block's mask, by the last warp: lane (r, c) of half-warp r takes byte c of rows r, r + 2, ...
     int32_t seen[kMaxQLen / 2];
@@ -786,7 +793,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
         sum += s_m[w][c] == kNegInf ? 0.f : s_l[w][c] * ex2_approx(s_m[w][c] - (mx == kNegInf ? 0.f : mx));
-      if (slot >= 0) {
+      if (kCut && slot >= 0) {
         prm.ws_ml[slot * (kNT * 8) + c] = make_float2(mx, sum);
       } else if (kWide && prm.splits > 1) {
         s_ml[c] = make_float2(mx, sum);
@@ -819,7 +826,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kWide>::kWarps * 32, Shape<kHd
         const float4 y = part[w * kFrag + x];
         a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
       }
-      if (slot >= 0) prm.ws_o[slot * kFrag + x] = a;
+      if (kCut && slot >= 0) prm.ws_o[slot * kFrag + x] = a;
       else if (kWide && prm.splits > 1) part[x] = a;  // (the only thread that reads the others of x)
       else write(x, a);
     }
@@ -994,11 +1001,11 @@ int col_tiles(int cols, int* nt) {  // columns run eight or sixteen to a CTA
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// How a call is laid out: shards of every sequence (1: none, 0: balanced pieces; wide: CTAs of its cluster), pieces, and
+// How a call is laid out: shards of every sequence (1: none, 0: balanced (1: none, 0: balanced pieces; kWideCtas: CTAs of its cluster), pieces, and
 // the workspace.
 struct Plan {
   int nt, ct, splits, units;
-  bool wide;    // an SM's warps in one CTA, `splits` of them in a cluster for a sequence
+  Ctas kind;    // kWideCtas: `splits` of them in a cluster for a sequence
   size_t slots, ml, span, bytes;  // partial states, and where (m, l) and the spans of pieces begin
 };
 
@@ -1016,7 +1023,7 @@ Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long cap
   const long long seqs = static_cast<long long>(bs) * h_kv;
   const int resident = device_sms() * (head_dim == 256 ? 2 : 3);  // Shape::kPerSm
   p.units = 0;
-  p.wide = false;
+  p.kind = kFillingCtas;
   // Few sequences: an SM's warps in one CTA, and CTAs in a cluster, which merges without a second kernel, as far as
   // clusters of that size fit on the GPU at once (eight CTAs 15 times, four 36 times).  A cluster's merge takes 1.4 us,
   // so short contexts stay with one CTA (8 sequences of 25 tiles: 6.3 us, in clusters of eight 7.1; of 50 tiles 7.7 and
@@ -1063,13 +1070,24 @@ Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long cap
     // Short contexts: one CTA or cluster a sequence takes no longer than pieces and their merge.  Many sequences: their
     // CTAs balance by themselves.  (The line's places are counted in 32 bits.)
     p.splits = 1;
-    p.wide = few && tiles > 4;
-    if (p.wide && tiles > alone) p.splits = cluster;
+    if (few && tiles > 4) {
+      p.kind = kWideCtas;
+      if (tiles > alone) p.splits = cluster;
+    } else if (const long long places = sms * (head_dim == 256 ? 2 : (head_dim == 64 && p.nt == 1 ? 4 : 3));
+               ctas > places && tiles <= kShort) {
+      // More than fit at once (places: Shape::kPerSm of kWholeCtas): half the warps in twice as many places, unless
+      // those are left emptier at the end and the contexts are not that short (512 sequences of 7 tiles 10.0 us, narrow
+      // 6.6, of 94 tiles 33.2 and 29.0; 1024 of 50 tiles 33.2 and 32.7, of 94 tiles 50.9 and 54.5; head_dim 256, 768 of
+      // 13 tiles 23.2 and 21.9, of 50 tiles 46.8 and 52.4)
+      const long long rounds = (ctas + places - 1) / places, narrow = (ctas + 2 * places - 1) / (2 * places);
+      if (tiles <= (head_dim == 256 ? 20 : 50) || 2 * narrow <= rounds) p.kind = kNarrowCtas;
+    }
   } else {
     p.splits = 0;
     p.units = std::max(1, resident / p.ct);
   }
-  p.slots = p.splits == 1 || p.wide ? 0 : static_cast<size_t>(p.ct) * (p.splits == 0 ? 2 * p.units : seqs * p.splits);
+  if (p.splits == 1 && p.kind == kFillingCtas) p.kind = kWholeCtas;
+  p.slots = p.splits == 1 || p.kind == kWideCtas ? 0 : static_cast<size_t>(p.ct) * (p.splits == 0 ? 2 * p.units : seqs * p.splits);
   p.ml = round_up(p.slots * p.nt * 8 * head_dim * sizeof(float), 256);
   p.span = p.ml + round_up(p.slots * p.nt * 8 * sizeof(float2), 256);
   p.bytes = p.span + (p.splits == 0 ? round_up(static_cast<size_t>(seqs) * sizeof(int2), 256) : 0);
@@ -1082,32 +1100,34 @@ bool sizes_ok(int bs, int h_q, int h_kv, int head_dim, int q_len, int window, in
          static_cast<long long>(q_len) * (h_q / h_kv) <= kMaxCols && window >= 0 && num_splits >= 0;
 }
 
-template <int kHd, int kNT, bool kWide>
+template <int kHd, int kNT, Ctas kCtas>
 cudaError_t launch_decode(const Params& prm, int seqs, int ct, cudaStream_t stream) {
-  using S = Shape<kHd, kNT, kWide>;
+  using S = Shape<kHd, kNT, kCtas>;
   constexpr size_t smem =
       std::max<size_t>(static_cast<size_t>(S::kWarps) * S::kStages * S::kU * Lay<kHd>::kBytes,
                        static_cast<size_t>(S::kWarps) * kNT * (kHd / 16) * 32 * sizeof(float4));
-  static_assert(S::kPerSm * (smem + 16 * 1024) <= 233472, "the CTAs fit in an SM's shared memory");
+  static_assert(S::kPerSm * (smem + (S::kNarrow ? 10 : 16) * 1024) <= 233472, "the CTAs fit in an SM's shared memory");
   static std::atomic<uint64_t> configured{0};
   const cudaError_t e = configure_once(configured, [&] {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(fp4_decode_kernel<kHd, kNT, kWide>),
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(fp4_decode_kernel<kHd, kNT, kCtas>),
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   });
   if (e != cudaSuccess) return e;
   const unsigned grid = prm.splits == 0 ? static_cast<unsigned>(prm.units)
                                         : static_cast<unsigned>(seqs) * static_cast<unsigned>(prm.splits);
-  if (kWide && prm.splits > 1)
-    return launch_dependent_clusters(prm.splits, fp4_decode_kernel<kHd, kNT, kWide>, dim3(grid, ct),
+  if (S::kWide && prm.splits > 1)
+    return launch_dependent_clusters(prm.splits, fp4_decode_kernel<kHd, kNT, kCtas>, dim3(grid, ct),
                                      dim3(S::kWarps * 32), smem, stream, prm);
-  return launch_dependent(fp4_decode_kernel<kHd, kNT, kWide>, dim3(grid, ct), dim3(S::kWarps * 32), smem, stream, prm);
+  return launch_dependent(fp4_decode_kernel<kHd, kNT, kCtas>, dim3(grid, ct), dim3(S::kWarps * 32), smem, stream, prm);
 }
 
 template <int kHd, int kNT>
-cudaError_t launch(const Params& prm, bool wide, int seqs, int ct, cudaStream_t stream) {
-  const cudaError_t e = wide ? launch_decode<kHd, kNT, true>(prm, seqs, ct, stream)
-                             : launch_decode<kHd, kNT, false>(prm, seqs, ct, stream);
-  if (e != cudaSuccess || prm.splits == 1 || wide) return e;
+cudaError_t launch(const Params& prm, Ctas ctas, int seqs, int ct, cudaStream_t stream) {
+  if (ctas == kWideCtas) return launch_decode<kHd, kNT, kWideCtas>(prm, seqs, ct, stream);
+  if (ctas == kWholeCtas) return launch_decode<kHd, kNT, kWholeCtas>(prm, seqs, ct, stream);
+  if (ctas == kNarrowCtas) return launch_decode<kHd, kNT, kNarrowCtas>(prm, seqs, ct, stream);
+  const cudaError_t e = launch_decode<kHd, kNT, kFillingCtas>(prm, seqs, ct, stream);
+  if (e != cudaSuccess) return e;
   // warps for the shards that a sequence has on average, four at a time each (100 sequences cut into 5: 19.4 us a call
   // with one warp, 25.3 with sixteen, most of them idle; 6 cut into 76: 17.9 with sixteen, 20.9 with four)
   constexpr unsigned kFrags = kNT * (kHd / 16);
@@ -1189,12 +1209,12 @@ fp8mla_status_t fp4_decode_entry(const Fp4DecodeArgs& a, cudaStream_t stream) {
   const int n = static_cast<int>(seqs);
   cudaError_t e;
   switch (a.head_dim + plan.nt) {
-    case 64 + 1: e = fp4::launch<64, 1>(p, plan.wide, n, plan.ct, stream); break;
-    case 64 + 2: e = fp4::launch<64, 2>(p, plan.wide, n, plan.ct, stream); break;
-    case 128 + 1: e = fp4::launch<128, 1>(p, plan.wide, n, plan.ct, stream); break;
-    case 128 + 2: e = fp4::launch<128, 2>(p, plan.wide, n, plan.ct, stream); break;
-    case 256 + 1: e = fp4::launch<256, 1>(p, plan.wide, n, plan.ct, stream); break;
-    default: e = fp4::launch<256, 2>(p, plan.wide, n, plan.ct, stream); break;
+    case 64 + 1: e = fp4::launch<64, 1>(p, plan.kind, n, plan.ct, stream); break;
+    case 64 + 2: e = fp4::launch<64, 2>(p, plan.kind, n, plan.ct, stream); break;
+    case 128 + 1: e = fp4::launch<128, 1>(p, plan.kind, n, plan.ct, stream); break;
+    case 128 + 2: e = fp4::launch<128, 2>(p, plan.kind, n, plan.ct, stream); break;
+    case 256 + 1: e = fp4::launch<256, 1>(p, plan.kind, n, plan.ct, stream); break;
+    default: e = fp4::launch<256, 2>(p, plan.kind, n, plan.ct, stream); break;
   }
   return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
 }

@@ -277,6 +277,22 @@ def test_many_sequences(bs):
     assert torch.all((out[live] - one[live]).abs().float() <= 2.0 ** -7 * one[live].abs().float() + 2.0 ** -9)
 
 
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("bs,h_kv,q_len,group,mask,window,sinks", [(90, 8, 1, 3, False, 0, True), (170, 8, 1, 4, False, 20, False),
+                                                                   (70, 9, 4, 4, True, 0, False), (200, 3, 2, 7, True, 9, True)])
+def test_many_short_sequences(hd, bs, h_kv, q_len, group, mask, window, sinks):
+    """More sequences than the GPU takes CTAs of four warps at once, of a few tiles each."""
+    rng = np.random.default_rng(bs + hd)
+    x = Inputs(400 + hd + bs, rng.integers(0, 70, bs), h_kv, group, hd, 16, q_len, mask, sinks)
+    out, lse = x.run(window=window)
+    x.check(out, lse, window=window, rows=[(int(b), int(h)) for b, h in zip(rng.integers(0, bs, 40),
+                                                                           rng.integers(0, h_kv * group, 40))])
+    one, lse1 = x.run(window=window, num_splits=1)  # the same sums in another order
+    live = torch.isfinite(lse1)
+    assert torch.equal(live, torch.isfinite(lse)) and torch.all((lse[live] - lse1[live]).abs() <= 2.0 ** -16)
+    assert torch.all((out - one).abs().float() <= 2.0 ** -7 * one.abs().float() + 2.0 ** -9)
+
+
 def test_bad_lengths_among_balanced_pieces():
     x = Inputs(50, [3000, 2000, 2500], 2, 4, 64, 16)
     good, good_lse = x.run()
