@@ -91,11 +91,11 @@ constexpr float kTau = 15.f;    // ... and moves when a score is this far above 
 // Warps of a CTA, CTAs of an SM, tiles a warp takes at a time, and stages of its ring.  Throughput: twelve warps of up
 // to 168 registers on an SM (eight at head_dim 256, twice the accumulators), in small CTAs, so that a piece's fill and
 // merge hide behind the other CTAs' loops (the 32-context batch: 8 warps x 2 CTAs 78 us, 4 x 4 70, 4 x 3 with two
-// tiles at a time 63).  kWideCtas: an SM's warps in one CTA, alone or in a cluster, for few sequences of short contexts,
-// where a warp's few tiles in a row are what takes the time.  kWholeCtas: the throughput form without the code for pieces,
-// for whole sequences (456 of one tile 5.3 us, with it 6.2).  kNarrowCtas: the same in CTAs of two warps, for more sequences
-// of short contexts than there are places for the others.
-enum Ctas { kFillingCtas, kWholeCtas, kWideCtas, kNarrowCtas };
+// tiles at a time 63): kFillingCtas, for pieces and shards, and kWholeCtas, the same without the code for them (456
+// sequences of one tile 5.3 us, with it 6.2).  kNarrowCtas: two warps, for more sequences of short contexts than there
+// are places for those.  kWideCtas: an SM's warps in one CTA, alone or in a cluster, for few sequences of short
+// contexts, where a warp's few tiles in a row are what takes the time.
+enum Ctas { kFillingCtas, kWholeCtas, kNarrowCtas, kWideCtas };
 template <int kHd, int kNT, Ctas kCtas>
 struct Shape {
   static constexpr bool kWide = kCtas == kWideCtas, kNarrow = kCtas == kNarrowCtas;
@@ -124,7 +124,7 @@ struct Params {
   float2* ws_ml;   // [slot][NT * 8]
   int2* ws_span;   // [bs * h_kv]: first and last piece of a (sequence, KV head) (balanced only)
   int num_blocks, max_blocks, bs, h_q, h_kv, group, q_len, window;
-  int splits;      // shards of every sequence, one CTA each (1: no merge), or 0: balanced pieces; wide: a cluster's CTAs
+  int splits;      // shards of every sequence, one CTA each (1: no merge), or 0: balanced pieces; wide: CTAs of a cluster
   int units;       // balanced: pieces there may be
   int page_shift;  // log2(page_size / 16)
   float softmax_scale;
@@ -377,7 +377,8 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
     uint4 qx[kSteps / 2];
     float sink = kNegInf;
     if (warp < kNT) {
-      const int c = warp * 8 + g, col = col0 + c, token = col / prm.group, hq = kvh * prm.group + col - token * prm.group;
+      const int c = warp * 8 + g, col = col0 + c, token = col / prm.group;
+      const int hq = kvh * prm.group + col - token * prm.group;
       const uint4* src = reinterpret_cast<const uint4*>(
           prm.q + ((static_cast<size_t>(b) * prm.q_len + token) * prm.h_q + hq) * kHd + t * (kHd / 4));
 #pragma unroll
@@ -891,7 +892,8 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
 // more, the warps take shards w, w + kGroups, ... of one step and meet in shared memory (few sequences, many shards:
 // three contexts cut into 76 shards each take 17.9 us a call with 16, 18.9 with 8, 20.9 with 4, 19.5 with 32).
 template <int kHd, int kNT, int kGroups>
-__global__ void __launch_bounds__(kGroups == 1 ? 128 : kGroups * 32) fp4_combine_kernel(const __grid_constant__ Params prm) {
+__global__ void __launch_bounds__(kGroups == 1 ? 128 : kGroups * 32)
+    fp4_combine_kernel(const __grid_constant__ Params prm) {
   constexpr int kSteps = kHd / 16, kFrag = kNT * kSteps * 32;
   __shared__ float4 s_o[kGroups][32], s_ml[kGroups][32];
   griddep_wait();
@@ -924,7 +926,8 @@ __global__ void __launch_bounds__(kGroups == 1 ? 128 : kGroups * 32) fp4_combine
   float sink[2] = {kNegInf, kNegInf};
 #pragma unroll
   for (int k = 0; k < 2; ++k)
-    if (prm.sinks != nullptr && c + k < ncols) sink[k] = __ldg(prm.sinks + kvh * prm.group + (col0 + c + k) % prm.group);
+    if (prm.sinks != nullptr && c + k < ncols)
+      sink[k] = __ldg(prm.sinks + kvh * prm.group + (col0 + c + k) % prm.group);
   float m0 = kNegInf, m1 = kNegInf, l0 = 0.f, l1 = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = group; s0 < count; s0 += 4 * kGroups) {  // four shards' loads in flight
@@ -1001,8 +1004,8 @@ int col_tiles(int cols, int* nt) {  // columns run eight or sixteen to a CTA
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// How a call is laid out: shards of every sequence (1: none, 0: balanced (1: none, 0: balanced pieces; kWideCtas: CTAs of its cluster), pieces, and
-// the workspace.
+// How a call is laid out: shards of every sequence (1: none, 0: balanced pieces; kWideCtas: CTAs of its cluster),
+// pieces, and the workspace.
 struct Plan {
   int nt, ct, splits, units;
   Ctas kind;    // kWideCtas: `splits` of them in a cluster for a sequence
@@ -1087,7 +1090,7 @@ Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long cap
     p.units = std::max(1, resident / p.ct);
   }
   if (p.splits == 1 && p.kind == kFillingCtas) p.kind = kWholeCtas;
-  p.slots = p.splits == 1 || p.kind == kWideCtas ? 0 : static_cast<size_t>(p.ct) * (p.splits == 0 ? 2 * p.units : seqs * p.splits);
+  p.slots = p.kind != kFillingCtas ? 0 : static_cast<size_t>(p.ct) * (p.splits == 0 ? 2 * p.units : seqs * p.splits);
   p.ml = round_up(p.slots * p.nt * 8 * head_dim * sizeof(float), 256);
   p.span = p.ml + round_up(p.slots * p.nt * 8 * sizeof(float2), 256);
   p.bytes = p.span + (p.splits == 0 ? round_up(static_cast<size_t>(seqs) * sizeof(int2), 256) : 0);
