@@ -94,7 +94,8 @@ void need_heads(const Tensor& x, const char* name, ScalarType type, const c10::D
 }
 
 // The same for an output: no two of its rows may share memory.
-void need_heads_out(const Tensor& x, const char* name, c10::IntArrayRef shape, ScalarType type, const c10::Device& dev) {
+void need_heads_out(const Tensor& x, const char* name, c10::IntArrayRef shape, ScalarType type,
+                    const c10::Device& dev) {
   need_heads(x, name, type, dev, shape[0], shape[2]);
   if (x.sizes() != shape) bad(std::string(name) + " must have its input's shape");
   if ((x.size(0) > 1 && x.stride(0) == 0) || (x.size(1) > 1 && x.stride(1) == 0))
@@ -358,7 +359,8 @@ PyObject* py_cache_read(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   return guarded([&]() -> PyObject* {
     const Tensor& cache = given(a[0], "cache");
     const Tensor& slots = given(a[1], "slots");
-    const Tensor *scale = maybe(a[2], "scale"), *rows = maybe(a[3], "row_scales"), *blocks = maybe(a[4], "block_scales");
+    const Tensor *scale = maybe(a[2], "scale"), *rows = maybe(a[3], "row_scales");
+    const Tensor* blocks = maybe(a[4], "block_scales");
     const Tensor* out = maybe(a[5], "out");
     if (!cache.is_cuda()) bad("cache must be a CUDA tensor");
     const c10::Device dev = cache.device();

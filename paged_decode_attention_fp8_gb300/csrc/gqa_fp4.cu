@@ -124,7 +124,7 @@ struct Params {
   float2* ws_ml;   // [slot][NT * 8]
   int2* ws_span;   // [bs * h_kv]: first and last piece of a (sequence, KV head) (balanced only)
   int num_blocks, max_blocks, bs, h_q, h_kv, group, q_len, window;
-  int splits;      // shards of every sequence, one CTA each (1: no merge), or 0: balanced pieces; wide: CTAs of a cluster
+  int splits;      // shards of every sequence, one CTA each (1: no merge), 0: balanced pieces; wide: CTAs of a cluster
   int units;       // balanced: pieces there may be
   int page_shift;  // log2(page_size / 16)
   float softmax_scale;

@@ -278,8 +278,9 @@ def test_many_sequences(bs):
 
 
 @pytest.mark.parametrize("hd", [64, 128, 256])
-@pytest.mark.parametrize("bs,h_kv,q_len,group,mask,window,sinks", [(90, 8, 1, 3, False, 0, True), (170, 8, 1, 4, False, 20, False),
-                                                                   (70, 9, 4, 4, True, 0, False), (200, 3, 2, 7, True, 9, True)])
+@pytest.mark.parametrize("bs,h_kv,q_len,group,mask,window,sinks", [
+    (90, 8, 1, 3, False, 0, True), (170, 8, 1, 4, False, 20, False),
+    (70, 9, 4, 4, True, 0, False), (200, 3, 2, 7, True, 9, True)])
 def test_many_short_sequences(hd, bs, h_kv, q_len, group, mask, window, sinks):
     """More sequences than the GPU takes CTAs of four warps at once, of a few tiles each."""
     rng = np.random.default_rng(bs + hd)
@@ -379,7 +380,8 @@ def test_served_batch_sampled():
 
 
 @pytest.mark.parametrize("window", [33, 900])
-@pytest.mark.parametrize("hd,q_len,group", [(64, 4, 2), (64, 4, 5), (128, 4, 2), (128, 6, 8), (256, 3, 2), (256, 16, 4)])
+@pytest.mark.parametrize("hd,q_len,group", [(64, 4, 2), (64, 4, 5), (128, 4, 2), (128, 6, 8), (256, 3, 2),
+                                            (256, 16, 4)])
 def test_a_nan_value_stays_with_the_tokens_that_see_it(hd, q_len, group, window):
     """A NaN V scale on the block's last key, which the last token alone sees, and on the key that the window leaves to
     the first token alone: those tokens' 16 dims are NaN and nothing else changes by a bit."""
