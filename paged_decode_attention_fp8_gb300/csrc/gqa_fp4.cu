@@ -17,7 +17,7 @@
 // 128, group 4): 63.4 us a call, 0.77 of the measured copy bandwidth; leaving
 // the loads out would save 1.5 us, the scale multiplications 9.5, the
 // conversions of V 10.  Sixteen columns double the products and leave twelve
-// warps less to hide with: four-token blocks under a 4096-key window 46.9 us,
+// warps less to hide with: four-token blocks under a 4096-key window 45.7 us,
 // 0.45.  head_dim 64 halves the bytes of a tile but not its overhead: three
 // contexts of 50k to 131k keys 17.9 us, 0.37, of which 8 are the lengths' sums,
 // the first tiles, the merge and two launches.
@@ -91,10 +91,10 @@ constexpr float kTau = 15.f;    // ... and moves when a score is this far above 
 // Warps of a CTA, CTAs of an SM, tiles a warp takes at a time, and stages of its ring.  Throughput: twelve warps of up
 // to 168 registers on an SM (eight at head_dim 256, twice the accumulators), in small CTAs, so that a piece's fill and
 // merge hide behind the other CTAs' loops (the 32-context batch: 8 warps x 2 CTAs 78 us, 4 x 4 70, 4 x 3 with two
-// tiles at a time 63): kFillingCtas, for pieces and shards, and kWholeCtas, the same without the code for them (456
-// sequences of one tile 5.3 us, with it 6.2).  kNarrowCtas: two warps, for more sequences of short contexts than there
-// are places for those.  kWideCtas: an SM's warps in one CTA, alone or in a cluster, for few sequences of short
-// contexts, where a warp's few tiles in a row are what takes the time.
+// tiles at a time 63): kFillingCtas, for pieces, and kWholeCtas, for whole sequences and asked-for shards, without the
+// code for pieces (456 sequences of one tile 5.3 us, with it 6.2).  kNarrowCtas: two warps, for more sequences of short
+// contexts than there are places for those.  kWideCtas: an SM's warps in one CTA, alone or in a cluster, for few
+// sequences of short contexts, where a warp's few tiles in a row are what takes the time.
 enum Ctas { kFillingCtas, kWholeCtas, kNarrowCtas, kWideCtas };
 template <int kHd, int kNT, Ctas kCtas>
 struct Shape {
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
     fp4_decode_kernel(const __grid_constant__ Params prm) {
   using L = Lay<kHd>;
   using S = Shape<kHd, kNT, kCtas>;
-  constexpr bool kWide = S::kWide, kCut = kCtas == kFillingCtas;  // kCut: a CTA may have a part of a sequence
+  constexpr bool kWide = S::kWide, kPieces = kCtas == kFillingCtas, kShards = kCtas == kWholeCtas;
   constexpr int kWarps = S::kWarps, kU = S::kU, kStages = S::kStages;
   constexpr int kStage = kU * L::kBytes;
   constexpr int kSteps = kHd / 16;     // products of a tile, for K and for V
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
   __shared__ float s_weight[kMaxCluster][kNT * 8];  // what the cluster's states are multiplied by
   __shared__ int64_t s_row[kNT * 8];
   __shared__ int s_tok[kNT * 8];              // a column's token
-  __shared__ int s_line[kCut ? kMaxLine + 1 : 1];
+  __shared__ int s_line[kPieces ? kMaxLine + 1 : 1];
   __shared__ int s_part[2][kWarps];
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
   // taking kFixed places and then one for every tile
   int cur = 0, end = 1;
   const int unit = blockIdx.x;
-  if (kCut && prm.splits == 0) {
+  if (kPieces) {
     // prefix sums of the sequences' places (of one KV head), a CTA's width of sequences at a time
     constexpr int kThreads = kWarps * 32, kRuns = (kMaxLine + kThreads - 1) / kThreads;
     int len[kRuns];
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
     // ---- the segment: tiles [t0, t1) of one (sequence, KV head)
     int b, kvh, t0, t1, s_k;
     long long slot = -1;  // where its partial state goes, or -1: the rows are finished here
-    if (kCut && prm.splits == 0) {
+    if (kPieces) {
       const int at = cur / prm.h_kv;
       int lo = 0, hi = prm.bs;  // s_line[lo] <= at < s_line[hi]
       while (hi - lo > 1) {
@@ -343,22 +343,27 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
       t0 = first;
       t1 = last;
     } else {
-      const int seq = kCut || kWide ? unit / prm.splits : unit;
+      const int seq = (kShards || kWide) && prm.splits > 1 ? unit / prm.splits : unit;
       b = seq / prm.h_kv;
       kvh = seq - b * prm.h_kv;
-      if (kCut && prm.splits > 1) slot = static_cast<long long>(blockIdx.y) * gridDim.x + unit;
+      if (kShards && prm.splits > 1) slot = static_cast<long long>(blockIdx.y) * gridDim.x + unit;
       cur = end;
     }
     auto lengths = [&]() {
-      if (kCut && prm.splits == 0) {
+      if (kPieces) {
         s_k = __ldg(prm.seqlens + b);
         t0 += first_tile(prm, s_k);
         t1 += first_tile(prm, s_k);
       } else {
         s_k = checked_len(prm, __ldg(prm.seqlens + b));
-        const int tiles = tiles_of(prm, s_k), split = kCut ? unit % prm.splits : 0, splits = kCut ? prm.splits : 1;
-        t0 = first_tile(prm, s_k) + static_cast<int>(static_cast<long long>(split) * tiles / splits);
-        t1 = first_tile(prm, s_k) + static_cast<int>(static_cast<long long>(split + 1) * tiles / splits);
+        const int tiles = tiles_of(prm, s_k);
+        t0 = first_tile(prm, s_k);
+        t1 = t0 + tiles;
+        if (kShards && prm.splits > 1) {  // (the divisions would cost a short call 0.4 us)
+          const int split = unit % prm.splits;
+          t1 = t0 + static_cast<int>(static_cast<long long>(split + 1) * tiles / prm.splits);
+          t0 += static_cast<int>(static_cast<long long>(split) * tiles / prm.splits);
+        }
       }
     };
     const int32_t* bt_row = prm.block_table + static_cast<size_t>(b) * prm.max_blocks;
@@ -794,7 +799,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
         sum += s_m[w][c] == kNegInf ? 0.f : s_l[w][c] * ex2_approx(s_m[w][c] - (mx == kNegInf ? 0.f : mx));
-      if (kCut && slot >= 0) {
+      if ((kPieces || kShards) && slot >= 0) {
         prm.ws_ml[slot * (kNT * 8) + c] = make_float2(mx, sum);
       } else if (kWide && prm.splits > 1) {
         s_ml[c] = make_float2(mx, sum);
@@ -827,7 +832,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
         const float4 y = part[w * kFrag + x];
         a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
       }
-      if (kCut && slot >= 0) prm.ws_o[slot * kFrag + x] = a;
+      if ((kPieces || kShards) && slot >= 0) prm.ws_o[slot * kFrag + x] = a;
       else if (kWide && prm.splits > 1) part[x] = a;  // (the only thread that reads the others of x)
       else write(x, a);
     }
@@ -1026,7 +1031,7 @@ Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long cap
   const long long seqs = static_cast<long long>(bs) * h_kv;
   const int resident = device_sms() * (head_dim == 256 ? 2 : 3);  // Shape::kPerSm
   p.units = 0;
-  p.kind = kFillingCtas;
+  p.kind = kWholeCtas;
   // Few sequences: an SM's warps in one CTA, and CTAs in a cluster, which merges without a second kernel, as far as
   // clusters of that size fit on the GPU at once (eight CTAs 15 times, four 36 times).  A cluster's merge takes 1.4 us,
   // so short contexts stay with one CTA (8 sequences of 25 tiles: 6.3 us, in clusters of eight 7.1; of 50 tiles 7.7 and
@@ -1086,11 +1091,13 @@ Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long cap
       if (tiles <= (head_dim == 256 ? 20 : 50) || 2 * narrow <= rounds) p.kind = kNarrowCtas;
     }
   } else {
+    p.kind = kFillingCtas;
     p.splits = 0;
     p.units = std::max(1, resident / p.ct);
   }
-  if (p.splits == 1 && p.kind == kFillingCtas) p.kind = kWholeCtas;
-  p.slots = p.kind != kFillingCtas ? 0 : static_cast<size_t>(p.ct) * (p.splits == 0 ? 2 * p.units : seqs * p.splits);
+  p.slots = 0;
+  if (p.kind == kFillingCtas) p.slots = static_cast<size_t>(p.ct) * 2 * p.units;
+  if (p.kind == kWholeCtas && p.splits > 1) p.slots = static_cast<size_t>(p.ct) * seqs * p.splits;
   p.ml = round_up(p.slots * p.nt * 8 * head_dim * sizeof(float), 256);
   p.span = p.ml + round_up(p.slots * p.nt * 8 * sizeof(float2), 256);
   p.bytes = p.span + (p.splits == 0 ? round_up(static_cast<size_t>(seqs) * sizeof(int2), 256) : 0);
@@ -1127,10 +1134,10 @@ cudaError_t launch_decode(const Params& prm, int seqs, int ct, cudaStream_t stre
 template <int kHd, int kNT>
 cudaError_t launch(const Params& prm, Ctas ctas, int seqs, int ct, cudaStream_t stream) {
   if (ctas == kWideCtas) return launch_decode<kHd, kNT, kWideCtas>(prm, seqs, ct, stream);
-  if (ctas == kWholeCtas) return launch_decode<kHd, kNT, kWholeCtas>(prm, seqs, ct, stream);
   if (ctas == kNarrowCtas) return launch_decode<kHd, kNT, kNarrowCtas>(prm, seqs, ct, stream);
-  const cudaError_t e = launch_decode<kHd, kNT, kFillingCtas>(prm, seqs, ct, stream);
-  if (e != cudaSuccess) return e;
+  const cudaError_t e = ctas == kWholeCtas ? launch_decode<kHd, kNT, kWholeCtas>(prm, seqs, ct, stream)
+                                           : launch_decode<kHd, kNT, kFillingCtas>(prm, seqs, ct, stream);
+  if (e != cudaSuccess || prm.splits == 1) return e;
   // warps for the shards that a sequence has on average, four at a time each (100 sequences cut into 5: 19.4 us a call
   // with one warp, 25.3 with sixteen, most of them idle; 6 cut into 76: 17.9 with sixteen, 20.9 with four)
   constexpr unsigned kFrags = kNT * (kHd / 16);
