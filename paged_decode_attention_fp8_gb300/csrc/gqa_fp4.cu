@@ -51,7 +51,9 @@
 //   * A column's reference is 7 (log2) below the largest score it was taken
 //     from and moves only when a score passes it by more than 15: P stays
 //     within f16 (2^15), weights down to 2^-21 of the largest keep f16's
-//     relative precision, and most tiles need no shuffle.
+//     relative precision, and most tiles need no shuffle.  Scores past 2^22,
+//     where the rounding of such a reference would show in the weights, are
+//     taken from the largest score itself, which moves with every larger one.
 //   * The work -- every (sequence, KV head)'s tiles in one line -- is cut into
 //     equal pieces, one per CTA that fits on the GPU at once: lengths are known
 //     on the device only, so each CTA sums them itself.  A piece holds the end
@@ -87,6 +89,7 @@ constexpr int kFixed = 32;      // what a sequence costs a CTA beside its tiles,
 constexpr int kShort = 96;      // tiles up to which a sequence is not cut (200 of 94 tiles: 16.7 us, cut 18.1)
 constexpr float kBelow = 7.f;   // a reference lies this far below the largest score (log2) ...
 constexpr float kTau = 15.f;    // ... and moves when a score is this far above it
+constexpr float kFar = 4194304.f;  // 2^22 (log2): where a reference rounded to float32 is off by up to a quarter
 
 // Warps of a CTA, CTAs of an SM, tiles a warp takes at a time, and stages of its ring.  Throughput: twelve warps of up
 // to 168 registers on an SM (eight at head_dim 256, twice the accumulators), in small CTAs, so that a piece's fill and
@@ -185,6 +188,8 @@ __device__ __forceinline__ int32_t ldg_now(const uint8_t* p) {
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar; }
 
 // finish_row, with a NaN sum passed on (finish_row takes one for no key at all).
 __device__ __forceinline__ void finish(float m, float l, float sink, float v_scale, float* f, float* lse) {
@@ -507,9 +512,12 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
     const int full_end = min(keys_end, prm.q_len == 1 && prm.spec_mask == nullptr ? s_k : max(0, start));
     const int full_lo = prm.window > 0 ? max(0, s_k - prm.window) : 0;
 
-    // u = score * cq (log2 units); p = 2^(u + neg_m); a score above `limit` moves the reference
+    // u = score * cq (log2 units); p = 2^(u + neg_m); a score above `limit` moves the reference.  Past kFar the
+    // rounding of neg_m would take p out of f16's range (from 2^28 on by more than 2^8), so there the reference is
+    // the largest score itself, held in `limit`: p = 2^((score - limit) cq + kBelow), and neg_m is for the merge.
     float o[kNT][kSteps][4];
     float neg_m[kNT][2], limit[kNT][2], l[kNT][2];
+    bool any_far = false;  // whether a column of this warp is there
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
 #pragma unroll
@@ -634,9 +642,11 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             if (!(mx <= limit[n][k])) {
               const float m = mx * cq[n][k] - kBelow;
-              const float alpha = limit[n][k] == kNegInf ? 0.f : ex2_approx(-neg_m[n][k] - m);
+              float down = -neg_m[n][k] - m;
+              if (is_far(m) && is_far(neg_m[n][k])) down = (limit[n][k] - mx) * cq[n][k];
+              const float alpha = limit[n][k] == kNegInf ? 0.f : ex2_approx(down);
               neg_m[n][k] = -m;
-              limit[n][k] = (m + kTau) / cq[n][k];
+              limit[n][k] = is_far(m) ? mx : (m + kTau) / cq[n][k];
               l[n][k] *= alpha;
 #pragma unroll
               for (int j = 0; j < kSteps; ++j) {
@@ -645,6 +655,10 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
               }
             }
           }
+        bool far = false;
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) far |= is_far(neg_m[n][0]) || is_far(neg_m[n][1]);
+        any_far = __any_sync(0xffffffffu, far);
       }
       uint32_t pf[kU][kNT][2];
 #pragma unroll
@@ -653,7 +667,14 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
         for (int n = 0; n < kNT; ++n) {
           float p[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) p[k] = ex2_approx(fmaf(s[u][n][k], cq[n][k & 1], neg_m[n][k & 1]));
+          for (int k = 0; k < 4; ++k) p[k] = fmaf(s[u][n][k], cq[n][k & 1], neg_m[n][k & 1]);
+          if (any_far) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (is_far(neg_m[n][k & 1])) p[k] = fmaf(s[u][n][k] - limit[n][k & 1], cq[n][k & 1], kBelow);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) p[k] = ex2_approx(p[k]);
           if constexpr (kMasked) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
