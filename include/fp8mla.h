@@ -367,7 +367,9 @@ FP8MLA_API fp8mla_status_t rotary_table(const double* inv_freq, int half, int64_
  *   q, k          dtype [n_tokens, heads, head_dim], token and head strides in
  *                 elements, the dims of a head contiguous
  *   q_out, k_out  the same shapes with strides of their own; may be q and k
- *                 (in place), must not overlap them otherwise
+ *                 (in place).  Else no row of an output may overlap another
+ *                 row or an input (refused; so are tensors of different
+ *                 strides whose extents meet)
  *   positions     int32 or (positions_64 != 0) int64 [n_tokens] (device)
  *   table         float32 [n_positions, rot / 2, 2], 8-byte aligned
  *   inverse       1: turn by the negative angle (the transpose: the gradient of
@@ -415,7 +417,8 @@ FP8MLA_API fp8mla_status_t rotary_apply(const void* q, int64_t q_token_stride, i
  *                 one of them; FP8MLA_KV_E2M1: k_scale and k_block_scales
  *                 (written).  The same for v
  *   q, q_out      bf16 [n_tokens, h_q, head_dim] or NULL; q_out contiguous,
- *                 rotated like K
+ *                 rotated like K; may be q
+ * What is written (caches, scales, q_out) overlaps nothing else (refused).
  * The rotated row is quantised from float32.  E4M3 rows follow
  * fp8_paged_cache_write's arithmetic; an E2M1 block stores
  * s8 = E4M3(amax * fp32(1 / fp32(6 scale))) and codes
@@ -441,7 +444,8 @@ FP8MLA_API fp8mla_status_t paged_kv_append(
  *   scales        as paged_kv_append: scale, row_scales, or scale and
  *                 block_scales (E2M1)
  *   out           bf16 [n, h_kv, head_dim], 16-byte aligned.  A negative slot
- *                 gives zeros; one past the cache too, with FP8MLA_DEV_BAD_SLOT
+ *                 gives zeros; one past the cache too, with FP8MLA_DEV_BAD_SLOT.
+ *                 Overlaps neither the cache nor its scales (refused)
  * head_dim a multiple of 8 (16 for E2M1) up to 1024. */
 FP8MLA_API fp8mla_status_t paged_cache_read(const void* cache, fp8mla_kv_dtype_t kv_dtype, const float* scale,
                                             const float* row_scales, const void* block_scales, const int32_t* slots,
@@ -464,6 +468,7 @@ FP8MLA_API fp8mla_status_t paged_cache_read(const void* cache, fp8mla_kv_dtype_t
  *   workspace    >= paged_gqa_fp4_workspace_bytes with max_seqlen the block
  *                table's max_blocks * page_size, 256-byte aligned; may be
  *                NULL when that is 0
+ *   out may be q; out, lse, workspace and q do not overlap otherwise (refused)
  * Products take K and V exactly and Q as it is; P is rounded to f16.  A NaN
  * reaches the rows that see its key, and those alone.  Scores may be of any
  * size that float32 holds in units of log2.

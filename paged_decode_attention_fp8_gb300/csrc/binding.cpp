@@ -93,7 +93,7 @@ void need_heads(const Tensor& x, const char* name, ScalarType type, const c10::D
   if (x.size(2) > 1 && x.stride(2) != 1) bad(std::string(name) + ": the dims of a head must be contiguous");
 }
 
-// The same for an output: no two of its rows may share memory.
+// The same for an output.  (Rows that share memory in other ways than these are refused by the library.)
 void need_heads_out(const Tensor& x, const char* name, c10::IntArrayRef shape, ScalarType type,
                     const c10::Device& dev) {
   need_heads(x, name, type, dev, shape[0], shape[2]);

@@ -72,6 +72,7 @@
 
 #include "common.cuh"
 #include "gqa_fp4.h"
+#include "host_util.h"
 
 namespace fp8mla {
 
@@ -1208,6 +1209,13 @@ fp8mla_status_t fp4_decode_entry(const Fp4DecodeArgs& a, cudaStream_t stream) {
   }
   const long long seqs = static_cast<long long>(a.bs) * a.h_kv;
   if (seqs * std::max(plan.splits, 1) > 0x7FFFFFFFll) return FP8MLA_ERR_INVALID_ARG;
+  // the output may take the queries' place (a row is written after its last reader); nothing else is shared
+  const uint64_t rows = static_cast<uint64_t>(a.bs) * a.q_len * a.h_q;
+  const Rows q = block_of(a.q, rows * a.head_dim * 2), out = block_of(a.out, rows * a.head_dim * 2);
+  const Rows lse = block_of(a.lse, rows * 4), ws = block_of(a.workspace, plan.bytes);
+  if (clobbers(out, q) || rows_overlap(lse, q) || rows_overlap(ws, q) || rows_overlap(out, lse) ||
+      rows_overlap(out, ws) || rows_overlap(lse, ws))
+    return FP8MLA_ERR_INVALID_ARG;
   fp4::Params p;
   p.q = static_cast<const uint16_t*>(a.q);
   p.k = static_cast<const uint8_t*>(a.k_cache);

@@ -35,6 +35,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "host_util.h"
 #include "kv_append.h"
 
 namespace fp8mla {
@@ -527,6 +528,35 @@ int kind_of(fp8mla_kv_dtype_t t, const void* scale, const void* row_scales, cons
   return scale != nullptr ? kTensor : kRowScales;
 }
 
+// Whether what an append writes overlaps: caches, scales and the rotated queries each other, or a tensor that it reads
+// (the rotated queries may take the queries' place).
+bool shares_memory(const KvAppendArgs& a, int kind, bool has_v) {
+  const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.page_size * a.h_kv;
+  Rows written[7], read[3];
+  int w = 0, r = 0;
+  for (int i = 0; i < (has_v ? 2 : 1); ++i) {
+    const CacheSide& s = a.side[i];
+    written[w++] = block_of(s.cache, rows * a.head_dim / (kind == kFp4 ? 2 : 1));
+    if (kind == kRowScales) written[w++] = block_of(s.row_scales, rows * 4);
+    if (kind == kFp4) written[w++] = block_of(s.block_scales, rows * a.head_dim / 16);
+    read[r++] = rows_of(s.x, s.token, s.head, a.n_tokens, a.h_kv, a.head_dim, 2);
+  }
+  const Rows q = rows_of(a.q, a.q_token, a.q_head, a.n_tokens, a.h_q, a.head_dim, 2);
+  if (a.q != nullptr) {
+    const Rows out = rows_of(a.q_out, static_cast<int64_t>(a.h_q) * a.head_dim, a.head_dim, a.n_tokens, a.h_q,
+                             a.head_dim, 2);
+    if (!same_rows(out, q)) read[r++] = q;
+    written[w++] = out;
+  }
+  for (int i = 0; i < w; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (rows_overlap(written[i], written[j])) return true;
+    for (int j = 0; j < r; ++j)
+      if (rows_overlap(written[i], read[j])) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 fp8mla_status_t kv_append_entry(const KvAppendArgs& a, cudaStream_t stream) {
@@ -562,6 +592,7 @@ fp8mla_status_t kv_append_entry(const KvAppendArgs& a, cudaStream_t stream) {
   if (a.q != nullptr && (a.q_out == nullptr || misaligned(a.q, 16) || misaligned(a.q_out, 16) ||
                          (a.q_token | a.q_head) % 8 != 0))
     return FP8MLA_ERR_INVALID_ARG;
+  if (shares_memory(a, kind, has_v)) return FP8MLA_ERR_INVALID_ARG;
   Params p;
   for (int i = 0; i < 2; ++i) {
     const CacheSide& s = a.side[i];
@@ -617,6 +648,12 @@ fp8mla_status_t cache_read_entry(const CacheReadArgs& a, cudaStream_t stream) {
   if (a.n == 0) return FP8MLA_OK;
   if (a.cache == nullptr || a.slots == nullptr || a.out == nullptr || misaligned(a.cache, 16) ||
       misaligned(a.out, 16) || misaligned(a.scale, 4) || misaligned(a.row_scales, 4))
+    return FP8MLA_ERR_INVALID_ARG;
+  const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.page_size * a.h_kv;
+  const Rows out = block_of(a.out, static_cast<uint64_t>(a.n) * a.h_kv * a.head_dim * 2);
+  if (rows_overlap(out, block_of(a.cache, rows * a.head_dim / (kind == kFp4 ? 2 : 1))) ||
+      rows_overlap(out, block_of(a.row_scales, rows * 4)) ||
+      rows_overlap(out, block_of(a.block_scales, rows * a.head_dim / 16)))
     return FP8MLA_ERR_INVALID_ARG;
   ReadParams p;
   p.cache = static_cast<const uint8_t*>(a.cache);

@@ -30,6 +30,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "host_util.h"
 #include "rotary.h"
 
 namespace fp8mla {
@@ -284,12 +285,21 @@ fp8mla_status_t rotary_apply_entry(const RotaryArgs& a, cudaStream_t stream) {
         reinterpret_cast<uintptr_t>(a.out[w]) % size)
       return FP8MLA_ERR_INVALID_ARG;
   }
+  if (a.dtype != FP8MLA_BF16 && a.dtype != FP8MLA_F16 && a.dtype != FP8MLA_F32) return FP8MLA_ERR_UNSUPPORTED_DTYPE;
+  // an output takes its own input's place or no tensor's: rows are read and written by many threads in any order
+  Rows in[2], out[2];
+  for (int w = 0; w < 2; ++w) {
+    in[w] = rows_of(a.x[w], a.x_token[w], a.x_head[w], a.n_tokens, a.heads[w], a.head_dim, size);
+    out[w] = rows_of(a.out[w], a.out_token[w], a.out_head[w], a.n_tokens, a.heads[w], a.head_dim, size);
+  }
+  if (rows_overlap_themselves(out[0]) || rows_overlap_themselves(out[1]) || rows_overlap(out[0], out[1]) ||
+      clobbers(out[0], in[0]) || clobbers(out[1], in[1]) || rows_overlap(out[0], in[1]) || rows_overlap(out[1], in[0]))
+    return FP8MLA_ERR_INVALID_ARG;
   cudaError_t e;
   switch (a.dtype) {
     case FP8MLA_BF16: e = launch_rotary<__nv_bfloat16>(a, stream); break;
     case FP8MLA_F16: e = launch_rotary<__half>(a, stream); break;
-    case FP8MLA_F32: e = launch_rotary<float>(a, stream); break;
-    default: return FP8MLA_ERR_UNSUPPORTED_DTYPE;
+    default: e = launch_rotary<float>(a, stream); break;
   }
   return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
 }
