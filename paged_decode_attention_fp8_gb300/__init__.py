@@ -563,6 +563,8 @@ def rotary_table(inv_freq: torch.Tensor, n_positions: int, *, factor: float = 1.
                  out: torch.Tensor | None = None) -> torch.Tensor:
     """float32 [n_positions, len(inv_freq), 2]: (cos, sin) of position * inv_freq, times factor.
     inv_freq float64 [rot / 2] (moved to `device`, by default its own or the current one)."""
+    if torch.is_grad_enabled() and (inv_freq.requires_grad or (out is not None and out.requires_grad)):
+        raise ValueError("a tensor requires a gradient, which this call does not carry")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
         raise ValueError("inv_freq must be float64 [rot / 2]")
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
@@ -593,7 +595,10 @@ def rotary_apply(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     interleaved; the others are copied.  inverse=True turns back (the transpose: the gradient of the
     rotation).  A token with a negative position is padding: its output rows are left as they are.
     q_out / k_out may be q / k (in place), strided like them; else an output's rows overlap neither each other nor
-    another tensor.  New contiguous tensors when not given.  Returns (q_out, k_out)."""
+    another tensor.  New contiguous tensors when not given.  Returns (q_out, k_out).
+
+    No gradient is recorded, here or in the calls below: while autograd records, a tensor that requires one
+    is refused.  A training step calls both directions from a torch.autograd.Function."""
     return _native().rotary_apply(q, k, positions, table, interleaved, rot_offset, inverse, q_out, k_out)
 
 

@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -18,6 +19,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <string>
 
 #include "fp8mla.h"
@@ -67,6 +69,19 @@ bool truth(PyObject* o) {
   const int x = PyObject_IsTrue(o);
   if (x < 0) throw PyFailure{};
   return x != 0;
+}
+
+// The calls record nothing for autograd: a tensor whose gradient would be lost is refused.
+void need_no_grad(std::initializer_list<const Tensor*> tensors) {
+  if (!at::GradMode::is_enabled()) return;
+  for (const Tensor* t : tensors)
+    if (t != nullptr && t->requires_grad())
+      bad("a tensor requires a gradient, which this call does not carry: detach it, or call under torch.no_grad()");
+}
+// After the call: autograd must not take what it saved of these tensors for their present values.
+void written(std::initializer_list<const Tensor*> tensors) {
+  for (const Tensor* t : tensors)
+    if (t != nullptr && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
 }
 
 void* ptr(const Tensor* t) { return t == nullptr ? nullptr : t->data_ptr(); }
@@ -221,6 +236,8 @@ PyObject* py_rotary_apply(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const Tensor* k = maybe(a[1], "k");
     const Tensor& pos = given(a[2], "positions");
     const Tensor& table = given(a[3], "table");
+    const Tensor *q_out = maybe(a[7], "q_out"), *k_out = maybe(a[8], "k_out");
+    need_no_grad({&q, k, &table, q_out, k_out});
     const ScalarType type = q.scalar_type();
     if (!q.is_cuda() || (type != ScalarType::BFloat16 && type != ScalarType::Half && type != ScalarType::Float))
       bad("q must be a CUDA tensor of bfloat16, float16 or float32");
@@ -231,8 +248,6 @@ PyObject* py_rotary_apply(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (k != nullptr) need_heads(*k, "k", type, dev, n, hd);
     const int wide = need_positions(pos, dev, n);
     need_table(table, dev);
-    const Tensor* q_out = maybe(a[7], "q_out");
-    const Tensor* k_out = maybe(a[8], "k_out");
     if (k_out != nullptr && k == nullptr) bad("k_out without k");
     const c10::cuda::CUDAGuard guard(dev);
     Tensor q_new, k_new;
@@ -260,6 +275,7 @@ PyObject* py_rotary_apply(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                        dim32(2 * table.size(1), "rot"), small(a[5], "rot_offset"), truth(a[4]) ? 1 : 0,
                        truth(a[6]) ? 1 : 0, stream_of(dev)),
           "rotary_apply");
+    written({q_out, k_out});
     PyObject* qo = wrap(q_out, a[7]);
     PyObject* ko = k == nullptr ? Py_NewRef(Py_None) : wrap(k_out, a[8]);
     if (qo == nullptr || ko == nullptr) {
@@ -291,6 +307,7 @@ PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const Tensor *kb = maybe(a[13], "k_block_scales"), *vb = maybe(a[14], "v_block_scales");
     const Tensor* q = maybe(a[15], "q");
     const Tensor* q_out = maybe(a[16], "q_out");
+    need_no_grad({&k0, v0, &kc, vc, table, ks, vs, kr, vr, kb, vb, q, q_out});
     if (!k0.is_cuda() || k0.scalar_type() != ScalarType::BFloat16) bad("k must be a CUDA bf16 tensor");
     const c10::Device dev = k0.device();
     const Tensor k = k0.dim() == 2 ? k0.unsqueeze(1) : k0;
@@ -348,6 +365,7 @@ PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                           q != nullptr ? q->stride(1) : 0, ptr(q_out), q != nullptr ? dim32(q->size(1), "h_q") : 0,
                           stream_of(dev)),
           "paged_kv_append");
+    written({&kc, vc, kr, vr, kb, vb, q_out});
     if (q == nullptr) return Py_NewRef(Py_None);
     return wrap(q_out, a[16]);
   });
@@ -362,6 +380,7 @@ PyObject* py_cache_read(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const Tensor *scale = maybe(a[2], "scale"), *rows = maybe(a[3], "row_scales");
     const Tensor* blocks = maybe(a[4], "block_scales");
     const Tensor* out = maybe(a[5], "out");
+    need_no_grad({&cache, scale, rows, blocks, out});
     if (!cache.is_cuda()) bad("cache must be a CUDA tensor");
     const c10::Device dev = cache.device();
     const fp8mla_kv_dtype_t code = kv_code(cache, blocks);
@@ -383,6 +402,7 @@ PyObject* py_cache_read(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                            ptr_as<const int32_t>(&slots), dim32(n, "n"), dim32(s.h_kv, "h_kv"), dim32(hd, "head_dim"),
                            dim32(s.page, "page"), dim32(s.blocks, "num_blocks"), out->data_ptr(), stream_of(dev)),
           "paged_cache_read");
+    written({out});
     return wrap(out, a[5]);
   });
 }
@@ -400,6 +420,7 @@ PyObject* py_decode_fp4(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const Tensor *ks = maybe(a[7], "k_scale"), *vs = maybe(a[8], "v_scale");
     const Tensor *mask = maybe(a[10], "spec_mask"), *sinks = maybe(a[12], "sinks");
     const Tensor *out = maybe(a[14], "out"), *lse = maybe(a[15], "lse"), *ws = maybe(a[16], "workspace");
+    need_no_grad({&q, &kc, &vc, kb, vb, ks, vs, sinks, out, lse});
     if (!q.is_cuda() || q.scalar_type() != ScalarType::BFloat16 || (q.dim() != 3 && q.dim() != 4) ||
         !q.is_contiguous())
       bad("q must be a contiguous CUDA bf16 tensor [bs, q_len, h_q, hd] or [bs, h_q, hd]");
@@ -466,6 +487,7 @@ PyObject* py_decode_fp4(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                                out->data_ptr(), ptr_as<float>(lse), b32, hq32, hkv32, hd32, dim32(s.page, "page"),
                                stream_of(dev)),
           "paged_gqa_decode_fp4");
+    written({out, lse});
     PyObject* po = wrap(out, a[14]);
     PyObject* pl = wrap(lse, a[15]);
     if (po == nullptr || pl == nullptr) {
