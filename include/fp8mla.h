@@ -427,7 +427,8 @@ FP8MLA_API fp8mla_status_t rotary_apply(const void* q, int64_t q_token_stride, i
  * saturates (not with row scales), and a NaN is stored as NaN, in E2M1 in its
  * block's scale.  Scales are normal floats > 0 for which 6 * 448 * scale and
  * scale / 512 are normal too.  Two tokens with one
- * slot race.  Requires head_dim a multiple of 16 in [16, 1024]; with a table
+ * slot race.  Requires num_blocks * page_size < 2^31 (slots), n_tokens * heads
+ * < 2^31 and head_dim a multiple of 16 in [16, 1024]; with a table
  * rot a multiple of 16 and rot_offset of 8 (of 16 when interleaved); in E2M1
  * with the half layout rot a multiple of 32 and rot_offset of 16. */
 FP8MLA_API fp8mla_status_t paged_kv_append(
@@ -446,7 +447,8 @@ FP8MLA_API fp8mla_status_t paged_kv_append(
  *   out           bf16 [n, h_kv, head_dim], 16-byte aligned.  A negative slot
  *                 gives zeros; one past the cache too, with FP8MLA_DEV_BAD_SLOT.
  *                 Overlaps neither the cache nor its scales (refused)
- * head_dim a multiple of 8 (16 for E2M1) up to 1024. */
+ * head_dim a multiple of 8 (16 for E2M1) up to 1024, num_blocks * page_size and
+ * n * h_kv < 2^31. */
 FP8MLA_API fp8mla_status_t paged_cache_read(const void* cache, fp8mla_kv_dtype_t kv_dtype, const float* scale,
                                             const float* row_scales, const void* block_scales, const int32_t* slots,
                                             int n, int h_kv, int head_dim, int page_size, int num_blocks, void* out,

@@ -1187,9 +1187,8 @@ fp8mla_status_t fp4_decode_entry(const Fp4DecodeArgs& a, cudaStream_t stream) {
   int page_shift = 0;
   while (page_shift < 5 && (fp4::kTile << page_shift) != a.page_size) ++page_shift;
   if (page_shift == 5) return FP8MLA_ERR_INVALID_ARG;  // 16, 32, 64, 128 or 256 keys a page
-  if (static_cast<long long>(a.num_blocks) * a.page_size >= (1ll << 31) ||
-      static_cast<long long>(a.num_blocks) * a.page_size * a.h_kv >= (1ll << 32))
-    return FP8MLA_ERR_INVALID_ARG;  // rows are counted in 32 bits
+  const long long slots = static_cast<long long>(a.num_blocks) * a.page_size;
+  if (slots >= (1ll << 32) || slots * a.h_kv >= (1ll << 32)) return FP8MLA_ERR_INVALID_ARG;  // rows: 32 bits
   if (a.bs == 0) return FP8MLA_OK;
   if (a.q == nullptr || a.k_cache == nullptr || a.v_cache == nullptr || a.k_block_scales == nullptr ||
       a.v_block_scales == nullptr || a.k_scale == nullptr || a.v_scale == nullptr || a.block_table == nullptr ||

@@ -1,0 +1,27 @@
+"""Both sides of the documented size limits of the append, read-back and 4-bit decode entries (nothing is launched:
+what passes the limits is stopped by a later check, or has no token)."""
+
+import pytest
+
+from tests.test_operators_capi_cpu import _append, _decode, _read
+
+
+@pytest.mark.parametrize("h_kv,page", [(1, 256), (1, 16), (2, 256), (8, 64)])
+def test_decode_takes_fewer_than_2_to_32_rows(h_kv, page):
+    most = (1 << 32) // (h_kv * page)
+    a = dict(h_kv=h_kv, h_q=4 * h_kv, page=page, splits=2, mb=1024 // page, wsb=256)
+    assert _decode(**a, blocks=most - 1) == 3  # the workspace is too small: past every other check of sizes
+    assert _decode(**a, blocks=most) == 1
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_slots_are_below_2_to_31(page):
+    most = (1 << 31) // page
+    for call in (_append, _read):
+        assert call(n=0, h_kv=1, page=page, blocks=most - 1) == 0
+        assert call(n=0, h_kv=1, page=page, blocks=most) == 1
+
+
+def test_rows_of_a_call_are_below_2_to_31():
+    assert _append(n=(1 << 31) // 8, h_kv=8, h_q=1) == 1 and _append(n=(1 << 31) // 32, h_kv=1, h_q=32) == 1
+    assert _read(n=(1 << 31) // 8, h_kv=8) == 1
