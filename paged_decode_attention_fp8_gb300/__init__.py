@@ -612,7 +612,8 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor | None, slot_mapping: torch
                     v_block_scales=None, q: torch.Tensor | None = None, q_out: torch.Tensor | None = None):
     """Write new K and V rows into paged caches in one launch, K rotated by its position on the way.
 
-    k, v bf16 [n, h_kv, head_dim] (strided along tokens and heads; v and v_cache may be None); caches
+    k, v bf16 [n, h_kv, head_dim] (strided along tokens and heads by multiples of 8 values and 16-byte
+    aligned, like q; v and v_cache may be None); caches
     E4M3 (or uint8) [num_blocks, h_kv, page, head_dim] with k_scale (float32 [1]) or k_row_scales
     (float32 [num_blocks, h_kv, page], written), or 4-bit (uint8 [num_blocks, h_kv, page,
     head_dim / 2]) with k_scale and k_block_scales (E4M3 [num_blocks, h_kv, page, head_dim / 16],

@@ -92,6 +92,8 @@ P* ptr_as(const Tensor* t) {
 fp8mla_stream_t stream_of(const c10::Device& d) {
   return reinterpret_cast<fp8mla_stream_t>(c10::cuda::getCurrentCUDAStream(d.index()).stream());
 }
+// A dimension's stride; that of a single element means nothing and may be anything.
+int64_t stride_of(const Tensor* t, int d) { return t == nullptr || t->size(d) <= 1 ? 0 : t->stride(d); }
 int dim32(int64_t x, const char* name) {
   if (x > INT32_MAX) bad(std::string(name) + " is too large");
   return static_cast<int>(x);
@@ -267,9 +269,9 @@ PyObject* py_rotary_apply(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     }
     const fp8mla_dtype_t code =
         type == ScalarType::BFloat16 ? FP8MLA_BF16 : (type == ScalarType::Half ? FP8MLA_F16 : FP8MLA_F32);
-    auto st = [](const Tensor* t, int d) { return t == nullptr ? int64_t{0} : t->stride(d); };
-    check(rotary_apply(q.data_ptr(), q.stride(0), q.stride(1), q_out->data_ptr(), q_out->stride(0), q_out->stride(1),
-                       dim32(q.size(1), "h_q"), ptr(k), st(k, 0), st(k, 1), ptr(k_out), st(k_out, 0), st(k_out, 1),
+    check(rotary_apply(q.data_ptr(), stride_of(&q, 0), stride_of(&q, 1), q_out->data_ptr(), stride_of(q_out, 0),
+                       stride_of(q_out, 1), dim32(q.size(1), "h_q"), ptr(k), stride_of(k, 0), stride_of(k, 1),
+                       ptr(k_out), stride_of(k_out, 0), stride_of(k_out, 1),
                        k == nullptr ? 0 : dim32(k->size(1), "h_k"), code, pos.data_ptr(), wide,
                        ptr_as<const float>(&table), table.size(0), dim32(n, "n_tokens"), dim32(hd, "head_dim"),
                        dim32(2 * table.size(1), "rot"), small(a[5], "rot_offset"), truth(a[4]) ? 1 : 0,
@@ -353,17 +355,17 @@ PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       bad("q_out without q");
     }
     const bool has_v = v0 != nullptr;
-    check(paged_kv_append(k.data_ptr(), k.stride(0), k.stride(1), has_v ? v.data_ptr() : nullptr,
-                          has_v ? v.stride(0) : 0, has_v ? v.stride(1) : 0, ptr_as<const int32_t>(&slots),
+    const Tensor* pv = has_v ? &v : nullptr;
+    check(paged_kv_append(k.data_ptr(), stride_of(&k, 0), stride_of(&k, 1), ptr(pv), stride_of(pv, 0),
+                          stride_of(pv, 1), ptr_as<const int32_t>(&slots),
                           dim32(n, "n_tokens"), dim32(h_kv, "h_kv"), dim32(hd, "head_dim"), dim32(shape.page, "page"),
                           dim32(shape.blocks, "num_blocks"), code, kc.data_ptr(), ptr(vc), ptr_as<const float>(ks),
                           ptr_as<const float>(vs), ptr_as<float>(kr), ptr_as<float>(vr), ptr(kb), ptr(vb),
                           table != nullptr ? pos->data_ptr() : nullptr, wide, ptr_as<const float>(table),
                           table != nullptr ? table->size(0) : 0,
                           table != nullptr ? dim32(2 * table->size(1), "rot") : 0, small(a[8], "rot_offset"),
-                          truth(a[7]) ? 1 : 0, ptr(q), q != nullptr ? q->stride(0) : 0,
-                          q != nullptr ? q->stride(1) : 0, ptr(q_out), q != nullptr ? dim32(q->size(1), "h_q") : 0,
-                          stream_of(dev)),
+                          truth(a[7]) ? 1 : 0, ptr(q), stride_of(q, 0), stride_of(q, 1), ptr(q_out),
+                          q != nullptr ? dim32(q->size(1), "h_q") : 0, stream_of(dev)),
           "paged_kv_append");
     written({&kc, vc, kr, vr, kb, vb, q_out});
     if (q == nullptr) return Py_NewRef(Py_None);
