@@ -54,6 +54,12 @@ def _run(cmd, what: str) -> None:
         raise RuntimeError(f"{what} failed:\n{res.stdout}\n{res.stderr}")
 
 
+def _binding_for() -> str:
+    """What the binding is compiled against."""
+    import torch
+    return f"torch {torch.__version__}, Python {sys.version}"
+
+
 def _compile_binding(src: str, obj: str) -> None:
     import torch
     root = os.path.dirname(torch.__file__)
@@ -93,7 +99,13 @@ def build(verbose: bool = False, extra=(), force: bool = False) -> str:
         if force or _stale(obj, [src, *headers]):
             jobs.append((src, obj))
     bind_src, bind_obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o")
+    bind_for = os.path.join(BUILD, "binding.for")  # written after the link
     bind_stale = force or _stale(bind_obj, [bind_src, os.path.join(ROOT, "include", "fp8mla.h"), __file__])
+    if not os.path.exists(bind_for):
+        bind_stale = True
+    else:
+        with open(bind_for) as f:
+            bind_stale |= f.read() != _binding_for()
     if jobs or bind_stale:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
             futs = [ex.submit(_compile_binding, bind_src, bind_obj)] if bind_stale else []
@@ -109,6 +121,8 @@ def build(verbose: bool = False, extra=(), force: bool = False) -> str:
         os.replace(tmp, LIB)
     if bind_stale or _stale(BINDING, [bind_obj, LIB]):
         _link_binding(bind_obj)
+        with open(bind_for, "w") as f:
+            f.write(_binding_for())
     if verbose:
         print(LIB)
     return LIB
