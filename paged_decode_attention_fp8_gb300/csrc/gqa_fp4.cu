@@ -1198,6 +1198,9 @@ fp8mla_status_t fp4_decode_entry(const Fp4DecodeArgs& a, cudaStream_t stream) {
        reinterpret_cast<uintptr_t>(a.v_cache) | reinterpret_cast<uintptr_t>(a.k_block_scales) |
        reinterpret_cast<uintptr_t>(a.v_block_scales) | reinterpret_cast<uintptr_t>(a.out)) & 15u)
     return FP8MLA_ERR_INVALID_ARG;
+  if (misaligned(a.k_scale, 4) || misaligned(a.v_scale, 4) || misaligned(a.block_table, 4) ||
+      misaligned(a.seqlens, 4) || misaligned(a.sinks, 4) || misaligned(a.lse, 4))
+    return FP8MLA_ERR_INVALID_ARG;
   const long long capacity = static_cast<long long>(a.max_blocks) * a.page_size;
   if (capacity > 0x7FFFFF00ll) return FP8MLA_ERR_INVALID_ARG;
   const fp4::Plan plan =

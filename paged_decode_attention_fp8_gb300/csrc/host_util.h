@@ -26,6 +26,8 @@ inline auto once_per_device(std::atomic<uint64_t>& done, int dev, F&& set) -> de
   return r;
 }
 
+inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
 // Where the rows of a tensor [n, heads, width] lie, in bytes: row (i, h) is [at + i token + h head, ... + width).
 // A plain block of memory is one row.
 struct Rows {

@@ -518,8 +518,6 @@ cudaError_t launch_read(const ReadParams& p, int kind, cudaStream_t stream) {
   }
 }
 
-bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
-
 // The cache's kind from the scales given, or -1: E4M3 takes one scale or one per row, E2M1 one scale and the blocks'.
 int kind_of(fp8mla_kv_dtype_t t, const void* scale, const void* row_scales, const void* block_scales) {
   if (t == FP8MLA_KV_E2M1)
@@ -582,7 +580,9 @@ fp8mla_status_t kv_append_entry(const KvAppendArgs& a, cudaStream_t stream) {
     return FP8MLA_ERR_INVALID_ARG;  // nothing to rotate the queries with
   }
   if (a.n_tokens == 0) return FP8MLA_OK;
-  if (a.slot_mapping == nullptr || (a.table != nullptr && a.positions == nullptr)) return FP8MLA_ERR_INVALID_ARG;
+  if (a.slot_mapping == nullptr || misaligned(a.slot_mapping, 4)) return FP8MLA_ERR_INVALID_ARG;
+  if (a.table != nullptr && (a.positions == nullptr || misaligned(a.positions, a.positions_64 ? 8 : 4)))
+    return FP8MLA_ERR_INVALID_ARG;
   for (int i = 0; i < (has_v ? 2 : 1); ++i) {
     const CacheSide& s = a.side[i];
     if (s.x == nullptr || s.cache == nullptr || misaligned(s.x, 16) || misaligned(s.cache, 16) ||
@@ -647,7 +647,7 @@ fp8mla_status_t cache_read_entry(const CacheReadArgs& a, cudaStream_t stream) {
     return FP8MLA_ERR_INVALID_ARG;
   if (a.n == 0) return FP8MLA_OK;
   if (a.cache == nullptr || a.slots == nullptr || a.out == nullptr || misaligned(a.cache, 16) ||
-      misaligned(a.out, 16) || misaligned(a.scale, 4) || misaligned(a.row_scales, 4))
+      misaligned(a.out, 16) || misaligned(a.slots, 4) || misaligned(a.scale, 4) || misaligned(a.row_scales, 4))
     return FP8MLA_ERR_INVALID_ARG;
   const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.page_size * a.h_kv;
   const Rows out = block_of(a.out, static_cast<uint64_t>(a.n) * a.h_kv * a.head_dim * 2);

@@ -276,7 +276,8 @@ fp8mla_status_t rotary_apply_entry(const RotaryArgs& a, cudaStream_t stream) {
       a.rot > a.head_dim - a.rot_offset || a.n_positions < 1)
     return FP8MLA_ERR_INVALID_ARG;
   if (a.n_tokens == 0) return FP8MLA_OK;
-  if (a.positions == nullptr || a.table == nullptr || (reinterpret_cast<uintptr_t>(a.table) & 7u))
+  if (a.positions == nullptr || a.table == nullptr || misaligned(a.positions, a.positions_64 ? 8 : 4) ||
+      misaligned(a.table, 8))
     return FP8MLA_ERR_INVALID_ARG;
   const uintptr_t size = a.dtype == FP8MLA_F32 ? 4 : 2;
   for (int w = 0; w < 2; ++w) {
