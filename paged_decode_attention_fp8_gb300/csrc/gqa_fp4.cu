@@ -510,15 +510,15 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
     // Tiles whose keys every column sees: before the speculative block (or, for one token, the end) and, with a
     // window, from the last token's first key on.
     const int keys_end = min(s_k, t1 * kTile);  // the segment's
-    const int full_end = min(keys_end, prm.q_len == 1 && prm.spec_mask == nullptr ? s_k : max(0, start));
+    int full_end = min(keys_end, prm.q_len == 1 && prm.spec_mask == nullptr ? s_k : max(0, start));
     const int full_lo = prm.window > 0 ? max(0, s_k - prm.window) : 0;
 
     // u = score * cq (log2 units); p = 2^(u + neg_m); a score above `limit` moves the reference.  Past kFar the
     // rounding of neg_m would take p out of f16's range (from 2^28 on by more than 2^8), so there the reference is
-    // the largest score itself, held in `limit`: p = 2^((score - limit) cq + kBelow), and neg_m is for the merge.
+    // the largest score itself, held in `limit`: p = 2^((score - limit) cq + kBelow), and neg_m is for the merge.  The
+    // path for masks has the code for this; a warp that meets such a score takes it from there on (full_end = -1).
     float o[kNT][kSteps][4];
     float neg_m[kNT][2], limit[kNT][2], l[kNT][2];
-    bool any_far = false;  // whether a column of this warp is there
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
 #pragma unroll
@@ -633,6 +633,16 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
           grow |= !(top[n][k] <= limit[n][k]);  // (a NaN score moves it, and its column stays NaN)
         }
       if (__any_sync(0xffffffffu, grow)) {
+        if constexpr (!kMasked) {
+          bool far = false;
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+            far |= is_far(top[n][0] * cq[n][0] - kBelow) || is_far(top[n][1] * cq[n][1] - kBelow);
+          if (__any_sync(0xffffffffu, far)) {
+            full_end = -1;
+            return false;
+          }
+        }
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
@@ -644,10 +654,10 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
             if (!(mx <= limit[n][k])) {
               const float m = mx * cq[n][k] - kBelow;
               float down = -neg_m[n][k] - m;
-              if (is_far(m) && is_far(neg_m[n][k])) down = (limit[n][k] - mx) * cq[n][k];
+              if (kMasked && is_far(m) && is_far(neg_m[n][k])) down = (limit[n][k] - mx) * cq[n][k];
               const float alpha = limit[n][k] == kNegInf ? 0.f : ex2_approx(down);
               neg_m[n][k] = -m;
-              limit[n][k] = is_far(m) ? mx : (m + kTau) / cq[n][k];
+              limit[n][k] = kMasked && is_far(m) ? mx : (m + kTau) / cq[n][k];
               l[n][k] *= alpha;
 #pragma unroll
               for (int j = 0; j < kSteps; ++j) {
@@ -656,10 +666,12 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
               }
             }
           }
-        bool far = false;
+        if constexpr (kMasked) {
+          bool far = false;
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) far |= is_far(neg_m[n][0]) || is_far(neg_m[n][1]);
-        any_far = __any_sync(0xffffffffu, far);
+          for (int n = 0; n < kNT; ++n) far |= is_far(neg_m[n][0]) || is_far(neg_m[n][1]);
+          if (__any_sync(0xffffffffu, far)) full_end = -1;
+        }
       }
       uint32_t pf[kU][kNT][2];
 #pragma unroll
@@ -669,7 +681,7 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
           float p[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) p[k] = fmaf(s[u][n][k], cq[n][k & 1], neg_m[n][k & 1]);
-          if (any_far) {
+          if constexpr (kMasked) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               if (is_far(neg_m[n][k & 1])) p[k] = fmaf(s[u][n][k] - limit[n][k & 1], cq[n][k & 1], kBelow);
@@ -772,13 +784,13 @@ __global__ void __launch_bounds__(Shape<kHd, kNT, kCtas>::kWarps * 32, Shape<kHd
       st += kStage;
       if (st == st_end) st -= kStages * kStage;
       tok0 += stride * kTile;
+      return true;
     };
     for (int i = 0; i < n_mine; ++i) {
       cp_async_wait_group<kStages - 2>();
       __syncwarp();
       issue(i + kStages - 1, std::false_type{});
-      if (tok0 + kU * kTile <= full_end && tok0 >= full_lo) tiles(std::false_type{});
-      else tiles(std::true_type{});
+      if (tok0 + kU * kTile > full_end || tok0 < full_lo || !tiles(std::false_type{})) tiles(std::true_type{});
     }
 
     // ---- the warps' states are merged in shared memory, in fragment order
