@@ -121,6 +121,11 @@ typedef enum {
 /* Type of the values rotary_apply turns. */
 typedef enum { FP8MLA_BF16 = 0, FP8MLA_F16 = 1, FP8MLA_F32 = 2 } fp8mla_dtype_t;
 
+/* Layout of a rotated part and what becomes of padding: rotary_apply, paged_kv_append. */
+#define FP8MLA_ROTARY_INTERLEAVED 0x1 /* pairs (2i, 2i + 1), else (i, i + rot / 2) */
+#define FP8MLA_ROTARY_ZERO_Q 0x2      /* q_out's rows of tokens without a position become zeros, else are left */
+#define FP8MLA_ROTARY_ZERO_K 0x4      /* the same for k_out (rotary_apply only) */
+
 /* Device status bits reported by fp8mla_get_last_device_error. */
 #define FP8MLA_DEV_WAIT_TIMEOUT 0x1u   /* a bounded mbarrier wait ran out; the CTA stopped */
 #define FP8MLA_DEV_BAD_PAGE 0x2u       /* block-table entry outside [0, num_pages) */
@@ -372,12 +377,14 @@ FP8MLA_API fp8mla_status_t rotary_table(const double* inv_freq, int half, int64_
  *                 strides whose extents meet)
  *   positions     int32 or (positions_64 != 0) int64 [n_tokens] (device)
  *   table         float32 [n_positions, rot / 2, 2], 8-byte aligned
+ *   layout        FP8MLA_ROTARY_* bits
  *   inverse       1: turn by the negative angle (the transpose: the gradient of
  *                 the rotation, and its inverse where factor is 1)
  * Every value is computed in float32 (products and sum each rounded) and
  * rounded once; dims outside the rotated part are copied.  A token with a
  * negative position is padding: its heads are not written.  A position >=
- * n_positions sets FP8MLA_DEV_BAD_POSITION and its heads are not written.
+ * n_positions sets FP8MLA_DEV_BAD_POSITION and its heads are not written.  (Or
+ * both become zeros: see layout.)
  * Requires 2 <= head_dim <= 8192, rot even, rot_offset + rot <= head_dim.  Any
  * stride and alignment of the type works; 16-byte aligned tensors whose
  * strides and rot_offset are multiples of 8 and rot of 16 go 8 pairs at a time. */
@@ -387,7 +394,7 @@ FP8MLA_API fp8mla_status_t rotary_apply(const void* q, int64_t q_token_stride, i
                                         int64_t k_out_token_stride, int64_t k_out_head_stride, int h_k,
                                         fp8mla_dtype_t dtype, const void* positions, int positions_64,
                                         const float* table, int64_t n_positions, int n_tokens, int head_dim, int rot,
-                                        int rot_offset, int interleaved, int inverse, fp8mla_stream_t stream);
+                                        int rot_offset, int layout, int inverse, fp8mla_stream_t stream);
 
 /* ---------------------------------------------------------- 4-bit cache ---
  * A cached row of head_dim values is head_dim / 2 bytes of E2M1 codes (sign,
@@ -417,7 +424,8 @@ FP8MLA_API fp8mla_status_t rotary_apply(const void* q, int64_t q_token_stride, i
  *                 one of them; FP8MLA_KV_E2M1: k_scale and k_block_scales
  *                 (written).  The same for v
  *   q, q_out      bf16 [n_tokens, h_q, head_dim] or NULL; q_out contiguous,
- *                 rotated like K; may be q
+ *                 rotated like K; may be q.  A token without a position
+ *                 leaves its rows, or zeros them (layout)
  * What is written (caches, scales, q_out) overlaps nothing else (refused).
  * The rotated row is quantised from float32.  E4M3 rows follow
  * fp8_paged_cache_write's arithmetic; an E2M1 block stores
@@ -437,7 +445,7 @@ FP8MLA_API fp8mla_status_t paged_kv_append(
     int num_blocks, fp8mla_kv_dtype_t kv_dtype, void* k_cache, void* v_cache, const float* k_scale,
     const float* v_scale, float* k_row_scales, float* v_row_scales, void* k_block_scales, void* v_block_scales,
     const void* positions, int positions_64, const float* table, int64_t n_positions, int rot, int rot_offset,
-    int interleaved, const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out, int h_q,
+    int layout, const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out, int h_q,
     fp8mla_stream_t stream);
 
 /* paged_cache_read -- rows of a paged cache as bf16: out[i][h] is the row of

@@ -593,7 +593,8 @@ def rotary_apply(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
 
     Dims [rot_offset, rot_offset + rot) of a head turn in pairs (i, i + rot / 2), or (2i, 2i + 1) when
     interleaved; the others are copied.  inverse=True turns back (the transpose: the gradient of the
-    rotation).  A token with a negative position is padding: its output rows are left as they are.
+    rotation).  A token with a negative position is padding: its output rows are left as they are (zeros in a
+    tensor that the call makes).
     q_out / k_out may be q / k (in place), strided like them; else an output's rows overlap neither each other nor
     another tensor.  New contiguous tensors when not given.  Returns (q_out, k_out).
 
@@ -621,7 +622,8 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor | None, slot_mapping: torch
     slot_mapping int32 [n] (block * page + offset; negative = skip K and V).  With a table
     (``rotary_table``) and positions (int32 or int64 [n]; negative = padding, nothing is written) K's
     dims [rot_offset, rot_offset + rot) turn as in ``rotary_apply``, and queries q bf16
-    [n, h_q, head_dim] can be rotated along: returns them (q_out, new when not given), or None.  q_out may be q;
+    [n, h_q, head_dim] can be rotated along: returns them (q_out; new when not given, then with zeros for
+    padding), or None.  q_out may be q;
     else nothing that is written overlaps another tensor."""
     return _native().paged_kv_append(k, v, slot_mapping, k_cache, v_cache, positions, table, interleaved, rot_offset,
                                      k_scale, v_scale, k_row_scales, v_row_scales, k_block_scales, v_block_scales, q,

@@ -252,7 +252,10 @@ PyObject* py_rotary_apply(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     need_table(table, dev);
     if (k_out != nullptr && k == nullptr) bad("k_out without k");
     const c10::cuda::CUDAGuard guard(dev);
-    Tensor q_new, k_new;
+    Tensor q_new, k_new;  // nothing else will have written their rows of padding
+    int layout = truth(a[4]) ? FP8MLA_ROTARY_INTERLEAVED : 0;
+    if (q_out == nullptr) layout |= FP8MLA_ROTARY_ZERO_Q;
+    if (k_out == nullptr) layout |= FP8MLA_ROTARY_ZERO_K;
     if (q_out == nullptr) {
       q_new = make(q.sizes(), type, dev);
       q_out = &q_new;
@@ -274,8 +277,8 @@ PyObject* py_rotary_apply(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                        ptr(k_out), stride_of(k_out, 0), stride_of(k_out, 1),
                        k == nullptr ? 0 : dim32(k->size(1), "h_k"), code, pos.data_ptr(), wide,
                        ptr_as<const float>(&table), table.size(0), dim32(n, "n_tokens"), dim32(hd, "head_dim"),
-                       dim32(2 * table.size(1), "rot"), small(a[5], "rot_offset"), truth(a[4]) ? 1 : 0,
-                       truth(a[6]) ? 1 : 0, stream_of(dev)),
+                       dim32(2 * table.size(1), "rot"), small(a[5], "rot_offset"), layout, truth(a[6]) ? 1 : 0,
+                       stream_of(dev)),
           "rotary_apply");
     written({q_out, k_out});
     PyObject* qo = wrap(q_out, a[7]);
@@ -340,7 +343,9 @@ PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       wide = need_positions(*pos, dev, n);
       need_table(*table, dev);
     }
-    Tensor q_new;
+    Tensor q_new;  // nothing else will have written its rows of padding
+    const int layout =
+        (truth(a[7]) ? FP8MLA_ROTARY_INTERLEAVED : 0) | (q_out == nullptr ? FP8MLA_ROTARY_ZERO_Q : 0);
     const c10::cuda::CUDAGuard guard(dev);
     if (q != nullptr) {
       if (table == nullptr) bad("q is rotated by a table: give one");
@@ -364,7 +369,7 @@ PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                           table != nullptr ? pos->data_ptr() : nullptr, wide, ptr_as<const float>(table),
                           table != nullptr ? table->size(0) : 0,
                           table != nullptr ? dim32(2 * table->size(1), "rot") : 0, small(a[8], "rot_offset"),
-                          truth(a[7]) ? 1 : 0, ptr(q), stride_of(q, 0), stride_of(q, 1), ptr(q_out),
+                          layout, ptr(q), stride_of(q, 0), stride_of(q, 1), ptr(q_out),
                           q != nullptr ? dim32(q->size(1), "h_q") : 0, stream_of(dev)),
           "paged_kv_append");
     written({&kc, vc, kr, vr, kb, vb, q_out});

@@ -421,7 +421,7 @@ fp8mla_status_t rotary_apply(const void* q, int64_t q_token_stride, int64_t q_he
                              int64_t k_token_stride, int64_t k_head_stride, void* k_out, int64_t k_out_token_stride,
                              int64_t k_out_head_stride, int h_k, fp8mla_dtype_t dtype, const void* positions,
                              int positions_64, const float* table, int64_t n_positions, int n_tokens, int head_dim,
-                             int rot, int rot_offset, int interleaved, int inverse, fp8mla_stream_t stream) {
+                             int rot, int rot_offset, int layout, int inverse, fp8mla_stream_t stream) {
   RotaryArgs a;
   a.x[0] = q, a.x[1] = k;
   a.out[0] = q_out, a.out[1] = k_out;
@@ -438,7 +438,7 @@ fp8mla_status_t rotary_apply(const void* q, int64_t q_token_stride, int64_t q_he
   a.head_dim = head_dim;
   a.rot = rot;
   a.rot_offset = rot_offset;
-  a.interleaved = interleaved;
+  a.layout = layout;
   a.inverse = inverse;
   a.dtype = dtype;
   return rotary_apply_entry(a, reinterpret_cast<cudaStream_t>(stream));
@@ -450,7 +450,7 @@ fp8mla_status_t paged_kv_append(const void* k, int64_t k_token_stride, int64_t k
                                 fp8mla_kv_dtype_t kv_dtype, void* k_cache, void* v_cache, const float* k_scale,
                                 const float* v_scale, float* k_row_scales, float* v_row_scales, void* k_block_scales,
                                 void* v_block_scales, const void* positions, int positions_64, const float* table,
-                                int64_t n_positions, int rot, int rot_offset, int interleaved, const void* q,
+                                int64_t n_positions, int rot, int rot_offset, int layout, const void* q,
                                 int64_t q_token_stride, int64_t q_head_stride, void* q_out, int h_q,
                                 fp8mla_stream_t stream) {
   KvAppendArgs a;
@@ -467,7 +467,7 @@ fp8mla_status_t paged_kv_append(const void* k, int64_t k_token_stride, int64_t k
   a.n_positions = n_positions;
   a.rot = rot;
   a.rot_offset = rot_offset;
-  a.interleaved = interleaved;
+  a.layout = layout;
   a.n_tokens = n_tokens;
   a.h_q = h_q;
   a.h_kv = h_kv;

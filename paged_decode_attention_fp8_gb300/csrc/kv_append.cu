@@ -76,6 +76,7 @@ struct Params {
   FastDiv page;
   uint32_t num_slots;
   int positions_64, rot, rot_offset, interleaved, head_dim;
+  int zero_q;          // queries of tokens without a position become zeros
   uint32_t first[4];   // CTAs [first[i], first[i + 1]) take class i
 };
 
@@ -113,6 +114,12 @@ template <int kP>
 struct Values {
   uint4 a[kP], b[kP];
 };
+
+// Zeros for a row of queries without a position, by the lanes of its group.  (A call of its own, out of the loop's
+// registers: selecting the values instead cost the latent case 0.4 us.)
+__device__ __noinline__ void zero_row(uint8_t* row, int head_dim, int sub, int lanes) {
+  for (int c = sub; c < head_dim / 8; c += lanes) reinterpret_cast<uint4*>(row)[c] = make_uint4(0, 0, 0, 0);
+}
 
 // kL lanes a row, kP pairs of chunks a lane.  A warp's steps are a pipeline: slots and positions two steps ahead,
 // values one ahead, and the table's rows asked into L1 one ahead (where every lane has one piece: a prompt's K and V
@@ -245,6 +252,8 @@ __device__ __forceinline__ void run_class(const Params& prm, const Source& src, 
             dst[c1[j]] = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]), pack_bf16x2(b[4], b[5]),
                                     pack_bf16x2(b[6], b[7]));
           }
+      } else if (prm.zero_q && row < src.rows) {
+        zero_row(src.out + static_cast<int64_t>(row) * prm.head_dim * 2, prm.head_dim, sub, kL);
       }
       return;
     }
@@ -560,7 +569,8 @@ bool shares_memory(const KvAppendArgs& a, int kind, bool has_v) {
 fp8mla_status_t kv_append_entry(const KvAppendArgs& a, cudaStream_t stream) {
   if (a.kv_dtype != FP8MLA_KV_E4M3 && a.kv_dtype != FP8MLA_KV_E2M1) return FP8MLA_ERR_UNSUPPORTED_DTYPE;
   if (a.n_tokens < 0 || a.h_kv < 1 || a.head_dim < 16 || a.head_dim % 16 != 0 || a.head_dim > kMaxHeadDim ||
-      a.page_size < 1 || a.num_blocks < 1 || (a.q != nullptr && a.h_q < 1))
+      a.page_size < 1 || a.num_blocks < 1 || (a.q != nullptr && a.h_q < 1) || a.layout < 0 ||
+      a.layout > (FP8MLA_ROTARY_INTERLEAVED | FP8MLA_ROTARY_ZERO_Q))
     return FP8MLA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(a.n_tokens) * std::max(a.h_kv, a.q != nullptr ? a.h_q : 1) >= (1ll << 31) ||
       static_cast<int64_t>(a.num_blocks) * a.page_size >= (1ll << 31))
@@ -571,11 +581,12 @@ fp8mla_status_t kv_append_entry(const KvAppendArgs& a, cudaStream_t stream) {
   if (has_v && kind_of(a.kv_dtype, a.side[1].scale, a.side[1].row_scales, a.side[1].block_scales) != kind)
     return FP8MLA_ERR_INVALID_ARG;
   if (a.table != nullptr) {
-    if (a.rot < 16 || a.rot % 16 != 0 || a.rot_offset < 0 || a.rot_offset % (a.interleaved ? 16 : 8) != 0 ||
+    const bool interleaved = a.layout & FP8MLA_ROTARY_INTERLEAVED;
+    if (a.rot < 16 || a.rot % 16 != 0 || a.rot_offset < 0 || a.rot_offset % (interleaved ? 16 : 8) != 0 ||
         a.rot > a.head_dim - a.rot_offset || a.n_positions < 1 || a.n_positions > 0x7FFFFFFF || misaligned(a.table, 16))
       return FP8MLA_ERR_INVALID_ARG;
     // blocks of 16 values do not straddle a half layout's pieces
-    if (kind == kFp4 && !a.interleaved && (a.rot % 32 != 0 || a.rot_offset % 16 != 0)) return FP8MLA_ERR_INVALID_ARG;
+    if (kind == kFp4 && !interleaved && (a.rot % 32 != 0 || a.rot_offset % 16 != 0)) return FP8MLA_ERR_INVALID_ARG;
   } else if (a.q != nullptr) {
     return FP8MLA_ERR_INVALID_ARG;  // nothing to rotate the queries with
   }
@@ -618,7 +629,8 @@ fp8mla_status_t kv_append_entry(const KvAppendArgs& a, cudaStream_t stream) {
   p.num_slots = static_cast<uint32_t>(static_cast<int64_t>(a.num_blocks) * a.page_size);
   p.rot = a.rot;
   p.rot_offset = a.rot_offset;
-  p.interleaved = a.interleaved;
+  p.interleaved = a.layout & FP8MLA_ROTARY_INTERLEAVED;
+  p.zero_q = a.layout & FP8MLA_ROTARY_ZERO_Q;
   p.head_dim = a.head_dim;
   const int pairs = a.head_dim / 16;
   cudaError_t e;

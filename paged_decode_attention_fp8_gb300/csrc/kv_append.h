@@ -28,7 +28,7 @@ struct KvAppendArgs {
   int positions_64;
   const float* table;            // null: no rotation
   int64_t n_positions;
-  int rot, rot_offset, interleaved;
+  int rot, rot_offset, layout;
   int n_tokens, h_q, h_kv, head_dim, page_size, num_blocks;
   fp8mla_kv_dtype_t kv_dtype;
 };

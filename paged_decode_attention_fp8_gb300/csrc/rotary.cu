@@ -97,11 +97,29 @@ struct Params {
   const void* positions;
   const float2* table;
   int64_t n_positions;
-  int n_tokens, rot, rot_offset, inverse, positions_64;
+  int n_tokens, rot, rot_offset, inverse, positions_64, head_dim;
+  int zero;         // bit w: out[w]'s rows of tokens without a position become zeros
   int units;        // pieces of a head: rotated ones, then (unless in place) copied ones
   int rot_units;
   int unit_lanes, head_lanes, token_lanes;  // a thread's piece, head and token within its block
 };
+
+// Zeros for the rows of this thread's token, which has no position: its share of the dims of its heads.  (A call of its
+// own, so that the kernel's registers do not know of it.)
+template <typename T, int kV>
+__device__ __noinline__ void zero_rows(const Params& prm) {
+  const int ul = threadIdx.x % prm.unit_lanes;
+  const int hl = threadIdx.x / prm.unit_lanes % prm.head_lanes;
+  const int64_t token =
+      static_cast<int64_t>(blockIdx.x) * prm.token_lanes + threadIdx.x / (prm.unit_lanes * prm.head_lanes);
+  const Vec<T, kV> none = {};
+  for (int w = 0; w < 2; ++w) {
+    if (!((prm.zero >> w) & 1)) continue;
+    for (int h = hl; h < prm.heads[w]; h += prm.head_lanes)
+      for (int d = ul * kV; d < prm.head_dim; d += prm.unit_lanes * kV)
+        none.store(static_cast<T*>(prm.out[w]) + token * prm.out_token[w] + h * prm.out_head[w] + d);
+  }
+}
 
 // kV: pairs of a piece (8, or 1 where the sizes, strides or addresses do not allow 16-byte accesses); a copied
 // piece is kV values.
@@ -154,7 +172,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas) rotary_kernel(const
             b[k].load(p + d1);
           }
         }
-        if (skipped()) return;
+        if (skipped()) {
+          if (prm.zero != 0) zero_rows<T, kV>(prm);
+          return;
+        }
         if (h0 == hl) {
           const float2* row = prm.table + pos * (prm.rot / 2) + kV * u;
           if constexpr (kV == 1) {
@@ -200,7 +221,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T>::kCtas) rotary_kernel(const
         }
       }
     } else {  // a copied piece, outside the rotated part
-      if (skipped()) return;
+      if (skipped()) {
+        if (prm.zero != 0) zero_rows<T, kV>(prm);
+        return;
+      }
       int d = (u - prm.rot_units) * kV;
       if (d >= prm.rot_offset) d += prm.rot;
       for (int h = hl; h < heads; h += prm.head_lanes) {
@@ -237,6 +261,8 @@ cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t stream) {
   p.rot = a.rot;
   p.rot_offset = a.rot_offset;
   p.inverse = a.inverse;
+  p.head_dim = a.head_dim;
+  p.zero = a.layout / FP8MLA_ROTARY_ZERO_Q;
   p.rot_units = a.rot / (2 * v);
   p.units = p.rot_units + (in_place ? 0 : (a.head_dim - a.rot) / v);
   const int heads = a.heads[0] + a.heads[1];
@@ -247,9 +273,9 @@ cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t stream) {
   const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.n_tokens) + p.token_lanes - 1) / p.token_lanes);
   const dim3 grid(blocks), block(threads);
   if (wide)
-    return a.interleaved ? launch_dependent(rotary_kernel<T, 8, true>, grid, block, 0, stream, p)
+    return a.layout & FP8MLA_ROTARY_INTERLEAVED ? launch_dependent(rotary_kernel<T, 8, true>, grid, block, 0, stream, p)
                          : launch_dependent(rotary_kernel<T, 8, false>, grid, block, 0, stream, p);
-  return a.interleaved ? launch_dependent(rotary_kernel<T, 1, true>, grid, block, 0, stream, p)
+  return a.layout & FP8MLA_ROTARY_INTERLEAVED ? launch_dependent(rotary_kernel<T, 1, true>, grid, block, 0, stream, p)
                        : launch_dependent(rotary_kernel<T, 1, false>, grid, block, 0, stream, p);
 }
 
@@ -273,7 +299,8 @@ fp8mla_status_t rotary_table_entry(const double* inv_freq, int half, int64_t n_p
 fp8mla_status_t rotary_apply_entry(const RotaryArgs& a, cudaStream_t stream) {
   if (a.n_tokens < 0 || a.heads[0] < 1 || a.heads[1] < 0 || a.heads[0] > (1 << 20) || a.heads[1] > (1 << 20) ||
       a.head_dim < 2 || a.head_dim > 8192 || a.rot < 2 || a.rot % 2 != 0 || a.rot_offset < 0 ||
-      a.rot > a.head_dim - a.rot_offset || a.n_positions < 1)
+      a.rot > a.head_dim - a.rot_offset || a.n_positions < 1 || a.layout < 0 ||
+      a.layout > (FP8MLA_ROTARY_INTERLEAVED | FP8MLA_ROTARY_ZERO_Q | FP8MLA_ROTARY_ZERO_K))
     return FP8MLA_ERR_INVALID_ARG;
   if (a.n_tokens == 0) return FP8MLA_OK;
   if (a.positions == nullptr || a.table == nullptr || misaligned(a.positions, a.positions_64 ? 8 : 4) ||

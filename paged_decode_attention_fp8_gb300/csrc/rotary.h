@@ -18,7 +18,7 @@ struct RotaryArgs {
   int positions_64;
   const float* table;        // [n_positions, rot / 2, 2]
   int64_t n_positions;
-  int n_tokens, head_dim, rot, rot_offset, interleaved, inverse;
+  int n_tokens, head_dim, rot, rot_offset, layout, inverse;
   fp8mla_dtype_t dtype;
 };
 

@@ -38,3 +38,8 @@ def test_misaligned_indexes_and_scales_are_refused(call, over):
              _append: dict(v=2 * P, kc=3 * P, vc=4 * P, k_blk=5 * P, v_blk=6 * P, q=7 * P, qo=8 * P),
              _read: dict(cache=2 * P, blk=3 * P, out=4 * P), _decode: dict(q=2 * P, out=3 * P, lse=4 * P)}[call]
     assert call(**{**apart, **over}) == 1
+
+
+def test_unknown_layout_bits_are_refused():
+    assert _apply(inter=8) == 1 and _apply(inter=-1) == 1 and _append(n=0, inter=4) == 1 and _append(n=0, inter=-1) == 1
+    assert _apply(n=0, inter=7) == 0 and _append(n=0, inter=3) == 0
