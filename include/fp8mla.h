@@ -473,13 +473,16 @@ FP8MLA_API fp8mla_status_t paged_cache_read(const void* cache, fp8mla_kv_dtype_t
  *                about 1000 up with few sequences, more as they come to fill the
  *                GPU), one CTA where the sequences fill it many times
  *                over, else the keys of all sequences cut into equal pieces,
- *                one per CTA that fits on the GPU; 1 = one CTA each; k > 1 = every sequence in k shards, at most one per
- *                128 keys of the block table
+ *                one per CTA that fits on the GPU; 1 = one CTA each; k > 1 =
+ *                every sequence in k shards, at most one per 128 keys of the
+ *                block table (the way to cut one long context among very many
+ *                short ones, which auto leaves whole)
  *   workspace    >= paged_gqa_fp4_workspace_bytes with max_seqlen the block
  *                table's max_blocks * page_size, 256-byte aligned; may be
  *                NULL when that is 0
  *   out may be q; out, lse, workspace and q do not overlap otherwise (refused)
- * Products take K and V exactly and Q as it is; P is rounded to f16.  A NaN
+ * Products take K and V exactly, Q's values from 2^-31 of a head's largest on
+ * exactly (others to 2^-39 of it); P is rounded to f16.  A NaN
  * reaches the rows that see its key, and those alone.  Scores may be of any
  * size that float32 holds in units of log2.
  * Scales are normal floats > 0.  Requires head_dim 64, 128 or 256, page_size

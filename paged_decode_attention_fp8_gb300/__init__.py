@@ -619,8 +619,8 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor | None, slot_mapping: torch
     (float32 [num_blocks, h_kv, page], written), or 4-bit (uint8 [num_blocks, h_kv, page,
     head_dim / 2]) with k_scale and k_block_scales (E4M3 [num_blocks, h_kv, page, head_dim / 16],
     written); the same for V.  The dense MLA cache [num_pages, page, d] takes k [n, d] or [n, 1, d].
-    slot_mapping int32 [n] (block * page + offset; negative = skip K and V).  With a table
-    (``rotary_table``) and positions (int32 or int64 [n]; negative = padding, nothing is written) K's
+    slot_mapping int32 [n] (block * page + offset; negative = skip K and V; two tokens with one slot race).
+    With a table (``rotary_table``) and positions (int32 or int64 [n]; negative = padding, nothing is written) K's
     dims [rot_offset, rot_offset + rot) turn as in ``rotary_apply``, and queries q bf16
     [n, h_q, head_dim] can be rotated along: returns them (q_out; new when not given, then with zeros for
     padding), or None.  q_out may be q;

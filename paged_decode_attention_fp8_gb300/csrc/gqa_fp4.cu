@@ -14,13 +14,15 @@
 // conversion and a multiplication for two codes, which issue at half rate, so
 // the instructions that make operands and the memory are both close to their
 // limit.  Measured (32 contexts of 1024 to 16384 keys, 8 KV heads, head_dim
-// 128, group 4): 63.4 us a call, 0.77 of the measured copy bandwidth; leaving
-// the loads out would save 1.5 us, the scale multiplications 9.5, the
-// conversions of V 10.  Sixteen columns double the products and leave twelve
-// warps less to hide with: four-token blocks under a 4096-key window 45.7 us,
-// 0.45.  head_dim 64 halves the bytes of a tile but not its overhead: three
-// contexts of 50k to 131k keys 17.9 us, 0.37, of which 8 are the lengths' sums,
-// the first tiles, the merge and two launches.
+// 128, group 4): 64.4 us a call, 0.75 of the measured copy bandwidth (head_dim
+// 256, 4 KV heads 0.77); leaving the loads out would save 1.5 us, the scale
+// multiplications 9.5, the conversions of V 10.  Sixteen columns double the
+// products and leave twelve warps less to hide with: four-token blocks under a
+// 4096-key window 47.5 us, 0.44, without the window 0.55.  More columns convert
+// K and V once for every sixteen: 32 columns 166 us, 0.30.  head_dim 64 halves
+// the bytes of a tile but not its overhead: the batch 0.55, three contexts of
+// 50k to 131k keys 18.8 us, 0.35, of which 8 are the lengths' sums, the first
+// tiles, the merge and two launches.
 //
 // Design:
 //   * A warp works alone on tiles of 16 keys: it fetches them into its own
@@ -46,8 +48,12 @@
 //     same pairs come out of the probabilities' transpose.
 //   * E2M1 * E4M3 has at most six significant bits and lies in f16's range
 //     (subnormals included), so K and V operands are exact.  Q is bf16 times
-//     a power of two per column, exact in f16 down to 2^-38 of its largest
-//     value; P is rounded to f16 (half a step: 2^-11), sums are f32.
+//     a power of two per column, which puts its largest value into [2^14,
+//     2^15): exact in f16 from 2^-31 of that value on, smaller ones off by at
+//     most 2^-39 of it (more where the largest is below 2^-86).  P is rounded
+//     to f16 (half a step: 2^-11) and its sum is not: a second f16 term of P
+//     would double the products to take 1 % off the output's error, which is
+//     bf16's rounding.  Sums are f32.
 //   * A column's reference is 7 (log2) below the largest score it was taken
 //     from and moves only when a score passes it by more than 15: P stays
 //     within f16 (2^15), weights down to 2^-21 of the largest keep f16's
@@ -62,8 +68,9 @@
 //     Few sequences of short contexts, for which two launches are too many, go
 //     uncut, to one CTA of up to sixteen warps each or to a cluster of two to
 //     eight, whose CTAs take their tiles in turn and merge over the cluster's
-//     shared memory (one context of 777 keys, 8 KV heads: 6.5 us a call; one
-//     CTA each 8.2).
+//     shared memory (one context of 777 keys, 8 KV heads: 6.8 us a call; one
+//     CTA each 8.2; through pieces, where the block table holds more keys than
+//     the rule allows, 8.4 instead of 7.2).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -1066,8 +1073,10 @@ Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long cap
   const int resident = device_sms() * (head_dim == 256 ? 2 : 3);  // Shape::kPerSm
   p.units = 0;
   p.kind = kWholeCtas;
-  // Few sequences: an SM's warps in one CTA, and CTAs in a cluster, which merges without a second kernel, as far as
-  // clusters of that size fit on the GPU at once (eight CTAs 15 times, four 36 times).  A cluster's merge takes 1.4 us,
+  // Few sequences: an SM's warps in one CTA, and CTAs in a cluster, which merges without a second kernel, while
+  // clusters of that size surely fit on the GPU at once: eight CTAs up to a twelfth of the SMs, four up to 4 / 19, two
+  // up to 9 / 19 (of 152 SMs 12, 32 and 72 clusters; 15, 36 and 76 did fit, but 16 of eight, in two waves, took 13 us).
+  // The lengths are not known here, so what counts is what the block table holds.  A cluster's merge takes 1.4 us,
   // so short contexts stay with one CTA (8 sequences of 25 tiles: 6.3 us, in clusters of eight 7.1; of 50 tiles 7.7 and
   // 7.1; sixteen columns, of 50 tiles 10.5 and 8.6).
   // Cutting into pieces gains by the SMs that would otherwise idle and by equal shares, and pays for the second kernel:
@@ -1109,8 +1118,10 @@ Plan make_plan(int bs, int h_q, int h_kv, int head_dim, int q_len, long long cap
     p.splits = static_cast<int>(std::min<long long>(num_splits, std::max(1LL, (tiles + 7) / 8)));
   } else if (tiles <= uncut || ctas >= 8LL * resident || bs > kMaxLine ||
              seqs * (tiles + kFixed) > 0x7FFFFFFFll) {
-    // Short contexts: one CTA or cluster a sequence takes no longer than pieces and their merge.  Many sequences: their
-    // CTAs balance by themselves.  (The line's places are counted in 32 bits.)
+    // Short contexts: one CTA or cluster a sequence takes no longer than pieces and their merge.  Many sequences of
+    // like lengths: their CTAs balance by themselves.  A far longer one among them keeps its CTAs alone at the end (512
+    // of 1000 keys 122 us, one of them of 131072 keys 752, in four asked-for shards 257).  (The line's places are
+    // counted in 32 bits.)
     p.splits = 1;
     if (few && tiles > 4) {
       p.kind = kWideCtas;

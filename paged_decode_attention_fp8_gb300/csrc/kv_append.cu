@@ -25,10 +25,15 @@
 // pipeline: the chain position -> table row -> rotation is longer than a
 // memory access, so slots and positions come two steps ahead, values and the
 // table's rows (into L1) one.  A 16384-token prompt, 8 KV heads of 128, E4M3:
-// 22.0 us, 4.97 TB/s, 0.73 of the measured copy bandwidth (131072 tokens 0.78);
-// 2049 latent rows of 576 with 16 query heads 12.9 us, 0.91; 65537 rows x 8
-// heads read back 35.1 us, 0.85; 8193 tokens into 4 bits and back 25.2 us, where
-// a block's two conversions and reciprocal weigh as much as its bytes.
+// 22.0 us, 4.97 TB/s, 0.73 of the measured copy bandwidth (131072 tokens 0.85:
+// the rest is ramp); 2049 latent rows of 576 with 16 query heads 13.0 us, 0.90.
+// With row scales, whose amax and two divisions stand before a row's codes,
+// 25.5 us, 0.64 (131072 tokens 0.74).  Into 4 bits 24.4 us, 0.57, and 0.61 at
+// 131072 tokens, so not the ramp but the arithmetic holds it: per 16 values an
+// amax, two conversions of a scale, a reciprocal, their exchange between lanes
+// and 16 products and conversions.  Reading 65537 rows x 8 heads back takes 34.8
+// us, 0.86 (4 bits 32.0, 0.79; 8193 rows 6.2, 0.51: ramp).  8193 tokens into 4
+// bits (12.8 us) and both caches read back: 24.9 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -634,7 +639,8 @@ fp8mla_status_t kv_append_entry(const KvAppendArgs& a, cudaStream_t stream) {
   p.head_dim = a.head_dim;
   const int pairs = a.head_dim / 16;
   cudaError_t e;
-  // the fewest lanes with one piece each; three where that leaves fewer of them idle (head_dim 192, 576)
+  // the fewest lanes with one piece each; three where that leaves fewer of them idle (head_dim 192, 576).  Rows above
+  // 768 values take two pieces a lane, and at three CTAs of 80 registers spill 28 to 88 bytes: no cache here has them
   if (pairs <= 1) e = launch_append<1, 1>(p, kind, stream);
   else if (pairs <= 2) e = launch_append<2, 1>(p, kind, stream);
   else if (pairs <= 4) e = launch_append<4, 1>(p, kind, stream);
