@@ -483,8 +483,8 @@ FP8MLA_API fp8mla_status_t paged_cache_read(const void* cache, fp8mla_kv_dtype_t
  *   out may be q; out, lse, workspace and q do not overlap otherwise (refused)
  * Products take K and V exactly, Q's values from 2^-31 of a head's largest on
  * exactly (others to 2^-39 of it); P is rounded to f16.  A NaN
- * reaches the rows that see its key, and those alone.  Scores may be of any
- * size that float32 holds in units of log2.
+ * reaches the rows that see its key, and those alone.  Scores and sinks may be
+ * of any size that float32 holds in units of log2.
  * Scales are normal floats > 0.  Requires head_dim 64, 128 or 256, page_size
  * 16, 32, 64, 128 or 256, q_len <= 16, h_q % h_kv == 0, q_len * (h_q / h_kv)
  * <= 128 and fewer than 2^32 rows (num_blocks * h_kv * page_size) a cache. */

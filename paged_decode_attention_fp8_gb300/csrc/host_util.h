@@ -106,7 +106,9 @@ inline bool rows_overlap_themselves(const Rows& r) {
   const int64_t outer = few_heads ? r.head : r.token, inner = few_heads ? r.token : r.head;
   const int64_t outers = few_heads ? r.heads : r.n, inners = few_heads ? r.n : r.heads;
   if (hits(inner, 0, 1, inners - 1, -r.width, r.width)) return true;
-  if (outer >= inner * (inners - 1) + r.width && inner >= 0) return false;  // each set of rows behind the one before
+  // the usual cases: each set of rows behind the one before, or between its rows
+  if (inner >= 0 && outer >= inner * (inners - 1) + r.width) return false;
+  if (outer >= r.width && inner >= outer * (outers - 1) + r.width) return false;
   if (outers > (1 << 16)) return true;
   for (int64_t i = 1; i < outers; ++i)
     if (hits(inner, outer * i, 1 - inners, inners - 1, -r.width, r.width)) return true;
