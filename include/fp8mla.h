@@ -502,6 +502,93 @@ FP8MLA_API fp8mla_status_t paged_gqa_decode_fp4(const void* q, const void* k_cac
 FP8MLA_API size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int head_dim, int q_len,
                                                 int64_t max_seqlen, int window, int num_splits);
 
+/* ------------------------------------- many rows to paged E4M3 keys ---
+ * paged_cross_attention -- attention of each sequence's query tokens to all
+ * keys of that sequence's pages, whose number is independent of the tokens'
+ * (an encoder's states, a document, a shared prefix):
+ *   out[i, h] = softmax_j(softmax_scale q[i, h] . k_j) v_j over the kv_lens[b]
+ *   keys of token i's sequence b, KV head h / (h_q / h_kv).
+ *   q            bf16 [n_tokens, h_q, head_dim], strided along tokens and heads
+ *                (elements, multiples of 8), 16-byte aligned; so is out
+ *   k_cache, v_cache  E4M3 [num_blocks, h_kv, page_size, head_dim], 16-byte
+ *                aligned; k_scale, v_scale float32 [1], or [num_blocks, h_kv,
+ *                page_size] (16-byte aligned) with scale_rows
+ *   q_starts     int32 [bs + 1], not falling: sequence b has the tokens
+ *                [q_starts[b], q_starts[b + 1]); NULL: token b (n_tokens >= bs)
+ *   block_table  int32 [bs, max_blocks]; kv_lens int32 [bs], 0 allowed
+ *   out, lse     bf16, float32 [n_tokens, h_q] contiguous (natural log).  A
+ *                sequence without keys gives zeros and -inf.  Rows of tokens of
+ *                no sequence are left as they are, or get zeros (fill_out) and
+ *                -inf (fill_lse)
+ *   workspace    >= paged_cross_workspace_bytes, 256-byte aligned
+ * out may be q (strided alike); out, lse, workspace and q do not overlap
+ * otherwise (refused).  A length or token range that does not fit sets
+ * FP8MLA_DEV_BAD_SEQLEN and counts as empty, a page outside the cache
+ * FP8MLA_DEV_BAD_PAGE.  Products take K and V exactly, Q's values from 2^-31 of
+ * a row's largest on exactly (others to 2^-39 of it); P is rounded to f16, sums
+ * are float32.  A NaN reaches the rows of its sequence, and those alone.
+ * Requires head_dim 64 or 128, page_size 16, 32, 64, 128 or 256, h_q % h_kv == 0,
+ * n_tokens * h_q <= 2^30, max_blocks * page_size <= 2^30, scales > 0. */
+FP8MLA_API fp8mla_status_t paged_cross_attention(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache, const void* v_cache,
+    fp8mla_kv_dtype_t kv_dtype, int num_blocks, const float* k_scale, const float* v_scale, int scale_rows,
+    const int32_t* q_starts, const int32_t* block_table, int max_blocks, const int32_t* kv_lens, float softmax_scale,
+    void* workspace, size_t workspace_bytes, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+    int fill_out, int fill_lse, int n_tokens, int bs, int h_q, int h_kv, int head_dim, int page_size,
+    fp8mla_stream_t stream);
+
+/* Workspace bytes of paged_cross_attention on the current device; max_keys =
+ * max_blocks * page_size.  0 for sizes it refuses. */
+FP8MLA_API size_t paged_cross_workspace_bytes(int n_tokens, int bs, int h_q, int h_kv, int head_dim, int64_t max_keys);
+
+/* paged_gqa_decode_shared -- a decode step of sequences that share prefixes:
+ * each of the n_prefixes prefixes is cached once, and its keys are read once
+ * for all its sequences.  A row sees its prefix's keys, then its sequence's
+ * own ones; positions are the caller's business (rotated when appended).
+ *   q            bf16 [bs, q_len, h_q, head_dim], the last q_len own positions
+ *   prefix_table int32 [n_prefixes, prefix_blocks], prefix_lens int32
+ *                [n_prefixes] (0 allowed), prefix_starts int32 [n_prefixes + 1],
+ *                not falling: prefix g belongs to the sequences
+ *                [prefix_starts[g], prefix_starts[g + 1]); others have none
+ *   block_table  int32 [bs, max_blocks], seqlens int32 [bs]: own keys, the
+ *                step's q_len ones included; 0 allowed
+ *   spec_mask, sinks, out, lse  as paged_gqa_decode_ext (block key x of a
+ *                sequence is its own key seqlens - q_len + x; one that would
+ *                lie before key 0 does not exist)
+ *   workspace    >= paged_gqa_shared_workspace_bytes, 256-byte aligned
+ * The rest as paged_cross_attention; a NaN in the block's keys reaches only the
+ * rows that see it.  q_len <= 32. */
+FP8MLA_API fp8mla_status_t paged_gqa_decode_shared(
+    const void* q, const void* k_cache, const void* v_cache, fp8mla_kv_dtype_t kv_dtype, int num_blocks,
+    const float* k_scale, const float* v_scale, int scale_rows, const int32_t* prefix_table, int prefix_blocks,
+    const int32_t* prefix_lens, const int32_t* prefix_starts, int n_prefixes, const int32_t* block_table, int max_blocks,
+    const int32_t* seqlens, float softmax_scale, int q_len, const uint8_t* spec_mask, const float* sinks,
+    void* workspace, size_t workspace_bytes, void* out, float* lse, int bs, int h_q, int h_kv, int head_dim,
+    int page_size, fp8mla_stream_t stream);
+
+/* Workspace bytes of paged_gqa_decode_shared on the current device, with the
+ * tables' keys (blocks * page_size).  0 for sizes it refuses. */
+FP8MLA_API size_t paged_gqa_shared_workspace_bytes(int bs, int q_len, int h_q, int h_kv, int head_dim, int n_prefixes,
+                                                   int64_t max_prefix_keys, int64_t max_keys);
+
+/* attention_merge -- joins attention results over disjoint keys, as the calls
+ * of this header return them:
+ *   lse = log sum_p exp(lses[p]), out = sum_p exp(lses[p] - lse) outs[p].
+ *   outs         host array of `parts` device pointers, bf16 [n_tokens, heads,
+ *                dim] strided along tokens and heads (host arrays of strides in
+ *                elements, multiples of 8), 16-byte aligned; so is out
+ *   lses         host array of device pointers, float32 [n_tokens, heads]
+ * A part whose lse is -inf does not count, whatever its row holds; no part:
+ * zeros and -inf.  Sums in float32, rounded once.  out may be one of outs
+ * (strided alike); out and lse overlap nothing else (refused).
+ * 1 <= parts <= FP8MLA_MERGE_MAX_PARTS, dim a multiple of 8 up to 1024,
+ * n_tokens * heads * dim <= 2^33. */
+#define FP8MLA_MERGE_MAX_PARTS 8
+FP8MLA_API fp8mla_status_t attention_merge(const void* const* outs, const int64_t* out_token_strides,
+                                           const int64_t* out_head_strides, const float* const* lses, int parts,
+                                           void* out, int64_t token_stride, int64_t head_stride, float* lse,
+                                           int n_tokens, int heads, int dim, fp8mla_stream_t stream);
+
 /* ------------------------------------------------------ no allocation ---
  * fp8mla_decode_no_alloc -- the dense MLA decode for callers that cannot
  * allocate device memory: code running where cudaMalloc is not allowed or

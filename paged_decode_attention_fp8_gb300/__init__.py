@@ -81,6 +81,13 @@ _SIGNATURES = {
     "paged_gqa_decode_fp4": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _P, _F, _I, _P, _I, _P, _I, _P, _SZ, _P,
                                   _P, _I, _I, _I, _I, _I, _P]),
     "paged_gqa_fp4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _L, _I, _I]),
+    "paged_cross_attention": (_I, [_P, _L, _L, _P, _P, _I, _I, _P, _P, _I, _P, _P, _I, _P, _F, _P, _SZ, _P, _L, _L,
+                                   _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "paged_cross_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _L]),
+    "paged_gqa_decode_shared": (_I, [_P, _P, _P, _I, _I, _P, _P, _I, _P, _I, _P, _P, _I, _P, _I, _P, _F, _I, _P, _P,
+                                     _P, _SZ, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "paged_gqa_shared_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _L, _L]),
+    "attention_merge": (_I, [_P, _P, _P, _P, _I, _P, _L, _L, _P, _I, _I, _I, _P]),
     "fp8mla_get_last_device_error": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "fp8mla_get_wait_timeout_site": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "fp8mla_set_wait_test": (_I, [ctypes.c_int32, ctypes.c_uint64]),
@@ -656,6 +663,63 @@ def paged_gqa_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     return _native().paged_gqa_decode_fp4(q, k_cache, v_cache, k_block_scales, v_block_scales, block_table, seqlens,
                                           k_scale, v_scale, softmax_scale, spec_mask, window, sinks, num_splits, out,
                                           lse, workspace)
+
+
+# ------------------------------- many rows, shared prefixes, partial results --
+
+
+def cross_workspace_bytes(n_tokens: int, bs: int, h_q: int, h_kv: int, head_dim: int, max_keys: int) -> int:
+    """Workspace of ``paged_cross_attention`` on the current device; max_keys = the block table's keys."""
+    return lib().paged_cross_workspace_bytes(n_tokens, bs, h_q, h_kv, head_dim, max_keys)
+
+
+def paged_cross_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                          kv_lens: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                          softmax_scale: float | None = None, *, q_starts: torch.Tensor | None = None, out=None,
+                          lse=None, workspace=None):
+    """Attention of each sequence's query tokens to all keys of its pages (an encoder's states, a document, a
+    prefix), however many tokens and keys there are.  q bf16 [n, h_q, hd] (strided along tokens and heads by
+    multiples of 8 values and 16-byte aligned, like out); caches E4M3 [num_blocks, h_kv, page, hd], hd 64 or 128,
+    pages of 16 to 256; k_scale / v_scale float32 [1] or per cached row [num_blocks, h_kv, page]; block_table int32
+    [bs, max_blocks], kv_lens int32 [bs] (0 allowed).  Sequence b has the tokens [q_starts[b], q_starts[b + 1])
+    (int32 [bs + 1]), or token b without q_starts.
+
+    Returns (out bf16 like q, lse float32 [n, h_q]); a sequence without keys gives zeros and -inf, and so do tokens
+    of no sequence in outputs that the call makes (given ones keep those rows).  out may be q."""
+    return _native().paged_cross_attention(q, k_cache, v_cache, block_table, kv_lens, k_scale, v_scale, softmax_scale,
+                                           q_starts, out, lse, workspace)
+
+
+def gqa_shared_workspace_bytes(bs: int, q_len: int, h_q: int, h_kv: int, head_dim: int, n_prefixes: int,
+                               max_prefix_keys: int, max_keys: int) -> int:
+    """Workspace of ``paged_gqa_decode_shared`` on the current device, with the two tables' keys."""
+    return lib().paged_gqa_shared_workspace_bytes(bs, q_len, h_q, h_kv, head_dim, n_prefixes, max_prefix_keys,
+                                                  max_keys)
+
+
+def paged_gqa_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                            prefix_table: torch.Tensor, prefix_lens: torch.Tensor, prefix_starts: torch.Tensor,
+                            block_table: torch.Tensor, seqlens: torch.Tensor, k_scale: torch.Tensor,
+                            v_scale: torch.Tensor, softmax_scale: float | None = None, spec_mask=None, sinks=None,
+                            out=None, lse=None, workspace=None):
+    """Decode step of sequences that share prefixes, whose keys are cached once and read once for all of them.
+    q bf16 [bs, q_len, h_q, hd] (the last q_len own positions, at most 32) or [bs, h_q, hd]; caches and scales as
+    ``paged_cross_attention``; prefix g (prefix_table int32 [n_prefixes, blocks], prefix_lens int32 [n_prefixes])
+    belongs to the sequences [prefix_starts[g], prefix_starts[g + 1]) (int32 [n_prefixes + 1]), the others have none;
+    block_table int32 [bs, max_blocks] and seqlens int32 [bs] are the sequences' own keys behind it, the step's
+    included; spec_mask and sinks as ``paged_gqa_decode_ext``.  Returns (out bf16 like q, lse float32 without its
+    last dim); out may be q."""
+    return _native().paged_gqa_decode_shared(q, k_cache, v_cache, prefix_table, prefix_lens, prefix_starts,
+                                             block_table, seqlens, k_scale, v_scale, softmax_scale, spec_mask, sinks,
+                                             out, lse, workspace)
+
+
+def attention_merge(outs, lses, *, out=None, lse=None):
+    """Join 1 to 8 attention results over disjoint keys: lse = log sum exp(lses), out = sum exp(lses[p] - lse) outs[p].
+    outs bf16 [n, heads, dim] each (strided along tokens and heads by multiples of 8 values, 16-byte aligned), lses
+    float32 [n, heads]; a part whose lse is -inf does not count, whatever its row holds.  Returns (out, lse); out may
+    be one of outs."""
+    return _native().attention_merge(outs, lses, out, lse)
 
 
 def wait_timeout_site(device=None):

@@ -1,0 +1,131 @@
+// Joins attention results over disjoint keys:
+//   lse = log sum_p exp(lse_p),   out = sum_p exp(lse_p - lse) out_p.
+//
+// Bound by HBM: each part is read once, the result written once.  A thread takes 16-byte pieces (eight values) of a row
+// in every part, two rows of the grid apart so that twice the parts' loads are in flight; the weights come from the
+// rows' sums, which the threads of a row read from L1.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attention_merge.h"
+#include "common.cuh"
+
+namespace fp8mla {
+namespace merge {
+
+constexpr int kMost = FP8MLA_MERGE_MAX_PARTS, kThreads = 256, kEach = 2;
+
+struct Params {
+  const uint16_t* x[kMost];
+  const float* l[kMost];
+  int64_t token[kMost + 1], head[kMost + 1];  // the last: of the result
+  uint16_t* out;
+  float* lse;
+  uint32_t pieces;  // of 16 bytes, of all rows
+  FastDiv wide, heads;
+};
+
+template <int kParts>
+__global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__ Params p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  uint32_t at[kEach], row[kEach], tok[kEach], head[kEach], ch[kEach];
+  bool in[kEach];
+  uint4 x[kEach][kParts];
+  float w[kEach][kParts];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    at[e] = (blockIdx.x * kEach + e) * kThreads + threadIdx.x;
+    in[e] = at[e] < p.pieces;
+    if (!in[e]) continue;
+    row[e] = fast_div(at[e], p.wide);
+    ch[e] = at[e] - row[e] * p.wide.d;
+    tok[e] = fast_div(row[e], p.heads);
+    head[e] = row[e] - tok[e] * p.heads.d;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      x[e][i] = __ldg(reinterpret_cast<const uint4*>(p.x[i] + tok[e] * p.token[i] + head[e] * p.head[i]) + ch[e]);
+      w[e][i] = __ldg(p.l[i] + row[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    if (!in[e]) continue;
+    float top = kNegInf, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) top = fmaxf(top, w[e][i]);
+    bool nan = false;
+    const float base = top == kNegInf ? 0.f : top;
+    float acc[8] = {};
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      nan |= w[e][i] != w[e][i];
+      const float f = ex2_approx((w[e][i] - base) * kLog2e);
+      sum += f;
+      if (w[e][i] == kNegInf) continue;  // a part without keys: whatever its row holds
+      const uint32_t h[4] = {x[e][i].x, x[e][i].y, x[e][i].z, x[e][i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[2 * k] += f * bf16_lo(h[k]);
+        acc[2 * k + 1] += f * bf16_hi(h[k]);
+      }
+    }
+    float f = sum > 0.f ? 1.f / sum : 0.f;
+    if (nan) f = __int_as_float(0x7FFFFFFF);
+    uint32_t h[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = pack_bf16x2(acc[2 * k] * f, acc[2 * k + 1] * f);
+    reinterpret_cast<uint4*>(p.out + tok[e] * p.token[kMost] + head[e] * p.head[kMost])[ch[e]] =
+        make_uint4(h[0], h[1], h[2], h[3]);
+    if (ch[e] == 0) p.lse[row[e]] = nan ? f : (sum > 0.f ? base + lg2_approx(sum) * kLn2 : kNegInf);
+  }
+}
+
+}  // namespace merge
+
+fp8mla_status_t merge_entry(const MergeArgs& a, cudaStream_t stream) {
+  using namespace merge;
+  if (a.parts < 1 || a.parts > kMost || a.n_tokens < 0 || a.heads < 1 || a.dim < 8 || a.dim % 8 != 0 || a.dim > 1024 ||
+      a.outs == nullptr || a.lses == nullptr || a.out_tokens == nullptr || a.out_heads == nullptr)
+    return FP8MLA_ERR_INVALID_ARG;
+  const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.heads;
+  const int64_t pieces = rows * (a.dim / 8);
+  if (rows > (1ll << 30) || pieces > (1ll << 30)) return FP8MLA_ERR_INVALID_ARG;
+  if (rows == 0) return FP8MLA_OK;
+  if (a.out == nullptr || a.lse == nullptr || misaligned(a.out, 16) || misaligned(a.lse, 4) || ((a.token | a.head) & 7))
+    return FP8MLA_ERR_INVALID_ARG;
+  const Rows out = rows_of(a.out, a.token, a.head, a.n_tokens, a.heads, a.dim, 2), lse = block_of(a.lse, rows * 4);
+  if (rows_overlap_themselves(out) || rows_overlap(out, lse)) return FP8MLA_ERR_INVALID_ARG;
+  Params p = {};
+  for (int i = 0; i < a.parts; ++i) {
+    if (a.outs[i] == nullptr || a.lses[i] == nullptr || misaligned(a.outs[i], 16) || misaligned(a.lses[i], 4) ||
+        ((a.out_tokens[i] | a.out_heads[i]) & 7))
+      return FP8MLA_ERR_INVALID_ARG;
+    // the result may take a part's place, the sums may not: the threads of a row read them at different times
+    const Rows x = rows_of(a.outs[i], a.out_tokens[i], a.out_heads[i], a.n_tokens, a.heads, a.dim, 2);
+    const Rows l = block_of(a.lses[i], rows * 4);
+    if (clobbers(out, x) || rows_overlap(out, l) || rows_overlap(lse, x) || rows_overlap(lse, l))
+      return FP8MLA_ERR_INVALID_ARG;
+    p.x[i] = static_cast<const uint16_t*>(a.outs[i]);
+    p.l[i] = a.lses[i];
+    p.token[i] = a.out_tokens[i];
+    p.head[i] = a.out_heads[i];
+  }
+  p.token[kMost] = a.token;
+  p.head[kMost] = a.head;
+  p.out = static_cast<uint16_t*>(a.out);
+  p.lse = a.lse;
+  p.pieces = static_cast<uint32_t>(pieces);
+  p.wide = make_fast_div(a.dim / 8);
+  p.heads = make_fast_div(a.heads);
+  using Kernel = void (*)(const Params);
+  static const Kernel kernels[kMost] = {merge_kernel<1>, merge_kernel<2>, merge_kernel<3>, merge_kernel<4>,
+                                        merge_kernel<5>, merge_kernel<6>, merge_kernel<7>, merge_kernel<8>};
+  const unsigned grid = static_cast<unsigned>((pieces + kThreads * kEach - 1) / (kThreads * kEach));
+  return launch_dependent(kernels[a.parts - 1], dim3(grid), dim3(kThreads), 0, stream, p) == cudaSuccess
+             ? FP8MLA_OK
+             : FP8MLA_ERR_CUDA;
+}
+
+}  // namespace fp8mla

@@ -1,5 +1,6 @@
 // Native marshalling of the per-step operators for Python: rotary_apply,
-// paged_kv_append, paged_cache_read and paged_gqa_decode_fp4.
+// paged_kv_append, paged_cache_read, paged_gqa_decode_fp4,
+// paged_cross_attention, paged_gqa_decode_shared and attention_merge.
 //
 // A decode step calls these once per layer and their kernels take a few
 // microseconds, so the host's share counts: the same checks in Python with a
@@ -509,6 +510,225 @@ PyObject* py_decode_fp4(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   });
 }
 
+// A pair of objects, both taken over.
+PyObject* pair(PyObject* a, PyObject* b) {
+  PyObject* r = a != nullptr && b != nullptr ? PyTuple_Pack(2, a, b) : nullptr;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  return r;
+}
+
+// K and V caches in E4M3 with one scale each or one per row; returns whether the scales go by row.
+int need_e4m3_caches(const Tensor& kc, const Tensor& vc, const Tensor& ks, const Tensor& vs, const CacheShape& s,
+                     int64_t hd, const c10::Device& dev, const char* where) {
+  if (kc.dim() != 4 || vc.sizes() != kc.sizes() || vc.scalar_type() != kc.scalar_type() || vc.device() != dev ||
+      !vc.is_contiguous())
+    bad("k_cache and v_cache must match");
+  if (kv_code(kc, nullptr) != FP8MLA_KV_E4M3) throw BadStatus{FP8MLA_ERR_UNSUPPORTED_DTYPE, where};
+  if (s.wide != hd) bad("head_dim mismatch");
+  const bool rows = ks.numel() != 1 || vs.numel() != 1;
+  need_scales("k", s, hd, FP8MLA_KV_E4M3, rows ? nullptr : &ks, rows ? &ks : nullptr, nullptr, dev);
+  need_scales("v", s, hd, FP8MLA_KV_E4M3, rows ? nullptr : &vs, rows ? &vs : nullptr, nullptr, dev);
+  return rows ? 1 : 0;
+}
+int64_t need_block_table(const Tensor& t, const char* name, int64_t n, const c10::Device& dev) {
+  if (t.device() != dev || t.scalar_type() != ScalarType::Int || t.dim() != 2 || t.size(0) != n || !t.is_contiguous())
+    bad(std::string(name) + " must be contiguous int32 [" + std::to_string(n) + ", max_blocks] on " + dev.str());
+  return t.size(1);
+}
+float softmax_scale_of(PyObject* o, int64_t hd) {
+  double scale = 1.0 / std::sqrt(static_cast<double>(hd));
+  if (o != Py_None) {
+    scale = PyFloat_AsDouble(o);
+    if (scale == -1.0 && PyErr_Occurred()) throw PyFailure{};
+  }
+  return static_cast<float>(scale);
+}
+const Tensor* need_workspace(const Tensor* ws, Tensor* made, size_t need, const c10::Device& dev) {
+  if (ws == nullptr) {
+    *made = make({static_cast<int64_t>(need)}, ScalarType::Byte, dev);
+    return made;
+  }
+  if (ws->device() != dev || !ws->is_contiguous()) bad("workspace must be a contiguous tensor on " + dev.str());
+  return ws;
+}
+
+// (q, k_cache, v_cache, block_table, kv_lens, k_scale, v_scale, softmax_scale, q_starts, out, lse, workspace)
+// -> (out, lse)
+PyObject* py_cross(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  if (!count(nargs, 12)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor &q = given(a[0], "q"), &kc = given(a[1], "k_cache"), &vc = given(a[2], "v_cache");
+    const Tensor &bt = given(a[3], "block_table"), &kl = given(a[4], "kv_lens");
+    const Tensor &ks = given(a[5], "k_scale"), &vs = given(a[6], "v_scale");
+    const Tensor *starts = maybe(a[8], "q_starts"), *out = maybe(a[9], "out"), *lse = maybe(a[10], "lse");
+    const Tensor* ws = maybe(a[11], "workspace");
+    need_no_grad({&q, &kc, &vc, &ks, &vs, out, lse});
+    if (!q.is_cuda()) bad("q must be a CUDA bf16 tensor [n, h_q, head_dim]");
+    const c10::Device dev = q.device();
+    const int64_t n = q.dim() > 0 ? q.size(0) : 0;
+    need_heads(q, "q", ScalarType::BFloat16, dev, n);
+    const int64_t h_q = q.size(1), hd = q.size(2);
+    const CacheShape s = cache_shape(kc, "k_cache", dev);
+    const int by_row = need_e4m3_caches(kc, vc, ks, vs, s, hd, dev, "paged_cross_attention");
+    need_int32(kl, "kv_lens", dev, -1);
+    const int64_t bs = kl.size(0), blocks = need_block_table(bt, "block_table", bs, dev);
+    if (starts != nullptr) need_int32(*starts, "q_starts", dev, bs + 1);
+    if (starts == nullptr && n != bs) bad("without q_starts, q has a token for each sequence");
+    const float scale = softmax_scale_of(a[7], hd);
+    const int n32 = dim32(n, "n"), bs32 = dim32(bs, "bs"), hq32 = dim32(h_q, "h_q"), hkv32 = dim32(s.h_kv, "h_kv"),
+              hd32 = dim32(hd, "head_dim");
+    const c10::cuda::CUDAGuard guard(dev);
+    Tensor out_new, lse_new, ws_new;  // nothing else will have written their rows of no sequence
+    const int fill = starts != nullptr, fill_out = fill && out == nullptr, fill_lse = fill && lse == nullptr;
+    if (out == nullptr) {
+      out_new = make(q.sizes(), ScalarType::BFloat16, dev);
+      out = &out_new;
+    } else {
+      need_heads_out(*out, "out", q.sizes(), ScalarType::BFloat16, dev);
+    }
+    const c10::IntArrayRef rows = q.sizes().slice(0, 2);
+    if (lse == nullptr) {
+      lse_new = make(rows, ScalarType::Float, dev);
+      lse = &lse_new;
+    } else {
+      need_like(*lse, "lse", rows, ScalarType::Float, dev);
+    }
+    ws = need_workspace(ws, &ws_new, paged_cross_workspace_bytes(n32, bs32, hq32, hkv32, hd32, blocks * s.page), dev);
+    check(paged_cross_attention(q.data_ptr(), stride_of(&q, 0), stride_of(&q, 1), kc.data_ptr(), vc.data_ptr(),
+                                FP8MLA_KV_E4M3, dim32(s.blocks, "num_blocks"), ptr_as<const float>(&ks),
+                                ptr_as<const float>(&vs), by_row, ptr_as<const int32_t>(starts),
+                                ptr_as<const int32_t>(&bt), dim32(blocks, "max_blocks"), ptr_as<const int32_t>(&kl),
+                                scale, ptr(ws), ws->nbytes(), out->data_ptr(), stride_of(out, 0), stride_of(out, 1),
+                                ptr_as<float>(lse), fill_out, fill_lse, n32, bs32, hq32, hkv32, hd32,
+                                dim32(s.page, "page"), stream_of(dev)),
+          "paged_cross_attention");
+    written({out, lse});
+    return pair(wrap(out, a[9]), wrap(lse, a[10]));
+  });
+}
+
+// (q, k_cache, v_cache, prefix_table, prefix_lens, prefix_starts, block_table, seqlens, k_scale, v_scale,
+//  softmax_scale, spec_mask, sinks, out, lse, workspace) -> (out, lse)
+PyObject* py_shared(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  if (!count(nargs, 16)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor &q = given(a[0], "q"), &kc = given(a[1], "k_cache"), &vc = given(a[2], "v_cache");
+    const Tensor &pt = given(a[3], "prefix_table"), &pl = given(a[4], "prefix_lens"), &ps = given(a[5], "prefix_starts");
+    const Tensor &bt = given(a[6], "block_table"), &sl = given(a[7], "seqlens");
+    const Tensor &ks = given(a[8], "k_scale"), &vs = given(a[9], "v_scale");
+    const Tensor *mask = maybe(a[11], "spec_mask"), *sinks = maybe(a[12], "sinks");
+    const Tensor *out = maybe(a[13], "out"), *lse = maybe(a[14], "lse"), *ws = maybe(a[15], "workspace");
+    need_no_grad({&q, &kc, &vc, &ks, &vs, sinks, out, lse});
+    if (!q.is_cuda() || q.scalar_type() != ScalarType::BFloat16 || (q.dim() != 3 && q.dim() != 4) || !q.is_contiguous())
+      bad("q must be a contiguous CUDA bf16 tensor [bs, q_len, h_q, hd] or [bs, h_q, hd]");
+    const c10::Device dev = q.device();
+    const int64_t bs = q.size(0), h_q = q.size(-2), hd = q.size(-1), q_len = q.dim() == 4 ? q.size(1) : 1;
+    const CacheShape s = cache_shape(kc, "k_cache", dev);
+    const int by_row = need_e4m3_caches(kc, vc, ks, vs, s, hd, dev, "paged_gqa_decode_shared");
+    need_int32(pl, "prefix_lens", dev, -1);
+    const int64_t n_prefixes = pl.size(0), prefix_blocks = need_block_table(pt, "prefix_table", n_prefixes, dev);
+    need_int32(ps, "prefix_starts", dev, n_prefixes + 1);
+    const int64_t blocks = need_block_table(bt, "block_table", bs, dev);
+    need_int32(sl, "seqlens", dev, bs);
+    if (mask != nullptr &&
+        (mask->device() != dev || mask->scalar_type() != ScalarType::Byte || mask->dim() != 3 || mask->size(0) != bs ||
+         mask->size(1) != q_len || mask->size(2) != q_len || !mask->is_contiguous()))
+      bad("spec_mask must be contiguous uint8 [bs, q_len, q_len]");
+    if (sinks != nullptr && (sinks->device() != dev || sinks->scalar_type() != ScalarType::Float || sinks->dim() != 1 ||
+                             sinks->size(0) != h_q || !sinks->is_contiguous()))
+      bad("sinks must be contiguous float32 [h_q]");
+    const float scale = softmax_scale_of(a[10], hd);
+    const int bs32 = dim32(bs, "bs"), ql32 = dim32(q_len, "q_len"), hq32 = dim32(h_q, "h_q"),
+              hkv32 = dim32(s.h_kv, "h_kv"), hd32 = dim32(hd, "head_dim"), np32 = dim32(n_prefixes, "n_prefixes");
+    const c10::cuda::CUDAGuard guard(dev);
+    Tensor out_new, lse_new, ws_new;
+    if (out == nullptr) {
+      out_new = make(q.sizes(), ScalarType::BFloat16, dev);
+      out = &out_new;
+    } else {
+      need_like(*out, "out", q.sizes(), ScalarType::BFloat16, dev);
+    }
+    const c10::IntArrayRef rows = q.sizes().slice(0, q.dim() - 1);
+    if (lse == nullptr) {
+      lse_new = make(rows, ScalarType::Float, dev);
+      lse = &lse_new;
+    } else {
+      need_like(*lse, "lse", rows, ScalarType::Float, dev);
+    }
+    ws = need_workspace(ws, &ws_new,
+                        paged_gqa_shared_workspace_bytes(bs32, ql32, hq32, hkv32, hd32, np32,
+                                                         np32 > 0 ? prefix_blocks * s.page : 0, blocks * s.page),
+                        dev);
+    check(paged_gqa_decode_shared(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), FP8MLA_KV_E4M3,
+                                  dim32(s.blocks, "num_blocks"), ptr_as<const float>(&ks), ptr_as<const float>(&vs),
+                                  by_row, ptr_as<const int32_t>(&pt), dim32(prefix_blocks, "prefix_blocks"),
+                                  ptr_as<const int32_t>(&pl), ptr_as<const int32_t>(&ps), np32,
+                                  ptr_as<const int32_t>(&bt), dim32(blocks, "max_blocks"), ptr_as<const int32_t>(&sl),
+                                  scale, ql32, ptr_as<const uint8_t>(mask), ptr_as<const float>(sinks), ptr(ws),
+                                  ws->nbytes(), out->data_ptr(), ptr_as<float>(lse), bs32, hq32, hkv32, hd32,
+                                  dim32(s.page, "page"), stream_of(dev)),
+          "paged_gqa_decode_shared");
+    written({out, lse});
+    return pair(wrap(out, a[13]), wrap(lse, a[14]));
+  });
+}
+
+// (outs, lses, out, lse) -> (out, lse); outs and lses are lists or tuples
+PyObject* py_merge(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  if (!count(nargs, 4)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    if ((!PyList_Check(a[0]) && !PyTuple_Check(a[0])) || (!PyList_Check(a[1]) && !PyTuple_Check(a[1])))
+      bad("outs and lses must be lists or tuples of tensors");
+    const Py_ssize_t parts = PySequence_Fast_GET_SIZE(a[0]);
+    if (parts < 1 || parts > FP8MLA_MERGE_MAX_PARTS || PySequence_Fast_GET_SIZE(a[1]) != parts)
+      bad("outs and lses must have the same 1 to " + std::to_string(FP8MLA_MERGE_MAX_PARTS) + " parts");
+    const Tensor *out = maybe(a[2], "out"), *lse = maybe(a[3], "lse");
+    need_no_grad({out, lse});
+    const Tensor& first = given(PySequence_Fast_GET_ITEM(a[0], 0), "outs");
+    if (!first.is_cuda()) bad("outs must be CUDA bf16 tensors [n, heads, dim]");
+    const c10::Device dev = first.device();
+    const int64_t n = first.dim() > 0 ? first.size(0) : 0;
+    need_heads(first, "outs", ScalarType::BFloat16, dev, n);
+    const c10::IntArrayRef rows = first.sizes().slice(0, 2);
+    const void* xs[FP8MLA_MERGE_MAX_PARTS];
+    const float* ls[FP8MLA_MERGE_MAX_PARTS];
+    int64_t tokens[FP8MLA_MERGE_MAX_PARTS], heads[FP8MLA_MERGE_MAX_PARTS];
+    for (Py_ssize_t i = 0; i < parts; ++i) {
+      const Tensor& x = given(PySequence_Fast_GET_ITEM(a[0], i), "outs");
+      const Tensor& l = given(PySequence_Fast_GET_ITEM(a[1], i), "lses");
+      need_no_grad({&x, &l});
+      need_heads(x, "outs", ScalarType::BFloat16, dev, n, first.size(2));
+      if (x.sizes() != first.sizes()) bad("outs must have the same shape");
+      need_like(l, "lses", rows, ScalarType::Float, dev);
+      xs[i] = x.data_ptr();
+      ls[i] = l.data_ptr<float>();
+      tokens[i] = stride_of(&x, 0);
+      heads[i] = stride_of(&x, 1);
+    }
+    const c10::cuda::CUDAGuard guard(dev);
+    Tensor out_new, lse_new;
+    if (out == nullptr) {
+      out_new = make(first.sizes(), ScalarType::BFloat16, dev);
+      out = &out_new;
+    } else {
+      need_heads_out(*out, "out", first.sizes(), ScalarType::BFloat16, dev);
+    }
+    if (lse == nullptr) {
+      lse_new = make(rows, ScalarType::Float, dev);
+      lse = &lse_new;
+    } else {
+      need_like(*lse, "lse", rows, ScalarType::Float, dev);
+    }
+    check(attention_merge(xs, tokens, heads, ls, static_cast<int>(parts), out->data_ptr(), stride_of(out, 0),
+                          stride_of(out, 1), ptr_as<float>(lse), dim32(n, "n"), dim32(first.size(1), "heads"),
+                          dim32(first.size(2), "dim"), stream_of(dev)),
+          "attention_merge");
+    written({out, lse});
+    return pair(wrap(out, a[2]), wrap(lse, a[3]));
+  });
+}
+
 PyObject* py_set_error(PyObject*, PyObject* cls) {
   Py_XDECREF(g_status_error);
   Py_INCREF(cls);
@@ -525,6 +745,9 @@ PyMethodDef g_methods[] = {
     {"paged_kv_append", fast(py_kv_append), METH_FASTCALL, nullptr},
     {"paged_cache_read", fast(py_cache_read), METH_FASTCALL, nullptr},
     {"paged_gqa_decode_fp4", fast(py_decode_fp4), METH_FASTCALL, nullptr},
+    {"paged_cross_attention", fast(py_cross), METH_FASTCALL, nullptr},
+    {"paged_gqa_decode_shared", fast(py_shared), METH_FASTCALL, nullptr},
+    {"attention_merge", fast(py_merge), METH_FASTCALL, nullptr},
     {"set_error", py_set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

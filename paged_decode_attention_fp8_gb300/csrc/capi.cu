@@ -6,12 +6,14 @@
 #include <cstring>
 #include <mutex>
 
+#include "attention_merge.h"
 #include "cache_write.h"
 #include "fp8mla.h"
 #include "gqa_decode.h"
 #include "gqa_fp4.h"
 #include "kv_append.h"
 #include "mla_decode.h"
+#include "ragged_gqa.h"
 #include "rotary.h"
 #include "sparse_mla.h"
 
@@ -540,13 +542,101 @@ size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int head_dim, in
   return fp4_workspace_bytes(bs, h_q, h_kv, head_dim, q_len, max_seqlen, window, num_splits);
 }
 
+fp8mla_status_t paged_cross_attention(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache, const void* v_cache,
+    fp8mla_kv_dtype_t kv_dtype, int num_blocks, const float* k_scale, const float* v_scale, int scale_rows,
+    const int32_t* q_starts, const int32_t* block_table, int max_blocks, const int32_t* kv_lens, float softmax_scale,
+    void* workspace, size_t workspace_bytes, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+    int fill_out, int fill_lse, int n_tokens, int bs, int h_q, int h_kv, int head_dim, int page_size,
+    fp8mla_stream_t stream) {
+  const fp8mla_status_t st = check_kv_dtype(kv_dtype);
+  if (st != FP8MLA_OK) return st;
+  CrossArgs a;
+  a.q = q;
+  a.q_token = q_token_stride;
+  a.q_head = q_head_stride;
+  a.cache = RaggedCache{k_cache, v_cache, k_scale, v_scale, scale_rows, num_blocks, page_size};
+  a.q_starts = q_starts;
+  a.block_table = block_table;
+  a.kv_lens = kv_lens;
+  a.max_blocks = max_blocks;
+  a.softmax_scale = softmax_scale;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.out = out;
+  a.out_token = out_token_stride;
+  a.out_head = out_head_stride;
+  a.lse = lse;
+  a.fill_out = fill_out;
+  a.fill_lse = fill_lse;
+  a.n_tokens = n_tokens;
+  a.bs = bs;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.head_dim = head_dim;
+  return cross_entry(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t paged_cross_workspace_bytes(int n_tokens, int bs, int h_q, int h_kv, int head_dim, int64_t max_keys) {
+  return cross_workspace_bytes(n_tokens, bs, h_q, h_kv, head_dim, max_keys);
+}
+
+fp8mla_status_t paged_gqa_decode_shared(
+    const void* q, const void* k_cache, const void* v_cache, fp8mla_kv_dtype_t kv_dtype, int num_blocks,
+    const float* k_scale, const float* v_scale, int scale_rows, const int32_t* prefix_table, int prefix_blocks,
+    const int32_t* prefix_lens, const int32_t* prefix_starts, int n_prefixes, const int32_t* block_table, int max_blocks,
+    const int32_t* seqlens, float softmax_scale, int q_len, const uint8_t* spec_mask, const float* sinks,
+    void* workspace, size_t workspace_bytes, void* out, float* lse, int bs, int h_q, int h_kv, int head_dim,
+    int page_size, fp8mla_stream_t stream) {
+  const fp8mla_status_t st = check_kv_dtype(kv_dtype);
+  if (st != FP8MLA_OK) return st;
+  SharedArgs a;
+  a.q = q;
+  a.cache = RaggedCache{k_cache, v_cache, k_scale, v_scale, scale_rows, num_blocks, page_size};
+  a.prefix_table = prefix_table;
+  a.prefix_lens = prefix_lens;
+  a.prefix_starts = prefix_starts;
+  a.n_prefixes = n_prefixes;
+  a.prefix_blocks = prefix_blocks;
+  a.block_table = block_table;
+  a.seqlens = seqlens;
+  a.max_blocks = max_blocks;
+  a.softmax_scale = softmax_scale;
+  a.q_len = q_len;
+  a.spec_mask = spec_mask;
+  a.sinks = sinks;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.out = out;
+  a.lse = lse;
+  a.bs = bs;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.head_dim = head_dim;
+  return shared_entry(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t paged_gqa_shared_workspace_bytes(int bs, int q_len, int h_q, int h_kv, int head_dim, int n_prefixes,
+                                        int64_t max_prefix_keys, int64_t max_keys) {
+  return shared_workspace_bytes(bs, q_len, h_q, h_kv, head_dim, n_prefixes, max_prefix_keys, max_keys);
+}
+
+fp8mla_status_t attention_merge(const void* const* outs, const int64_t* out_token_strides,
+                                const int64_t* out_head_strides, const float* const* lses, int parts, void* out,
+                                int64_t token_stride, int64_t head_stride, float* lse, int n_tokens, int heads, int dim,
+                                fp8mla_stream_t stream) {
+  return merge_entry(MergeArgs{outs, out_token_strides, out_head_strides, lses, parts, out, token_stride, head_stride,
+                               lse, n_tokens, heads, dim},
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
 fp8mla_status_t fp8mla_get_last_device_error(fp8mla_stream_t stream, uint32_t* code_out) {
   if (code_out == nullptr) return FP8MLA_ERR_INVALID_ARG;
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return FP8MLA_ERR_CUDA;
   *code_out = mla_read_and_clear_status() | metadata_read_and_clear_status() |
               sparse_read_and_clear_status() | gqa_read_and_clear_status() |
               cache_write_read_and_clear_status() | rotary_read_and_clear_status() |
-              kv_append_read_and_clear_status() | fp4_read_and_clear_status();
+              kv_append_read_and_clear_status() | fp4_read_and_clear_status() | ragged_read_and_clear_status();
   return FP8MLA_OK;
 }
 

@@ -1,0 +1,1403 @@
+// Attention of runs of query rows to paged E4M3 keys, all of them visible: cross attention to an encoder's states, and
+// the two halves (shared prefix, own keys) of a decode step behind shared prefixes.
+//
+// A segment is a run of query tokens and the list of pages they all read.  With G query heads to a KV head, the rows of
+// (segment, KV head) are its tokens' G heads one token after the other, and
+//   out[r] = sum_j softmax_j(c q_r . k_j) v_j,   lse[r] = log sum_j exp(c q_r . k_j).
+//
+// One CTA an SM walks its share of a line of work: every (segment, KV head, 256 rows) is an item of the line, as long as
+// its key tiles of 128 and a fixed part take.  The line is cut into equal shares on the device, since lengths are known
+// there alone; an item that a cut meets leaves partial sums in the workspace, merged by a second launch.
+//
+// Per item the rows are the M of the matrix products (f16, tcgen05): S = Q K^T and O += P V, 128 rows in the lanes of
+// TMEM, P written over S by the threads that own the rows.  K and V are exact in f16, Q takes a power of two per row.
+//   up to 256 rows: two streams of 128 rows, each with its own S and O; the tensor core works for one while the other's
+//     softmax runs.
+//   up to 128 rows: one stream, S in two buffers by tile parity, and both softmax warpgroups share a tile's columns.
+// Warps: 0-3 and 4-7 the two softmax warpgroups, 8-11 turn raw tiles into f16, 12 issues the products, 13 copies raw
+// tiles (one bulk copy per page and operand), 14 and 15 fill rows of no sequence.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "common.cuh"
+#include "ragged_gqa.h"
+
+namespace fp8mla {
+
+__device__ uint32_t g_status_ragged;
+
+namespace ragged {
+
+constexpr int kTile = 128;      // keys a tile, rows a stream
+constexpr int kItemRows = 256;  // rows an item
+constexpr int kThreads = 512;
+constexpr float kLift = 7.f;    // P = 2^(score - reference + 7): 2^15 at most in f16, normal down to 2^-21 of the largest
+constexpr float kTau = 8.f;     // the reference moves when a score passes it by more
+
+// Lengths of the line, in eighths of a tile of 256 rows.
+constexpr int kPairTile = 8, kOneTile = 5, kPairFixed = 12, kOneFixed = 8, kEmpty = 1;
+
+struct List {
+  const int32_t* starts;  // segment s has the tokens [per starts[s], per starts[s + 1]); null: [per s, per (s + 1))
+  const int32_t* lens;
+  const int32_t* table;
+  int n, max_blocks, per;
+  int less;  // the last keys that are left out
+};
+
+struct Cut {  // the item that a share begins and does not end
+  long long start, end;
+  int valid, head, t0, row0, rows;
+};
+
+struct Params {
+  const uint16_t* q;
+  const uint8_t *k, *v;
+  const float *k_scale, *v_scale;
+  uint16_t* out;
+  float* lse;
+  long long* lo;        // [units + 1] where the shares begin
+  int* units;
+  long long* seg_at;    // joined: where the segments begin
+  Cut* cuts;            // [units]
+  float2* slot_ml;      // [2 units][slot_rows]
+  float* slot_o;        // [2 units][slot_rows][hd]
+  float2* plane_ml[2];  // joined: whole items of either list, [tokens * h_q]
+  float* plane_o[2];
+  const uint8_t* spec_mask;
+  const float* sinks;
+  long long q_tok, q_head, o_tok, o_head;
+  List list[2];
+  FastDiv group;
+  float softmax_scale;
+  int joined, tokens, h_q, h_kv, num_blocks, page_shift, slot_rows, fill_out, fill_lse, q_len;
+};
+
+// ---------------------------------------------------------------- the line --
+
+struct Seg {
+  int t0, rows, keys, tiles, row_tiles;
+  int full, last;  // length of an item of 256 rows and of the last one
+  long long head;  // of all items of a KV head
+};
+
+__device__ __forceinline__ int seg_len(const List& l, int s, int page_shift, uint32_t* bad) {
+  const int n = __ldg(l.lens + s);
+  if (n < 0 || n > (static_cast<long long>(l.max_blocks) << page_shift)) {
+    *bad = FP8MLA_DEV_BAD_SEQLEN;
+    return 0;
+  }
+  return n;
+}
+
+__device__ __forceinline__ Seg read_seg(const Params& p, int s, uint32_t* bad) {
+  const List& l = s < p.list[0].n ? p.list[0] : p.list[1];
+  if (s >= p.list[0].n) s -= p.list[0].n;
+  Seg g;
+  int t1;
+  if (l.starts != nullptr) {
+    const long long a = static_cast<long long>(__ldg(l.starts + s)) * l.per;
+    const long long b = static_cast<long long>(__ldg(l.starts + s + 1)) * l.per;
+    const bool ok = a >= 0 && a <= b && b <= p.tokens;
+    if (!ok) *bad = FP8MLA_DEV_BAD_SEQLEN;
+    g.t0 = ok ? static_cast<int>(a) : 0;
+    t1 = ok ? static_cast<int>(b) : 0;
+  } else {
+    g.t0 = s * l.per;
+    t1 = g.t0 + l.per;
+  }
+  g.rows = (t1 - g.t0) * static_cast<int>(p.group.d);
+  g.keys = max(0, seg_len(l, s, p.page_shift, bad) - l.less);
+  g.tiles = (g.keys + kTile - 1) / kTile;
+  g.row_tiles = (g.rows + kItemRows - 1) / kItemRows;
+  if (g.tiles > 0) {
+    g.full = kPairFixed + g.tiles * kPairTile;
+    g.last = g.rows - (g.row_tiles - 1) * kItemRows > kTile ? g.full : kOneFixed + g.tiles * kOneTile;
+  } else {
+    g.full = g.last = p.joined ? 0 : kEmpty;
+  }
+  g.head = g.row_tiles > 0 ? static_cast<long long>(g.row_tiles - 1) * g.full + g.last : 0;
+  return g;
+}
+
+// Where a share that would begin `off` into an item of this length does: at a tile, at least `few` from either end.
+__device__ __forceinline__ int cut_at(int off, int len, bool pair, int tiles, int few) {
+  const int fixed = pair ? kPairFixed : kOneFixed, each = pair ? kPairTile : kOneTile;
+  if (tiles == 0) return off > 0 ? len : 0;
+  const int t = off <= fixed ? 0 : (off - fixed + each / 2) / each;
+  if (t >= few && tiles - t >= few) return fixed + t * each;
+  return 2 * t < tiles ? 0 : len;
+}
+
+struct Plan {
+  long long lo, hi, seg_at;  // this share, and where the segment begins that it begins in
+  long long sums[17];
+  int seg, units;
+};
+
+// The share of CTA `unit`; the threads of the block together.
+__device__ __forceinline__ void make_plan(const Params& p, Plan* plan, int unit) {
+  const int n = p.list[0].n + p.list[1].n;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  uint32_t bad = 0;
+  long long mine = 0;
+  int most = 0;
+  Seg g = {};
+  for (int s = threadIdx.x; s < n; s += kThreads) {
+    g = read_seg(p, s, &bad);
+    mine += g.head * p.h_kv;
+    most = max(most, g.full);
+  }
+  if (bad && unit == 0) atomicOr(&g_status_ragged, bad);
+  auto scan = [&](long long x, long long* all) {  // sum of the threads before this one, and of all
+    long long s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    if (lane == 31) plan->sums[warp] = s;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const long long y = plan->sums[w];
+      if (w < warp) before += y;
+      total += y;
+    }
+    __syncthreads();
+    *all = total;
+    return before + s - x;
+  };
+  long long total;
+  long long at = scan(mine, &total);
+  const int units = static_cast<int>(
+      max(1ll, min(static_cast<long long>(gridDim.x), total / (kPairFixed + 2 * kPairTile))));
+  const int few = static_cast<int>(max(1ll, min(4ll, total / units / (3 * kPairTile))));
+  if (threadIdx.x == 0) {
+    plan->units = units;
+    plan->lo = 0;
+    plan->hi = total;
+    plan->seg = 0;
+    plan->seg_at = 0;
+  }
+  __syncthreads();
+  const long long raw[2] = {total * unit / units, total * (unit + 1) / units};
+  long long base = 0;
+  for (int s0 = 0; s0 < n; s0 += kThreads) {
+    const int s = s0 + threadIdx.x;
+    long long len = 0;
+    if (n > kThreads) {
+      if (s < n) {
+        g = read_seg(p, s, &bad);
+        len = g.head * p.h_kv;
+      }
+      long long all;
+      at = base + scan(len, &all);
+      base += all;
+    } else {
+      len = mine;
+    }
+    if (s < n && p.joined && unit == 0) p.seg_at[s] = at;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (raw[e] >= at && raw[e] < at + len) {
+        const long long in = raw[e] - at;
+        const long long h = in / g.head;
+        const int rest = static_cast<int>(in - h * g.head);
+        const int rt = min(rest / max(g.full, 1), g.row_tiles - 1);
+        const bool last = rt == g.row_tiles - 1;
+        const bool pair = !last || g.last == g.full;
+        const long long to = at + h * g.head + static_cast<long long>(rt) * g.full +
+                             cut_at(rest - rt * g.full, last ? g.last : g.full, pair, g.tiles, few);
+        if (e == 0) {
+          plan->lo = to;
+          plan->seg = s;
+          plan->seg_at = at;
+        } else {
+          plan->hi = to;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && unit < units) {
+    if (!p.joined) p.cuts[unit].valid = 0;
+    p.lo[unit] = plan->lo;
+    if (unit == units - 1) {
+      p.lo[units] = plan->hi;
+      *p.units = units;
+    }
+  }
+}
+
+struct Item {
+  int list, seg, head, t0, row0, rows, keys, tile_lo, tile_hi;
+  bool pair, whole, first;
+};
+
+// The items of a share, one after the other.
+struct Walk {
+  Seg g;
+  int seg, head, rt, off, left;
+  bool first;
+  __device__ __forceinline__ Walk(const Params& p, const Plan& plan, bool any) {
+    left = any ? static_cast<int>(plan.hi - plan.lo) : 0;
+    seg = plan.seg;
+    first = true;
+    head = rt = off = 0;
+    if (left <= 0) return;
+    uint32_t bad = 0;
+    g = read_seg(p, seg, &bad);
+    const long long in = plan.lo - plan.seg_at;
+    if (g.head > 0) {
+      head = static_cast<int>(in / g.head);
+      const int rest = static_cast<int>(in - head * g.head);
+      if (head < p.h_kv) {
+        rt = min(rest / max(g.full, 1), g.row_tiles - 1);
+        off = rest - rt * g.full;
+      }
+    } else {
+      head = p.h_kv;
+    }
+  }
+  __device__ __forceinline__ bool next(const Params& p, Item* it) {
+    if (left <= 0) return false;
+    const int n = p.list[0].n + p.list[1].n;
+    while (head == p.h_kv || g.head == 0) {
+      if (++seg >= n) return false;
+      uint32_t bad = 0;
+      g = read_seg(p, seg, &bad);
+      head = rt = 0;
+    }
+    const bool last = rt == g.row_tiles - 1;
+    const int len = last ? g.last : g.full;
+    it->list = seg < p.list[0].n ? 0 : 1;
+    it->seg = it->list ? seg - p.list[0].n : seg;
+    it->head = head;
+    it->t0 = g.t0;
+    it->row0 = rt * kItemRows;
+    it->rows = min(kItemRows, g.rows - it->row0);
+    it->keys = g.keys;
+    it->pair = it->rows > kTile;
+    const int fixed = it->pair ? kPairFixed : kOneFixed, each = it->pair ? kPairTile : kOneTile;
+    it->tile_lo = off > 0 ? (off - fixed) / each : 0;
+    if (len - off <= left) {
+      it->tile_hi = g.tiles;
+      left -= len - off;
+    } else {
+      it->tile_hi = (off + left - fixed) / each;
+      left = 0;
+    }
+    it->whole = it->tile_lo == 0 && it->tile_hi == g.tiles;
+    it->first = first;
+    first = false;
+    off = 0;
+    if (++rt == g.row_tiles) {
+      rt = 0;
+      ++head;
+    }
+    return true;
+  }
+};
+
+// ------------------------------------------------------------- the kernel --
+
+template <int kHd, bool kRows>
+struct Lay {
+  static constexpr int kHalves = kHd / 64;                // blocks of 64 dims, 128 bytes a row in f16
+  static constexpr int kQ = kHalves * kTile * 128;        // a stream's Q
+  static constexpr int kF = kHalves * kTile * 128;        // a tile of K or V in f16
+  static constexpr int kRaw = kTile * kHd;                // the same as codes
+  static constexpr int kSlots = 3, kRaws = kRows && kHd == 128 ? 3 : (kHd == 64 ? 8 : 4);
+  static constexpr int kOffF = 2 * kQ, kOffRaw = kOffF + kSlots * kF, kOffCtl = kOffRaw + kRaws * kRaw;
+};
+
+template <int kHd, bool kRows>
+struct Control {
+  Plan plan;
+  uint64_t raw_full[8], raw_empty[8];
+  uint64_t f_full[3], f_empty[3];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t q_full, q_empty, pv_done, xchg, scl_full[3], final_mma;
+  uint32_t tmem_base, abort_flag;
+  float q_scale[2][kTile];
+  float row_l[2][kTile];
+  float scl[kRows ? 3 : 1][3][kRows ? kTile : 4];                                      // K scale, log2 V scale, 1 / V scale
+  float raw_scl[kRows ? Lay<kHd, kRows>::kRaws : 1][2][kRows ? kTile : 4];
+};
+
+template <int kHd, bool kRows>
+constexpr size_t smem_bytes() {
+  return Lay<kHd, kRows>::kOffCtl + sizeof(Control<kHd, kRows>);
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  const bool ok = wait_bounded(bar, parity, abort_flag, &g_status_ragged);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// The tile of K or V that comes at place `at` of an item's sequence of 2 T tiles, as the products take them: streams of
+// their own K0 V0 K1 V1 .., one stream K0 K1 V0 K2 V1 ..
+__device__ __forceinline__ int tile_at(int at, int tiles, bool pair, bool* is_v) {
+  if (pair) {
+    *is_v = at & 1;
+    return at >> 1;
+  }
+  if (at == 0 || at == 2 * tiles - 1) {
+    *is_v = at != 0;
+    return at == 0 ? 0 : tiles - 1;
+  }
+  *is_v = !(at & 1);
+  return (at & 1) ? (at + 1) >> 1 : (at >> 1) - 1;
+}
+
+// Rows of the item in shared memory as f16, each times a power of two that puts its largest value into [2^14, 2^15).
+template <int kHd>
+__device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t* q_tile, float* q_scale, int row0,
+                                       int first, int count, int lane) {
+  constexpr int kLanes = kHd / 8, kStep = 32 / kLanes, kFly = 8;  // lanes a row, rows a pass, passes in flight
+  const int ch = lane % kLanes, sub = lane / kLanes;
+  for (int base = first; base < first + count; base += kStep * kFly) {
+    uint4 x[kFly];
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const int row = base + i * kStep + sub;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (row < first + count && row0 + row < it.rows) {
+        const uint32_t r = static_cast<uint32_t>(it.row0 + row0 + row);
+        const uint32_t t = fast_div(r, p.group);
+        const int head = it.head * static_cast<int>(p.group.d) + static_cast<int>(r - t * p.group.d);
+        x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (it.t0 + static_cast<long long>(t)) * p.q_tok +
+                                                    head * p.q_head + ch * 8));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const int row = base + i * kStep + sub;
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const int e = max(static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu) - 127 - 14, -100);
+      const float inv = exp2i(-e);
+      if (row < first + count && row0 + row < it.rows) {
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv);
+        *reinterpret_cast<uint4*>(q_tile + (ch / 8) * (kTile * 128) + row * 128 + (((ch % 8) ^ (row % 8)) << 4)) =
+            make_uint4(h[0], h[1], h[2], h[3]);
+        if (ch == 0) q_scale[row] = exp2i(e);
+      }
+    }
+    if (row0 + base + kStep * kFly >= it.rows) break;
+  }
+}
+
+template <int kHd, bool kRows>
+__global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_constant__ Params p) {
+  using L = Lay<kHd, kRows>;
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's unit; there is no other shared memory
+  Control<kHd, kRows>* sm = reinterpret_cast<Control<kHd, kRows>*>(smem + L::kOffCtl);
+  volatile uint32_t* abort_flag = &sm->abort_flag;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int unit = blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&sm->raw_full[i], kRows ? 33 : 1);  // the bytes' arrival (+ the scales: one per lane)
+      mbar_init(&sm->raw_empty[i], 4);              // converter warps
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&sm->f_full[i], 4);
+      mbar_init(&sm->f_empty[i], 1);  // commits
+      mbar_init(&sm->scl_full[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm->s_full[i], 1);
+      mbar_init(&sm->p_full[i], 8);
+      mbar_init(&sm->o_full[i], 1);
+    }
+    mbar_init(&sm->q_full, 8);
+    mbar_init(&sm->q_empty, 1);
+    mbar_init(&sm->pv_done, 1);
+    mbar_init(&sm->xchg, 8);
+    mbar_init(&sm->final_mma, 1);
+    sm->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&sm->tmem_base, 512);
+    tmem_relinquish();
+  }
+  griddep_wait();  // inputs may come from the previous kernel in the stream
+  griddep_launch_dependents();
+  make_plan(p, &sm->plan, unit);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem_base;
+  const bool any = unit < sm->plan.units;
+  // TMEM columns: S of either stream or tile parity, then O of either stream (one stream: P behind O)
+  constexpr uint32_t kTS = 0, kTO = 256;
+
+  if (warp < 8) {
+    more_registers<184>();
+    // ------------------------------------------------ softmax, epilogue --
+    const int wg = warp / 4, w = warp % 4;
+    const int r = w * 32 + lane;  // TMEM lane: row of the stream
+    const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+    const float k_scale = kRows ? 1.f : __ldg(p.k_scale), v_scale = kRows ? 1.f : __ldg(p.v_scale);
+    const float c0 = p.softmax_scale * kLog2e * k_scale;
+    uint32_t s_use[2] = {0, 0}, o_use[2] = {0, 0}, item_no = 0, pv_base = 0, tile_no = 0, xchgs = 0;
+    bool ok = true, was_pair = true;
+    Walk walk(p, sm->plan, any);
+    Item it;
+    bool more = walk.next(p, &it);
+    auto fetch_q = [&] {
+      const int row0 = it.pair ? wg * kTile : 0;
+      uint8_t* qt = smem + (it.pair ? wg * L::kQ : 0);
+      float* qs = sm->q_scale[it.pair ? wg : 0];
+      if (it.pair)
+        load_q<kHd>(p, it, qt, qs, row0, w * 32, 32, lane);
+      else
+        load_q<kHd>(p, it, qt, qs, 0, (w + 4 * wg) * 16, 16, lane);
+      fence_proxy_async_smem();
+      warp_arrive(&sm->q_full);
+    };
+    auto exchange = [&]() -> bool {
+      warp_arrive(&sm->xchg);
+      return warp_wait(&sm->xchg, xchgs++ & 1, abort_flag);
+    };
+    if (more && it.tile_hi > it.tile_lo) fetch_q();
+    while (more && ok) {
+      const Item cur = it;
+      const int tiles = cur.tile_hi - cur.tile_lo;
+      const int row = cur.pair ? wg * kTile + r : r;  // of the item
+      const bool live = row < cur.rows;
+      const uint32_t rr = static_cast<uint32_t>(cur.row0 + row);
+      const uint32_t tok = fast_div(rr, p.group);
+      const int head = cur.head * static_cast<int>(p.group.d) + static_cast<int>(rr - tok * p.group.d);
+      const long long token = cur.t0 + static_cast<long long>(tok);
+      if (tiles == 0) {  // no key: zeros, -inf
+        more = walk.next(p, &it);
+        if (!exchange()) break;  // every row's scale of the item before has been read
+        if (more && it.tile_hi > it.tile_lo) fetch_q();
+        if (live && (cur.pair || wg == 0)) {
+          uint4* o = reinterpret_cast<uint4*>(p.out + token * p.o_tok + head * p.o_head);
+#pragma unroll
+          for (int i = 0; i < kHd / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
+          p.lse[token * p.h_q + head] = kNegInf;
+        }
+        continue;
+      }
+      if (!warp_wait(&sm->q_full, item_no & 1, abort_flag)) break;
+      if (cur.pair != was_pair && !exchange()) break;  // the other form's columns are free
+      was_pair = cur.pair;
+      const float c = c0 * (live ? sm->q_scale[cur.pair ? wg : 0][r] : 1.f);
+      const float cc = kRows ? 1.f : c;  // units of the reference to log2
+      const bool busy = __any_sync(0xffffffffu, live);
+      float ref = kNegInf, l = 0.f;
+      auto steps = [&](auto one) {
+        constexpr bool kOne = decltype(one)::value;
+        constexpr int kCols = kOne ? kTile / 2 : kTile;        // whose exponentials this thread takes
+        constexpr int kOCols = kOne ? kHd / 2 : kHd;           // of O that it rescales
+        const uint32_t t_o = tmem + lanes + kTO + (kOne ? wg * kOCols : wg * 128);
+        for (int i = 0; i < tiles; ++i) {
+          const int buf = kOne ? (i & 1) : wg;
+          const uint32_t t_s = tmem + lanes + kTS + buf * 128;
+          const uint32_t t_p = kOne ? tmem + lanes + kTO + 128 + buf * 64 + wg * 32 : t_s;
+          const int valid = min(kTile, cur.keys - (cur.tile_lo + i) * kTile);
+          if (!warp_wait(&sm->s_full[buf], s_use[buf]++ & 1, abort_flag)) return false;
+          if (kRows && !warp_wait(&sm->scl_full[tile_no % 3], (tile_no / 3) & 1, abort_flag)) return false;
+          if (busy) {
+            tc_fence_after();
+            uint32_t s[kCols];
+            const int col0 = kOne ? wg * kCols : 0;
+#pragma unroll
+            for (int k = 0; k < kCols; k += 32) tmem_ld32(t_s + col0 + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
+            uint32_t other[kOne ? 64 : 1];
+            if constexpr (kOne) {
+#pragma unroll
+              for (int k = 0; k < 64; k += 32)
+                tmem_ld32(t_s + (64 - col0) + k, *reinterpret_cast<uint32_t(*)[32]>(other + k));
+            }
+            tmem_ld_wait();
+            float* x = reinterpret_cast<float*>(s);
+            float* y = reinterpret_cast<float*>(other);
+            if (valid < kTile) {
+#pragma unroll
+              for (int j = 0; j < kCols; ++j) x[j] = col0 + j < valid ? x[j] : kNegInf;
+              if constexpr (kOne) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) y[j] = 64 - col0 + j < valid ? y[j] : kNegInf;
+              }
+            }
+            [[maybe_unused]] const float* sk = sm->scl[kRows ? tile_no % 3 : 0][0];
+            [[maybe_unused]] const float* lv = sm->scl[kRows ? tile_no % 3 : 0][1];
+            [[maybe_unused]] const float* iv = sm->scl[kRows ? tile_no % 3 : 0][2];
+            if constexpr (kRows) {  // scores in log2 with the K scale of their key and its V scale
+#pragma unroll
+              for (int j = 0; j < kCols; j += 2) {
+                const float2 a = *reinterpret_cast<const float2*>(sk + col0 + j);
+                const float2 b = *reinterpret_cast<const float2*>(lv + col0 + j);
+                const float2 u = fma_f32x2(mul_f32x2(make_float2(x[j], x[j + 1]), make_float2(c, c)), a, b);
+                x[j] = u.x, x[j + 1] = u.y;
+              }
+              if constexpr (kOne) {
+#pragma unroll
+                for (int j = 0; j < 64; j += 2) {
+                  const float2 a = *reinterpret_cast<const float2*>(sk + 64 - col0 + j);
+                  const float2 b = *reinterpret_cast<const float2*>(lv + 64 - col0 + j);
+                  const float2 u = fma_f32x2(mul_f32x2(make_float2(y[j], y[j + 1]), make_float2(c, c)), a, b);
+                  y[j] = u.x, y[j + 1] = u.y;
+                }
+              }
+            }
+            float mx[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = x[k];
+#pragma unroll
+            for (int j = 4; j + 8 <= kCols; j += 8) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mx[k] = fmax3(mx[k], x[j + 2 * k], x[j + 2 * k + 1]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[kCols - 4 + k]);
+            if constexpr (kOne) {
+#pragma unroll
+              for (int j = 0; j < 64; j += 8) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx[k] = fmax3(mx[k], y[j + 2 * k], y[j + 2 * k + 1]);
+              }
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const bool raise = (top - ref) * cc > kTau;
+            if (i == 0) {
+              ref = top == kNegInf ? 0.f : top;
+            } else if (__any_sync(0xffffffffu, raise && live)) {
+              if (kOne && !warp_wait(&sm->pv_done, (pv_base + i - 1) & 1, abort_flag)) return false;
+              tc_fence_after();
+              const float alpha = raise ? ex2_approx((ref - top) * cc) : 1.f;
+              if (raise) ref = top;
+              l *= alpha;
+#pragma unroll
+              for (int k = 0; k < kOCols; k += 32) {
+                uint32_t o[32];
+                tmem_ld32(t_o + k, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                tmem_st32(t_o + k, o);
+              }
+            }
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int k = 0; k < kCols; k += 32) {
+              uint32_t h[16];
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                float2 d = add_f32x2(make_float2(x[k + j], x[k + j + 1]), make_float2(-ref, -ref));
+                if constexpr (kRows)
+                  d = add_f32x2(d, make_float2(kLift, kLift));
+                else
+                  d = fma_f32x2(d, make_float2(cc, cc), make_float2(kLift, kLift));
+                d.x = ex2_approx(d.x);
+                d.y = ex2_approx(d.y);
+                if constexpr (kRows)
+                  sum[(j >> 1) & 1] = fma_f32x2(d, *reinterpret_cast<const float2*>(iv + col0 + k + j), sum[(j >> 1) & 1]);
+                else
+                  sum[(j >> 1) & 1] = add_f32x2(sum[(j >> 1) & 1], d);
+                h[j / 2] = pack_f16x2(d.x, d.y);
+              }
+              tmem_st16(t_p + k / 2, h);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          ++tile_no;
+          warp_arrive(&sm->p_full[buf]);
+          if (!kOne && lane == 0) mbar_arrive(&sm->p_full[buf]);  // the barrier counts eight warps
+        }
+        return true;
+      };
+      ok = cur.pair ? steps(std::false_type{}) : steps(std::true_type{});
+      if (!ok) break;
+      if (cur.pair)
+        s_use[1 - wg] += tiles;
+      else
+        pv_base += tiles;
+      // Q of the next item, while the last product runs.  Where another warp reads the rows' scales, all have to be
+      // done with those of this item.
+      more = walk.next(p, &it);
+      if (!cur.pair) sm->row_l[wg][r] = l;
+      if ((!cur.pair || (more && !it.pair)) && !exchange()) break;
+      if (!cur.pair) l = sm->row_l[0][r] + sm->row_l[1][r];
+      if (!warp_wait(&sm->q_empty, item_no & 1, abort_flag)) break;
+      ++item_no;
+      if (more && it.tile_hi > it.tile_lo) fetch_q();
+      const int os = cur.pair ? wg : 0;
+      if (!warp_wait(&sm->o_full[os], o_use[os]++ & 1, abort_flag)) break;
+      if (cur.pair) ++o_use[1 - wg];
+      tc_fence_after();
+      if (busy) {
+        const int dims = cur.pair ? kHd : kHd / 2, dim0 = cur.pair ? 0 : wg * (kHd / 2);
+        const uint32_t t_o = tmem + lanes + kTO + os * 128 + dim0;
+        const float m = ref * cc;
+        const bool direct = cur.whole && !p.joined;
+        const float f = direct ? v_scale / l : 1.f;
+        uint16_t* orow = p.out + token * p.o_tok + head * p.o_head + dim0;
+        float* frow = nullptr;
+        if (!direct && live) {
+          float2* ml;
+          if (cur.whole) {
+            const long long at = token * p.h_q + head;
+            frow = p.plane_o[cur.list] + at * kHd + dim0;
+            ml = p.plane_ml[cur.list] + at;
+          } else {
+            const long long at = static_cast<long long>(2 * unit + (cur.first ? 0 : 1)) * p.slot_rows + row;
+            frow = p.slot_o + at * kHd + dim0;
+            ml = p.slot_ml + at;
+          }
+          if (cur.pair || wg == 0) *ml = make_float2(m, l);
+        } else if (live && (cur.pair || wg == 0)) {
+          p.lse[token * p.h_q + head] = (m + lg2_approx(l) - kLift) * kLn2;
+        }
+        for (int k = 0; k < dims; k += 32) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32(t_o + k, o);
+          tmem_ld_wait();
+          if (direct && live) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t h[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                h[e] = pack_bf16x2(__uint_as_float(o[j + 2 * e]) * f, __uint_as_float(o[j + 2 * e + 1]) * f);
+              *reinterpret_cast<uint4*>(orow + k + j) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          } else if (live) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<uint4*>(frow + k + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          }
+        }
+        __syncwarp();
+        tc_fence_before();
+      }
+      if (!p.joined && threadIdx.x == 0 && !more && cur.tile_lo == 0 && !cur.whole) {
+        Cut* cut = p.cuts + unit;
+        cut->head = cur.head;
+        cut->t0 = cur.t0;
+        cut->row0 = cur.row0;
+        cut->rows = cur.rows;
+        const int all = (cur.keys + kTile - 1) / kTile;
+        const int len = cur.pair ? kPairFixed + all * kPairTile : kOneFixed + all * kOneTile;
+        cut->start = sm->plan.hi - (cur.pair ? kPairFixed + cur.tile_hi * kPairTile : kOneFixed + cur.tile_hi * kOneTile);
+        cut->end = cut->start + len;
+        cut->valid = 2 + (cur.first ? 0 : 1);
+      }
+    }
+  } else if (warp < 12) {
+    fewer_registers<72>();
+    // ------------------------------------------------ codes to f16 tiles --
+    const int tid = threadIdx.x - 256;
+    uint32_t f = 0, raw = 0, tile_no = 0;
+    bool ok = true;
+    Walk walk(p, sm->plan, any);
+    Item it;
+    while (ok && walk.next(p, &it)) {
+      const int tiles = it.tile_hi - it.tile_lo;
+      for (int at = 0; at < 2 * tiles; ++at, ++f, ++raw) {
+        bool is_v;
+        const int tile = it.tile_lo + tile_at(at, tiles, it.pair, &is_v);
+        const int valid = min(kTile, it.keys - tile * kTile);
+        const int rs = raw % L::kRaws, fs = f % L::kSlots;
+        if (!warp_wait(&sm->raw_full[rs], (raw / L::kRaws) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (f >= L::kSlots && !warp_wait(&sm->f_empty[fs], (f / L::kSlots - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* src = smem + L::kOffRaw + rs * L::kRaw;
+        uint8_t* dst = smem + L::kOffF + fs * L::kF;
+        if constexpr (kRows) {
+          if (!is_v) {  // past the end: one, so that a stale scale cannot turn a zero weight into a NaN
+            const float a = tid < valid ? sm->raw_scl[rs][0][tid] : 1.f, b = tid < valid ? sm->raw_scl[rs][1][tid] : 1.f;
+            const int ss = tile_no % 3;
+            sm->scl[ss][0][tid] = a;
+            sm->scl[ss][1][tid] = lg2_approx(b);
+            sm->scl[ss][2][tid] = 1.f / b;
+            warp_arrive(&sm->scl_full[ss]);
+            ++tile_no;
+          }
+        }
+        constexpr int kLanes = kHd / 16, kIters = kTile * kLanes / 128;  // 16-byte pieces a row, a thread's pieces
+        uint4 x[kIters];
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+          const int piece = i * 128 + tid;
+          x[i] = *reinterpret_cast<const uint4*>(src + piece * 16);
+          if (piece / kLanes >= valid) x[i] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+          const int piece = i * 128 + tid, key = piece / kLanes, ch = piece % kLanes;
+          const uint4 a = make_uint4(e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16), e4m3x2_to_f16x2(x[i].y),
+                                     e4m3x2_to_f16x2(x[i].y >> 16));
+          const uint4 b = make_uint4(e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16), e4m3x2_to_f16x2(x[i].w),
+                                     e4m3x2_to_f16x2(x[i].w >> 16));
+          // two 16-byte pieces of the 128-byte row; the second block of dims stores them the other way round, so that
+          // a quarter warp meets every bank once
+          const bool swap = ch >= 4;
+          uint8_t* to = dst + (ch / 4) * (kTile * 128) + key * 128;
+          const int c0 = (ch % 4) * 2, x8 = key % 8;
+          *reinterpret_cast<uint4*>(to + (((c0 + (swap ? 1 : 0)) ^ x8) << 4)) = swap ? b : a;
+          *reinterpret_cast<uint4*>(to + (((c0 + (swap ? 0 : 1)) ^ x8) << 4)) = swap ? a : b;
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&sm->f_full[fs]);
+        warp_arrive(&sm->raw_empty[rs]);
+      }
+    }
+  } else {
+    fewer_registers<72>();
+    if (warp == 12) {
+      // ------------------------------------------------ matrix products --
+      constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, kTile, 128);  // f16: Q (K-major) x K (K-major)
+      constexpr uint32_t idesc_pv = make_idesc(0, 0, 0, 1, kHd, 128);    // f16: P (TMEM) x V (MN-major)
+      const bool leader = elect_one();
+      const uint32_t qb = smem_u32(smem), fb = qb + L::kOffF;
+      uint32_t f = 0, p_use[2] = {0, 0}, item_no = 0;
+      bool ok = true;
+      Walk walk(p, sm->plan, any);
+      Item it;
+      auto wait_f = [&](uint32_t at) { return warp_wait(&sm->f_full[at % L::kSlots], (at / L::kSlots) & 1, abort_flag); };
+      auto issue_qk = [&](int q, int buf, uint32_t at) {  // S[buf] = Q[q] K^T
+        tc_fence_after();
+        const uint32_t a = qb + q * L::kQ, b = fb + (at % L::kSlots) * L::kF;
+#pragma unroll
+        for (int kk = 0; kk < kHd / 16; ++kk) {
+          const uint32_t off = (kk / 4) * (kTile * 128) + (kk % 4) * 32;
+          mma_f16_ss_if(leader, tmem + kTS + buf * 128, make_sdesc(a + off, 16, 1024, SWIZZLE_128B),
+                        make_sdesc(b + off, 16, 1024, SWIZZLE_128B), idesc_qk, kk > 0 ? 1u : 0u);
+        }
+        tc_commit_if(leader, &sm->s_full[buf]);
+      };
+      auto issue_pv = [&](uint32_t t_o, uint32_t t_p, uint32_t at, bool fresh) {  // O += P V
+        tc_fence_after();
+        const uint32_t b = fb + (at % L::kSlots) * L::kF;
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_f16_ts_if(leader, tmem + t_o, tmem + t_p + kk * 8,
+                        make_sdesc(b + kk * 2048, kTile * 128, 1024, SWIZZLE_128B), idesc_pv, (fresh && kk == 0) ? 0u : 1u);
+      };
+      auto release = [&](uint32_t at) { tc_commit_if(leader, &sm->f_empty[at % L::kSlots]); };
+      while (ok && walk.next(p, &it)) {
+        const int tiles = it.tile_hi - it.tile_lo;
+        if (tiles == 0) continue;
+        ok = false;
+        if (!warp_wait(&sm->q_full, item_no++ & 1, abort_flag) || !wait_f(f)) break;
+        if (it.pair) {
+          issue_qk(0, 0, f);
+          issue_qk(1, 1, f);
+          release(f);
+          if (tiles == 1) tc_commit_if(leader, &sm->q_empty);
+          int i = 0;
+          for (; i < tiles; ++i) {
+            const uint32_t fv = f + 2 * i + 1, fk = fv + 1;
+            const bool last = i + 1 == tiles;
+            if (!wait_f(fv) || !warp_wait(&sm->p_full[0], p_use[0]++ & 1, abort_flag)) break;
+            issue_pv(kTO, kTS, fv, i == 0);
+            if (last) {
+              tc_commit_if(leader, &sm->o_full[0]);
+            } else {
+              if (!wait_f(fk)) break;
+              issue_qk(0, 0, fk);
+            }
+            if (!warp_wait(&sm->p_full[1], p_use[1]++ & 1, abort_flag)) break;
+            issue_pv(kTO + 128, kTS + 128, fv, i == 0);
+            release(fv);
+            if (last) {
+              tc_commit_if(leader, &sm->o_full[1]);
+            } else {
+              issue_qk(1, 1, fk);
+              release(fk);
+              if (i + 2 == tiles) tc_commit_if(leader, &sm->q_empty);
+            }
+          }
+          if (i < tiles) break;
+        } else {
+          // places: K0 at f, K1 at f + 1, V0, K2, V1, K3 ..
+          issue_qk(0, 0, f);
+          release(f);
+          if (tiles > 1) {
+            if (!wait_f(f + 1)) break;
+            issue_qk(0, 1, f + 1);
+            release(f + 1);
+          }
+          if (tiles <= 2) tc_commit_if(leader, &sm->q_empty);
+          int i = 0;
+          for (; i < tiles; ++i) {
+            const int buf = i & 1;
+            const uint32_t fv = f + (i + 1 < tiles ? 2 * i + 2 : 2 * i + 1);
+            if (!wait_f(fv) || !warp_wait(&sm->p_full[buf], p_use[buf]++ & 1, abort_flag)) break;
+            issue_pv(kTO, kTO + 128 + buf * 64, fv, i == 0);
+            tc_commit_if(leader, &sm->pv_done);
+            release(fv);
+            if (i + 1 == tiles) tc_commit_if(leader, &sm->o_full[0]);
+            if (i + 2 < tiles) {
+              if (!wait_f(fv + 1)) break;
+              issue_qk(0, buf, fv + 1);
+              release(fv + 1);
+              if (i + 3 == tiles) tc_commit_if(leader, &sm->q_empty);
+            }
+          }
+          if (i < tiles) break;
+        }
+        f += 2 * tiles;
+        ok = true;
+      }
+      if (leader) tc_commit(&sm->final_mma);
+      __syncwarp();
+      warp_wait(&sm->final_mma, 0, nullptr);
+    } else if (warp == 13) {
+      // --------------------------------------------- copies of raw tiles --
+      uint32_t raw = 0;
+      bool ok = true;
+      Walk walk(p, sm->plan, any);
+      Item it;
+      const int chunk_shift = min(p.page_shift, 7);  // keys a copy
+      const int chunks = kTile >> chunk_shift;
+      while (ok && walk.next(p, &it)) {
+        const int tiles = it.tile_hi - it.tile_lo;
+        const List& l = p.list[it.list];
+        const int32_t* table = l.table + static_cast<long long>(it.seg) * l.max_blocks;
+        // lane c: the page of chunk c of a tile
+        auto fetch = [&](int tile) {
+          const int key = tile * kTile + (lane << chunk_shift);
+          return tile < it.tile_hi && lane < chunks && key < it.keys ? __ldg(table + (key >> p.page_shift)) : 0;
+        };
+        int page[2] = {fetch(it.tile_lo), fetch(it.tile_lo + 1)};
+        int next = fetch(it.tile_lo + 2);
+        for (int at = 0; at < 2 * tiles; ++at, ++raw) {
+          bool is_v;
+          const int t = tile_at(at, tiles, it.pair, &is_v), tile = it.tile_lo + t;
+          const int rs = raw % L::kRaws;
+          const int valid = min(kTile, it.keys - tile * kTile);
+          int block = (t & 1) ? page[1] : page[0];
+          if (block < 0 || block >= p.num_blocks) {
+            atomicOr(&g_status_ragged, FP8MLA_DEV_BAD_PAGE);
+            block = 0;
+          }
+          if (raw >= L::kRaws && !warp_wait(&sm->raw_empty[rs], (raw / L::kRaws - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&sm->raw_full[rs], static_cast<uint32_t>(valid) * kHd);
+          __syncwarp();
+          const int first = lane << chunk_shift;
+          const long long in_page = (static_cast<long long>(tile) * kTile + first) & ((1 << p.page_shift) - 1);
+          const long long line = ((static_cast<long long>(block) * p.h_kv + it.head) << p.page_shift) + in_page;
+          if (lane < chunks && first < valid)
+            bulk_load(smem + L::kOffRaw + rs * L::kRaw + first * kHd, (is_v ? p.v : p.k) + line * kHd,
+                      static_cast<uint32_t>(min(1 << chunk_shift, valid - first)) * kHd, &sm->raw_full[rs]);
+          if constexpr (kRows) {
+            if (!is_v) {  // scales of four keys a lane
+              const int key = lane * 4;
+              const int from = __shfl_sync(0xffffffffu, block, key >> chunk_shift);
+              const long long at4 = ((static_cast<long long>(from) * p.h_kv + it.head) << p.page_shift) +
+                                    ((static_cast<long long>(tile) * kTile + key) & ((1 << p.page_shift) - 1));
+              if (key < valid) {
+                cp_async16(smem_u32(&sm->raw_scl[rs][0][key]), p.k_scale + at4, 16u);
+                cp_async16(smem_u32(&sm->raw_scl[rs][1][key]), p.v_scale + at4, 16u);
+              }
+            }
+            cp_async_mbar_arrive(&sm->raw_full[rs]);
+          }
+          if (is_v) {  // the tile is done: its place takes the one after the next
+            if (t & 1)
+              page[1] = next;
+            else
+              page[0] = next;
+            next = fetch(tile + 3);
+          }
+        }
+      }
+      if constexpr (kRows) cp_async_wait_all();  // this lane's copies have landed before the CTA can exit
+      for (uint32_t j = raw > L::kRaws ? raw - L::kRaws : 0; j < raw; ++j)
+        warp_wait(&sm->raw_full[j % L::kRaws], (j / L::kRaws) & 1, nullptr);
+    } else if (p.fill_out || p.fill_lse) {
+      // ------------------------------------------- rows of no sequence --
+      const List& l = p.list[0];
+      const int lo = l.starts ? min(max(__ldg(l.starts), 0), p.tokens) : 0;
+      const int hi = l.starts ? min(max(__ldg(l.starts + l.n), lo), p.tokens) : min(l.n, p.tokens);
+      const int none = lo + p.tokens - hi;
+      const long long heads = static_cast<long long>(none) * p.h_q;
+      for (long long i = unit * 2 + (warp - 14); i < heads; i += 2 * gridDim.x) {
+        int t = static_cast<int>(i / p.h_q);
+        const int h = static_cast<int>(i % p.h_q);
+        if (t >= lo) t += hi - lo;
+        if (p.fill_out && lane < kHd / 8)
+          *reinterpret_cast<uint4*>(p.out + t * p.o_tok + h * p.o_head + lane * 8) = make_uint4(0, 0, 0, 0);
+        if (p.fill_lse && lane == 0) p.lse[static_cast<long long>(t) * p.h_q + h] = kNegInf;
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ merges --
+
+// A row's sum over the pieces [slot lo (at s0), slots 0 of the units after it up to `last`], by one warp: lane l owns
+// dims [kV l, kV l + kV).
+template <int kHd>
+struct RowSum {
+  static constexpr int kV = kHd / 32;
+  float m = kNegInf, l = 0.f, acc[kV] = {};
+  __device__ __forceinline__ void add(float pm, float pl, const float* o, int lane) {
+    const float top = fmaxf(m, pm);
+    if (top == kNegInf) return;
+    const float a = ex2_approx(m - top), b = ex2_approx(pm - top);
+    m = top;
+    l = l * a + pl * b;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] = acc[i] * a + __ldcg(o + lane * kV + i) * b;
+  }
+  __device__ __forceinline__ void pieces(const Params& p, int unit, int last, int slot, int row, int lane) {
+    for (int v = unit; v <= last; ++v) {
+      if (v > unit && p.lo[v + 1] <= p.lo[v]) continue;  // a share without work
+      const long long at = static_cast<long long>(2 * v + (v == unit ? slot : 0)) * p.slot_rows + row;
+      const float2 ml = p.slot_ml[at];
+      add(ml.x, ml.y, p.slot_o + at * kHd, lane);
+    }
+  }
+  __device__ __forceinline__ void finish(uint16_t* out, float* lse, float sink, float v_scale, int lane) {
+    float f, ls;
+    finish_row(m - kLift, l, sink, v_scale, &f, &ls);
+    if (l != l) f = ls = l;  // NaN
+    uint16_t* to = out + lane * kV;
+    if constexpr (kV == 4) {
+      *reinterpret_cast<uint2*>(to) =
+          make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f));
+    } else {
+      *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(acc[0] * f, acc[1] * f);
+    }
+    if (lane == 0) *lse = ls;
+  }
+};
+
+constexpr int kMergeRows = 32;  // rows of an item a CTA merges
+
+template <int kHd>
+__global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant__ Params p, int scale_rows) {
+  griddep_wait();
+  const int unit = blockIdx.x, units = *p.units;
+  if (unit >= units) return;
+  const Cut cut = p.cuts[unit];
+  const int row0 = blockIdx.y * kMergeRows;
+  if (cut.valid == 0 || row0 >= cut.rows) return;
+  int last = unit;
+  while (last + 1 < units && p.lo[last + 1] < cut.end) ++last;
+  const int lane = threadIdx.x % 32;
+  const float v_scale = scale_rows ? 1.f : *p.v_scale;
+  for (int row = row0 + threadIdx.x / 32; row < min(cut.rows, row0 + kMergeRows); row += 4) {
+    RowSum<kHd> sum;
+    sum.pieces(p, unit, last, cut.valid - 2, row, lane);
+    const uint32_t r = static_cast<uint32_t>(cut.row0 + row), t = fast_div(r, p.group);
+    const int head = cut.head * static_cast<int>(p.group.d) + static_cast<int>(r - t * p.group.d);
+    const long long token = cut.t0 + static_cast<long long>(t);
+    sum.finish(p.out + token * p.o_tok + head * p.o_head, p.lse + token * p.h_q + head, kNegInf, v_scale, lane);
+  }
+}
+
+// Row = (token, query head) of a decode step behind shared prefixes: its prefix, its own keys before the block, the
+// block's keys that it sees, its sink.  One warp a row.
+template <int kHd>
+__global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant__ Params p, int scale_rows) {
+  griddep_wait();
+  constexpr int kV = kHd / 32;
+  const int lane = threadIdx.x % 32;
+  const int group = static_cast<int>(p.group.d), rows = p.q_len * group;
+  const int b = blockIdx.x / p.h_kv, kvh = blockIdx.x % p.h_kv;
+  const int row = blockIdx.y * 4 + threadIdx.x / 32;
+  if (row >= rows) return;
+  const int tok = row / group, head = kvh * group + row % group;
+  const long long token = static_cast<long long>(b) * p.q_len + tok, at = token * p.h_q + head;
+  const int units = *p.units;
+  const float k_scale = scale_rows ? 1.f : *p.k_scale, v_scale = scale_rows ? 1.f : *p.v_scale;
+  uint32_t bad = 0;
+  RowSum<kHd> sum;
+  auto list = [&](int which, int seg) {
+    const Seg g = read_seg(p, which ? p.list[0].n + seg : seg, &bad);
+    if (g.tiles == 0) return;
+    const int r = static_cast<int>(token - g.t0) * group + row % group;
+    const int rt = r / kItemRows;
+    const long long start = p.seg_at[which ? p.list[0].n + seg : seg] + kvh * g.head + static_cast<long long>(rt) * g.full;
+    const long long end = start + (rt == g.row_tiles - 1 ? g.last : g.full);
+    int first = 0, last = 0;  // the shares that begin at or before the item, and before its end
+    for (int v = lane; v < units; v += 32) {
+      const long long lo = p.lo[v];
+      first += lo <= start;
+      last += lo < end;
+    }
+    first = __reduce_add_sync(0xffffffffu, first) - 1;
+    last = __reduce_add_sync(0xffffffffu, last) - 1;
+    if (first == last) {
+      const float2 ml = p.plane_ml[which][at];
+      sum.add(ml.x, ml.y, p.plane_o[which] + at * kHd, lane);
+    } else {
+      sum.pieces(p, first, last, p.lo[first] == start ? 0 : 1, r - rt * kItemRows, lane);
+    }
+  };
+  for (int g0 = 0; g0 < p.list[0].n; g0 += 32) {
+    const int g = g0 + lane;
+    bool here = false;
+    if (g < p.list[0].n) {
+      const int lo = __ldg(p.list[0].starts + g), hi = __ldg(p.list[0].starts + g + 1);
+      here = lo >= 0 && lo <= b && b < hi && static_cast<long long>(hi) * p.q_len <= p.tokens;
+    }
+    const unsigned in = __ballot_sync(0xffffffffu, here);
+    if (in != 0) {
+      list(0, g0 + __ffs(in) - 1);
+      break;
+    }
+  }
+  list(1, b);
+  if (p.list[1].less > 0) {
+    const List& l = p.list[1];
+    const int len = seg_len(l, b, p.page_shift, &bad);
+    float q[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+      q[i] = __uint_as_float(static_cast<uint32_t>(p.q[token * p.q_tok + head * p.q_head + lane * kV + i]) << 16);
+    const float c = p.softmax_scale * kLog2e * k_scale;
+    for (int x = max(0, p.q_len - len); x < p.q_len; ++x) {
+      const bool sees = p.spec_mask != nullptr
+                            ? p.spec_mask[(static_cast<long long>(b) * p.q_len + tok) * p.q_len + x] != 0
+                            : x <= tok;
+      if (!sees) continue;
+      const int key = len - p.q_len + x;
+      int block = __ldg(l.table + static_cast<long long>(b) * l.max_blocks + (key >> p.page_shift));
+      if (block < 0 || block >= p.num_blocks) {
+        if (lane == 0) atomicOr(&g_status_ragged, FP8MLA_DEV_BAD_PAGE);
+        block = 0;
+      }
+      const long long line =
+          ((static_cast<long long>(block) * p.h_kv + kvh) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+      float kx[kV], vx[kV];
+      if constexpr (kV == 4) {
+        const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(p.k + line * kHd) + lane);
+        const uint32_t d = __ldg(reinterpret_cast<const uint32_t*>(p.v + line * kHd) + lane);
+        const uint32_t h[4] = {e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(d), e4m3x2_to_f16x2(d >> 16)};
+        kx[0] = f16_lo(h[0]), kx[1] = f16_hi(h[0]), kx[2] = f16_lo(h[1]), kx[3] = f16_hi(h[1]);
+        vx[0] = f16_lo(h[2]), vx[1] = f16_hi(h[2]), vx[2] = f16_lo(h[3]), vx[3] = f16_hi(h[3]);
+      } else {
+        const uint32_t a = e4m3x2_to_f16x2(__ldg(reinterpret_cast<const uint16_t*>(p.k + line * kHd) + lane));
+        const uint32_t d = e4m3x2_to_f16x2(__ldg(reinterpret_cast<const uint16_t*>(p.v + line * kHd) + lane));
+        kx[0] = f16_lo(a), kx[1] = f16_hi(a);
+        vx[0] = f16_lo(d), vx[1] = f16_hi(d);
+      }
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < kV; ++i) dot += q[i] * kx[i];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      float s = dot * c, sv = 1.f;
+      if (scale_rows) {
+        s *= __ldg(p.k_scale + line);
+        sv = __ldg(p.v_scale + line);
+      }
+      const float m = s + kLift, top = s == s ? fmaxf(sum.m, m) : fmaxf(sum.m, 0.f);  // the pieces' sums are lifted
+      if (top == kNegInf) continue;
+      const float a = ex2_approx(sum.m - top), w = ex2_approx(m - top);
+      sum.m = top;
+      sum.l = sum.l * a + w;
+#pragma unroll
+      for (int i = 0; i < kV; ++i) sum.acc[i] = sum.acc[i] * a + vx[i] * (w * sv);
+    }
+  }
+  sum.finish(p.out + at * kHd, p.lse + at, p.sinks ? p.sinks[head] : kNegInf, v_scale, lane);
+}
+
+// -------------------------------------------------------------------- host --
+
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+struct Space {  // the workspace: offsets, and the grid it is for
+  int grid, slot_rows;
+  size_t units, lo, seg_at, cuts, slot_ml, slot_o, plane_ml[2], plane_o[2], bytes;
+};
+
+// tokens and segments of a list that reads up to max_keys keys a segment
+long long most_work(long long tokens, long long segs, int h_kv, int group, long long max_keys) {
+  const long long tiles = (max_keys + kTile - 1) / kTile;
+  return h_kv * (tokens * group / kItemRows + segs) * (kPairFixed + kPairTile * std::max(tiles, 1ll));
+}
+
+Space lay_out(long long work, long long tokens, int segs, int h_q, int group, int hd, bool joined) {
+  Space s;
+  s.grid = static_cast<int>(std::max(1ll, std::min<long long>(device_sms(), work / (kPairFixed + 2 * kPairTile))));
+  s.slot_rows = static_cast<int>(std::min<long long>(kItemRows, std::max(1ll, tokens * group)));
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round_up(bytes, 256);
+    return here;
+  };
+  const size_t slots = s.grid > 1 ? static_cast<size_t>(2) * s.grid * s.slot_rows : 0;
+  const size_t rows = joined ? static_cast<size_t>(tokens) * h_q : 0;
+  s.units = take(256);
+  s.lo = take((s.grid + 1) * sizeof(long long));
+  s.seg_at = take(joined ? segs * sizeof(long long) : 0);
+  s.cuts = take(joined ? 0 : s.grid * sizeof(Cut));
+  s.slot_ml = take(slots * sizeof(float2));
+  s.slot_o = take(slots * hd * sizeof(float));
+  for (int i = 0; i < 2; ++i) {
+    s.plane_ml[i] = take(rows * sizeof(float2));
+    s.plane_o[i] = take(rows * hd * sizeof(float));
+  }
+  s.bytes = at;
+  return s;
+}
+
+void use(Params* p, const Space& s, void* workspace) {
+  char* w = static_cast<char*>(workspace);
+  p->units = reinterpret_cast<int*>(w + s.units);
+  p->lo = reinterpret_cast<long long*>(w + s.lo);
+  p->seg_at = reinterpret_cast<long long*>(w + s.seg_at);
+  p->cuts = reinterpret_cast<Cut*>(w + s.cuts);
+  p->slot_ml = reinterpret_cast<float2*>(w + s.slot_ml);
+  p->slot_o = reinterpret_cast<float*>(w + s.slot_o);
+  for (int i = 0; i < 2; ++i) {
+    p->plane_ml[i] = reinterpret_cast<float2*>(w + s.plane_ml[i]);
+    p->plane_o[i] = reinterpret_cast<float*>(w + s.plane_o[i]);
+  }
+  p->slot_rows = s.slot_rows;
+}
+
+template <int kHd, bool kRows>
+cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
+  constexpr size_t smem = smem_bytes<kHd, kRows>();
+  static_assert(smem <= 232448, "the tiles fit in shared memory");
+  static std::atomic<uint64_t> configured{0};
+  const cudaError_t e = configure_once(configured, [&] {
+    cudaFuncAttributes f;
+    cudaError_t x = cudaFuncGetAttributes(&f, ragged_kernel<kHd, kRows>);
+    // the warpgroups' shares, 2 x 184 + 2 x 72 registers a thread, come out of what the launch takes
+    if (x == cudaSuccess && f.numRegs * kThreads < 2 * 128 * (184 + 72)) x = cudaErrorInvalidConfiguration;
+    return x != cudaSuccess ? x
+                            : cudaFuncSetAttribute(ragged_kernel<kHd, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+  });
+  if (e != cudaSuccess) return e;
+  return launch_dependent(ragged_kernel<kHd, kRows>, dim3(grid), dim3(kThreads), smem, stream, p);
+}
+
+cudaError_t launch_any(const Params& p, int hd, int scale_rows, int grid, cudaStream_t stream) {
+  if (hd == 64) return scale_rows ? launch<64, true>(p, grid, stream) : launch<64, false>(p, grid, stream);
+  return scale_rows ? launch<128, true>(p, grid, stream) : launch<128, false>(p, grid, stream);
+}
+
+bool cache_ok(const RaggedCache& c, int h_kv, int* page_shift) {
+  int shift = 4;
+  while (shift < 9 && (1 << shift) != c.page_size) ++shift;
+  if (shift == 9 || c.num_blocks < 1) return false;  // 16, 32, 64, 128 or 256 keys a page
+  *page_shift = shift;
+  if (c.k == nullptr || c.v == nullptr || c.k_scale == nullptr || c.v_scale == nullptr) return false;
+  const uintptr_t need = c.scale_rows ? 16 : 4;
+  return !misaligned(c.k, 16) && !misaligned(c.v, 16) && !misaligned(c.k_scale, need) && !misaligned(c.v_scale, need) &&
+         h_kv >= 1;
+}
+
+bool heads_ok(int h_q, int h_kv, int head_dim) {
+  return (head_dim == 64 || head_dim == 128) && h_q >= 1 && h_kv >= 1 && h_q % h_kv == 0 && h_q <= 65536;
+}
+
+void fill_cache(Params* p, const RaggedCache& c) {
+  p->k = static_cast<const uint8_t*>(c.k);
+  p->v = static_cast<const uint8_t*>(c.v);
+  p->k_scale = c.k_scale;
+  p->v_scale = c.v_scale;
+  p->num_blocks = c.num_blocks;
+}
+
+constexpr long long kMostKeys = 1ll << 30;  // a segment
+constexpr long long kMostRows = 1ll << 30;  // tokens * h_q
+
+}  // namespace ragged
+
+size_t cross_workspace_bytes(int n_tokens, int bs, int h_q, int h_kv, int head_dim, long long max_keys) {
+  using namespace ragged;
+  if (!heads_ok(h_q, h_kv, head_dim) || n_tokens < 0 || bs < 0 || max_keys < 0 || max_keys > kMostKeys ||
+      static_cast<long long>(n_tokens) * h_q > kMostRows)
+    return 0;
+  const int group = h_q / h_kv;
+  return lay_out(most_work(n_tokens, bs, h_kv, group, max_keys), n_tokens, bs, h_q, group, head_dim, false).bytes;
+}
+
+fp8mla_status_t cross_entry(const CrossArgs& a, cudaStream_t stream) {
+  using namespace ragged;
+  Params p = {};
+  if (!heads_ok(a.h_q, a.h_kv, a.head_dim) || a.n_tokens < 0 || a.bs < 0 || a.max_blocks < 1 ||
+      !(a.softmax_scale > 0.f) || !cache_ok(a.cache, a.h_kv, &p.page_shift))
+    return FP8MLA_ERR_INVALID_ARG;
+  const long long max_keys = static_cast<long long>(a.max_blocks) << p.page_shift;
+  const long long rows = static_cast<long long>(a.n_tokens) * a.h_q;
+  if (max_keys > kMostKeys || rows > kMostRows || (a.q_starts == nullptr && a.n_tokens < a.bs))
+    return FP8MLA_ERR_INVALID_ARG;
+  if (a.n_tokens == 0 || (a.bs == 0 && !a.fill_out && !a.fill_lse)) return FP8MLA_OK;
+  if (a.q == nullptr || a.out == nullptr || a.lse == nullptr || (a.bs > 0 && (a.block_table == nullptr || a.kv_lens == nullptr)))
+    return FP8MLA_ERR_INVALID_ARG;
+  if (misaligned(a.q, 16) || misaligned(a.out, 16) || misaligned(a.lse, 4) || misaligned(a.q_starts, 4) ||
+      misaligned(a.block_table, 4) || misaligned(a.kv_lens, 4) || ((a.q_token | a.q_head | a.out_token | a.out_head) & 7))
+    return FP8MLA_ERR_INVALID_ARG;
+  const int group = a.h_q / a.h_kv;
+  const Space s =
+      lay_out(most_work(a.n_tokens, a.bs, a.h_kv, group, max_keys), a.n_tokens, a.bs, a.h_q, group, a.head_dim, false);
+  if (a.workspace == nullptr || misaligned(a.workspace, 256)) return FP8MLA_ERR_INVALID_ARG;
+  if (a.workspace_bytes < s.bytes) return FP8MLA_ERR_WORKSPACE_TOO_SMALL;
+  // the output may take the queries' place; nothing else is shared
+  const Rows q = rows_of(a.q, a.q_token, a.q_head, a.n_tokens, a.h_q, a.head_dim, 2);
+  const Rows out = rows_of(a.out, a.out_token, a.out_head, a.n_tokens, a.h_q, a.head_dim, 2);
+  const Rows lse = block_of(a.lse, rows * 4), ws = block_of(a.workspace, s.bytes);
+  if (clobbers(out, q) || rows_overlap_themselves(out) || rows_overlap(lse, q) || rows_overlap(ws, q) ||
+      rows_overlap(out, lse) || rows_overlap(out, ws) || rows_overlap(lse, ws))
+    return FP8MLA_ERR_INVALID_ARG;
+  p.q = static_cast<const uint16_t*>(a.q);
+  fill_cache(&p, a.cache);
+  p.out = static_cast<uint16_t*>(a.out);
+  p.lse = a.lse;
+  p.q_tok = a.q_token, p.q_head = a.q_head, p.o_tok = a.out_token, p.o_head = a.out_head;
+  p.list[0] = List{a.q_starts, a.kv_lens, a.block_table, a.bs, a.max_blocks, 1, 0};
+  p.list[1] = List{};
+  p.group = make_fast_div(group);
+  p.softmax_scale = a.softmax_scale;
+  p.tokens = a.n_tokens;
+  p.h_q = a.h_q;
+  p.h_kv = a.h_kv;
+  p.fill_out = a.fill_out;
+  p.fill_lse = a.fill_lse;
+  use(&p, s, a.workspace);
+  cudaError_t e = launch_any(p, a.head_dim, a.cache.scale_rows, s.grid, stream);
+  if (e == cudaSuccess && s.grid > 1) {
+    const dim3 grid(s.grid, (s.slot_rows + kMergeRows - 1) / kMergeRows);
+    e = a.head_dim == 64
+            ? launch_dependent(cross_merge_kernel<64>, grid, dim3(128), 0, stream, p, a.cache.scale_rows)
+            : launch_dependent(cross_merge_kernel<128>, grid, dim3(128), 0, stream, p, a.cache.scale_rows);
+  }
+  return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
+}
+
+namespace ragged {
+long long shared_work(int bs, int q_len, int h_kv, int group, int n_prefixes, long long max_prefix_keys,
+                      long long max_keys) {
+  const long long tokens = static_cast<long long>(bs) * q_len;
+  return (n_prefixes > 0 ? most_work(tokens, n_prefixes, h_kv, group, max_prefix_keys) : 0) +
+         most_work(tokens, bs, h_kv, group, max_keys);
+}
+bool shared_sizes_ok(int bs, int q_len, int h_q, int h_kv, int head_dim, int n_prefixes, long long max_prefix_keys,
+                     long long max_keys) {
+  return heads_ok(h_q, h_kv, head_dim) && bs >= 0 && q_len >= 1 && q_len <= 32 && n_prefixes >= 0 &&
+         max_prefix_keys >= 0 && max_prefix_keys <= kMostKeys && max_keys >= 0 && max_keys <= kMostKeys &&
+         static_cast<long long>(bs) * q_len * h_q <= kMostRows && static_cast<long long>(bs) * h_kv <= 0x7FFFFFFF &&
+         static_cast<long long>(n_prefixes) + bs <= kMostRows;
+}
+}  // namespace ragged
+
+size_t shared_workspace_bytes(int bs, int q_len, int h_q, int h_kv, int head_dim, int n_prefixes,
+                              long long max_prefix_keys, long long max_keys) {
+  using namespace ragged;
+  if (!shared_sizes_ok(bs, q_len, h_q, h_kv, head_dim, n_prefixes, max_prefix_keys, max_keys)) return 0;
+  const int group = h_q / h_kv;
+  return lay_out(shared_work(bs, q_len, h_kv, group, n_prefixes, max_prefix_keys, max_keys),
+                 static_cast<long long>(bs) * q_len, n_prefixes + bs, h_q, group, head_dim, true)
+      .bytes;
+}
+
+fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream) {
+  using namespace ragged;
+  Params p = {};
+  if (!cache_ok(a.cache, a.h_kv, &p.page_shift) || a.max_blocks < 1 || (a.n_prefixes > 0 && a.prefix_blocks < 1) ||
+      !(a.softmax_scale > 0.f))
+    return FP8MLA_ERR_INVALID_ARG;
+  const long long prefix_keys = a.n_prefixes > 0 ? static_cast<long long>(a.prefix_blocks) << p.page_shift : 0;
+  const long long keys = static_cast<long long>(a.max_blocks) << p.page_shift;
+  if (!shared_sizes_ok(a.bs, a.q_len, a.h_q, a.h_kv, a.head_dim, a.n_prefixes, prefix_keys, keys))
+    return FP8MLA_ERR_INVALID_ARG;
+  if (a.bs == 0) return FP8MLA_OK;
+  if (a.q == nullptr || a.out == nullptr || a.lse == nullptr || a.block_table == nullptr || a.seqlens == nullptr ||
+      (a.n_prefixes > 0 && (a.prefix_table == nullptr || a.prefix_lens == nullptr || a.prefix_starts == nullptr)))
+    return FP8MLA_ERR_INVALID_ARG;
+  if (misaligned(a.q, 16) || misaligned(a.out, 16) || misaligned(a.lse, 4) || misaligned(a.block_table, 4) ||
+      misaligned(a.seqlens, 4) || misaligned(a.prefix_table, 4) || misaligned(a.prefix_lens, 4) ||
+      misaligned(a.prefix_starts, 4) || misaligned(a.sinks, 4))
+    return FP8MLA_ERR_INVALID_ARG;
+  const int group = a.h_q / a.h_kv;
+  const long long tokens = static_cast<long long>(a.bs) * a.q_len;
+  const Space s = lay_out(shared_work(a.bs, a.q_len, a.h_kv, group, a.n_prefixes, prefix_keys, keys), tokens,
+                          a.n_prefixes + a.bs, a.h_q, group, a.head_dim, true);
+  if (a.workspace == nullptr || misaligned(a.workspace, 256)) return FP8MLA_ERR_INVALID_ARG;
+  if (a.workspace_bytes < s.bytes) return FP8MLA_ERR_WORKSPACE_TOO_SMALL;
+  const uint64_t rows = static_cast<uint64_t>(tokens) * a.h_q;
+  const Rows q = block_of(a.q, rows * a.head_dim * 2), out = block_of(a.out, rows * a.head_dim * 2);
+  const Rows lse = block_of(a.lse, rows * 4), ws = block_of(a.workspace, s.bytes);
+  if (clobbers(out, q) || rows_overlap(lse, q) || rows_overlap(ws, q) || rows_overlap(out, lse) ||
+      rows_overlap(out, ws) || rows_overlap(lse, ws))
+    return FP8MLA_ERR_INVALID_ARG;
+  p.q = static_cast<const uint16_t*>(a.q);
+  fill_cache(&p, a.cache);
+  p.out = static_cast<uint16_t*>(a.out);
+  p.lse = a.lse;
+  p.q_tok = p.o_tok = static_cast<long long>(a.h_q) * a.head_dim;
+  p.q_head = p.o_head = a.head_dim;
+  const bool block = a.q_len > 1 || a.spec_mask != nullptr;
+  p.list[0] = List{a.prefix_starts, a.prefix_lens, a.prefix_table, a.n_prefixes, a.prefix_blocks, a.q_len, 0};
+  p.list[1] = List{nullptr, a.seqlens, a.block_table, a.bs, a.max_blocks, a.q_len, block ? a.q_len : 0};
+  p.spec_mask = a.spec_mask;
+  p.sinks = a.sinks;
+  p.group = make_fast_div(group);
+  p.softmax_scale = a.softmax_scale;
+  p.joined = 1;
+  p.tokens = static_cast<int>(tokens);
+  p.h_q = a.h_q;
+  p.h_kv = a.h_kv;
+  p.q_len = a.q_len;
+  use(&p, s, a.workspace);
+  cudaError_t e = launch_any(p, a.head_dim, a.cache.scale_rows, s.grid, stream);
+  if (e == cudaSuccess) {
+    const dim3 grid(static_cast<unsigned>(a.bs) * a.h_kv, (a.q_len * group + 3) / 4);
+    e = a.head_dim == 64
+            ? launch_dependent(shared_merge_kernel<64>, grid, dim3(128), 0, stream, p, a.cache.scale_rows)
+            : launch_dependent(shared_merge_kernel<128>, grid, dim3(128), 0, stream, p, a.cache.scale_rows);
+  }
+  return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
+}
+
+uint32_t ragged_read_and_clear_status() {
+  uint32_t v = 0, z = 0;
+  cudaMemcpyFromSymbol(&v, g_status_ragged, sizeof(v));
+  cudaMemcpyToSymbol(g_status_ragged, &z, sizeof(z));
+  return v;
+}
+
+}  // namespace fp8mla
