@@ -15,7 +15,7 @@
 //     softmax runs.
 //   up to 128 rows: one stream, S in two buffers by tile parity, and both softmax warpgroups share a tile's columns.
 // Warps: 0-3 and 4-7 the two softmax warpgroups, 8-11 turn raw tiles into f16, 12 issues the products, 13 copies raw
-// tiles (one bulk copy per page and operand), 14 and 15 fill rows of no sequence.
+// tiles (one bulk copy per page and operand), 14 tells the others the share's items, 15 fills rows of no sequence.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -35,6 +35,7 @@ namespace ragged {
 constexpr int kTile = 128;      // keys a tile, rows a stream
 constexpr int kItemRows = 256;  // rows an item
 constexpr int kThreads = 512;
+constexpr int kSoftmaxRegs = 192, kConvertRegs = 64, kIssueRegs = 64;  // registers a thread of the warpgroups
 constexpr float kLift = 7.f;    // P = 2^(score - reference + 7): 2^15 at most in f16, normal down to 2^-21 of the largest
 constexpr float kTau = 8.f;     // the reference moves when a score passes it by more
 
@@ -51,7 +52,7 @@ struct List {
 
 struct Cut {  // the item that a share begins and does not end
   long long start, end;
-  int valid, head, t0, row0, rows;
+  int valid, slot, head, t0, row0, rows;
 };
 
 struct Params {
@@ -235,18 +236,21 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan* plan, int unit)
   }
 }
 
+// One item of a share, or the part of it that lies in the share.
 struct Item {
   int list, seg, head, t0, row0, rows, keys, tile_lo, tile_hi;
-  bool pair, whole, first;
+  int slot;  // where its sums go: kDirect the outputs, kPlane the list's plane, else the workspace's slot
+  bool pair, end;
 };
+constexpr int kDirect = -1, kPlane = -2;
 
 // The items of a share, one after the other.
 struct Walk {
   Seg g;
   int seg, head, rt, off, left;
   bool first;
-  __device__ __forceinline__ Walk(const Params& p, const Plan& plan, bool any) {
-    left = any ? static_cast<int>(plan.hi - plan.lo) : 0;
+  __device__ __forceinline__ Walk(const Params& p, const Plan& plan) {
+    left = static_cast<int>(plan.hi - plan.lo);
     seg = plan.seg;
     first = true;
     head = rt = off = 0;
@@ -254,6 +258,7 @@ struct Walk {
     uint32_t bad = 0;
     g = read_seg(p, seg, &bad);
     const long long in = plan.lo - plan.seg_at;
+    head = p.h_kv;
     if (g.head > 0) {
       head = static_cast<int>(in / g.head);
       const int rest = static_cast<int>(in - head * g.head);
@@ -261,11 +266,9 @@ struct Walk {
         rt = min(rest / max(g.full, 1), g.row_tiles - 1);
         off = rest - rt * g.full;
       }
-    } else {
-      head = p.h_kv;
     }
   }
-  __device__ __forceinline__ bool next(const Params& p, Item* it) {
+  __device__ __forceinline__ bool next(const Params& p, const Plan& plan, int unit, Item* it) {
     if (left <= 0) return false;
     const int n = p.list[0].n + p.list[1].n;
     while (head == p.h_kv || g.head == 0) {
@@ -274,8 +277,7 @@ struct Walk {
       g = read_seg(p, seg, &bad);
       head = rt = 0;
     }
-    const bool last = rt == g.row_tiles - 1;
-    const int len = last ? g.last : g.full;
+    const int len = rt == g.row_tiles - 1 ? g.last : g.full;
     it->list = seg < p.list[0].n ? 0 : 1;
     it->seg = it->list ? seg - p.list[0].n : seg;
     it->head = head;
@@ -286,15 +288,16 @@ struct Walk {
     it->pair = it->rows > kTile;
     const int fixed = it->pair ? kPairFixed : kOneFixed, each = it->pair ? kPairTile : kOneTile;
     it->tile_lo = off > 0 ? (off - fixed) / each : 0;
-    if (len - off <= left) {
-      it->tile_hi = g.tiles;
-      left -= len - off;
-    } else {
-      it->tile_hi = (off + left - fixed) / each;
-      left = 0;
+    it->tile_hi = len - off <= left ? g.tiles : (off + left - fixed) / each;
+    const int slot = 2 * unit + (first ? 0 : 1);
+    const bool whole = it->tile_lo == 0 && it->tile_hi == g.tiles;
+    it->slot = !whole ? slot : (p.joined ? kPlane : kDirect);
+    it->end = false;
+    if (!p.joined && it->tile_lo == 0 && !whole && threadIdx.x % 32 == 0) {
+      const long long start = plan.hi - left;  // off is 0
+      p.cuts[unit] = Cut{start, start + len, 1, slot, head, g.t0, it->row0, it->rows};
     }
-    it->whole = it->tile_lo == 0 && it->tile_hi == g.tiles;
-    it->first = first;
+    left = len - off <= left ? left - (len - off) : 0;
     first = false;
     off = 0;
     if (++rt == g.row_tiles) {
@@ -317,6 +320,9 @@ struct Lay {
   static constexpr int kOffF = 2 * kQ, kOffRaw = kOffF + kSlots * kF, kOffCtl = kOffRaw + kRaws * kRaw;
 };
 
+constexpr int kItems = 4;       // items told ahead
+constexpr int kItemWarps = 14;  // that are told
+
 template <int kHd, bool kRows>
 struct Control {
   Plan plan;
@@ -324,6 +330,8 @@ struct Control {
   uint64_t f_full[3], f_empty[3];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t q_full, q_empty, pv_done, xchg, scl_full[3], final_mma;
+  uint64_t item_full[kItems], item_empty[kItems];
+  Item item[kItems];
   uint32_t tmem_base, abort_flag;
   float q_scale[2][kTile];
   float row_l[2][kTile];
@@ -358,24 +366,27 @@ __device__ __forceinline__ int tile_at(int at, int tiles, bool pair, bool* is_v)
   return (at & 1) ? (at + 1) >> 1 : (at >> 1) - 1;
 }
 
-// Rows of the item in shared memory as f16, each times a power of two that puts its largest value into [2^14, 2^15).
+// Rows [first, first + count) of a stream (row0: its first in the item) in shared memory as f16, each times a power of
+// two that puts its largest value into [2^14, 2^15).
 template <int kHd>
 __device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t* q_tile, float* q_scale, int row0,
                                        int first, int count, int lane) {
   constexpr int kLanes = kHd / 8, kStep = 32 / kLanes, kFly = 8;  // lanes a row, rows a pass, passes in flight
   const int ch = lane % kLanes, sub = lane / kLanes;
-  for (int base = first; base < first + count; base += kStep * kFly) {
+  const int end = min(first + count, it.rows - row0);
+  const int item_row = it.row0 + row0, head0 = it.head * static_cast<int>(p.group.d), t0 = it.t0;
+  for (int base = first; base < end; base += kStep * kFly) {
     uint4 x[kFly];
 #pragma unroll
     for (int i = 0; i < kFly; ++i) {
       const int row = base + i * kStep + sub;
       x[i] = make_uint4(0, 0, 0, 0);
-      if (row < first + count && row0 + row < it.rows) {
-        const uint32_t r = static_cast<uint32_t>(it.row0 + row0 + row);
+      if (row < end) {
+        const uint32_t r = static_cast<uint32_t>(item_row + row);
         const uint32_t t = fast_div(r, p.group);
-        const int head = it.head * static_cast<int>(p.group.d) + static_cast<int>(r - t * p.group.d);
-        x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (it.t0 + static_cast<long long>(t)) * p.q_tok +
-                                                    head * p.q_head + ch * 8));
+        const int head = head0 + static_cast<int>(r - t * p.group.d);
+        x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (t0 + static_cast<long long>(t)) * p.q_tok + head * p.q_head +
+                                                    ch * 8));
       }
     }
 #pragma unroll
@@ -389,7 +400,7 @@ __device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t*
       for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const int e = max(static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu) - 127 - 14, -100);
       const float inv = exp2i(-e);
-      if (row < first + count && row0 + row < it.rows) {
+      if (row < end) {
         uint32_t h[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv);
@@ -398,8 +409,12 @@ __device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t*
         if (ch == 0) q_scale[row] = exp2i(e);
       }
     }
-    if (row0 + base + kStep * kFly >= it.rows) break;
   }
+}
+
+// Eight codes to eight f16 values.
+__device__ __forceinline__ uint4 to_f16(uint2 x) {
+  return make_uint4(e4m3x2_to_f16x2(x.x), e4m3x2_to_f16x2(x.x >> 16), e4m3x2_to_f16x2(x.y), e4m3x2_to_f16x2(x.y >> 16));
 }
 
 template <int kHd, bool kRows>
@@ -426,6 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
       mbar_init(&sm->p_full[i], 8);
       mbar_init(&sm->o_full[i], 1);
     }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&sm->item_full[i], 1);
+      mbar_init(&sm->item_empty[i], kItemWarps);
+    }
     mbar_init(&sm->q_full, 8);
     mbar_init(&sm->q_empty, 1);
     mbar_init(&sm->pv_done, 1);
@@ -445,31 +464,31 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
-  const bool any = unit < sm->plan.units;
+  // the item of number n, or none: every warp's own count
+  auto get_item = [&](uint32_t n) -> const Item* {
+    if (!warp_wait(&sm->item_full[n % kItems], (n / kItems) & 1, abort_flag)) return nullptr;
+    const Item* it = &sm->item[n % kItems];
+    return it->end ? nullptr : it;
+  };
+  auto drop_item = [&](uint32_t n) { warp_arrive(&sm->item_empty[n % kItems]); };
   // TMEM columns: S of either stream or tile parity, then O of either stream (one stream: P behind O)
   constexpr uint32_t kTS = 0, kTO = 256;
 
   if (warp < 8) {
-    more_registers<184>();
+    more_registers<kSoftmaxRegs>();
     // ------------------------------------------------ softmax, epilogue --
     const int wg = warp / 4, w = warp % 4;
     const int r = w * 32 + lane;  // TMEM lane: row of the stream
-    const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
-    const float k_scale = kRows ? 1.f : __ldg(p.k_scale), v_scale = kRows ? 1.f : __ldg(p.v_scale);
-    const float c0 = p.softmax_scale * kLog2e * k_scale;
-    uint32_t s_use[2] = {0, 0}, o_use[2] = {0, 0}, item_no = 0, pv_base = 0, tile_no = 0, xchgs = 0;
-    bool ok = true, was_pair = true;
-    Walk walk(p, sm->plan, any);
-    Item it;
-    bool more = walk.next(p, &it);
-    auto fetch_q = [&] {
-      const int row0 = it.pair ? wg * kTile : 0;
-      uint8_t* qt = smem + (it.pair ? wg * L::kQ : 0);
-      float* qs = sm->q_scale[it.pair ? wg : 0];
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
+    const float c0 = p.softmax_scale * kLog2e * (kRows ? 1.f : __ldg(p.k_scale));
+    uint32_t s_phase = 0, o_phase = 0;  // a bit per barrier
+    uint32_t n = 0, worked = 0, pv_base = 0, tile_no = 0, xchgs = 0;
+    bool was_pair = true;
+    auto fetch_q = [&](const Item& it) {
       if (it.pair)
-        load_q<kHd>(p, it, qt, qs, row0, w * 32, 32, lane);
+        load_q<kHd>(p, it, smem + wg * L::kQ, sm->q_scale[wg], wg * kTile, w * 32, 32, lane);
       else
-        load_q<kHd>(p, it, qt, qs, 0, (w + 4 * wg) * 16, 16, lane);
+        load_q<kHd>(p, it, smem, sm->q_scale[0], 0, (w + 4 * wg) * 16, 16, lane);
       fence_proxy_async_smem();
       warp_arrive(&sm->q_full);
     };
@@ -477,262 +496,233 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
       warp_arrive(&sm->xchg);
       return warp_wait(&sm->xchg, xchgs++ & 1, abort_flag);
     };
-    if (more && it.tile_hi > it.tile_lo) fetch_q();
-    while (more && ok) {
-      const Item cur = it;
-      const int tiles = cur.tile_hi - cur.tile_lo;
-      const int row = cur.pair ? wg * kTile + r : r;  // of the item
-      const bool live = row < cur.rows;
-      const uint32_t rr = static_cast<uint32_t>(cur.row0 + row);
-      const uint32_t tok = fast_div(rr, p.group);
-      const int head = cur.head * static_cast<int>(p.group.d) + static_cast<int>(rr - tok * p.group.d);
-      const long long token = cur.t0 + static_cast<long long>(tok);
-      if (tiles == 0) {  // no key: zeros, -inf
-        more = walk.next(p, &it);
-        if (!exchange()) break;  // every row's scale of the item before has been read
-        if (more && it.tile_hi > it.tile_lo) fetch_q();
-        if (live && (cur.pair || wg == 0)) {
-          uint4* o = reinterpret_cast<uint4*>(p.out + token * p.o_tok + head * p.o_head);
-#pragma unroll
-          for (int i = 0; i < kHd / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
-          p.lse[token * p.h_q + head] = kNegInf;
-        }
-        continue;
-      }
-      if (!warp_wait(&sm->q_full, item_no & 1, abort_flag)) break;
-      if (cur.pair != was_pair && !exchange()) break;  // the other form's columns are free
-      was_pair = cur.pair;
-      const float c = c0 * (live ? sm->q_scale[cur.pair ? wg : 0][r] : 1.f);
-      const float cc = kRows ? 1.f : c;  // units of the reference to log2
-      const bool busy = __any_sync(0xffffffffu, live);
-      float ref = kNegInf, l = 0.f;
-      auto steps = [&](auto one) {
-        constexpr bool kOne = decltype(one)::value;
-        constexpr int kCols = kOne ? kTile / 2 : kTile;        // whose exponentials this thread takes
-        constexpr int kOCols = kOne ? kHd / 2 : kHd;           // of O that it rescales
-        const uint32_t t_o = tmem + lanes + kTO + (kOne ? wg * kOCols : wg * 128);
-        for (int i = 0; i < tiles; ++i) {
-          const int buf = kOne ? (i & 1) : wg;
-          const uint32_t t_s = tmem + lanes + kTS + buf * 128;
-          const uint32_t t_p = kOne ? tmem + lanes + kTO + 128 + buf * 64 + wg * 32 : t_s;
-          const int valid = min(kTile, cur.keys - (cur.tile_lo + i) * kTile);
-          if (!warp_wait(&sm->s_full[buf], s_use[buf]++ & 1, abort_flag)) return false;
-          if (kRows && !warp_wait(&sm->scl_full[tile_no % 3], (tile_no / 3) & 1, abort_flag)) return false;
-          if (busy) {
-            tc_fence_after();
-            uint32_t s[kCols];
-            const int col0 = kOne ? wg * kCols : 0;
-#pragma unroll
-            for (int k = 0; k < kCols; k += 32) tmem_ld32(t_s + col0 + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
-            uint32_t other[kOne ? 64 : 1];
-            if constexpr (kOne) {
-#pragma unroll
-              for (int k = 0; k < 64; k += 32)
-                tmem_ld32(t_s + (64 - col0) + k, *reinterpret_cast<uint32_t(*)[32]>(other + k));
-            }
-            tmem_ld_wait();
-            float* x = reinterpret_cast<float*>(s);
-            float* y = reinterpret_cast<float*>(other);
-            if (valid < kTile) {
-#pragma unroll
-              for (int j = 0; j < kCols; ++j) x[j] = col0 + j < valid ? x[j] : kNegInf;
-              if constexpr (kOne) {
-#pragma unroll
-                for (int j = 0; j < 64; ++j) y[j] = 64 - col0 + j < valid ? y[j] : kNegInf;
-              }
-            }
-            [[maybe_unused]] const float* sk = sm->scl[kRows ? tile_no % 3 : 0][0];
-            [[maybe_unused]] const float* lv = sm->scl[kRows ? tile_no % 3 : 0][1];
-            [[maybe_unused]] const float* iv = sm->scl[kRows ? tile_no % 3 : 0][2];
-            if constexpr (kRows) {  // scores in log2 with the K scale of their key and its V scale
-#pragma unroll
-              for (int j = 0; j < kCols; j += 2) {
-                const float2 a = *reinterpret_cast<const float2*>(sk + col0 + j);
-                const float2 b = *reinterpret_cast<const float2*>(lv + col0 + j);
-                const float2 u = fma_f32x2(mul_f32x2(make_float2(x[j], x[j + 1]), make_float2(c, c)), a, b);
-                x[j] = u.x, x[j + 1] = u.y;
-              }
-              if constexpr (kOne) {
-#pragma unroll
-                for (int j = 0; j < 64; j += 2) {
-                  const float2 a = *reinterpret_cast<const float2*>(sk + 64 - col0 + j);
-                  const float2 b = *reinterpret_cast<const float2*>(lv + 64 - col0 + j);
-                  const float2 u = fma_f32x2(mul_f32x2(make_float2(y[j], y[j + 1]), make_float2(c, c)), a, b);
-                  y[j] = u.x, y[j + 1] = u.y;
-                }
-              }
-            }
-            float mx[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = x[k];
-#pragma unroll
-            for (int j = 4; j + 8 <= kCols; j += 8) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mx[k] = fmax3(mx[k], x[j + 2 * k], x[j + 2 * k + 1]);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[kCols - 4 + k]);
-            if constexpr (kOne) {
-#pragma unroll
-              for (int j = 0; j < 64; j += 8) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mx[k] = fmax3(mx[k], y[j + 2 * k], y[j + 2 * k + 1]);
-              }
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const bool raise = (top - ref) * cc > kTau;
-            if (i == 0) {
-              ref = top == kNegInf ? 0.f : top;
-            } else if (__any_sync(0xffffffffu, raise && live)) {
-              if (kOne && !warp_wait(&sm->pv_done, (pv_base + i - 1) & 1, abort_flag)) return false;
+    const Item* it = get_item(0);
+    if (it != nullptr && it->tile_hi > it->tile_lo) fetch_q(*it);
+    while (it != nullptr) {
+      const int tiles = it->tile_hi - it->tile_lo;
+      const bool pair = it->pair;
+      const int row = pair ? wg * kTile + r : r;  // of the item
+      const bool live = row < it->rows;
+      float ref = kNegInf, l = 0.f, cc = 1.f;
+      if (tiles > 0) {
+        if (!warp_wait(&sm->q_full, worked & 1, abort_flag)) break;
+        if (pair != was_pair && !exchange()) break;  // the other form's columns are free
+        was_pair = pair;
+        const float c = c0 * (live ? sm->q_scale[pair ? wg : 0][r] : 1.f);
+        if (!kRows) cc = c;  // units of the reference to log2
+        const bool busy = __any_sync(0xffffffffu, live);
+        int keys = it->keys - it->tile_lo * kTile;  // left
+        auto steps = [&](auto one) {
+          constexpr bool kOne = decltype(one)::value;
+          constexpr int kCols = kOne ? kTile / 2 : kTile;  // whose exponentials this thread takes
+          constexpr int kOCols = kOne ? kHd / 2 : kHd;     // of O that it rescales
+          const int col0 = kOne ? wg * kCols : 0;
+          const uint32_t t_o = lanes + kTO + (kOne ? wg * kOCols : wg * 128);
+          for (int i = 0; i < tiles; ++i, keys -= kTile) {
+            const int buf = kOne ? (i & 1) : wg;
+            if (!warp_wait(&sm->s_full[buf], (s_phase >> buf) & 1, abort_flag)) return false;
+            s_phase ^= 1u << buf;
+            if (kRows && !warp_wait(&sm->scl_full[tile_no % 3], (tile_no / 3) & 1, abort_flag)) return false;
+            if (busy) {
+              const uint32_t t_s = lanes + kTS + buf * 128;
+              const uint32_t t_p = kOne ? lanes + kTO + 128 + buf * 64 + wg * 32 : t_s;
               tc_fence_after();
-              const float alpha = raise ? ex2_approx((ref - top) * cc) : 1.f;
-              if (raise) ref = top;
-              l *= alpha;
+              float x[kCols];
+              float top = kNegInf;
+              [[maybe_unused]] const float* sk = sm->scl[kRows ? tile_no % 3 : 0][0];
+              [[maybe_unused]] const float* lv = sm->scl[kRows ? tile_no % 3 : 0][1];
+              [[maybe_unused]] const float* iv = sm->scl[kRows ? tile_no % 3 : 0][2];
+              // 32 scores of column `at` on: masked past the end; with row scales in log2, times their key's K scale
+              // and its V scale
+              auto scores = [&](float* y, int at) {
+                if (keys < kTile) {
 #pragma unroll
-              for (int k = 0; k < kOCols; k += 32) {
-                uint32_t o[32];
-                tmem_ld32(t_o + k, o);
+                  for (int j = 0; j < 32; ++j) y[j] = at + j < keys ? y[j] : kNegInf;
+                }
+                if constexpr (kRows) {
+#pragma unroll
+                  for (int j = 0; j < 32; j += 2) {
+                    const float2 u = fma_f32x2(mul_f32x2(make_float2(y[j], y[j + 1]), make_float2(c, c)),
+                                               *reinterpret_cast<const float2*>(sk + at + j),
+                                               *reinterpret_cast<const float2*>(lv + at + j));
+                    y[j] = u.x, y[j + 1] = u.y;
+                  }
+                }
+                float m0 = y[0], m1 = y[1];
+#pragma unroll
+                for (int j = 2; j < 30; j += 4) m0 = fmax3(m0, y[j], y[j + 1]), m1 = fmax3(m1, y[j + 2], y[j + 3]);
+                top = fmax3(top, m0, m1);
+                top = fmax3(top, y[30], y[31]);
+              };
+              if constexpr (kOne) {  // the other half's scores for the maximum alone
+                float y[64];
+#pragma unroll
+                for (int k = 0; k < 64; k += 32) tmem_ld32(t_s + (64 - col0) + k, *reinterpret_cast<uint32_t(*)[32]>(y + k));
+#pragma unroll
+                for (int k = 0; k < kCols; k += 32) tmem_ld32(t_s + col0 + k, *reinterpret_cast<uint32_t(*)[32]>(x + k));
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                tmem_st32(t_o + k, o);
-              }
-            }
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                for (int k = 0; k < 64; k += 32) scores(y + k, 64 - col0 + k);
+              } else {
 #pragma unroll
-            for (int k = 0; k < kCols; k += 32) {
-              uint32_t h[16];
-#pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                float2 d = add_f32x2(make_float2(x[k + j], x[k + j + 1]), make_float2(-ref, -ref));
-                if constexpr (kRows)
-                  d = add_f32x2(d, make_float2(kLift, kLift));
-                else
-                  d = fma_f32x2(d, make_float2(cc, cc), make_float2(kLift, kLift));
-                d.x = ex2_approx(d.x);
-                d.y = ex2_approx(d.y);
-                if constexpr (kRows)
-                  sum[(j >> 1) & 1] = fma_f32x2(d, *reinterpret_cast<const float2*>(iv + col0 + k + j), sum[(j >> 1) & 1]);
-                else
-                  sum[(j >> 1) & 1] = add_f32x2(sum[(j >> 1) & 1], d);
-                h[j / 2] = pack_f16x2(d.x, d.y);
+                for (int k = 0; k < kCols; k += 32) tmem_ld32(t_s + k, *reinterpret_cast<uint32_t(*)[32]>(x + k));
+                tmem_ld_wait();
               }
-              tmem_st16(t_p + k / 2, h);
+#pragma unroll
+              for (int k = 0; k < kCols; k += 32) scores(x + k, col0 + k);
+              const bool raise = (top - ref) * cc > kTau;
+              if (i == 0) {
+                ref = top == kNegInf ? 0.f : top;
+              } else if (__any_sync(0xffffffffu, raise && live)) {
+                if (kOne && !warp_wait(&sm->pv_done, (pv_base + i - 1) & 1, abort_flag)) return false;
+                tc_fence_after();
+                const float alpha = raise ? ex2_approx((ref - top) * cc) : 1.f;
+                if (raise) ref = top;
+                l *= alpha;
+#pragma unroll
+                for (int k = 0; k < kOCols; k += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(t_o + k, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                  tmem_st16(t_o + k, o);
+                }
+              }
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+              for (int k = 0; k < kCols; k += 32) {
+                uint32_t h[16];
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                  float2 d = add_f32x2(make_float2(x[k + j], x[k + j + 1]), make_float2(-ref, -ref));
+                  if constexpr (kRows)
+                    d = add_f32x2(d, make_float2(kLift, kLift));
+                  else
+                    d = fma_f32x2(d, make_float2(cc, cc), make_float2(kLift, kLift));
+                  d.x = ex2_approx(d.x);
+                  d.y = ex2_approx(d.y);
+                  if constexpr (kRows)
+                    sum[(j >> 1) & 1] =
+                        fma_f32x2(d, *reinterpret_cast<const float2*>(iv + col0 + k + j), sum[(j >> 1) & 1]);
+                  else
+                    sum[(j >> 1) & 1] = add_f32x2(sum[(j >> 1) & 1], d);
+                  h[j / 2] = pack_f16x2(d.x, d.y);
+                }
+                tmem_st16(t_p + k / 2, h);
+              }
+              l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+              tmem_st_wait();
+              tc_fence_before();
             }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            tmem_st_wait();
-            tc_fence_before();
+            ++tile_no;
+            warp_arrive(&sm->p_full[buf]);
+            if (!kOne && lane == 0) mbar_arrive(&sm->p_full[buf]);  // the barrier counts eight warps
           }
-          ++tile_no;
-          warp_arrive(&sm->p_full[buf]);
-          if (!kOne && lane == 0) mbar_arrive(&sm->p_full[buf]);  // the barrier counts eight warps
-        }
-        return true;
-      };
-      ok = cur.pair ? steps(std::false_type{}) : steps(std::true_type{});
-      if (!ok) break;
-      if (cur.pair)
-        s_use[1 - wg] += tiles;
-      else
-        pv_base += tiles;
+          return true;
+        };
+        if (!(pair ? steps(std::false_type{}) : steps(std::true_type{}))) break;
+        if (pair)
+          s_phase ^= (tiles & 1) << (1 - wg);
+        else
+          pv_base += tiles;
+      }
       // Q of the next item, while the last product runs.  Where another warp reads the rows' scales, all have to be
       // done with those of this item.
-      more = walk.next(p, &it);
-      if (!cur.pair) sm->row_l[wg][r] = l;
-      if ((!cur.pair || (more && !it.pair)) && !exchange()) break;
-      if (!cur.pair) l = sm->row_l[0][r] + sm->row_l[1][r];
-      if (!warp_wait(&sm->q_empty, item_no & 1, abort_flag)) break;
-      ++item_no;
-      if (more && it.tile_hi > it.tile_lo) fetch_q();
-      const int os = cur.pair ? wg : 0;
-      if (!warp_wait(&sm->o_full[os], o_use[os]++ & 1, abort_flag)) break;
-      if (cur.pair) ++o_use[1 - wg];
-      tc_fence_after();
-      if (busy) {
-        const int dims = cur.pair ? kHd : kHd / 2, dim0 = cur.pair ? 0 : wg * (kHd / 2);
-        const uint32_t t_o = tmem + lanes + kTO + os * 128 + dim0;
-        const float m = ref * cc;
-        const bool direct = cur.whole && !p.joined;
-        const float f = direct ? v_scale / l : 1.f;
-        uint16_t* orow = p.out + token * p.o_tok + head * p.o_head + dim0;
-        float* frow = nullptr;
-        if (!direct && live) {
-          float2* ml;
-          if (cur.whole) {
-            const long long at = token * p.h_q + head;
-            frow = p.plane_o[cur.list] + at * kHd + dim0;
-            ml = p.plane_ml[cur.list] + at;
-          } else {
-            const long long at = static_cast<long long>(2 * unit + (cur.first ? 0 : 1)) * p.slot_rows + row;
-            frow = p.slot_o + at * kHd + dim0;
-            ml = p.slot_ml + at;
-          }
-          if (cur.pair || wg == 0) *ml = make_float2(m, l);
-        } else if (live && (cur.pair || wg == 0)) {
-          p.lse[token * p.h_q + head] = (m + lg2_approx(l) - kLift) * kLn2;
-        }
-        for (int k = 0; k < dims; k += 32) {
-          uint32_t o[32];
-          __syncwarp();
-          tmem_ld32(t_o + k, o);
-          tmem_ld_wait();
-          if (direct && live) {
+      const Item* next = get_item(n + 1);
+      if (!pair) sm->row_l[wg][r] = l;
+      if ((!pair || tiles == 0 || (next != nullptr && !next->pair)) && !exchange()) break;
+      if (!pair) l = sm->row_l[0][r] + sm->row_l[1][r];
+      if (tiles > 0) {
+        if (!warp_wait(&sm->q_empty, worked & 1, abort_flag)) break;
+        ++worked;
+      }
+      if (next != nullptr && next->tile_hi > next->tile_lo) fetch_q(*next);
+      const int os = pair ? wg : 0;
+      if (tiles > 0) {
+        if (!warp_wait(&sm->o_full[os], (o_phase >> os) & 1, abort_flag)) break;
+        o_phase ^= pair ? 3u : 1u;
+        tc_fence_after();
+      }
+      if (__any_sync(0xffffffffu, live)) {
+        const uint32_t rr = static_cast<uint32_t>(it->row0 + row);
+        const uint32_t tok = fast_div(rr, p.group);
+        const int head = it->head * static_cast<int>(p.group.d) + static_cast<int>(rr - tok * p.group.d);
+        const long long token = it->t0 + static_cast<long long>(tok), at = token * p.h_q + head;
+        const int dims = pair ? kHd : kHd / 2, dim0 = pair ? 0 : wg * (kHd / 2);
+        const uint32_t t_o = lanes + kTO + os * 128 + dim0;
+        const bool leads = live && (pair || wg == 0);
+        if (it->slot == kDirect) {
+          // a sequence without keys: zeros, -inf
+          const float f = tiles > 0 ? (kRows ? 1.f : __ldg(p.v_scale)) / l : 0.f;
+          uint16_t* to = p.out + token * p.o_tok + head * p.o_head + dim0;
+          if (leads) p.lse[at] = tiles > 0 ? (ref * cc + lg2_approx(l) - kLift) * kLn2 : kNegInf;
+          for (int k = 0; k < dims; k += 32) {
+            uint32_t o[32] = {};
+            __syncwarp();
+            if (tiles > 0) {
+              tmem_ld32(t_o + k, o);
+              tmem_ld_wait();
+            }
+            if (!live) continue;
 #pragma unroll
             for (int j = 0; j < 32; j += 8) {
               uint32_t h[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 h[e] = pack_bf16x2(__uint_as_float(o[j + 2 * e]) * f, __uint_as_float(o[j + 2 * e + 1]) * f);
-              *reinterpret_cast<uint4*>(orow + k + j) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(to + k + j) = make_uint4(h[0], h[1], h[2], h[3]);
             }
-          } else if (live) {
+          }
+        } else {
+          const bool plane = it->slot == kPlane;
+          const long long place = plane ? at : static_cast<long long>(it->slot) * p.slot_rows + row;
+          float* to = (plane ? p.plane_o[it->list] : p.slot_o) + place * kHd + dim0;
+          if (leads) (plane ? p.plane_ml[it->list] : p.slot_ml)[place] = make_float2(ref * cc, l);
+          for (int k = 0; k < dims; k += 32) {
+            uint32_t o[32];
+            __syncwarp();
+            tmem_ld32(t_o + k, o);
+            tmem_ld_wait();
+            if (!live) continue;
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<uint4*>(frow + k + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+              *reinterpret_cast<uint4*>(to + k + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           }
         }
         __syncwarp();
         tc_fence_before();
       }
-      if (!p.joined && threadIdx.x == 0 && !more && cur.tile_lo == 0 && !cur.whole) {
-        Cut* cut = p.cuts + unit;
-        cut->head = cur.head;
-        cut->t0 = cur.t0;
-        cut->row0 = cur.row0;
-        cut->rows = cur.rows;
-        const int all = (cur.keys + kTile - 1) / kTile;
-        const int len = cur.pair ? kPairFixed + all * kPairTile : kOneFixed + all * kOneTile;
-        cut->start = sm->plan.hi - (cur.pair ? kPairFixed + cur.tile_hi * kPairTile : kOneFixed + cur.tile_hi * kOneTile);
-        cut->end = cut->start + len;
-        cut->valid = 2 + (cur.first ? 0 : 1);
-      }
+      drop_item(n++);
+      it = next;
     }
   } else if (warp < 12) {
-    fewer_registers<72>();
+    fewer_registers<kConvertRegs>();
     // ------------------------------------------------ codes to f16 tiles --
+    // A thread takes eight codes of every eighth (hd 64: sixteenth) row: 16 bytes of f16 at a place of the swizzled row
+    // that is the same each time, and the quarters of a warp meet every bank once.
     const int tid = threadIdx.x - 256;
-    uint32_t f = 0, raw = 0, tile_no = 0;
+    constexpr int kLanes = kHd / 8, kRowsAStep = 128 / kLanes, kSteps = kTile / kRowsAStep;
+    const int key0 = tid / kLanes, ch = tid % kLanes;
+    const uint32_t to = (ch / 8) * (kTile * 128) + key0 * 128 + (((ch % 8) ^ (key0 % 8)) << 4);
+    uint32_t f = 0, rs = 0, raw_phase = 0, fs = 0, f_phase = 1, tile_no = 0;
     bool ok = true;
-    Walk walk(p, sm->plan, any);
-    Item it;
-    while (ok && walk.next(p, &it)) {
-      const int tiles = it.tile_hi - it.tile_lo;
-      for (int at = 0; at < 2 * tiles; ++at, ++f, ++raw) {
+    for (uint32_t n = 0; ok; ++n) {
+      const Item* it = get_item(n);
+      if (it == nullptr) break;
+      const int tiles = it->tile_hi - it->tile_lo, left = it->keys - it->tile_lo * kTile;
+      const bool pair = it->pair;
+      drop_item(n);
+      for (int at = 0; at < 2 * tiles; ++at, ++f) {
         bool is_v;
-        const int tile = it.tile_lo + tile_at(at, tiles, it.pair, &is_v);
-        const int valid = min(kTile, it.keys - tile * kTile);
-        const int rs = raw % L::kRaws, fs = f % L::kSlots;
-        if (!warp_wait(&sm->raw_full[rs], (raw / L::kRaws) & 1, abort_flag)) {
+        const int valid = left - tile_at(at, tiles, pair, &is_v) * kTile;
+        if (!warp_wait(&sm->raw_full[rs], raw_phase, abort_flag) ||
+            (f >= L::kSlots && !warp_wait(&sm->f_empty[fs], f_phase, abort_flag))) {
           ok = false;
           break;
         }
-        if (f >= L::kSlots && !warp_wait(&sm->f_empty[fs], (f / L::kSlots - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint8_t* src = smem + L::kOffRaw + rs * L::kRaw;
-        uint8_t* dst = smem + L::kOffF + fs * L::kF;
+        const uint8_t* src = smem + L::kOffRaw + rs * L::kRaw + tid * 8;
+        uint8_t* dst = smem + L::kOffF + fs * L::kF + to;
         if constexpr (kRows) {
           if (!is_v) {  // past the end: one, so that a stale scale cannot turn a zero weight into a NaN
             const float a = tid < valid ? sm->raw_scl[rs][0][tid] : 1.f, b = tid < valid ? sm->raw_scl[rs][1][tid] : 1.f;
@@ -744,47 +734,42 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
             ++tile_no;
           }
         }
-        constexpr int kLanes = kHd / 16, kIters = kTile * kLanes / 128;  // 16-byte pieces a row, a thread's pieces
-        uint4 x[kIters];
 #pragma unroll
-        for (int i = 0; i < kIters; ++i) {
-          const int piece = i * 128 + tid;
-          x[i] = *reinterpret_cast<const uint4*>(src + piece * 16);
-          if (piece / kLanes >= valid) x[i] = make_uint4(0, 0, 0, 0);
-        }
+        for (int i = 0; i < kSteps; i += 8) {
+          uint2 x[8];
 #pragma unroll
-        for (int i = 0; i < kIters; ++i) {
-          const int piece = i * 128 + tid, key = piece / kLanes, ch = piece % kLanes;
-          const uint4 a = make_uint4(e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16), e4m3x2_to_f16x2(x[i].y),
-                                     e4m3x2_to_f16x2(x[i].y >> 16));
-          const uint4 b = make_uint4(e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16), e4m3x2_to_f16x2(x[i].w),
-                                     e4m3x2_to_f16x2(x[i].w >> 16));
-          // two 16-byte pieces of the 128-byte row; the second block of dims stores them the other way round, so that
-          // a quarter warp meets every bank once
-          const bool swap = ch >= 4;
-          uint8_t* to = dst + (ch / 4) * (kTile * 128) + key * 128;
-          const int c0 = (ch % 4) * 2, x8 = key % 8;
-          *reinterpret_cast<uint4*>(to + (((c0 + (swap ? 1 : 0)) ^ x8) << 4)) = swap ? b : a;
-          *reinterpret_cast<uint4*>(to + (((c0 + (swap ? 0 : 1)) ^ x8) << 4)) = swap ? a : b;
+          for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const uint2*>(src + (i + j) * 1024);
+          if (valid < kTile) {  // rows past the end: zeros
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (key0 + (i + j) * kRowsAStep >= valid) x[j] = make_uint2(0, 0);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(dst + (i + j) * kRowsAStep * 128) = to_f16(x[j]);
         }
         fence_proxy_async_smem();
         warp_arrive(&sm->f_full[fs]);
         warp_arrive(&sm->raw_empty[rs]);
+        if (++rs == L::kRaws) rs = 0, raw_phase ^= 1;
+        if (++fs == L::kSlots) fs = 0, f_phase ^= 1;
       }
     }
   } else {
-    fewer_registers<72>();
+    fewer_registers<kIssueRegs>();
     if (warp == 12) {
       // ------------------------------------------------ matrix products --
       constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, kTile, 128);  // f16: Q (K-major) x K (K-major)
       constexpr uint32_t idesc_pv = make_idesc(0, 0, 0, 1, kHd, 128);    // f16: P (TMEM) x V (MN-major)
       const bool leader = elect_one();
       const uint32_t qb = smem_u32(smem), fb = qb + L::kOffF;
-      uint32_t f = 0, p_use[2] = {0, 0}, item_no = 0;
+      uint32_t f = 0, p_phase = 0, worked = 0;
       bool ok = true;
-      Walk walk(p, sm->plan, any);
-      Item it;
       auto wait_f = [&](uint32_t at) { return warp_wait(&sm->f_full[at % L::kSlots], (at / L::kSlots) & 1, abort_flag); };
+      auto wait_p = [&](int buf) {
+        const bool done = warp_wait(&sm->p_full[buf], (p_phase >> buf) & 1, abort_flag);
+        p_phase ^= 1u << buf;
+        return done;
+      };
       auto issue_qk = [&](int q, int buf, uint32_t at) {  // S[buf] = Q[q] K^T
         tc_fence_after();
         const uint32_t a = qb + q * L::kQ, b = fb + (at % L::kSlots) * L::kF;
@@ -805,21 +790,25 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
                         make_sdesc(b + kk * 2048, kTile * 128, 1024, SWIZZLE_128B), idesc_pv, (fresh && kk == 0) ? 0u : 1u);
       };
       auto release = [&](uint32_t at) { tc_commit_if(leader, &sm->f_empty[at % L::kSlots]); };
-      while (ok && walk.next(p, &it)) {
-        const int tiles = it.tile_hi - it.tile_lo;
+      for (uint32_t n = 0; ok; ++n) {
+        const Item* it = get_item(n);
+        if (it == nullptr) break;
+        const int tiles = it->tile_hi - it->tile_lo;
+        const bool pair = it->pair;
+        drop_item(n);
         if (tiles == 0) continue;
         ok = false;
-        if (!warp_wait(&sm->q_full, item_no++ & 1, abort_flag) || !wait_f(f)) break;
-        if (it.pair) {
+        if (!warp_wait(&sm->q_full, worked++ & 1, abort_flag) || !wait_f(f)) break;
+        int i = 0;
+        if (pair) {
           issue_qk(0, 0, f);
           issue_qk(1, 1, f);
           release(f);
           if (tiles == 1) tc_commit_if(leader, &sm->q_empty);
-          int i = 0;
           for (; i < tiles; ++i) {
             const uint32_t fv = f + 2 * i + 1, fk = fv + 1;
             const bool last = i + 1 == tiles;
-            if (!wait_f(fv) || !warp_wait(&sm->p_full[0], p_use[0]++ & 1, abort_flag)) break;
+            if (!wait_f(fv) || !wait_p(0)) break;
             issue_pv(kTO, kTS, fv, i == 0);
             if (last) {
               tc_commit_if(leader, &sm->o_full[0]);
@@ -827,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
               if (!wait_f(fk)) break;
               issue_qk(0, 0, fk);
             }
-            if (!warp_wait(&sm->p_full[1], p_use[1]++ & 1, abort_flag)) break;
+            if (!wait_p(1)) break;
             issue_pv(kTO + 128, kTS + 128, fv, i == 0);
             release(fv);
             if (last) {
@@ -838,7 +827,6 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
               if (i + 2 == tiles) tc_commit_if(leader, &sm->q_empty);
             }
           }
-          if (i < tiles) break;
         } else {
           // places: K0 at f, K1 at f + 1, V0, K2, V1, K3 ..
           issue_qk(0, 0, f);
@@ -849,11 +837,10 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
             release(f + 1);
           }
           if (tiles <= 2) tc_commit_if(leader, &sm->q_empty);
-          int i = 0;
           for (; i < tiles; ++i) {
             const int buf = i & 1;
             const uint32_t fv = f + (i + 1 < tiles ? 2 * i + 2 : 2 * i + 1);
-            if (!wait_f(fv) || !warp_wait(&sm->p_full[buf], p_use[buf]++ & 1, abort_flag)) break;
+            if (!wait_f(fv) || !wait_p(buf)) break;
             issue_pv(kTO, kTO + 128 + buf * 64, fv, i == 0);
             tc_commit_if(leader, &sm->pv_done);
             release(fv);
@@ -865,8 +852,8 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
               if (i + 3 == tiles) tc_commit_if(leader, &sm->q_empty);
             }
           }
-          if (i < tiles) break;
         }
+        if (i < tiles) break;
         f += 2 * tiles;
         ok = true;
       }
@@ -877,27 +864,29 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
       // --------------------------------------------- copies of raw tiles --
       uint32_t raw = 0;
       bool ok = true;
-      Walk walk(p, sm->plan, any);
-      Item it;
       const int chunk_shift = min(p.page_shift, 7);  // keys a copy
-      const int chunks = kTile >> chunk_shift;
-      while (ok && walk.next(p, &it)) {
-        const int tiles = it.tile_hi - it.tile_lo;
-        const List& l = p.list[it.list];
-        const int32_t* table = l.table + static_cast<long long>(it.seg) * l.max_blocks;
+      const int chunks = kTile >> chunk_shift, in_page = (1 << p.page_shift) - 1;
+      const int first = lane << chunk_shift;
+      for (uint32_t n = 0; ok; ++n) {
+        const Item* it = get_item(n);
+        if (it == nullptr) break;
+        const int tile_lo = it->tile_lo, tile_hi = it->tile_hi, keys = it->keys, head = it->head;
+        const int tiles = tile_hi - tile_lo;
+        const bool pair = it->pair;
+        const int32_t* table = p.list[it->list].table + static_cast<long long>(it->seg) * p.list[it->list].max_blocks;
+        drop_item(n);
         // lane c: the page of chunk c of a tile
         auto fetch = [&](int tile) {
-          const int key = tile * kTile + (lane << chunk_shift);
-          return tile < it.tile_hi && lane < chunks && key < it.keys ? __ldg(table + (key >> p.page_shift)) : 0;
+          const int key = tile * kTile + first;
+          return tile < tile_hi && lane < chunks && key < keys ? __ldg(table + (key >> p.page_shift)) : 0;
         };
-        int page[2] = {fetch(it.tile_lo), fetch(it.tile_lo + 1)};
-        int next = fetch(it.tile_lo + 2);
+        int even = fetch(tile_lo), odd = fetch(tile_lo + 1), next = fetch(tile_lo + 2);  // by the tile's number in the item
         for (int at = 0; at < 2 * tiles; ++at, ++raw) {
           bool is_v;
-          const int t = tile_at(at, tiles, it.pair, &is_v), tile = it.tile_lo + t;
+          const int t = tile_at(at, tiles, pair, &is_v), tile = tile_lo + t;
           const int rs = raw % L::kRaws;
-          const int valid = min(kTile, it.keys - tile * kTile);
-          int block = (t & 1) ? page[1] : page[0];
+          const int valid = min(kTile, keys - tile * kTile);
+          int block = (t & 1) ? odd : even;
           if (block < 0 || block >= p.num_blocks) {
             atomicOr(&g_status_ragged, FP8MLA_DEV_BAD_PAGE);
             block = 0;
@@ -908,9 +897,8 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
           }
           if (lane == 0) mbar_arrive_expect_tx(&sm->raw_full[rs], static_cast<uint32_t>(valid) * kHd);
           __syncwarp();
-          const int first = lane << chunk_shift;
-          const long long in_page = (static_cast<long long>(tile) * kTile + first) & ((1 << p.page_shift) - 1);
-          const long long line = ((static_cast<long long>(block) * p.h_kv + it.head) << p.page_shift) + in_page;
+          const long long line = ((static_cast<long long>(block) * p.h_kv + head) << p.page_shift) +
+                                 ((tile * kTile + first) & in_page);
           if (lane < chunks && first < valid)
             bulk_load(smem + L::kOffRaw + rs * L::kRaw + first * kHd, (is_v ? p.v : p.k) + line * kHd,
                       static_cast<uint32_t>(min(1 << chunk_shift, valid - first)) * kHd, &sm->raw_full[rs]);
@@ -918,8 +906,8 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
             if (!is_v) {  // scales of four keys a lane
               const int key = lane * 4;
               const int from = __shfl_sync(0xffffffffu, block, key >> chunk_shift);
-              const long long at4 = ((static_cast<long long>(from) * p.h_kv + it.head) << p.page_shift) +
-                                    ((static_cast<long long>(tile) * kTile + key) & ((1 << p.page_shift) - 1));
+              const long long at4 = ((static_cast<long long>(from) * p.h_kv + head) << p.page_shift) +
+                                    ((tile * kTile + key) & in_page);
               if (key < valid) {
                 cp_async16(smem_u32(&sm->raw_scl[rs][0][key]), p.k_scale + at4, 16u);
                 cp_async16(smem_u32(&sm->raw_scl[rs][1][key]), p.v_scale + at4, 16u);
@@ -929,9 +917,9 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
           }
           if (is_v) {  // the tile is done: its place takes the one after the next
             if (t & 1)
-              page[1] = next;
+              odd = next;
             else
-              page[0] = next;
+              even = next;
             next = fetch(tile + 3);
           }
         }
@@ -939,14 +927,27 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
       if constexpr (kRows) cp_async_wait_all();  // this lane's copies have landed before the CTA can exit
       for (uint32_t j = raw > L::kRaws ? raw - L::kRaws : 0; j < raw; ++j)
         warp_wait(&sm->raw_full[j % L::kRaws], (j / L::kRaws) & 1, nullptr);
+    } else if (warp == 14) {
+      // ------------------------------------------------- the share's items --
+      if (unit >= sm->plan.units) sm->plan.hi = sm->plan.lo;
+      __syncwarp();
+      Walk walk(p, sm->plan);
+      Item it;
+      bool more = true;
+      for (uint32_t n = 0; more; ++n) {
+        it.end = !walk.next(p, sm->plan, unit, &it);
+        more = !it.end;
+        if (n >= kItems && !warp_wait(&sm->item_empty[n % kItems], (n / kItems - 1) & 1, abort_flag)) break;
+        if (lane == 0) sm->item[n % kItems] = it;
+        warp_arrive(&sm->item_full[n % kItems]);
+      }
     } else if (p.fill_out || p.fill_lse) {
       // ------------------------------------------- rows of no sequence --
       const List& l = p.list[0];
       const int lo = l.starts ? min(max(__ldg(l.starts), 0), p.tokens) : 0;
       const int hi = l.starts ? min(max(__ldg(l.starts + l.n), lo), p.tokens) : min(l.n, p.tokens);
-      const int none = lo + p.tokens - hi;
-      const long long heads = static_cast<long long>(none) * p.h_q;
-      for (long long i = unit * 2 + (warp - 14); i < heads; i += 2 * gridDim.x) {
+      const long long heads = static_cast<long long>(lo + p.tokens - hi) * p.h_q;
+      for (long long i = unit; i < heads; i += gridDim.x) {
         int t = static_cast<int>(i / p.h_q);
         const int h = static_cast<int>(i % p.h_q);
         if (t >= lo) t += hi - lo;
@@ -1022,7 +1023,7 @@ __global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant_
   const float v_scale = scale_rows ? 1.f : *p.v_scale;
   for (int row = row0 + threadIdx.x / 32; row < min(cut.rows, row0 + kMergeRows); row += 4) {
     RowSum<kHd> sum;
-    sum.pieces(p, unit, last, cut.valid - 2, row, lane);
+    sum.pieces(p, unit, last, cut.slot & 1, row, lane);
     const uint32_t r = static_cast<uint32_t>(cut.row0 + row), t = fast_div(r, p.group);
     const int head = cut.head * static_cast<int>(p.group.d) + static_cast<int>(r - t * p.group.d);
     const long long token = cut.t0 + static_cast<long long>(t);
@@ -1203,8 +1204,8 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   const cudaError_t e = configure_once(configured, [&] {
     cudaFuncAttributes f;
     cudaError_t x = cudaFuncGetAttributes(&f, ragged_kernel<kHd, kRows>);
-    // the warpgroups' shares, 2 x 184 + 2 x 72 registers a thread, come out of what the launch takes
-    if (x == cudaSuccess && f.numRegs * kThreads < 2 * 128 * (184 + 72)) x = cudaErrorInvalidConfiguration;
+    // the warpgroups' shares come out of what the launch takes
+    if (x == cudaSuccess && f.numRegs * kThreads < 128 * (2 * kSoftmaxRegs + kConvertRegs + kIssueRegs)) x = cudaErrorInvalidConfiguration;
     return x != cudaSuccess ? x
                             : cudaFuncSetAttribute(ragged_kernel<kHd, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem));
