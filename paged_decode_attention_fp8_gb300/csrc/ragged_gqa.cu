@@ -14,6 +14,8 @@
 //   up to 256 rows: two streams of 128 rows, each with its own S and O; the tensor core works for one while the other's
 //     softmax runs.
 //   up to 128 rows: one stream, S in two buffers by tile parity, and both softmax warpgroups share a tile's columns.
+//   up to 32 rows: the same with the rows in all four quarters of the lanes, each with P for its own 32 keys of a tile
+//     (zero for the others) and a reference of its own: eight warps share the softmax, the quarters are summed at the end.
 // Warps: 0-3 and 4-7 the two softmax warpgroups, 8-11 turn raw tiles into f16, 12 issues the products, 13 copies raw
 // tiles (one bulk copy per page and operand), 14 tells the others the share's items, 15 fills rows of no sequence.
 #include <cuda.h>
@@ -240,8 +242,11 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan* plan, int unit)
 struct Item {
   int list, seg, head, t0, row0, rows, keys, tile_lo, tile_hi;
   int slot;  // where its sums go: kDirect the outputs, kPlane the list's plane, else the workspace's slot
-  bool pair, end;
+  int form;
+  bool end;
 };
+constexpr int kFew = 32;                         // rows that lie in all quarters
+enum { kFormPair = 0, kFormOne = 1, kFormFew = 2 };
 constexpr int kDirect = -1, kPlane = -2;
 
 // The items of a share, one after the other.
@@ -285,8 +290,9 @@ struct Walk {
     it->row0 = rt * kItemRows;
     it->rows = min(kItemRows, g.rows - it->row0);
     it->keys = g.keys;
-    it->pair = it->rows > kTile;
-    const int fixed = it->pair ? kPairFixed : kOneFixed, each = it->pair ? kPairTile : kOneTile;
+    it->form = it->rows > kTile ? kFormPair : (it->rows > kFew ? kFormOne : kFormFew);
+    const bool pair = it->form == kFormPair;
+    const int fixed = pair ? kPairFixed : kOneFixed, each = pair ? kPairTile : kOneTile;
     it->tile_lo = off > 0 ? (off - fixed) / each : 0;
     it->tile_hi = len - off <= left ? g.tiles : (off + left - fixed) / each;
     const int slot = 2 * unit + (first ? 0 : 1);
@@ -317,7 +323,10 @@ struct Lay {
   static constexpr int kF = kHalves * kTile * 128;        // a tile of K or V in f16
   static constexpr int kRaw = kTile * kHd;                // the same as codes
   static constexpr int kSlots = 3, kRaws = kRows && kHd == 128 ? 3 : (kHd == 64 ? 8 : 4);
-  static constexpr int kOffF = 2 * kQ, kOffRaw = kOffF + kSlots * kF, kOffCtl = kOffRaw + kRaws * kRaw;
+  static constexpr int kOffF = 2 * kQ, kOffRaw = kOffF + kSlots * kF, kOffSum = kHd == 128 ? kQ : kOffRaw + kRaws * kRaw;
+  static constexpr int kSum = 2 * 4 * kFew * 32 * 4;  // sums of the quarters, 32 dims of either half; the second Q's place
+  static constexpr int kOffCtl = kOffRaw + kRaws * kRaw + (kHd == 128 ? 0 : kSum);
+  static_assert(kHd != 128 || kSum <= kQ, "");
 };
 
 constexpr int kItems = 4;       // items told ahead
@@ -333,10 +342,11 @@ struct Control {
   uint64_t item_full[kItems], item_empty[kItems];
   Item item[kItems];
   uint32_t tmem_base, abort_flag;
-  float q_scale[2][kTile];
+  float q_scale[2][kTile];  // (up to 32 rows: the second holds the quarters' references)
   float row_l[2][kTile];
-  float scl[kRows ? 3 : 1][3][kRows ? kTile : 4];                                      // K scale, log2 V scale, 1 / V scale
-  float raw_scl[kRows ? Lay<kHd, kRows>::kRaws : 1][2][kRows ? kTile : 4];
+  alignas(16) float4 scl_k[kRows ? 3 : 1][kRows ? kTile / 2 : 1];  // of two keys: K scales, log2 of V scales
+  alignas(16) float scl_v[kRows ? 3 : 1][kRows ? kTile : 4];       // 1 / V scale
+  alignas(16) float raw_scl[kRows ? Lay<kHd, kRows>::kRaws : 1][2][kRows ? kTile : 4];
 };
 
 template <int kHd, bool kRows>
@@ -367,10 +377,10 @@ __device__ __forceinline__ int tile_at(int at, int tiles, bool pair, bool* is_v)
 }
 
 // Rows [first, first + count) of a stream (row0: its first in the item) in shared memory as f16, each times a power of
-// two that puts its largest value into [2^14, 2^15).
+// two that puts its largest value into [2^14, 2^15); where `quarters`, in all quarters of the lanes.
 template <int kHd>
 __device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t* q_tile, float* q_scale, int row0,
-                                       int first, int count, int lane) {
+                                       int first, int count, bool quarters, int lane) {
   constexpr int kLanes = kHd / 8, kStep = 32 / kLanes, kFly = 8;  // lanes a row, rows a pass, passes in flight
   const int ch = lane % kLanes, sub = lane / kLanes;
   const int end = min(first + count, it.rows - row0);
@@ -398,14 +408,18 @@ __device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t*
       for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
 #pragma unroll
       for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const int e = max(static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu) - 127 - 14, -100);
+      const int e = max(static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu) - 127 - 14, -60);
       const float inv = exp2i(-e);
       if (row < end) {
         uint32_t h[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv);
-        *reinterpret_cast<uint4*>(q_tile + (ch / 8) * (kTile * 128) + row * 128 + (((ch % 8) ^ (row % 8)) << 4)) =
-            make_uint4(h[0], h[1], h[2], h[3]);
+        uint8_t* to = q_tile + (ch / 8) * (kTile * 128) + row * 128 + (((ch % 8) ^ (row % 8)) << 4);
+        *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (quarters) {
+#pragma unroll
+          for (int k = 1; k < 4; ++k) *reinterpret_cast<uint4*>(to + k * 32 * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
         if (ch == 0) q_scale[row] = exp2i(e);
       }
     }
@@ -483,12 +497,14 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
     const float c0 = p.softmax_scale * kLog2e * (kRows ? 1.f : __ldg(p.k_scale));
     uint32_t s_phase = 0, o_phase = 0;  // a bit per barrier
     uint32_t n = 0, worked = 0, pv_base = 0, tile_no = 0, xchgs = 0;
-    bool was_pair = true;
+    int was = -1;
     auto fetch_q = [&](const Item& it) {
-      if (it.pair)
-        load_q<kHd>(p, it, smem + wg * L::kQ, sm->q_scale[wg], wg * kTile, w * 32, 32, lane);
+      if (it.form == kFormPair)
+        load_q<kHd>(p, it, smem + wg * L::kQ, sm->q_scale[wg], wg * kTile, w * 32, 32, false, lane);
+      else if (it.form == kFormOne)
+        load_q<kHd>(p, it, smem, sm->q_scale[0], 0, warp * 16, 16, false, lane);
       else
-        load_q<kHd>(p, it, smem, sm->q_scale[0], 0, (w + 4 * wg) * 16, 16, lane);
+        load_q<kHd>(p, it, smem, sm->q_scale[0], 0, warp * 4, 4, true, lane);
       fence_proxy_async_smem();
       warp_arrive(&sm->q_full);
     };
@@ -499,82 +515,95 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
     const Item* it = get_item(0);
     if (it != nullptr && it->tile_hi > it->tile_lo) fetch_q(*it);
     while (it != nullptr) {
-      const int tiles = it->tile_hi - it->tile_lo;
-      const bool pair = it->pair;
-      const int row = pair ? wg * kTile + r : r;  // of the item
+      const int tiles = it->tile_hi - it->tile_lo, form = it->form;
+      const bool pair = form == kFormPair, few = form == kFormFew;
+      const int row = pair ? wg * kTile + r : (few ? lane : r);  // of the item
       const bool live = row < it->rows;
       float ref = kNegInf, l = 0.f, cc = 1.f;
       if (tiles > 0) {
         if (!warp_wait(&sm->q_full, worked & 1, abort_flag)) break;
-        if (pair != was_pair && !exchange()) break;  // the other form's columns are free
-        was_pair = pair;
-        const float c = c0 * (live ? sm->q_scale[pair ? wg : 0][r] : 1.f);
+        if (form != was) {
+          if (was >= 0 && !exchange()) break;  // the other form's columns are free
+          if (few) {               // P: a quarter's own keys alone are written, the others stay zero
+            const uint32_t none[32] = {};
+            tmem_st32(lanes + kTO + 128 + wg * 64, none);
+            tmem_st32(lanes + kTO + 128 + wg * 64 + 32, none);
+            tmem_st_wait();
+            tc_fence_before();
+            if (!exchange()) break;
+          }
+        }
+        was = form;
+        const float c = c0 * (live ? sm->q_scale[pair ? wg : 0][few ? lane : r] : 1.f);
         if (!kRows) cc = c;  // units of the reference to log2
         const bool busy = __any_sync(0xffffffffu, live);
         int keys = it->keys - it->tile_lo * kTile;  // left
-        auto steps = [&](auto one) {
-          constexpr bool kOne = decltype(one)::value;
-          constexpr int kCols = kOne ? kTile / 2 : kTile;  // whose exponentials this thread takes
-          constexpr int kOCols = kOne ? kHd / 2 : kHd;     // of O that it rescales
-          const int col0 = kOne ? wg * kCols : 0;
-          const uint32_t t_o = lanes + kTO + (kOne ? wg * kOCols : wg * 128);
+        auto steps = [&](auto which) {
+          constexpr int kForm = decltype(which)::value;
+          constexpr bool kPair = kForm == kFormPair;
+          constexpr int kCols = kPair ? kTile : (kForm == kFormOne ? kTile / 2 : 16);  // whose exponentials this thread takes
+          constexpr int kChunk = kCols < 32 ? kCols : 32;
+          constexpr int kOCols = kPair ? kHd : kHd / 2;  // of O that it rescales
+          // its columns, and (not a pair) as many that the other warpgroup takes, looked at for the maximum alone
+          const int col0 = kPair ? 0 : (kForm == kFormOne ? wg * kCols : w * 32 + wg * kCols);
+          const int other0 = kForm == kFormOne ? kCols - col0 : w * 32 + (1 - wg) * kCols;
+          const uint32_t t_o = lanes + kTO + wg * (kPair ? 128 : kOCols);
           for (int i = 0; i < tiles; ++i, keys -= kTile) {
-            const int buf = kOne ? (i & 1) : wg;
+            const int buf = kPair ? wg : (i & 1);
             if (!warp_wait(&sm->s_full[buf], (s_phase >> buf) & 1, abort_flag)) return false;
             s_phase ^= 1u << buf;
             if (kRows && !warp_wait(&sm->scl_full[tile_no % 3], (tile_no / 3) & 1, abort_flag)) return false;
             if (busy) {
               const uint32_t t_s = lanes + kTS + buf * 128;
-              const uint32_t t_p = kOne ? lanes + kTO + 128 + buf * 64 + wg * 32 : t_s;
+              const uint32_t t_p = kPair ? t_s : lanes + kTO + 128 + buf * 64 + col0 / 2;
               tc_fence_after();
               float x[kCols];
               float top = kNegInf;
-              [[maybe_unused]] const float* sk = sm->scl[kRows ? tile_no % 3 : 0][0];
-              [[maybe_unused]] const float* lv = sm->scl[kRows ? tile_no % 3 : 0][1];
-              [[maybe_unused]] const float* iv = sm->scl[kRows ? tile_no % 3 : 0][2];
-              // 32 scores of column `at` on: masked past the end; with row scales in log2, times their key's K scale
-              // and its V scale
+              [[maybe_unused]] const float4* kl = sm->scl_k[kRows ? tile_no % 3 : 0];
+              [[maybe_unused]] const float* iv = sm->scl_v[kRows ? tile_no % 3 : 0];
+              auto load = [&](float* y, int at) {
+                if constexpr (kChunk == 32)
+                  tmem_ld32(t_s + at, *reinterpret_cast<uint32_t(*)[32]>(y));
+                else
+                  tmem_ld16(t_s + at, *reinterpret_cast<uint32_t(*)[16]>(y));
+              };
+              // scores of column `at` on: masked past the end; with row scales in log2, times their key's K scale and
+              // its V scale
               auto scores = [&](float* y, int at) {
                 if (keys < kTile) {
 #pragma unroll
-                  for (int j = 0; j < 32; ++j) y[j] = at + j < keys ? y[j] : kNegInf;
+                  for (int j = 0; j < kChunk; ++j) y[j] = at + j < keys ? y[j] : kNegInf;
                 }
                 if constexpr (kRows) {
 #pragma unroll
-                  for (int j = 0; j < 32; j += 2) {
+                  for (int j = 0; j < kChunk; j += 2) {
+                    const float4 a = kl[(at + j) / 2];
                     const float2 u = fma_f32x2(mul_f32x2(make_float2(y[j], y[j + 1]), make_float2(c, c)),
-                                               *reinterpret_cast<const float2*>(sk + at + j),
-                                               *reinterpret_cast<const float2*>(lv + at + j));
+                                               make_float2(a.x, a.y), make_float2(a.z, a.w));
                     y[j] = u.x, y[j + 1] = u.y;
                   }
                 }
                 float m0 = y[0], m1 = y[1];
 #pragma unroll
-                for (int j = 2; j < 30; j += 4) m0 = fmax3(m0, y[j], y[j + 1]), m1 = fmax3(m1, y[j + 2], y[j + 3]);
+                for (int j = 2; j + 4 <= kChunk; j += 4) m0 = fmax3(m0, y[j], y[j + 1]), m1 = fmax3(m1, y[j + 2], y[j + 3]);
                 top = fmax3(top, m0, m1);
-                top = fmax3(top, y[30], y[31]);
+                top = fmax3(top, y[kChunk - 2], y[kChunk - 1]);
               };
-              if constexpr (kOne) {  // the other half's scores for the maximum alone
-                float y[64];
+              float y[kPair ? 1 : kCols];
 #pragma unroll
-                for (int k = 0; k < 64; k += 32) tmem_ld32(t_s + (64 - col0) + k, *reinterpret_cast<uint32_t(*)[32]>(y + k));
+              for (int k = 0; !kPair && k < kCols; k += kChunk) load(y + k, other0 + k);
 #pragma unroll
-                for (int k = 0; k < kCols; k += 32) tmem_ld32(t_s + col0 + k, *reinterpret_cast<uint32_t(*)[32]>(x + k));
-                tmem_ld_wait();
+              for (int k = 0; k < kCols; k += kChunk) load(x + k, col0 + k);
+              tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 64; k += 32) scores(y + k, 64 - col0 + k);
-              } else {
+              for (int k = 0; !kPair && k < kCols; k += kChunk) scores(y + k, other0 + k);
 #pragma unroll
-                for (int k = 0; k < kCols; k += 32) tmem_ld32(t_s + k, *reinterpret_cast<uint32_t(*)[32]>(x + k));
-                tmem_ld_wait();
-              }
-#pragma unroll
-              for (int k = 0; k < kCols; k += 32) scores(x + k, col0 + k);
+              for (int k = 0; k < kCols; k += kChunk) scores(x + k, col0 + k);
               const bool raise = (top - ref) * cc > kTau;
               if (i == 0) {
                 ref = top == kNegInf ? 0.f : top;
               } else if (__any_sync(0xffffffffu, raise && live)) {
-                if (kOne && !warp_wait(&sm->pv_done, (pv_base + i - 1) & 1, abort_flag)) return false;
+                if (!kPair && !warp_wait(&sm->pv_done, (pv_base + i - 1) & 1, abort_flag)) return false;
                 tc_fence_after();
                 const float alpha = raise ? ex2_approx((ref - top) * cc) : 1.f;
                 if (raise) ref = top;
@@ -591,25 +620,35 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
               }
               float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-              for (int k = 0; k < kCols; k += 32) {
-                uint32_t h[16];
+              for (int k = 0; k < kCols; k += kChunk) {
+                uint32_t h[kChunk / 2];
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                  float2 d = add_f32x2(make_float2(x[k + j], x[k + j + 1]), make_float2(-ref, -ref));
-                  if constexpr (kRows)
-                    d = add_f32x2(d, make_float2(kLift, kLift));
-                  else
-                    d = fma_f32x2(d, make_float2(cc, cc), make_float2(kLift, kLift));
-                  d.x = ex2_approx(d.x);
-                  d.y = ex2_approx(d.y);
-                  if constexpr (kRows)
-                    sum[(j >> 1) & 1] =
-                        fma_f32x2(d, *reinterpret_cast<const float2*>(iv + col0 + k + j), sum[(j >> 1) & 1]);
-                  else
-                    sum[(j >> 1) & 1] = add_f32x2(sum[(j >> 1) & 1], d);
-                  h[j / 2] = pack_f16x2(d.x, d.y);
+                for (int j = 0; j < kChunk; j += 4) {
+                  float2 d[2];
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    d[e] = add_f32x2(make_float2(x[k + j + 2 * e], x[k + j + 2 * e + 1]), make_float2(-ref, -ref));
+                    if constexpr (kRows)
+                      d[e] = add_f32x2(d[e], make_float2(kLift, kLift));
+                    else
+                      d[e] = fma_f32x2(d[e], make_float2(cc, cc), make_float2(kLift, kLift));
+                    d[e].x = ex2_approx(d[e].x);
+                    d[e].y = ex2_approx(d[e].y);
+                    h[j / 2 + e] = pack_f16x2(d[e].x, d[e].y);
+                  }
+                  if constexpr (kRows) {
+                    const float4 v = *reinterpret_cast<const float4*>(iv + col0 + k + j);
+                    sum[0] = fma_f32x2(d[0], make_float2(v.x, v.y), sum[0]);
+                    sum[1] = fma_f32x2(d[1], make_float2(v.z, v.w), sum[1]);
+                  } else {
+                    sum[0] = add_f32x2(sum[0], d[0]);
+                    sum[1] = add_f32x2(sum[1], d[1]);
+                  }
                 }
-                tmem_st16(t_p + k / 2, h);
+                if constexpr (kChunk == 32)
+                  tmem_st16(t_p + k / 2, h);
+                else
+                  tmem_st8(t_p + k / 2, h);
               }
               l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
               tmem_st_wait();
@@ -617,11 +656,18 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
             }
             ++tile_no;
             warp_arrive(&sm->p_full[buf]);
-            if (!kOne && lane == 0) mbar_arrive(&sm->p_full[buf]);  // the barrier counts eight warps
+            if (kPair && lane == 0) mbar_arrive(&sm->p_full[buf]);  // the barrier counts eight warps
           }
           return true;
         };
-        if (!(pair ? steps(std::false_type{}) : steps(std::true_type{}))) break;
+        bool ok;
+        if (pair)
+          ok = steps(std::integral_constant<int, kFormPair>{});
+        else if (few)
+          ok = steps(std::integral_constant<int, kFormFew>{});
+        else
+          ok = steps(std::integral_constant<int, kFormOne>{});
+        if (!ok) break;
         if (pair)
           s_phase ^= (tiles & 1) << (1 - wg);
         else
@@ -630,64 +676,136 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
       // Q of the next item, while the last product runs.  Where another warp reads the rows' scales, all have to be
       // done with those of this item.
       const Item* next = get_item(n + 1);
-      if (!pair) sm->row_l[wg][r] = l;
-      if ((!pair || tiles == 0 || (next != nullptr && !next->pair)) && !exchange()) break;
-      if (!pair) l = sm->row_l[0][r] + sm->row_l[1][r];
+      const bool fetch = next != nullptr && next->tile_hi > next->tile_lo;
+      const bool late = few && tiles > 0 && fetch && next->form == kFormPair;  // the quarters' sums lie where its Q goes
+      if (!pair && tiles > 0) sm->row_l[wg][r] = l;
+      if ((!pair || tiles == 0 || (next != nullptr && next->form != kFormPair)) && !exchange()) break;
+      if (form == kFormOne && tiles > 0) l = sm->row_l[0][r] + sm->row_l[1][r];
       if (tiles > 0) {
         if (!warp_wait(&sm->q_empty, worked & 1, abort_flag)) break;
         ++worked;
       }
-      if (next != nullptr && next->tile_hi > next->tile_lo) fetch_q(*next);
+      if (fetch && !late) fetch_q(*next);
       const int os = pair ? wg : 0;
       if (tiles > 0) {
         if (!warp_wait(&sm->o_full[os], (o_phase >> os) & 1, abort_flag)) break;
         o_phase ^= pair ? 3u : 1u;
         tc_fence_after();
       }
-      if (__any_sync(0xffffffffu, live)) {
-        const uint32_t rr = static_cast<uint32_t>(it->row0 + row);
+      // Results of four or 32 values of a row (of the item): rounded to the outputs, or as they are to the workspace.
+      const int slot = it->slot;
+      const float v_scale = kRows ? 1.f : __ldg(p.v_scale);
+      auto place_of = [&](int of_row, int* head, long long* token) {
+        const uint32_t rr = static_cast<uint32_t>(it->row0 + of_row);
         const uint32_t tok = fast_div(rr, p.group);
-        const int head = it->head * static_cast<int>(p.group.d) + static_cast<int>(rr - tok * p.group.d);
-        const long long token = it->t0 + static_cast<long long>(tok), at = token * p.h_q + head;
+        *head = it->head * static_cast<int>(p.group.d) + static_cast<int>(rr - tok * p.group.d);
+        *token = it->t0 + static_cast<long long>(tok);
+      };
+      auto put_sums = [&](int of_row, int head, long long token, float m, float sum) {
+        const long long at = token * p.h_q + head;
+        if (slot == kDirect)  // a sequence without keys: -inf
+          p.lse[at] = tiles > 0 ? (m + lg2_approx(sum) - kLift) * kLn2 : kNegInf;
+        else if (slot == kPlane)
+          p.plane_ml[it->list][at] = make_float2(m, sum);
+        else
+          p.slot_ml[static_cast<long long>(slot) * p.slot_rows + of_row] = make_float2(m, sum);
+      };
+      auto row_at = [&](int of_row, int head, long long token) -> float* {
+        return slot == kPlane ? p.plane_o[it->list] + (token * p.h_q + head) * kHd
+                              : p.slot_o + (static_cast<long long>(slot) * p.slot_rows + of_row) * kHd;
+      };
+      if (few && tiles > 0) {
+        if (wg == 0) sm->q_scale[1][r] = ref;
+        if (!exchange()) break;
+        const float unit_of = cc;  // this thread's row is its lane's in every quarter
+        float m = kNegInf;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float lk = sm->row_l[0][k * 32 + lane] + sm->row_l[1][k * 32 + lane];
+          if (!(lk == 0.f)) m = fmaxf(m, sm->q_scale[1][k * 32 + lane] * unit_of);
+        }
+        float sum = 0.f, mine = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float lk = sm->row_l[0][k * 32 + lane] + sm->row_l[1][k * 32 + lane];
+          const float f = lk == 0.f ? 0.f : ex2_approx(sm->q_scale[1][k * 32 + lane] * unit_of - m);
+          sum += lk * f;
+          if (k == w) mine = f;
+        }
+        int head;
+        long long token;
+        place_of(lane, &head, &token);
+        if (warp == 0 && live) put_sums(lane, head, token, m, sum);
+        if (slot == kDirect) mine *= v_scale / sum;
+        const int out_row = threadIdx.x / 8, piece = threadIdx.x % 8;  // of 32 rows, of eight times four dims
+        place_of(out_row, &head, &token);
+        float* quarters = reinterpret_cast<float*>(smem + L::kOffSum);  // [half][quarter][row][32], 16 bytes swizzled
+        for (int k = 0; k < kHd / 2; k += 32) {
+          uint32_t o[32];
+          tmem_ld32(lanes + kTO + wg * (kHd / 2) + k, o);
+          tmem_ld_wait();
+          float* to = quarters + ((wg * 4 + w) * kFew + lane) * 32;
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(to + ((j ^ (lane % 8)) * 4)) =
+                  make_float4(__uint_as_float(o[4 * j]) * mine, __uint_as_float(o[4 * j + 1]) * mine,
+                              __uint_as_float(o[4 * j + 2]) * mine, __uint_as_float(o[4 * j + 3]) * mine);
+          }
+          if (!exchange()) break;
+          if (out_row < it->rows) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float4 b = *reinterpret_cast<const float4*>(
+                    quarters + ((half * 4 + q) * kFew + out_row) * 32 + ((piece ^ (out_row % 8)) * 4));
+                a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+              }
+              const int dim = half * (kHd / 2) + k + piece * 4;
+              if (slot == kDirect)
+                *reinterpret_cast<uint2*>(p.out + token * p.o_tok + head * p.o_head + dim) =
+                    make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+              else
+                *reinterpret_cast<float4*>(row_at(out_row, head, token) + dim) = a;
+            }
+          }
+          if ((k + 32 < kHd / 2 || late) && !exchange()) break;  // read before the next are written
+        }
+        tc_fence_before();
+        if (late) fetch_q(*next);
+      } else if (__any_sync(0xffffffffu, live)) {
+        int head;
+        long long token;
+        place_of(row, &head, &token);
         const int dims = pair ? kHd : kHd / 2, dim0 = pair ? 0 : wg * (kHd / 2);
         const uint32_t t_o = lanes + kTO + os * 128 + dim0;
-        const bool leads = live && (pair || wg == 0);
-        if (it->slot == kDirect) {
-          // a sequence without keys: zeros, -inf
-          const float f = tiles > 0 ? (kRows ? 1.f : __ldg(p.v_scale)) / l : 0.f;
-          uint16_t* to = p.out + token * p.o_tok + head * p.o_head + dim0;
-          if (leads) p.lse[at] = tiles > 0 ? (ref * cc + lg2_approx(l) - kLift) * kLn2 : kNegInf;
-          for (int k = 0; k < dims; k += 32) {
-            uint32_t o[32] = {};
-            __syncwarp();
-            if (tiles > 0) {
-              tmem_ld32(t_o + k, o);
-              tmem_ld_wait();
-            }
-            if (!live) continue;
+        if (live && (pair || (few ? warp == 0 : wg == 0))) put_sums(row, head, token, ref * cc, l);
+        const float f = tiles > 0 ? v_scale / l : 0.f;
+        const bool mine = live && (!few || w == 0);
+        for (int k = 0; k < dims; k += 32) {
+          uint32_t o[32] = {};
+          __syncwarp();
+          if (tiles > 0) {
+            tmem_ld32(t_o + k, o);
+            tmem_ld_wait();
+          }
+          if (slot == kDirect) {
+            uint16_t* to = p.out + token * p.o_tok + head * p.o_head + dim0 + k;
 #pragma unroll
             for (int j = 0; j < 32; j += 8) {
               uint32_t h[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 h[e] = pack_bf16x2(__uint_as_float(o[j + 2 * e]) * f, __uint_as_float(o[j + 2 * e + 1]) * f);
-              *reinterpret_cast<uint4*>(to + k + j) = make_uint4(h[0], h[1], h[2], h[3]);
+              if (mine) *reinterpret_cast<uint4*>(to + j) = make_uint4(h[0], h[1], h[2], h[3]);
             }
-          }
-        } else {
-          const bool plane = it->slot == kPlane;
-          const long long place = plane ? at : static_cast<long long>(it->slot) * p.slot_rows + row;
-          float* to = (plane ? p.plane_o[it->list] : p.slot_o) + place * kHd + dim0;
-          if (leads) (plane ? p.plane_ml[it->list] : p.slot_ml)[place] = make_float2(ref * cc, l);
-          for (int k = 0; k < dims; k += 32) {
-            uint32_t o[32];
-            __syncwarp();
-            tmem_ld32(t_o + k, o);
-            tmem_ld_wait();
-            if (!live) continue;
+          } else {
+            float* to = row_at(row, head, token) + dim0 + k;
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<uint4*>(to + k + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+              if (mine) *reinterpret_cast<uint4*>(to + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           }
         }
         __syncwarp();
@@ -711,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
       const Item* it = get_item(n);
       if (it == nullptr) break;
       const int tiles = it->tile_hi - it->tile_lo, left = it->keys - it->tile_lo * kTile;
-      const bool pair = it->pair;
+      const bool pair = it->form == kFormPair;
       drop_item(n);
       for (int at = 0; at < 2 * tiles; ++at, ++f) {
         bool is_v;
@@ -727,9 +845,10 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
           if (!is_v) {  // past the end: one, so that a stale scale cannot turn a zero weight into a NaN
             const float a = tid < valid ? sm->raw_scl[rs][0][tid] : 1.f, b = tid < valid ? sm->raw_scl[rs][1][tid] : 1.f;
             const int ss = tile_no % 3;
-            sm->scl[ss][0][tid] = a;
-            sm->scl[ss][1][tid] = lg2_approx(b);
-            sm->scl[ss][2][tid] = 1.f / b;
+            float* two = reinterpret_cast<float*>(&sm->scl_k[ss][tid / 2]) + tid % 2;
+            two[0] = a;
+            two[2] = lg2_approx(b);
+            sm->scl_v[ss][tid] = 1.f / b;
             warp_arrive(&sm->scl_full[ss]);
             ++tile_no;
           }
@@ -794,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
         const Item* it = get_item(n);
         if (it == nullptr) break;
         const int tiles = it->tile_hi - it->tile_lo;
-        const bool pair = it->pair;
+        const bool pair = it->form == kFormPair;
         drop_item(n);
         if (tiles == 0) continue;
         ok = false;
@@ -872,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
         if (it == nullptr) break;
         const int tile_lo = it->tile_lo, tile_hi = it->tile_hi, keys = it->keys, head = it->head;
         const int tiles = tile_hi - tile_lo;
-        const bool pair = it->pair;
+        const bool pair = it->form == kFormPair;
         const int32_t* table = p.list[it->list].table + static_cast<long long>(it->seg) * p.list[it->list].max_blocks;
         drop_item(n);
         // lane c: the page of chunk c of a tile
