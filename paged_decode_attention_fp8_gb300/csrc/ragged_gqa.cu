@@ -9,20 +9,22 @@
 // its key tiles of 128 and a fixed part take.  The line is cut into equal shares on the device, since lengths are known
 // there alone; an item that a cut meets leaves partial sums in the workspace, merged by a second launch.
 //
-// Per item the rows are the M of the matrix products (f16, tcgen05): S = Q K^T and O += P V, 128 rows in the lanes of
-// TMEM, P written over S by the threads that own the rows.  K and V are exact in f16, Q takes a power of two per row.
+// Per item the rows are the M of the matrix products (tcgen05): S = Q K^T and O += P V, 128 rows in the lanes of TMEM,
+// P written over S by the threads that own the rows.  K is read as it is cached, Q times a power of two per row as two
+// E4M3 terms that sum to it; P is f16, and V is turned into f16, which holds it exactly.
 //   up to 256 rows: two streams of 128 rows, each with its own S and O; the tensor core works for one while the other's
 //     softmax runs.
 //   up to 128 rows: one stream, S in two buffers by tile parity, and both softmax warpgroups share a tile's columns.
 //   up to 32 rows: the same with the rows in all four quarters of the lanes, each with P for its own 32 keys of a tile
 //     (zero for the others) and a reference of its own: eight warps share the softmax, the quarters are summed at the end.
-// Warps: 0-3 and 4-7 the two softmax warpgroups, 8-11 turn raw tiles into f16, 12 issues the products, 13 copies raw
-// tiles (one bulk copy per page and operand), 14 tells the others the share's items, 15 fills rows of no sequence.
+// Warps: 0-3 and 4-7 the two softmax warpgroups, 8-11 turn V into f16, 12 issues the products, 13 copies tiles (one TMA
+// copy per page and operand), 14 tells the others the share's items, 15 fills rows of no sequence.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
@@ -39,10 +41,12 @@ constexpr int kItemRows = 256;  // rows an item
 constexpr int kThreads = 512;
 constexpr int kSoftmaxRegs = 192, kConvertRegs = 64, kIssueRegs = 64;  // registers a thread of the warpgroups
 constexpr float kLift = 7.f;    // P = 2^(score - reference + 7): 2^15 at most in f16, normal down to 2^-21 of the largest
+constexpr float kFar = 1048576.f;  // 2^20 in log2 units: up to here the lift and the difference keep their fraction
 constexpr float kTau = 8.f;     // the reference moves when a score passes it by more
 
 // Lengths of the line, in eighths of a tile of 256 rows.
 constexpr int kPairTile = 8, kOneTile = 5, kPairFixed = 12, kOneFixed = 8, kEmpty = 1;
+constexpr int kLeast = kPairFixed + 2 * kPairTile;  // of a share
 
 struct List {
   const int32_t* starts;  // segment s has the tokens [per starts[s], per starts[s + 1]); null: [per s, per (s + 1))
@@ -137,9 +141,11 @@ __device__ __forceinline__ int cut_at(int off, int len, bool pair, int tiles, in
 }
 
 struct Plan {
-  long long lo, hi, seg_at;  // this share, and where the segment begins that it begins in
-  long long sums[17];
-  int seg, units;
+  Seg g;  // where this share begins: the segment, the item and how far into it
+  int seg, head, rt, off;
+  int units;
+  long long lo, hi;  // the share
+  long long sums[kThreads / 32];
 };
 
 // The share of CTA `unit`; the threads of the block together.
@@ -148,12 +154,10 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan* plan, int unit)
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   uint32_t bad = 0;
   long long mine = 0;
-  int most = 0;
   Seg g = {};
   for (int s = threadIdx.x; s < n; s += kThreads) {
     g = read_seg(p, s, &bad);
     mine += g.head * p.h_kv;
-    most = max(most, g.full);
   }
   if (bad && unit == 0) atomicOr(&g_status_ragged, bad);
   auto scan = [&](long long x, long long* all) {  // sum of the threads before this one, and of all
@@ -172,70 +176,91 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan* plan, int unit)
       if (w < warp) before += y;
       total += y;
     }
-    __syncthreads();
     *all = total;
     return before + s - x;
   };
   long long total;
   long long at = scan(mine, &total);
-  const int units = static_cast<int>(
-      max(1ll, min(static_cast<long long>(gridDim.x), total / (kPairFixed + 2 * kPairTile))));
-  const int few = static_cast<int>(max(1ll, min(4ll, total / units / (3 * kPairTile))));
+  int units, few;
+  long long raw[2];
+  if (total < (1 << 24)) {  // 32-bit division
+    const uint32_t t = static_cast<uint32_t>(total);
+    units = static_cast<int>(max(1u, min(gridDim.x, t / kLeast)));
+    few = static_cast<int>(t / units / (3 * kPairTile));
+    raw[0] = t * unit / units;
+    raw[1] = t * (unit + 1) / units;
+  } else {
+    units = gridDim.x;
+    few = 4;
+    raw[0] = total * unit / units;
+    raw[1] = total * (unit + 1) / units;
+  }
+  few = max(1, min(4, few));
+  // one thread finds each end of the share in its segment
+  auto locate = [&](int s, long long from, long long len) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (raw[e] < from || raw[e] >= from + len) continue;
+      const long long in = raw[e] - from;
+      int h, rest;
+      if (in < (1ll << 31) && g.head < (1ll << 31)) {
+        h = static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(g.head));
+        rest = static_cast<int>(static_cast<uint32_t>(in) - static_cast<uint32_t>(h) * static_cast<uint32_t>(g.head));
+      } else {
+        h = static_cast<int>(in / g.head);
+        rest = static_cast<int>(min(in - h * g.head, 0x7FFFFFFFll));
+      }
+      int rt = min(rest / g.full, g.row_tiles - 1);
+      const bool last = rt == g.row_tiles - 1;
+      const int item = last ? g.last : g.full;
+      int off = cut_at(rest - rt * g.full, item, item == g.full && g.tiles > 0, g.tiles, few);
+      const long long to = from + h * g.head + static_cast<long long>(rt) * g.full + off;
+      if (e == 0) {
+        plan->lo = p.lo[unit] = to;
+        if (off == item) {  // the next item's beginning
+          off = 0;
+          if (++rt == g.row_tiles) rt = 0, ++h;
+        }
+        plan->g = g;
+        plan->seg = s;
+        plan->head = h;
+        plan->rt = rt;
+        plan->off = off;
+      } else {
+        plan->hi = to;
+      }
+    }
+  };
   if (threadIdx.x == 0) {
     plan->units = units;
-    plan->lo = 0;
-    plan->hi = total;
-    plan->seg = 0;
-    plan->seg_at = 0;
+    if (total == 0) plan->lo = 0;
+    if (raw[1] >= total) plan->hi = total;
+    if (!p.joined) p.cuts[unit].valid = 0;
+    if (unit == units - 1) {
+      p.lo[units] = total;
+      *p.units = units;
+    }
   }
-  __syncthreads();
-  const long long raw[2] = {total * unit / units, total * (unit + 1) / units};
-  long long base = 0;
-  for (int s0 = 0; s0 < n; s0 += kThreads) {
-    const int s = s0 + threadIdx.x;
-    long long len = 0;
-    if (n > kThreads) {
+  if (n <= kThreads) {
+    if (p.joined && unit == 0 && static_cast<int>(threadIdx.x) < n) p.seg_at[threadIdx.x] = at;
+    locate(threadIdx.x, at, mine);
+  } else {
+    long long base = 0;
+    for (int s0 = 0; s0 < n; s0 += kThreads) {
+      __syncthreads();  // the sums have been read
+      const int s = s0 + static_cast<int>(threadIdx.x);
+      long long len = 0, all;
       if (s < n) {
         g = read_seg(p, s, &bad);
         len = g.head * p.h_kv;
       }
-      long long all;
       at = base + scan(len, &all);
       base += all;
-    } else {
-      len = mine;
-    }
-    if (s < n && p.joined && unit == 0) p.seg_at[s] = at;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (raw[e] >= at && raw[e] < at + len) {
-        const long long in = raw[e] - at;
-        const long long h = in / g.head;
-        const int rest = static_cast<int>(in - h * g.head);
-        const int rt = min(rest / max(g.full, 1), g.row_tiles - 1);
-        const bool last = rt == g.row_tiles - 1;
-        const bool pair = !last || g.last == g.full;
-        const long long to = at + h * g.head + static_cast<long long>(rt) * g.full +
-                             cut_at(rest - rt * g.full, last ? g.last : g.full, pair, g.tiles, few);
-        if (e == 0) {
-          plan->lo = to;
-          plan->seg = s;
-          plan->seg_at = at;
-        } else {
-          plan->hi = to;
-        }
-      }
+      if (s < n && p.joined && unit == 0) p.seg_at[s] = at;
+      locate(s, at, len);
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0 && unit < units) {
-    if (!p.joined) p.cuts[unit].valid = 0;
-    p.lo[unit] = plan->lo;
-    if (unit == units - 1) {
-      p.lo[units] = plan->hi;
-      *p.units = units;
-    }
-  }
 }
 
 // One item of a share, or the part of it that lies in the share.
@@ -254,24 +279,14 @@ struct Walk {
   Seg g;
   int seg, head, rt, off, left;
   bool first;
-  __device__ __forceinline__ Walk(const Params& p, const Plan& plan) {
-    left = static_cast<int>(plan.hi - plan.lo);
+  __device__ __forceinline__ Walk(const Plan& plan, int unit) {
+    left = unit < plan.units ? static_cast<int>(min(plan.hi - plan.lo, 0x7FFFFFFFll)) : 0;
+    g = plan.g;
     seg = plan.seg;
+    head = plan.head;
+    rt = plan.rt;
+    off = plan.off;
     first = true;
-    head = rt = off = 0;
-    if (left <= 0) return;
-    uint32_t bad = 0;
-    g = read_seg(p, seg, &bad);
-    const long long in = plan.lo - plan.seg_at;
-    head = p.h_kv;
-    if (g.head > 0) {
-      head = static_cast<int>(in / g.head);
-      const int rest = static_cast<int>(in - head * g.head);
-      if (head < p.h_kv) {
-        rt = min(rest / max(g.full, 1), g.row_tiles - 1);
-        off = rest - rt * g.full;
-      }
-    }
   }
   __device__ __forceinline__ bool next(const Params& p, const Plan& plan, int unit, Item* it) {
     if (left <= 0) return false;
@@ -318,15 +333,19 @@ struct Walk {
 
 template <int kHd, bool kRows>
 struct Lay {
-  static constexpr int kHalves = kHd / 64;                // blocks of 64 dims, 128 bytes a row in f16
-  static constexpr int kQ = kHalves * kTile * 128;        // a stream's Q
-  static constexpr int kF = kHalves * kTile * 128;        // a tile of K or V in f16
-  static constexpr int kRaw = kTile * kHd;                // the same as codes
-  static constexpr int kSlots = 3, kRaws = kRows && kHd == 128 ? 3 : (kHd == 64 ? 8 : 4);
-  static constexpr int kOffF = 2 * kQ, kOffRaw = kOffF + kSlots * kF, kOffSum = kHd == 128 ? kQ : kOffRaw + kRaws * kRaw;
+  static constexpr int kQ = 2 * kTile * kHd;         // a stream's Q: two E4M3 terms a value
+  static constexpr int kRaw = kTile * kHd;           // a tile of K or V as codes
+  static constexpr int kF = kTile * kHd * 2;         // a tile of V in f16
+  static constexpr int kKs = kHd == 128 ? 3 : 6, kVs = kHd == 128 ? (kRows ? 2 : 3) : 6, kFs = kHd == 128 ? 2 : 3;
+  // Scales of a tile's rows: those of tile i are written once V of tile i - 1 is converted, which waits for the product
+  // with P of tile i - 1 - kFs, so the softmax is done with tile i - 1 - kFs.
+  static constexpr int kScls = kFs + 1;
   static constexpr int kSum = 2 * 4 * kFew * 32 * 4;  // sums of the quarters, 32 dims of either half; the second Q's place
-  static constexpr int kOffCtl = kOffRaw + kRaws * kRaw + (kHd == 128 ? 0 : kSum);
+  static constexpr int kOffK = 2 * kQ, kOffV = kOffK + kKs * kRaw, kOffF = kOffV + kVs * kRaw;
+  static constexpr int kOffSum = kHd == 128 ? kQ : kOffF + kFs * kF;
+  static constexpr int kOffCtl = kOffF + kFs * kF + (kHd == 128 ? 0 : kSum);
   static_assert(kHd != 128 || kSum <= kQ, "");
+  static constexpr uint32_t kSwizzle = kHd == 128 ? SWIZZLE_128B : 4;  // of a row of codes
 };
 
 constexpr int kItems = 4;       // items told ahead
@@ -334,19 +353,19 @@ constexpr int kItemWarps = 14;  // that are told
 
 template <int kHd, bool kRows>
 struct Control {
+  using L = Lay<kHd, kRows>;
   Plan plan;
-  uint64_t raw_full[8], raw_empty[8];
-  uint64_t f_full[3], f_empty[3];
+  uint64_t k_full[L::kKs], k_empty[L::kKs], v_full[L::kVs], v_empty[L::kVs], f_full[L::kFs], f_empty[L::kFs];
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t q_full, q_empty, pv_done, xchg, scl_full[3], final_mma;
+  uint64_t q_full, q_empty, pv_done, xchg, scl_full[L::kScls], final_mma;
   uint64_t item_full[kItems], item_empty[kItems];
   Item item[kItems];
   uint32_t tmem_base, abort_flag;
   float q_scale[2][kTile];  // (up to 32 rows: the second holds the quarters' references)
   float row_l[2][kTile];
-  alignas(16) float4 scl_k[kRows ? 3 : 1][kRows ? kTile / 2 : 1];  // of two keys: K scales, log2 of V scales
-  alignas(16) float scl_v[kRows ? 3 : 1][kRows ? kTile : 4];       // 1 / V scale
-  alignas(16) float raw_scl[kRows ? Lay<kHd, kRows>::kRaws : 1][2][kRows ? kTile : 4];
+  alignas(16) float4 scl_k[kRows ? L::kScls : 1][kRows ? kTile / 2 : 1];  // of two keys: K scales, log2 of V scales
+  alignas(16) float scl_v[kRows ? L::kScls : 1][kRows ? kTile : 4];       // 1 / V scale
+  alignas(16) float raw_scl[kRows ? L::kVs : 1][2][kRows ? kTile : 4];
 };
 
 template <int kHd, bool kRows>
@@ -361,8 +380,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
-// The tile of K or V that comes at place `at` of an item's sequence of 2 T tiles, as the products take them: streams of
-// their own K0 V0 K1 V1 .., one stream K0 K1 V0 K2 V1 ..
+// The tile of K or V that is copied at place `at` of an item's sequence of 2 T tiles, as the products take them: streams
+// of their own K0 V0 K1 V1 .., one stream K0 K1 V0 K2 V1 ..
 __device__ __forceinline__ int tile_at(int at, int tiles, bool pair, bool* is_v) {
   if (pair) {
     *is_v = at & 1;
@@ -376,49 +395,64 @@ __device__ __forceinline__ int tile_at(int at, int tiles, bool pair, bool* is_v)
   return (at & 1) ? (at + 1) >> 1 : (at >> 1) - 1;
 }
 
-// Rows [first, first + count) of a stream (row0: its first in the item) in shared memory as f16, each times a power of
-// two that puts its largest value into [2^14, 2^15); where `quarters`, in all quarters of the lanes.
+// Smallest e with amax <= 448 * 2^e, from -60 on (what is smaller still makes no score).
+__device__ __forceinline__ int exponent_448(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  return max(static_cast<int>(bits >> 23) - 127 - ((bits & 0x7FFFFFu) <= 0x600000u ? 8 : 7), -60);
+}
+
+// Rows [first, first + count) of a stream (row0: its first in the item) in shared memory: each times a power of two that
+// puts its largest value up to 448, as two E4M3 terms, x = E4M3(x) + E4M3(x - E4M3(x)) (exact for bf16 from 2^-10 of the
+// row's largest value on).  Where `quarters`, in all quarters of the lanes.  head_dim 128: a tile of 128-byte rows per
+// term; 64: both terms in one row.
 template <int kHd>
 __device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t* q_tile, float* q_scale, int row0,
                                        int first, int count, bool quarters, int lane) {
-  constexpr int kLanes = kHd / 8, kStep = 32 / kLanes, kFly = 8;  // lanes a row, rows a pass, passes in flight
+  constexpr int kLanes = kHd / 16, kStep = 32 / kLanes, kFly = kHd == 128 ? 4 : 2;  // lanes a row, rows a pass, passes in flight
   const int ch = lane % kLanes, sub = lane / kLanes;
   const int end = min(first + count, it.rows - row0);
   const int item_row = it.row0 + row0, head0 = it.head * static_cast<int>(p.group.d), t0 = it.t0;
   for (int base = first; base < end; base += kStep * kFly) {
-    uint4 x[kFly];
+    uint4 x[kFly][2];
 #pragma unroll
     for (int i = 0; i < kFly; ++i) {
       const int row = base + i * kStep + sub;
-      x[i] = make_uint4(0, 0, 0, 0);
+      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
       if (row < end) {
         const uint32_t r = static_cast<uint32_t>(item_row + row);
         const uint32_t t = fast_div(r, p.group);
         const int head = head0 + static_cast<int>(r - t * p.group.d);
-        x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (t0 + static_cast<long long>(t)) * p.q_tok + head * p.q_head +
-                                                    ch * 8));
+        const uint4* from = reinterpret_cast<const uint4*>(p.q + (t0 + static_cast<long long>(t)) * p.q_tok +
+                                                           head * p.q_head + ch * 16);
+        x[i][0] = __ldg(from);
+        x[i][1] = __ldg(from + 1);
       }
     }
 #pragma unroll
     for (int i = 0; i < kFly; ++i) {
       const int row = base + i * kStep + sub;
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      const uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
       float amax = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+      for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
 #pragma unroll
       for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const int e = max(static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu) - 127 - 14, -60);
-      const float inv = exp2i(-e);
+      const int e = exponent_448(amax);
+      const float inv = amax < -kNegInf ? exp2i(-e) : __int_as_float(0x7FFFFFFF);  // an infinity makes no score either
       if (row < end) {
-        uint32_t h[4];
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv);
-        uint8_t* to = q_tile + (ch / 8) * (kTile * 128) + row * 128 + (((ch % 8) ^ (row % 8)) << 4);
-        *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (quarters) {
+        for (int k = 0; k < 4; ++k)
+          split_e4m3x4(bf16_lo(w[2 * k]) * inv, bf16_hi(w[2 * k]) * inv, bf16_lo(w[2 * k + 1]) * inv,
+                       bf16_hi(w[2 * k + 1]) * inv, hi[k], lo[k]);
+        constexpr int kLoChunk = kHd == 128 ? 0 : 4, kLoTile = kHd == 128 ? kTile * 128 : 0;
+        uint8_t* to = q_tile + row * 128;
 #pragma unroll
-          for (int k = 1; k < 4; ++k) *reinterpret_cast<uint4*>(to + k * 32 * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+        for (int k = 0; k < 4; ++k) {
+          if (k > 0 && !quarters) break;
+          *reinterpret_cast<uint4*>(to + k * 32 * 128 + ((ch ^ (row % 8)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(to + k * 32 * 128 + kLoTile + (((ch + kLoChunk) ^ (row % 8)) << 4)) =
+              make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         if (ch == 0) q_scale[row] = exp2i(e);
       }
@@ -432,7 +466,9 @@ __device__ __forceinline__ uint4 to_f16(uint2 x) {
 }
 
 template <int kHd, bool kRows>
-__global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    ragged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ Params p) {
   using L = Lay<kHd, kRows>;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's unit; there is no other shared memory
   Control<kHd, kRows>* sm = reinterpret_cast<Control<kHd, kRows>*>(smem + L::kOffCtl);
@@ -441,15 +477,19 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
   const int unit = blockIdx.x;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 8; ++i) {
-      mbar_init(&sm->raw_full[i], kRows ? 33 : 1);  // the bytes' arrival (+ the scales: one per lane)
-      mbar_init(&sm->raw_empty[i], 4);              // converter warps
+    for (int i = 0; i < L::kKs; ++i) {
+      mbar_init(&sm->k_full[i], 1);
+      mbar_init(&sm->k_empty[i], 1);  // commits
     }
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < L::kVs; ++i) {
+      mbar_init(&sm->v_full[i], kRows ? 33 : 1);  // the bytes' arrival (+ the scales: one per lane)
+      mbar_init(&sm->v_empty[i], 4);              // converter warps
+    }
+    for (int i = 0; i < L::kFs; ++i) {
       mbar_init(&sm->f_full[i], 4);
       mbar_init(&sm->f_empty[i], 1);  // commits
-      mbar_init(&sm->scl_full[i], 4);
     }
+    for (int i = 0; i < L::kScls; ++i) mbar_init(&sm->scl_full[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->s_full[i], 1);
       mbar_init(&sm->p_full[i], 8);
@@ -552,15 +592,15 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
             const int buf = kPair ? wg : (i & 1);
             if (!warp_wait(&sm->s_full[buf], (s_phase >> buf) & 1, abort_flag)) return false;
             s_phase ^= 1u << buf;
-            if (kRows && !warp_wait(&sm->scl_full[tile_no % 3], (tile_no / 3) & 1, abort_flag)) return false;
+            if (kRows && !warp_wait(&sm->scl_full[tile_no % L::kScls], (tile_no / L::kScls) & 1, abort_flag)) return false;
             if (busy) {
               const uint32_t t_s = lanes + kTS + buf * 128;
               const uint32_t t_p = kPair ? t_s : lanes + kTO + 128 + buf * 64 + col0 / 2;
               tc_fence_after();
               float x[kCols];
               float top = kNegInf;
-              [[maybe_unused]] const float4* kl = sm->scl_k[kRows ? tile_no % 3 : 0];
-              [[maybe_unused]] const float* iv = sm->scl_v[kRows ? tile_no % 3 : 0];
+              [[maybe_unused]] const float4* kl = sm->scl_k[kRows ? tile_no % L::kScls : 0];
+              [[maybe_unused]] const float* iv = sm->scl_v[kRows ? tile_no % L::kScls : 0];
               auto load = [&](float* y, int at) {
                 if constexpr (kChunk == 32)
                   tmem_ld32(t_s + at, *reinterpret_cast<uint32_t(*)[32]>(y));
@@ -583,30 +623,18 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
                     y[j] = u.x, y[j + 1] = u.y;
                   }
                 }
+              };
+              auto raise_top = [&](const float* y) {
                 float m0 = y[0], m1 = y[1];
 #pragma unroll
                 for (int j = 2; j + 4 <= kChunk; j += 4) m0 = fmax3(m0, y[j], y[j + 1]), m1 = fmax3(m1, y[j + 2], y[j + 3]);
                 top = fmax3(top, m0, m1);
                 top = fmax3(top, y[kChunk - 2], y[kChunk - 1]);
               };
-              float y[kPair ? 1 : kCols];
-#pragma unroll
-              for (int k = 0; !kPair && k < kCols; k += kChunk) load(y + k, other0 + k);
-#pragma unroll
-              for (int k = 0; k < kCols; k += kChunk) load(x + k, col0 + k);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; !kPair && k < kCols; k += kChunk) scores(y + k, other0 + k);
-#pragma unroll
-              for (int k = 0; k < kCols; k += kChunk) scores(x + k, col0 + k);
-              const bool raise = (top - ref) * cc > kTau;
-              if (i == 0) {
-                ref = top == kNegInf ? 0.f : top;
-              } else if (__any_sync(0xffffffffu, raise && live)) {
+              // O and l follow a new reference.
+              auto rescale = [&](float alpha) -> bool {
                 if (!kPair && !warp_wait(&sm->pv_done, (pv_base + i - 1) & 1, abort_flag)) return false;
                 tc_fence_after();
-                const float alpha = raise ? ex2_approx((ref - top) * cc) : 1.f;
-                if (raise) ref = top;
                 l *= alpha;
 #pragma unroll
                 for (int k = 0; k < kOCols; k += 16) {
@@ -617,40 +645,112 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
                   for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
                   tmem_st16(t_o + k, o);
                 }
-              }
-              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                return true;
+              };
+              // P = 2^(x cc + lift - ref cc) in one operation where the product is small enough for the sum to keep the
+              // fraction; else the differences first
+              float bias = 0.f;
+              bool far = false;
+              auto set_bias = [&] {
+                far = fabsf(ref * cc) > kFar;
+                if (__any_sync(0xffffffffu, far)) {
+                  const float by = far ? ref : 0.f;
 #pragma unroll
-              for (int k = 0; k < kCols; k += kChunk) {
-                uint32_t h[kChunk / 2];
+                  for (int j = 0; j < kCols; ++j) x[j] -= by;
+                }
+                bias = far ? kLift : kLift - ref * cc;
+              };
+              float2 sum[2];
+              auto weigh = [&] {
+                sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int j = 0; j < kChunk; j += 4) {
-                  float2 d[2];
+                for (int k = 0; k < kCols; k += kChunk) {
+                  uint32_t h[kChunk / 2];
 #pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    d[e] = add_f32x2(make_float2(x[k + j + 2 * e], x[k + j + 2 * e + 1]), make_float2(-ref, -ref));
-                    if constexpr (kRows)
-                      d[e] = add_f32x2(d[e], make_float2(kLift, kLift));
-                    else
-                      d[e] = fma_f32x2(d[e], make_float2(cc, cc), make_float2(kLift, kLift));
-                    d[e].x = ex2_approx(d[e].x);
-                    d[e].y = ex2_approx(d[e].y);
-                    h[j / 2 + e] = pack_f16x2(d[e].x, d[e].y);
+                  for (int j = 0; j < kChunk; j += 4) {
+                    float2 d[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                      const float2 xx = make_float2(x[k + j + 2 * e], x[k + j + 2 * e + 1]);
+                      if constexpr (kRows)
+                        d[e] = add_f32x2(xx, make_float2(bias, bias));
+                      else
+                        d[e] = fma_f32x2(xx, make_float2(cc, cc), make_float2(bias, bias));
+                      d[e].x = ex2_approx(d[e].x);
+                      d[e].y = ex2_approx(d[e].y);
+                      h[j / 2 + e] = pack_f16x2(d[e].x, d[e].y);
+                    }
+                    if constexpr (kRows) {
+                      const float4 v = *reinterpret_cast<const float4*>(iv + col0 + k + j);
+                      sum[0] = fma_f32x2(d[0], make_float2(v.x, v.y), sum[0]);
+                      sum[1] = fma_f32x2(d[1], make_float2(v.z, v.w), sum[1]);
+                    } else {
+                      sum[0] = add_f32x2(sum[0], d[0]);
+                      sum[1] = add_f32x2(sum[1], d[1]);
+                    }
                   }
-                  if constexpr (kRows) {
-                    const float4 v = *reinterpret_cast<const float4*>(iv + col0 + k + j);
-                    sum[0] = fma_f32x2(d[0], make_float2(v.x, v.y), sum[0]);
-                    sum[1] = fma_f32x2(d[1], make_float2(v.z, v.w), sum[1]);
-                  } else {
-                    sum[0] = add_f32x2(sum[0], d[0]);
-                    sum[1] = add_f32x2(sum[1], d[1]);
+                  if constexpr (kChunk == 32)
+                    tmem_st16(t_p + k / 2, h);
+                  else
+                    tmem_st8(t_p + k / 2, h);
+                }
+              };
+              float y[kPair ? 1 : kCols];
+#pragma unroll
+              for (int k = 0; !kPair && k < kCols; k += kChunk) load(y + k, other0 + k);
+#pragma unroll
+              for (int k = 0; k < kCols; k += kChunk) load(x + k, col0 + k);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; !kPair && k < kCols; k += kChunk) scores(y + k, other0 + k), raise_top(y + k);
+#pragma unroll
+              for (int k = 0; k < kCols; k += kChunk) scores(x + k, col0 + k);
+              if (!kPair || kRows || i == 0) {
+#pragma unroll
+                for (int k = 0; k < kCols; k += kChunk) raise_top(x + k);
+                if (i == 0) {
+                  ref = top == kNegInf ? 0.f : top;
+                } else {
+                  const bool raise = (top - ref) * cc > kTau;
+                  if (__any_sync(0xffffffffu, raise && live)) {
+                    const float alpha = raise ? ex2_approx((ref - top) * cc) : 1.f;
+                    if (raise) ref = top;
+                    if (!rescale(alpha)) return false;
                   }
                 }
-                if constexpr (kChunk == 32)
-                  tmem_st16(t_p + k / 2, h);
-                else
-                  tmem_st8(t_p + k / 2, h);
               }
-              l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+              set_bias();
+              if constexpr (kPair && !kRows) {
+                // No maximum is taken: 128 weights of scores up to the reference sum to 2^14 at most.  Where they sum to
+                // more than 2^15 (one past the reference by more than 8 does), the reference moves and they are weighed
+                // again.
+                for (bool again = false;; again = true) {
+                  weigh();
+                  const float add = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                  if (i == 0 || again || !__any_sync(0xffffffffu, live && !(add <= 32768.f))) {
+                    l += add;
+                    break;
+                  }
+                  top = kNegInf;
+#pragma unroll
+                  for (int k = 0; k < kCols; k += kChunk) raise_top(x + k);
+                  const float step = far ? top : top - ref;
+                  const bool raise = step * cc > 0.f;
+                  if (!rescale(raise ? ex2_approx(-step * cc) : 1.f)) return false;
+                  if (raise) {
+                    ref = far ? ref + top : top;
+                    const bool now = far || fabsf(ref * cc) > kFar;
+                    const float by = now ? top : 0.f;
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) x[j] -= by;
+                    far = now;
+                    bias = far ? kLift : kLift - ref * cc;
+                  }
+                }
+              } else {
+                weigh();
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+              }
               tmem_st_wait();
               tc_fence_before();
             }
@@ -816,99 +916,99 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
     }
   } else if (warp < 12) {
     fewer_registers<kConvertRegs>();
-    // ------------------------------------------------ codes to f16 tiles --
+    // ---------------------------------------------- V's codes to f16 tiles --
     // A thread takes eight codes of every eighth (hd 64: sixteenth) row: 16 bytes of f16 at a place of the swizzled row
     // that is the same each time, and the quarters of a warp meet every bank once.
     const int tid = threadIdx.x - 256;
     constexpr int kLanes = kHd / 8, kRowsAStep = 128 / kLanes, kSteps = kTile / kRowsAStep;
     const int key0 = tid / kLanes, ch = tid % kLanes;
+    const uint32_t from = kHd == 128 ? key0 * 128 + (((ch / 2) ^ (key0 % 8)) << 4) + (ch % 2) * 8
+                                     : key0 * 64 + (((ch / 2) ^ ((key0 / 2) % 4)) << 4) + (ch % 2) * 8;
     const uint32_t to = (ch / 8) * (kTile * 128) + key0 * 128 + (((ch % 8) ^ (key0 % 8)) << 4);
-    uint32_t f = 0, rs = 0, raw_phase = 0, fs = 0, f_phase = 1, tile_no = 0;
+    uint32_t done = 0, vs = 0, v_phase = 0, fs = 0, f_phase = 1;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
       const Item* it = get_item(n);
       if (it == nullptr) break;
-      const int tiles = it->tile_hi - it->tile_lo, left = it->keys - it->tile_lo * kTile;
-      const bool pair = it->form == kFormPair;
+      const int tiles = it->tile_hi - it->tile_lo;
+      int valid = it->keys - it->tile_lo * kTile;
       drop_item(n);
-      for (int at = 0; at < 2 * tiles; ++at, ++f) {
-        bool is_v;
-        const int valid = left - tile_at(at, tiles, pair, &is_v) * kTile;
-        if (!warp_wait(&sm->raw_full[rs], raw_phase, abort_flag) ||
-            (f >= L::kSlots && !warp_wait(&sm->f_empty[fs], f_phase, abort_flag))) {
-          ok = false;
-          break;
+      for (int i = 0; i < tiles; ++i, ++done, valid -= kTile) {
+        ok = false;
+        if (!warp_wait(&sm->v_full[vs], v_phase, abort_flag)) break;
+        if constexpr (kRows) {  // past the end: one, so that a stale scale cannot turn a zero weight into a NaN
+          const float a = tid < valid ? sm->raw_scl[vs][0][tid] : 1.f, b = tid < valid ? sm->raw_scl[vs][1][tid] : 1.f;
+          const int ss = done % L::kScls;
+          float* two = reinterpret_cast<float*>(&sm->scl_k[ss][tid / 2]) + tid % 2;
+          two[0] = a;
+          two[2] = lg2_approx(b);
+          sm->scl_v[ss][tid] = 1.f / b;
+          warp_arrive(&sm->scl_full[ss]);
         }
-        const uint8_t* src = smem + L::kOffRaw + rs * L::kRaw + tid * 8;
+        if (done >= L::kFs && !warp_wait(&sm->f_empty[fs], f_phase, abort_flag)) break;
+        const uint8_t* src = smem + L::kOffV + vs * L::kRaw + from;
         uint8_t* dst = smem + L::kOffF + fs * L::kF + to;
-        if constexpr (kRows) {
-          if (!is_v) {  // past the end: one, so that a stale scale cannot turn a zero weight into a NaN
-            const float a = tid < valid ? sm->raw_scl[rs][0][tid] : 1.f, b = tid < valid ? sm->raw_scl[rs][1][tid] : 1.f;
-            const int ss = tile_no % 3;
-            float* two = reinterpret_cast<float*>(&sm->scl_k[ss][tid / 2]) + tid % 2;
-            two[0] = a;
-            two[2] = lg2_approx(b);
-            sm->scl_v[ss][tid] = 1.f / b;
-            warp_arrive(&sm->scl_full[ss]);
-            ++tile_no;
-          }
-        }
 #pragma unroll
-        for (int i = 0; i < kSteps; i += 8) {
+        for (int k = 0; k < kSteps; k += 8) {
           uint2 x[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const uint2*>(src + (i + j) * 1024);
+          for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const uint2*>(src + (k + j) * 1024);
           if (valid < kTile) {  // rows past the end: zeros
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              if (key0 + (i + j) * kRowsAStep >= valid) x[j] = make_uint2(0, 0);
+              if (key0 + (k + j) * kRowsAStep >= valid) x[j] = make_uint2(0, 0);
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(dst + (i + j) * kRowsAStep * 128) = to_f16(x[j]);
+          for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(dst + (k + j) * kRowsAStep * 128) = to_f16(x[j]);
         }
         fence_proxy_async_smem();
         warp_arrive(&sm->f_full[fs]);
-        warp_arrive(&sm->raw_empty[rs]);
-        if (++rs == L::kRaws) rs = 0, raw_phase ^= 1;
-        if (++fs == L::kSlots) fs = 0, f_phase ^= 1;
+        warp_arrive(&sm->v_empty[vs]);
+        if (++vs == L::kVs) vs = 0, v_phase ^= 1;
+        if (++fs == L::kFs) fs = 0, f_phase ^= 1;
+        ok = true;
       }
     }
   } else {
     fewer_registers<kIssueRegs>();
     if (warp == 12) {
       // ------------------------------------------------ matrix products --
-      constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, kTile, 128);  // f16: Q (K-major) x K (K-major)
+      constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, kTile, 128);  // E4M3: Q (K-major) x K (K-major)
       constexpr uint32_t idesc_pv = make_idesc(0, 0, 0, 1, kHd, 128);    // f16: P (TMEM) x V (MN-major)
       const bool leader = elect_one();
-      const uint32_t qb = smem_u32(smem), fb = qb + L::kOffF;
-      uint32_t f = 0, p_phase = 0, worked = 0;
+      const uint32_t qb = smem_u32(smem), kb = qb + L::kOffK, fb = qb + L::kOffF;
+      uint32_t at = 0, p_phase = 0, worked = 0;  // at: tiles before this item's
       bool ok = true;
-      auto wait_f = [&](uint32_t at) { return warp_wait(&sm->f_full[at % L::kSlots], (at / L::kSlots) & 1, abort_flag); };
+      auto wait_k = [&](uint32_t t) { return warp_wait(&sm->k_full[t % L::kKs], (t / L::kKs) & 1, abort_flag); };
+      auto wait_v = [&](uint32_t t) { return warp_wait(&sm->f_full[t % L::kFs], (t / L::kFs) & 1, abort_flag); };
       auto wait_p = [&](int buf) {
         const bool done = warp_wait(&sm->p_full[buf], (p_phase >> buf) & 1, abort_flag);
         p_phase ^= 1u << buf;
         return done;
       };
-      auto issue_qk = [&](int q, int buf, uint32_t at) {  // S[buf] = Q[q] K^T
+      auto issue_qk = [&](int q, int buf, uint32_t t) {  // S[buf] = Q[q] K^T, both terms of Q
         tc_fence_after();
-        const uint32_t a = qb + q * L::kQ, b = fb + (at % L::kSlots) * L::kF;
+        const uint32_t a = qb + q * L::kQ, b = kb + (t % L::kKs) * L::kRaw;
 #pragma unroll
-        for (int kk = 0; kk < kHd / 16; ++kk) {
-          const uint32_t off = (kk / 4) * (kTile * 128) + (kk % 4) * 32;
-          mma_f16_ss_if(leader, tmem + kTS + buf * 128, make_sdesc(a + off, 16, 1024, SWIZZLE_128B),
-                        make_sdesc(b + off, 16, 1024, SWIZZLE_128B), idesc_qk, kk > 0 ? 1u : 0u);
+        for (int term = 0; term < 2; ++term) {
+#pragma unroll
+          for (int kk = 0; kk < kHd / 32; ++kk)
+            mma_f8_ss_if(leader, tmem + kTS + buf * 128,
+                         make_sdesc(a + term * (kHd == 128 ? kTile * 128 : 64) + kk * 32, 16, 1024, SWIZZLE_128B),
+                         make_sdesc(b + kk * 32, 16, 8 * kHd, L::kSwizzle), idesc_qk, term + kk > 0 ? 1u : 0u);
         }
         tc_commit_if(leader, &sm->s_full[buf]);
       };
-      auto issue_pv = [&](uint32_t t_o, uint32_t t_p, uint32_t at, bool fresh) {  // O += P V
+      auto issue_pv = [&](uint32_t t_o, uint32_t t_p, uint32_t t, bool fresh) {  // O += P V
         tc_fence_after();
-        const uint32_t b = fb + (at % L::kSlots) * L::kF;
+        const uint32_t b = fb + (t % L::kFs) * L::kF;
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
           mma_f16_ts_if(leader, tmem + t_o, tmem + t_p + kk * 8,
                         make_sdesc(b + kk * 2048, kTile * 128, 1024, SWIZZLE_128B), idesc_pv, (fresh && kk == 0) ? 0u : 1u);
       };
-      auto release = [&](uint32_t at) { tc_commit_if(leader, &sm->f_empty[at % L::kSlots]); };
+      auto free_k = [&](uint32_t t) { tc_commit_if(leader, &sm->k_empty[t % L::kKs]); };
+      auto free_v = [&](uint32_t t) { tc_commit_if(leader, &sm->f_empty[t % L::kFs]); };
       for (uint32_t n = 0; ok; ++n) {
         const Item* it = get_item(n);
         if (it == nullptr) break;
@@ -917,71 +1017,70 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
         drop_item(n);
         if (tiles == 0) continue;
         ok = false;
-        if (!warp_wait(&sm->q_full, worked++ & 1, abort_flag) || !wait_f(f)) break;
+        if (!warp_wait(&sm->q_full, worked++ & 1, abort_flag) || !wait_k(at)) break;
         int i = 0;
         if (pair) {
-          issue_qk(0, 0, f);
-          issue_qk(1, 1, f);
-          release(f);
+          issue_qk(0, 0, at);
+          issue_qk(1, 1, at);
+          free_k(at);
           if (tiles == 1) tc_commit_if(leader, &sm->q_empty);
           for (; i < tiles; ++i) {
-            const uint32_t fv = f + 2 * i + 1, fk = fv + 1;
+            const uint32_t t = at + i;
             const bool last = i + 1 == tiles;
-            if (!wait_f(fv) || !wait_p(0)) break;
-            issue_pv(kTO, kTS, fv, i == 0);
+            if (!wait_v(t) || !wait_p(0)) break;
+            issue_pv(kTO, kTS, t, i == 0);
             if (last) {
               tc_commit_if(leader, &sm->o_full[0]);
             } else {
-              if (!wait_f(fk)) break;
-              issue_qk(0, 0, fk);
+              if (!wait_k(t + 1)) break;
+              issue_qk(0, 0, t + 1);
             }
             if (!wait_p(1)) break;
-            issue_pv(kTO + 128, kTS + 128, fv, i == 0);
-            release(fv);
+            issue_pv(kTO + 128, kTS + 128, t, i == 0);
+            free_v(t);
             if (last) {
               tc_commit_if(leader, &sm->o_full[1]);
             } else {
-              issue_qk(1, 1, fk);
-              release(fk);
+              issue_qk(1, 1, t + 1);
+              free_k(t + 1);
               if (i + 2 == tiles) tc_commit_if(leader, &sm->q_empty);
             }
           }
         } else {
-          // places: K0 at f, K1 at f + 1, V0, K2, V1, K3 ..
-          issue_qk(0, 0, f);
-          release(f);
+          issue_qk(0, 0, at);
+          free_k(at);
           if (tiles > 1) {
-            if (!wait_f(f + 1)) break;
-            issue_qk(0, 1, f + 1);
-            release(f + 1);
+            if (!wait_k(at + 1)) break;
+            issue_qk(0, 1, at + 1);
+            free_k(at + 1);
           }
           if (tiles <= 2) tc_commit_if(leader, &sm->q_empty);
           for (; i < tiles; ++i) {
             const int buf = i & 1;
-            const uint32_t fv = f + (i + 1 < tiles ? 2 * i + 2 : 2 * i + 1);
-            if (!wait_f(fv) || !wait_p(buf)) break;
-            issue_pv(kTO, kTO + 128 + buf * 64, fv, i == 0);
+            const uint32_t t = at + i;
+            if (!wait_v(t) || !wait_p(buf)) break;
+            issue_pv(kTO, kTO + 128 + buf * 64, t, i == 0);
             tc_commit_if(leader, &sm->pv_done);
-            release(fv);
+            free_v(t);
             if (i + 1 == tiles) tc_commit_if(leader, &sm->o_full[0]);
             if (i + 2 < tiles) {
-              if (!wait_f(fv + 1)) break;
-              issue_qk(0, buf, fv + 1);
-              release(fv + 1);
+              if (!wait_k(t + 2)) break;
+              issue_qk(0, buf, t + 2);
+              free_k(t + 2);
               if (i + 3 == tiles) tc_commit_if(leader, &sm->q_empty);
             }
           }
         }
         if (i < tiles) break;
-        f += 2 * tiles;
+        at += tiles;
         ok = true;
       }
       if (leader) tc_commit(&sm->final_mma);
       __syncwarp();
       warp_wait(&sm->final_mma, 0, nullptr);
     } else if (warp == 13) {
-      // --------------------------------------------- copies of raw tiles --
-      uint32_t raw = 0;
+      // ----------------------------------------------------- copies of tiles --
+      uint32_t k_done = 0, v_done = 0;  // tiles copied
       bool ok = true;
       const int chunk_shift = min(p.page_shift, 7);  // keys a copy
       const int chunks = kTile >> chunk_shift, in_page = (1 << p.page_shift) - 1;
@@ -1000,57 +1099,62 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_kernel(const __grid_consta
           return tile < tile_hi && lane < chunks && key < keys ? __ldg(table + (key >> p.page_shift)) : 0;
         };
         int even = fetch(tile_lo), odd = fetch(tile_lo + 1), next = fetch(tile_lo + 2);  // by the tile's number in the item
-        for (int at = 0; at < 2 * tiles; ++at, ++raw) {
+        for (int at = 0; at < 2 * tiles; ++at) {
           bool is_v;
           const int t = tile_at(at, tiles, pair, &is_v), tile = tile_lo + t;
-          const int rs = raw % L::kRaws;
           const int valid = min(kTile, keys - tile * kTile);
           int block = (t & 1) ? odd : even;
           if (block < 0 || block >= p.num_blocks) {
             atomicOr(&g_status_ragged, FP8MLA_DEV_BAD_PAGE);
             block = 0;
           }
-          if (raw >= L::kRaws && !warp_wait(&sm->raw_empty[rs], (raw / L::kRaws - 1) & 1, abort_flag)) {
+          const uint32_t c = is_v ? v_done : k_done, ring = is_v ? L::kVs : L::kKs, slot = c % ring;
+          uint64_t* full = is_v ? &sm->v_full[slot] : &sm->k_full[slot];
+          uint64_t* empty = is_v ? &sm->v_empty[slot] : &sm->k_empty[slot];
+          if (c >= ring && !warp_wait(empty, (c / ring - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(&sm->raw_full[rs], static_cast<uint32_t>(valid) * kHd);
+          if (lane == 0)  // whole pages, or 128 keys of one
+            mbar_arrive_expect_tx(full, static_cast<uint32_t>(((valid - 1) >> chunk_shift) + 1) * (kHd << chunk_shift));
           __syncwarp();
-          const long long line = ((static_cast<long long>(block) * p.h_kv + head) << p.page_shift) +
-                                 ((tile * kTile + first) & in_page);
+          const int row = ((block * p.h_kv + head) << p.page_shift) + ((tile * kTile + first) & in_page);
           if (lane < chunks && first < valid)
-            bulk_load(smem + L::kOffRaw + rs * L::kRaw + first * kHd, (is_v ? p.v : p.k) + line * kHd,
-                      static_cast<uint32_t>(min(1 << chunk_shift, valid - first)) * kHd, &sm->raw_full[rs]);
+            tma_load_3d(smem + (is_v ? L::kOffV : L::kOffK) + slot * L::kRaw + first * kHd, is_v ? &tm_v : &tm_k, full, 0,
+                        row, 0);
           if constexpr (kRows) {
-            if (!is_v) {  // scales of four keys a lane
+            if (is_v) {  // scales of four keys a lane
               const int key = lane * 4;
               const int from = __shfl_sync(0xffffffffu, block, key >> chunk_shift);
               const long long at4 = ((static_cast<long long>(from) * p.h_kv + head) << p.page_shift) +
                                     ((tile * kTile + key) & in_page);
               if (key < valid) {
-                cp_async16(smem_u32(&sm->raw_scl[rs][0][key]), p.k_scale + at4, 16u);
-                cp_async16(smem_u32(&sm->raw_scl[rs][1][key]), p.v_scale + at4, 16u);
+                cp_async16(smem_u32(&sm->raw_scl[slot][0][key]), p.k_scale + at4, 16u);
+                cp_async16(smem_u32(&sm->raw_scl[slot][1][key]), p.v_scale + at4, 16u);
               }
+              cp_async_mbar_arrive(full);
             }
-            cp_async_mbar_arrive(&sm->raw_full[rs]);
           }
-          if (is_v) {  // the tile is done: its place takes the one after the next
+          if (!is_v) {
+            ++k_done;
+          } else {  // the tile is done: its place takes the one after the next
             if (t & 1)
               odd = next;
             else
               even = next;
             next = fetch(tile + 3);
+            ++v_done;
           }
         }
       }
       if constexpr (kRows) cp_async_wait_all();  // this lane's copies have landed before the CTA can exit
-      for (uint32_t j = raw > L::kRaws ? raw - L::kRaws : 0; j < raw; ++j)
-        warp_wait(&sm->raw_full[j % L::kRaws], (j / L::kRaws) & 1, nullptr);
+      for (uint32_t j = k_done > L::kKs ? k_done - L::kKs : 0; j < k_done; ++j)
+        warp_wait(&sm->k_full[j % L::kKs], (j / L::kKs) & 1, nullptr);
+      for (uint32_t j = v_done > L::kVs ? v_done - L::kVs : 0; j < v_done; ++j)
+        warp_wait(&sm->v_full[j % L::kVs], (j / L::kVs) & 1, nullptr);
     } else if (warp == 14) {
       // ------------------------------------------------- the share's items --
-      if (unit >= sm->plan.units) sm->plan.hi = sm->plan.lo;
-      __syncwarp();
-      Walk walk(p, sm->plan);
+      Walk walk(sm->plan, unit);
       Item it;
       bool more = true;
       for (uint32_t n = 0; more; ++n) {
@@ -1276,7 +1380,7 @@ long long most_work(long long tokens, long long segs, int h_kv, int group, long 
 
 Space lay_out(long long work, long long tokens, int segs, int h_q, int group, int hd, bool joined) {
   Space s;
-  s.grid = static_cast<int>(std::max(1ll, std::min<long long>(device_sms(), work / (kPairFixed + 2 * kPairTile))));
+  s.grid = static_cast<int>(std::max(1ll, std::min<long long>(device_sms(), work / (kLeast))));
   s.slot_rows = static_cast<int>(std::min<long long>(kItemRows, std::max(1ll, tokens * group)));
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -1315,8 +1419,37 @@ void use(Params* p, const Space& s, void* workspace) {
   p->slot_rows = s.slot_rows;
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// View {hd, rows, 1} of a cache as rows of codes; box = a page's rows, 128 at most.
+bool encode_rows(CUtensorMap* map, const void* base, int hd, long long rows, int page) {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(rows), 1};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(rows) * hd};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(hd), static_cast<cuuint32_t>(std::min(page, kTile)), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int kHd, bool kRows>
 cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
+  CUtensorMap tk, tv;
+  const long long rows = (static_cast<long long>(p.num_blocks) * p.h_kv) << p.page_shift;
+  if (!encode_rows(&tk, p.k, kHd, rows, 1 << p.page_shift) || !encode_rows(&tv, p.v, kHd, rows, 1 << p.page_shift))
+    return cudaErrorInvalidValue;
   constexpr size_t smem = smem_bytes<kHd, kRows>();
   static_assert(smem <= 232448, "the tiles fit in shared memory");
   static std::atomic<uint64_t> configured{0};
@@ -1330,7 +1463,7 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
                                                    static_cast<int>(smem));
   });
   if (e != cudaSuccess) return e;
-  return launch_dependent(ragged_kernel<kHd, kRows>, dim3(grid), dim3(kThreads), smem, stream, p);
+  return launch_dependent(ragged_kernel<kHd, kRows>, dim3(grid), dim3(kThreads), smem, stream, tk, tv, p);
 }
 
 cudaError_t launch_any(const Params& p, int hd, int scale_rows, int grid, cudaStream_t stream) {
@@ -1342,6 +1475,7 @@ bool cache_ok(const RaggedCache& c, int h_kv, int* page_shift) {
   int shift = 4;
   while (shift < 9 && (1 << shift) != c.page_size) ++shift;
   if (shift == 9 || c.num_blocks < 1) return false;  // 16, 32, 64, 128 or 256 keys a page
+  if (((static_cast<long long>(c.num_blocks) * h_kv) << shift) >= (1ll << 31)) return false;  // rows: copies' coordinates
   *page_shift = shift;
   if (c.k == nullptr || c.v == nullptr || c.k_scale == nullptr || c.v_scale == nullptr) return false;
   const uintptr_t need = c.scale_rows ? 16 : 4;
