@@ -17,8 +17,8 @@
 //   up to 128 rows: one stream, S in two buffers by tile parity, and both softmax warpgroups share a tile's columns.
 //   up to 32 rows: the same with the rows in all four quarters of the lanes, each with P for its own 32 keys of a tile
 //     (zero for the others) and a reference of its own: eight warps share the softmax, the quarters are summed at the end.
-// Warps: 0-3 and 4-7 the two softmax warpgroups, 8-11 turn V into f16, 12 issues the products, 13 copies tiles (one TMA
-// copy per page and operand), 14 tells the others the share's items, 15 fills rows of no sequence.
+// Warps: 0-3 and 4-7 the two softmax warpgroups, 8-11 lay out Q and turn V into f16, 12 issues the products, 13 and 15 copy tiles
+// of K and of V (one TMA copy a page), 14 finds the CTA's share, tells the others its items and fills rows of no sequence.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -39,7 +39,7 @@ namespace ragged {
 constexpr int kTile = 128;      // keys a tile, rows a stream
 constexpr int kItemRows = 256;  // rows an item
 constexpr int kThreads = 512;
-constexpr int kSoftmaxRegs = 192, kConvertRegs = 64, kIssueRegs = 64;  // registers a thread of the warpgroups
+constexpr int kSoftmaxRegs = 184, kConvertRegs = 72, kIssueRegs = 72;  // registers a thread of the warpgroups
 constexpr float kLift = 7.f;    // P = 2^(score - reference + 7): 2^15 at most in f16, normal down to 2^-21 of the largest
 constexpr float kFar = 1048576.f;  // 2^20 in log2 units: up to here the lift and the difference keep their fraction
 constexpr float kTau = 8.f;     // the reference moves when a score passes it by more
@@ -80,6 +80,7 @@ struct Params {
   long long q_tok, q_head, o_tok, o_head;
   List list[2];
   FastDiv group;
+  unsigned long long per_unit;  // 2^64 / grid
   float softmax_scale;
   int joined, tokens, h_q, h_kv, num_blocks, page_shift, slot_rows, fill_out, fill_lse, q_len;
 };
@@ -140,129 +141,6 @@ __device__ __forceinline__ int cut_at(int off, int len, bool pair, int tiles, in
   return 2 * t < tiles ? 0 : len;
 }
 
-struct Plan {
-  Seg g;  // where this share begins: the segment, the item and how far into it
-  int seg, head, rt, off;
-  int units;
-  long long lo, hi;  // the share
-  long long sums[kThreads / 32];
-};
-
-// The share of CTA `unit`; the threads of the block together.
-__device__ __forceinline__ void make_plan(const Params& p, Plan* plan, int unit) {
-  const int n = p.list[0].n + p.list[1].n;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  uint32_t bad = 0;
-  long long mine = 0;
-  Seg g = {};
-  for (int s = threadIdx.x; s < n; s += kThreads) {
-    g = read_seg(p, s, &bad);
-    mine += g.head * p.h_kv;
-  }
-  if (bad && unit == 0) atomicOr(&g_status_ragged, bad);
-  auto scan = [&](long long x, long long* all) {  // sum of the threads before this one, and of all
-    long long s = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    if (lane == 31) plan->sums[warp] = s;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const long long y = plan->sums[w];
-      if (w < warp) before += y;
-      total += y;
-    }
-    *all = total;
-    return before + s - x;
-  };
-  long long total;
-  long long at = scan(mine, &total);
-  int units, few;
-  long long raw[2];
-  if (total < (1 << 24)) {  // 32-bit division
-    const uint32_t t = static_cast<uint32_t>(total);
-    units = static_cast<int>(max(1u, min(gridDim.x, t / kLeast)));
-    few = static_cast<int>(t / units / (3 * kPairTile));
-    raw[0] = t * unit / units;
-    raw[1] = t * (unit + 1) / units;
-  } else {
-    units = gridDim.x;
-    few = 4;
-    raw[0] = total * unit / units;
-    raw[1] = total * (unit + 1) / units;
-  }
-  few = max(1, min(4, few));
-  // one thread finds each end of the share in its segment
-  auto locate = [&](int s, long long from, long long len) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (raw[e] < from || raw[e] >= from + len) continue;
-      const long long in = raw[e] - from;
-      int h, rest;
-      if (in < (1ll << 31) && g.head < (1ll << 31)) {
-        h = static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(g.head));
-        rest = static_cast<int>(static_cast<uint32_t>(in) - static_cast<uint32_t>(h) * static_cast<uint32_t>(g.head));
-      } else {
-        h = static_cast<int>(in / g.head);
-        rest = static_cast<int>(min(in - h * g.head, 0x7FFFFFFFll));
-      }
-      int rt = min(rest / g.full, g.row_tiles - 1);
-      const bool last = rt == g.row_tiles - 1;
-      const int item = last ? g.last : g.full;
-      int off = cut_at(rest - rt * g.full, item, item == g.full && g.tiles > 0, g.tiles, few);
-      const long long to = from + h * g.head + static_cast<long long>(rt) * g.full + off;
-      if (e == 0) {
-        plan->lo = p.lo[unit] = to;
-        if (off == item) {  // the next item's beginning
-          off = 0;
-          if (++rt == g.row_tiles) rt = 0, ++h;
-        }
-        plan->g = g;
-        plan->seg = s;
-        plan->head = h;
-        plan->rt = rt;
-        plan->off = off;
-      } else {
-        plan->hi = to;
-      }
-    }
-  };
-  if (threadIdx.x == 0) {
-    plan->units = units;
-    if (total == 0) plan->lo = 0;
-    if (raw[1] >= total) plan->hi = total;
-    if (!p.joined) p.cuts[unit].valid = 0;
-    if (unit == units - 1) {
-      p.lo[units] = total;
-      *p.units = units;
-    }
-  }
-  if (n <= kThreads) {
-    if (p.joined && unit == 0 && static_cast<int>(threadIdx.x) < n) p.seg_at[threadIdx.x] = at;
-    locate(threadIdx.x, at, mine);
-  } else {
-    long long base = 0;
-    for (int s0 = 0; s0 < n; s0 += kThreads) {
-      __syncthreads();  // the sums have been read
-      const int s = s0 + static_cast<int>(threadIdx.x);
-      long long len = 0, all;
-      if (s < n) {
-        g = read_seg(p, s, &bad);
-        len = g.head * p.h_kv;
-      }
-      at = base + scan(len, &all);
-      base += all;
-      if (s < n && p.joined && unit == 0) p.seg_at[s] = at;
-      locate(s, at, len);
-    }
-  }
-  __syncthreads();
-}
-
 // One item of a share, or the part of it that lies in the share.
 struct Item {
   int list, seg, head, t0, row0, rows, keys, tile_lo, tile_hi;
@@ -274,60 +152,150 @@ constexpr int kFew = 32;                         // rows that lie in all quarter
 enum { kFormPair = 0, kFormOne = 1, kFormFew = 2 };
 constexpr int kDirect = -1, kPlane = -2;
 
-// The items of a share, one after the other.
+// Where a share is: the segment, the item, how far into it, and how much is left.
 struct Walk {
   Seg g;
-  int seg, head, rt, off, left;
+  int seg, head, rt, off;
+  long long left, hi;
   bool first;
-  __device__ __forceinline__ Walk(const Plan& plan, int unit) {
-    left = unit < plan.units ? static_cast<int>(min(plan.hi - plan.lo, 0x7FFFFFFFll)) : 0;
-    g = plan.g;
-    seg = plan.seg;
-    head = plan.head;
-    rt = plan.rt;
-    off = plan.off;
-    first = true;
-  }
-  __device__ __forceinline__ bool next(const Params& p, const Plan& plan, int unit, Item* it) {
-    if (left <= 0) return false;
-    const int n = p.list[0].n + p.list[1].n;
-    while (head == p.h_kv || g.head == 0) {
-      if (++seg >= n) return false;
-      uint32_t bad = 0;
-      g = read_seg(p, seg, &bad);
-      head = rt = 0;
-    }
-    const int len = rt == g.row_tiles - 1 ? g.last : g.full;
-    it->list = seg < p.list[0].n ? 0 : 1;
-    it->seg = it->list ? seg - p.list[0].n : seg;
-    it->head = head;
-    it->t0 = g.t0;
-    it->row0 = rt * kItemRows;
-    it->rows = min(kItemRows, g.rows - it->row0);
-    it->keys = g.keys;
-    it->form = it->rows > kTile ? kFormPair : (it->rows > kFew ? kFormOne : kFormFew);
-    const bool pair = it->form == kFormPair;
-    const int fixed = pair ? kPairFixed : kOneFixed, each = pair ? kPairTile : kOneTile;
-    it->tile_lo = off > 0 ? (off - fixed) / each : 0;
-    it->tile_hi = len - off <= left ? g.tiles : (off + left - fixed) / each;
-    const int slot = 2 * unit + (first ? 0 : 1);
-    const bool whole = it->tile_lo == 0 && it->tile_hi == g.tiles;
-    it->slot = !whole ? slot : (p.joined ? kPlane : kDirect);
-    it->end = false;
-    if (!p.joined && it->tile_lo == 0 && !whole && threadIdx.x % 32 == 0) {
-      const long long start = plan.hi - left;  // off is 0
-      p.cuts[unit] = Cut{start, start + len, 1, slot, head, g.t0, it->row0, it->rows};
-    }
-    left = len - off <= left ? left - (len - off) : 0;
-    first = false;
-    off = 0;
-    if (++rt == g.row_tiles) {
-      rt = 0;
-      ++head;
-    }
-    return true;
-  }
 };
+
+// The beginning of CTA `unit`'s share, by one warp; it is short, as its instructions come from memory in every launch.
+__device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk) {
+  const int n = p.list[0].n + p.list[1].n;
+  const int lane = threadIdx.x % 32;
+  uint32_t bad = 0;
+  int units = 1, few = 1;
+  long long total = 0, raw[2] = {0, 0};
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {  // the sum, then where the share's ends are
+    long long from = 0;
+#pragma unroll 1
+    for (int s0 = 0; s0 < n; s0 += 32) {
+      const int s = s0 + lane;
+      Seg g = {};
+      if (s < n) g = read_seg(p, s, &bad);
+      const long long len = g.head * p.h_kv;
+      long long sum = len;
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const long long at = from + sum - len;
+      from += __shfl_sync(0xffffffffu, sum, 31);
+      if (pass == 0) continue;
+      if (s < n && p.joined && unit == 0) p.seg_at[s] = at;  // the merge looks segments up
+#pragma unroll 1
+      for (int e = 0; e < 2; ++e) {
+        const long long want = e ? raw[1] : raw[0];
+        if (want < at || want >= at + len) continue;
+        long long in = want - at;
+        int h = 0;
+        while (in >= g.head) in -= g.head, ++h;
+        const int rest = static_cast<int>(min(in, 0x7FFFFFFFll));
+        int rt = min(rest / g.full, g.row_tiles - 1);
+        const int item = rt == g.row_tiles - 1 ? g.last : g.full;
+        int off = cut_at(rest - rt * g.full, item, item == g.full && g.tiles > 0, g.tiles, few);
+        const long long to = want - in + static_cast<long long>(rt) * g.full + off;
+        if (e) {
+          walk->hi = to;
+        } else {
+          if (off == item) {  // the next item's beginning
+            off = 0;
+            if (++rt == g.row_tiles) rt = 0, ++h;
+          }
+          walk->g = g;
+          walk->seg = s;
+          walk->head = h;
+          walk->rt = rt;
+          walk->off = off;
+          p.lo[unit] = to;
+          walk->left = to;  // for now
+        }
+      }
+      if (!p.joined && from > raw[1]) break;
+    }
+    if (pass == 1) break;
+    total = from;
+    if (total < (1 << 24)) {
+      const uint32_t t = static_cast<uint32_t>(total);
+      units = static_cast<int>(max(1u, min(gridDim.x, t / kLeast)));
+      few = static_cast<int>(t / units / (3 * kPairTile));
+      raw[0] = t * unit / units;
+      raw[1] = t * (unit + 1) / units;
+    } else {
+      units = gridDim.x;
+      few = 4;
+      raw[0] = __umul64hi(total * unit, p.per_unit);  // 2^64 / grid
+      raw[1] = __umul64hi(total * (unit + 1), p.per_unit);
+    }
+    few = max(1, min(4, few));
+    if (unit + 1 >= units) raw[1] = total;
+    if (unit >= units) raw[0] = total;
+    if (lane == 0) {
+      walk->left = raw[0];
+      walk->hi = total;
+      walk->first = true;
+      if (bad && unit == 0) atomicOr(&g_status_ragged, bad);
+      if (!p.joined) p.cuts[unit].valid = 0;
+      if (unit == units - 1) {
+        p.lo[units] = total;
+        *p.units = units;
+      }
+    }
+    __syncwarp();
+    if (raw[0] >= total) {
+      if (lane == 0 && unit < units) p.lo[unit] = raw[0];
+      if (!(p.joined && unit == 0)) break;
+    }
+  }
+  __syncwarp();
+  if (lane == 0) walk->left = walk->hi - walk->left;
+  __syncwarp();
+}
+
+// The next item of a share (one thread).
+__device__ __forceinline__ bool next_item(const Params& p, int unit, Walk* w, Item* it) {
+  const long long left = w->left;
+  if (left <= 0) return false;
+  const int n = p.list[0].n + p.list[1].n;
+  while (w->head == p.h_kv || w->g.head == 0) {
+    if (++w->seg >= n) return false;
+    uint32_t bad = 0;
+    w->g = read_seg(p, w->seg, &bad);
+    w->head = w->rt = 0;
+  }
+  const int rt = w->rt, off = w->off, tiles = w->g.tiles;
+  const int len = rt == w->g.row_tiles - 1 ? w->g.last : w->g.full;
+  const int row0 = rt * kItemRows, rows = min(kItemRows, w->g.rows - row0);
+  const int list = w->seg < p.list[0].n ? 0 : 1;
+  it->list = list;
+  it->seg = list ? w->seg - p.list[0].n : w->seg;
+  it->head = w->head;
+  it->t0 = w->g.t0;
+  it->row0 = row0;
+  it->rows = rows;
+  it->keys = w->g.keys;
+  it->form = rows > kTile ? kFormPair : (rows > kFew ? kFormOne : kFormFew);
+  const int fixed = rows > kTile ? kPairFixed : kOneFixed, each = rows > kTile ? kPairTile : kOneTile;
+  const int tile_lo = off > 0 ? (off - fixed) / each : 0;
+  const bool ends = len - off <= left;
+  const int tile_hi = ends ? tiles : (off + static_cast<int>(left) - fixed) / each;
+  const bool whole = tile_lo == 0 && tile_hi == tiles;
+  const int slot = 2 * unit + (w->first ? 0 : 1);
+  it->tile_lo = tile_lo;
+  it->tile_hi = tile_hi;
+  it->slot = !whole ? slot : (p.joined ? kPlane : kDirect);
+  if (!p.joined && tile_lo == 0 && !whole)
+    p.cuts[unit] = Cut{w->hi - left, w->hi - left + len, 1, slot, w->head, w->g.t0, row0, rows};
+  w->left = ends ? left - (len - off) : 0;
+  w->first = false;
+  w->off = 0;
+  w->rt = rt + 1 == w->g.row_tiles ? 0 : rt + 1;
+  if (w->rt == 0) ++w->head;
+  return true;
+}
 
 // ------------------------------------------------------------- the kernel --
 
@@ -349,20 +317,21 @@ struct Lay {
 };
 
 constexpr int kItems = 4;       // items told ahead
-constexpr int kItemWarps = 14;  // that are told
+constexpr int kItemWarps = 15;  // that are told
 
 template <int kHd, bool kRows>
 struct Control {
   using L = Lay<kHd, kRows>;
-  Plan plan;
   uint64_t k_full[L::kKs], k_empty[L::kKs], v_full[L::kVs], v_empty[L::kVs], f_full[L::kFs], f_empty[L::kFs];
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t q_full, q_empty, pv_done, xchg, scl_full[L::kScls], final_mma;
+  uint64_t q_full, q_seen, q_empty, pv_done, xchg, scl_full[L::kScls], final_mma;
   uint64_t item_full[kItems], item_empty[kItems];
   Item item[kItems];
+  Walk walk;
   uint32_t tmem_base, abort_flag;
-  float q_scale[2][kTile];  // (up to 32 rows: the second holds the quarters' references)
-  float row_l[2][kTile];
+  uint32_t sums_read;            // warps that are done with a few-row item's sums
+  int8_t q_exp[2][kTile];        // of Q's rows, by stream
+  float row_l[2][kTile], row_m[kTile];
   alignas(16) float4 scl_k[kRows ? L::kScls : 1][kRows ? kTile / 2 : 1];  // of two keys: K scales, log2 of V scales
   alignas(16) float scl_v[kRows ? L::kScls : 1][kRows ? kTile : 4];       // 1 / V scale
   alignas(16) float raw_scl[kRows ? L::kVs : 1][2][kRows ? kTile : 4];
@@ -378,22 +347,28 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
-
-// The tile of K or V that is copied at place `at` of an item's sequence of 2 T tiles, as the products take them: streams
-// of their own K0 V0 K1 V1 .., one stream K0 K1 V0 K2 V1 ..
-__device__ __forceinline__ int tile_at(int at, int tiles, bool pair, bool* is_v) {
-  if (pair) {
-    *is_v = at & 1;
-    return at >> 1;
+// Until *count has reached `want` (it only grows), with the limits of a bounded wait.
+__device__ __forceinline__ bool wait_count(volatile uint32_t* count, uint32_t want, volatile uint32_t* abort_flag) {
+  const uint64_t t0 = globaltimer_ns();
+  bool ok = true;
+  for (uint32_t it = 1; static_cast<int32_t>(*count - want) < 0; ++it) {
+    if ((it & 31u) != 0) continue;
+    if (*abort_flag) {
+      ok = false;
+      break;
+    }
+    if (it > kWaitMinPolls && globaltimer_ns() - t0 > *(volatile uint64_t*)&g_wait_limit_ns) {
+      *abort_flag = 1u;
+      atomicOr(&g_status_ragged, FP8MLA_DEV_WAIT_TIMEOUT);
+      ok = false;
+      break;
+    }
   }
-  if (at == 0 || at == 2 * tiles - 1) {
-    *is_v = at != 0;
-    return at == 0 ? 0 : tiles - 1;
-  }
-  *is_v = !(at & 1);
-  return (at & 1) ? (at + 1) >> 1 : (at >> 1) - 1;
+  __threadfence_block();
+  return __all_sync(0xffffffffu, ok);
 }
+
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // Smallest e with amax <= 448 * 2^e, from -60 on (what is smaller still makes no score).
 __device__ __forceinline__ int exponent_448(float amax) {
@@ -406,9 +381,9 @@ __device__ __forceinline__ int exponent_448(float amax) {
 // row's largest value on).  Where `quarters`, in all quarters of the lanes.  head_dim 128: a tile of 128-byte rows per
 // term; 64: both terms in one row.
 template <int kHd>
-__device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t* q_tile, float* q_scale, int row0,
+__device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t* q_tile, int8_t* q_exp, int row0,
                                        int first, int count, bool quarters, int lane) {
-  constexpr int kLanes = kHd / 16, kStep = 32 / kLanes, kFly = kHd == 128 ? 4 : 2;  // lanes a row, rows a pass, passes in flight
+  constexpr int kLanes = kHd / 16, kStep = 32 / kLanes, kFly = 2;  // lanes a row, rows a pass, passes in flight
   const int ch = lane % kLanes, sub = lane / kLanes;
   const int end = min(first + count, it.rows - row0);
   const int item_row = it.row0 + row0, head0 = it.head * static_cast<int>(p.group.d), t0 = it.t0;
@@ -454,7 +429,7 @@ __device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t*
           *reinterpret_cast<uint4*>(to + k * 32 * 128 + kLoTile + (((ch + kLoChunk) ^ (row % 8)) << 4)) =
               make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-        if (ch == 0) q_scale[row] = exp2i(e);
+        if (ch == 0) q_exp[row] = static_cast<int8_t>(e);
       }
     }
   }
@@ -499,21 +474,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm->item_full[i], 1);
       mbar_init(&sm->item_empty[i], kItemWarps);
     }
-    mbar_init(&sm->q_full, 8);
+    mbar_init(&sm->q_full, 4);  // converter warps
+    mbar_init(&sm->q_seen, 8);  // softmax warps: its exponents read
     mbar_init(&sm->q_empty, 1);
     mbar_init(&sm->pv_done, 1);
     mbar_init(&sm->xchg, 8);
     mbar_init(&sm->final_mma, 1);
     sm->abort_flag = 0;
+    sm->sums_read = 0;
     fence_barrier_init();
   }
   if (warp == 12) {
     tmem_alloc(&sm->tmem_base, 512);
     tmem_relinquish();
   }
+  // what the first steps need of the arguments, while the previous kernel ends
+  asm volatile("" ::"l"(p.list[0].starts), "l"(p.list[1].lens), "r"(p.page_shift), "l"(p.lo), "l"(p.q_tok), "l"(p.plane_o[1]));
   griddep_wait();  // inputs may come from the previous kernel in the stream
   griddep_launch_dependents();
-  make_plan(p, &sm->plan, unit);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -536,29 +514,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
     const float c0 = p.softmax_scale * kLog2e * (kRows ? 1.f : __ldg(p.k_scale));
     uint32_t s_phase = 0, o_phase = 0;  // a bit per barrier
-    uint32_t n = 0, worked = 0, pv_base = 0, tile_no = 0, xchgs = 0;
+    uint32_t worked = 0, pv_base = 0, tile_no = 0, xchgs = 0;
     int was = -1;
-    auto fetch_q = [&](const Item& it) {
-      if (it.form == kFormPair)
-        load_q<kHd>(p, it, smem + wg * L::kQ, sm->q_scale[wg], wg * kTile, w * 32, 32, false, lane);
-      else if (it.form == kFormOne)
-        load_q<kHd>(p, it, smem, sm->q_scale[0], 0, warp * 16, 16, false, lane);
-      else
-        load_q<kHd>(p, it, smem, sm->q_scale[0], 0, warp * 4, 4, true, lane);
-      fence_proxy_async_smem();
-      warp_arrive(&sm->q_full);
-    };
     auto exchange = [&]() -> bool {
       warp_arrive(&sm->xchg);
       return warp_wait(&sm->xchg, xchgs++ & 1, abort_flag);
     };
-    const Item* it = get_item(0);
-    if (it != nullptr && it->tile_hi > it->tile_lo) fetch_q(*it);
-    while (it != nullptr) {
+    for (uint32_t n = 0;; ++n) {
+      const Item* it = get_item(n);
+      if (it == nullptr) break;
       const int tiles = it->tile_hi - it->tile_lo, form = it->form;
       const bool pair = form == kFormPair, few = form == kFormFew;
       const int row = pair ? wg * kTile + r : (few ? lane : r);  // of the item
       const bool live = row < it->rows;
+      const bool busy = __any_sync(0xffffffffu, live);
       float ref = kNegInf, l = 0.f, cc = 1.f;
       if (tiles > 0) {
         if (!warp_wait(&sm->q_full, worked & 1, abort_flag)) break;
@@ -574,9 +543,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         was = form;
-        const float c = c0 * (live ? sm->q_scale[pair ? wg : 0][few ? lane : r] : 1.f);
+        const float c = c0 * (live ? exp2i(sm->q_exp[pair ? wg : 0][few ? lane : r]) : 1.f);
+        warp_arrive(&sm->q_seen);
         if (!kRows) cc = c;  // units of the reference to log2
-        const bool busy = __any_sync(0xffffffffu, live);
         int keys = it->keys - it->tile_lo * kTile;  // left
         auto steps = [&](auto which) {
           constexpr int kForm = decltype(which)::value;
@@ -773,25 +742,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           pv_base += tiles;
       }
-      // Q of the next item, while the last product runs.  Where another warp reads the rows' scales, all have to be
-      // done with those of this item.
-      const Item* next = get_item(n + 1);
-      const bool fetch = next != nullptr && next->tile_hi > next->tile_lo;
-      const bool late = few && tiles > 0 && fetch && next->form == kFormPair;  // the quarters' sums lie where its Q goes
-      if (!pair && tiles > 0) sm->row_l[wg][r] = l;
-      if ((!pair || tiles == 0 || (next != nullptr && next->form != kFormPair)) && !exchange()) break;
-      if (form == kFormOne && tiles > 0) l = sm->row_l[0][r] + sm->row_l[1][r];
-      if (tiles > 0) {
-        if (!warp_wait(&sm->q_empty, worked & 1, abort_flag)) break;
-        ++worked;
-      }
-      if (fetch && !late) fetch_q(*next);
+      if (tiles > 0) ++worked;
       const int os = pair ? wg : 0;
-      if (tiles > 0) {
-        if (!warp_wait(&sm->o_full[os], (o_phase >> os) & 1, abort_flag)) break;
+      auto wait_o = [&]() -> bool {
+        if (!warp_wait(&sm->o_full[os], (o_phase >> os) & 1, abort_flag)) return false;
         o_phase ^= pair ? 3u : 1u;
         tc_fence_after();
-      }
+        return true;
+      };
       // Results of four or 32 values of a row (of the item): rounded to the outputs, or as they are to the workspace.
       const int slot = it->slot;
       const float v_scale = kRows ? 1.f : __ldg(p.v_scale);
@@ -815,21 +773,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                               : p.slot_o + (static_cast<long long>(slot) * p.slot_rows + of_row) * kHd;
       };
       if (few && tiles > 0) {
-        if (wg == 0) sm->q_scale[1][r] = ref;
+        sm->row_l[wg][r] = l;
+        if (wg == 0) sm->row_m[r] = ref;
         if (!exchange()) break;
-        const float unit_of = cc;  // this thread's row is its lane's in every quarter
-        float m = kNegInf;
+        float m = kNegInf, lk[4];  // this thread's row is its lane's in every quarter
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float lk = sm->row_l[0][k * 32 + lane] + sm->row_l[1][k * 32 + lane];
-          if (!(lk == 0.f)) m = fmaxf(m, sm->q_scale[1][k * 32 + lane] * unit_of);
+          lk[k] = sm->row_l[0][k * 32 + lane] + sm->row_l[1][k * 32 + lane];
+          if (!(lk[k] == 0.f)) m = fmaxf(m, sm->row_m[k * 32 + lane] * cc);
         }
         float sum = 0.f, mine = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float lk = sm->row_l[0][k * 32 + lane] + sm->row_l[1][k * 32 + lane];
-          const float f = lk == 0.f ? 0.f : ex2_approx(sm->q_scale[1][k * 32 + lane] * unit_of - m);
-          sum += lk * f;
+          const float f = lk[k] == 0.f ? 0.f : ex2_approx(sm->row_m[k * 32 + lane] * cc - m);
+          sum += lk[k] * f;
           if (k == w) mine = f;
         }
         int head;
@@ -839,31 +796,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (slot == kDirect) mine *= v_scale / sum;
         const int out_row = threadIdx.x / 8, piece = threadIdx.x % 8;  // of 32 rows, of eight times four dims
         place_of(out_row, &head, &token);
-        float* quarters = reinterpret_cast<float*>(smem + L::kOffSum);  // [half][quarter][row][32], 16 bytes swizzled
-        for (int k = 0; k < kHd / 2; k += 32) {
-          uint32_t o[32];
-          tmem_ld32(lanes + kTO + wg * (kHd / 2) + k, o);
-          tmem_ld_wait();
-          float* to = quarters + ((wg * 4 + w) * kFew + lane) * 32;
-          if (live) {
+        // the quarters' sums [half][quarter][row][dims], 16 bytes swizzled: as many dims at a time as there is room for
+        const int rows = kHd == 128 && it->rows <= 16 ? 16 : 32, dims = 1024 / rows;
+        float* quarters = reinterpret_cast<float*>(smem + L::kOffSum);
+        if (!wait_o()) break;
+        bool ok = true;
+        for (int k0 = 0; ok && k0 < kHd / 2; k0 += dims) {
+          for (int k = 0; k < dims; k += 32) {
+            uint32_t o[32];
+            __syncwarp();
+            tmem_ld32(lanes + kTO + wg * (kHd / 2) + k0 + k, o);
+            tmem_ld_wait();
+            float* to = quarters + ((wg * 4 + w) * rows + lane) * dims + k;
+            if (live) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<float4*>(to + ((j ^ (lane % 8)) * 4)) =
-                  make_float4(__uint_as_float(o[4 * j]) * mine, __uint_as_float(o[4 * j + 1]) * mine,
-                              __uint_as_float(o[4 * j + 2]) * mine, __uint_as_float(o[4 * j + 3]) * mine);
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float4*>(to + ((j ^ (lane % 8)) * 4)) =
+                    make_float4(__uint_as_float(o[4 * j]) * mine, __uint_as_float(o[4 * j + 1]) * mine,
+                                __uint_as_float(o[4 * j + 2]) * mine, __uint_as_float(o[4 * j + 3]) * mine);
+            }
           }
-          if (!exchange()) break;
-          if (out_row < it->rows) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
+          ok = exchange();
+          if (ok && out_row < it->rows) {
+            for (int k = 0; k < 2 * dims; k += 32) {  // either half's dims
+              const int half = k >= dims ? 1 : 0, in = k - half * dims;
               float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const float4 b = *reinterpret_cast<const float4*>(
-                    quarters + ((half * 4 + q) * kFew + out_row) * 32 + ((piece ^ (out_row % 8)) * 4));
+                    quarters + ((half * 4 + q) * rows + out_row) * dims + in + ((piece ^ (out_row % 8)) * 4));
                 a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
               }
-              const int dim = half * (kHd / 2) + k + piece * 4;
+              const int dim = half * (kHd / 2) + k0 + in + piece * 4;
               if (slot == kDirect)
                 *reinterpret_cast<uint2*>(p.out + token * p.o_tok + head * p.o_head + dim) =
                     make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
@@ -871,11 +835,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<float4*>(row_at(out_row, head, token) + dim) = a;
             }
           }
-          if ((k + 32 < kHd / 2 || late) && !exchange()) break;  // read before the next are written
+          if (ok && k0 + dims < kHd / 2) ok = exchange();  // read before the next are written
         }
+        if (!ok) break;
         tc_fence_before();
-        if (late) fetch_q(*next);
-      } else if (__any_sync(0xffffffffu, live)) {
+        __syncwarp();
+        if (lane == 0) {
+          __threadfence_block();
+          atomicAdd(&sm->sums_read, 1u);
+        }
+      } else {
+        if (form == kFormOne && tiles > 0) {  // either warpgroup has half the keys' weights
+          sm->row_l[wg][r] = l;
+          if (!exchange()) break;
+          l = sm->row_l[0][r] + sm->row_l[1][r];
+          if (!exchange()) break;  // read before the next item's are written
+        }
+        if (tiles > 0 && !wait_o()) break;
         int head;
         long long token;
         place_of(row, &head, &token);
@@ -884,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live && (pair || (few ? warp == 0 : wg == 0))) put_sums(row, head, token, ref * cc, l);
         const float f = tiles > 0 ? v_scale / l : 0.f;
         const bool mine = live && (!few || w == 0);
-        for (int k = 0; k < dims; k += 32) {
+        for (int k = 0; busy && k < dims; k += 32) {
           uint32_t o[32] = {};
           __syncwarp();
           if (tiles > 0) {
@@ -911,8 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         tc_fence_before();
       }
-      drop_item(n++);
-      it = next;
+      drop_item(n);
     }
   } else if (warp < 12) {
     fewer_registers<kConvertRegs>();
@@ -925,12 +900,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t from = kHd == 128 ? key0 * 128 + (((ch / 2) ^ (key0 % 8)) << 4) + (ch % 2) * 8
                                      : key0 * 64 + (((ch / 2) ^ ((key0 / 2) % 4)) << 4) + (ch % 2) * 8;
     const uint32_t to = (ch / 8) * (kTile * 128) + key0 * 128 + (((ch % 8) ^ (key0 % 8)) << 4);
-    uint32_t done = 0, vs = 0, v_phase = 0, fs = 0, f_phase = 1;
+    uint32_t done = 0, vs = 0, v_phase = 0, fs = 0, f_phase = 1, worked = 0, sums = 0;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
       const Item* it = get_item(n);
       if (it == nullptr) break;
       const int tiles = it->tile_hi - it->tile_lo;
+      if (tiles > 0) {
+        // Q, once the products have left the one before, and the softmax has seen it (else it would miss a phase)
+        const int form = it->form, w = warp - 8;
+        if (worked > 0 && (!warp_wait(&sm->q_empty, (worked - 1) & 1, abort_flag) ||
+                           !warp_wait(&sm->q_seen, (worked - 1) & 1, abort_flag)))
+          break;
+        if (kHd == 128 && form == kFormPair && !wait_count(&sm->sums_read, sums, abort_flag)) break;  // they lie there
+        int8_t* q_exp = sm->q_exp[0];
+        if (form == kFormPair)
+          load_q<kHd>(p, *it, smem + (w / 2) * L::kQ, q_exp + (w / 2) * kTile, (w / 2) * kTile, (w % 2) * 64, 64, false,
+                      lane);
+        else
+          load_q<kHd>(p, *it, smem, q_exp, 0, w * (form == kFormOne ? 32 : 8), form == kFormOne ? 32 : 8,
+                      form == kFormFew, lane);
+        fence_proxy_async_smem();
+        warp_arrive(&sm->q_full);
+        ++worked;
+        if (form == kFormFew) sums += 8;
+      }
       int valid = it->keys - it->tile_lo * kTile;
       drop_item(n);
       for (int i = 0; i < tiles; ++i, ++done, valid -= kTile) {
@@ -1078,105 +1072,100 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (leader) tc_commit(&sm->final_mma);
       __syncwarp();
       warp_wait(&sm->final_mma, 0, nullptr);
-    } else if (warp == 13) {
-      // ----------------------------------------------------- copies of tiles --
-      uint32_t k_done = 0, v_done = 0;  // tiles copied
+    } else if (warp != 14) {
+      // -------------------------------------- copies of tiles: 13 K, 15 V --
+      const bool is_v = warp == 15;
+      const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+      const uint32_t ring = is_v ? L::kVs : L::kKs;
+      uint64_t* full = is_v ? sm->v_full : sm->k_full;
+      uint64_t* empty = is_v ? sm->v_empty : sm->k_empty;
+      uint8_t* tiles_at = smem + (is_v ? L::kOffV : L::kOffK);
+      const bool leader = elect_one();
+      if (leader) tma_prefetch_desc(map);
+      uint32_t done = 0, slot = 0, phase = 1;
       bool ok = true;
       const int chunk_shift = min(p.page_shift, 7);  // keys a copy
       const int chunks = kTile >> chunk_shift, in_page = (1 << p.page_shift) - 1;
-      const int first = lane << chunk_shift;
       for (uint32_t n = 0; ok; ++n) {
         const Item* it = get_item(n);
         if (it == nullptr) break;
-        const int tile_lo = it->tile_lo, tile_hi = it->tile_hi, keys = it->keys, head = it->head;
-        const int tiles = tile_hi - tile_lo;
-        const bool pair = it->form == kFormPair;
+        const int tile_hi = it->tile_hi, keys = it->keys, head = it->head;
+        int tile = it->tile_lo;
         const int32_t* table = p.list[it->list].table + static_cast<long long>(it->seg) * p.list[it->list].max_blocks;
         drop_item(n);
         // lane c: the page of chunk c of a tile
-        auto fetch = [&](int tile) {
-          const int key = tile * kTile + first;
-          return tile < tile_hi && lane < chunks && key < keys ? __ldg(table + (key >> p.page_shift)) : 0;
+        auto fetch = [&](int t) {
+          const int key = t * kTile + (lane << chunk_shift);
+          return t < tile_hi && lane < chunks && key < keys ? __ldg(table + (key >> p.page_shift)) : 0;
         };
-        int even = fetch(tile_lo), odd = fetch(tile_lo + 1), next = fetch(tile_lo + 2);  // by the tile's number in the item
-        for (int at = 0; at < 2 * tiles; ++at) {
-          bool is_v;
-          const int t = tile_at(at, tiles, pair, &is_v), tile = tile_lo + t;
-          const int valid = min(kTile, keys - tile * kTile);
-          int block = (t & 1) ? odd : even;
+        int block = fetch(tile), next = fetch(tile + 1);
+        for (; tile < tile_hi; ++tile, ++done) {
           if (block < 0 || block >= p.num_blocks) {
             atomicOr(&g_status_ragged, FP8MLA_DEV_BAD_PAGE);
             block = 0;
           }
-          const uint32_t c = is_v ? v_done : k_done, ring = is_v ? L::kVs : L::kKs, slot = c % ring;
-          uint64_t* full = is_v ? &sm->v_full[slot] : &sm->k_full[slot];
-          uint64_t* empty = is_v ? &sm->v_empty[slot] : &sm->k_empty[slot];
-          if (c >= ring && !warp_wait(empty, (c / ring - 1) & 1, abort_flag)) {
+          if (done >= ring && !warp_wait(empty + slot, phase, abort_flag)) {
             ok = false;
             break;
           }
-          if (lane == 0)  // whole pages, or 128 keys of one
-            mbar_arrive_expect_tx(full, static_cast<uint32_t>(((valid - 1) >> chunk_shift) + 1) * (kHd << chunk_shift));
-          __syncwarp();
-          const int row = ((block * p.h_kv + head) << p.page_shift) + ((tile * kTile + first) & in_page);
-          if (lane < chunks && first < valid)
-            tma_load_3d(smem + (is_v ? L::kOffV : L::kOffK) + slot * L::kRaw + first * kHd, is_v ? &tm_v : &tm_k, full, 0,
-                        row, 0);
+          const int valid = min(kTile, keys - tile * kTile);
+          const int copies = ((valid - 1) >> chunk_shift) + 1;  // whole pages, or 128 keys of one
+          if (leader) mbar_arrive_expect_tx(full + slot, static_cast<uint32_t>(copies) * (kHd << chunk_shift));
+          const int row = ((block * p.h_kv + head) << p.page_shift) + ((tile * kTile) & in_page);
+          uint8_t* to = tiles_at + slot * L::kRaw;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (c >= copies) break;
+            const int from = __shfl_sync(0xffffffffu, row, c);
+            if (leader) tma_load_3d(to + c * (kHd << chunk_shift), map, full + slot, 0, from, 0);
+          }
           if constexpr (kRows) {
             if (is_v) {  // scales of four keys a lane
               const int key = lane * 4;
-              const int from = __shfl_sync(0xffffffffu, block, key >> chunk_shift);
-              const long long at4 = ((static_cast<long long>(from) * p.h_kv + head) << p.page_shift) +
-                                    ((tile * kTile + key) & in_page);
+              const int from = __shfl_sync(0xffffffffu, row, key >> chunk_shift);
+              const int at4 = from + (key & ((1 << chunk_shift) - 1));
               if (key < valid) {
                 cp_async16(smem_u32(&sm->raw_scl[slot][0][key]), p.k_scale + at4, 16u);
                 cp_async16(smem_u32(&sm->raw_scl[slot][1][key]), p.v_scale + at4, 16u);
               }
-              cp_async_mbar_arrive(full);
+              cp_async_mbar_arrive(full + slot);
             }
           }
-          if (!is_v) {
-            ++k_done;
-          } else {  // the tile is done: its place takes the one after the next
-            if (t & 1)
-              odd = next;
-            else
-              even = next;
-            next = fetch(tile + 3);
-            ++v_done;
-          }
+          block = next;
+          next = fetch(tile + 2);
+          if (++slot == ring) slot = 0, phase ^= 1;
         }
       }
       if constexpr (kRows) cp_async_wait_all();  // this lane's copies have landed before the CTA can exit
-      for (uint32_t j = k_done > L::kKs ? k_done - L::kKs : 0; j < k_done; ++j)
-        warp_wait(&sm->k_full[j % L::kKs], (j / L::kKs) & 1, nullptr);
-      for (uint32_t j = v_done > L::kVs ? v_done - L::kVs : 0; j < v_done; ++j)
-        warp_wait(&sm->v_full[j % L::kVs], (j / L::kVs) & 1, nullptr);
+      for (uint32_t j = done > ring ? done - ring : 0; j < done; ++j)
+        warp_wait(full + j % ring, (j / ring) & 1, nullptr);
     } else if (warp == 14) {
       // ------------------------------------------------- the share's items --
-      Walk walk(sm->plan, unit);
-      Item it;
+      find_share(p, unit, &sm->walk);
       bool more = true;
+#pragma unroll 1
       for (uint32_t n = 0; more; ++n) {
-        it.end = !walk.next(p, sm->plan, unit, &it);
-        more = !it.end;
         if (n >= kItems && !warp_wait(&sm->item_empty[n % kItems], (n / kItems - 1) & 1, abort_flag)) break;
-        if (lane == 0) sm->item[n % kItems] = it;
+        Item* it = &sm->item[n % kItems];
+        if (lane == 0) it->end = !next_item(p, unit, &sm->walk, it);
+        __syncwarp();
+        more = !it->end;
         warp_arrive(&sm->item_full[n % kItems]);
       }
-    } else if (p.fill_out || p.fill_lse) {
-      // ------------------------------------------- rows of no sequence --
-      const List& l = p.list[0];
-      const int lo = l.starts ? min(max(__ldg(l.starts), 0), p.tokens) : 0;
-      const int hi = l.starts ? min(max(__ldg(l.starts + l.n), lo), p.tokens) : min(l.n, p.tokens);
-      const long long heads = static_cast<long long>(lo + p.tokens - hi) * p.h_q;
-      for (long long i = unit; i < heads; i += gridDim.x) {
-        int t = static_cast<int>(i / p.h_q);
-        const int h = static_cast<int>(i % p.h_q);
-        if (t >= lo) t += hi - lo;
-        if (p.fill_out && lane < kHd / 8)
-          *reinterpret_cast<uint4*>(p.out + t * p.o_tok + h * p.o_head + lane * 8) = make_uint4(0, 0, 0, 0);
-        if (p.fill_lse && lane == 0) p.lse[static_cast<long long>(t) * p.h_q + h] = kNegInf;
+      // and rows of no sequence
+      if (p.fill_out || p.fill_lse) {
+        const List& l = p.list[0];
+        const int lo = l.starts ? min(max(__ldg(l.starts), 0), p.tokens) : 0;
+        const int hi = l.starts ? min(max(__ldg(l.starts + l.n), lo), p.tokens) : min(l.n, p.tokens);
+        const long long heads = static_cast<long long>(lo + p.tokens - hi) * p.h_q;
+        for (long long i = unit; i < heads; i += gridDim.x) {
+          int t = static_cast<int>(i / p.h_q);
+          const int h = static_cast<int>(i % p.h_q);
+          if (t >= lo) t += hi - lo;
+          if (p.fill_out && lane < kHd / 8)
+            *reinterpret_cast<uint4*>(p.out + t * p.o_tok + h * p.o_head + lane * 8) = make_uint4(0, 0, 0, 0);
+          if (p.fill_lse && lane == 0) p.lse[static_cast<long long>(t) * p.h_q + h] = kNegInf;
+        }
       }
     }
   }
@@ -1417,6 +1406,7 @@ void use(Params* p, const Space& s, void* workspace) {
     p->plane_o[i] = reinterpret_cast<float*>(w + s.plane_o[i]);
   }
   p->slot_rows = s.slot_rows;
+  p->per_unit = ~0ull / static_cast<unsigned>(s.grid);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
