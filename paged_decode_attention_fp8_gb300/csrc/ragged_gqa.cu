@@ -328,7 +328,7 @@ struct Control {
   uint64_t item_full[kItems], item_empty[kItems];
   Item item[kItems];
   Walk walk;
-  uint32_t tmem_base, abort_flag;
+  uint32_t tmem_base, abort_flag, never;  // never: the flag of waits that no other warp ends
   uint32_t sums_read;            // warps that are done with a few-row item's sums
   int8_t q_exp[2][kTile];        // of Q's rows, by stream
   float row_l[2][kTile], row_m[kTile];
@@ -342,30 +342,37 @@ constexpr size_t smem_bytes() {
   return Lay<kHd, kRows>::kOffCtl + sizeof(Control<kHd, kRows>);
 }
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  const bool ok = wait_bounded(bar, parity, abort_flag, &g_status_ragged);
+// Bounded waits of this kernel, in few instructions (it has to stay in the instruction cache): after kWaitLimit of
+// polling without success, or once another warp gave up, false; the CTA then reports it at its end.
+constexpr uint32_t kWaitLimit = 3500000000u;  // ns
+__device__ __forceinline__ uint32_t timer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+template <typename Done>
+__device__ __forceinline__ bool wait_until(volatile uint32_t* abort_flag, Done done) {
+  bool ok = done();
+  if (!ok) {
+    const uint32_t t0 = timer_lo();
+    uint32_t polls = 0;
+#pragma unroll 1
+    do {
+      if (*abort_flag) break;
+      if (++polls > kWaitMinPolls && timer_lo() - t0 > kWaitLimit) *abort_flag = 1u;
+      ok = done();
+    } while (!ok);
+  }
   return __all_sync(0xffffffffu, ok);
 }
-
-// Until *count has reached `want` (it only grows), with the limits of a bounded wait.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  return wait_until(abort_flag, [&] { return mbar_try_wait(bar, parity); });
+}
+// Until *count has reached `want` (it only grows).
 __device__ __forceinline__ bool wait_count(volatile uint32_t* count, uint32_t want, volatile uint32_t* abort_flag) {
-  const uint64_t t0 = globaltimer_ns();
-  bool ok = true;
-  for (uint32_t it = 1; static_cast<int32_t>(*count - want) < 0; ++it) {
-    if ((it & 31u) != 0) continue;
-    if (*abort_flag) {
-      ok = false;
-      break;
-    }
-    if (it > kWaitMinPolls && globaltimer_ns() - t0 > *(volatile uint64_t*)&g_wait_limit_ns) {
-      *abort_flag = 1u;
-      atomicOr(&g_status_ragged, FP8MLA_DEV_WAIT_TIMEOUT);
-      ok = false;
-      break;
-    }
-  }
+  const bool ok = wait_until(abort_flag, [&] { return static_cast<int32_t>(*count - want) >= 0; });
   __threadfence_block();
-  return __all_sync(0xffffffffu, ok);
+  return ok;
 }
 
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
@@ -387,6 +394,7 @@ __device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t*
   const int ch = lane % kLanes, sub = lane / kLanes;
   const int end = min(first + count, it.rows - row0);
   const int item_row = it.row0 + row0, head0 = it.head * static_cast<int>(p.group.d), t0 = it.t0;
+#pragma unroll 1
   for (int base = first; base < end; base += kStep * kFly) {
     uint4 x[kFly][2];
 #pragma unroll
@@ -480,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm->pv_done, 1);
     mbar_init(&sm->xchg, 8);
     mbar_init(&sm->final_mma, 1);
-    sm->abort_flag = 0;
+    sm->abort_flag = sm->never = 0;
     sm->sums_read = 0;
     fence_barrier_init();
   }
@@ -548,15 +556,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!kRows) cc = c;  // units of the reference to log2
         int keys = it->keys - it->tile_lo * kTile;  // left
         auto steps = [&](auto which) {
-          constexpr int kForm = decltype(which)::value;
-          constexpr bool kPair = kForm == kFormPair;
-          constexpr int kCols = kPair ? kTile : (kForm == kFormOne ? kTile / 2 : 16);  // whose exponentials this thread takes
-          constexpr int kChunk = kCols < 32 ? kCols : 32;
+          constexpr bool kPair = decltype(which)::value;
           constexpr int kOCols = kPair ? kHd : kHd / 2;  // of O that it rescales
-          // its columns, and (not a pair) as many that the other warpgroup takes, looked at for the maximum alone
-          const int col0 = kPair ? 0 : (kForm == kFormOne ? wg * kCols : w * 32 + wg * kCols);
-          const int other0 = kForm == kFormOne ? kCols - col0 : w * 32 + (1 - wg) * kCols;
           const uint32_t t_o = lanes + kTO + wg * (kPair ? 128 : kOCols);
+          // one stream: either warpgroup's columns, of the quarter's 32 where the rows lie in all quarters
+          const int cols = few ? 16 : 64, col0 = (few ? w * 32 : 0) + wg * cols, end0 = few ? w * 32 + 32 : 128;
+          // O and l follow a new reference.
+          auto rescale = [&](int i, float alpha) -> bool {
+            if (!kPair && !warp_wait(&sm->pv_done, (pv_base + i - 1) & 1, abort_flag)) return false;
+            tc_fence_after();
+            l *= alpha;
+#pragma unroll 1
+            for (int k = 0; k < kOCols; k += 16) {
+              uint32_t o[16];
+              tmem_ld16(t_o + k, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st16(t_o + k, o);
+            }
+            return true;
+          };
+#pragma unroll 1
           for (int i = 0; i < tiles; ++i, keys -= kTile) {
             const int buf = kPair ? wg : (i & 1);
             if (!warp_wait(&sm->s_full[buf], (s_phase >> buf) & 1, abort_flag)) return false;
@@ -564,79 +585,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kRows && !warp_wait(&sm->scl_full[tile_no % L::kScls], (tile_no / L::kScls) & 1, abort_flag)) return false;
             if (busy) {
               const uint32_t t_s = lanes + kTS + buf * 128;
-              const uint32_t t_p = kPair ? t_s : lanes + kTO + 128 + buf * 64 + col0 / 2;
+              const uint32_t t_p = kPair ? t_s : lanes + kTO + 128 + buf * 64;
               tc_fence_after();
-              float x[kCols];
-              float top = kNegInf;
               [[maybe_unused]] const float4* kl = sm->scl_k[kRows ? tile_no % L::kScls : 0];
               [[maybe_unused]] const float* iv = sm->scl_v[kRows ? tile_no % L::kScls : 0];
-              auto load = [&](float* y, int at) {
-                if constexpr (kChunk == 32)
-                  tmem_ld32(t_s + at, *reinterpret_cast<uint32_t(*)[32]>(y));
-                else
-                  tmem_ld16(t_s + at, *reinterpret_cast<uint32_t(*)[16]>(y));
-              };
+              constexpr int kChunk = kPair ? kTile : 16;
+              float x[kChunk];
               // scores of column `at` on: masked past the end; with row scales in log2, times their key's K scale and
               // its V scale
-              auto scores = [&](float* y, int at) {
+              auto scores = [&](int at) {
+                if constexpr (kPair) {
+#pragma unroll
+                  for (int k = 0; k < kChunk; k += 32) tmem_ld32(t_s + k, *reinterpret_cast<uint32_t(*)[32]>(x + k));
+                } else {
+                  tmem_ld16(t_s + at, *reinterpret_cast<uint32_t(*)[16]>(x));
+                }
+                tmem_ld_wait();
                 if (keys < kTile) {
 #pragma unroll
-                  for (int j = 0; j < kChunk; ++j) y[j] = at + j < keys ? y[j] : kNegInf;
+                  for (int j = 0; j < kChunk; ++j) x[j] = at + j < keys ? x[j] : kNegInf;
                 }
                 if constexpr (kRows) {
 #pragma unroll
                   for (int j = 0; j < kChunk; j += 2) {
                     const float4 a = kl[(at + j) / 2];
-                    const float2 u = fma_f32x2(mul_f32x2(make_float2(y[j], y[j + 1]), make_float2(c, c)),
+                    const float2 u = fma_f32x2(mul_f32x2(make_float2(x[j], x[j + 1]), make_float2(c, c)),
                                                make_float2(a.x, a.y), make_float2(a.z, a.w));
-                    y[j] = u.x, y[j + 1] = u.y;
+                    x[j] = u.x, x[j + 1] = u.y;
                   }
                 }
               };
-              auto raise_top = [&](const float* y) {
-                float m0 = y[0], m1 = y[1];
+              auto largest = [&](float top) {
+                float m0 = x[0], m1 = x[1];
 #pragma unroll
-                for (int j = 2; j + 4 <= kChunk; j += 4) m0 = fmax3(m0, y[j], y[j + 1]), m1 = fmax3(m1, y[j + 2], y[j + 3]);
-                top = fmax3(top, m0, m1);
-                top = fmax3(top, y[kChunk - 2], y[kChunk - 1]);
+                for (int j = 2; j + 4 <= kChunk; j += 4) m0 = fmax3(m0, x[j], x[j + 1]), m1 = fmax3(m1, x[j + 2], x[j + 3]);
+                return fmax3(fmax3(top, m0, m1), x[kChunk - 2], x[kChunk - 1]);
               };
-              // O and l follow a new reference.
-              auto rescale = [&](float alpha) -> bool {
-                if (!kPair && !warp_wait(&sm->pv_done, (pv_base + i - 1) & 1, abort_flag)) return false;
-                tc_fence_after();
-                l *= alpha;
+              auto subtract = [&](float by) {
 #pragma unroll
-                for (int k = 0; k < kOCols; k += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(t_o + k, o);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                  tmem_st16(t_o + k, o);
+                for (int j = 0; j < kChunk; j += 2) {
+                  const float2 d = add_f32x2(make_float2(x[j], x[j + 1]), make_float2(-by, -by));
+                  x[j] = d.x, x[j + 1] = d.y;
                 }
-                return true;
               };
-              // P = 2^(x cc + lift - ref cc) in one operation where the product is small enough for the sum to keep the
-              // fraction; else the differences first
-              float bias = 0.f;
-              bool far = false;
-              auto set_bias = [&] {
-                far = fabsf(ref * cc) > kFar;
-                if (__any_sync(0xffffffffu, far)) {
-                  const float by = far ? ref : 0.f;
+              // P = 2^(x cc + bias) to column `at` on, and the sum of the weights.  bias = lift - ref cc, in one
+              // operation where the product is small enough for the sum to keep its fraction; else (far) x holds the
+              // differences to the reference
+              float bias;
+              auto weigh = [&](int at) -> float {
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                constexpr int kPut = kPair ? 32 : 16;
 #pragma unroll
-                  for (int j = 0; j < kCols; ++j) x[j] -= by;
-                }
-                bias = far ? kLift : kLift - ref * cc;
-              };
-              float2 sum[2];
-              auto weigh = [&] {
-                sum[0] = sum[1] = make_float2(0.f, 0.f);
+                for (int k = 0; k < kChunk; k += kPut) {
+                  uint32_t h[kPut / 2];
 #pragma unroll
-                for (int k = 0; k < kCols; k += kChunk) {
-                  uint32_t h[kChunk / 2];
-#pragma unroll
-                  for (int j = 0; j < kChunk; j += 4) {
+                  for (int j = 0; j < kPut; j += 4) {
                     float2 d[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -650,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       h[j / 2 + e] = pack_f16x2(d[e].x, d[e].y);
                     }
                     if constexpr (kRows) {
-                      const float4 v = *reinterpret_cast<const float4*>(iv + col0 + k + j);
+                      const float4 v = *reinterpret_cast<const float4*>(iv + at + k + j);
                       sum[0] = fma_f32x2(d[0], make_float2(v.x, v.y), sum[0]);
                       sum[1] = fma_f32x2(d[1], make_float2(v.z, v.w), sum[1]);
                     } else {
@@ -658,67 +661,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                       sum[1] = add_f32x2(sum[1], d[1]);
                     }
                   }
-                  if constexpr (kChunk == 32)
+                  if constexpr (kPair)
                     tmem_st16(t_p + k / 2, h);
                   else
-                    tmem_st8(t_p + k / 2, h);
+                    tmem_st8(t_p + at / 2, h);
                 }
+                return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
               };
-              float y[kPair ? 1 : kCols];
-#pragma unroll
-              for (int k = 0; !kPair && k < kCols; k += kChunk) load(y + k, other0 + k);
-#pragma unroll
-              for (int k = 0; k < kCols; k += kChunk) load(x + k, col0 + k);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; !kPair && k < kCols; k += kChunk) scores(y + k, other0 + k), raise_top(y + k);
-#pragma unroll
-              for (int k = 0; k < kCols; k += kChunk) scores(x + k, col0 + k);
-              if (!kPair || kRows || i == 0) {
-#pragma unroll
-                for (int k = 0; k < kCols; k += kChunk) raise_top(x + k);
-                if (i == 0) {
-                  ref = top == kNegInf ? 0.f : top;
-                } else {
-                  const bool raise = (top - ref) * cc > kTau;
-                  if (__any_sync(0xffffffffu, raise && live)) {
-                    const float alpha = raise ? ex2_approx((ref - top) * cc) : 1.f;
-                    if (raise) ref = top;
-                    if (!rescale(alpha)) return false;
+              if constexpr (kPair) {
+                scores(0);
+                bool far = fabsf(ref * cc) > kFar && i > 0;
+                if (__any_sync(0xffffffffu, far)) subtract(far ? ref : 0.f);
+                bias = far ? kLift : kLift - ref * cc;
+                // Without row scales no maximum is taken: 128 weights of scores up to the reference sum to 2^14 at most.
+                // Where they sum to more than 2^15 (one past the reference by more than 8 does), the reference moves and
+                // they are weighed again.
+                bool look = kRows || i == 0;
+#pragma unroll 1
+                for (bool again = false;;) {
+                  if (look) {
+                    const float top = largest(kNegInf);
+                    const float step = i == 0 || far ? top : top - ref;  // of the reference, where it moves
+                    const bool raise = i > 0 && step * cc > (again ? 0.f : kTau);
+                    if (i > 0 && __any_sync(0xffffffffu, raise && live) &&
+                        !rescale(i, raise ? ex2_approx(-step * cc) : 1.f))
+                      return false;
+                    float by = 0.f;
+                    if (i == 0) {
+                      ref = top == kNegInf ? 0.f : top;
+                      far = fabsf(ref * cc) > kFar;
+                      by = far ? ref : 0.f;
+                    } else if (raise) {
+                      ref = far ? ref + top : top;
+                      by = far || fabsf(ref * cc) > kFar ? top : 0.f;
+                      far = far || fabsf(ref * cc) > kFar;
+                    }
+                    if (__any_sync(0xffffffffu, by != 0.f)) subtract(by);
+                    bias = far ? kLift : kLift - ref * cc;
                   }
-                }
-              }
-              set_bias();
-              if constexpr (kPair && !kRows) {
-                // No maximum is taken: 128 weights of scores up to the reference sum to 2^14 at most.  Where they sum to
-                // more than 2^15 (one past the reference by more than 8 does), the reference moves and they are weighed
-                // again.
-                for (bool again = false;; again = true) {
-                  weigh();
-                  const float add = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                  if (i == 0 || again || !__any_sync(0xffffffffu, live && !(add <= 32768.f))) {
+                  const float add = weigh(0);
+                  if (look || !__any_sync(0xffffffffu, live && !(add <= 32768.f))) {
                     l += add;
                     break;
                   }
-                  top = kNegInf;
-#pragma unroll
-                  for (int k = 0; k < kCols; k += kChunk) raise_top(x + k);
-                  const float step = far ? top : top - ref;
-                  const bool raise = step * cc > 0.f;
-                  if (!rescale(raise ? ex2_approx(-step * cc) : 1.f)) return false;
-                  if (raise) {
-                    ref = far ? ref + top : top;
-                    const bool now = far || fabsf(ref * cc) > kFar;
-                    const float by = now ? top : 0.f;
-#pragma unroll
-                    for (int j = 0; j < kCols; ++j) x[j] -= by;
-                    far = now;
-                    bias = far ? kLift : kLift - ref * cc;
-                  }
+                  look = again = true;
                 }
               } else {
-                weigh();
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                float top = kNegInf;
+#pragma unroll 1
+                for (int at = end0 - 2 * cols; at < end0; at += 16) {  // both warpgroups' columns
+                  scores(at);
+                  top = largest(top);
+                }
+                const bool raise = (top - ref) * cc > kTau;
+                if (i == 0) {
+                  ref = top == kNegInf ? 0.f : top;
+                } else if (__any_sync(0xffffffffu, raise && live)) {
+                  if (!rescale(i, raise ? ex2_approx((ref - top) * cc) : 1.f)) return false;
+                  if (raise) ref = top;
+                }
+                const bool far = fabsf(ref * cc) > kFar;
+                bias = far ? kLift : kLift - ref * cc;
+#pragma unroll 1
+                for (int at = col0; at < col0 + cols; at += 16) {
+                  scores(at);
+                  subtract(far ? ref : 0.f);
+                  l += weigh(at);
+                }
               }
               tmem_st_wait();
               tc_fence_before();
@@ -729,14 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        bool ok;
-        if (pair)
-          ok = steps(std::integral_constant<int, kFormPair>{});
-        else if (few)
-          ok = steps(std::integral_constant<int, kFormFew>{});
-        else
-          ok = steps(std::integral_constant<int, kFormOne>{});
-        if (!ok) break;
+        if (!(pair ? steps(std::true_type{}) : steps(std::false_type{}))) break;
         if (pair)
           s_phase ^= (tiles & 1) << (1 - wg);
         else
@@ -801,7 +803,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* quarters = reinterpret_cast<float*>(smem + L::kOffSum);
         if (!wait_o()) break;
         bool ok = true;
+#pragma unroll 1
         for (int k0 = 0; ok && k0 < kHd / 2; k0 += dims) {
+#pragma unroll 1
           for (int k = 0; k < dims; k += 32) {
             uint32_t o[32];
             __syncwarp();
@@ -818,6 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ok = exchange();
           if (ok && out_row < it->rows) {
+#pragma unroll 1
             for (int k = 0; k < 2 * dims; k += 32) {  // either half's dims
               const int half = k >= dims ? 1 : 0, in = k - half * dims;
               float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -860,6 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live && (pair || (few ? warp == 0 : wg == 0))) put_sums(row, head, token, ref * cc, l);
         const float f = tiles > 0 ? v_scale / l : 0.f;
         const bool mine = live && (!few || w == 0);
+#pragma unroll 1
         for (int k = 0; busy && k < dims; k += 32) {
           uint32_t o[32] = {};
           __syncwarp();
@@ -914,12 +920,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         if (kHd == 128 && form == kFormPair && !wait_count(&sm->sums_read, sums, abort_flag)) break;  // they lie there
         int8_t* q_exp = sm->q_exp[0];
-        if (form == kFormPair)
-          load_q<kHd>(p, *it, smem + (w / 2) * L::kQ, q_exp + (w / 2) * kTile, (w / 2) * kTile, (w % 2) * 64, 64, false,
-                      lane);
-        else
-          load_q<kHd>(p, *it, smem, q_exp, 0, w * (form == kFormOne ? 32 : 8), form == kFormOne ? 32 : 8,
-                      form == kFormFew, lane);
+        const int stream = form == kFormPair ? w / 2 : 0;
+        const int count = form == kFormPair ? 64 : (form == kFormOne ? 32 : 8);  // a warp's rows
+        load_q<kHd>(p, *it, smem + stream * L::kQ, q_exp + stream * kTile, stream * kTile,
+                    (form == kFormPair ? w % 2 : w) * count, count, form == kFormFew, lane);
         fence_proxy_async_smem();
         warp_arrive(&sm->q_full);
         ++worked;
@@ -980,26 +984,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         p_phase ^= 1u << buf;
         return done;
       };
+      // (descriptors count in 16 bytes; loops are kept short for the instruction cache)
+      const uint64_t q_desc = make_sdesc(qb, 16, 1024, SWIZZLE_128B), k_desc = make_sdesc(kb, 16, 8 * kHd, L::kSwizzle);
+      const uint64_t v_desc = make_sdesc(fb, kTile * 128, 1024, SWIZZLE_128B);
       auto issue_qk = [&](int q, int buf, uint32_t t) {  // S[buf] = Q[q] K^T, both terms of Q
         tc_fence_after();
-        const uint32_t a = qb + q * L::kQ, b = kb + (t % L::kKs) * L::kRaw;
-#pragma unroll
+        const uint64_t a = q_desc + q * (L::kQ >> 4), b = k_desc + (t % L::kKs) * (L::kRaw >> 4);
+#pragma unroll 1
         for (int term = 0; term < 2; ++term) {
+          const uint64_t at_term = a + term * ((kHd == 128 ? kTile * 128 : 64) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kHd / 32; ++kk)
-            mma_f8_ss_if(leader, tmem + kTS + buf * 128,
-                         make_sdesc(a + term * (kHd == 128 ? kTile * 128 : 64) + kk * 32, 16, 1024, SWIZZLE_128B),
-                         make_sdesc(b + kk * 32, 16, 8 * kHd, L::kSwizzle), idesc_qk, term + kk > 0 ? 1u : 0u);
+            mma_f8_ss_if(leader, tmem + kTS + buf * 128, at_term + 2 * kk, b + 2 * kk, idesc_qk,
+                         kk > 0 ? 1u : static_cast<uint32_t>(term));
         }
         tc_commit_if(leader, &sm->s_full[buf]);
       };
       auto issue_pv = [&](uint32_t t_o, uint32_t t_p, uint32_t t, bool fresh) {  // O += P V
         tc_fence_after();
-        const uint32_t b = fb + (t % L::kFs) * L::kF;
+        const uint64_t b = v_desc + (t % L::kFs) * (L::kF >> 4);
+#pragma unroll 1
+        for (int k = 0; k < kTile / 16; k += 4) {
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_f16_ts_if(leader, tmem + t_o, tmem + t_p + kk * 8,
-                        make_sdesc(b + kk * 2048, kTile * 128, 1024, SWIZZLE_128B), idesc_pv, (fresh && kk == 0) ? 0u : 1u);
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ts_if(leader, tmem + t_o, tmem + t_p + (k + kk) * 8, b + (k + kk) * 128, idesc_pv,
+                          (kk > 0 || k > 0 || !fresh) ? 1u : 0u);
+        }
       };
       auto free_k = [&](uint32_t t) { tc_commit_if(leader, &sm->k_empty[t % L::kKs]); };
       auto free_v = [&](uint32_t t) { tc_commit_if(leader, &sm->f_empty[t % L::kFs]); };
@@ -1011,67 +1021,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         drop_item(n);
         if (tiles == 0) continue;
         ok = false;
-        if (!warp_wait(&sm->q_full, worked++ & 1, abort_flag) || !wait_k(at)) break;
-        int i = 0;
-        if (pair) {
-          issue_qk(0, 0, at);
-          issue_qk(1, 1, at);
-          free_k(at);
-          if (tiles == 1) tc_commit_if(leader, &sm->q_empty);
-          for (; i < tiles; ++i) {
-            const uint32_t t = at + i;
-            const bool last = i + 1 == tiles;
-            if (!wait_v(t) || !wait_p(0)) break;
-            issue_pv(kTO, kTS, t, i == 0);
-            if (last) {
-              tc_commit_if(leader, &sm->o_full[0]);
-            } else {
-              if (!wait_k(t + 1)) break;
-              issue_qk(0, 0, t + 1);
-            }
-            if (!wait_p(1)) break;
-            issue_pv(kTO + 128, kTS + 128, t, i == 0);
-            free_v(t);
-            if (last) {
-              tc_commit_if(leader, &sm->o_full[1]);
-            } else {
-              issue_qk(1, 1, t + 1);
-              free_k(t + 1);
-              if (i + 2 == tiles) tc_commit_if(leader, &sm->q_empty);
-            }
+        if (!warp_wait(&sm->q_full, worked++ & 1, abort_flag)) break;
+        // Operation j is a product with P and one with K two operations ahead, in its buffer: with two streams S(j % 2)
+        // and a tile in two operations, with one stream the tile's parity and a tile in each.
+        const int per = pair ? 2 : 1, ops = tiles * per;
+        int j = -2;
+#pragma unroll 1
+        for (; j < ops; ++j) {
+          const int buf = j & 1;
+          if (j >= 0) {
+            const int i = pair ? j >> 1 : j, o = pair ? buf : 0;
+            const bool starts = !pair || buf == 0, ends = !pair || buf == 1;
+            if ((starts && !wait_v(at + i)) || !wait_p(buf)) break;
+            issue_pv(kTO + o * 128, pair ? kTS + buf * 128 : kTO + 128 + buf * 64, at + i, i == 0);
+            if (!pair) tc_commit_if(leader, &sm->pv_done);
+            if (ends) free_v(at + i);
+            if (i + 1 == tiles) tc_commit_if(leader, &sm->o_full[o]);
           }
-        } else {
-          issue_qk(0, 0, at);
-          free_k(at);
-          if (tiles > 1) {
-            if (!wait_k(at + 1)) break;
-            issue_qk(0, 1, at + 1);
-            free_k(at + 1);
-          }
-          if (tiles <= 2) tc_commit_if(leader, &sm->q_empty);
-          for (; i < tiles; ++i) {
-            const int buf = i & 1;
-            const uint32_t t = at + i;
-            if (!wait_v(t) || !wait_p(buf)) break;
-            issue_pv(kTO, kTO + 128 + buf * 64, t, i == 0);
-            tc_commit_if(leader, &sm->pv_done);
-            free_v(t);
-            if (i + 1 == tiles) tc_commit_if(leader, &sm->o_full[0]);
-            if (i + 2 < tiles) {
-              if (!wait_k(t + 2)) break;
-              issue_qk(0, buf, t + 2);
-              free_k(t + 2);
-              if (i + 3 == tiles) tc_commit_if(leader, &sm->q_empty);
-            }
+          if (j + 2 < ops) {
+            const int i = pair ? (j + 2) >> 1 : j + 2;
+            const bool starts = !pair || buf == 0, ends = !pair || buf == 1;
+            if (starts && !wait_k(at + i)) break;
+            issue_qk(pair ? buf : 0, buf, at + i);
+            if (ends) free_k(at + i);
+            if (j + 3 == ops) tc_commit_if(leader, &sm->q_empty);
           }
         }
-        if (i < tiles) break;
+        if (j < ops) break;
         at += tiles;
         ok = true;
       }
       if (leader) tc_commit(&sm->final_mma);
       __syncwarp();
-      warp_wait(&sm->final_mma, 0, nullptr);
+      warp_wait(&sm->final_mma, 0, &sm->never);
     } else if (warp != 14) {
       // -------------------------------------- copies of tiles: 13 K, 15 V --
       const bool is_v = warp == 15;
@@ -1113,9 +1095,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (leader) mbar_arrive_expect_tx(full + slot, static_cast<uint32_t>(copies) * (kHd << chunk_shift));
           const int row = ((block * p.h_kv + head) << p.page_shift) + ((tile * kTile) & in_page);
           uint8_t* to = tiles_at + slot * L::kRaw;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (c >= copies) break;
+#pragma unroll 1
+          for (int c = 0; c < copies; ++c) {
             const int from = __shfl_sync(0xffffffffu, row, c);
             if (leader) tma_load_3d(to + c * (kHd << chunk_shift), map, full + slot, 0, from, 0);
           }
@@ -1137,8 +1118,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if constexpr (kRows) cp_async_wait_all();  // this lane's copies have landed before the CTA can exit
+#pragma unroll 1
       for (uint32_t j = done > ring ? done - ring : 0; j < done; ++j)
-        warp_wait(full + j % ring, (j / ring) & 1, nullptr);
+        warp_wait(full + j % ring, (j / ring) & 1, &sm->never);
     } else if (warp == 14) {
       // ------------------------------------------------- the share's items --
       find_share(p, unit, &sm->walk);
@@ -1157,10 +1139,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const List& l = p.list[0];
         const int lo = l.starts ? min(max(__ldg(l.starts), 0), p.tokens) : 0;
         const int hi = l.starts ? min(max(__ldg(l.starts + l.n), lo), p.tokens) : min(l.n, p.tokens);
-        const long long heads = static_cast<long long>(lo + p.tokens - hi) * p.h_q;
-        for (long long i = unit; i < heads; i += gridDim.x) {
+        const uint32_t heads = static_cast<uint32_t>(lo + p.tokens - hi) * p.h_q;
+#pragma unroll 1
+        for (uint32_t i = unit; i < heads; i += gridDim.x) {
           int t = static_cast<int>(i / p.h_q);
-          const int h = static_cast<int>(i % p.h_q);
+          const int h = static_cast<int>(i - t * p.h_q);
           if (t >= lo) t += hi - lo;
           if (p.fill_out && lane < kHd / 8)
             *reinterpret_cast<uint4*>(p.out + t * p.o_tok + h * p.o_head + lane * 8) = make_uint4(0, 0, 0, 0);
@@ -1173,6 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && (sm->abort_flag | sm->never) != 0) atomicOr(&g_status_ragged, FP8MLA_DEV_WAIT_TIMEOUT);
   if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
