@@ -39,8 +39,9 @@ namespace ragged {
 constexpr int kTile = 128;      // keys a tile, rows a stream
 constexpr int kItemRows = 256;  // rows an item
 constexpr int kThreads = 512;
-constexpr int kSoftmaxRegs = 184, kConvertRegs = 72, kIssueRegs = 72;  // registers a thread of the warpgroups
+constexpr int kSoftmaxRegs = 192, kConvertRegs = 72, kIssueRegs = 56;  // registers a thread of the warpgroups
 constexpr float kLift = 7.f;    // P = 2^(score - reference + 7): 2^15 at most in f16, normal down to 2^-21 of the largest
+constexpr uint32_t kNone = 0xFF800000u;  // -inf: the score of a key past the end
 constexpr float kFar = 1048576.f;  // 2^20 in log2 units: up to here the lift and the difference keep their fraction
 constexpr float kTau = 8.f;     // the reference moves when a score passes it by more
 
@@ -52,7 +53,8 @@ struct List {
   const int32_t* starts;  // segment s has the tokens [per starts[s], per starts[s + 1]); null: [per s, per (s + 1))
   const int32_t* lens;
   const int32_t* table;
-  int n, max_blocks, per;
+  int n, max_blocks, max_keys, per;
+  int most;  // starts at most
   int less;  // the last keys that are left out
 };
 
@@ -93,33 +95,30 @@ struct Seg {
   long long head;  // of all items of a KV head
 };
 
-__device__ __forceinline__ int seg_len(const List& l, int s, int page_shift, uint32_t* bad) {
+__device__ __forceinline__ int seg_len(const List& l, int s, uint32_t* bad) {
   const int n = __ldg(l.lens + s);
-  if (n < 0 || n > (static_cast<long long>(l.max_blocks) << page_shift)) {
-    *bad = FP8MLA_DEV_BAD_SEQLEN;
-    return 0;
-  }
-  return n;
+  if (static_cast<uint32_t>(n) <= static_cast<uint32_t>(l.max_keys)) return n;
+  *bad = FP8MLA_DEV_BAD_SEQLEN;
+  return 0;
 }
 
 __device__ __forceinline__ Seg read_seg(const Params& p, int s, uint32_t* bad) {
   const List& l = s < p.list[0].n ? p.list[0] : p.list[1];
   if (s >= p.list[0].n) s -= p.list[0].n;
   Seg g;
-  int t1;
+  int a = s, b = s + 1;
   if (l.starts != nullptr) {
-    const long long a = static_cast<long long>(__ldg(l.starts + s)) * l.per;
-    const long long b = static_cast<long long>(__ldg(l.starts + s + 1)) * l.per;
-    const bool ok = a >= 0 && a <= b && b <= p.tokens;
-    if (!ok) *bad = FP8MLA_DEV_BAD_SEQLEN;
-    g.t0 = ok ? static_cast<int>(a) : 0;
-    t1 = ok ? static_cast<int>(b) : 0;
-  } else {
-    g.t0 = s * l.per;
-    t1 = g.t0 + l.per;
+    a = __ldg(l.starts + s);
+    b = __ldg(l.starts + s + 1);
+    if (a < 0 || a > b || b > l.most) {
+      *bad = FP8MLA_DEV_BAD_SEQLEN;
+      a = b = 0;
+    }
   }
+  g.t0 = a * l.per;
+  const int t1 = b * l.per;
   g.rows = (t1 - g.t0) * static_cast<int>(p.group.d);
-  g.keys = max(0, seg_len(l, s, p.page_shift, bad) - l.less);
+  g.keys = max(0, seg_len(l, s, bad) - l.less);
   g.tiles = (g.keys + kTile - 1) / kTile;
   g.row_tiles = (g.rows + kItemRows - 1) / kItemRows;
   if (g.tiles > 0) {
@@ -390,31 +389,31 @@ __device__ __forceinline__ int exponent_448(float amax) {
 template <int kHd>
 __device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t* q_tile, int8_t* q_exp, int row0,
                                        int first, int count, bool quarters, int lane) {
-  constexpr int kLanes = kHd / 16, kStep = 32 / kLanes, kFly = 2;  // lanes a row, rows a pass, passes in flight
-  const int ch = lane % kLanes, sub = lane / kLanes;
+  constexpr int kLanes = kHd / 16, kStep = 32 / kLanes;  // lanes a row, rows a pass
+  const int ch = lane % kLanes;
   const int end = min(first + count, it.rows - row0);
   const int item_row = it.row0 + row0, head0 = it.head * static_cast<int>(p.group.d), t0 = it.t0;
-#pragma unroll 1
-  for (int base = first; base < end; base += kStep * kFly) {
-    uint4 x[kFly][2];
-#pragma unroll
-    for (int i = 0; i < kFly; ++i) {
-      const int row = base + i * kStep + sub;
-      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-      if (row < end) {
-        const uint32_t r = static_cast<uint32_t>(item_row + row);
-        const uint32_t t = fast_div(r, p.group);
-        const int head = head0 + static_cast<int>(r - t * p.group.d);
-        const uint4* from = reinterpret_cast<const uint4*>(p.q + (t0 + static_cast<long long>(t)) * p.q_tok +
-                                                           head * p.q_head + ch * 16);
-        x[i][0] = __ldg(from);
-        x[i][1] = __ldg(from + 1);
-      }
+  uint4 x[2], ahead[2];
+  auto load = [&](int row) {
+    ahead[0] = ahead[1] = make_uint4(0, 0, 0, 0);
+    if (row < end) {
+      const uint32_t r = static_cast<uint32_t>(item_row + row);
+      const uint32_t t = fast_div(r, p.group);
+      const int head = head0 + static_cast<int>(r - t * p.group.d);
+      const uint4* from =
+          reinterpret_cast<const uint4*>(p.q + (t0 + static_cast<long long>(t)) * p.q_tok + head * p.q_head + ch * 16);
+      ahead[0] = __ldg(from);
+      ahead[1] = __ldg(from + 1);
     }
-#pragma unroll
-    for (int i = 0; i < kFly; ++i) {
-      const int row = base + i * kStep + sub;
-      const uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+  };
+  int row = first + lane / kLanes;
+  if (first < end) load(row);
+#pragma unroll 1
+  for (int base = first; base < end; base += kStep, row += kStep) {
+    x[0] = ahead[0], x[1] = ahead[1];
+    if (base + kStep < end) load(row + kStep);
+    {
+      const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
       float amax = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
@@ -589,10 +588,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
               [[maybe_unused]] const float4* kl = sm->scl_k[kRows ? tile_no % L::kScls : 0];
               [[maybe_unused]] const float* iv = sm->scl_v[kRows ? tile_no % L::kScls : 0];
+              if (keys < kTile) {  // scores past the end (either warpgroup writes all of them)
+                int k = keys;
+                const uint32_t none[8] = {kNone, kNone, kNone, kNone, kNone, kNone, kNone, kNone};
+#pragma unroll 1
+                for (; k % 8 != 0; ++k) tmem_st1(t_s + k, kNone);
+#pragma unroll 1
+                for (; k < kTile; k += 8) tmem_st8(t_s + k, none);
+                tmem_st_wait();
+              }
               constexpr int kChunk = kPair ? kTile : 16;
               float x[kChunk];
-              // scores of column `at` on: masked past the end; with row scales in log2, times their key's K scale and
-              // its V scale
+              // scores of column `at` on; with row scales in log2, times their key's K scale and its V scale
               auto scores = [&](int at) {
                 if constexpr (kPair) {
 #pragma unroll
@@ -601,10 +608,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tmem_ld16(t_s + at, *reinterpret_cast<uint32_t(*)[16]>(x));
                 }
                 tmem_ld_wait();
-                if (keys < kTile) {
-#pragma unroll
-                  for (int j = 0; j < kChunk; ++j) x[j] = at + j < keys ? x[j] : kNegInf;
-                }
                 if constexpr (kRows) {
 #pragma unroll
                   for (int j = 0; j < kChunk; j += 2) {
@@ -670,35 +673,29 @@ __global__ void __launch_bounds__(kThreads, 1)
               };
               if constexpr (kPair) {
                 scores(0);
-                bool far = fabsf(ref * cc) > kFar && i > 0;
-                if (__any_sync(0xffffffffu, far)) subtract(far ? ref : 0.f);
-                bias = far ? kLift : kLift - ref * cc;
+                bool far = fabsf(ref * cc) > kFar && i > 0, less = false;  // less: x holds differences
                 // Without row scales no maximum is taken: 128 weights of scores up to the reference sum to 2^14 at most.
                 // Where they sum to more than 2^15 (one past the reference by more than 8 does), the reference moves and
                 // they are weighed again.
                 bool look = kRows || i == 0;
 #pragma unroll 1
                 for (bool again = false;;) {
+                  float by = far && !less ? ref : 0.f;
                   if (look) {
                     const float top = largest(kNegInf);
-                    const float step = i == 0 || far ? top : top - ref;  // of the reference, where it moves
+                    const float step = i == 0 || less ? top : top - ref;  // of the reference, where it moves
                     const bool raise = i > 0 && step * cc > (again ? 0.f : kTau);
                     if (i > 0 && __any_sync(0xffffffffu, raise && live) &&
                         !rescale(i, raise ? ex2_approx(-step * cc) : 1.f))
                       return false;
-                    float by = 0.f;
-                    if (i == 0) {
-                      ref = top == kNegInf ? 0.f : top;
-                      far = fabsf(ref * cc) > kFar;
-                      by = far ? ref : 0.f;
-                    } else if (raise) {
-                      ref = far ? ref + top : top;
-                      by = far || fabsf(ref * cc) > kFar ? top : 0.f;
-                      far = far || fabsf(ref * cc) > kFar;
-                    }
-                    if (__any_sync(0xffffffffu, by != 0.f)) subtract(by);
-                    bias = far ? kLift : kLift - ref * cc;
+                    if (i == 0) ref = top == kNegInf ? 0.f : top;
+                    if (raise) ref = less ? ref + top : top;
+                    far = less || fabsf(ref * cc) > kFar;
+                    by = !far ? 0.f : (less ? (raise ? top : 0.f) : ref);
                   }
+                  if (__any_sync(0xffffffffu, by != 0.f)) subtract(by);
+                  less = far;
+                  bias = far ? kLift : kLift - ref * cc;
                   const float add = weigh(0);
                   if (look || !__any_sync(0xffffffffu, live && !(add <= 32768.f))) {
                     l += add;
@@ -744,64 +741,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           pv_base += tiles;
       }
-      if (tiles > 0) ++worked;
+      // Where the results of a row go: rounded to the outputs (kDirect), or as they are to the workspace.  A thread has
+      // its lane's row, or (split: the rows lie in all quarters) four dims of row threadIdx.x / 8 at a time.
+      const bool split = few && tiles > 0, direct = it->slot == kDirect;
+      const int put_row = split ? threadIdx.x / 8 : row;
+      const bool put = put_row < it->rows && (split || !few || w == 0);
+      const uint32_t rr = static_cast<uint32_t>(it->row0 + put_row), tok = fast_div(rr, p.group);
+      const int head = it->head * static_cast<int>(p.group.d) + static_cast<int>(rr - tok * p.group.d);
+      const long long token = it->t0 + static_cast<long long>(tok), at = token * p.h_q + head;
+      const long long place = it->slot >= 0 ? static_cast<long long>(it->slot) * p.slot_rows + put_row : at;
+      uint16_t* out = p.out + token * p.o_tok + head * p.o_head;
+      float* sums = (it->slot >= 0 ? p.slot_o : p.plane_o[it->list]) + place * kHd;
+      float m = ref * cc, sum = l, part[4];
+      if (split) {
+        sm->row_l[wg][r] = l;
+        if (wg == 0) sm->row_m[r] = m;
+        if (!exchange()) break;
+        m = kNegInf;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          part[k] = sm->row_l[0][k * 32 + put_row] + sm->row_l[1][k * 32 + put_row];
+          if (!(part[k] == 0.f)) m = fmaxf(m, sm->row_m[k * 32 + put_row]);
+        }
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float f = part[k] == 0.f ? 0.f : ex2_approx(sm->row_m[k * 32 + put_row] - m);
+          sum += part[k] * f;
+          part[k] = f;
+        }
+      } else if (form == kFormOne && tiles > 0) {  // either warpgroup has half the keys' weights
+        sm->row_l[wg][r] = l;
+        if (!exchange()) break;
+        sum = sm->row_l[0][r] + sm->row_l[1][r];
+        if (!exchange()) break;  // read before the next item's are written
+      }
+      if (put && (split ? threadIdx.x % 8 == 0 : pair || wg == 0)) {
+        if (direct)  // a sequence without keys: -inf
+          p.lse[at] = tiles > 0 ? (m + lg2_approx(sum) - kLift) * kLn2 : kNegInf;
+        else
+          (it->slot >= 0 ? p.slot_ml : p.plane_ml[it->list])[place] = make_float2(m, sum);
+      }
+      const float unit_o = !direct ? 1.f : (tiles > 0 ? (kRows ? 1.f : __ldg(p.v_scale)) / sum : 0.f);
       const int os = pair ? wg : 0;
-      auto wait_o = [&]() -> bool {
-        if (!warp_wait(&sm->o_full[os], (o_phase >> os) & 1, abort_flag)) return false;
+      if (tiles > 0) {
+        ++worked;
+        if (!warp_wait(&sm->o_full[os], (o_phase >> os) & 1, abort_flag)) break;
         o_phase ^= pair ? 3u : 1u;
         tc_fence_after();
-        return true;
-      };
-      // Results of four or 32 values of a row (of the item): rounded to the outputs, or as they are to the workspace.
-      const int slot = it->slot;
-      const float v_scale = kRows ? 1.f : __ldg(p.v_scale);
-      auto place_of = [&](int of_row, int* head, long long* token) {
-        const uint32_t rr = static_cast<uint32_t>(it->row0 + of_row);
-        const uint32_t tok = fast_div(rr, p.group);
-        *head = it->head * static_cast<int>(p.group.d) + static_cast<int>(rr - tok * p.group.d);
-        *token = it->t0 + static_cast<long long>(tok);
-      };
-      auto put_sums = [&](int of_row, int head, long long token, float m, float sum) {
-        const long long at = token * p.h_q + head;
-        if (slot == kDirect)  // a sequence without keys: -inf
-          p.lse[at] = tiles > 0 ? (m + lg2_approx(sum) - kLift) * kLn2 : kNegInf;
-        else if (slot == kPlane)
-          p.plane_ml[it->list][at] = make_float2(m, sum);
-        else
-          p.slot_ml[static_cast<long long>(slot) * p.slot_rows + of_row] = make_float2(m, sum);
-      };
-      auto row_at = [&](int of_row, int head, long long token) -> float* {
-        return slot == kPlane ? p.plane_o[it->list] + (token * p.h_q + head) * kHd
-                              : p.slot_o + (static_cast<long long>(slot) * p.slot_rows + of_row) * kHd;
-      };
-      if (few && tiles > 0) {
-        sm->row_l[wg][r] = l;
-        if (wg == 0) sm->row_m[r] = ref;
-        if (!exchange()) break;
-        float m = kNegInf, lk[4];  // this thread's row is its lane's in every quarter
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          lk[k] = sm->row_l[0][k * 32 + lane] + sm->row_l[1][k * 32 + lane];
-          if (!(lk[k] == 0.f)) m = fmaxf(m, sm->row_m[k * 32 + lane] * cc);
-        }
-        float sum = 0.f, mine = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float f = lk[k] == 0.f ? 0.f : ex2_approx(sm->row_m[k * 32 + lane] * cc - m);
-          sum += lk[k] * f;
-          if (k == w) mine = f;
-        }
-        int head;
-        long long token;
-        place_of(lane, &head, &token);
-        if (warp == 0 && live) put_sums(lane, head, token, m, sum);
-        if (slot == kDirect) mine *= v_scale / sum;
-        const int out_row = threadIdx.x / 8, piece = threadIdx.x % 8;  // of 32 rows, of eight times four dims
-        place_of(out_row, &head, &token);
+      }
+      if (split) {
         // the quarters' sums [half][quarter][row][dims], 16 bytes swizzled: as many dims at a time as there is room for
         const int rows = kHd == 128 && it->rows <= 16 ? 16 : 32, dims = 1024 / rows;
         float* quarters = reinterpret_cast<float*>(smem + L::kOffSum);
-        if (!wait_o()) break;
         bool ok = true;
 #pragma unroll 1
         for (int k0 = 0; ok && k0 < kHd / 2; k0 += dims) {
@@ -815,13 +807,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (live) {
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<float4*>(to + ((j ^ (lane % 8)) * 4)) =
-                    make_float4(__uint_as_float(o[4 * j]) * mine, __uint_as_float(o[4 * j + 1]) * mine,
-                                __uint_as_float(o[4 * j + 2]) * mine, __uint_as_float(o[4 * j + 3]) * mine);
+                *reinterpret_cast<uint4*>(to + ((j ^ (lane % 8)) * 4)) =
+                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
             }
           }
           ok = exchange();
-          if (ok && out_row < it->rows) {
+          if (ok && put) {
 #pragma unroll 1
             for (int k = 0; k < 2 * dims; k += 32) {  // either half's dims
               const int half = k >= dims ? 1 : 0, in = k - half * dims;
@@ -829,70 +820,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const float4 b = *reinterpret_cast<const float4*>(
-                    quarters + ((half * 4 + q) * rows + out_row) * dims + in + ((piece ^ (out_row % 8)) * 4));
-                a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+                    quarters + ((half * 4 + q) * rows + put_row) * dims + in + (((threadIdx.x ^ put_row) % 8) * 4));
+                a.x += b.x * part[q], a.y += b.y * part[q], a.z += b.z * part[q], a.w += b.w * part[q];
               }
-              const int dim = half * (kHd / 2) + k0 + in + piece * 4;
-              if (slot == kDirect)
-                *reinterpret_cast<uint2*>(p.out + token * p.o_tok + head * p.o_head + dim) =
-                    make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+              const int dim = half * (kHd / 2) + k0 + in + (threadIdx.x % 8) * 4;
+              if (direct)
+                *reinterpret_cast<uint2*>(out + dim) = make_uint2(pack_bf16x2(a.x * unit_o, a.y * unit_o),
+                                                                  pack_bf16x2(a.z * unit_o, a.w * unit_o));
               else
-                *reinterpret_cast<float4*>(row_at(out_row, head, token) + dim) = a;
+                *reinterpret_cast<float4*>(sums + dim) = a;
             }
           }
           if (ok && k0 + dims < kHd / 2) ok = exchange();  // read before the next are written
         }
         if (!ok) break;
-        tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           __threadfence_block();
           atomicAdd(&sm->sums_read, 1u);
         }
-      } else {
-        if (form == kFormOne && tiles > 0) {  // either warpgroup has half the keys' weights
-          sm->row_l[wg][r] = l;
-          if (!exchange()) break;
-          l = sm->row_l[0][r] + sm->row_l[1][r];
-          if (!exchange()) break;  // read before the next item's are written
-        }
-        if (tiles > 0 && !wait_o()) break;
-        int head;
-        long long token;
-        place_of(row, &head, &token);
+      } else if (busy) {
         const int dims = pair ? kHd : kHd / 2, dim0 = pair ? 0 : wg * (kHd / 2);
-        const uint32_t t_o = lanes + kTO + os * 128 + dim0;
-        if (live && (pair || (few ? warp == 0 : wg == 0))) put_sums(row, head, token, ref * cc, l);
-        const float f = tiles > 0 ? v_scale / l : 0.f;
-        const bool mine = live && (!few || w == 0);
 #pragma unroll 1
-        for (int k = 0; busy && k < dims; k += 32) {
+        for (int k = dim0; k < dim0 + dims; k += 32) {
           uint32_t o[32] = {};
           __syncwarp();
           if (tiles > 0) {
-            tmem_ld32(t_o + k, o);
+            tmem_ld32(lanes + kTO + os * 128 + k, o);
             tmem_ld_wait();
           }
-          if (slot == kDirect) {
-            uint16_t* to = p.out + token * p.o_tok + head * p.o_head + dim0 + k;
+          if (!put) continue;
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
+          for (int j = 0; j < 32; j += 8) {
+            if (direct) {
               uint32_t h[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                h[e] = pack_bf16x2(__uint_as_float(o[j + 2 * e]) * f, __uint_as_float(o[j + 2 * e + 1]) * f);
-              if (mine) *reinterpret_cast<uint4*>(to + j) = make_uint4(h[0], h[1], h[2], h[3]);
+                h[e] = pack_bf16x2(__uint_as_float(o[j + 2 * e]) * unit_o, __uint_as_float(o[j + 2 * e + 1]) * unit_o);
+              *reinterpret_cast<uint4*>(out + k + j) = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+              *reinterpret_cast<uint4*>(sums + k + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+              *reinterpret_cast<uint4*>(sums + k + j + 4) = make_uint4(o[j + 4], o[j + 5], o[j + 6], o[j + 7]);
             }
-          } else {
-            float* to = row_at(row, head, token) + dim0 + k;
-#pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              if (mine) *reinterpret_cast<uint4*>(to + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           }
         }
-        __syncwarp();
-        tc_fence_before();
       }
+      __syncwarp();
+      tc_fence_before();
       drop_item(n);
     }
   } else if (warp < 12) {
@@ -1282,7 +1256,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
   list(1, b);
   if (p.list[1].less > 0) {
     const List& l = p.list[1];
-    const int len = seg_len(l, b, p.page_shift, &bad);
+    const int len = seg_len(l, b, &bad);
     float q[kV];
 #pragma unroll
     for (int i = 0; i < kV; ++i)
@@ -1516,7 +1490,7 @@ fp8mla_status_t cross_entry(const CrossArgs& a, cudaStream_t stream) {
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
   p.q_tok = a.q_token, p.q_head = a.q_head, p.o_tok = a.out_token, p.o_head = a.out_head;
-  p.list[0] = List{a.q_starts, a.kv_lens, a.block_table, a.bs, a.max_blocks, 1, 0};
+  p.list[0] = List{a.q_starts, a.kv_lens, a.block_table, a.bs, a.max_blocks, static_cast<int>(max_keys), 1, a.n_tokens, 0};
   p.list[1] = List{};
   p.group = make_fast_div(group);
   p.softmax_scale = a.softmax_scale;
@@ -1599,8 +1573,10 @@ fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream) {
   p.q_tok = p.o_tok = static_cast<long long>(a.h_q) * a.head_dim;
   p.q_head = p.o_head = a.head_dim;
   const bool block = a.q_len > 1 || a.spec_mask != nullptr;
-  p.list[0] = List{a.prefix_starts, a.prefix_lens, a.prefix_table, a.n_prefixes, a.prefix_blocks, a.q_len, 0};
-  p.list[1] = List{nullptr, a.seqlens, a.block_table, a.bs, a.max_blocks, a.q_len, block ? a.q_len : 0};
+  p.list[0] = List{a.prefix_starts, a.prefix_lens, a.prefix_table, a.n_prefixes, a.prefix_blocks,
+                   static_cast<int>(prefix_keys), a.q_len, a.bs, 0};
+  p.list[1] = List{nullptr, a.seqlens, a.block_table, a.bs, a.max_blocks, static_cast<int>(keys), a.q_len, a.bs,
+                   block ? a.q_len : 0};
   p.spec_mask = a.spec_mask;
   p.sinks = a.sinks;
   p.group = make_fast_div(group);
