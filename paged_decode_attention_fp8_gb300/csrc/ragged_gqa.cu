@@ -948,6 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc_qk = make_idesc(0, 0, 0, 0, kTile, 128);  // E4M3: Q (K-major) x K (K-major)
       constexpr uint32_t idesc_pv = make_idesc(0, 0, 0, 1, kHd, 128);    // f16: P (TMEM) x V (MN-major)
       const bool leader = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);  // the same in all lanes, as the compiler sees it
       const uint32_t qb = smem_u32(smem), kb = qb + L::kOffK, fb = qb + L::kOffF;
       uint32_t at = 0, p_phase = 0, worked = 0;  // at: tiles before this item's
       bool ok = true;
@@ -964,12 +965,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto issue_qk = [&](int q, int buf, uint32_t t) {  // S[buf] = Q[q] K^T, both terms of Q
         tc_fence_after();
         const uint64_t a = q_desc + q * (L::kQ >> 4), b = k_desc + (t % L::kKs) * (L::kRaw >> 4);
-#pragma unroll 1
+#pragma unroll
         for (int term = 0; term < 2; ++term) {
           const uint64_t at_term = a + term * ((kHd == 128 ? kTile * 128 : 64) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kHd / 32; ++kk)
-            mma_f8_ss_if(leader, tmem + kTS + buf * 128, at_term + 2 * kk, b + 2 * kk, idesc_qk,
+            mma_f8_ss_if(leader, tm + kTS + buf * 128, at_term + 2 * kk, b + 2 * kk, idesc_qk,
                          kk > 0 ? 1u : static_cast<uint32_t>(term));
         }
         tc_commit_if(leader, &sm->s_full[buf]);
@@ -977,11 +978,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto issue_pv = [&](uint32_t t_o, uint32_t t_p, uint32_t t, bool fresh) {  // O += P V
         tc_fence_after();
         const uint64_t b = v_desc + (t % L::kFs) * (L::kF >> 4);
-#pragma unroll 1
+#pragma unroll
         for (int k = 0; k < kTile / 16; k += 4) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ts_if(leader, tmem + t_o, tmem + t_p + (k + kk) * 8, b + (k + kk) * 128, idesc_pv,
+            mma_f16_ts_if(leader, tm + t_o, tm + t_p + (k + kk) * 8, b + (k + kk) * 128, idesc_pv,
                           (kk > 0 || k > 0 || !fresh) ? 1u : 0u);
         }
       };
@@ -990,8 +991,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t n = 0; ok; ++n) {
         const Item* it = get_item(n);
         if (it == nullptr) break;
-        const int tiles = it->tile_hi - it->tile_lo;
-        const bool pair = it->form == kFormPair;
+        const int tiles = __shfl_sync(0xffffffffu, it->tile_hi - it->tile_lo, 0);
+        const bool pair = __shfl_sync(0xffffffffu, it->form, 0) == kFormPair;
         drop_item(n);
         if (tiles == 0) continue;
         ok = false;
