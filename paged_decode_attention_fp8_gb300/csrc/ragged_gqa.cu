@@ -1140,165 +1140,198 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ merges --
 
-// A row's sum over the pieces [slot lo (at s0), slots 0 of the units after it up to `last`], by one warp: lane l owns
-// dims [kV l, kV l + kV).
+constexpr int kMergeThreads = 128;
+// Lanes a row: eight where an item's 256 rows are merged, few pieces each; four dims a lane where rows are few and their
+// prefix lies in many pieces.
+constexpr int kCrossRows = kMergeThreads / 8;
 template <int kHd>
+constexpr int kSharedRows = kMergeThreads * 4 / kHd;
+
+// A row's sum, by kLanes lanes: lane d of them owns dims [kV d, kV d + kV).
+template <int kHd, int kLanes>
 struct RowSum {
-  static constexpr int kV = kHd / 32;
+  static constexpr int kV = kHd / kLanes;
   float m = kNegInf, l = 0.f, acc[kV] = {};
-  __device__ __forceinline__ void add(float pm, float pl, const float* o, int lane) {
-    const float top = fmaxf(m, pm);
-    if (top == kNegInf) return;
-    const float a = ex2_approx(m - top), b = ex2_approx(pm - top);
-    m = top;
-    l = l * a + pl * b;
+
+  // The pieces of an item in the shares [first, last] (none: last < first): the first in slot `slot` of its share, the
+  // others in slot 0; an item of one share that is whole lies in the plane instead (plane_o).  lo: where the shares
+  // begin.  All lanes of the warp together.
+  __device__ __forceinline__ void add(const Params& p, const long long* lo, int first, int last, int slot, int row,
+                                      const float2* plane_ml, const float* plane_o, int at, int d) {
+    const int count = last - first + 1;
+    const int most = __reduce_max_sync(0xffffffffu, count);
+    const float* from = plane_o != nullptr ? plane_o : p.slot_o;
+#pragma unroll 1
+    for (int base = 0; base < most; base += kLanes) {
+      const int v = first + base + d;
+      bool ok = base + d < count;
+      if (ok && plane_o == nullptr && v > first && lo[v + 1] <= lo[v]) ok = false;  // a share without work
+      const int idx = plane_o != nullptr ? at : (2 * v + (v == first ? slot : 0)) * p.slot_rows + row;
+      float2 ml = make_float2(kNegInf, 0.f);
+      if (ok) ml = (plane_o != nullptr ? plane_ml : p.slot_ml)[idx];
+      float top = fmaxf(m, ml.x);
 #pragma unroll
-    for (int i = 0; i < kV; ++i) acc[i] = acc[i] * a + __ldcg(o + lane * kV + i) * b;
-  }
-  __device__ __forceinline__ void pieces(const Params& p, int unit, int last, int slot, int row, int lane) {
-    for (int v = unit; v <= last; ++v) {
-      if (v > unit && p.lo[v + 1] <= p.lo[v]) continue;  // a share without work
-      const long long at = static_cast<long long>(2 * v + (v == unit ? slot : 0)) * p.slot_rows + row;
-      const float2 ml = p.slot_ml[at];
-      add(ml.x, ml.y, p.slot_o + at * kHd, lane);
+      for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float a = top == kNegInf ? 1.f : ex2_approx(m - top);
+      const float w = ok && top != kNegInf ? ex2_approx(ml.x - top) : 0.f;
+      float add_l = ok ? w * ml.y : 0.f;
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) add_l += __shfl_xor_sync(0xffffffffu, add_l, o);
+      m = top;
+      l = l * a + add_l;
+#pragma unroll
+      for (int i = 0; i < kV; ++i) acc[i] *= a;
+      const int n = min(kLanes, most - base);
+#pragma unroll 4
+      for (int q = 0; q < n; ++q) {
+        const float wq = __shfl_sync(0xffffffffu, w, q, kLanes);
+        const int iq = __shfl_sync(0xffffffffu, idx, q, kLanes);
+        if (__shfl_sync(0xffffffffu, ok, q, kLanes)) {
+          const float4* x = reinterpret_cast<const float4*>(from + static_cast<long long>(iq) * kHd + d * kV);
+#pragma unroll
+          for (int i = 0; i < kV / 4; ++i) {
+            const float4 y = __ldcg(x + i);
+            acc[4 * i] += y.x * wq, acc[4 * i + 1] += y.y * wq, acc[4 * i + 2] += y.z * wq, acc[4 * i + 3] += y.w * wq;
+          }
+        }
+      }
     }
   }
-  __device__ __forceinline__ void finish(uint16_t* out, float* lse, float sink, float v_scale, int lane) {
+  __device__ __forceinline__ void finish(uint16_t* out, float* lse, float sink, float v_scale, int d) {
     float f, ls;
     finish_row(m - kLift, l, sink, v_scale, &f, &ls);
     if (l != l) f = ls = l;  // NaN
-    uint16_t* to = out + lane * kV;
-    if constexpr (kV == 4) {
-      *reinterpret_cast<uint2*>(to) =
-          make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f));
-    } else {
-      *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(acc[0] * f, acc[1] * f);
-    }
-    if (lane == 0) *lse = ls;
+#pragma unroll
+    for (int i = 0; i < kV; i += 4)
+      *reinterpret_cast<uint2*>(out + d * kV + i) =
+          make_uint2(pack_bf16x2(acc[i] * f, acc[i + 1] * f), pack_bf16x2(acc[i + 2] * f, acc[i + 3] * f));
+    if (d == 0) *lse = ls;
   }
 };
 
-constexpr int kMergeRows = 32;  // rows of an item a CTA merges
+constexpr int kMostUnits = 512;  // shares (one an SM)
 
-template <int kHd>
-__global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant__ Params p, int scale_rows) {
-  griddep_wait();
-  const int unit = blockIdx.x, units = *p.units;
-  if (unit >= units) return;
-  const Cut cut = p.cuts[unit];
-  const int row0 = blockIdx.y * kMergeRows;
-  if (cut.valid == 0 || row0 >= cut.rows) return;
-  int last = unit;
-  while (last + 1 < units && p.lo[last + 1] < cut.end) ++last;
-  const int lane = threadIdx.x % 32;
-  const float v_scale = scale_rows ? 1.f : *p.v_scale;
-  for (int row = row0 + threadIdx.x / 32; row < min(cut.rows, row0 + kMergeRows); row += 4) {
-    RowSum<kHd> sum;
-    sum.pieces(p, unit, last, cut.slot & 1, row, lane);
-    const uint32_t r = static_cast<uint32_t>(cut.row0 + row), t = fast_div(r, p.group);
-    const int head = cut.head * static_cast<int>(p.group.d) + static_cast<int>(r - t * p.group.d);
-    const long long token = cut.t0 + static_cast<long long>(t);
-    sum.finish(p.out + token * p.o_tok + head * p.o_head, p.lse + token * p.h_q + head, kNegInf, v_scale, lane);
-  }
+// Where the shares begin, in shared memory; how many there are.
+__device__ __forceinline__ int load_shares(const Params& p, int grid, long long* lo) {
+  for (int v = threadIdx.x; v <= grid; v += kMergeThreads) lo[v] = p.lo[v];  // (past the last share: anything)
+  const int units = *p.units;
+  __syncthreads();
+  return units;
 }
 
-// Row = (token, query head) of a decode step behind shared prefixes: its prefix, its own keys before the block, the
-// block's keys that it sees, its sink.  One warp a row.
 template <int kHd>
-__global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant__ Params p, int scale_rows) {
+__global__ void __launch_bounds__(kMergeThreads) cross_merge_kernel(const __grid_constant__ Params p, int scale_rows) {
   griddep_wait();
-  constexpr int kV = kHd / 32;
-  const int lane = threadIdx.x % 32;
+  __shared__ long long lo[kMostUnits + 1];
+  const int unit = blockIdx.x, row0 = blockIdx.y * kCrossRows;
+  const Cut cut = p.cuts[unit];
+  const float v_scale = scale_rows ? 1.f : *p.v_scale;
+  const int units = load_shares(p, gridDim.x, lo);
+  if (unit >= units || cut.valid == 0 || row0 >= cut.rows) return;
+  int last = unit;
+  while (last + 1 < units && lo[last + 1] < cut.end) ++last;
+  const int d = threadIdx.x % 8, row = row0 + threadIdx.x / 8;
+  const bool live = row < cut.rows;
+  RowSum<kHd, 8> sum;
+  sum.add(p, lo, unit, live ? last : unit - 1, cut.slot & 1, row, nullptr, nullptr, 0, d);
+  if (!live) return;
+  const uint32_t r = static_cast<uint32_t>(cut.row0 + row), t = fast_div(r, p.group);
+  const int head = cut.head * static_cast<int>(p.group.d) + static_cast<int>(r - t * p.group.d);
+  const long long token = cut.t0 + static_cast<long long>(t);
+  sum.finish(p.out + token * p.o_tok + head * p.o_head, p.lse + token * p.h_q + head, kNegInf, v_scale, d);
+}
+
+// Row = (sequence, KV head, token, head of its group) of a decode step behind shared prefixes: its prefix, its own keys
+// before the block, the block's keys that it sees, its sink.
+template <int kHd>
+__global__ void __launch_bounds__(kMergeThreads)
+    shared_merge_kernel(const __grid_constant__ Params p, int scale_rows, int grid, int total) {
+  griddep_wait();
+  constexpr int kV = 4, kLanes = kHd / kV;
+  __shared__ long long lo[kMostUnits + 1];
+  const int d = threadIdx.x % kLanes;
   const int group = static_cast<int>(p.group.d), rows = p.q_len * group;
-  const int b = blockIdx.x / p.h_kv, kvh = blockIdx.x % p.h_kv;
-  const int row = blockIdx.y * 4 + threadIdx.x / 32;
-  if (row >= rows) return;
-  const int tok = row / group, head = kvh * group + row % group;
-  const long long token = static_cast<long long>(b) * p.q_len + tok, at = token * p.h_q + head;
-  const int units = *p.units;
+  const int of_all = min(blockIdx.x * kSharedRows<kHd> + static_cast<int>(threadIdx.x) / kLanes, total - 1);  // (the last again)
+  const int pair = of_all / rows, row = of_all - pair * rows;
+  const int b = pair / p.h_kv, kvh = pair - b * p.h_kv;
+  const int tok = row / group, head = kvh * group + row - tok * group;
+  const int token = b * p.q_len + tok, at = token * p.h_q + head;
   const float k_scale = scale_rows ? 1.f : *p.k_scale, v_scale = scale_rows ? 1.f : *p.v_scale;
   uint32_t bad = 0;
-  RowSum<kHd> sum;
-  auto list = [&](int which, int seg) {
-    const Seg g = read_seg(p, which ? p.list[0].n + seg : seg, &bad);
-    if (g.tiles == 0) return;
-    const int r = static_cast<int>(token - g.t0) * group + row % group;
-    const int rt = r / kItemRows;
-    const long long start = p.seg_at[which ? p.list[0].n + seg : seg] + kvh * g.head + static_cast<long long>(rt) * g.full;
-    const long long end = start + (rt == g.row_tiles - 1 ? g.last : g.full);
-    int first = 0, last = 0;  // the shares that begin at or before the item, and before its end
-    for (int v = lane; v < units; v += 32) {
-      const long long lo = p.lo[v];
-      first += lo <= start;
-      last += lo < end;
+  // its prefix (-1: none), looked for by the row's lanes
+  int prefix = -1;
+  for (int g0 = 0; g0 < p.list[0].n; g0 += kLanes) {
+    const int g = g0 + d;
+    if (g < p.list[0].n && prefix < 0) {
+      const int first = __ldg(p.list[0].starts + g), end = __ldg(p.list[0].starts + g + 1);
+      if (first >= 0 && first <= b && b < end && end <= p.list[0].most) prefix = g;
     }
-    first = __reduce_add_sync(0xffffffffu, first) - 1;
-    last = __reduce_add_sync(0xffffffffu, last) - 1;
-    if (first == last) {
-      const float2 ml = p.plane_ml[which][at];
-      sum.add(ml.x, ml.y, p.plane_o[which] + at * kHd, lane);
-    } else {
-      sum.pieces(p, first, last, p.lo[first] == start ? 0 : 1, r - rt * kItemRows, lane);
-    }
-  };
-  for (int g0 = 0; g0 < p.list[0].n; g0 += 32) {
-    const int g = g0 + lane;
-    bool here = false;
-    if (g < p.list[0].n) {
-      const int lo = __ldg(p.list[0].starts + g), hi = __ldg(p.list[0].starts + g + 1);
-      here = lo >= 0 && lo <= b && b < hi && static_cast<long long>(hi) * p.q_len <= p.tokens;
-    }
-    const unsigned in = __ballot_sync(0xffffffffu, here);
-    if (in != 0) {
-      list(0, g0 + __ffs(in) - 1);
-      break;
-    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) prefix = max(prefix, __shfl_xor_sync(0xffffffffu, prefix, o));
   }
-  list(1, b);
+  const int units = load_shares(p, grid, lo);
+  RowSum<kHd, kLanes> sum;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int seg = which ? p.list[0].n + b : prefix;
+    int first = 0, last = -1, slot = 0, item_row = 0;
+    const float* plane = nullptr;
+    if (seg >= 0) {
+      const Seg g = read_seg(p, seg, &bad);
+      if (g.tiles > 0) {
+        const int r = (b * p.q_len - g.t0) * group + row, rt = r / kItemRows;
+        item_row = r - rt * kItemRows;
+        const long long start = p.seg_at[seg] + kvh * g.head + static_cast<long long>(rt) * g.full;
+        const long long end = start + (rt == g.row_tiles - 1 ? g.last : g.full);
+        auto shares_below = [&](long long x) {  // how many begin before x
+          int n = 0;
+          for (int step = 256; step > 0; step >>= 1)
+            if (n + step <= units && lo[n + step - 1] < x) n += step;
+          return n;
+        };
+        first = shares_below(start + 1) - 1;
+        last = shares_below(end) - 1;
+        slot = lo[first] == start ? 0 : 1;
+        if (first == last) plane = p.plane_o[which];
+      }
+    }
+    sum.add(p, lo, first, last, slot, item_row, p.plane_ml[which], plane, at, d);
+  }
   if (p.list[1].less > 0) {
     const List& l = p.list[1];
     const int len = seg_len(l, b, &bad);
-    float q[kV];
-#pragma unroll
-    for (int i = 0; i < kV; ++i)
-      q[i] = __uint_as_float(static_cast<uint32_t>(p.q[token * p.q_tok + head * p.q_head + lane * kV + i]) << 16);
+    const uint2 q2 = *reinterpret_cast<const uint2*>(p.q + token * p.q_tok + head * p.q_head + d * kV);
+    const float q[kV] = {bf16_lo(q2.x), bf16_hi(q2.x), bf16_lo(q2.y), bf16_hi(q2.y)};
     const float c = p.softmax_scale * kLog2e * k_scale;
-    for (int x = max(0, p.q_len - len); x < p.q_len; ++x) {
-      const bool sees = p.spec_mask != nullptr
-                            ? p.spec_mask[(static_cast<long long>(b) * p.q_len + tok) * p.q_len + x] != 0
-                            : x <= tok;
-      if (!sees) continue;
+    for (int x = 0; x < p.q_len; ++x) {
       const int key = len - p.q_len + x;
-      int block = __ldg(l.table + static_cast<long long>(b) * l.max_blocks + (key >> p.page_shift));
-      if (block < 0 || block >= p.num_blocks) {
-        if (lane == 0) atomicOr(&g_status_ragged, FP8MLA_DEV_BAD_PAGE);
-        block = 0;
-      }
-      const long long line =
-          ((static_cast<long long>(block) * p.h_kv + kvh) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
-      float kx[kV], vx[kV];
-      if constexpr (kV == 4) {
-        const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(p.k + line * kHd) + lane);
-        const uint32_t d = __ldg(reinterpret_cast<const uint32_t*>(p.v + line * kHd) + lane);
-        const uint32_t h[4] = {e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(d), e4m3x2_to_f16x2(d >> 16)};
-        kx[0] = f16_lo(h[0]), kx[1] = f16_hi(h[0]), kx[2] = f16_lo(h[1]), kx[3] = f16_hi(h[1]);
-        vx[0] = f16_lo(h[2]), vx[1] = f16_hi(h[2]), vx[2] = f16_lo(h[3]), vx[3] = f16_hi(h[3]);
-      } else {
-        const uint32_t a = e4m3x2_to_f16x2(__ldg(reinterpret_cast<const uint16_t*>(p.k + line * kHd) + lane));
-        const uint32_t d = e4m3x2_to_f16x2(__ldg(reinterpret_cast<const uint16_t*>(p.v + line * kHd) + lane));
-        kx[0] = f16_lo(a), kx[1] = f16_hi(a);
-        vx[0] = f16_lo(d), vx[1] = f16_hi(d);
-      }
-      float dot = 0.f;
+      bool sees = key >= 0;
+      if (sees)
+        sees = p.spec_mask != nullptr
+                   ? p.spec_mask[(static_cast<long long>(b) * p.q_len + tok) * p.q_len + x] != 0
+                   : x <= tok;
+      float kx[kV], vx[kV], s = 0.f, sk = 1.f, sv = 1.f;
+      if (sees) {
+        int block = __ldg(l.table + static_cast<long long>(b) * l.max_blocks + (key >> p.page_shift));
+        if (block < 0 || block >= p.num_blocks) {
+          if (d == 0) atomicOr(&g_status_ragged, FP8MLA_DEV_BAD_PAGE);
+          block = 0;
+        }
+        const long long line =
+            ((static_cast<long long>(block) * p.h_kv + kvh) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+        const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(p.k + line * kHd) + d);
+        const uint32_t e = __ldg(reinterpret_cast<const uint32_t*>(p.v + line * kHd) + d);
+        if (scale_rows) sk = __ldg(p.k_scale + line), sv = __ldg(p.v_scale + line);
+        const uint4 h = to_f16(make_uint2(a, e));
+        kx[0] = f16_lo(h.x), kx[1] = f16_hi(h.x), kx[2] = f16_lo(h.y), kx[3] = f16_hi(h.y);
+        vx[0] = f16_lo(h.z), vx[1] = f16_hi(h.z), vx[2] = f16_lo(h.w), vx[3] = f16_hi(h.w);
 #pragma unroll
-      for (int i = 0; i < kV; ++i) dot += q[i] * kx[i];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      float s = dot * c, sv = 1.f;
-      if (scale_rows) {
-        s *= __ldg(p.k_scale + line);
-        sv = __ldg(p.v_scale + line);
+        for (int i = 0; i < kV; ++i) s += q[i] * kx[i];
       }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (!sees) continue;
+      s *= c * sk;
       const float m = s + kLift, top = s == s ? fmaxf(sum.m, m) : fmaxf(sum.m, 0.f);  // the pieces' sums are lifted
       if (top == kNegInf) continue;
       const float a = ex2_approx(sum.m - top), w = ex2_approx(m - top);
@@ -1308,7 +1341,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
       for (int i = 0; i < kV; ++i) sum.acc[i] = sum.acc[i] * a + vx[i] * (w * sv);
     }
   }
-  sum.finish(p.out + at * kHd, p.lse + at, p.sinks ? p.sinks[head] : kNegInf, v_scale, lane);
+  sum.finish(p.out + static_cast<long long>(at) * kHd, p.lse + at, p.sinks ? p.sinks[head] : kNegInf, v_scale, d);
 }
 
 // -------------------------------------------------------------------- host --
@@ -1503,10 +1536,10 @@ fp8mla_status_t cross_entry(const CrossArgs& a, cudaStream_t stream) {
   use(&p, s, a.workspace);
   cudaError_t e = launch_any(p, a.head_dim, a.cache.scale_rows, s.grid, stream);
   if (e == cudaSuccess && s.grid > 1) {
-    const dim3 grid(s.grid, (s.slot_rows + kMergeRows - 1) / kMergeRows);
+    const dim3 grid(s.grid, (s.slot_rows + kCrossRows - 1) / kCrossRows);
     e = a.head_dim == 64
-            ? launch_dependent(cross_merge_kernel<64>, grid, dim3(128), 0, stream, p, a.cache.scale_rows)
-            : launch_dependent(cross_merge_kernel<128>, grid, dim3(128), 0, stream, p, a.cache.scale_rows);
+            ? launch_dependent(cross_merge_kernel<64>, grid, dim3(kMergeThreads), 0, stream, p, a.cache.scale_rows)
+            : launch_dependent(cross_merge_kernel<128>, grid, dim3(kMergeThreads), 0, stream, p, a.cache.scale_rows);
   }
   return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
 }
@@ -1590,10 +1623,13 @@ fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream) {
   use(&p, s, a.workspace);
   cudaError_t e = launch_any(p, a.head_dim, a.cache.scale_rows, s.grid, stream);
   if (e == cudaSuccess) {
-    const dim3 grid(static_cast<unsigned>(a.bs) * a.h_kv, (a.q_len * group + 3) / 4);
-    e = a.head_dim == 64
-            ? launch_dependent(shared_merge_kernel<64>, grid, dim3(128), 0, stream, p, a.cache.scale_rows)
-            : launch_dependent(shared_merge_kernel<128>, grid, dim3(128), 0, stream, p, a.cache.scale_rows);
+    const int total = static_cast<int>(rows);
+    const int each = a.head_dim == 64 ? kSharedRows<64> : kSharedRows<128>;
+    const dim3 grid((total + each - 1) / each), block(kMergeThreads);
+    e = a.head_dim == 64 ? launch_dependent(shared_merge_kernel<64>, grid, block, 0, stream, p, a.cache.scale_rows, s.grid,
+                                            total)
+                         : launch_dependent(shared_merge_kernel<128>, grid, block, 0, stream, p, a.cache.scale_rows,
+                                            s.grid, total);
   }
   return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
 }
