@@ -45,8 +45,9 @@ constexpr uint32_t kNone = 0xFF800000u;  // -inf: the score of a key past the en
 constexpr float kFar = 1048576.f;  // 2^20 in log2 units: up to here the lift and the difference keep their fraction
 constexpr float kTau = 8.f;     // the reference moves when a score passes it by more
 
-// Lengths of the line, in eighths of a tile of 256 rows.
-constexpr int kPairTile = 8, kOneTile = 5, kPairFixed = 12, kOneFixed = 8, kEmpty = 1;
+// Lengths of the line: what a tile takes with up to 256 rows (Params::pair_tile: longer with row scales) and up to 128
+// rows, and an item's beginning and end, in tenths of a microsecond.
+constexpr int kPairTile = 19, kPairRowsTile = 23, kOneTile = 10, kPairFixed = 32, kOneFixed = 22, kEmpty = 2;
 constexpr int kLeast = kPairFixed + 2 * kPairTile;  // of a share
 
 struct List {
@@ -84,7 +85,7 @@ struct Params {
   FastDiv group;
   unsigned long long per_unit;  // 2^64 / grid
   float softmax_scale;
-  int joined, tokens, h_q, h_kv, num_blocks, page_shift, slot_rows, fill_out, fill_lse, q_len;
+  int pair_tile, joined, tokens, h_q, h_kv, num_blocks, page_shift, slot_rows, fill_out, fill_lse, q_len;
 };
 
 // ---------------------------------------------------------------- the line --
@@ -95,34 +96,39 @@ struct Seg {
   long long head;  // of all items of a KV head
 };
 
-__device__ __forceinline__ int seg_len(const List& l, int s, uint32_t* bad) {
-  const int n = __ldg(l.lens + s);
+struct Bounds {  // of a segment, as the caller gives them
+  int a, b, len;
+};
+__device__ __forceinline__ Bounds load_bounds(const Params& p, int s) {
+  const List& l = s < p.list[0].n ? p.list[0] : p.list[1];
+  if (s >= p.list[0].n) s -= p.list[0].n;
+  Bounds x{s, s + 1, __ldg(l.lens + s)};
+  if (l.starts != nullptr) x.a = __ldg(l.starts + s), x.b = __ldg(l.starts + s + 1);
+  return x;
+}
+
+__device__ __forceinline__ int seg_len(const List& l, int n, uint32_t* bad) {
   if (static_cast<uint32_t>(n) <= static_cast<uint32_t>(l.max_keys)) return n;
   *bad = FP8MLA_DEV_BAD_SEQLEN;
   return 0;
 }
 
-__device__ __forceinline__ Seg read_seg(const Params& p, int s, uint32_t* bad) {
+__device__ __forceinline__ Seg make_seg(const Params& p, int s, const Bounds& x, uint32_t* bad) {
   const List& l = s < p.list[0].n ? p.list[0] : p.list[1];
-  if (s >= p.list[0].n) s -= p.list[0].n;
   Seg g;
-  int a = s, b = s + 1;
-  if (l.starts != nullptr) {
-    a = __ldg(l.starts + s);
-    b = __ldg(l.starts + s + 1);
-    if (a < 0 || a > b || b > l.most) {
-      *bad = FP8MLA_DEV_BAD_SEQLEN;
-      a = b = 0;
-    }
+  int a = x.a, b = x.b;
+  if (a < 0 || a > b || b > l.most) {
+    *bad = FP8MLA_DEV_BAD_SEQLEN;
+    a = b = 0;
   }
   g.t0 = a * l.per;
   const int t1 = b * l.per;
   g.rows = (t1 - g.t0) * static_cast<int>(p.group.d);
-  g.keys = max(0, seg_len(l, s, bad) - l.less);
+  g.keys = max(0, seg_len(l, x.len, bad) - l.less);
   g.tiles = (g.keys + kTile - 1) / kTile;
   g.row_tiles = (g.rows + kItemRows - 1) / kItemRows;
   if (g.tiles > 0) {
-    g.full = kPairFixed + g.tiles * kPairTile;
+    g.full = kPairFixed + g.tiles * p.pair_tile;
     g.last = g.rows - (g.row_tiles - 1) * kItemRows > kTile ? g.full : kOneFixed + g.tiles * kOneTile;
   } else {
     g.full = g.last = p.joined ? 0 : kEmpty;
@@ -131,9 +137,13 @@ __device__ __forceinline__ Seg read_seg(const Params& p, int s, uint32_t* bad) {
   return g;
 }
 
+__device__ __forceinline__ Seg read_seg(const Params& p, int s, uint32_t* bad) {
+  return make_seg(p, s, load_bounds(p, s), bad);
+}
+
 // Where a share that would begin `off` into an item of this length does: at a tile, at least `few` from either end.
-__device__ __forceinline__ int cut_at(int off, int len, bool pair, int tiles, int few) {
-  const int fixed = pair ? kPairFixed : kOneFixed, each = pair ? kPairTile : kOneTile;
+__device__ __forceinline__ int cut_at(int off, int len, bool pair, int pair_tile, int tiles, int few) {
+  const int fixed = pair ? kPairFixed : kOneFixed, each = pair ? pair_tile : kOneTile;
   if (tiles == 0) return off > 0 ? len : 0;
   const int t = off <= fixed ? 0 : (off - fixed + each / 2) / each;
   if (t >= few && tiles - t >= few) return fixed + t * each;
@@ -159,32 +169,87 @@ struct Walk {
   bool first;
 };
 
+constexpr int kGroups = 64;  // of segments, whose places on the line are kept
+
 // The beginning of CTA `unit`'s share, by one warp; it is short, as its instructions come from memory in every launch.
-__device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk) {
+// First the line's length, with the places where groups of segments begin; then the segments that hold the share's ends.
+__device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk, long long (&group_at)[kGroups]) {
   const int n = p.list[0].n + p.list[1].n;
   const int lane = threadIdx.x % 32;
+  const int each = ((n + 31) / 32 + kGroups - 1) / kGroups * 32;  // segments a group
   uint32_t bad = 0;
-  int units = 1, few = 1;
-  long long total = 0, raw[2] = {0, 0};
+  // a lane's segment of the 32 from s0 on, and where it begins if those begin at `from`
+  Seg g;
+  auto place = [&](int s0, const Bounds& x, long long from, long long* len, long long* all) {
+    const int s = s0 + lane;
+    *len = 0;
+    if (s < n) {
+      g = make_seg(p, s, x, &bad);
+      *len = g.head * p.h_kv;
+    }
+    long long sum = *len;
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {  // the sum, then where the share's ends are
-    long long from = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    *all = __shfl_sync(0xffffffffu, sum, 31);
+    return from + sum - *len;
+  };
+  long long total = 0, len, all;
+  Bounds x = {};
+  if (n > 0) x = load_bounds(p, min(lane, n - 1));
 #pragma unroll 1
-    for (int s0 = 0; s0 < n; s0 += 32) {
-      const int s = s0 + lane;
-      Seg g = {};
-      if (s < n) g = read_seg(p, s, &bad);
-      const long long len = g.head * p.h_kv;
-      long long sum = len;
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const Bounds now = x;
+    if (s0 + 32 < n) x = load_bounds(p, min(s0 + 32 + lane, n - 1));
+    const long long at = place(s0, now, total, &len, &all);
+    if (lane == 0 && s0 % each == 0) group_at[s0 / each] = total;
+    // the merge looks segments up: a CTA writes the places of some
+    if (p.joined && (s0 >> 5) % gridDim.x == unit && s0 + lane < n) p.seg_at[s0 + lane] = at;
+    total += all;
+  }
+  if (bad && unit == 0) atomicOr(&g_status_ragged, bad);
+  int units, few;
+  long long raw[2];
+  if (total < (1 << 24)) {
+    const uint32_t t = static_cast<uint32_t>(total);
+    units = static_cast<int>(max(1u, min(gridDim.x, t / kLeast)));
+    few = static_cast<int>(t / units / (3 * kPairTile));
+    raw[0] = t * unit / units;
+    raw[1] = t * (unit + 1) / units;
+  } else {
+    units = gridDim.x;
+    few = 4;
+    raw[0] = __umul64hi(total * unit, p.per_unit);  // 2^64 / grid
+    raw[1] = __umul64hi(total * (unit + 1), p.per_unit);
+  }
+  few = max(1, min(4, few));
+  if (unit + 1 >= units) raw[1] = total;
+  if (unit >= units) raw[0] = total;
+  if (lane == 0) {
+    walk->left = raw[0];
+    walk->hi = total;
+    walk->first = true;
+    if (!p.joined) p.cuts[unit].valid = 0;
+    if (unit == units - 1) {
+      p.lo[units] = total;
+      *p.units = units;
+    }
+    if (raw[0] >= total && unit < units) p.lo[unit] = total;
+  }
+  __syncwarp();
+  if (raw[0] < total) {
+    const int groups = (n + each - 1) / each;
+    const uint32_t below = __ballot_sync(0xffffffffu, lane < groups && group_at[lane] <= raw[0]);
+    const uint32_t more = __ballot_sync(0xffffffffu, lane + 32 < groups && group_at[(lane + 32) % kGroups] <= raw[0]);
+    int s0 = (__popc(below) + __popc(more) - 1) * each;
+    long long from = group_at[s0 / each];
+    __syncwarp();
 #pragma unroll 1
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
-      }
-      const long long at = from + sum - len;
-      from += __shfl_sync(0xffffffffu, sum, 31);
-      if (pass == 0) continue;
-      if (s < n && p.joined && unit == 0) p.seg_at[s] = at;  // the merge looks segments up
+    for (; s0 < n && from <= raw[1]; s0 += 32) {
+      const long long at = place(s0, load_bounds(p, min(s0 + lane, n - 1)), from, &len, &all);
+      from += all;
 #pragma unroll 1
       for (int e = 0; e < 2; ++e) {
         const long long want = e ? raw[1] : raw[0];
@@ -195,7 +260,7 @@ __device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk
         const int rest = static_cast<int>(min(in, 0x7FFFFFFFll));
         int rt = min(rest / g.full, g.row_tiles - 1);
         const int item = rt == g.row_tiles - 1 ? g.last : g.full;
-        int off = cut_at(rest - rt * g.full, item, item == g.full && g.tiles > 0, g.tiles, few);
+        int off = cut_at(rest - rt * g.full, item, item == g.full && g.tiles > 0, p.pair_tile, g.tiles, few);
         const long long to = want - in + static_cast<long long>(rt) * g.full + off;
         if (e) {
           walk->hi = to;
@@ -205,7 +270,7 @@ __device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk
             if (++rt == g.row_tiles) rt = 0, ++h;
           }
           walk->g = g;
-          walk->seg = s;
+          walk->seg = s0 + lane;
           walk->head = h;
           walk->rt = rt;
           walk->off = off;
@@ -213,40 +278,6 @@ __device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk
           walk->left = to;  // for now
         }
       }
-      if (!p.joined && from > raw[1]) break;
-    }
-    if (pass == 1) break;
-    total = from;
-    if (total < (1 << 24)) {
-      const uint32_t t = static_cast<uint32_t>(total);
-      units = static_cast<int>(max(1u, min(gridDim.x, t / kLeast)));
-      few = static_cast<int>(t / units / (3 * kPairTile));
-      raw[0] = t * unit / units;
-      raw[1] = t * (unit + 1) / units;
-    } else {
-      units = gridDim.x;
-      few = 4;
-      raw[0] = __umul64hi(total * unit, p.per_unit);  // 2^64 / grid
-      raw[1] = __umul64hi(total * (unit + 1), p.per_unit);
-    }
-    few = max(1, min(4, few));
-    if (unit + 1 >= units) raw[1] = total;
-    if (unit >= units) raw[0] = total;
-    if (lane == 0) {
-      walk->left = raw[0];
-      walk->hi = total;
-      walk->first = true;
-      if (bad && unit == 0) atomicOr(&g_status_ragged, bad);
-      if (!p.joined) p.cuts[unit].valid = 0;
-      if (unit == units - 1) {
-        p.lo[units] = total;
-        *p.units = units;
-      }
-    }
-    __syncwarp();
-    if (raw[0] >= total) {
-      if (lane == 0 && unit < units) p.lo[unit] = raw[0];
-      if (!(p.joined && unit == 0)) break;
     }
   }
   __syncwarp();
@@ -277,7 +308,7 @@ __device__ __forceinline__ bool next_item(const Params& p, int unit, Walk* w, It
   it->rows = rows;
   it->keys = w->g.keys;
   it->form = rows > kTile ? kFormPair : (rows > kFew ? kFormOne : kFormFew);
-  const int fixed = rows > kTile ? kPairFixed : kOneFixed, each = rows > kTile ? kPairTile : kOneTile;
+  const int fixed = rows > kTile ? kPairFixed : kOneFixed, each = rows > kTile ? p.pair_tile : kOneTile;
   const int tile_lo = off > 0 ? (off - fixed) / each : 0;
   const bool ends = len - off <= left;
   const int tile_hi = ends ? tiles : (off + static_cast<int>(left) - fixed) / each;
@@ -327,6 +358,7 @@ struct Control {
   uint64_t item_full[kItems], item_empty[kItems];
   Item item[kItems];
   Walk walk;
+  long long group_at[kGroups];
   uint32_t tmem_base, abort_flag, never;  // never: the flag of waits that no other warp ends
   uint32_t sums_read;            // warps that are done with a few-row item's sums
   int8_t q_exp[2][kTile];        // of Q's rows, by stream
@@ -1098,7 +1130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_wait(full + j % ring, (j / ring) & 1, &sm->never);
     } else if (warp == 14) {
       // ------------------------------------------------- the share's items --
-      find_share(p, unit, &sm->walk);
+      find_share(p, unit, &sm->walk, sm->group_at);
       bool more = true;
 #pragma unroll 1
       for (uint32_t n = 0; more; ++n) {
@@ -1299,7 +1331,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   }
   if (p.list[1].less > 0) {
     const List& l = p.list[1];
-    const int len = seg_len(l, b, &bad);
+    const int len = seg_len(l, __ldg(l.lens + b), &bad);
     const uint2 q2 = *reinterpret_cast<const uint2*>(p.q + token * p.q_tok + head * p.q_head + d * kV);
     const float q[kV] = {bf16_lo(q2.x), bf16_hi(q2.x), bf16_lo(q2.y), bf16_hi(q2.y)};
     const float c = p.softmax_scale * kLog2e * k_scale;
@@ -1356,7 +1388,7 @@ struct Space {  // the workspace: offsets, and the grid it is for
 // tokens and segments of a list that reads up to max_keys keys a segment
 long long most_work(long long tokens, long long segs, int h_kv, int group, long long max_keys) {
   const long long tiles = (max_keys + kTile - 1) / kTile;
-  return h_kv * (tokens * group / kItemRows + segs) * (kPairFixed + kPairTile * std::max(tiles, 1ll));
+  return h_kv * (tokens * group / kItemRows + segs) * (kPairFixed + kPairRowsTile * std::max(tiles, 1ll));
 }
 
 Space lay_out(long long work, long long tokens, int segs, int h_q, int group, int hd, bool joined) {
@@ -1475,6 +1507,7 @@ void fill_cache(Params* p, const RaggedCache& c) {
   p->k_scale = c.k_scale;
   p->v_scale = c.v_scale;
   p->num_blocks = c.num_blocks;
+  p->pair_tile = c.scale_rows ? kPairRowsTile : kPairTile;
 }
 
 constexpr long long kMostKeys = 1ll << 30;  // a segment
