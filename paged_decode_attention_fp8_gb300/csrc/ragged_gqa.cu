@@ -45,10 +45,19 @@ constexpr uint32_t kNone = 0xFF800000u;  // -inf: the score of a key past the en
 constexpr float kFar = 1048576.f;  // 2^20 in log2 units: up to here the lift and the difference keep their fraction
 constexpr float kTau = 8.f;     // the reference moves when a score passes it by more
 
-// Lengths of the line: what a tile takes with up to 256 rows (Params::pair_tile: longer with row scales) and up to 128
-// rows, and an item's beginning and end, in tenths of a microsecond.
-constexpr int kPairTile = 19, kPairRowsTile = 23, kOneTile = 10, kPairFixed = 32, kOneFixed = 22, kEmpty = 2;
-constexpr int kLeast = kPairFixed + 2 * kPairTile;  // of a share
+// Up to 32 rows lie in all quarters (few), up to 128 are one stream, up to 256 a pair of streams.
+constexpr int kFew = 32;
+enum { kFormPair = 0, kFormOne = 1, kFormFew = 2, kForms = 3 };
+
+// Lengths of the line, in twentieths of a microsecond: what a key tile takes, and an item's beginning and end, by form.
+// Measured as the shares' ends over their items and tiles (decode steps, prompts and prefixes of either kind).
+struct Lengths {
+  int each[kForms], fixed[kForms];
+};
+constexpr Lengths kLengths[2][2] = {{{{24, 24, 13}, {60, 30, 26}}, {{42, 34, 15}, {56, 31, 28}}},    // head_dim 64
+                                    {{{37, 26, 16}, {80, 45, 33}}, {{46, 35, 20}, {90, 58, 38}}}};  // 128: plain, row scales
+constexpr int kEmpty = 4;   // an item without keys
+constexpr int kLeast = 60;  // a share
 
 struct List {
   const int32_t* starts;  // segment s has the tokens [per starts[s], per starts[s + 1]); null: [per s, per (s + 1))
@@ -85,7 +94,8 @@ struct Params {
   FastDiv group;
   unsigned long long per_unit;  // 2^64 / grid
   float softmax_scale;
-  int pair_tile, joined, tokens, h_q, h_kv, num_blocks, page_shift, slot_rows, fill_out, fill_lse, q_len;
+  Lengths lengths;
+  int joined, tokens, h_q, h_kv, num_blocks, page_shift, slot_rows, fill_out, fill_lse, q_len;
 };
 
 // ---------------------------------------------------------------- the line --
@@ -95,6 +105,10 @@ struct Seg {
   int full, last;  // length of an item of 256 rows and of the last one
   long long head;  // of all items of a KV head
 };
+
+__device__ __forceinline__ int form_of(int rows) {
+  return rows > kTile ? kFormPair : (rows > kFew ? kFormOne : kFormFew);
+}
 
 struct Bounds {  // of a segment, as the caller gives them
   int a, b, len;
@@ -127,11 +141,11 @@ __device__ __forceinline__ Seg make_seg(const Params& p, int s, const Bounds& x,
   g.keys = max(0, seg_len(l, x.len, bad) - l.less);
   g.tiles = (g.keys + kTile - 1) / kTile;
   g.row_tiles = (g.rows + kItemRows - 1) / kItemRows;
+  g.full = g.last = p.joined ? 0 : kEmpty;
   if (g.tiles > 0) {
-    g.full = kPairFixed + g.tiles * p.pair_tile;
-    g.last = g.rows - (g.row_tiles - 1) * kItemRows > kTile ? g.full : kOneFixed + g.tiles * kOneTile;
-  } else {
-    g.full = g.last = p.joined ? 0 : kEmpty;
+    const int form = form_of(g.rows - (g.row_tiles - 1) * kItemRows);
+    g.full = p.lengths.fixed[kFormPair] + g.tiles * p.lengths.each[kFormPair];
+    g.last = p.lengths.fixed[form] + g.tiles * p.lengths.each[form];
   }
   g.head = g.row_tiles > 0 ? static_cast<long long>(g.row_tiles - 1) * g.full + g.last : 0;
   return g;
@@ -142,8 +156,9 @@ __device__ __forceinline__ Seg read_seg(const Params& p, int s, uint32_t* bad) {
 }
 
 // Where a share that would begin `off` into an item of this length does: at a tile, at least `few` from either end.
-__device__ __forceinline__ int cut_at(int off, int len, bool pair, int pair_tile, int tiles, int few) {
-  const int fixed = pair ? kPairFixed : kOneFixed, each = pair ? pair_tile : kOneTile;
+__device__ __forceinline__ int cut_at(const Params& p, int off, int len, int form, int tiles, int few) {
+  const int fixed = p.lengths.fixed[form], each = p.lengths.each[form];
+  if (form != kFormPair) few = min(few, 2);  // little is written and merged
   if (tiles == 0) return off > 0 ? len : 0;
   const int t = off <= fixed ? 0 : (off - fixed + each / 2) / each;
   if (t >= few && tiles - t >= few) return fixed + t * each;
@@ -157,8 +172,6 @@ struct Item {
   int form;
   bool end;
 };
-constexpr int kFew = 32;                         // rows that lie in all quarters
-enum { kFormPair = 0, kFormOne = 1, kFormFew = 2 };
 constexpr int kDirect = -1, kPlane = -2;
 
 // Where a share is: the segment, the item, how far into it, and how much is left.
@@ -215,7 +228,7 @@ __device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk
   if (total < (1 << 24)) {
     const uint32_t t = static_cast<uint32_t>(total);
     units = static_cast<int>(max(1u, min(gridDim.x, t / kLeast)));
-    few = static_cast<int>(t / units / (3 * kPairTile));
+    few = static_cast<int>(t / units / (3u * p.lengths.each[kFormPair]));
     raw[0] = t * unit / units;
     raw[1] = t * (unit + 1) / units;
   } else {
@@ -260,7 +273,7 @@ __device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk
         const int rest = static_cast<int>(min(in, 0x7FFFFFFFll));
         int rt = min(rest / g.full, g.row_tiles - 1);
         const int item = rt == g.row_tiles - 1 ? g.last : g.full;
-        int off = cut_at(rest - rt * g.full, item, item == g.full && g.tiles > 0, p.pair_tile, g.tiles, few);
+        int off = cut_at(p, rest - rt * g.full, item, form_of(g.rows - rt * kItemRows), g.tiles, few);
         const long long to = want - in + static_cast<long long>(rt) * g.full + off;
         if (e) {
           walk->hi = to;
@@ -307,8 +320,9 @@ __device__ __forceinline__ bool next_item(const Params& p, int unit, Walk* w, It
   it->row0 = row0;
   it->rows = rows;
   it->keys = w->g.keys;
-  it->form = rows > kTile ? kFormPair : (rows > kFew ? kFormOne : kFormFew);
-  const int fixed = rows > kTile ? kPairFixed : kOneFixed, each = rows > kTile ? p.pair_tile : kOneTile;
+  const int form = form_of(rows);
+  it->form = form;
+  const int fixed = p.lengths.fixed[form], each = p.lengths.each[form];
   const int tile_lo = off > 0 ? (off - fixed) / each : 0;
   const bool ends = len - off <= left;
   const int tile_hi = ends ? tiles : (off + static_cast<int>(left) - fixed) / each;
@@ -1388,7 +1402,7 @@ struct Space {  // the workspace: offsets, and the grid it is for
 // tokens and segments of a list that reads up to max_keys keys a segment
 long long most_work(long long tokens, long long segs, int h_kv, int group, long long max_keys) {
   const long long tiles = (max_keys + kTile - 1) / kTile;
-  return h_kv * (tokens * group / kItemRows + segs) * (kPairFixed + kPairRowsTile * std::max(tiles, 1ll));
+  return h_kv * (tokens * group / kItemRows + segs) * (100 + 50 * std::max(tiles, 1ll));  // at most
 }
 
 Space lay_out(long long work, long long tokens, int segs, int h_q, int group, int hd, bool joined) {
@@ -1501,13 +1515,13 @@ bool heads_ok(int h_q, int h_kv, int head_dim) {
   return (head_dim == 64 || head_dim == 128) && h_q >= 1 && h_kv >= 1 && h_q % h_kv == 0 && h_q <= 65536;
 }
 
-void fill_cache(Params* p, const RaggedCache& c) {
+void fill_cache(Params* p, const RaggedCache& c, int head_dim) {
   p->k = static_cast<const uint8_t*>(c.k);
   p->v = static_cast<const uint8_t*>(c.v);
   p->k_scale = c.k_scale;
   p->v_scale = c.v_scale;
   p->num_blocks = c.num_blocks;
-  p->pair_tile = c.scale_rows ? kPairRowsTile : kPairTile;
+  p->lengths = kLengths[head_dim == 128][c.scale_rows != 0];
 }
 
 constexpr long long kMostKeys = 1ll << 30;  // a segment
@@ -1553,7 +1567,7 @@ fp8mla_status_t cross_entry(const CrossArgs& a, cudaStream_t stream) {
       rows_overlap(out, lse) || rows_overlap(out, ws) || rows_overlap(lse, ws))
     return FP8MLA_ERR_INVALID_ARG;
   p.q = static_cast<const uint16_t*>(a.q);
-  fill_cache(&p, a.cache);
+  fill_cache(&p, a.cache, a.head_dim);
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
   p.q_tok = a.q_token, p.q_head = a.q_head, p.o_tok = a.out_token, p.o_head = a.out_head;
@@ -1634,7 +1648,7 @@ fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream) {
       rows_overlap(out, ws) || rows_overlap(lse, ws))
     return FP8MLA_ERR_INVALID_ARG;
   p.q = static_cast<const uint16_t*>(a.q);
-  fill_cache(&p, a.cache);
+  fill_cache(&p, a.cache, a.head_dim);
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
   p.q_tok = p.o_tok = static_cast<long long>(a.h_q) * a.head_dim;
