@@ -55,8 +55,8 @@ struct Lengths {
   int each[kForms], fixed[kForms];
 };
 constexpr Lengths kLengths[2][2] = {{{{24, 24, 13}, {60, 30, 26}}, {{42, 34, 15}, {56, 31, 28}}},    // head_dim 64
-                                    {{{37, 26, 16}, {80, 45, 33}}, {{46, 35, 20}, {90, 58, 38}}}};  // 128: plain, row scales
-constexpr int kEmpty = 4;   // an item without keys
+                                    {{{37, 26, 18}, {80, 45, 38}}, {{52, 35, 20}, {95, 58, 38}}}};  // 128: plain, row scales
+constexpr int kEmpty = 15;  // an item without keys
 constexpr int kLeast = 60;  // a share
 
 struct List {
