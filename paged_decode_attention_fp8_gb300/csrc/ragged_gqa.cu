@@ -209,14 +209,14 @@ __device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk
     *all = __shfl_sync(0xffffffffu, sum, 31);
     return from + sum - *len;
   };
-  long long total = 0, len, all;
+  long long total = 0, at = 0, len = 0, all;
   Bounds x = {};
   if (n > 0) x = load_bounds(p, min(lane, n - 1));
 #pragma unroll 1
   for (int s0 = 0; s0 < n; s0 += 32) {
     const Bounds now = x;
     if (s0 + 32 < n) x = load_bounds(p, min(s0 + 32 + lane, n - 1));
-    const long long at = place(s0, now, total, &len, &all);
+    at = place(s0, now, total, &len, &all);
     if (lane == 0 && s0 % each == 0) group_at[s0 / each] = total;
     // the merge looks segments up: a CTA writes the places of some
     if (p.joined && (s0 >> 5) % gridDim.x == unit && s0 + lane < n) p.seg_at[s0 + lane] = at;
@@ -261,29 +261,35 @@ __device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk
     __syncwarp();
 #pragma unroll 1
     for (; s0 < n && from <= raw[1]; s0 += 32) {
-      const long long at = place(s0, load_bounds(p, min(s0 + lane, n - 1)), from, &len, &all);
+      all = total;
+      if (n > 32) at = place(s0, load_bounds(p, min(s0 + lane, n - 1)), from, &len, &all);
       from += all;
-#pragma unroll 1
-      for (int e = 0; e < 2; ++e) {
-        const long long want = e ? raw[1] : raw[0];
-        if (want < at || want >= at + len) continue;
-        long long in = want - at;
+      // lane 0 takes the share's beginning, lane 1 its end
+      const uint32_t begins = __ballot_sync(0xffffffffu, raw[0] >= at && raw[0] < at + len);
+      const uint32_t ends = __ballot_sync(0xffffffffu, raw[1] >= at && raw[1] < at + len);
+      const uint32_t mine = lane == 0 ? begins : ends;
+      const int src = max(__ffs(mine) - 1, 0);
+      if ((begins >> lane) & 1) walk->g = g, walk->seg = s0 + lane;
+      const long long want = lane == 0 ? raw[0] : raw[1], head = __shfl_sync(0xffffffffu, g.head, src);
+      long long in = want - __shfl_sync(0xffffffffu, at, src);
+      const int full = __shfl_sync(0xffffffffu, g.full, src), last = __shfl_sync(0xffffffffu, g.last, src);
+      const int rows = __shfl_sync(0xffffffffu, g.rows, src), row_tiles = __shfl_sync(0xffffffffu, g.row_tiles, src);
+      const int tiles = __shfl_sync(0xffffffffu, g.tiles, src);
+      if (lane < 2 && mine != 0) {
         int h = 0;
-        while (in >= g.head) in -= g.head, ++h;
+        while (in >= head) in -= head, ++h;
         const int rest = static_cast<int>(min(in, 0x7FFFFFFFll));
-        int rt = min(rest / g.full, g.row_tiles - 1);
-        const int item = rt == g.row_tiles - 1 ? g.last : g.full;
-        int off = cut_at(p, rest - rt * g.full, item, form_of(g.rows - rt * kItemRows), g.tiles, few);
-        const long long to = want - in + static_cast<long long>(rt) * g.full + off;
-        if (e) {
+        int rt = min(rest / full, row_tiles - 1);
+        const int item = rt == row_tiles - 1 ? last : full;
+        int off = cut_at(p, rest - rt * full, item, form_of(rows - rt * kItemRows), tiles, few);
+        const long long to = want - in + static_cast<long long>(rt) * full + off;
+        if (lane == 1) {
           walk->hi = to;
         } else {
           if (off == item) {  // the next item's beginning
             off = 0;
-            if (++rt == g.row_tiles) rt = 0, ++h;
+            if (++rt == row_tiles) rt = 0, ++h;
           }
-          walk->g = g;
-          walk->seg = s0 + lane;
           walk->head = h;
           walk->rt = rt;
           walk->off = off;
