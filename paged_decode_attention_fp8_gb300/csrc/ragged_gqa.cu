@@ -58,6 +58,7 @@ constexpr Lengths kLengths[2][2] = {{{{24, 24, 13}, {60, 30, 26}}, {{42, 34, 15}
                                     {{{37, 26, 18}, {80, 45, 38}}, {{52, 35, 20}, {95, 58, 38}}}};  // 128: plain, row scales
 constexpr int kEmpty = 15;  // an item without keys
 constexpr int kLeast = 60;  // a share
+constexpr int kMostUnits = 256;  // shares (one an SM)
 
 struct List {
   const int32_t* starts;  // segment s has the tokens [per starts[s], per starts[s + 1]); null: [per s, per (s + 1))
@@ -225,7 +226,7 @@ __device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk
   if (bad && unit == 0) atomicOr(&g_status_ragged, bad);
   int units, few;
   long long raw[2];
-  if (total < (1 << 24)) {
+  if (total < (1 << 24)) {  // times 256 shares: 32 bits
     const uint32_t t = static_cast<uint32_t>(total);
     units = static_cast<int>(max(1u, min(gridDim.x, t / kLeast)));
     few = static_cast<int>(t / units / (3u * p.lengths.each[kFormPair]));
@@ -278,11 +279,14 @@ __device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk
       if (lane < 2 && mine != 0) {
         int h = 0;
         while (in >= head) in -= head, ++h;
-        const int rest = static_cast<int>(min(in, 0x7FFFFFFFll));
-        int rt = min(rest / full, row_tiles - 1);
+        // in / full, of up to 2^22 items: the quotient in 24 bits, then put right (a 64-bit division would be a call)
+        int rt = min(static_cast<int>(__fdividef(static_cast<float>(in), static_cast<float>(full))), row_tiles - 1);
+        while (rt > 0 && static_cast<long long>(rt) * full > in) --rt;
+        while (rt < row_tiles - 1 && static_cast<long long>(rt + 1) * full <= in) ++rt;
+        const long long before = static_cast<long long>(rt) * full;
         const int item = rt == row_tiles - 1 ? last : full;
-        int off = cut_at(p, rest - rt * full, item, form_of(rows - rt * kItemRows), tiles, few);
-        const long long to = want - in + static_cast<long long>(rt) * full + off;
+        int off = cut_at(p, static_cast<int>(in - before), item, form_of(rows - rt * kItemRows), tiles, few);
+        const long long to = want - in + before + off;
         if (lane == 1) {
           walk->hi = to;
         } else {
@@ -1261,8 +1265,6 @@ struct RowSum {
   }
 };
 
-constexpr int kMostUnits = 512;  // shares (one an SM)
-
 // Where the shares begin, in shared memory; how many there are.
 __device__ __forceinline__ int load_shares(const Params& p, int grid, long long* lo) {
   for (int v = threadIdx.x; v <= grid; v += kMergeThreads) lo[v] = p.lo[v];  // (past the last share: anything)
@@ -1406,14 +1408,14 @@ struct Space {  // the workspace: offsets, and the grid it is for
 };
 
 // tokens and segments of a list that reads up to max_keys keys a segment
-long long most_work(long long tokens, long long segs, int h_kv, int group, long long max_keys) {
+double most_work(long long tokens, long long segs, int h_kv, int group, long long max_keys) {
   const long long tiles = (max_keys + kTile - 1) / kTile;
-  return h_kv * (tokens * group / kItemRows + segs) * (100 + 50 * std::max(tiles, 1ll));  // at most
+  return static_cast<double>(h_kv) * (tokens * group / kItemRows + segs) * (100 + 52 * std::max(tiles, 1ll));  // at most
 }
 
-Space lay_out(long long work, long long tokens, int segs, int h_q, int group, int hd, bool joined) {
+Space lay_out(double work, long long tokens, int segs, int h_q, int group, int hd, bool joined) {
   Space s;
-  s.grid = static_cast<int>(std::max(1ll, std::min<long long>(device_sms(), work / (kLeast))));
+  s.grid = static_cast<int>(std::max(1.0, std::min<double>(std::min(device_sms(), kMostUnits), work / kLeast)));
   s.slot_rows = static_cast<int>(std::min<long long>(kItemRows, std::max(1ll, tokens * group)));
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -1598,7 +1600,7 @@ fp8mla_status_t cross_entry(const CrossArgs& a, cudaStream_t stream) {
 }
 
 namespace ragged {
-long long shared_work(int bs, int q_len, int h_kv, int group, int n_prefixes, long long max_prefix_keys,
+double shared_work(int bs, int q_len, int h_kv, int group, int n_prefixes, long long max_prefix_keys,
                       long long max_keys) {
   const long long tokens = static_cast<long long>(bs) * q_len;
   return (n_prefixes > 0 ? most_work(tokens, n_prefixes, h_kv, group, max_prefix_keys) : 0) +

@@ -244,3 +244,25 @@ def test_no_tokens_and_no_sequences():
                                         q_starts=torch.zeros(1, dtype=torch.int32, device=DEV))
     assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
     assert fm.last_device_error() == 0
+
+
+def test_a_line_past_32_bits():
+    """One head's items add up to more than 2^31 of the units in which work is shared: 11250 of 8192 tiles.
+
+    512 times the same 2048 keys leave the output as it is and lift lse by log 512.  Either output is off by half a step
+    of bf16, 2^-8 of it, and 2^-11 of the largest value for P in f16; the long sum also by its 65536 additions of 16 keys
+    in 32 bits (2^-23 each of the sum of |p v|, if they truncate), its l by 8192 of them (2^-24).
+    """
+    tokens, h_q, hd, page = 45000, 64, 64, 256
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    k, v = (torch.randn(8, 1, page, hd, generator=gen, device=DEV).to(torch.float8_e4m3fn) for _ in range(2))
+    q = (3 * torch.randn(tokens, h_q, hd, generator=gen, device=DEV)).to(torch.bfloat16)
+    table = (torch.arange(4096, device=DEV, dtype=torch.int32) % 8)[None].contiguous()
+    one, starts = torch.ones(1, device=DEV), torch.tensor([0, tokens], dtype=torch.int32, device=DEV)
+    short, long = (fm.paged_cross_attention(q, k, v, table, torch.tensor([n], dtype=torch.int32, device=DEV), one, one,
+                                            softmax_scale=hd ** -0.5, q_starts=starts) for n in (2048, 1 << 20))
+    want, got = short[0].float(), long[0].float()
+    largest = float(v.float().abs().max())
+    assert bool(((got - want).abs() <= want.abs() * 2 ** -7 + largest * (2 ** -10 + 2 ** -7)).all())
+    assert float((long[1] - short[1] - np.log(512)).abs().max()) <= 2 ** -10
+    assert fm.last_device_error() == 0
