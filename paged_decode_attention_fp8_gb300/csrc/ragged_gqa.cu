@@ -1305,7 +1305,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   __shared__ long long lo[kMostUnits + 1];
   const int d = threadIdx.x % kLanes;
   const int group = static_cast<int>(p.group.d), rows = p.q_len * group;
-  const int of_all = min(blockIdx.x * kSharedRows<kHd> + static_cast<int>(threadIdx.x) / kLanes, total - 1);  // (the last again)
+  // (lanes past the last row compute it again and write nothing: it may lie where Q did)
+  const int mine = blockIdx.x * kSharedRows<kHd> + static_cast<int>(threadIdx.x) / kLanes, of_all = min(mine, total - 1);
   const int pair = of_all / rows, row = of_all - pair * rows;
   const int b = pair / p.h_kv, kvh = pair - b * p.h_kv;
   const int tok = row / group, head = kvh * group + row - tok * group;
@@ -1395,6 +1396,7 @@ __global__ void __launch_bounds__(kMergeThreads)
       for (int i = 0; i < kV; ++i) sum.acc[i] = sum.acc[i] * a + vx[i] * (w * sv);
     }
   }
+  if (mine >= total) return;
   sum.finish(p.out + static_cast<long long>(at) * kHd, p.lse + at, p.sinks ? p.sinks[head] : kNegInf, v_scale, d);
 }
 

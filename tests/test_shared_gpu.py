@@ -178,3 +178,16 @@ def test_a_step_with_the_other_calls():
     for o, l in (joined, whole):
         assert np.all(np.abs(o.double().cpu().numpy() - want[0]) <= 2.0 ** -7 * np.abs(want[0]) + 2.0 ** -6 * want[2])
         assert np.all(np.abs(l.double().cpu().numpy() - want[1]) <= 1e-3)
+
+
+@pytest.mark.parametrize("hd,h_q,bs", [(64, 3, 1), (64, 3, 3), (128, 3, 1), (128, 1, 3)])
+def test_blocks_in_place_of_odd_numbers_of_rows(hd, h_q, bs):
+    """Blocks whose result takes the queries' place, with rows that are no multiple of what a thread block joins."""
+    lens = [40, 3, 130][:bs]
+    pool, q, m, s, want = inputs.shared_case(9, [70], [0, bs], lens, 1, h_q, hd, 16, False, 3, True)
+    first = _call(pool, q, [70], [0, bs], lens, m, s)
+    assert inputs.within(*first, want, 200) is None
+    for _ in range(20):
+        here = q.to(DEV)
+        out, lse = _call(pool, here, [70], [0, bs], lens, m, s, out=here)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
