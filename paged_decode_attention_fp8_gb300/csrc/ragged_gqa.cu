@@ -37,7 +37,7 @@
 //
 // Measured (GB300, calls from a graph over three inputs): 2048 tokens x 32 heads by 16384 keys of 8 heads, head_dim 128,
 // 380 us = 1446 TFLOP/s, 0.76 of a library bf16 product; 64 tokens by 128 to 1600 keys with row scales 50 us, by 16000
-// keys 5.4 TB/s, 0.79 of a copy; one token by 777 keys 14 us; 64 sequences behind a prefix of 32768 keys 82 us.
+// keys 5.4 TB/s, 0.79 of a copy; one token by 777 keys 14 us; 64 sequences behind a prefix of 32768 keys 80 us.
 // In the first of them the tensor pipe is active 61 to 63 % of the time, XU 31, ALU 25, DRAM 2: no unit is full.  A tile
 // takes either stream about 3400 cycles for 2048 of the tensor core: product, scores loaded (220), weighed (1150), P
 // written (250), the issuing warp's turn (600), product with P and the next with K, each queued behind the other
@@ -116,7 +116,7 @@ struct Params {
   const float* sinks;
   long long q_tok, q_head, o_tok, o_head;
   List list[2];
-  FastDiv group;
+  FastDiv group, of_rows, of_heads;  // of_rows: a sequence's of a KV head
   unsigned long long per_unit;  // 2^64 / grid
   float softmax_scale;
   Lengths lengths;
@@ -1223,38 +1223,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 //
 // exp2(m_i - m) weighs the pieces' sums and rows, m their largest reference.  Bound by latency: the pieces were just
 // written and lie in L2, so what counts is that all of a row's pieces are asked for at once (a lane holds one piece's
-// weight and tells it to the others): 8-piece rounds took prompts from 49 to 39 us.  Cold under a profiler cross_merge
-// takes 5 to 7 us, shared_merge 8.5 (64 rows a head) to 17 (256).
+// weight and tells it to the others; prompts 49 -> 39 us), the pieces of a row's prefix with those of its own keys, and
+// that the code is short (shared_merge 22 KB -> 15: shared batch 82 -> 80 us).  Cold under a profiler cross_merge takes 5
+// to 6 us, shared_merge 8 (128 rows) to 16 (6144 with blocks of four keys).
 
 constexpr int kMergeThreads = 128;
-// Lanes a row: eight where an item's 256 rows are merged, few pieces each; four dims a lane where rows are few and their
-// prefix lies in many pieces.
+// Lanes a row: eight where an item's 256 rows are merged, few pieces each.  Behind shared prefixes four dims a lane where
+// rows are few and their prefix lies in many pieces (2048 rows of 12 pieces: a call 80 us, with eight dims 85), eight
+// where at four the thread blocks would not all be resident, eight on each of 152 SMs, 32 rows of 128 dims an SM (6144 and
+// 8192 rows: 96 -> 91 us, 137 -> 134).
 constexpr int kCrossRows = kMergeThreads / 8;
-template <int kHd>
-constexpr int kSharedRows = kMergeThreads * 4 / kHd;
+template <int kHd, int kV>
+constexpr int kSharedRows = kMergeThreads * kV / kHd;
+
+// A row's share of an item's pieces, in `count` shares from `first` on: the first in slot `slot` of its share, the others
+// in slot 0, in row `row` of the slot; an item of one share that is whole lies in row `row` of a plane (ml, o) instead.
+struct Pieces {
+  int first = 0, count = 0, slot = 0, row = 0;
+  const float2* ml = nullptr;
+  const float* o = nullptr;
+};
 
 // A row's sum, by kLanes lanes: lane d of them owns dims [kV d, kV d + kV).
 template <int kHd, int kLanes>
 struct RowSum {
   static constexpr int kV = kHd / kLanes;
+  static constexpr int kBatch = kV == 16 ? 2 : 4;  // pieces in flight
   float m = kNegInf, l = 0.f, acc[kV] = {};
 
-  // The pieces of an item in the shares [first, last] (none: last < first): the first in slot `slot` of its share, the
-  // others in slot 0; an item of one share that is whole lies in the plane instead (plane_o).  lo: where the shares
-  // begin.  All lanes of the warp together.
-  __device__ __forceinline__ void add(const Params& p, const long long* lo, int first, int last, int slot, int row,
-                                      const float2* plane_ml, const float* plane_o, int at, int d) {
-    const int count = last - first + 1;
+  // Adds the pieces of up to two items (all lanes of the warp together).  lo: where the shares begin.
+  __device__ __forceinline__ void add(const Params& p, const long long* lo, const Pieces& x, const Pieces& y, int d) {
+    const int count = x.count + y.count;
     const int most = __reduce_max_sync(0xffffffffu, count);
-    const float* from = plane_o != nullptr ? plane_o : p.slot_o;
 #pragma unroll 1
     for (int base = 0; base < most; base += kLanes) {
-      const int v = first + base + d;
-      bool ok = base + d < count;
-      if (ok && plane_o == nullptr && v > first && lo[v + 1] <= lo[v]) ok = false;  // a share without work
-      const int idx = plane_o != nullptr ? at : (2 * v + (v == first ? slot : 0)) * p.slot_rows + row;
+      // a lane's piece
+      const int i = base + d;
+      const bool second = i >= x.count;
+      const int j = second ? i - x.count : i, v = (second ? y.first : x.first) + j;
+      const float* plane = second ? y.o : x.o;
+      bool ok = i < count;
+      if (ok && plane == nullptr && j > 0 && lo[v + 1] <= lo[v]) ok = false;  // a share without work
+      const long long idx = plane != nullptr ? (second ? y.row : x.row)
+                                             : (2 * v + (j == 0 ? (second ? y.slot : x.slot) : 0)) * p.slot_rows +
+                                                   (second ? y.row : x.row);
+      const float* at = (plane != nullptr ? plane : p.slot_o) + idx * kHd;
       float2 ml = make_float2(kNegInf, 0.f);
-      if (ok) ml = (plane_o != nullptr ? plane_ml : p.slot_ml)[idx];
+      if (ok) ml = (plane != nullptr ? (second ? y.ml : x.ml) : p.slot_ml)[idx];
       float top = fmaxf(m, ml.x);
 #pragma unroll
       for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -1267,17 +1282,29 @@ struct RowSum {
       l = l * a + add_l;
 #pragma unroll
       for (int i = 0; i < kV; ++i) acc[i] *= a;
+      // batches without a remainder, as long code comes from memory in every launch
+      const uint32_t there = __ballot_sync(0xffffffffu, ok) >> (threadIdx.x % 32 - d);
       const int n = min(kLanes, most - base);
-#pragma unroll 4
-      for (int q = 0; q < n; ++q) {
-        const float wq = __shfl_sync(0xffffffffu, w, q, kLanes);
-        const int iq = __shfl_sync(0xffffffffu, idx, q, kLanes);
-        if (__shfl_sync(0xffffffffu, ok, q, kLanes)) {
-          const float4* x = reinterpret_cast<const float4*>(from + static_cast<long long>(iq) * kHd + d * kV);
+#pragma unroll 1
+      for (int q = 0; q < n; q += kBatch) {
+        float4 z[kBatch][kV / 4];
+        float wq[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          wq[e] = __shfl_sync(0xffffffffu, w, q + e, kLanes);
+          const unsigned long long from = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), q + e, kLanes);
 #pragma unroll
           for (int i = 0; i < kV / 4; ++i) {
-            const float4 y = __ldcg(x + i);
-            acc[4 * i] += y.x * wq, acc[4 * i + 1] += y.y * wq, acc[4 * i + 2] += y.z * wq, acc[4 * i + 3] += y.w * wq;
+            z[e][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if ((there >> (q + e)) & 1) z[e][i] = __ldcg(reinterpret_cast<const float4*>(from) + d * (kV / 4) + i);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+#pragma unroll
+          for (int i = 0; i < kV / 4; ++i) {
+            acc[4 * i] += z[e][i].x * wq[e], acc[4 * i + 1] += z[e][i].y * wq[e];
+            acc[4 * i + 2] += z[e][i].z * wq[e], acc[4 * i + 3] += z[e][i].w * wq[e];
           }
         }
       }
@@ -1297,6 +1324,7 @@ struct RowSum {
 
 // Where the shares begin, in shared memory; how many there are.
 __device__ __forceinline__ int load_shares(const Params& p, int grid, long long* lo) {
+#pragma unroll 2
   for (int v = threadIdx.x; v <= grid; v += kMergeThreads) lo[v] = p.lo[v];  // (past the last share: anything)
   const int units = *p.units;
   __syncthreads();
@@ -1304,7 +1332,7 @@ __device__ __forceinline__ int load_shares(const Params& p, int grid, long long*
 }
 
 template <int kHd>
-__global__ void __launch_bounds__(kMergeThreads) cross_merge_kernel(const __grid_constant__ Params p, int scale_rows) {
+__global__ void __launch_bounds__(kMergeThreads, 8) cross_merge_kernel(const __grid_constant__ Params p, int scale_rows) {
   griddep_wait();
   __shared__ long long lo[kMostUnits + 1];
   const int unit = blockIdx.x, row0 = blockIdx.y * kCrossRows;
@@ -1316,8 +1344,10 @@ __global__ void __launch_bounds__(kMergeThreads) cross_merge_kernel(const __grid
   while (last + 1 < units && lo[last + 1] < cut.end) ++last;
   const int d = threadIdx.x % 8, row = row0 + threadIdx.x / 8;
   const bool live = row < cut.rows;
+  Pieces pieces;
+  pieces.first = unit, pieces.count = live ? last - unit + 1 : 0, pieces.slot = cut.slot & 1, pieces.row = row;
   RowSum<kHd, 8> sum;
-  sum.add(p, lo, unit, live ? last : unit - 1, cut.slot & 1, row, nullptr, nullptr, 0, d);
+  sum.add(p, lo, pieces, Pieces(), d);
   if (!live) return;
   const uint32_t r = static_cast<uint32_t>(cut.row0 + row), t = fast_div(r, p.group);
   const int head = cut.head * static_cast<int>(p.group.d) + static_cast<int>(r - t * p.group.d);
@@ -1327,24 +1357,28 @@ __global__ void __launch_bounds__(kMergeThreads) cross_merge_kernel(const __grid
 
 // Row = (sequence, KV head, token, head of its group) of a decode step behind shared prefixes: its prefix, its own keys
 // before the block, the block's keys that it sees, its sink.
-template <int kHd>
+template <int kHd, int kV>
 __global__ void __launch_bounds__(kMergeThreads)
     shared_merge_kernel(const __grid_constant__ Params p, int scale_rows, int grid, int total) {
   griddep_wait();
-  constexpr int kV = 4, kLanes = kHd / kV;
+  constexpr int kLanes = kHd / kV;
   __shared__ long long lo[kMostUnits + 1];
   const int d = threadIdx.x % kLanes;
   const int group = static_cast<int>(p.group.d), rows = p.q_len * group;
   // (lanes past the last row compute it again and write nothing: it may lie where Q did)
-  const int mine = blockIdx.x * kSharedRows<kHd> + static_cast<int>(threadIdx.x) / kLanes, of_all = min(mine, total - 1);
-  const int pair = of_all / rows, row = of_all - pair * rows;
-  const int b = pair / p.h_kv, kvh = pair - b * p.h_kv;
-  const int tok = row / group, head = kvh * group + row - tok * group;
+  const int mine = blockIdx.x * kSharedRows<kHd, kV> + static_cast<int>(threadIdx.x) / kLanes, of_all = min(mine, total - 1);
+  const int pair = fast_div(of_all, p.of_rows), row = of_all - pair * rows;
+  const int b = fast_div(pair, p.of_heads), kvh = pair - b * p.h_kv;
+  const int tok = fast_div(row, p.group), head = kvh * group + row - tok * group;
   const int token = b * p.q_len + tok, at = token * p.h_q + head;
   const float k_scale = scale_rows ? 1.f : *p.k_scale, v_scale = scale_rows ? 1.f : *p.v_scale;
   uint32_t bad = 0;
+  const int own = p.list[0].n + b;
+  const Bounds own_bounds = load_bounds(p, own);  // (asked for before they are needed, like the prefix's)
+  const long long own_at = p.seg_at[own];
   // its prefix (-1: none), looked for by the row's lanes
   int prefix = -1;
+#pragma unroll 1
   for (int g0 = 0; g0 < p.list[0].n; g0 += kLanes) {
     const int g = g0 + d;
     if (g < p.list[0].n && prefix < 0) {
@@ -1354,78 +1388,101 @@ __global__ void __launch_bounds__(kMergeThreads)
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) prefix = max(prefix, __shfl_xor_sync(0xffffffffu, prefix, o));
   }
+  const int some = max(prefix, 0);
+  const Bounds bounds = load_bounds(p, some);  // (without prefixes: a sequence's)
+  const long long prefix_at = p.seg_at[some];
   const int units = load_shares(p, grid, lo);
-  RowSum<kHd, kLanes> sum;
+  auto shares_below = [&](long long x) {  // how many begin before x
+    int n = 0;
 #pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const int seg = which ? p.list[0].n + b : prefix;
-    int first = 0, last = -1, slot = 0, item_row = 0;
-    const float* plane = nullptr;
-    if (seg >= 0) {
-      const Seg g = read_seg(p, seg, &bad);
-      if (g.tiles > 0) {
-        const int r = (b * p.q_len - g.t0) * group + row, rt = r / kItemRows;
-        item_row = r - rt * kItemRows;
-        const long long start = p.seg_at[seg] + kvh * g.head + static_cast<long long>(rt) * g.full;
-        const long long end = start + (rt == g.row_tiles - 1 ? g.last : g.full);
-        auto shares_below = [&](long long x) {  // how many begin before x
-          int n = 0;
-          for (int step = 256; step > 0; step >>= 1)
-            if (n + step <= units && lo[n + step - 1] < x) n += step;
-          return n;
-        };
-        first = shares_below(start + 1) - 1;
-        last = shares_below(end) - 1;
-        slot = lo[first] == start ? 0 : 1;
-        if (first == last) plane = p.plane_o[which];
-      }
-    }
-    sum.add(p, lo, first, last, slot, item_row, p.plane_ml[which], plane, at, d);
+    for (int step = 256; step > 0; step >>= 1)
+      if (n + step <= units && lo[n + step - 1] < x) n += step;
+    return n;
+  };
+  Pieces front, back;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {  // (once: the code is short for the instruction cache)
+    if (which == 0 && prefix < 0) continue;
+    const Seg g = make_seg(p, which ? own : prefix, which ? own_bounds : bounds, &bad);
+    if (g.tiles == 0) continue;
+    const int r = (b * p.q_len - g.t0) * group + row, rt = r / kItemRows;
+    const long long start = (which ? own_at : prefix_at) + kvh * g.head + static_cast<long long>(rt) * g.full;
+    const long long end = start + (rt == g.row_tiles - 1 ? g.last : g.full);
+    Pieces y;
+    y.first = shares_below(start + 1) - 1;
+    y.count = shares_below(end) - y.first;
+    y.slot = lo[y.first] == start ? 0 : 1;
+    y.row = r - rt * kItemRows;
+    if (y.count == 1) y.o = p.plane_o[which], y.ml = p.plane_ml[which], y.row = at;
+    if (which)
+      back = y;
+    else
+      front = y;
   }
-  if (p.list[1].less > 0) {
+  RowSum<kHd, kLanes> sum;
+  if (p.list[1].less > 0) {  // the block's keys: every lane looks one up, then they are weighed in turn
     const List& l = p.list[1];
-    const int len = seg_len(l, __ldg(l.lens + b), &bad);
-    const uint2 q2 = *reinterpret_cast<const uint2*>(p.q + token * p.q_tok + head * p.q_head + d * kV);
-    const float q[kV] = {bf16_lo(q2.x), bf16_hi(q2.x), bf16_lo(q2.y), bf16_hi(q2.y)};
+    const int len = seg_len(l, own_bounds.len, &bad);
+    float q[kV];
+#pragma unroll
+    for (int i = 0; i < kV; i += 4) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p.q + token * p.q_tok + head * p.q_head + d * kV + i);
+      q[i] = bf16_lo(x.x), q[i + 1] = bf16_hi(x.x), q[i + 2] = bf16_lo(x.y), q[i + 3] = bf16_hi(x.y);
+    }
     const float c = p.softmax_scale * kLog2e * k_scale;
-    for (int x = 0; x < p.q_len; ++x) {
-      const int key = len - p.q_len + x;
-      bool sees = key >= 0;
+#pragma unroll 1
+    for (int x0 = 0; x0 < p.q_len; x0 += kLanes) {
+      const int x = x0 + d, key = len - p.q_len + x;
+      bool sees = x < p.q_len && key >= 0;
       if (sees)
-        sees = p.spec_mask != nullptr
-                   ? p.spec_mask[(static_cast<long long>(b) * p.q_len + tok) * p.q_len + x] != 0
-                   : x <= tok;
-      float kx[kV], vx[kV], s = 0.f, sk = 1.f, sv = 1.f;
+        sees = p.spec_mask != nullptr ? p.spec_mask[(static_cast<long long>(b) * p.q_len + tok) * p.q_len + x] != 0
+                                      : x <= tok;
+      int line = 0;
+      float sk = 1.f, sv = 1.f;
       if (sees) {
         int block = __ldg(l.table + static_cast<long long>(b) * l.max_blocks + (key >> p.page_shift));
         if (block < 0 || block >= p.num_blocks) {
-          if (d == 0) atomicOr(&g_status_ragged, FP8MLA_DEV_BAD_PAGE);
+          atomicOr(&g_status_ragged, FP8MLA_DEV_BAD_PAGE);
           block = 0;
         }
-        const long long line =
-            ((static_cast<long long>(block) * p.h_kv + kvh) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
-        const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(p.k + line * kHd) + d);
-        const uint32_t e = __ldg(reinterpret_cast<const uint32_t*>(p.v + line * kHd) + d);
+        line = ((block * p.h_kv + kvh) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
         if (scale_rows) sk = __ldg(p.k_scale + line), sv = __ldg(p.v_scale + line);
-        const uint4 h = to_f16(make_uint2(a, e));
-        kx[0] = f16_lo(h.x), kx[1] = f16_hi(h.x), kx[2] = f16_lo(h.y), kx[3] = f16_hi(h.y);
-        vx[0] = f16_lo(h.z), vx[1] = f16_hi(h.z), vx[2] = f16_lo(h.w), vx[3] = f16_hi(h.w);
-#pragma unroll
-        for (int i = 0; i < kV; ++i) s += q[i] * kx[i];
       }
+      const uint32_t seen = __ballot_sync(0xffffffffu, sees) >> (threadIdx.x % 32 - d);
+      const int n = min(kLanes, p.q_len - x0);
+#pragma unroll 1
+      for (int j0 = 0; j0 < n; j0 += 2)
 #pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (!sees) continue;
-      s *= c * sk;
-      const float m = s + kLift, top = s == s ? fmaxf(sum.m, m) : fmaxf(sum.m, 0.f);  // the pieces' sums are lifted
-      if (top == kNegInf) continue;
-      const float a = ex2_approx(sum.m - top), w = ex2_approx(m - top);
-      sum.m = top;
-      sum.l = sum.l * a + w;
+      for (int j = j0; j < j0 + 2; ++j) {
+        const long long from = __shfl_sync(0xffffffffu, line, j, kLanes) * static_cast<long long>(kHd);
+        uint32_t wk[kV / 2], wv[kV / 2];  // (unseen: the cache's first row)
 #pragma unroll
-      for (int i = 0; i < kV; ++i) sum.acc[i] = sum.acc[i] * a + vx[i] * (w * sv);
+        for (int i = 0; i < kV / 4; ++i) {
+          const uint4 h = to_f16(make_uint2(__ldg(reinterpret_cast<const uint32_t*>(p.k + from) + d * (kV / 4) + i),
+                                            __ldg(reinterpret_cast<const uint32_t*>(p.v + from) + d * (kV / 4) + i)));
+          wk[2 * i] = h.x, wk[2 * i + 1] = h.y, wv[2 * i] = h.z, wv[2 * i + 1] = h.w;
+        }
+        const float skj = __shfl_sync(0xffffffffu, sk, j, kLanes), svj = __shfl_sync(0xffffffffu, sv, j, kLanes);
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kV; i += 2) s += q[i] * f16_lo(wk[i / 2]) + q[i + 1] * f16_hi(wk[i / 2]);
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        s *= c * skj;
+        const float m = s + kLift, top = s == s ? fmaxf(sum.m, m) : fmaxf(sum.m, 0.f);  // the pieces' sums are lifted
+        if (!((seen >> j) & 1) || top == kNegInf) continue;
+        const float f = ex2_approx(sum.m - top), w = ex2_approx(m - top);
+        sum.m = top;
+        sum.l = sum.l * f + w;
+#pragma unroll
+        for (int i = 0; i < kV; i += 2) {
+          sum.acc[i] = sum.acc[i] * f + f16_lo(wv[i / 2]) * (w * svj);
+          sum.acc[i + 1] = sum.acc[i + 1] * f + f16_hi(wv[i / 2]) * (w * svj);
+        }
+      }
     }
   }
+  sum.add(p, lo, front, back, d);
   if (mine >= total) return;
   sum.finish(p.out + static_cast<long long>(at) * kHd, p.lse + at, p.sinks ? p.sinks[head] : kNegInf, v_scale, d);
 }
@@ -1702,6 +1759,8 @@ fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream) {
   p.spec_mask = a.spec_mask;
   p.sinks = a.sinks;
   p.group = make_fast_div(group);
+  p.of_rows = make_fast_div(a.q_len * group);
+  p.of_heads = make_fast_div(a.h_kv);
   p.softmax_scale = a.softmax_scale;
   p.joined = 1;
   p.tokens = static_cast<int>(tokens);
@@ -1712,12 +1771,16 @@ fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream) {
   cudaError_t e = launch_any(p, a.head_dim, a.cache.scale_rows, s.grid, stream);
   if (e == cudaSuccess) {
     const int total = static_cast<int>(rows);
-    const int each = a.head_dim == 64 ? kSharedRows<64> : kSharedRows<128>;
-    const dim3 grid((total + each - 1) / each), block(kMergeThreads);
-    e = a.head_dim == 64 ? launch_dependent(shared_merge_kernel<64>, grid, block, 0, stream, p, a.cache.scale_rows, s.grid,
-                                            total)
-                         : launch_dependent(shared_merge_kernel<128>, grid, block, 0, stream, p, a.cache.scale_rows,
-                                            s.grid, total);
+    auto merge = [&](auto kernel, int each) {
+      e = launch_dependent(kernel, dim3((total + each - 1) / each), dim3(kMergeThreads), 0, stream, p, a.cache.scale_rows,
+                           s.grid, total);
+    };
+    const bool many = total > device_sms() * 32 * 128 / a.head_dim;
+    if (a.head_dim == 64)
+      many ? merge(shared_merge_kernel<64, 8>, kSharedRows<64, 8>) : merge(shared_merge_kernel<64, 4>, kSharedRows<64, 4>);
+    else
+      many ? merge(shared_merge_kernel<128, 8>, kSharedRows<128, 8>)
+           : merge(shared_merge_kernel<128, 4>, kSharedRows<128, 4>);
   }
   return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
 }

@@ -191,3 +191,12 @@ def test_blocks_in_place_of_odd_numbers_of_rows(hd, h_q, bs):
         here = q.to(DEV)
         out, lse = _call(pool, here, [70], [0, bs], lens, m, s, out=here)
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("hd,rows", [(64, False), (128, True)])
+@pytest.mark.parametrize("q_len", [1, 9])
+def test_more_rows_than_are_joined_at_a_time(hd, rows, q_len):
+    """Past the rows from which a row is joined by half as many lanes (4864 of 128 dims, 9728 of 64)."""
+    bs = 1300 if q_len == 1 else 190
+    lens = np.random.default_rng(11).integers(0, 40, bs).tolist()
+    _check(11, [150, 9], [0, bs // 2, bs - 20], lens, 2, 4, hd, 16, rows, q_len=q_len, mask=q_len > 1, sinks=True)
