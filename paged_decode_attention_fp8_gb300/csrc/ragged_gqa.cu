@@ -180,12 +180,21 @@ __device__ __forceinline__ Seg read_seg(const Params& p, int s, uint32_t* bad) {
   return make_seg(p, s, load_bounds(p, s), bad);
 }
 
+// a / b for 0 <= a < 2^30, 0 < b: a quotient in 24 bits, put right (the division of integers is several times as long, and
+// one warp does these while all others wait).
+__device__ __forceinline__ int quick_div(int a, int b) {
+  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+  while (q * b > a) --q;
+  while (q * b + b <= a) ++q;
+  return q;
+}
+
 // Where a share that would begin `off` into an item of this length does: at a tile, at least `few` from either end.
 __device__ __forceinline__ int cut_at(const Params& p, int off, int len, int form, int tiles, int few) {
   const int fixed = p.lengths.fixed[form], each = p.lengths.each[form];
   if (form != kFormPair) few = min(few, 2);  // little is written and merged
   if (tiles == 0) return off > 0 ? len : 0;
-  const int t = off <= fixed ? 0 : (off - fixed + each / 2) / each;
+  const int t = off <= fixed ? 0 : quick_div(off - fixed + each / 2, each);
   if (t >= few && tiles - t >= few) return fixed + t * each;
   return 2 * t < tiles ? 0 : len;
 }
@@ -250,12 +259,13 @@ __device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk
   if (bad && unit == 0) atomicOr(&g_status_ragged, bad);
   int units, few;
   long long raw[2];
-  if (total < (1 << 24)) {  // times 256 shares: 32 bits
+  if (total < (1 << 24)) {
     const uint32_t t = static_cast<uint32_t>(total);
     units = static_cast<int>(max(1u, min(gridDim.x, t / kLeast)));
-    few = static_cast<int>(t / units / (3u * p.lengths.each[kFormPair]));
-    raw[0] = t * unit / units;
-    raw[1] = t * (unit + 1) / units;
+    const float step = __fdividef(static_cast<float>(t), static_cast<float>(units));  // the same in every CTA
+    few = static_cast<int>(__fdividef(step, static_cast<float>(3 * p.lengths.each[kFormPair])));
+    raw[0] = min(t, static_cast<uint32_t>(step * static_cast<float>(unit)));
+    raw[1] = min(t, static_cast<uint32_t>(step * static_cast<float>(unit + 1)));
   } else {
     units = gridDim.x;
     few = 4;
@@ -357,9 +367,9 @@ __device__ __forceinline__ bool next_item(const Params& p, int unit, Walk* w, It
   const int form = form_of(rows);
   it->form = form;
   const int fixed = p.lengths.fixed[form], each = p.lengths.each[form];
-  const int tile_lo = off > 0 ? (off - fixed) / each : 0;
+  const int tile_lo = off > 0 ? quick_div(off - fixed, each) : 0;
   const bool ends = len - off <= left;
-  const int tile_hi = ends ? tiles : (off + static_cast<int>(left) - fixed) / each;
+  const int tile_hi = ends ? tiles : quick_div(off + static_cast<int>(left) - fixed, each);
   const bool whole = tile_lo == 0 && tile_hi == tiles;
   const int slot = 2 * unit + (w->first ? 0 : 1);
   it->tile_lo = tile_lo;
