@@ -37,7 +37,7 @@
 //
 // Measured (GB300, calls from a graph over three inputs): 2048 tokens x 32 heads by 16384 keys of 8 heads, head_dim 128,
 // 380 us = 1446 TFLOP/s, 0.76 of a library bf16 product; 64 tokens by 128 to 1600 keys with row scales 50 us, by 16000
-// keys 5.4 TB/s, 0.79 of a copy; one token by 777 keys 14 us; 64 sequences behind a prefix of 32768 keys 80 us.
+// keys 5.4 TB/s, 0.79 of a copy; one token by 777 keys 12.5 us; 64 sequences behind a prefix of 32768 keys 80 us.
 // In the first of them the tensor pipe is active 61 to 63 % of the time, XU 31, ALU 25, DRAM 2: no unit is full.  A tile
 // takes either stream about 3400 cycles for 2048 of the tensor core: product, scores loaded (220), weighed (1150), P
 // written (250), the issuing warp's turn (600), product with P and the next with K, each queued behind the other
@@ -83,6 +83,7 @@ constexpr Lengths kLengths[2][2] = {{{{24, 24, 13}, {60, 30, 26}}, {{42, 34, 15}
 constexpr int kEmpty = 15;  // an item without keys
 constexpr int kLeast = 60;  // a share
 constexpr int kMostUnits = 256;  // shares (one an SM)
+constexpr int kWhole = 140;      // items of a call that is not cut
 
 struct List {
   const int32_t* starts;  // segment s has the tokens [per starts[s], per starts[s + 1]); null: [per s, per (s + 1))
@@ -120,7 +121,7 @@ struct Params {
   unsigned long long per_unit;  // 2^64 / grid
   float softmax_scale;
   Lengths lengths;
-  int joined, tokens, h_q, h_kv, num_blocks, page_shift, slot_rows, fill_out, fill_lse, q_len;
+  int joined, whole, tokens, h_q, h_kv, num_blocks, page_shift, slot_rows, fill_out, fill_lse, q_len;
 };
 
 // ---------------------------------------------------------------- the line --
@@ -131,7 +132,7 @@ struct Seg {
   long long head;  // of all items of a KV head
 };
 
-__device__ __forceinline__ int form_of(int rows) {
+__host__ __device__ __forceinline__ int form_of(int rows) {
   return rows > kTile ? kFormPair : (rows > kFew ? kFormOne : kFormFew);
 }
 
@@ -195,7 +196,7 @@ __device__ __forceinline__ int cut_at(const Params& p, int off, int len, int for
   if (form != kFormPair) few = min(few, 2);  // little is written and merged
   if (tiles == 0) return off > 0 ? len : 0;
   const int t = off <= fixed ? 0 : quick_div(off - fixed + each / 2, each);
-  if (t >= few && tiles - t >= few) return fixed + t * each;
+  if (t >= few && tiles - t >= few && !p.whole) return fixed + t * each;
   return 2 * t < tiles ? 0 : len;
 }
 
@@ -1689,8 +1690,15 @@ fp8mla_status_t cross_entry(const CrossArgs& a, cudaStream_t stream) {
   p.fill_out = a.fill_out;
   p.fill_lse = a.fill_lse;
   use(&p, s, a.workspace);
+  // Items that are short and no more than the SMs, as far as the table's width shows, are not cut, and the merge's launch
+  // is left out.  One token x 16 heads of 64 by 100, 400, 1024, 1280, 2048 keys (lengths 39 to 234): 9.9, 9.9, 12.8, 14.4,
+  // 19.3 us whole, 11.5, 12.8, 13.5, 13.7, 14.2 cut; 128 items of up to 640 keys of 128 dims (138) 13.9 and 17.4.
+  const long long tiles = (max_keys + kTile - 1) / kTile, all_rows = static_cast<long long>(a.n_tokens) * group;
+  const int form = form_of(a.q_starts ? static_cast<int>(std::min<long long>(all_rows, kItemRows)) : group);
+  const long long items = a.h_kv * (a.q_starts ? all_rows / kItemRows + a.bs : a.bs);
+  p.whole = items <= device_sms() && p.lengths.fixed[form] + tiles * p.lengths.each[form] <= kWhole;
   cudaError_t e = launch_any(p, a.head_dim, a.cache.scale_rows, s.grid, stream);
-  if (e == cudaSuccess && s.grid > 1) {
+  if (e == cudaSuccess && s.grid > 1 && !p.whole) {
     const dim3 grid(s.grid, (s.slot_rows + kCrossRows - 1) / kCrossRows);
     e = a.head_dim == 64
             ? launch_dependent(cross_merge_kernel<64>, grid, dim3(kMergeThreads), 0, stream, p, a.cache.scale_rows)

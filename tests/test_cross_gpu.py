@@ -266,3 +266,16 @@ def test_a_line_past_32_bits():
     assert bool(((got - want).abs() <= want.abs() * 2 ** -7 + largest * (2 ** -10 + 2 ** -7)).all())
     assert float((long[1] - short[1] - np.log(512)).abs().max()) <= 2 ** -10
     assert fm.last_device_error() == 0
+
+
+@pytest.mark.parametrize("tokens,bs,h_kv,group,hd,rows,keys", [
+    (1, 1, 16, 1, 64, False, 1024), (1, 1, 16, 1, 64, False, 1153), (1, 19, 8, 4, 128, True, 600),
+    (1, 20, 8, 4, 128, True, 600), (200, 2, 4, 1, 64, False, 384), (200, 2, 4, 1, 64, False, 400)])
+def test_around_the_border_of_whole_items(tokens, bs, h_kv, group, hd, rows, keys):
+    """Calls of few short items, which are not cut and merged, and calls just past them."""
+    rng = np.random.default_rng(keys)
+    lens = rng.integers(0, keys + 1, bs)
+    lens[0] = keys
+    _check(12, [tokens] * bs, lens.tolist(), h_kv, group, hd, 16, rows)
+    pool, q, _, want = inputs.cross_case(13, [1] * bs, lens.tolist(), h_kv, group, hd, 16, rows)
+    assert inputs.within(*_call(pool, q, lens.tolist(), None), want, keys) is None
