@@ -200,3 +200,9 @@ def test_more_rows_than_are_joined_at_a_time(hd, rows, q_len):
     bs = 1300 if q_len == 1 else 190
     lens = np.random.default_rng(11).integers(0, 40, bs).tolist()
     _check(11, [150, 9], [0, bs // 2, bs - 20], lens, 2, 4, hd, 16, rows, q_len=q_len, mask=q_len > 1, sinks=True)
+
+
+@pytest.mark.parametrize("hd,q_len", [(64, 1), (128, 3)])
+def test_no_prefixes(hd, q_len):
+    """A batch in which nothing is shared: tables of no rows."""
+    _check(14, [], [0], [3, 40, 0, 200], 2, 2, hd, 16, False, q_len=q_len, sinks=True)
