@@ -511,8 +511,9 @@ FP8MLA_API size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int h
  *   q            bf16 [n_tokens, h_q, head_dim], strided along tokens and heads
  *                (elements, multiples of 8), 16-byte aligned; so is out
  *   k_cache, v_cache  E4M3 [num_blocks, h_kv, page_size, head_dim], 16-byte
- *                aligned; k_scale, v_scale float32 [1], or [num_blocks, h_kv,
- *                page_size] (16-byte aligned) with scale_rows
+ *                aligned; k_scale, v_scale float32 [1] (2^-80 to 2^80), or
+ *                [num_blocks, h_kv, page_size] (16-byte aligned; finite, not
+ *                negative) with scale_rows
  *   q_starts     int32 [bs + 1], not falling: sequence b has the tokens
  *                [q_starts[b], q_starts[b + 1]); NULL: token b (n_tokens >= bs)
  *   block_table  int32 [bs, max_blocks]; kv_lens int32 [bs], 0 allowed
@@ -528,7 +529,7 @@ FP8MLA_API size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int h
  * a row's largest on exactly (others to 2^-18 of it); P is rounded to f16, sums
  * are float32.  A NaN reaches the rows of its sequence, and those alone.
  * Requires head_dim 64 or 128, page_size 16, 32, 64, 128 or 256, h_q % h_kv == 0,
- * n_tokens * h_q <= 2^30, max_blocks * page_size <= 2^30, scales > 0, fewer than
+ * n_tokens * h_q <= 2^30, max_blocks * page_size <= 2^30, fewer than
  * 2^31 rows (num_blocks * h_kv * page_size) a cache. */
 FP8MLA_API fp8mla_status_t paged_cross_attention(
     const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache, const void* v_cache,

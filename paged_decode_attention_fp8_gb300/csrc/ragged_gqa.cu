@@ -68,6 +68,11 @@ constexpr float kLift = 7.f;    // P = 2^(score - reference + 7): 2^15 at most i
 constexpr uint32_t kNone = 0xFF800000u;  // -inf: the score of a key past the end
 constexpr float kFar = 1048576.f;  // 2^20 in log2 units: up to here the lift and the difference keep their fraction
 constexpr float kTau = 8.f;     // the reference moves when a score passes it by more
+constexpr float kNoRef = -1e30f;  // the reference of a row whose V scales so far are all zero
+// V's row scales within 2^+-40 enter the weights, and the sum of exponentials divides them out again.  Past that the
+// smallest weights vanish beside the largest, and 1 / scale and the sum leave float32: from the first tile with such a scale
+// on, an item's sum is taken from the scores alone, relative to their own maximum.
+constexpr float kSmallScale = 0x1p-40f, kLargeScale = 0x1p40f;
 
 // Up to 32 rows lie in all quarters (few), up to 128 are one stream, up to 256 a pair of streams.
 constexpr int kFew = 32;
@@ -421,9 +426,10 @@ struct Control {
   uint32_t tmem_base, abort_flag, never;  // never: the flag of waits that no other warp ends
   uint32_t sums_read;            // warps that are done with a few-row item's sums
   int8_t q_exp[2][kTile];        // of Q's rows, by stream
-  float row_l[2][kTile], row_m[kTile];
+  float row_l[2][kTile], row_m[kTile];  // (row_l while an item's sum is apart: the largest score of this thread's row)
   alignas(16) float4 scl_k[kRows ? L::kScls : 1][kRows ? kTile / 2 : 1];  // of two keys: K scales, log2 of V scales
-  alignas(16) float scl_v[kRows ? L::kScls : 1][kRows ? kTile : 4];       // 1 / V scale
+  alignas(16) float scl_v[kRows ? L::kScls : 1][kRows ? kTile : 4];       // 1 / V scale (0 where that is far from one)
+  alignas(4) uint8_t scl_far[kRows ? L::kScls : 1][4];  // a tile's V scales that are, by warps' keys
   alignas(16) float raw_scl[kRows ? L::kVs : 1][2][kRows ? kTile : 4];
 };
 
@@ -628,6 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = row < it->rows;
       const bool busy = __any_sync(0xffffffffu, live);
       float ref = kNegInf, l = 0.f, cc = 1.f;
+      [[maybe_unused]] bool apart = false;  // a tile's V scales were far from one (the same in all warps)
       if (tiles > 0) {
         if (!warp_wait(&sm->q_full, worked & 1, abort_flag)) break;
         if (form != was) {
@@ -656,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto rescale = [&](int i, float alpha) -> bool {
             if (!kPair && !warp_wait(&sm->pv_done, (pv_base + i - 1) & 1, abort_flag)) return false;
             tc_fence_after();
-            l *= alpha;
+            if (!kRows || !apart) l *= alpha;
 #pragma unroll 1
             for (int k = 0; k < kOCols; k += 16) {
               uint32_t o[16];
@@ -671,9 +678,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < tiles; ++i, keys -= kTile) {
             const int buf = kPair ? wg : (i & 1);
+            if (kRows && !warp_wait(&sm->scl_full[tile_no % L::kScls], (tile_no / L::kScls) & 1, abort_flag)) return false;
+            [[maybe_unused]] const bool first = !apart;
+            if constexpr (kRows)  // (before the wait for S, which hides it)
+              apart = apart || *reinterpret_cast<const volatile uint32_t*>(sm->scl_far[tile_no % L::kScls]) != 0;
             if (!warp_wait(&sm->s_full[buf], (s_phase >> buf) & 1, abort_flag)) return false;
             s_phase ^= 1u << buf;
-            if (kRows && !warp_wait(&sm->scl_full[tile_no % L::kScls], (tile_no / L::kScls) & 1, abort_flag)) return false;
             if (busy) {
               const uint32_t t_s = lanes + kTS + buf * 128;
               const uint32_t t_p = kPair ? t_s : lanes + kTO + 128 + buf * 64;
@@ -688,6 +698,43 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (; k < kTile; k += 8) tmem_st8(t_s + k, none);
                 tmem_st_wait();
+              }
+              if constexpr (kRows) {
+                if (apart) {  // the sum from the scores alone
+                  uint32_t y[16];
+                  auto raw = [&](int at) {
+                    tmem_ld16(t_s + at, y);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                      const float4 a = kl[(at + j) / 2];
+                      const float2 z = make_float2(__uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+                      const float2 u = mul_f32x2(mul_f32x2(z, make_float2(c, c)), make_float2(a.x, a.y));
+                      y[j] = __float_as_uint(u.x), y[j + 1] = __float_as_uint(u.y);
+                    }
+                  };
+                  // until now l was relative to the reference, which no score passed by more than 48 (both warpgroups
+                  // find the same, whatever their own keys' weights)
+                  volatile float* top_score = &sm->row_l[wg][r];
+                  float was_top = i > 0 ? ref : kNegInf;
+                  if (!first) was_top = *top_score;
+                  float top = was_top;
+#pragma unroll 1
+                  for (int at = kPair ? 0 : end0 - 2 * cols; at < (kPair ? kTile : end0); at += 16) {
+                    raw(at);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) top = fmaxf(top, __uint_as_float(y[j]));
+                  }
+                  if (top != was_top) l *= ex2_approx(was_top - top);
+                  *top_score = top;
+                  const float by = top == kNegInf ? 0.f : top;
+#pragma unroll 1
+                  for (int at = kPair ? 0 : col0; at < (kPair ? kTile : col0 + cols); at += 16) {
+                    raw(at);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) l += ex2_approx(__uint_as_float(y[j]) - by + kLift);
+                  }
+                }
               }
               constexpr int kChunk = kPair ? kTile : 16;
               float x[kChunk];
@@ -780,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (i > 0 && __any_sync(0xffffffffu, raise && live) &&
                         !rescale(i, raise ? ex2_approx(-step * cc) : 1.f))
                       return false;
-                    if (i == 0) ref = top == kNegInf ? 0.f : top;
+                    if (i == 0) ref = top == kNegInf ? (kRows ? kNoRef : 0.f) : top;
                     if (raise) ref = less ? ref + top : top;
                     far = less || fabsf(ref * cc) > kFar;
                     by = !far ? 0.f : (less ? (raise ? top : 0.f) : ref);
@@ -790,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   bias = far ? kLift : kLift - ref * cc;
                   const float add = weigh(0);
                   if (look || !__any_sync(0xffffffffu, live && !(add <= 32768.f))) {
-                    l += add;
+                    if (!kRows || !apart) l += add;
                     break;
                   }
                   look = again = true;
@@ -804,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const bool raise = (top - ref) * cc > kTau;
                 if (i == 0) {
-                  ref = top == kNegInf ? 0.f : top;
+                  ref = top == kNegInf ? (kRows ? kNoRef : 0.f) : top;
                 } else if (__any_sync(0xffffffffu, raise && live)) {
                   if (!rescale(i, raise ? ex2_approx((ref - top) * cc) : 1.f)) return false;
                   if (raise) ref = top;
@@ -815,7 +862,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int at = col0; at < col0 + cols; at += 16) {
                   scores(at);
                   subtract(far ? ref : 0.f);
-                  l += weigh(at);
+                  const float add = weigh(at);
+                  if (!kRows || !apart) l += add;
                 }
               }
               tmem_st_wait();
@@ -845,6 +893,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint16_t* out = p.out + token * p.o_tok + head * p.o_head;
       float* sums = (it->slot >= 0 ? p.slot_o : p.plane_o[it->list]) + place * kHd;
       float m = ref * cc, sum = l, part[4];
+      // apart: O, relative to the reference, follows the sum (in two steps: either of them stays in float32's range)
+      [[maybe_unused]] float half = 1.f;
+      if (kRows && apart) {
+        const float top_score = sm->row_l[wg][r];
+        if (top_score != kNegInf) m = top_score, half = ex2_approx(0.5f * (ref - top_score));
+      }
       if (split) {
         sm->row_l[wg][r] = l;
         if (wg == 0) sm->row_m[r] = m;
@@ -874,6 +928,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           (it->slot >= 0 ? p.slot_ml : p.plane_ml[it->list])[place] = make_float2(m, sum);
       }
+      [[maybe_unused]] auto follow = [&](uint32_t (&o)[32]) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * half * half);
+      };
       const float unit_o = !direct ? 1.f : (tiles > 0 ? (kRows ? 1.f : __ldg(p.v_scale)) / sum : 0.f);
       const int os = pair ? wg : 0;
       if (tiles > 0) {
@@ -895,6 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             tmem_ld32(lanes + kTO + wg * (kHd / 2) + k0 + k, o);
             tmem_ld_wait();
+            if (kRows && apart) follow(o);
             float* to = quarters + ((wg * 4 + w) * rows + lane) * dims + k;
             if (live) {
 #pragma unroll
@@ -940,6 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tiles > 0) {
             tmem_ld32(lanes + kTO + os * 128 + k, o);
             tmem_ld_wait();
+            if (kRows && apart) follow(o);
           }
           if (!put) continue;
 #pragma unroll
@@ -1004,9 +1064,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float a = tid < valid ? sm->raw_scl[vs][0][tid] : 1.f, b = tid < valid ? sm->raw_scl[vs][1][tid] : 1.f;
           const int ss = done % L::kScls;
           float* two = reinterpret_cast<float*>(&sm->scl_k[ss][tid / 2]) + tid % 2;
+          const bool near = b >= kSmallScale && b <= kLargeScale;
+          const bool far = __any_sync(0xffffffffu, !near);
           two[0] = a;
-          two[2] = lg2_approx(b);
-          sm->scl_v[ss][tid] = 1.f / b;
+          two[2] = b < 0x1p-126f ? lg2_approx(b * 0x1p64f) - 64.f : lg2_approx(b);
+          sm->scl_v[ss][tid] = near ? 1.f / b : 0.f;
+          if (lane == 0) sm->scl_far[ss][warp - 8] = far;
           warp_arrive(&sm->scl_full[ss]);
         }
         if (done >= L::kFs && !warp_wait(&sm->f_empty[fs], f_phase, abort_flag)) break;
