@@ -581,8 +581,9 @@ FP8MLA_API size_t paged_gqa_shared_workspace_bytes(int bs, int q_len, int h_q, i
  *                elements, multiples of 8), 16-byte aligned; so is out
  *   lses         host array of device pointers, float32 [n_tokens, heads]
  * A part whose lse is -inf does not count, whatever its row holds; no part:
- * zeros and -inf.  Sums in float32, rounded once.  out may be one of outs
- * (strided alike); out and lse overlap nothing else (refused).
+ * zeros and -inf.  An lse of NaN or +inf gives NaN in both.  Sums in float32,
+ * rounded once.  out may be one of outs (strided alike); out and lse overlap
+ * nothing else (refused).
  * 1 <= parts <= FP8MLA_MERGE_MAX_PARTS, dim a multiple of 8 up to 1024,
  * n_tokens * heads * dim <= 2^33. */
 #define FP8MLA_MERGE_MAX_PARTS 8

@@ -717,8 +717,8 @@ def paged_gqa_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
 def attention_merge(outs, lses, *, out=None, lse=None):
     """Join 1 to 8 attention results over disjoint keys: lse = log sum exp(lses), out = sum exp(lses[p] - lse) outs[p].
     outs bf16 [n, heads, dim] each (strided along tokens and heads by multiples of 8 values, 16-byte aligned), lses
-    float32 [n, heads]; a part whose lse is -inf does not count, whatever its row holds.  Returns (out, lse); out may
-    be one of outs."""
+    float32 [n, heads]; a part whose lse is -inf does not count, whatever its row holds, and one of NaN or +inf gives
+    NaN.  Returns (out, lse); out may be one of outs."""
     return _native().attention_merge(outs, lses, out, lse)
 
 

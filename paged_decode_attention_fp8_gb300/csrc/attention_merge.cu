@@ -57,12 +57,10 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__
     float top = kNegInf, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kParts; ++i) top = fmaxf(top, w[e][i]);
-    bool nan = false;
     const float base = top == kNegInf ? 0.f : top;
     float acc[8] = {};
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
-      nan |= w[e][i] != w[e][i];
       const float f = ex2_approx((w[e][i] - base) * kLog2e);
       sum += f;
       if (w[e][i] == kNegInf) continue;  // a part without keys: whatever its row holds
@@ -73,6 +71,7 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__
         acc[2 * k + 1] += f * bf16_hi(h[k]);
       }
     }
+    const bool nan = sum != sum;  // a sum that is NaN or +inf: it has no weight
     float f = sum > 0.f ? 1.f / sum : 0.f;
     if (nan) f = __int_as_float(0x7FFFFFFF);
     uint32_t h[4];
