@@ -152,9 +152,12 @@ __device__ __forceinline__ Bounds load_bounds(const Params& p, int s) {
   return x;
 }
 
+constexpr uint32_t kBadRange = 1u << 31;  // beside the status bits, for the kernel alone: a segment's tokens do not fit
+__device__ __forceinline__ bool range_ok(const List& l, int a, int b) { return a >= 0 && a <= b && b <= l.most; }
+
 __device__ __forceinline__ int seg_len(const List& l, int n, uint32_t* bad) {
   if (static_cast<uint32_t>(n) <= static_cast<uint32_t>(l.max_keys)) return n;
-  *bad = FP8MLA_DEV_BAD_SEQLEN;
+  *bad |= FP8MLA_DEV_BAD_SEQLEN;
   return 0;
 }
 
@@ -162,8 +165,8 @@ __device__ __forceinline__ Seg make_seg(const Params& p, int s, const Bounds& x,
   const List& l = s < p.list[0].n ? p.list[0] : p.list[1];
   Seg g;
   int a = x.a, b = x.b;
-  if (a < 0 || a > b || b > l.most) {
-    *bad = FP8MLA_DEV_BAD_SEQLEN;
+  if (!range_ok(l, a, b)) {
+    *bad |= FP8MLA_DEV_BAD_SEQLEN | kBadRange;
     a = b = 0;
   }
   g.t0 = a * l.per;
@@ -226,7 +229,8 @@ constexpr int kGroups = 64;  // of segments, whose places on the line are kept
 
 // The beginning of CTA `unit`'s share, by one warp; it is short, as its instructions come from memory in every launch.
 // First the line's length, with the places where groups of segments begin; then the segments that hold the share's ends.
-__device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk, long long (&group_at)[kGroups]) {
+// Returns whether all segments' tokens fit.
+__device__ __forceinline__ bool find_share(const Params& p, int unit, Walk* walk, long long (&group_at)[kGroups]) {
   const int n = p.list[0].n + p.list[1].n;
   const int lane = threadIdx.x % 32;
   const int each = ((n + 31) / 32 + kGroups - 1) / kGroups * 32;  // segments a group
@@ -262,7 +266,8 @@ __device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk
     if (p.joined && (s0 >> 5) % gridDim.x == unit && s0 + lane < n) p.seg_at[s0 + lane] = at;
     total += all;
   }
-  if (bad && unit == 0) atomicOr(&g_status_ragged, bad);
+  const bool fits = !__any_sync(0xffffffffu, (bad & kBadRange) != 0);
+  if (bad && unit == 0) atomicOr(&g_status_ragged, bad & ~kBadRange);
   int units, few;
   long long raw[2];
   if (total < (1 << 24)) {
@@ -346,6 +351,7 @@ __device__ __forceinline__ void find_share(const Params& p, int unit, Walk* walk
   __syncwarp();
   if (lane == 0) walk->left = walk->hi - walk->left;
   __syncwarp();
+  return fits;
 }
 
 // The next item of a share (one thread).
@@ -1253,7 +1259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_wait(full + j % ring, (j / ring) & 1, &sm->never);
     } else if (warp == 14) {
       // ------------------------------------------------- the share's items --
-      find_share(p, unit, &sm->walk, sm->group_at);
+      const bool fits = find_share(p, unit, &sm->walk, sm->group_at);
       bool more = true;
 #pragma unroll 1
       for (uint32_t n = 0; more; ++n) {
@@ -1267,17 +1273,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       // and rows of no sequence
       if (p.fill_out || p.fill_lse) {
         const List& l = p.list[0];
-        const int lo = l.starts ? min(max(__ldg(l.starts), 0), p.tokens) : 0;
-        const int hi = l.starts ? min(max(__ldg(l.starts + l.n), lo), p.tokens) : min(l.n, p.tokens);
-        const uint32_t heads = static_cast<uint32_t>(lo + p.tokens - hi) * p.h_q;
-#pragma unroll 1
-        for (uint32_t i = unit; i < heads; i += gridDim.x) {
-          int t = static_cast<int>(i / p.h_q);
-          const int h = static_cast<int>(i - t * p.h_q);
-          if (t >= lo) t += hi - lo;
+        auto fill = [&](int t, int h) {
           if (p.fill_out && lane < kHd / 8)
             *reinterpret_cast<uint4*>(p.out + t * p.o_tok + h * p.o_head + lane * 8) = make_uint4(0, 0, 0, 0);
           if (p.fill_lse && lane == 0) p.lse[static_cast<long long>(t) * p.h_q + h] = kNegInf;
+        };
+        if (fits) {  // those in front of the first one and behind the last
+          const int lo = l.starts ? min(max(__ldg(l.starts), 0), p.tokens) : 0;
+          const int hi = l.starts ? min(max(__ldg(l.starts + l.n), lo), p.tokens) : min(l.n, p.tokens);
+          const uint32_t heads = static_cast<uint32_t>(lo + p.tokens - hi) * p.h_q;
+#pragma unroll 1
+          for (uint32_t i = unit; i < heads; i += gridDim.x) {
+            int t = static_cast<int>(i / p.h_q);
+            const int h = static_cast<int>(i - t * p.h_q);
+            if (t >= lo) t += hi - lo;
+            fill(t, h);
+          }
+        } else {  // a lane's token is looked for in every segment
+#pragma unroll 1
+          for (int t0 = unit * 32; t0 < p.tokens; t0 += gridDim.x * 32) {
+            const int t = t0 + lane;
+            bool has = t >= p.tokens;
+            int a = __ldg(l.starts);
+#pragma unroll 4
+            for (int s = 0; s < l.n; ++s) {
+              const int b = __ldg(l.starts + s + 1);
+              has |= range_ok(l, a, b) && a <= t && t < b;
+              a = b;
+            }
+            uint32_t without = __ballot_sync(0xffffffffu, !has);
+#pragma unroll 1
+            for (; without != 0; without &= without - 1)
+#pragma unroll 1
+              for (int h = 0; h < p.h_q; ++h) fill(t0 + __ffs(without) - 1, h);
+          }
         }
       }
     }
