@@ -516,7 +516,8 @@ FP8MLA_API size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int h
  *                negative) with scale_rows
  *   q_starts     int32 [bs + 1], not falling: sequence b has the tokens
  *                [q_starts[b], q_starts[b + 1]); NULL: token b (n_tokens >= bs)
- *   block_table  int32 [bs, max_blocks]; kv_lens int32 [bs], 0 allowed
+ *   block_table  int32 [bs, max_blocks] (NULL where max_blocks is 0: no keys);
+ *                kv_lens int32 [bs], 0 allowed
  *   out, lse     bf16, float32 [n_tokens, h_q] contiguous (natural log).  A
  *                sequence without keys gives zeros and -inf.  Rows of tokens of
  *                no sequence are left as they are, or get zeros (fill_out) and
@@ -529,7 +530,7 @@ FP8MLA_API size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int h
  * a row's largest on exactly (others to 2^-18 of it); P is rounded to f16, sums
  * are float32.  A NaN reaches the rows of its sequence, and those alone.
  * Requires head_dim 64 or 128, page_size 16, 32, 64, 128 or 256, h_q % h_kv == 0,
- * n_tokens * h_q <= 2^30, max_blocks * page_size <= 2^30, fewer than
+ * h_q <= 65536, n_tokens * h_q <= 2^30, max_blocks * page_size <= 2^30, fewer than
  * 2^31 rows (num_blocks * h_kv * page_size) a cache. */
 FP8MLA_API fp8mla_status_t paged_cross_attention(
     const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache, const void* v_cache,
@@ -553,7 +554,8 @@ FP8MLA_API size_t paged_cross_workspace_bytes(int n_tokens, int bs, int h_q, int
  *                not falling: prefix g belongs to the sequences
  *                [prefix_starts[g], prefix_starts[g + 1]); others have none
  *   block_table  int32 [bs, max_blocks], seqlens int32 [bs]: own keys, the
- *                step's q_len ones included; 0 allowed
+ *                step's q_len ones included; 0 allowed.  A table without columns
+ *                is NULL here too
  *   spec_mask, sinks, out, lse  as paged_gqa_decode_ext (block key x of a
  *                sequence is its own key seqlens - q_len + x; one that would
  *                lie before key 0 does not exist)

@@ -536,6 +536,8 @@ int64_t need_block_table(const Tensor& t, const char* name, int64_t n, const c10
     bad(std::string(name) + " must be contiguous int32 [" + std::to_string(n) + ", max_blocks] on " + dev.str());
   return t.size(1);
 }
+// (a table without columns has no memory, whatever it is a view of)
+const int32_t* table_ptr(const Tensor& t) { return t.numel() > 0 ? static_cast<const int32_t*>(t.data_ptr()) : nullptr; }
 float softmax_scale_of(PyObject* o, int64_t hd) {
   double scale = 1.0 / std::sqrt(static_cast<double>(hd));
   if (o != Py_None) {
@@ -598,7 +600,7 @@ PyObject* py_cross(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     check(paged_cross_attention(q.data_ptr(), stride_of(&q, 0), stride_of(&q, 1), kc.data_ptr(), vc.data_ptr(),
                                 FP8MLA_KV_E4M3, dim32(s.blocks, "num_blocks"), ptr_as<const float>(&ks),
                                 ptr_as<const float>(&vs), by_row, ptr_as<const int32_t>(starts),
-                                ptr_as<const int32_t>(&bt), dim32(blocks, "max_blocks"), ptr_as<const int32_t>(&kl),
+                                table_ptr(bt), dim32(blocks, "max_blocks"), ptr_as<const int32_t>(&kl),
                                 scale, ptr(ws), ws->nbytes(), out->data_ptr(), stride_of(out, 0), stride_of(out, 1),
                                 ptr_as<float>(lse), fill_out, fill_lse, n32, bs32, hq32, hkv32, hd32,
                                 dim32(s.page, "page"), stream_of(dev)),
@@ -662,9 +664,9 @@ PyObject* py_shared(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                         dev);
     check(paged_gqa_decode_shared(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), FP8MLA_KV_E4M3,
                                   dim32(s.blocks, "num_blocks"), ptr_as<const float>(&ks), ptr_as<const float>(&vs),
-                                  by_row, ptr_as<const int32_t>(&pt), dim32(prefix_blocks, "prefix_blocks"),
+                                  by_row, table_ptr(pt), dim32(prefix_blocks, "prefix_blocks"),
                                   ptr_as<const int32_t>(&pl), ptr_as<const int32_t>(&ps), np32,
-                                  ptr_as<const int32_t>(&bt), dim32(blocks, "max_blocks"), ptr_as<const int32_t>(&sl),
+                                  table_ptr(bt), dim32(blocks, "max_blocks"), ptr_as<const int32_t>(&sl),
                                   scale, ql32, ptr_as<const uint8_t>(mask), ptr_as<const float>(sinks), ptr(ws),
                                   ws->nbytes(), out->data_ptr(), ptr_as<float>(lse), bs32, hq32, hkv32, hd32,
                                   dim32(s.page, "page"), stream_of(dev)),

@@ -1730,6 +1730,9 @@ constexpr long long kMostRows = 1ll << 30;  // tokens * h_q
 
 }  // namespace ragged
 
+// A table of no columns has no memory: then all lengths are 0.
+static bool table_ok(const int32_t* table, int columns) { return columns > 0 ? table != nullptr : table == nullptr; }
+
 size_t cross_workspace_bytes(int n_tokens, int bs, int h_q, int h_kv, int head_dim, long long max_keys) {
   using namespace ragged;
   if (!heads_ok(h_q, h_kv, head_dim) || n_tokens < 0 || bs < 0 || max_keys < 0 || max_keys > kMostKeys ||
@@ -1742,7 +1745,7 @@ size_t cross_workspace_bytes(int n_tokens, int bs, int h_q, int h_kv, int head_d
 fp8mla_status_t cross_entry(const CrossArgs& a, cudaStream_t stream) {
   using namespace ragged;
   Params p = {};
-  if (!heads_ok(a.h_q, a.h_kv, a.head_dim) || a.n_tokens < 0 || a.bs < 0 || a.max_blocks < 1 ||
+  if (!heads_ok(a.h_q, a.h_kv, a.head_dim) || a.n_tokens < 0 || a.bs < 0 || a.max_blocks < 0 ||
       !(a.softmax_scale > 0.f) || !cache_ok(a.cache, a.h_kv, &p.page_shift))
     return FP8MLA_ERR_INVALID_ARG;
   const long long max_keys = static_cast<long long>(a.max_blocks) << p.page_shift;
@@ -1750,7 +1753,7 @@ fp8mla_status_t cross_entry(const CrossArgs& a, cudaStream_t stream) {
   if (max_keys > kMostKeys || rows > kMostRows || (a.q_starts == nullptr && a.n_tokens < a.bs))
     return FP8MLA_ERR_INVALID_ARG;
   if (a.n_tokens == 0 || (a.bs == 0 && !a.fill_out && !a.fill_lse)) return FP8MLA_OK;
-  if (a.q == nullptr || a.out == nullptr || a.lse == nullptr || (a.bs > 0 && (a.block_table == nullptr || a.kv_lens == nullptr)))
+  if (a.q == nullptr || a.out == nullptr || a.lse == nullptr || (a.bs > 0 && (!table_ok(a.block_table, a.max_blocks) || a.kv_lens == nullptr)))
     return FP8MLA_ERR_INVALID_ARG;
   if (misaligned(a.q, 16) || misaligned(a.out, 16) || misaligned(a.lse, 4) || misaligned(a.q_starts, 4) ||
       misaligned(a.block_table, 4) || misaligned(a.kv_lens, 4) || ((a.q_token | a.q_head | a.out_token | a.out_head) & 7))
@@ -1828,7 +1831,7 @@ size_t shared_workspace_bytes(int bs, int q_len, int h_q, int h_kv, int head_dim
 fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream) {
   using namespace ragged;
   Params p = {};
-  if (!cache_ok(a.cache, a.h_kv, &p.page_shift) || a.max_blocks < 1 || (a.n_prefixes > 0 && a.prefix_blocks < 1) ||
+  if (!cache_ok(a.cache, a.h_kv, &p.page_shift) || a.max_blocks < 0 || (a.n_prefixes > 0 && a.prefix_blocks < 0) ||
       !(a.softmax_scale > 0.f))
     return FP8MLA_ERR_INVALID_ARG;
   const long long prefix_keys = a.n_prefixes > 0 ? static_cast<long long>(a.prefix_blocks) << p.page_shift : 0;
@@ -1836,8 +1839,9 @@ fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream) {
   if (!shared_sizes_ok(a.bs, a.q_len, a.h_q, a.h_kv, a.head_dim, a.n_prefixes, prefix_keys, keys))
     return FP8MLA_ERR_INVALID_ARG;
   if (a.bs == 0) return FP8MLA_OK;
-  if (a.q == nullptr || a.out == nullptr || a.lse == nullptr || a.block_table == nullptr || a.seqlens == nullptr ||
-      (a.n_prefixes > 0 && (a.prefix_table == nullptr || a.prefix_lens == nullptr || a.prefix_starts == nullptr)))
+  if (a.q == nullptr || a.out == nullptr || a.lse == nullptr || a.seqlens == nullptr ||
+      !table_ok(a.block_table, a.max_blocks) ||
+      (a.n_prefixes > 0 && (!table_ok(a.prefix_table, a.prefix_blocks) || a.prefix_lens == nullptr || a.prefix_starts == nullptr)))
     return FP8MLA_ERR_INVALID_ARG;
   if (misaligned(a.q, 16) || misaligned(a.out, 16) || misaligned(a.lse, 4) || misaligned(a.block_table, 4) ||
       misaligned(a.seqlens, 4) || misaligned(a.prefix_table, 4) || misaligned(a.prefix_lens, 4) ||
