@@ -523,8 +523,8 @@ FP8MLA_API size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int h
  *                no sequence are left as they are, or get zeros (fill_out) and
  *                -inf (fill_lse)
  *   workspace    >= paged_cross_workspace_bytes, 256-byte aligned
- * out may be q (strided alike); out, lse, workspace and q do not overlap
- * otherwise (refused).  A length or token range that does not fit sets
+ * out may be q (strided alike); out, lse and workspace overlap nothing else
+ * (refused).  A length or token range that does not fit sets
  * FP8MLA_DEV_BAD_SEQLEN and counts as empty, a page outside the cache
  * FP8MLA_DEV_BAD_PAGE.  Products take K and V exactly, Q's values from 2^-10 of
  * a row's largest on exactly (others to 2^-18 of it); P is rounded to f16, sums

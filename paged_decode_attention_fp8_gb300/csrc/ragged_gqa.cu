@@ -48,6 +48,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 #include <type_traits>
 
@@ -1725,6 +1726,20 @@ void fill_cache(Params* p, const RaggedCache& c, int head_dim) {
   p->lengths = kLengths[head_dim == 128][c.scale_rows != 0];
 }
 
+// Whether memory that a call writes meets an input of it (the queries are looked at apart: the output may take their place).
+bool meets(std::initializer_list<Rows> written, std::initializer_list<Rows> inputs) {
+  for (const Rows& w : written)
+    for (const Rows& in : inputs)
+      if (rows_overlap(w, in)) return true;
+  return false;
+}
+bool meets_cache(std::initializer_list<Rows> written, const RaggedCache& c, int h_kv, int head_dim) {
+  const uint64_t rows = static_cast<uint64_t>(c.num_blocks) * h_kv * c.page_size, scales = (c.scale_rows ? rows : 1) * 4;
+  return meets(written, {block_of(c.k, rows * head_dim), block_of(c.v, rows * head_dim), block_of(c.k_scale, scales),
+                         block_of(c.v_scale, scales)});
+}
+uint64_t words(long long n, long long m = 1) { return static_cast<uint64_t>(n) * static_cast<uint64_t>(m) * 4; }
+
 constexpr long long kMostKeys = 1ll << 30;  // a segment
 constexpr long long kMostRows = 1ll << 30;  // tokens * h_q
 
@@ -1768,7 +1783,10 @@ fp8mla_status_t cross_entry(const CrossArgs& a, cudaStream_t stream) {
   const Rows out = rows_of(a.out, a.out_token, a.out_head, a.n_tokens, a.h_q, a.head_dim, 2);
   const Rows lse = block_of(a.lse, rows * 4), ws = block_of(a.workspace, s.bytes);
   if (clobbers(out, q) || rows_overlap_themselves(out) || rows_overlap(lse, q) || rows_overlap(ws, q) ||
-      rows_overlap(out, lse) || rows_overlap(out, ws) || rows_overlap(lse, ws))
+      rows_overlap(out, lse) || rows_overlap(out, ws) || rows_overlap(lse, ws) ||
+      meets_cache({out, lse, ws}, a.cache, a.h_kv, a.head_dim) ||
+      meets({out, lse, ws}, {block_of(a.q_starts, words(a.bs + 1ll)), block_of(a.block_table, words(a.bs, a.max_blocks)),
+                             block_of(a.kv_lens, words(a.bs))}))
     return FP8MLA_ERR_INVALID_ARG;
   p.q = static_cast<const uint16_t*>(a.q);
   fill_cache(&p, a.cache, a.head_dim);
@@ -1857,7 +1875,14 @@ fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream) {
   const Rows q = block_of(a.q, rows * a.head_dim * 2), out = block_of(a.out, rows * a.head_dim * 2);
   const Rows lse = block_of(a.lse, rows * 4), ws = block_of(a.workspace, s.bytes);
   if (clobbers(out, q) || rows_overlap(lse, q) || rows_overlap(ws, q) || rows_overlap(out, lse) ||
-      rows_overlap(out, ws) || rows_overlap(lse, ws))
+      rows_overlap(out, ws) || rows_overlap(lse, ws) || meets_cache({out, lse, ws}, a.cache, a.h_kv, a.head_dim) ||
+      meets({out, lse, ws}, {block_of(a.block_table, words(a.bs, a.max_blocks)), block_of(a.seqlens, words(a.bs)),
+                             block_of(a.spec_mask, static_cast<uint64_t>(tokens) * a.q_len),
+                             block_of(a.sinks, words(a.h_q))}) ||
+      (a.n_prefixes > 0 &&
+       meets({out, lse, ws}, {block_of(a.prefix_table, words(a.n_prefixes, a.prefix_blocks)),
+                              block_of(a.prefix_lens, words(a.n_prefixes)),
+                              block_of(a.prefix_starts, words(a.n_prefixes + 1ll))})))
     return FP8MLA_ERR_INVALID_ARG;
   p.q = static_cast<const uint16_t*>(a.q);
   fill_cache(&p, a.cache, a.head_dim);
