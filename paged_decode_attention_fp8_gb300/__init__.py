@@ -731,9 +731,10 @@ def wait_timeout_site(device=None):
 
 
 def set_wait_test(fault_page: int = 0, wait_limit_ns: int = 0) -> None:
-    """Test hook of the bounded waits of the FP8-dots MLA decode (current device):
-    fault_page = p + 1 makes CTA 0 of work unit 0 skip the loads of its p-th page,
-    so its waits run out (0 = off); wait_limit_ns replaces the wait limit (0 = default)."""
+    """Test hook of the bounded waits of the FP8-dots MLA decode, cross attention and shared
+    prefixes (current device): fault_page = p + 1 makes CTA 0 of work unit 0 skip the loads of
+    its p-th page (tile of 128 keys of K), so its waits run out (0 = off); wait_limit_ns replaces
+    the wait limit (0 = default)."""
     _check(lib().fp8mla_set_wait_test(int(fault_page), int(wait_limit_ns)), "fp8mla_set_wait_test")
 
 

@@ -58,6 +58,10 @@
 namespace fp8mla {
 
 __device__ uint32_t g_status_ragged;
+// Test hook (ragged_set_wait_test): how long a wait may take, and the tile of K, from 1 on, that CTA 0 does not copy.
+constexpr uint32_t kRaggedWaitLimit = 3500000000u;  // ns, of 32 bits
+__device__ uint32_t g_ragged_wait_limit = kRaggedWaitLimit;
+__device__ uint32_t g_ragged_fault_tile = 0;
 
 namespace ragged {
 
@@ -445,9 +449,8 @@ constexpr size_t smem_bytes() {
   return Lay<kHd, kRows>::kOffCtl + sizeof(Control<kHd, kRows>);
 }
 
-// Bounded waits of this kernel, in few instructions (it has to stay in the instruction cache): after kWaitLimit of
+// Bounded waits of this kernel, in few instructions (it has to stay in the instruction cache): after the limit of
 // polling without success, or once another warp gave up, false; the CTA then reports it at its end.
-constexpr uint32_t kWaitLimit = 3500000000u;  // ns
 __device__ __forceinline__ uint32_t timer_lo() {
   uint32_t t;
   asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
@@ -462,7 +465,7 @@ __device__ __forceinline__ bool wait_until(volatile uint32_t* abort_flag, Done d
 #pragma unroll 1
     do {
       if (*abort_flag) break;
-      if (++polls > kWaitMinPolls && timer_lo() - t0 > kWaitLimit) *abort_flag = 1u;
+      if (++polls > kWaitMinPolls && timer_lo() - t0 > *(volatile uint32_t*)&g_ragged_wait_limit) *abort_flag = 1u;
       ok = done();
     } while (!ok);
   }
@@ -1201,6 +1204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* tiles_at = smem + (is_v ? L::kOffV : L::kOffK);
       const bool leader = elect_one();
       if (leader) tma_prefetch_desc(map);
+      const uint32_t fault = unit == 0 && !is_v ? *reinterpret_cast<volatile uint32_t*>(&g_ragged_fault_tile) : 0;
       uint32_t done = 0, slot = 0, phase = 1;
       bool ok = true;
       const int chunk_shift = min(p.page_shift, 7);  // keys a copy
@@ -1228,8 +1232,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const int valid = min(kTile, keys - tile * kTile);
-          const int copies = ((valid - 1) >> chunk_shift) + 1;  // whole pages, or 128 keys of one
-          if (leader) mbar_arrive_expect_tx(full + slot, static_cast<uint32_t>(copies) * (kHd << chunk_shift));
+          // whole pages, or 128 keys of one
+          const int copies = done + 1 == fault ? 0 : ((valid - 1) >> chunk_shift) + 1;
+          if (leader && copies > 0) mbar_arrive_expect_tx(full + slot, static_cast<uint32_t>(copies) * (kHd << chunk_shift));
           const int row = ((block * p.h_kv + head) << p.page_shift) + ((tile * kTile) & in_page);
           uint8_t* to = tiles_at + slot * L::kRaw;
 #pragma unroll 1
@@ -1257,7 +1262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kRows) cp_async_wait_all();  // this lane's copies have landed before the CTA can exit
 #pragma unroll 1
       for (uint32_t j = done > ring ? done - ring : 0; j < done; ++j)
-        warp_wait(full + j % ring, (j / ring) & 1, &sm->never);
+        if (j + 1 != fault) warp_wait(full + j % ring, (j / ring) & 1, &sm->never);
     } else if (warp == 14) {
       // ------------------------------------------------- the share's items --
       const bool fits = find_share(p, unit, &sm->walk, sm->group_at);
@@ -1922,6 +1927,14 @@ fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream) {
            : merge(shared_merge_kernel<128, 4>, kSharedRows<128, 4>);
   }
   return e == cudaSuccess ? FP8MLA_OK : FP8MLA_ERR_CUDA;
+}
+
+cudaError_t ragged_set_wait_test(int fault_tile, uint64_t wait_limit_ns) {
+  const uint32_t tile = static_cast<uint32_t>(fault_tile), most = kRaggedWaitLimit;
+  const uint32_t limit = wait_limit_ns == 0 ? most : static_cast<uint32_t>(std::min<uint64_t>(wait_limit_ns, most));
+  cudaError_t e = cudaMemcpyToSymbol(g_ragged_fault_tile, &tile, sizeof(tile));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_ragged_wait_limit, &limit, sizeof(limit));
+  return e;
 }
 
 uint32_t ragged_read_and_clear_status() {

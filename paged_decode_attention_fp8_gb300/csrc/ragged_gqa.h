@@ -62,6 +62,9 @@ size_t cross_workspace_bytes(int n_tokens, int bs, int h_q, int h_kv, int head_d
 fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream);
 size_t shared_workspace_bytes(int bs, int q_len, int h_q, int h_kv, int head_dim, int n_prefixes,
                               long long max_prefix_keys, long long max_keys);
+// Test hook of the bounded waits: CTA 0 of later launches skips its fault_tile-th tile of K (0 = off); wait_limit_ns
+// replaces the wait limit (0 = the default, the most).
+cudaError_t ragged_set_wait_test(int fault_tile, uint64_t wait_limit_ns);
 uint32_t ragged_read_and_clear_status();
 
 }  // namespace fp8mla
