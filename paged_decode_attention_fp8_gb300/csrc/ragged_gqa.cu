@@ -456,16 +456,22 @@ __device__ __forceinline__ uint32_t timer_lo() {
   asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
   return t;
 }
-template <typename Done>
+// Waits for an item to be told or left take as long as items do, up to half a minute for 2^30 keys: kItemLimits times the
+// limit.  The warps that are at work on one have the plain limit, and end these waits where they give up.
+constexpr int kItemLimits = 32;
+template <int kLimits = 1, typename Done>
 __device__ __forceinline__ bool wait_until(volatile uint32_t* abort_flag, Done done) {
   bool ok = done();
   if (!ok) {
-    const uint32_t t0 = timer_lo();
-    uint32_t polls = 0;
+    uint32_t t0 = timer_lo(), polls = 0;
+    [[maybe_unused]] int limits = kLimits;
 #pragma unroll 1
     do {
       if (*abort_flag) break;
-      if (++polls > kWaitMinPolls && timer_lo() - t0 > *(volatile uint32_t*)&g_ragged_wait_limit) *abort_flag = 1u;
+      if (++polls > kWaitMinPolls && timer_lo() - t0 > *(volatile uint32_t*)&g_ragged_wait_limit) {
+        if (kLimits == 1 || --limits == 0) *abort_flag = 1u;
+        t0 = timer_lo(), polls = 0;
+      }
       ok = done();
     } while (!ok);
   }
@@ -473,6 +479,9 @@ __device__ __forceinline__ bool wait_until(volatile uint32_t* abort_flag, Done d
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
   return wait_until(abort_flag, [&] { return mbar_try_wait(bar, parity); });
+}
+__device__ __forceinline__ bool warp_wait_item(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  return wait_until<kItemLimits>(abort_flag, [&] { return mbar_try_wait(bar, parity); });
 }
 // Until *count has reached `want` (it only grows).
 __device__ __forceinline__ bool wait_count(volatile uint32_t* count, uint32_t want, volatile uint32_t* abort_flag) {
@@ -613,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm->tmem_base;
   // the item of number n, or none: every warp's own count
   auto get_item = [&](uint32_t n) -> const Item* {
-    if (!warp_wait(&sm->item_full[n % kItems], (n / kItems) & 1, abort_flag)) return nullptr;
+    if (!warp_wait_item(&sm->item_full[n % kItems], (n / kItems) & 1, abort_flag)) return nullptr;
     const Item* it = &sm->item[n % kItems];
     return it->end ? nullptr : it;
   };
@@ -1269,7 +1278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool more = true;
 #pragma unroll 1
       for (uint32_t n = 0; more; ++n) {
-        if (n >= kItems && !warp_wait(&sm->item_empty[n % kItems], (n / kItems - 1) & 1, abort_flag)) break;
+        if (n >= kItems && !warp_wait_item(&sm->item_empty[n % kItems], (n / kItems - 1) & 1, abort_flag)) break;
         Item* it = &sm->item[n % kItems];
         if (lane == 0) it->end = !next_item(p, unit, &sm->walk, it);
         __syncwarp();

@@ -66,3 +66,28 @@ def test_shared(q_len, hd, fault):
     pool, q, m, s, want = inputs.shared_case(33, [900], [0, 2], lens, 1, 2, hd, 16, hd == 64, q_len=q_len, sinks=True)
     before, _ = _runs_out(lambda: shared(pool, q, [900], [0, 2], lens, m, s), fault)
     assert inputs.within(*before, want, 1400) is None
+
+
+def test_items_longer_than_the_limit():
+    """A warp that tells items waits for whole ones: their length is no sign of a hang.  Each CTA has one of 2^26 keys (about
+    half a second, the limit is 20 ms and 65536 polls, a quarter of a second) and some of a few keys."""
+    dev, sms = torch.device("cuda"), torch.cuda.get_device_properties(0).multi_processor_count
+    gen = torch.Generator(device=dev).manual_seed(34)
+    k, v = (torch.randn(8, 1, 256, 64, generator=gen, device=dev).to(torch.float8_e4m3fn) for _ in range(2))
+    group = torch.tensor([256, 1, 1, 1, 1], dtype=torch.int32, device=dev).repeat(sms)
+    lens = torch.where(group == 256, 1 << 26, 20).to(torch.int32)
+    starts = torch.cat((torch.zeros(1, dtype=torch.int32, device=dev), group.cumsum(0, dtype=torch.int32)))
+    q = torch.randn(int(starts[-1]), 1, 64, generator=gen, device=dev).to(torch.bfloat16)
+    table = (torch.arange((1 << 26) // 256, device=dev, dtype=torch.int32) % 8).expand(5 * sms, -1).contiguous()
+    one = torch.ones(1, device=dev)
+    fm.last_device_error()
+    try:
+        fm.set_wait_test(0, LIMIT_NS)
+        out, lse = fm.paged_cross_attention(q, k, v, table, lens, one, one, q_starts=starts)
+        assert fm.last_device_error() == 0
+    finally:
+        fm.set_wait_test(0, 0)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    short = torch.repeat_interleave(group == 1, group.long())
+    want = fm.paged_cross_attention(q[short], k, v, table[:4 * sms, :1].contiguous(), lens[group == 1], one, one)
+    assert torch.equal(out[short], want[0]) and torch.equal(lse[short], want[1])
