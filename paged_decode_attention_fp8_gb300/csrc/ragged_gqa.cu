@@ -58,10 +58,6 @@
 namespace fp8mla {
 
 __device__ uint32_t g_status_ragged;
-// Test hook (ragged_set_wait_test): how long a wait may take, and the tile of K, from 1 on, that CTA 0 does not copy.
-constexpr uint32_t kRaggedWaitLimit = 3500000000u;  // ns, of 32 bits
-__device__ uint32_t g_ragged_wait_limit = kRaggedWaitLimit;
-__device__ uint32_t g_ragged_fault_tile = 0;
 
 namespace ragged {
 
@@ -90,6 +86,7 @@ struct Lengths {
 };
 constexpr Lengths kLengths[2][2] = {{{{24, 24, 13}, {60, 30, 26}}, {{42, 34, 15}, {56, 31, 28}}},    // head_dim 64
                                     {{{37, 26, 18}, {80, 45, 38}}, {{52, 35, 20}, {95, 58, 38}}}};  // 128: plain, row scales
+constexpr uint32_t kWaitLimit = 3500000000u;  // ns of a wait, in 32 bits
 constexpr int kEmpty = 15;  // an item without keys
 constexpr int kLeast = 60;  // a share
 constexpr int kMostUnits = 256;  // shares (one an SM)
@@ -132,6 +129,7 @@ struct Params {
   float softmax_scale;
   Lengths lengths;
   int joined, whole, tokens, h_q, h_kv, num_blocks, page_shift, slot_rows, fill_out, fill_lse, q_len;
+  uint32_t wait_limit, fault_tile;  // of the test hook: ns; the tile of K, from 1 on, that CTA 0 does not copy
 };
 
 // ---------------------------------------------------------------- the line --
@@ -456,36 +454,39 @@ __device__ __forceinline__ uint32_t timer_lo() {
   asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
   return t;
 }
-// Waits for an item to be told or left take as long as items do, up to half a minute for 2^30 keys: kItemLimits times the
-// limit.  The warps that are at work on one have the plain limit, and end these waits where they give up.
-constexpr int kItemLimits = 32;
-template <int kLimits = 1, typename Done>
-__device__ __forceinline__ bool wait_until(volatile uint32_t* abort_flag, Done done) {
+// (The limit is an argument of the kernel: read from device memory in every wait's loop it is longer code, shared many 135 ->
+// 140 us, and with a second count in the waits for items 157.)
+struct Waits {
+  volatile uint32_t* abort_flag;
+  uint32_t limit;
+};
+// Waits for an item to be told or left take as long as items do, half a minute for 2^30 keys: they have 2^24 polls (3.8 us
+// each, 64 s) before the limit counts.  The warps at work on an item give up long before, and end these waits.
+constexpr uint32_t kItemPolls = 1u << 24;
+template <uint32_t kPolls = kWaitMinPolls, typename Done>
+__device__ __forceinline__ bool wait_until(const Waits& w, Done done) {
   bool ok = done();
   if (!ok) {
-    uint32_t t0 = timer_lo(), polls = 0;
-    [[maybe_unused]] int limits = kLimits;
+    const uint32_t t0 = timer_lo();
+    uint32_t polls = 0;
 #pragma unroll 1
     do {
-      if (*abort_flag) break;
-      if (++polls > kWaitMinPolls && timer_lo() - t0 > *(volatile uint32_t*)&g_ragged_wait_limit) {
-        if (kLimits == 1 || --limits == 0) *abort_flag = 1u;
-        t0 = timer_lo(), polls = 0;
-      }
+      if (*w.abort_flag) break;
+      if (++polls > kPolls && timer_lo() - t0 > w.limit) *w.abort_flag = 1u;
       ok = done();
     } while (!ok);
   }
   return __all_sync(0xffffffffu, ok);
 }
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  return wait_until(abort_flag, [&] { return mbar_try_wait(bar, parity); });
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Waits& w) {
+  return wait_until(w, [&] { return mbar_try_wait(bar, parity); });
 }
-__device__ __forceinline__ bool warp_wait_item(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  return wait_until<kItemLimits>(abort_flag, [&] { return mbar_try_wait(bar, parity); });
+__device__ __forceinline__ bool warp_wait_item(uint64_t* bar, uint32_t parity, const Waits& w) {
+  return wait_until<kItemPolls>(w, [&] { return mbar_try_wait(bar, parity); });
 }
 // Until *count has reached `want` (it only grows).
-__device__ __forceinline__ bool wait_count(volatile uint32_t* count, uint32_t want, volatile uint32_t* abort_flag) {
-  const bool ok = wait_until(abort_flag, [&] { return static_cast<int32_t>(*count - want) >= 0; });
+__device__ __forceinline__ bool wait_count(volatile uint32_t* count, uint32_t want, const Waits& w) {
+  const bool ok = wait_until(w, [&] { return static_cast<int32_t>(*count - want) >= 0; });
   __threadfence_block();
   return ok;
 }
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Lay<kHd, kRows>;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's unit; there is no other shared memory
   Control<kHd, kRows>* sm = reinterpret_cast<Control<kHd, kRows>*>(smem + L::kOffCtl);
-  volatile uint32_t* abort_flag = &sm->abort_flag;
+  const Waits waits{&sm->abort_flag, p.wait_limit}, to_the_end{&sm->never, p.wait_limit};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int unit = blockIdx.x;
 
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm->tmem_base;
   // the item of number n, or none: every warp's own count
   auto get_item = [&](uint32_t n) -> const Item* {
-    if (!warp_wait_item(&sm->item_full[n % kItems], (n / kItems) & 1, abort_flag)) return nullptr;
+    if (!warp_wait_item(&sm->item_full[n % kItems], (n / kItems) & 1, waits)) return nullptr;
     const Item* it = &sm->item[n % kItems];
     return it->end ? nullptr : it;
   };
@@ -642,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int was = -1;
     auto exchange = [&]() -> bool {
       warp_arrive(&sm->xchg);
-      return warp_wait(&sm->xchg, xchgs++ & 1, abort_flag);
+      return warp_wait(&sm->xchg, xchgs++ & 1, waits);
     };
     for (uint32_t n = 0;; ++n) {
       const Item* it = get_item(n);
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ref = kNegInf, l = 0.f, cc = 1.f;
       [[maybe_unused]] bool apart = false;  // a tile's V scales were far from one (the same in all warps)
       if (tiles > 0) {
-        if (!warp_wait(&sm->q_full, worked & 1, abort_flag)) break;
+        if (!warp_wait(&sm->q_full, worked & 1, waits)) break;
         if (form != was) {
           if (was >= 0 && !exchange()) break;  // the other form's columns are free
           if (few) {               // P: a quarter's own keys alone are written, the others stay zero
@@ -680,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int cols = few ? 16 : 64, col0 = (few ? w * 32 : 0) + wg * cols, end0 = few ? w * 32 + 32 : 128;
           // O and l follow a new reference.
           auto rescale = [&](int i, float alpha) -> bool {
-            if (!kPair && !warp_wait(&sm->pv_done, (pv_base + i - 1) & 1, abort_flag)) return false;
+            if (!kPair && !warp_wait(&sm->pv_done, (pv_base + i - 1) & 1, waits)) return false;
             tc_fence_after();
             if (!kRows || !apart) l *= alpha;
 #pragma unroll 1
@@ -697,11 +698,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < tiles; ++i, keys -= kTile) {
             const int buf = kPair ? wg : (i & 1);
-            if (kRows && !warp_wait(&sm->scl_full[tile_no % L::kScls], (tile_no / L::kScls) & 1, abort_flag)) return false;
+            if (kRows && !warp_wait(&sm->scl_full[tile_no % L::kScls], (tile_no / L::kScls) & 1, waits)) return false;
             [[maybe_unused]] const bool first = !apart;
             if constexpr (kRows)  // (before the wait for S, which hides it)
               apart = apart || *reinterpret_cast<const volatile uint32_t*>(sm->scl_far[tile_no % L::kScls]) != 0;
-            if (!warp_wait(&sm->s_full[buf], (s_phase >> buf) & 1, abort_flag)) return false;
+            if (!warp_wait(&sm->s_full[buf], (s_phase >> buf) & 1, waits)) return false;
             s_phase ^= 1u << buf;
             if (busy) {
               const uint32_t t_s = lanes + kTS + buf * 128;
@@ -955,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int os = pair ? wg : 0;
       if (tiles > 0) {
         ++worked;
-        if (!warp_wait(&sm->o_full[os], (o_phase >> os) & 1, abort_flag)) break;
+        if (!warp_wait(&sm->o_full[os], (o_phase >> os) & 1, waits)) break;
         o_phase ^= pair ? 3u : 1u;
         tc_fence_after();
       }
@@ -1060,10 +1061,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tiles > 0) {
         // Q, once the products have left the one before, and the softmax has seen it (else it would miss a phase)
         const int form = it->form, w = warp - 8;
-        if (worked > 0 && (!warp_wait(&sm->q_empty, (worked - 1) & 1, abort_flag) ||
-                           !warp_wait(&sm->q_seen, (worked - 1) & 1, abort_flag)))
+        if (worked > 0 && (!warp_wait(&sm->q_empty, (worked - 1) & 1, waits) ||
+                           !warp_wait(&sm->q_seen, (worked - 1) & 1, waits)))
           break;
-        if (kHd == 128 && form == kFormPair && !wait_count(&sm->sums_read, sums, abort_flag)) break;  // they lie there
+        if (kHd == 128 && form == kFormPair && !wait_count(&sm->sums_read, sums, waits)) break;  // they lie there
         int8_t* q_exp = sm->q_exp[0];
         const int stream = form == kFormPair ? w / 2 : 0;
         const int count = form == kFormPair ? 64 : (form == kFormOne ? 32 : 8);  // a warp's rows
@@ -1078,7 +1079,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       drop_item(n);
       for (int i = 0; i < tiles; ++i, ++done, valid -= kTile) {
         ok = false;
-        if (!warp_wait(&sm->v_full[vs], v_phase, abort_flag)) break;
+        if (!warp_wait(&sm->v_full[vs], v_phase, waits)) break;
         if constexpr (kRows) {  // past the end: one, so that a stale scale cannot turn a zero weight into a NaN
           const float a = tid < valid ? sm->raw_scl[vs][0][tid] : 1.f, b = tid < valid ? sm->raw_scl[vs][1][tid] : 1.f;
           const int ss = done % L::kScls;
@@ -1091,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) sm->scl_far[ss][warp - 8] = far;
           warp_arrive(&sm->scl_full[ss]);
         }
-        if (done >= L::kFs && !warp_wait(&sm->f_empty[fs], f_phase, abort_flag)) break;
+        if (done >= L::kFs && !warp_wait(&sm->f_empty[fs], f_phase, waits)) break;
         const uint8_t* src = smem + L::kOffV + vs * L::kRaw + from;
         uint8_t* dst = smem + L::kOffF + fs * L::kF + to;
 #pragma unroll
@@ -1126,10 +1127,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t qb = smem_u32(smem), kb = qb + L::kOffK, fb = qb + L::kOffF;
       uint32_t at = 0, p_phase = 0, worked = 0;  // at: tiles before this item's
       bool ok = true;
-      auto wait_k = [&](uint32_t t) { return warp_wait(&sm->k_full[t % L::kKs], (t / L::kKs) & 1, abort_flag); };
-      auto wait_v = [&](uint32_t t) { return warp_wait(&sm->f_full[t % L::kFs], (t / L::kFs) & 1, abort_flag); };
+      auto wait_k = [&](uint32_t t) { return warp_wait(&sm->k_full[t % L::kKs], (t / L::kKs) & 1, waits); };
+      auto wait_v = [&](uint32_t t) { return warp_wait(&sm->f_full[t % L::kFs], (t / L::kFs) & 1, waits); };
       auto wait_p = [&](int buf) {
-        const bool done = warp_wait(&sm->p_full[buf], (p_phase >> buf) & 1, abort_flag);
+        const bool done = warp_wait(&sm->p_full[buf], (p_phase >> buf) & 1, waits);
         p_phase ^= 1u << buf;
         return done;
       };
@@ -1170,7 +1171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         drop_item(n);
         if (tiles == 0) continue;
         ok = false;
-        if (!warp_wait(&sm->q_full, worked++ & 1, abort_flag)) break;
+        if (!warp_wait(&sm->q_full, worked++ & 1, waits)) break;
         // Operation j is a product with P and one with K two operations ahead, in its buffer: with two streams S(j % 2)
         // and a tile in two operations, with one stream the tile's parity and a tile in each.
         const int per = pair ? 2 : 1, ops = tiles * per;
@@ -1202,7 +1203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (leader) tc_commit(&sm->final_mma);
       __syncwarp();
-      warp_wait(&sm->final_mma, 0, &sm->never);
+      warp_wait(&sm->final_mma, 0, to_the_end);
     } else if (warp != 14) {
       // -------------------------------------- copies of tiles: 13 K, 15 V --
       const bool is_v = warp == 15;
@@ -1213,7 +1214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* tiles_at = smem + (is_v ? L::kOffV : L::kOffK);
       const bool leader = elect_one();
       if (leader) tma_prefetch_desc(map);
-      const uint32_t fault = unit == 0 && !is_v ? *reinterpret_cast<volatile uint32_t*>(&g_ragged_fault_tile) : 0;
+      const uint32_t fault = unit == 0 && !is_v ? p.fault_tile : 0;
       uint32_t done = 0, slot = 0, phase = 1;
       bool ok = true;
       const int chunk_shift = min(p.page_shift, 7);  // keys a copy
@@ -1236,7 +1237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicOr(&g_status_ragged, FP8MLA_DEV_BAD_PAGE);
             block = 0;
           }
-          if (done >= ring && !warp_wait(empty + slot, phase, abort_flag)) {
+          if (done >= ring && !warp_wait(empty + slot, phase, waits)) {
             ok = false;
             break;
           }
@@ -1271,14 +1272,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kRows) cp_async_wait_all();  // this lane's copies have landed before the CTA can exit
 #pragma unroll 1
       for (uint32_t j = done > ring ? done - ring : 0; j < done; ++j)
-        if (j + 1 != fault) warp_wait(full + j % ring, (j / ring) & 1, &sm->never);
+        if (j + 1 != fault) warp_wait(full + j % ring, (j / ring) & 1, to_the_end);
     } else if (warp == 14) {
       // ------------------------------------------------- the share's items --
       const bool fits = find_share(p, unit, &sm->walk, sm->group_at);
       bool more = true;
 #pragma unroll 1
       for (uint32_t n = 0; more; ++n) {
-        if (n >= kItems && !warp_wait_item(&sm->item_empty[n % kItems], (n / kItems - 1) & 1, abort_flag)) break;
+        if (n >= kItems && !warp_wait_item(&sm->item_empty[n % kItems], (n / kItems - 1) & 1, waits)) break;
         Item* it = &sm->item[n % kItems];
         if (lane == 0) it->end = !next_item(p, unit, &sm->walk, it);
         __syncwarp();
@@ -1607,6 +1608,18 @@ __global__ void __launch_bounds__(kMergeThreads)
 
 // -------------------------------------------------------------------- host --
 
+// The test hook's settings by device (limit 0: the default).
+constexpr int kMostDevices = 64;
+std::atomic<uint32_t> g_wait_limit[kMostDevices], g_fault_tile[kMostDevices];
+
+void use_wait_test(Params* p) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMostDevices) dev = 0;
+  const uint32_t limit = g_wait_limit[dev].load(std::memory_order_relaxed);
+  p->wait_limit = limit != 0 ? limit : kWaitLimit;
+  p->fault_tile = g_fault_tile[dev].load(std::memory_order_relaxed);
+}
+
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 struct Space {  // the workspace: offsets, and the grid it is for
@@ -1817,6 +1830,7 @@ fp8mla_status_t cross_entry(const CrossArgs& a, cudaStream_t stream) {
   p.fill_out = a.fill_out;
   p.fill_lse = a.fill_lse;
   use(&p, s, a.workspace);
+  use_wait_test(&p);
   // Items that are short and no more than the SMs, as far as the table's width shows, are not cut, and the merge's launch
   // is left out.  One token x 16 heads of 64 by 100, 400, 1024, 1280, 2048 keys (lengths 39 to 234): 9.9, 9.9, 12.8, 14.4,
   // 19.3 us whole, 11.5, 12.8, 13.5, 13.7, 14.2 cut; 128 items of up to 640 keys of 128 dims (138) 13.9 and 17.4.
@@ -1921,6 +1935,7 @@ fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream) {
   p.h_kv = a.h_kv;
   p.q_len = a.q_len;
   use(&p, s, a.workspace);
+  use_wait_test(&p);
   cudaError_t e = launch_any(p, a.head_dim, a.cache.scale_rows, s.grid, stream);
   if (e == cudaSuccess) {
     const int total = static_cast<int>(rows);
@@ -1939,11 +1954,12 @@ fp8mla_status_t shared_entry(const SharedArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t ragged_set_wait_test(int fault_tile, uint64_t wait_limit_ns) {
-  const uint32_t tile = static_cast<uint32_t>(fault_tile), most = kRaggedWaitLimit;
-  const uint32_t limit = wait_limit_ns == 0 ? most : static_cast<uint32_t>(std::min<uint64_t>(wait_limit_ns, most));
-  cudaError_t e = cudaMemcpyToSymbol(g_ragged_fault_tile, &tile, sizeof(tile));
-  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_ragged_wait_limit, &limit, sizeof(limit));
-  return e;
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= ragged::kMostDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  ragged::g_fault_tile[dev] = static_cast<uint32_t>(fault_tile);
+  ragged::g_wait_limit[dev] = static_cast<uint32_t>(std::min<uint64_t>(wait_limit_ns, ragged::kWaitLimit));
+  return cudaSuccess;
 }
 
 uint32_t ragged_read_and_clear_status() {
