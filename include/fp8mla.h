@@ -530,8 +530,9 @@ FP8MLA_API size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int h
  * a row's largest on exactly (others to 2^-18 of it); P is rounded to f16, sums
  * are float32.  A NaN reaches the rows of its sequence, and those alone.
  * Requires head_dim 64 or 128, page_size 16, 32, 64, 128 or 256, h_q % h_kv == 0,
- * h_q <= 65536, n_tokens * h_q <= 2^30, max_blocks * page_size <= 2^30, fewer than
- * 2^31 rows (num_blocks * h_kv * page_size) a cache. */
+ * h_q <= 65536, n_tokens * h_q <= 2^30, max_blocks * page_size <= 2^30,
+ * bs <= 2^26 (with n_prefixes, below), fewer than 2^31 rows (num_blocks * h_kv *
+ * page_size) a cache. */
 FP8MLA_API fp8mla_status_t paged_cross_attention(
     const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache, const void* v_cache,
     fp8mla_kv_dtype_t kv_dtype, int num_blocks, const float* k_scale, const float* v_scale, int scale_rows,

@@ -1769,6 +1769,8 @@ uint64_t words(long long n, long long m = 1) { return static_cast<uint64_t>(n) *
 
 constexpr long long kMostKeys = 1ll << 30;  // a segment
 constexpr long long kMostRows = 1ll << 30;  // tokens * h_q
+// Segments: every CTA counts through them (0.7 s for as many), and their numbers and a warp's more stay in 32 bits.
+constexpr long long kMostSegments = 1ll << 26;
 
 }  // namespace ragged
 
@@ -1777,7 +1779,7 @@ static bool table_ok(const int32_t* table, int columns) { return columns > 0 ? t
 
 size_t cross_workspace_bytes(int n_tokens, int bs, int h_q, int h_kv, int head_dim, long long max_keys) {
   using namespace ragged;
-  if (!heads_ok(h_q, h_kv, head_dim) || n_tokens < 0 || bs < 0 || max_keys < 0 || max_keys > kMostKeys ||
+  if (!heads_ok(h_q, h_kv, head_dim) || n_tokens < 0 || bs < 0 || bs > kMostSegments || max_keys < 0 || max_keys > kMostKeys ||
       static_cast<long long>(n_tokens) * h_q > kMostRows)
     return 0;
   const int group = h_q / h_kv;
@@ -1787,7 +1789,7 @@ size_t cross_workspace_bytes(int n_tokens, int bs, int h_q, int h_kv, int head_d
 fp8mla_status_t cross_entry(const CrossArgs& a, cudaStream_t stream) {
   using namespace ragged;
   Params p = {};
-  if (!heads_ok(a.h_q, a.h_kv, a.head_dim) || a.n_tokens < 0 || a.bs < 0 || a.max_blocks < 0 ||
+  if (!heads_ok(a.h_q, a.h_kv, a.head_dim) || a.n_tokens < 0 || a.bs < 0 || a.bs > kMostSegments || a.max_blocks < 0 ||
       !(a.softmax_scale > 0.f) || !cache_ok(a.cache, a.h_kv, &p.page_shift))
     return FP8MLA_ERR_INVALID_ARG;
   const long long max_keys = static_cast<long long>(a.max_blocks) << p.page_shift;
@@ -1860,7 +1862,7 @@ bool shared_sizes_ok(int bs, int q_len, int h_q, int h_kv, int head_dim, int n_p
   return heads_ok(h_q, h_kv, head_dim) && bs >= 0 && q_len >= 1 && q_len <= 32 && n_prefixes >= 0 &&
          max_prefix_keys >= 0 && max_prefix_keys <= kMostKeys && max_keys >= 0 && max_keys <= kMostKeys &&
          static_cast<long long>(bs) * q_len * h_q <= kMostRows && static_cast<long long>(bs) * h_kv <= 0x7FFFFFFF &&
-         static_cast<long long>(n_prefixes) + bs <= kMostRows;
+         static_cast<long long>(n_prefixes) + bs <= kMostSegments;
 }
 }  // namespace ragged
 
