@@ -199,9 +199,9 @@ FP8MLA_API fp8mla_status_t fp8mla_decode(const void* q, const void* kv_cache, fp
  *                  when set, row t of physical page p (its 512 latent and 64
  *                  RoPE values, K and V alike) is E4M3 code times
  *                  kv_scale_rows[p * 64 + t], every scale of a row a key uses
- *                  must be positive and finite, kv_scale is ignored (may be
- *                  NULL), and only FP8MLA_DOT_FP8 is accepted
- *                  (FP8MLA_ERR_INVALID_ARG otherwise)
+ *                  must be from 0 to 2^16 (those below 2^-110 count as that for
+ *                  V), kv_scale is ignored (may be NULL), and only
+ *                  FP8MLA_DOT_FP8 is accepted (FP8MLA_ERR_INVALID_ARG otherwise)
  *   kv_scale_rows NULL: exactly fp8mla_decode.
  * Other arguments, results and errors as fp8mla_decode. */
 FP8MLA_API fp8mla_status_t fp8mla_decode_ext(const void* q, const void* kv_cache, fp8mla_kv_dtype_t kv_dtype,
@@ -275,7 +275,8 @@ FP8MLA_API fp8mla_status_t paged_gqa_decode(const void* q, const void* k_cache, 
  *                sequence, taken to be its last q_len cache positions (token i
  *                at position s_k - q_len + i)
  *   k_scale, v_scale  float32 [1] each, or with scale_per_row != 0 one float
- *                per cached row, [num_blocks, h_kv, page_size], 16-byte aligned
+ *                per cached row, [num_blocks, h_kv, page_size], 16-byte aligned,
+ *                0 to 2^16; V's below 2^-110 count as 2^-110
  *   spec_mask    uint8 [bs, q_len, q_len] (device) or NULL: token i sees key
  *                s_k - q_len + c of its own block iff spec_mask[b][i][c] != 0;
  *                NULL = causal inside the block (c <= i).  Keys before the

@@ -211,6 +211,12 @@ __device__ __forceinline__ void finish_row(float m, float l, float sink, float v
   *lse = (mm + lg2_approx(den)) * kLn2;
 }
 
+// A V row's scale whose log2 goes into the row's weight and whose inverse takes it out of the sum: below 2^-126 the first
+// is -inf and the second past float32, and the sum of many keys is before that.  From 2^-110 down it counts as 2^-110, which
+// keeps the sum right (up to 2^17 keys that are all so small) and puts a row's values off by 2^-101 at most.  (A NaN stays
+// one.)
+__device__ __forceinline__ float v_row_scale(float s) { return s < 0x1p-110f ? 0x1p-110f : s; }
+
 // n / d by a multiply-high (see make_fast_div)
 struct FastDiv {
   uint32_t d, m, s;

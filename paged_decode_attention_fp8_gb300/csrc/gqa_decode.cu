@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(x2::kThreads, 2)
           break;
         }
         if (live) {
-          const float sv = sm->row_scale[st][1][r];
+          const float sv = v_row_scale(sm->row_scale[st][1][r]);
           sk = sm->row_scale[st][0][r];
           lsv = lg2_approx(sv);
           isv = 1.f / sv;

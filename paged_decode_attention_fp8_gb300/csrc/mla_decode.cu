@@ -636,8 +636,9 @@ __global__ void __launch_bounds__(f8::kThreads, 1)
         if constexpr (kRowScales) {  // key t's scale (1 past the end), its log2 and its inverse, for the softmax
           const float sgm = dead ? 1.f : bars->scl[st][0][t];
           bars->scl[st][0][t] = sgm;
-          bars->scl[st][1][t] = lg2_approx(sgm);
-          bars->scl[st][2][t] = 1.f / sgm;
+          const float sv = v_row_scale(sgm);
+          bars->scl[st][1][t] = lg2_approx(sv);
+          bars->scl[st][2][t] = 1.f / sv;
         }
         const uint4 z = make_uint4(0, 0, 0, 0);
         const int sw = t & 7;
