@@ -527,8 +527,8 @@ FP8MLA_API size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int h
  * out may be q (strided alike); out, lse and workspace overlap nothing else
  * (refused).  A length or token range that does not fit sets
  * FP8MLA_DEV_BAD_SEQLEN and counts as empty, a page outside the cache
- * FP8MLA_DEV_BAD_PAGE.  Products take K and V exactly, Q's values from 2^-10 of
- * a row's largest on exactly (others to 2^-18 of it); P is rounded to f16, sums
+ * FP8MLA_DEV_BAD_PAGE.  Products take K and V exactly, Q's values from 2^-9.8 of
+ * a row's largest on exactly (others to 2^-17.8 of it); P is rounded to f16, sums
  * are float32.  A NaN reaches the rows of its sequence, and those alone.
  * Requires head_dim 64 or 128, page_size 16, 32, 64, 128 or 256, h_q % h_kv == 0,
  * h_q <= 65536, n_tokens * h_q <= 2^30, max_blocks * page_size <= 2^30,

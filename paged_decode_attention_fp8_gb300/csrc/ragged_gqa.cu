@@ -31,13 +31,14 @@
 //     eight share them (decode step 114 -> 90 us).
 //   Shares of a line and not an item a CTA: lengths differ by ten times in a batch; lengths by form, head_dim and scales
 //     as measured (prompts 39 -> 37 us), empty sequences at their 0.75 us (decode step 54 -> 50).
-//   One warp that tells items: with the walk in every role they spilled (605 -> 421 us).  Short code: a launch's
+//   One warp that tells items: with the walk in every role they spilled (605 -> 421 us; 8 to 28 bytes now).  Short code: a launch's
 //     instructions come from memory, and a loop of all roles has to stay in the instruction cache (decode step 71 -> 53).
 //   No maximum where sums show that none is needed (pair form without row scales): 128 comparisons a row and tile less.
 //
 // Measured (GB300, calls from a graph over three inputs): 2048 tokens x 32 heads by 16384 keys of 8 heads, head_dim 128,
-// 380 us = 1446 TFLOP/s, 0.76 of a library bf16 product; 64 tokens by 128 to 1600 keys with row scales 50 us, by 16000
-// keys 5.4 TB/s, 0.79 of a copy; one token by 777 keys 12.5 us; 64 sequences behind a prefix of 32768 keys 80 us.
+// 387 us = 1420 TFLOP/s, 0.75 of a library bf16 product; 64 tokens by 128 to 1600 keys with row scales 51 us; 64 tokens by
+// 16000 keys 394 us = 0.79 of a copy, with row scales 506 = 0.63 (pages of 16; of 64: 385 and 436); one token by 777 keys
+// 12.7 us; 64 sequences behind a prefix of 32768 keys 80 us.
 // In the first of them the tensor pipe is active 61 to 63 % of the time, XU 31, ALU 25, DRAM 2: no unit is full.  A tile
 // takes either stream about 3400 cycles for 2048 of the tensor core: product, scores loaded (220), weighed (1150), P
 // written (250), the issuing warp's turn (600), product with P and the next with K, each queued behind the other
@@ -500,9 +501,9 @@ __device__ __forceinline__ int exponent_448(float amax) {
 }
 
 // Rows [first, first + count) of a stream (row0: its first in the item) in shared memory: each times a power of two that
-// puts its largest value up to 448, as two E4M3 terms, x = E4M3(x) + E4M3(x - E4M3(x)) (exact for bf16 from 2^-10 of the
-// row's largest value on).  Where `quarters`, in all quarters of the lanes.  head_dim 128: a tile of 128-byte rows per
-// term; 64: both terms in one row.
+// puts its largest value into (224, 448], as two E4M3 terms, x = E4M3(x) + E4M3(x - E4M3(x)): exact for bf16 from 2^-2 on
+// (2^-9.8 of the row's largest value), else off by 2^-10 at most, half of E4M3's last step (2^-17.8 of it).  Where
+// `quarters`, in all quarters of the lanes.  head_dim 128: a tile of 128-byte rows per term; 64: both terms in one row.
 template <int kHd>
 __device__ __forceinline__ void load_q(const Params& p, const Item& it, uint8_t* q_tile, int8_t* q_exp, int row0,
                                        int first, int count, bool quarters, int lane) {
@@ -1769,7 +1770,7 @@ uint64_t words(long long n, long long m = 1) { return static_cast<uint64_t>(n) *
 
 constexpr long long kMostKeys = 1ll << 30;  // a segment
 constexpr long long kMostRows = 1ll << 30;  // tokens * h_q
-// Segments: every CTA counts through them (0.7 s for as many), and their numbers and a warp's more stay in 32 bits.
+// Segments: every CTA counts through them (14 ns each, 0.9 s for as many), and their numbers stay in 32 bits.
 constexpr long long kMostSegments = 1ll << 26;
 
 }  // namespace ragged
@@ -1835,7 +1836,9 @@ fp8mla_status_t cross_entry(const CrossArgs& a, cudaStream_t stream) {
   use_wait_test(&p);
   // Items that are short and no more than the SMs, as far as the table's width shows, are not cut, and the merge's launch
   // is left out.  One token x 16 heads of 64 by 100, 400, 1024, 1280, 2048 keys (lengths 39 to 234): 9.9, 9.9, 12.8, 14.4,
-  // 19.3 us whole, 11.5, 12.8, 13.5, 13.7, 14.2 cut; 128 items of up to 640 keys of 128 dims (138) 13.9 and 17.4.
+  // 19.3 us whole, 11.5, 12.8, 13.5, 13.7, 14.2 cut; 128 items of up to 640 keys of 128 dims (138) 13.9 and 17.4.  A table
+  // that is wider than the keys, as one kept for the longest context, hides that they are short: then they are cut (777 keys
+  // of 64 dims 12.7 us, with a table of 16384 keys 13.3; 128 items of up to 600 keys 14.2 and 16.8).
   const long long tiles = (max_keys + kTile - 1) / kTile, all_rows = static_cast<long long>(a.n_tokens) * group;
   const int form = form_of(a.q_starts ? static_cast<int>(std::min<long long>(all_rows, kItemRows)) : group);
   const long long items = a.h_kv * (a.q_starts ? all_rows / kItemRows + a.bs : a.bs);
