@@ -461,9 +461,9 @@ struct Waits {
   volatile uint32_t* abort_flag;
   uint32_t limit;
 };
-// Waits for an item to be told or left take as long as items do, half a minute for 2^30 keys: they have 2^24 polls (3.8 us
-// each, 64 s) before the limit counts.  The warps at work on an item give up long before, and end these waits.
-constexpr uint32_t kItemPolls = 1u << 24;
+// Waits for an item to be told or left take as long as items do, half a minute for 2^30 keys and more with sums apart: they
+// have 2^25 polls (3.8 us each, two minutes) before the limit counts.  The warps at work on an item give up long before, and end these waits.
+constexpr uint32_t kItemPolls = 1u << 25;
 template <uint32_t kPolls = kWaitMinPolls, typename Done>
 __device__ __forceinline__ bool wait_until(const Waits& w, Done done) {
   bool ok = done();
@@ -1306,23 +1306,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t >= lo) t += hi - lo;
             fill(t, h);
           }
-        } else {  // a lane's token is looked for in every segment
+        } else {  // those that no segment has, a bit each: 32 kWords a lane at a time, while all segments pass by
+          constexpr int kWords = 4, kTokens = 32 * 32 * kWords;
 #pragma unroll 1
-          for (int t0 = unit * 32; t0 < p.tokens; t0 += gridDim.x * 32) {
-            const int t = t0 + lane;
-            bool has = t >= p.tokens;
-            int a = __ldg(l.starts);
-#pragma unroll 4
-            for (int s = 0; s < l.n; ++s) {
-              const int b = __ldg(l.starts + s + 1);
-              has |= range_ok(l, a, b) && a <= t && t < b;
-              a = b;
+          for (int t0 = unit * kTokens; t0 < p.tokens; t0 += gridDim.x * kTokens) {
+            uint32_t has[kWords] = {};
+#pragma unroll 1
+            for (int s0 = 0; s0 < l.n; s0 += 32) {
+              const int s = min(s0 + lane, l.n - 1);
+              const int a = __ldg(l.starts + s), b = __ldg(l.starts + s + 1);
+              uint32_t here = __ballot_sync(0xffffffffu, range_ok(l, a, b) && a < t0 + kTokens && b > t0);
+#pragma unroll 1
+              for (; here != 0; here &= here - 1) {
+                const int from = __shfl_sync(0xffffffffu, a, __ffs(here) - 1), to = __shfl_sync(0xffffffffu, b, __ffs(here) - 1);
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) {
+                  const int first = t0 + (k * 32 + lane) * 32, lo = max(from - first, 0), hi = min(to - first, 32);
+                  if (lo < hi) has[k] |= (~0u << lo) & (~0u >> (32 - hi));
+                }
+              }
             }
-            uint32_t without = __ballot_sync(0xffffffffu, !has);
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
 #pragma unroll 1
-            for (; without != 0; without &= without - 1)
+              for (int src = 0; src < 32; ++src) {
+                uint32_t without = ~__shfl_sync(0xffffffffu, has[k], src);
 #pragma unroll 1
-              for (int h = 0; h < p.h_q; ++h) fill(t0 + __ffs(without) - 1, h);
+                for (; without != 0; without &= without - 1) {
+                  const int t = t0 + (k * 32 + src) * 32 + __ffs(without) - 1;
+                  if (t >= p.tokens) break;
+#pragma unroll 1
+                  for (int h = 0; h < p.h_q; ++h) fill(t, h);
+                }
+              }
+            }
           }
         }
       }

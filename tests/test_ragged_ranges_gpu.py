@@ -68,3 +68,31 @@ def test_many_ranges_one_of_which_does_not_fit():
     assert fm.last_device_error() == fm.DEV_BAD_SEQLEN
     at = int(starts[bad])
     assert bool((out[at:] == 7).all()) and bool((lse[at:] == 5).all()) and bool((out[:3] == 7).all())
+
+
+def test_many_tokens_between_ranges():
+    """Ranges of thousands of tokens with gaps between them that falling and far starts leave."""
+    n = 20000
+    pool = inputs.Pool(23, [[40] * 8], 1, 64, 16, False)
+    k, v, table, ks, vs = pool.device(DEV)
+    q = pool.queries(n, 1).to(DEV)
+    starts = [0, 9001, 9001, 30000, 12000, 16999, 16999, 19998, 20001]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    lens = i32([40, 3, 40, 40, 33, 40, 7, 40])
+    want, want_lse = torch.zeros_like(q), torch.full((n, 1), -float("inf"), device=DEV)
+    for b, (lo, hi) in enumerate(zip(starts, starts[1:])):
+        if lo < hi <= n:
+            want[lo:hi], want_lse[lo:hi] = fm.paged_cross_attention(
+                q[lo:hi], k, v, table[b:b + 1], lens[b:b + 1], ks, vs, q_starts=i32([0, hi - lo]))
+    fm.last_device_error()
+    _used_memory(q)
+    out, lse = fm.paged_cross_attention(q, k, v, table, lens, ks, vs, q_starts=i32(starts))
+    assert fm.last_device_error() == fm.DEV_BAD_SEQLEN
+    gaps = torch.zeros(n, dtype=torch.bool, device=DEV)
+    gaps[9001:12000], gaps[19998:] = True, True
+    assert bool((out[gaps] == 0).all()) and bool((lse[gaps] == -float("inf")).all())
+    assert bool(torch.isfinite(lse[~gaps]).all())
+    # the same rows from items that are cut elsewhere: either rounds to bf16 (2^-8) and weighs in f16 (2^-11 of |v|)
+    most = float(v.float().nan_to_num().abs().max()) * float(vs)  # (NaN where no key is)
+    assert bool(((out.float() - want.float()).abs() <= 2.0 ** -7 * want.float().abs() + 2.0 ** -10 * most).all())
+    assert bool(((lse - want_lse).abs()[~gaps] <= 2.0 ** -16 * 40).all())
