@@ -199,8 +199,9 @@ FP8MLA_API fp8mla_status_t fp8mla_decode(const void* q, const void* kv_cache, fp
  *                  when set, row t of physical page p (its 512 latent and 64
  *                  RoPE values, K and V alike) is E4M3 code times
  *                  kv_scale_rows[p * 64 + t], every scale of a row a key uses
- *                  must be from 0 to 2^16 (those below 2^-110 count as that for
- *                  V), kv_scale is ignored (may be NULL), and only
+ *                  must be finite and not negative (below 2^-110 they count
+ *                  as that for V, where a sequence's lie within a factor of
+ *                  2^126), kv_scale is ignored (may be NULL), and only
  *                  FP8MLA_DOT_FP8 is accepted (FP8MLA_ERR_INVALID_ARG otherwise)
  *   kv_scale_rows NULL: exactly fp8mla_decode.
  * Other arguments, results and errors as fp8mla_decode. */
@@ -276,7 +277,8 @@ FP8MLA_API fp8mla_status_t paged_gqa_decode(const void* q, const void* k_cache, 
  *                at position s_k - q_len + i)
  *   k_scale, v_scale  float32 [1] each, or with scale_per_row != 0 one float
  *                per cached row, [num_blocks, h_kv, page_size], 16-byte aligned,
- *                0 to 2^16; V's below 2^-110 count as 2^-110
+ *                finite, not negative; V's below 2^-110 count as 2^-110, and
+ *                a sequence's lie within a factor of 2^126
  *   spec_mask    uint8 [bs, q_len, q_len] (device) or NULL: token i sees key
  *                s_k - q_len + c of its own block iff spec_mask[b][i][c] != 0;
  *                NULL = causal inside the block (c <= i).  Keys before the
@@ -513,8 +515,8 @@ FP8MLA_API size_t paged_gqa_fp4_workspace_bytes(int bs, int h_q, int h_kv, int h
  *                (elements, multiples of 8), 16-byte aligned; so is out
  *   k_cache, v_cache  E4M3 [num_blocks, h_kv, page_size, head_dim], 16-byte
  *                aligned; k_scale, v_scale float32 [1] (2^-80 to 2^80), or
- *                [num_blocks, h_kv, page_size] (16-byte aligned; finite, not
- *                negative) with scale_rows
+ *                [num_blocks, h_kv, page_size] (16-byte aligned; 0 to 2^80)
+ *                with scale_rows
  *   q_starts     int32 [bs + 1], not falling: sequence b has the tokens
  *                [q_starts[b], q_starts[b + 1]); NULL: token b (n_tokens >= bs)
  *   block_table  int32 [bs, max_blocks] (NULL where max_blocks is 0: no keys);

@@ -680,9 +680,9 @@ def paged_cross_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     """Attention of each sequence's query tokens to all keys of its pages (an encoder's states, a document, a
     prefix), however many tokens and keys there are.  q bf16 [n, h_q, hd] (strided along tokens and heads by
     multiples of 8 values and 16-byte aligned, like out); caches E4M3 [num_blocks, h_kv, page, hd], hd 64 or 128,
-    pages of 16 to 256; k_scale / v_scale float32 [1] or per cached row [num_blocks, h_kv, page] (from 0 on);
-    block_table int32 [bs, max_blocks] (or [bs, 0] where no sequence has a key), kv_lens int32 [bs] (0 allowed).  Sequence b has the tokens [q_starts[b], q_starts[b + 1])
-    (int32 [bs + 1]), or token b without q_starts.
+    pages of 16 to 256; k_scale / v_scale float32 [1] or per cached row [num_blocks, h_kv, page] (0 to 2^80);
+    block_table int32 [bs, max_blocks] (or [bs, 0] where no sequence has a key), kv_lens int32 [bs] (0 allowed).
+    Sequence b has the tokens [q_starts[b], q_starts[b + 1]) (int32 [bs + 1]), or token b without q_starts.
 
     Returns (out bf16 like q, lse float32 [n, h_q]); a sequence without keys gives zeros and -inf, and so do tokens
     of no sequence in outputs that the call makes (given ones keep those rows).  out may be q; outputs and workspace
